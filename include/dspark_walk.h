@@ -56,6 +56,7 @@ extern "C" {
 #define DSPARK_ETEMP (-7)        /* a temperature was negative or not finite (device-detected) */
 #define DSPARK_ELIMIT (-8)       /* B or gamma above dspark_walk_run_noalloc's fixed maximum */
 #define DSPARK_EINTERNAL (-9)    /* a device-side consistency check failed (a bug; tokens -1) */
+#define DSPARK_EPAGES (-10)      /* dspark_tree.h: a row range, length, path or page (device-detected) */
 
 /* Opaque handle: resident weight layout, rendezvous slots, status word. */
 typedef struct dspark_walk dspark_walk;

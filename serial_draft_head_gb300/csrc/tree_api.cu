@@ -1,0 +1,249 @@
+// tree_api.cu -- the C ABI of include/dspark_tree.h: argument checks, the
+// handle's device memory, and the launches.
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include <new>
+
+#include "../../include/dspark_tree.h"
+#include "tree_common.cuh"
+
+using namespace dspark::tree;
+
+struct dspark_tree {
+  int device = 0;
+  int sm_count = 0;
+  dspark_tree_config cfg{};
+  int* status = nullptr;
+};
+
+namespace {
+
+int cuda_code(cudaError_t e) {
+  if (e == cudaSuccess) return DSPARK_OK;
+  return e == cudaErrorMemoryAllocation ? DSPARK_ENOMEM : DSPARK_ECUDA;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+bool stride_ok(int64_t s, int es) { return s >= 0 && s <= ((int64_t)1 << 40) && s * es % 16 == 0; }
+
+// The calls work on the current device: it has to be the handle's.
+int check_device(const dspark_tree* h) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return DSPARK_ECUDA;
+  return dev == h->device ? DSPARK_OK : DSPARK_EINVAL;
+}
+
+int make_cache(const dspark_tree* h, const dspark_tree_cache* c, CacheView* out) {
+  if (!c || !c->k || !c->v) return DSPARK_EINVAL;
+  if (c->type != h->cfg.type && c->type != DSPARK_TYPE_E4M3) return DSPARK_EINVAL;
+  const bool e4m3 = c->type == DSPARK_TYPE_E4M3;
+  const int es = e4m3 ? 1 : 2;
+  if (e4m3 && (!c->k_scale || !c->v_scale || h->cfg.head_dim % 16)) return DSPARK_EINVAL;
+  if (c->n_pages < 1 || c->n_pages >= ((int64_t)1 << 31) || c->page_size < 1) return DSPARK_EINVAL;
+  if (!aligned16(c->k) || !aligned16(c->v)) return DSPARK_EINVAL;
+  out->k = static_cast<uint8_t*>(c->k);
+  out->v = static_cast<uint8_t*>(c->v);
+  out->ks = e4m3 ? c->k_scale : nullptr;
+  out->vs = e4m3 ? c->v_scale : nullptr;
+  for (int i = 0; i < 3; ++i) {
+    if (!stride_ok(c->k_stride[i], es) || !stride_ok(c->v_stride[i], es)) return DSPARK_EINVAL;
+    out->kst[i] = c->k_stride[i] * es;
+    out->vst[i] = c->v_stride[i] * es;
+    out->ksst[i] = out->vsst[i] = 0;
+    if (e4m3) {
+      if (c->k_scale_stride[i] < 0 || c->v_scale_stride[i] < 0) return DSPARK_EINVAL;
+      out->ksst[i] = c->k_scale_stride[i];
+      out->vsst[i] = c->v_scale_stride[i];
+    }
+  }
+  out->n_pages = c->n_pages;
+  out->page = FastDiv::of(c->page_size);
+  return DSPARK_OK;
+}
+
+int make_batch(const dspark_tree_batch* b, int page_size, bool rows, BatchView* out) {
+  if (!b || b->B < 0 || (rows && b->N < 0)) return DSPARK_EINVAL;
+  if (b->B == 0 || (rows && b->N == 0)) {
+    out->B = 0;
+    return DSPARK_OK;
+  }
+  if (!b->pages || !b->start || (rows && !b->first)) return DSPARK_EINVAL;
+  if (b->max_pages < 1 || b->pages_stride < 0) return DSPARK_EINVAL;
+  const int64_t max_pos = (int64_t)b->max_pages * page_size;
+  if (max_pos >= ((int64_t)1 << 31)) return DSPARK_EINVAL;
+  out->pages = b->pages;
+  out->start = b->start;
+  out->first = b->first;
+  out->pages_stride = b->pages_stride;
+  out->max_pos = max_pos;
+  out->B = b->B;
+  out->N = rows ? b->N : 0;
+  return DSPARK_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int dspark_tree_create(const dspark_tree_config* cfg, dspark_tree_t* out) {
+  if (out) *out = nullptr;
+  if (!cfg || !out) return DSPARK_EINVAL;
+  if (cfg->kv_heads < 1 || cfg->q_heads < cfg->kv_heads || cfg->q_heads % cfg->kv_heads ||
+      cfg->q_heads > 65535)
+    return DSPARK_EINVAL;
+  if (cfg->head_dim < 8 || cfg->head_dim % 8 || cfg->head_dim > DSPARK_TREE_MAX_HEAD_DIM)
+    return DSPARK_EINVAL;
+  if (cfg->type != DSPARK_TYPE_BF16 && cfg->type != DSPARK_TYPE_F16) return DSPARK_EINVAL;
+  if (cfg->max_requests < 1 || cfg->max_requests > DSPARK_TREE_MAX_REQUESTS ||
+      cfg->max_nodes < 1 || cfg->max_nodes > DSPARK_TREE_MAX_NODES)
+    return DSPARK_EINVAL;
+  int dev = 0, major = 0, minor = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return cuda_code(e);
+  if (major != 10 || minor != 3) return DSPARK_EUNSUPPORTED;
+  dspark_tree* h = new (std::nothrow) dspark_tree();
+  if (!h) return DSPARK_ENOMEM;
+  h->device = dev;
+  h->sm_count = sms;
+  h->cfg = *cfg;
+  e = cudaMalloc(&h->status, sizeof(int));
+  if (e == cudaSuccess) e = cudaMemset(h->status, 0, sizeof(int));
+  if (e != cudaSuccess) {
+    dspark_tree_destroy(h);
+    return cuda_code(e);
+  }
+  *out = h;
+  return DSPARK_OK;
+}
+
+int dspark_tree_write(dspark_tree_t h, const dspark_tree_cache* cache,
+                      const dspark_tree_batch* batch, const void* k, const int64_t* k_stride,
+                      const void* v, const int64_t* v_stride, void* stream) {
+  if (!h) return DSPARK_EINVAL;
+  RowsArgs a{};
+  int rc = check_device(h);
+  if (rc == DSPARK_OK) rc = make_cache(h, cache, &a.c);
+  if (rc == DSPARK_OK) rc = make_batch(batch, cache->page_size, true, &a.b);
+  if (rc != DSPARK_OK) return rc;
+  if (a.b.B == 0) return DSPARK_OK;
+  if (!k || !v || !k_stride || !v_stride || !aligned16(k) || !aligned16(v)) return DSPARK_EINVAL;
+  for (int i = 0; i < 2; ++i)
+    if (!stride_ok(k_stride[i], 2) || !stride_ok(v_stride[i], 2)) return DSPARK_EINVAL;
+  a.k = static_cast<const uint8_t*>(k);
+  a.v = static_cast<const uint8_t*>(v);
+  a.k_row = k_stride[0] * 2;
+  a.k_head = k_stride[1] * 2;
+  a.v_row = v_stride[0] * 2;
+  a.v_head = v_stride[1] * 2;
+  a.Hkv = h->cfg.kv_heads;
+  a.D = h->cfg.head_dim;
+  a.status = h->status;
+  return cuda_code(write_launch(a, h->cfg.type == DSPARK_TYPE_F16,
+                                cache->type == DSPARK_TYPE_E4M3, h->sm_count,
+                                static_cast<cudaStream_t>(stream)));
+}
+
+int dspark_tree_read(dspark_tree_t h, const dspark_tree_cache* cache,
+                     const dspark_tree_batch* batch, void* out_k, void* out_v, void* stream) {
+  if (!h) return DSPARK_EINVAL;
+  RowsArgs a{};
+  int rc = check_device(h);
+  if (rc == DSPARK_OK) rc = make_cache(h, cache, &a.c);
+  if (rc == DSPARK_OK) rc = make_batch(batch, cache->page_size, true, &a.b);
+  if (rc != DSPARK_OK) return rc;
+  if (a.b.B == 0) return DSPARK_OK;
+  if (!out_k || !out_v || !aligned16(out_k) || !aligned16(out_v)) return DSPARK_EINVAL;
+  a.out_k = static_cast<uint16_t*>(out_k);
+  a.out_v = static_cast<uint16_t*>(out_v);
+  a.Hkv = h->cfg.kv_heads;
+  a.D = h->cfg.head_dim;
+  a.status = h->status;
+  return cuda_code(read_launch(a, h->cfg.type == DSPARK_TYPE_F16,
+                               cache->type == DSPARK_TYPE_E4M3, h->sm_count,
+                               static_cast<cudaStream_t>(stream)));
+}
+
+int dspark_tree_keep(dspark_tree_t h, const dspark_tree_cache* cache,
+                     const dspark_tree_batch* batch, const int32_t* path, int64_t path_stride,
+                     int max_path, const int32_t* count, void* stream) {
+  if (!h) return DSPARK_EINVAL;
+  KeepArgs a{};
+  int rc = check_device(h);
+  if (rc == DSPARK_OK) rc = make_cache(h, cache, &a.c);
+  if (rc == DSPARK_OK) rc = make_batch(batch, cache->page_size, false, &a.b);
+  if (rc != DSPARK_OK) return rc;
+  if (max_path < 0 || max_path > DSPARK_TREE_MAX_NODES) return DSPARK_EINVAL;
+  if (a.b.B == 0 || max_path == 0) return DSPARK_OK;
+  if (!path || !count || path_stride < 0) return DSPARK_EINVAL;
+  a.path = path;
+  a.count = count;
+  a.path_stride = path_stride;
+  a.max_path = max_path;
+  a.Hkv = h->cfg.kv_heads;
+  a.scales = cache->type == DSPARK_TYPE_E4M3;
+  a.row_bytes = h->cfg.head_dim * (a.scales ? 1 : 2);
+  a.status = h->status;
+  return cuda_code(keep_launch(a, static_cast<cudaStream_t>(stream)));
+}
+
+int dspark_tree_attend(dspark_tree_t h, const dspark_tree_cache* cache,
+                       const dspark_tree_batch* batch, const void* q, const int64_t* q_stride,
+                       const uint32_t* mask, int64_t mask_stride, int mask_words, float scale,
+                       float softcap, void* out, float* lse, void* stream) {
+  if (!h) return DSPARK_EINVAL;
+  AttendArgs a{};
+  int rc = check_device(h);
+  if (rc == DSPARK_OK) rc = make_cache(h, cache, &a.c);
+  if (rc == DSPARK_OK) rc = make_batch(batch, cache->page_size, true, &a.b);
+  if (rc != DSPARK_OK) return rc;
+  if (!isfinite(scale) || !isfinite(softcap) || softcap < 0.f) return DSPARK_EINVAL;
+  if (a.b.B > h->cfg.max_requests) return DSPARK_EINVAL;
+  if (mask && (mask_words < 1 || mask_stride < 0)) return DSPARK_EINVAL;
+  if (a.b.B == 0) return DSPARK_OK;
+  if (!q || !q_stride || !out || !aligned16(q) || !aligned16(out)) return DSPARK_EINVAL;
+  if (!stride_ok(q_stride[0], 2) || !stride_ok(q_stride[1], 2)) return DSPARK_EINVAL;
+  a.q = static_cast<const uint8_t*>(q);
+  a.q_row = q_stride[0] * 2;
+  a.q_head = q_stride[1] * 2;
+  a.mask = mask;
+  a.mask_stride = mask_stride;
+  a.mask_words = mask ? mask_words : 0;
+  a.scale = scale;
+  a.softcap = softcap;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.Hq = h->cfg.q_heads;
+  a.Hkv = h->cfg.kv_heads;
+  a.G = a.Hq / a.Hkv;
+  a.D = h->cfg.head_dim;
+  a.max_nodes = h->cfg.max_nodes;
+  a.status = h->status;
+  return cuda_code(attend_launch(a, h->cfg.type == DSPARK_TYPE_F16,
+                                 cache->type == DSPARK_TYPE_E4M3,
+                                 static_cast<cudaStream_t>(stream)));
+}
+
+int dspark_tree_status(dspark_tree_t h, void* stream) {
+  if (!h) return DSPARK_EINVAL;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int st = 0;
+  cudaError_t e = cudaMemcpyAsync(&st, h->status, sizeof(int), cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaMemsetAsync(h->status, 0, sizeof(int), s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  return e == cudaSuccess ? st : cuda_code(e);
+}
+
+int dspark_tree_destroy(dspark_tree_t h) {
+  if (!h) return DSPARK_EINVAL;
+  const int rc = cuda_code(cudaDeviceSynchronize());
+  if (h->status) cudaFree(h->status);
+  delete h;
+  return rc;
+}
+
+}  // extern "C"

@@ -1,0 +1,167 @@
+// tree_common.cuh -- what the draft-check kernels share: the device view of a
+// paged cache and of a call's requests, element conversions, and the
+// arguments of the launches (tree_cache.cu, tree_attend.cu).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/dspark_tree.h"
+
+namespace dspark {
+namespace tree {
+
+// n / d for 0 <= n < 2^31 by one multiplication: with L = ceil(log2 d) and
+// mul = ceil(2^(31+L) / d) < 2^32 + 1, floor(n * mul / 2^(31+L)) is exact.
+struct FastDiv {
+  uint64_t mul;
+  int shift;
+  int d;
+  __host__ static FastDiv of(int d) {
+    FastDiv f;
+    int L = 0;
+    while (((int64_t)1 << L) < d) ++L;
+    f.shift = 31 + L;
+    f.mul = (((uint64_t)1 << f.shift) + (uint64_t)d - 1) / (uint64_t)d;
+    f.d = d;
+    return f;
+  }
+  __device__ __forceinline__ int div(int n) const {
+    return (int)(((uint64_t)(uint32_t)n * mul) >> shift);
+  }
+};
+
+// The cache with strides in bytes.
+struct CacheView {
+  uint8_t *k, *v;
+  uint8_t *ks, *vs;          // scale bytes, e4m3 only
+  int64_t kst[3], vst[3];    // page, slot, head
+  int64_t ksst[3], vsst[3];
+  int64_t n_pages;
+  FastDiv page;
+};
+
+struct BatchView {
+  const int32_t* pages;
+  const int32_t* start;
+  const int32_t* first;
+  int64_t pages_stride;
+  int64_t max_pos;           // max_pages * page_size < 2^31
+  int B, N;
+};
+
+// Status words set by the kernels (any of them: the host reads one word).
+__device__ __forceinline__ void set_status(int* status, int code) {
+  atomicExch(status, code);
+}
+
+// Rows and context length of request b; false if they do not fit the arrays.
+__device__ __forceinline__ bool request_rows(const BatchView& q, int b, int* row0, int* rows,
+                                             int* start) {
+  const int f0 = q.first[b], f1 = q.first[b + 1], s = q.start[b];
+  *row0 = f0;
+  *rows = 0;
+  *start = s;
+  if (f0 < 0 || f1 < f0 || f1 > q.N || s < 0 || (int64_t)s + (f1 - f0) > q.max_pos) return false;
+  *rows = f1 - f0;
+  return true;
+}
+
+// Page and slot of position pos (0 <= pos < max_pos) of request b; false if
+// the table's entry is no page of the cache.
+__device__ __forceinline__ bool locate(const CacheView& c, const BatchView& q, int b, int pos,
+                                       int64_t* page, int* slot) {
+  const int i = c.page.div(pos);
+  *slot = pos - i * c.page.d;
+  const int p = __ldg(q.pages + (int64_t)b * q.pages_stride + i);
+  *page = p;
+  return p >= 0 && p < c.n_pages;
+}
+
+// 2^(byte - 127) of a scale byte; 255 is NaN.
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+  return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255 ? 0x7fc00000u : byte << 23);
+}
+
+template <bool F16>
+__device__ __forceinline__ float to_float(uint16_t x) {
+  return F16 ? __half2float(__ushort_as_half(x)) : __uint_as_float((uint32_t)x << 16);
+}
+
+// Two floats to the 16-bit type, nearest even, `lo` in the low half.
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if (F16) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Values past the type's range become its largest finite one (NaN stays).
+template <bool F16>
+__device__ __forceinline__ float saturate16(float x) {
+  const float top = F16 ? 65504.f : 3.38953139e38f;
+  return fabsf(x) > top ? copysignf(top, x) : x;
+}
+
+// Two e4m3 codes to floats.
+__device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t codes) {
+  const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
+  return __half22float2(__half2(r));
+}
+
+struct AttendArgs {
+  CacheView c;
+  BatchView b;
+  const uint8_t* q;
+  int64_t q_row, q_head;     // bytes
+  const uint32_t* mask;
+  int64_t mask_stride;
+  int mask_words;
+  float scale, softcap;
+  uint16_t* out;
+  float* lse;
+  int Hq, Hkv, G, D;
+  int max_nodes;
+  int* status;
+};
+
+cudaError_t attend_launch(const AttendArgs& a, bool f16, bool e4m3, cudaStream_t stream);
+
+// Packed rows of the cache calls: strides in bytes.
+struct RowsArgs {
+  CacheView c;
+  BatchView b;
+  const uint8_t *k, *v;      // write: source rows
+  int64_t k_row, k_head, v_row, v_head;
+  uint16_t *out_k, *out_v;   // read: destination rows
+  int Hkv, D;
+  int* status;
+};
+
+cudaError_t write_launch(const RowsArgs& a, bool f16, bool e4m3, int sm_count,
+                         cudaStream_t stream);
+cudaError_t read_launch(const RowsArgs& a, bool f16, bool e4m3, int sm_count,
+                        cudaStream_t stream);
+
+struct KeepArgs {
+  CacheView c;
+  BatchView b;
+  const int32_t* path;
+  const int32_t* count;
+  int64_t path_stride;
+  int max_path;
+  int Hkv, row_bytes;        // bytes of one head's row
+  bool scales;
+  int* status;
+};
+
+cudaError_t keep_launch(const KeepArgs& a, cudaStream_t stream);
+
+}  // namespace tree
+}  // namespace dspark

@@ -838,6 +838,7 @@ const char* dspark_walk_strerror(int code) {
     case DSPARK_EUNSUPPORTED: return "unsupported rank or device (needs r = 256 on sm_103)";
     case DSPARK_ETEMP: return "temperature negative or not finite";
     case DSPARK_EINTERNAL: return "device-side consistency check failed";
+    case DSPARK_EPAGES: return "a request's rows, length, path or pages outside their bounds";
     case DSPARK_ELIMIT:
       return "batch or walk length above the allocation-free entry point's maximum (B <= 64, "
              "gamma <= 16)";

@@ -22,6 +22,7 @@ EUNSUPPORTED = -6
 ETEMP = -7
 ELIMIT = -8
 EINTERNAL = -9
+EPAGES = -10
 
 TRACE_SM_CLOCK = 0
 TRACE_GLOBAL_TIMER = 1
