@@ -32,6 +32,10 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
                : "memory");
 }
 
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
@@ -100,6 +104,24 @@ __device__ __forceinline__ void cp_async16_hint(void* dst, const void* src, uint
   asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)),
                "l"(src), "l"(policy)
                : "memory");
+}
+
+// cp_async16 that fills the 16 bytes with zeros instead of reading (src is not
+// read) unless `on`.
+__device__ __forceinline__ void cp_async16_or_zero(void* dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(on ? 16 : 0)
+               : "memory");
+}
+
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// Wait until at most N of this thread's commit groups are still in flight.
+template <int N>
+__device__ __forceinline__ void cp_async_wait_group() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ void cp_async4(void* dst, const void* src) {
@@ -179,6 +201,17 @@ __device__ __forceinline__ void tc_mma_tmem_a(uint32_t d_tmem, uint32_t a_tmem, 
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// D[tmem] (+)= A[smem desc] * B[smem desc]; kind::f16.
+__device__ __forceinline__ void tc_mma_smem(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
@@ -308,6 +341,16 @@ __device__ __forceinline__ uint64_t smem_desc_noswizzle(uint32_t saddr, uint32_t
   d |= (uint64_t)((sbo_bytes >> 4) & 0x3FFFu) << 32;
   d |= (uint64_t)1 << 46;  // descriptor version for sm_100
   return d;                // base offset 0, layout type 0 (no swizzle)
+}
+
+// The same for operands whose 64-element (128-byte) rows are swizzled in atoms
+// of 8 rows (16-byte chunk c of row r at chunk c ^ (r % 8)), each atom on a
+// 1,024-byte boundary.  K-major: stride = bytes between groups of 8 rows;
+// M/N-major: stride = bytes between groups of 8 K rows, leading = bytes between
+// 64-element blocks along M/N.
+__device__ __forceinline__ uint64_t smem_desc_swizzle128(uint32_t saddr, uint32_t leading_bytes,
+                                                         uint32_t stride_bytes) {
+  return smem_desc_noswizzle(saddr, leading_bytes, stride_bytes) | ((uint64_t)2 << 61);
 }
 
 // Instruction descriptor of kind::f16 with bf16 A and B, fp32 D, both

@@ -15,6 +15,11 @@ struct dspark_tree {
   int sm_count = 0;
   dspark_tree_config cfg{};
   int* status = nullptr;
+  void* parts = nullptr;          // attend's workspace
+  float* part_o = nullptr;
+  float2* part_ml = nullptr;
+  int4* part_of = nullptr;
+  int part_rows = 0;
 };
 
 namespace {
@@ -111,8 +116,23 @@ int dspark_tree_create(const dspark_tree_config* cfg, dspark_tree_t* out) {
   h->device = dev;
   h->sm_count = sms;
   h->cfg = *cfg;
-  e = cudaMalloc(&h->status, sizeof(int));
+  // two parts a CTA: the item it finishes for an earlier CTA, and the one it leaves to a later
+  const int G = cfg->q_heads / cfg->kv_heads;
+  const int64_t rows = (int64_t)cfg->max_nodes * G;
+  h->part_rows = rows >= kGroupRows ? kGroupRows : (int)((rows + 31) / 32 * 32);
+  const size_t n = (size_t)2 * sms * h->part_rows;
+  const size_t o_bytes = n * padded_dim(cfg->head_dim) * sizeof(float);
+  const size_t ml_bytes = n * sizeof(float2);
+  e = cudaMalloc(&h->parts, o_bytes + ml_bytes + (size_t)sms * sizeof(int4));
+  if (e == cudaSuccess) {
+    uint8_t* p = static_cast<uint8_t*>(h->parts);
+    h->part_o = reinterpret_cast<float*>(p);
+    h->part_ml = reinterpret_cast<float2*>(p + o_bytes);
+    h->part_of = reinterpret_cast<int4*>(p + o_bytes + ml_bytes);
+    e = cudaMalloc(&h->status, sizeof(int));
+  }
   if (e == cudaSuccess) e = cudaMemset(h->status, 0, sizeof(int));
+  if (e == cudaSuccess) e = attend_setup(cfg->type == DSPARK_TYPE_F16, cfg->head_dim);
   if (e != cudaSuccess) {
     dspark_tree_destroy(h);
     return cuda_code(e);
@@ -222,6 +242,12 @@ int dspark_tree_attend(dspark_tree_t h, const dspark_tree_cache* cache,
   a.G = a.Hq / a.Hkv;
   a.D = h->cfg.head_dim;
   a.max_nodes = h->cfg.max_nodes;
+  a.group = FastDiv::of(a.G);
+  a.n_cta = h->sm_count;
+  a.part_o = h->part_o;
+  a.part_ml = h->part_ml;
+  a.part_of = h->part_of;
+  a.part_rows = h->part_rows;
   a.status = h->status;
   return cuda_code(attend_launch(a, h->cfg.type == DSPARK_TYPE_F16,
                                  cache->type == DSPARK_TYPE_E4M3,
@@ -242,6 +268,7 @@ int dspark_tree_destroy(dspark_tree_t h) {
   if (!h) return DSPARK_EINVAL;
   const int rc = cuda_code(cudaDeviceSynchronize());
   if (h->status) cudaFree(h->status);
+  if (h->parts) cudaFree(h->parts);
   delete h;
   return rc;
 }

@@ -1,129 +1,1002 @@
-// tree_attend.cu -- attention of drafted rows over a paged cache.
+// tree_attend.cu -- attention of drafted rows over a paged cache on tcgen05.
 //
-// Per row and head, over the visible keys j: s_j = scale q.k_j (capped:
-// c tanh(s_j / c)), out = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m) with the
-// running maximum m, in one pass over K and V.  One block per (row, head):
-// scores of 128 keys at a time, one key a thread, then the values, one element
-// a thread.
+// Per cached head the rows that read it are (node, query head of the group):
+// T * G of them.  A work item is (request, cached head, up to 256 of its rows)
+// over all its keys, cut into tiles of 128 keys; a tile of one item is a unit.
+// The units of all items, in order, are split evenly over one CTA per SM: the
+// lengths are known on the device only, so every CTA sums them up itself.  An
+// item that lies inside one CTA's share is finished there; one that several
+// CTAs share leaves parts (unnormalised O, maximum, sum), joined by a second
+// kernel in a fixed order.
+//
+// Mathematics, per row, one pass over the tiles in the base-2 exponent:
+//   x_j = log2(e) * scale * q.k_j              (capped: log2(e) c tanh(s / c))
+//   p_j = 2^(x_j - m),  l = sum p_j,  O = sum p_j v_j
+// m follows the running maximum lazily: it moves, and O and l are rescaled,
+// only when the maximum has grown by more than 8, so p <= 2^8: O and l in fp32
+// keep their relative precision, and the read-modify-write of O is rare.  p is
+// rounded once to the 16-bit type for the second product (half a unit, as the
+// result itself is rounded); l sums the unrounded p.  For f16 m carries -7, so
+// that weights down to 2^-21 of the largest stay normal numbers.
+//
+// Roles of the 18 warps: 8 softmax warps in two groups of 128 threads (thread =
+// row = tensor-memory lane), 8 producer warps, 2 MMA warps (one thread each).
+// Two streams share the ring of key and value tiles: with more than 128 rows
+// each stream owns a row tile and both read every key tile; with fewer, the
+// streams take alternate key tiles of the one row tile and are joined at the
+// end.  Per stream: S = Q K^T (tcgen05, both operands in shared memory) into
+// tensor memory, softmax there, P written over S, O += P V with P read from
+// tensor memory.  One stream's softmax runs beside the other's products.
+//
+// Tensor memory (512 columns): S/P of the streams at 0 and 128, O at 256 and
+// 384.  Shared memory: two Q tiles and the ring, rows of 64 elements (128
+// bytes) swizzled in atoms of 8 rows; K is read K-major, V (same layout)
+// N-major.  The producers copy any strides and page size: 16-byte cp.async for
+// a 16-bit cache; e4m3 through registers, the scale multiplied in (exact in
+// bf16), so everything after the ring is the same.
+//
+// Keys past the end are zero rows and masked; draft rows of V that are not
+// finite would reach every row of the product (0 * NaN), so such elements are
+// zeroed in the ring and noted, and added at the end to the rows that see them.
 #include <math.h>
 
+#include "tc_ptx.cuh"
 #include "tree_common.cuh"
 
 namespace dspark {
 namespace tree {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kKeys = 128;              // keys of a tile
+constexpr int kSoftWarps = 8;
+constexpr int kProdWarps = 8;
+constexpr int kProd = kProdWarps * 32;
+constexpr int kThreads = (kSoftWarps + kProdWarps + 2) * 32;
+constexpr int kMmaWarp = kSoftWarps + kProdWarps;
+constexpr int kLag = 2;                 // slots a producer issues ahead of the one it completes
+constexpr int kBadSets = 8;             // segments the producers can be ahead, rounded up
+constexpr uint64_t kWaitLimitNs = 1000000000ull;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
-__device__ float block_max(float x, float* red) {
-  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = x;
-  __syncthreads();
-  x = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  __syncthreads();
-  return x;
+template <int DP>
+struct Layout {
+  static constexpr int kTile = kKeys * DP * 2;                  // bytes of a Q, K or V tile
+  static constexpr int kSlots = DP == 128 ? 5 : 8;
+  static constexpr int kRing = 2 * kTile;
+  static constexpr int kTail = kRing + kSlots * kTile;
+};
+
+struct Tail {
+  uint64_t full[8], empty[8], q_full, q_empty, s_full[2], p_full[2], o_done[2];
+  float2 ml[2][kKeys];
+  uint32_t bad[kBadSets][DSPARK_TREE_MAX_NODES / 32];
+  int64_t unit0, units, total;           // this CTA's share, and all units
+  int64_t warp_sum[kThreads / 32];
+  int b0;
+  int64_t off0;
+  uint32_t tmem;
+  int abort;
+};
+
+__device__ __forceinline__ uint64_t globaltimer_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+  return t;
 }
 
-__device__ float block_sum(float x, float* red) {
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = x;
-  __syncthreads();
-  x = red[0] + red[1] + red[2] + red[3];
-  __syncthreads();
-  return x;
-}
-
-template <bool F16, bool E4M3>
-__device__ __forceinline__ float element(const uint8_t* row, int i) {
-  if (!E4M3) return to_float<F16>(reinterpret_cast<const uint16_t*>(row)[i]);
-  return e4m3x2_to_float2(row[i]).x;
-}
-
-template <bool F16, bool E4M3>
-__global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
-  __shared__ float q[DSPARK_TREE_MAX_HEAD_DIM], p[kThreads], red[4];
-  __shared__ const uint8_t* vrow[kThreads];
-  __shared__ float vscale[kThreads];
-  __shared__ bool see_key[kThreads];
-  const int n = blockIdx.x, head = blockIdx.y, kvh = head / a.G, tid = threadIdx.x;
-  int lo = 0, hi = a.b.B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (a.b.first[mid] <= n) lo = mid;
-    else hi = mid - 1;
-  }
-  int row0, rows, start;
-  const bool ok = request_rows(a.b, lo, &row0, &rows, &start) && rows <= a.max_nodes &&
-                  (!a.mask || rows <= 32 * a.mask_words);
-  if (!ok) {
-    if (tid == 0) set_status(a.status, DSPARK_EPAGES);
-    return;
-  }
-  if (n < row0 || n >= row0 + rows) return;
-  const int node = n - row0, total = start + rows;
-  if (tid < a.D)
-    q[tid] = to_float<F16>(
-        reinterpret_cast<const uint16_t*>(a.q + n * a.q_row + head * a.q_head)[tid]);
-  __syncthreads();
-  float m = -INFINITY, l = 0.f, acc = 0.f;
-  for (int t0 = 0; t0 < total; t0 += kThreads) {
-    const int pos = t0 + tid;
-    bool see = pos < total;
-    if (see && pos >= start) {
-      const int j = pos - start;
-      see = a.mask ? (a.mask[n * a.mask_stride + j / 32] >> (j % 32)) & 1 : j <= node;
+// Every wait ends: past the limit the CTA's abort flag makes all its waits
+// return at once, the loops run on (all accesses stay in bounds), and the
+// status says so.
+__device__ __forceinline__ void wait(Tail* s, uint64_t* bar, uint32_t parity, int* status) {
+  if (ptx::mbar_try_wait(bar, parity)) return;
+  const uint64_t t0 = globaltimer_ns();
+  uint32_t spins = 0;
+  while (!ptx::mbar_try_wait(bar, parity)) {
+    if ((++spins & 63u) != 0u) continue;
+    if (*(volatile int*)&s->abort) return;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      *(volatile int*)&s->abort = 1;
+      set_status(status, DSPARK_ETIMEOUT);
+      return;
     }
-    float s = -INFINITY;
-    if (see) {
-      int64_t page;
-      int slot;
-      if (locate(a.c, a.b, lo, pos, &page, &slot)) {
-        const uint8_t* k = a.c.k + page * a.c.kst[0] + slot * a.c.kst[1] + kvh * a.c.kst[2];
-        vrow[tid] = a.c.v + page * a.c.vst[0] + slot * a.c.vst[1] + kvh * a.c.vst[2];
-        float x = 0.f;
-        for (int i = 0; i < a.D; ++i) x += q[i] * element<F16, E4M3>(k, i);
-        vscale[tid] = 1.f;
-        if (E4M3) {
-          x *= scale_value(a.c.ks[page * a.c.ksst[0] + slot * a.c.ksst[1] + kvh * a.c.ksst[2]]);
-          vscale[tid] =
-              scale_value(a.c.vs[page * a.c.vsst[0] + slot * a.c.vsst[1] + kvh * a.c.vsst[2]]);
+  }
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Rows of request b as attend takes them (0 if they do not fit), key tiles and
+// row groups.
+struct Request {
+  int row0, rows, start, tiles, groups;
+};
+
+__device__ __forceinline__ Request load_request(const AttendArgs& a, int b, bool* ok) {
+  Request r;
+  *ok = request_rows(a.b, b, &r.row0, &r.rows, &r.start) && r.rows <= a.max_nodes &&
+        (!a.mask || r.rows <= 32 * a.mask_words);
+  if (!*ok) r.rows = 0;
+  r.tiles = (r.start + r.rows + kKeys - 1) / kKeys;
+  r.groups = (r.rows * a.G + kGroupRows - 1) / kGroupRows;
+  return r;
+}
+
+__device__ __forceinline__ int64_t units_of(const AttendArgs& a, const Request& r) {
+  return r.rows == 0 ? 0 : (int64_t)r.tiles * r.groups * a.Hkv;
+}
+
+// First unit of CTA i's share of `total` units over n CTAs.
+__device__ __forceinline__ int64_t share(int64_t total, int n, int i) { return total * i / n; }
+
+// One CTA's part of an item: key tiles t0 .. t1-1 of `tiles`.
+struct Segment {
+  int b, row0, rows, start, head, group, t0, t1, tiles;
+  int64_t item_end;                     // unit after the item's last
+};
+
+struct Walker {
+  Request r;
+  int b, head, group, t0;
+  int64_t left, unit;
+
+  __device__ void init(const AttendArgs& a, const Tail* s) {
+    left = s->units;
+    unit = s->unit0;
+    b = s->b0;
+    if (left <= 0) return;
+    bool ok;
+    r = load_request(a, b, &ok);
+    const int64_t item = s->off0 / r.tiles;
+    t0 = (int)(s->off0 % r.tiles);
+    head = (int)(item / r.groups);
+    group = (int)(item % r.groups);
+  }
+
+  __device__ bool next(const AttendArgs& a, Segment* s) {
+    if (left <= 0) return false;
+    const int64_t rest = r.tiles - t0;
+    const int n = (int)(rest < left ? rest : left);
+    s->b = b;
+    s->row0 = r.row0;
+    s->rows = r.rows;
+    s->start = r.start;
+    s->head = head;
+    s->group = group;
+    s->t0 = t0;
+    s->t1 = t0 + n;
+    s->tiles = r.tiles;
+    s->item_end = unit + rest;
+    left -= n;
+    unit += n;
+    t0 += n;
+    if (t0 == r.tiles) {
+      t0 = 0;
+      if (++group == r.groups) {
+        group = 0;
+        if (++head == a.Hkv) {
+          head = 0;
+          bool ok;
+          if (left > 0) do {
+              r = load_request(a, ++b, &ok);
+            } while (r.rows == 0 && b + 1 < a.b.B);
+          if (r.rows == 0) left = 0;    // the arrays changed under the kernel
         }
-        s = x * a.scale;
-        if (a.softcap > 0.f) s = a.softcap * tanhf(s / a.softcap);
-      } else {
-        set_status(a.status, DSPARK_EPAGES);
-        see = false;
       }
     }
-    see_key[tid] = see;
-    const float m_new = fmaxf(m, block_max(s, red));
-    const float m_use = m_new == -INFINITY ? 0.f : m_new;
-    p[tid] = see ? expf(s - m_use) : 0.f;
-    const float back = expf(m - m_use);
-    l = l * back + block_sum(p[tid], red);
-    acc *= back;
-    if (tid < a.D)
-      for (int i = 0; i < kThreads; ++i)
-        if (see_key[i]) acc += p[i] * (element<F16, E4M3>(vrow[i], tid) * vscale[i]);
-    m = m_new;
-    __syncthreads();
+    return true;
   }
-  if (tid < a.D) {
-    const float o = l == 0.f ? 0.f : acc / l;
-    a.out[((int64_t)n * a.Hq + head) * a.D + tid] = (uint16_t)pack2<F16>(o, 0.f);
+};
+
+__device__ __forceinline__ int group_rows(const AttendArgs& a, const Segment& s) {
+  const int n = s.rows * a.G - s.group * kGroupRows;
+  return n < kGroupRows ? n : kGroupRows;
+}
+
+// Word w of the draft positions that node `node` of the segment's request sees
+// (bits past the request's rows are clear).
+__device__ __forceinline__ uint32_t sees_word(const AttendArgs& a, const Segment& s, int node,
+                                              int w) {
+  const int left = s.rows - 32 * w;
+  if (w < 0 || left <= 0) return 0;
+  uint32_t m;
+  if (a.mask) {
+    m = __ldg(a.mask + (int64_t)(s.row0 + node) * a.mask_stride + w);
+  } else {
+    const int n = node + 1 - 32 * w;
+    m = n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
   }
-  if (a.lse && tid == 0) a.lse[(int64_t)n * a.Hq + head] = l == 0.f ? -INFINITY : m + logf(l);
+  return left >= 32 ? m : m & ((1u << left) - 1u);
+}
+
+// Visibility of the 32 positions from `pos` on.
+__device__ __forceinline__ uint32_t sees_32(const AttendArgs& a, const Segment& s, int node,
+                                            int pos) {
+  const int j = pos - s.start;
+  if (j <= -32) return 0xffffffffu;
+  if (j < 0) return ((1u << -j) - 1u) | (sees_word(a, s, node, 0) << -j);
+  const int sh = j & 31;
+  const uint32_t lo = sees_word(a, s, node, j >> 5);
+  return sh ? (lo >> sh) | (sees_word(a, s, node, (j >> 5) + 1) << (32 - sh)) : lo;
+}
+
+// ------------------------------------------------------------- producers --
+
+template <bool F16>
+__device__ __forceinline__ bool nonfinite16(uint32_t x) {
+  constexpr uint32_t e = F16 ? 0x7c00u : 0x7f80u;
+  return (x & e) == e;
+}
+
+// Zeroes the non-finite elements of a 16-byte chunk; true if there were any.
+template <bool F16>
+__device__ __forceinline__ bool zero_nonfinite(uint4* x) {
+  uint32_t w[4] = {x->x, x->y, x->z, x->w};
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (nonfinite16<F16>(w[i])) {
+      w[i] &= 0xffff0000u;
+      any = true;
+    }
+    if (nonfinite16<F16>(w[i] >> 16)) {
+      w[i] &= 0x0000ffffu;
+      any = true;
+    }
+  }
+  if (any) *x = make_uint4(w[0], w[1], w[2], w[3]);
+  return any;
+}
+
+// Four e4m3 codes times 2^(byte - 127) in the 16-bit type, exact (see the
+// conditions at `easy_scale`).  bf16: sign and the seven other bits moved to
+// bf16's sign, exponent and mantissa fields stand for code * 2^-120.
+template <bool F16>
+__device__ __forceinline__ uint2 scale_codes(uint32_t w, uint32_t mul2) {
+  uint2 r;
+  if (F16) {
+    const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
+    const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
+    const __half2 m = *reinterpret_cast<const __half2*>(&mul2);
+    const __half2 x = __hmul2(__half2(lo), m), y = __hmul2(__half2(hi), m);
+    r.x = *reinterpret_cast<const uint32_t*>(&x);
+    r.y = *reinterpret_cast<const uint32_t*>(&y);
+  } else {
+    const uint32_t lo = __byte_perm(w, 0, 0x1404), hi = __byte_perm(w, 0, 0x3424);
+    const uint32_t a = (lo & 0x80008000u) | ((lo >> 4) & 0x07f007f0u);
+    const uint32_t b = (hi & 0x80008000u) | ((hi >> 4) & 0x07f007f0u);
+    const __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(&mul2);
+    const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), m);
+    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&b), m);
+    r.x = *reinterpret_cast<const uint32_t*>(&x);
+    r.y = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  return r;
+}
+
+// Scales whose product with any code is a finite number of the 16-bit type and
+// whose multiplier is one too: 2^(byte - 7) for bf16, 2^(byte - 127) for f16.
+template <bool F16>
+__device__ __forceinline__ bool easy_scale(uint32_t byte) {
+  return byte <= 134 && (!F16 || byte >= 113);
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t scale_mul2(uint32_t byte) {
+  return (F16 ? (byte - 112) << 10 : (byte + 120) << 7) * 0x00010001u;
+}
+
+// Any other scale: through fp32, rounded and saturated as the cache reads back.
+template <bool F16>
+__device__ __noinline__ uint2 scale_codes_any(uint32_t w, uint32_t byte) {
+  const float s = scale_value(byte);
+  const float2 x = e4m3x2_to_float2(w & 0xffffu), y = e4m3x2_to_float2(w >> 16);
+  return make_uint2(
+      pack2<F16>(saturate16<F16>(x.x * s), saturate16<F16>(x.y * s)),
+      pack2<F16>(saturate16<F16>(y.x * s), saturate16<F16>(y.y * s)));
+}
+
+// Byte offset of (row, 16-byte chunk) in a tile: 64-element blocks of 128 rows.
+__device__ __forceinline__ uint32_t tile_offset(int row, int chunk) {
+  return (uint32_t)(chunk >> 3) * (kKeys * 128) + (uint32_t)row * 128 +
+         (uint32_t)((chunk ^ row) & 7) * 16;
+}
+
+struct Place {
+  int page, slot;
+};
+
+// Page and slot of a position; positions past the end and bad pages: -1.
+__device__ __forceinline__ Place place_of(const AttendArgs& a, int b, int pos, int total) {
+  Place p{-1, 0};
+  if (pos < total) {
+    const int i = a.c.page.div(pos);
+    p.slot = pos - i * a.c.page.d;
+    p.page = __ldg(a.b.pages + (int64_t)b * a.b.pages_stride + i);
+    if ((uint32_t)p.page >= (uint64_t)a.c.n_pages) {
+      p.page = -1;
+      set_status(a.status, DSPARK_EPAGES);
+    }
+  }
+  return p;
+}
+
+template <bool F16, int DP>
+__device__ __forceinline__ void produce16(const AttendArgs& a, uint8_t* smem, Tail* sh) {
+  using L = Layout<DP>;
+  constexpr int kChunks = DP / 8;                // 16-byte chunks of a row
+  constexpr int kRows = kProd / kChunks;         // rows a pass
+  constexpr int kPasses = kKeys / kRows;
+  const int tid = threadIdx.x - kSoftWarps * 32, lane = threadIdx.x % 32;
+  const int chunk = tid % kChunks, r0 = tid / kChunks;
+  const bool in_dim = chunk * 8 < a.D;
+  uint8_t* ring = smem + L::kRing;
+  Walker w;
+  Segment s;
+  w.init(a, sh);
+  int n = 0, seg = 0;                            // slots issued, segments begun
+  // the V tile in flight: where it is and which of its positions are draft
+  int prev_pos = 0, prev_start = 0x7fffffff, prev_total = 0, prev_seg = 0;
+  auto complete = [&](int slot, bool v) {        // slot's copies of this thread have landed
+    if (v && prev_pos + kKeys > prev_start) {
+#pragma unroll 1
+      for (int i = 0; i < kPasses; ++i) {
+        const int row = r0 + i * kRows, pos = prev_pos + row;
+        if (pos < prev_start || pos >= prev_total) continue;
+        uint4* p = reinterpret_cast<uint4*>(ring + (slot % L::kSlots) * L::kTile +
+                                            tile_offset(row, chunk));
+        uint4 x = *p;
+        if (zero_nonfinite<F16>(&x)) {
+          *p = x;
+          const int j = pos - prev_start;
+          atomicOr(&sh->bad[prev_seg % kBadSets][j >> 5], 1u << (j & 31));
+        }
+      }
+    }
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&sh->full[slot % L::kSlots]);
+  };
+  for (; w.next(a, &s); ++seg) {
+    const int total = s.start + s.rows;
+    for (int t = s.t0; t < s.t1; ++t) {
+      Place p[kPasses];
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i)
+        p[i] = place_of(a, s.b, t * kKeys + r0 + i * kRows, total);
+#pragma unroll
+      for (int v = 0; v < 2; ++v, ++n) {
+        wait(sh, &sh->empty[n % L::kSlots], ((n / L::kSlots) & 1) ^ 1, a.status);
+        uint8_t* dst = ring + (n % L::kSlots) * L::kTile;
+        const int64_t* st = v ? a.c.vst : a.c.kst;
+        const uint8_t* src = (v ? a.c.v : a.c.k) + s.head * st[2] + chunk * 16;
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+          const bool on = in_dim && p[i].page >= 0;
+          const uint8_t* from = on ? src + p[i].page * st[0] + p[i].slot * st[1] : a.c.k;
+          ptx::cp_async16_or_zero(dst + tile_offset(r0 + i * kRows, chunk), from, on);
+        }
+        ptx::cp_async_commit();
+        if (n >= kLag) {
+          ptx::cp_async_wait_group<kLag>();
+          complete(n - kLag, v);
+        }
+      }
+      prev_pos = t * kKeys;
+      prev_start = s.start;
+      prev_total = total;
+      prev_seg = seg;
+    }
+  }
+  if (n > 0) {
+    ptx::cp_async_wait_group<1>();
+    complete(n - 2, false);
+    ptx::cp_async_wait_group<0>();
+    complete(n - 1, true);
+  }
+}
+
+template <bool F16, int DP>
+__device__ __forceinline__ void produce8(const AttendArgs& a, uint8_t* smem, Tail* sh) {
+  using L = Layout<DP>;
+  constexpr int kChunks = DP / 16;               // 16-code chunks of a row
+  constexpr int kRows = kProd / kChunks;
+  constexpr int kPasses = kKeys / kRows;
+  const int tid = threadIdx.x - kSoftWarps * 32, lane = threadIdx.x % 32;
+  const int chunk = tid % kChunks, r0 = tid / kChunks;
+  const bool in_dim = chunk * 16 < a.D;
+  uint8_t* ring = smem + L::kRing;
+  Walker w;
+  Segment s;
+  w.init(a, sh);
+  bool more = w.next(a, &s);
+  int t = s.t0, seg = 0;                         // the tile to load next
+  uint4 x[2][kPasses];                           // K and V codes and scales of the tile in flight
+  uint32_t byte[2][kPasses];
+  auto load = [&](int v) {
+    const int64_t* st = v ? a.c.vst : a.c.kst;
+    const int64_t* ss = v ? a.c.vsst : a.c.ksst;
+    const uint8_t* src = (v ? a.c.v : a.c.k) + s.head * st[2] + chunk * 16;
+    const uint8_t* sc = (v ? a.c.vs : a.c.ks) + s.head * ss[2];
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const Place p = place_of(a, s.b, t * kKeys + r0 + i * kRows, s.start + s.rows);
+      x[v][i] = make_uint4(0, 0, 0, 0);
+      byte[v][i] = 127;
+      if (in_dim && p.page >= 0) {
+        x[v][i] = __ldg(reinterpret_cast<const uint4*>(src + p.page * st[0] + p.slot * st[1]));
+        byte[v][i] = __ldg(sc + p.page * ss[0] + p.slot * ss[1]);
+      }
+    }
+  };
+  if (more) {
+    load(0);
+    load(1);
+  }
+  for (int n = 0; more;) {
+    // the tile whose codes are in registers
+    const int pos0 = t * kKeys, start = s.start, this_seg = seg;
+    if (++t == s.t1) {
+      more = w.next(a, &s);
+      t = s.t0;
+      ++seg;
+    }
+#pragma unroll
+    for (int v = 0; v < 2; ++v, ++n) {
+      wait(sh, &sh->empty[n % L::kSlots], ((n / L::kSlots) & 1) ^ 1, a.status);
+      uint8_t* dst = ring + (n % L::kSlots) * L::kTile;
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
+        const int row = r0 + i * kRows;
+        uint4 y[2];
+        if (easy_scale<F16>(byte[v][i])) {
+          const uint32_t m = scale_mul2<F16>(byte[v][i]);
+          const uint2 c0 = scale_codes<F16>(x[v][i].x, m), c1 = scale_codes<F16>(x[v][i].y, m);
+          const uint2 c2 = scale_codes<F16>(x[v][i].z, m), c3 = scale_codes<F16>(x[v][i].w, m);
+          y[0] = make_uint4(c0.x, c0.y, c1.x, c1.y);
+          y[1] = make_uint4(c2.x, c2.y, c3.x, c3.y);
+        } else {
+          const uint2 c0 = scale_codes_any<F16>(x[v][i].x, byte[v][i]);
+          const uint2 c1 = scale_codes_any<F16>(x[v][i].y, byte[v][i]);
+          const uint2 c2 = scale_codes_any<F16>(x[v][i].z, byte[v][i]);
+          const uint2 c3 = scale_codes_any<F16>(x[v][i].w, byte[v][i]);
+          y[0] = make_uint4(c0.x, c0.y, c1.x, c1.y);
+          y[1] = make_uint4(c2.x, c2.y, c3.x, c3.y);
+          const int j = pos0 + row - start;
+          if (v && j >= 0) {
+            const bool b0 = zero_nonfinite<F16>(&y[0]), b1 = zero_nonfinite<F16>(&y[1]);
+            if (b0 || b1) atomicOr(&sh->bad[this_seg % kBadSets][j >> 5], 1u << (j & 31));
+          }
+        }
+        // the upper half of a row's chunks stores its odd chunk first: the two
+        // 64-element blocks lie in the same banks
+        const int odd = chunk >= 4 ? 1 : 0;
+        *reinterpret_cast<uint4*>(dst + tile_offset(row, 2 * chunk + odd)) = odd ? y[1] : y[0];
+        *reinterpret_cast<uint4*>(dst + tile_offset(row, 2 * chunk + 1 - odd)) = odd ? y[0] : y[1];
+      }
+      if (more) load(v);
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sh->full[n % L::kSlots]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------- MMA --
+
+template <bool F16, int DP>
+__device__ __forceinline__ void issue(const AttendArgs& a, uint8_t* smem, Tail* sh, int stream) {
+  using L = Layout<DP>;
+  constexpr uint32_t kTypes = F16 ? (1u << 7) | (1u << 10) : 0u;   // bf16 fields, cleared for f16
+  constexpr uint32_t kQK = ptx::idesc_bf16_f32(128, kKeys) & ~kTypes;
+  constexpr uint32_t kPV = (ptx::idesc_bf16_f32(128, DP) & ~kTypes) | (1u << 16);  // B N-major
+  const uint32_t tm_s = sh->tmem + stream * 128, tm_o = sh->tmem + 256 + stream * 128;
+  const uint32_t ring = ptx::smem_u32(smem + L::kRing);
+  Walker w;
+  Segment s;
+  w.init(a, sh);
+  uint32_t slot0 = 0, count = 0;                 // the segment's first slot; own tiles so far
+  for (uint32_t seg = 0; w.next(a, &s); ++seg) {
+    const bool pair = group_rows(a, s) > kKeys;
+    const int n = s.t1 - s.t0, step = pair ? 1 : 2;
+    const uint32_t q = ptx::smem_u32(smem) + (pair ? stream * L::kTile : 0);
+    wait(sh, &sh->q_full, seg & 1, a.status);
+    for (int i = pair ? 0 : stream; i < n; i += step, ++count) {
+      const uint32_t ks = slot0 + 2 * i, vs = ks + 1;
+      // S and P share columns: the last product that reads P is done first
+      if (count > 0) wait(sh, &sh->o_done[stream], (count - 1) & 1, a.status);
+      wait(sh, &sh->full[ks % L::kSlots], (ks / L::kSlots) & 1, a.status);
+      ptx::tc_fence_after();
+      const uint32_t k_addr = ring + (ks % L::kSlots) * L::kTile;
+#pragma unroll
+      for (int k = 0; k < DP / 16; ++k) {
+        const uint32_t at = (k / 4) * (kKeys * 128) + (k % 4) * 32;
+        ptx::tc_mma_smem(tm_s, ptx::smem_desc_swizzle128(q + at, 16, 1024),
+                         ptx::smem_desc_swizzle128(k_addr + at, 16, 1024), kQK, k > 0);
+      }
+      ptx::tc_commit(&sh->s_full[stream]);
+      ptx::tc_commit(&sh->empty[ks % L::kSlots]);
+      if (!pair) ptx::tc_commit(&sh->empty[ks % L::kSlots]);   // the other stream's share
+      wait(sh, &sh->full[vs % L::kSlots], (vs / L::kSlots) & 1, a.status);
+      wait(sh, &sh->p_full[stream], count & 1, a.status);
+      ptx::tc_fence_after();
+      const uint32_t v_addr = ring + (vs % L::kSlots) * L::kTile;
+#pragma unroll
+      for (int k = 0; k < kKeys / 16; ++k)
+        ptx::tc_mma_tmem_a(tm_o, tm_s + 8 * k,
+                           ptx::smem_desc_swizzle128(v_addr + k * 2048, kKeys * 128, 1024), kPV,
+                           i >= step || k > 0);
+      ptx::tc_commit(&sh->o_done[stream]);
+      ptx::tc_commit(&sh->empty[vs % L::kSlots]);
+      if (!pair) ptx::tc_commit(&sh->empty[vs % L::kSlots]);
+    }
+    slot0 += 2 * n;
+    ptx::mbar_arrive(&sh->q_empty);
+  }
+  if (count > 0) wait(sh, &sh->o_done[stream], (count - 1) & 1, a.status);
+}
+
+// --------------------------------------------------------------- softmax --
+
+template <bool F16, bool E4M3>
+__device__ __forceinline__ float value_at(const AttendArgs& a, const Segment& s, int pos, int d) {
+  const Place p = place_of(a, s.b, pos, s.start + s.rows);
+  if (p.page < 0) return 0.f;
+  const uint8_t* row = a.c.v + p.page * a.c.vst[0] + p.slot * a.c.vst[1] + s.head * a.c.vst[2];
+  if (!E4M3) return to_float<F16>(reinterpret_cast<const uint16_t*>(row)[d]);
+  const uint8_t byte = a.c.vs[p.page * a.c.vsst[0] + p.slot * a.c.vsst[1] + s.head * a.c.vsst[2]];
+  return saturate16<F16>(e4m3x2_to_float2(row[d]).x * scale_value(byte));
+}
+
+// Adds the non-finite elements of the draft rows of V that this row sees to
+// columns d0 .. d0 + 31 of its O: what 0 < p times them comes to.
+template <bool F16, bool E4M3>
+__device__ __noinline__ void add_nonfinite(const AttendArgs& a, const Segment& s,
+                                           const uint32_t* bad, int node, int d0, float* o) {
+  for (int w = 0; w < DSPARK_TREE_MAX_NODES / 32; ++w) {
+    uint32_t m = bad[w] != 0 ? bad[w] & sees_word(a, s, node, w) : 0u;
+    while (m != 0) {
+      const int j = 32 * w + __ffs(m) - 1;
+      m &= m - 1;
+      for (int d = 0; d < 32 && d0 + d < a.D; ++d) {
+        const float v = value_at<F16, E4M3>(a, s, s.start + j, d0 + d);
+        if (!isfinite(v)) o[d] += v;
+      }
+    }
+  }
+}
+
+template <bool F16, bool E4M3, int DP>
+__device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail* sh) {
+  using L = Layout<DP>;
+  constexpr float kShift = F16 ? 7.f : 0.f;
+  const int wg = threadIdx.x / 128, lane_row = threadIdx.x % 128;
+  const int warp = threadIdx.x / 32 % 4;
+  const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+  const uint32_t tm_s = sh->tmem + lanes + wg * 128;
+  const uint32_t tm_o = sh->tmem + lanes + 256;
+  const float sl2 = fabsf(a.scale) * kLog2e;
+  const bool cap = a.softcap > 0.f;
+  const float cap2 = a.softcap * kLog2e;
+  // tanh(y) = 1 - 2 / (e^(2y) + 1): 2 y log2(e) per raw score
+  const float cap_in = cap ? 2.f * sl2 / a.softcap : 0.f;
+  const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+  auto score = [&](float raw) {
+    return cap ? cap2 - 2.f * cap2 * rcp(ex2(raw * cap_in) + 1.f) : raw * sl2;
+  };
+  Walker w;
+  Segment s;
+  w.init(a, sh);
+  uint32_t count[2] = {0, 0};                    // tiles of the streams so far
+  for (uint32_t seg = 0; w.next(a, &s); ++seg) {
+    const int rows = group_rows(a, s);
+    const bool pair = rows > kKeys;
+    const int n = s.t1 - s.t0;
+    // Q into shared memory, all 256 threads, when both MMA threads are past the last
+    if (seg > 0) wait(sh, &sh->q_empty, (seg - 1) & 1, a.status);
+    {
+      constexpr int kChunks = DP / 8;
+      const int q_rows = pair ? kGroupRows : kKeys;
+      for (int i = threadIdx.x; i < q_rows * kChunks; i += 256) {
+        const int r = i / kChunks, chunk = i % kChunks;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (r < rows && chunk * 8 < a.D) {
+          const int gr = s.group * kGroupRows + r, nd = a.group.div(gr);
+          const uint8_t* src = a.q + (int64_t)(s.row0 + nd) * a.q_row +
+                               (int64_t)(s.head * a.G + gr - nd * a.G) * a.q_head;
+          x = __ldg(reinterpret_cast<const uint4*>(src) + chunk);
+          x.x ^= flip;
+          x.y ^= flip;
+          x.z ^= flip;
+          x.w ^= flip;
+        }
+        *reinterpret_cast<uint4*>(smem + (r / kKeys) * L::kTile + tile_offset(r % kKeys, chunk)) = x;
+      }
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (threadIdx.x % 32 == 0) ptx::mbar_arrive(&sh->q_full);
+    }
+    const int local = (pair ? wg * kKeys : 0) + lane_row;        // row of the group
+    const bool valid = local < rows;
+    const bool warp_valid = local - threadIdx.x % 32 < rows;
+    const int grow = s.group * kGroupRows + (valid ? local : 0);
+    const int node = a.group.div(grow);
+    float mref = -INFINITY, l = 0.f;
+    const int step = pair ? 1 : 2;
+    for (int i = pair ? 0 : wg; i < n; i += step) {
+      wait(sh, &sh->s_full[wg], count[wg] & 1, a.status);
+      ++count[wg];
+      ptx::tc_fence_after();
+      if (warp_valid) {
+        const int pos0 = (s.t0 + i) * kKeys;
+        const bool masked = pos0 + kKeys > s.start;
+        uint32_t see[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          see[c] = masked ? sees_32(a, s, node, pos0 + 32 * c) : 0xffffffffu;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          ptx::tmem_ld32(tm_s + 32 * c, v);
+          ptx::tmem_wait_ld32(v);
+          if (masked) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              mx = fmaxf(mx, (see[c] >> k) & 1 ? __uint_as_float(v[k]) : -INFINITY);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(v[k]));
+          }
+        }
+        const float x_max = mx == -INFINITY ? -INFINITY : score(mx);
+        // the first tile sets m; later ones move it when it has grown enough
+        const bool move = x_max > mref + (mref == -INFINITY ? 0.f : kShift + 8.f);
+        const float m_new = move ? x_max - kShift : mref;
+        if (i >= step && __any_sync(0xffffffffu, move)) {
+          const float back = mref == -INFINITY ? 0.f : ex2(mref - m_new);
+          l *= back;
+#pragma unroll
+          for (int c = 0; c < DP / 32; ++c) {
+            uint32_t v[32];
+            ptx::tmem_ld32(tm_o + wg * 128 + 32 * c, v);
+            ptx::tmem_wait_ld32(v);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * back);
+            ptx::tmem_st32(tm_o + wg * 128 + 32 * c, v);
+          }
+        }
+        mref = m_new;
+        const float sub = mref == -INFINITY ? 0.f : mref;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32], pk[16];
+          ptx::tmem_ld32(tm_s + 32 * c, v);
+          ptx::tmem_wait_ld32(v);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const float raw = __uint_as_float(v[k]);
+            float p = cap ? ex2(score(raw) - sub) : ex2(fmaf(raw, sl2, -sub));
+            if (masked) p = (see[c] >> k) & 1 ? p : 0.f;
+            sum[k & 3] += p;
+            v[k] = __float_as_uint(p);
+          }
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            pk[k] = pack2<F16>(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
+          ptx::tmem_st16(tm_s + 16 * c, pk);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+      }
+      __syncwarp();
+      if (threadIdx.x % 32 == 0) ptx::mbar_arrive(&sh->p_full[wg]);
+    }
+
+    // the segment's result
+    const int n0 = pair ? n : (n + 1) / 2, n1 = pair ? n : n / 2;
+    count[wg ^ 1] += wg ? n0 : n1;
+    if (count[0] > 0) wait(sh, &sh->o_done[0], (count[0] - 1) & 1, a.status);
+    if (count[1] > 0) wait(sh, &sh->o_done[1], (count[1] - 1) & 1, a.status);
+    if (!pair) sh->ml[wg][lane_row] = make_float2(mref, l);
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    ptx::tc_fence_after();
+    float w0 = 1.f, w1 = 0.f;                    // weights of the two streams' O
+    if (!pair) {
+      const float2 x0 = sh->ml[0][lane_row], x1 = sh->ml[1][lane_row];
+      mref = fmaxf(x0.x, x1.x);
+      const float sub = mref == -INFINITY ? 0.f : mref;
+      w0 = ex2(x0.x - sub);
+      w1 = n1 > 0 ? ex2(x1.x - sub) : 0.f;
+      l = w0 * x0.y + (n1 > 0 ? w1 * x1.y : 0.f);
+    }
+    const bool whole = s.t0 == 0 && s.t1 == s.tiles;
+    const int part = 2 * blockIdx.x + (s.t0 == 0 ? 1 : 0);
+    const uint32_t* bad = sh->bad[seg % kBadSets];
+    uint32_t any_bad = 0;
+#pragma unroll
+    for (int k = 0; k < DSPARK_TREE_MAX_NODES / 32; ++k) any_bad |= bad[k];
+    if (warp_valid) {
+      const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      const int64_t out_row = (int64_t)(s.row0 + node) * a.Hq + s.head * a.G + grow - node * a.G;
+      // pair: a group its own row tile, all columns; else both tiles, half the columns
+      const int c0 = pair ? 0 : wg * (DP / 64), c1 = pair ? DP / 32 : c0 + DP / 64;
+#pragma unroll 1
+      for (int c = c0; c < c1; ++c) {
+        uint32_t v[32];
+        float o[32];
+        ptx::tmem_ld32(tm_o + (pair ? wg * 128 : 0) + 32 * c, v);
+        ptx::tmem_wait_ld32(v);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) o[k] = __uint_as_float(v[k]) * w0;
+        if (!pair && n1 > 0) {
+          ptx::tmem_ld32(tm_o + 128 + 32 * c, v);
+          ptx::tmem_wait_ld32(v);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = fmaf(__uint_as_float(v[k]), w1, o[k]);
+        }
+        if (any_bad != 0) add_nonfinite<F16, E4M3>(a, s, bad, node, 32 * c, o);
+        if (valid && whole) {
+          uint4* dst = reinterpret_cast<uint4*>(a.out + out_row * a.D + 32 * c);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              x[e] = l == 0.f ? 0u : pack2<F16>(o[8 * k + 2 * e] * inv, o[8 * k + 2 * e + 1] * inv);
+            if (32 * c + 8 * k < a.D) dst[k] = make_uint4(x[0], x[1], x[2], x[3]);
+          }
+        } else if (valid) {
+          float4* dst = reinterpret_cast<float4*>(a.part_o) +
+                        ((int64_t)part * (DP / 4) + 8 * c) * a.part_rows + local;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            dst[(int64_t)k * a.part_rows] =
+                make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        }
+        __syncwarp();
+      }
+      if (valid && (pair || wg == 0)) {
+        if (!whole) a.part_ml[(int64_t)part * a.part_rows + local] = make_float2(mref, l);
+        else if (a.lse) a.lse[out_row] = l == 0.f ? -INFINITY : (mref + log2f(l)) * kLn2;
+      }
+    }
+    if (!whole && s.t0 == 0 && threadIdx.x == 0) {
+      // the item's other parts lie in the CTAs up to the one that holds its last unit
+      const int64_t last = s.item_end - 1;
+      const int n_cta = (int)(sh->total < a.n_cta ? sh->total : a.n_cta);
+      int c = (int)(last * n_cta / sh->total);
+      while (share(sh->total, n_cta, c + 1) <= last) ++c;
+      while (share(sh->total, n_cta, c) > last) --c;
+      a.part_of[blockIdx.x] = make_int4(s.b, s.head, s.group, c - (int)blockIdx.x + 1);
+    }
+    ptx::tc_fence_before();
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    if (any_bad != 0 && threadIdx.x < DSPARK_TREE_MAX_NODES / 32)
+      sh->bad[seg % kBadSets][threadIdx.x] = 0;
+  }
+}
+
+// This CTA's share of the units: sums the requests' units in order.
+__device__ __forceinline__ void plan(const AttendArgs& a, Tail* sh) {
+  constexpr int kPer = (DSPARK_TREE_MAX_REQUESTS + 511) / 512;
+  int64_t mine[kPer], sum = 0;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int per = (a.b.B + 511) / 512;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int b = threadIdx.x * per + k;
+    mine[k] = 0;
+    if (k < per && threadIdx.x < 512 && b < a.b.B) {
+      bool ok;
+      mine[k] = units_of(a, load_request(a, b, &ok));
+      if (!ok && blockIdx.x == 0) set_status(a.status, DSPARK_EPAGES);
+    }
+    sum += mine[k];
+  }
+  int64_t incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) sh->warp_sum[warp] = incl;
+  __syncthreads();
+  int64_t before = incl - sum, total = 0;
+#pragma unroll
+  for (int k = 0; k < kThreads / 32; ++k) {
+    const int64_t y = sh->warp_sum[k];
+    if (k < warp) before += y;
+    total += y;
+  }
+  const int n = (int)(total < a.n_cta ? total : a.n_cta);
+  const int cta = blockIdx.x;
+  const int64_t u0 = cta < n ? share(total, n, cta) : total;
+  const int64_t u1 = cta < n ? share(total, n, cta + 1) : total;
+  if (threadIdx.x == 0) {
+    sh->unit0 = u0;
+    sh->units = u1 - u0;
+    sh->total = total;
+  }
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    if (u1 > u0 && u0 >= before && u0 < before + mine[k]) {
+      sh->b0 = threadIdx.x * per + k;
+      sh->off0 = u0 - before;
+    }
+    before += mine[k];
+  }
+}
+
+template <bool F16, bool E4M3, int DP>
+__global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_constant__ AttendArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Tail* sh = reinterpret_cast<Tail*>(smem + Layout<DP>::kTail);
+  const int warp = threadIdx.x / 32;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (warp == kMmaWarp) {
+    ptx::tmem_alloc(&sh->tmem, 512);
+    ptx::tmem_relinquish();
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 8; ++i) {
+      ptx::mbar_init(&sh->full[i], kProdWarps);
+      ptx::mbar_init(&sh->empty[i], 2);
+    }
+    ptx::mbar_init(&sh->q_full, kSoftWarps);
+    ptx::mbar_init(&sh->q_empty, 2);
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&sh->s_full[i], 1);
+      ptx::mbar_init(&sh->p_full[i], 4);
+      ptx::mbar_init(&sh->o_done[i], 1);
+    }
+    ptx::fence_mbar_init();
+    sh->abort = 0;
+    a.part_of[blockIdx.x] = make_int4(0, 0, 0, 0);
+  }
+  for (int i = threadIdx.x; i < kBadSets * (DSPARK_TREE_MAX_NODES / 32); i += kThreads)
+    (&sh->bad[0][0])[i] = 0;
+  plan(a, sh);
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp < kSoftWarps) {
+    softmax<F16, E4M3, DP>(a, smem, sh);
+  } else if (warp < kMmaWarp) {
+    if (E4M3) produce8<F16, DP>(a, smem, sh);
+    else produce16<F16, DP>(a, smem, sh);
+  } else if (threadIdx.x % 32 == 0) {
+    issue<F16, DP>(a, smem, sh, warp - kMmaWarp);
+  }
+  __syncwarp();
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) ptx::tmem_dealloc(sh->tmem, 512);
+}
+
+// Joins the parts of the items that several CTAs share: block (c, y) takes rows
+// 32 y .. of the item whose first part CTA c left.  The parts are added in the
+// order of the keys, so the result does not depend on timing.
+constexpr int kJoinThreads = 256;
+
+template <bool F16, int DP>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttendArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 of = a.part_of[blockIdx.x];
+  if (of.w == 0) return;
+  bool ok;
+  const Request r = load_request(a, of.x, &ok);
+  const int local = blockIdx.y * 32 + threadIdx.x % 32;
+  const int grow = of.z * kGroupRows + local;
+  if (local >= kGroupRows || grow >= r.rows * a.G) return;
+  const int node = a.group.div(grow);
+  const int64_t out_row = (int64_t)(r.row0 + node) * a.Hq + of.y * a.G + grow - node * a.G;
+  const int p0 = 2 * blockIdx.x + 1, parts = of.w;
+  auto part = [&](int i) { return i == 0 ? p0 : p0 - 1 + 2 * i; };   // slot 0 of the later CTAs
+  float m = -INFINITY;
+#pragma unroll 4
+  for (int i = 0; i < parts; ++i)
+    m = fmaxf(m, a.part_ml[(int64_t)part(i) * a.part_rows + local].x);
+  const float sub = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+  constexpr int kEach = DP / 4 / (kJoinThreads / 32);       // float4 columns a thread
+  float4 o[kEach];
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int g0 = threadIdx.x / 32;
+#pragma unroll 2
+  for (int i = 0; i < parts; ++i) {
+    const float2 ml = a.part_ml[(int64_t)part(i) * a.part_rows + local];
+    const float w = ex2(ml.x - sub);
+    l = fmaf(ml.y, w, l);
+    const float4* src = reinterpret_cast<const float4*>(a.part_o) +
+                        (int64_t)part(i) * (DP / 4) * a.part_rows + local;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const float4 x = src[(int64_t)(g0 + k * (kJoinThreads / 32)) * a.part_rows];
+      o[k].x = fmaf(x.x, w, o[k].x);
+      o[k].y = fmaf(x.y, w, o[k].y);
+      o[k].z = fmaf(x.z, w, o[k].z);
+      o[k].w = fmaf(x.w, w, o[k].w);
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int d = 4 * (g0 + k * (kJoinThreads / 32));
+    if (d >= a.D) continue;
+    const uint2 y = l == 0.f ? make_uint2(0u, 0u)
+                             : make_uint2(pack2<F16>(o[k].x * inv, o[k].y * inv),
+                                          pack2<F16>(o[k].z * inv, o[k].w * inv));
+    *reinterpret_cast<uint2*>(a.out + out_row * a.D + d) = y;
+  }
+  if (g0 == 0 && a.lse) a.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+template <int DP>
+constexpr size_t smem_bytes() {
+  return Layout<DP>::kTail + sizeof(Tail);
+}
+
+template <bool F16, bool E4M3, int DP>
+cudaError_t launch(const AttendArgs& a, cudaStream_t stream) {
+  attend_kernel<F16, E4M3, DP><<<a.n_cta, kThreads, smem_bytes<DP>(), stream>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // the join may be set up while the main kernel runs; it waits for it itself
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(a.n_cta, (a.part_rows + 31) / 32);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<F16, DP>, a);
+}
+
+template <bool F16, int DP>
+cudaError_t setup() {
+  static_assert(smem_bytes<DP>() <= 232448, "shared memory of an SM");
+  cudaError_t e = cudaFuncSetAttribute(attend_kernel<F16, false, DP>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)smem_bytes<DP>());
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(attend_kernel<F16, true, DP>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<DP>());
 }
 
 }  // namespace
 
+cudaError_t attend_setup(bool f16, int D) {
+  if (padded_dim(D) == 64) return f16 ? setup<true, 64>() : setup<false, 64>();
+  return f16 ? setup<true, 128>() : setup<false, 128>();
+}
+
 cudaError_t attend_launch(const AttendArgs& a, bool f16, bool e4m3, cudaStream_t stream) {
-  const dim3 grid(a.b.N, a.Hq);
-  if (f16 && e4m3) attend_kernel<true, true><<<grid, kThreads, 0, stream>>>(a);
-  else if (f16) attend_kernel<true, false><<<grid, kThreads, 0, stream>>>(a);
-  else if (e4m3) attend_kernel<false, true><<<grid, kThreads, 0, stream>>>(a);
-  else attend_kernel<false, false><<<grid, kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  const int sel = (f16 ? 4 : 0) + (e4m3 ? 2 : 0) + (padded_dim(a.D) == 128 ? 1 : 0);
+  switch (sel) {
+    case 0: return launch<false, false, 64>(a, stream);
+    case 1: return launch<false, false, 128>(a, stream);
+    case 2: return launch<false, true, 64>(a, stream);
+    case 3: return launch<false, true, 128>(a, stream);
+    case 4: return launch<true, false, 64>(a, stream);
+    case 5: return launch<true, false, 128>(a, stream);
+    case 6: return launch<true, true, 64>(a, stream);
+    default: return launch<true, true, 128>(a, stream);
+  }
 }
 
 }  // namespace tree

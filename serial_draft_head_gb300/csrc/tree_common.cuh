@@ -128,9 +128,22 @@ struct AttendArgs {
   float* lse;
   int Hq, Hkv, G, D;
   int max_nodes;
+  FastDiv group;             // by G
+  int n_cta;
+  // partial results of items that several CTAs share: per CTA two parts of
+  // part_rows rows: O (fp32, [D / 4][part_rows][4]) and {m, l} a row
+  float* part_o;
+  float2* part_ml;
+  int4* part_of;             // per CTA: {request, head << 8 | row group, parts, 0} it starts
+  int part_rows;
   int* status;
 };
 
+// Head dimension as the kernel lays it out, and rows of one part.
+inline int padded_dim(int D) { return D <= 64 ? 64 : 128; }
+constexpr int kGroupRows = 256;    // rows (nodes x heads of one group) of a work item
+
+cudaError_t attend_setup(bool f16, int D);
 cudaError_t attend_launch(const AttendArgs& a, bool f16, bool e4m3, cudaStream_t stream);
 
 // Packed rows of the cache calls: strides in bytes.
