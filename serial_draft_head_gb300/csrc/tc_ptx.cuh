@@ -61,6 +61,31 @@ __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t by
       : "memory");
 }
 
+// 4-D tiled copy global -> shared of the box of `map` at coordinates (x, y, z, w);
+// x times the element size is a multiple of 16 bytes.  Coordinates outside the
+// tensor read zeros.
+__device__ __forceinline__ void tma_load_4d(void* dst, const void* map, int x, int y, int z, int w,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void prefetch_tensormap(const void* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
+// 16-byte read-only global load that leaves L1 to others.
+__device__ __forceinline__ uint4 ldg_nc_na(const void* p) {
+  uint4 x;
+  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+      : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+      : "l"(p));
+  return x;
+}
+
 // L2 eviction policies for the cache-hinted loads below: lines fetched under
 // evict_last are the last candidates for eviction, under evict_first the first.
 __device__ __forceinline__ uint64_t policy_evict_last() {

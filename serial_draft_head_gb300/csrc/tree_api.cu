@@ -1,5 +1,6 @@
 // tree_api.cu -- the C ABI of include/dspark_tree.h: argument checks, the
 // handle's device memory, and the launches.
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -20,6 +21,7 @@ struct dspark_tree {
   float2* part_ml = nullptr;
   int4* part_of = nullptr;
   int part_rows = 0;
+  PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
 };
 
 namespace {
@@ -66,6 +68,34 @@ int make_cache(const dspark_tree* h, const dspark_tree_cache* c, CacheView* out)
   out->n_pages = c->n_pages;
   out->page = FastDiv::of(c->page_size);
   return DSPARK_OK;
+}
+
+// Tiled-copy maps of a 16-bit cache whose pages cut a 128-key tile evenly (a
+// page is a whole number of tiles, or a tile a whole number of pages of at
+// least 16 slots).  Others, and strides the maps do not take, have none.
+void make_maps(const dspark_tree* h, const dspark_tree_cache* c, const CacheView& v, TileMaps* m) {
+  m->rows = 0;
+  const int page = c->page_size;
+  if (c->type == DSPARK_TYPE_E4M3 || !h->encode) return;
+  if (!(page % 128 == 0 || (page >= 16 && 128 % page == 0))) return;
+  const cuuint64_t dims[4] = {(cuuint64_t)h->cfg.head_dim, (cuuint64_t)page,
+                              (cuuint64_t)h->cfg.kv_heads, (cuuint64_t)c->n_pages};
+  const cuuint32_t box[4] = {64, (cuuint32_t)(page < 128 ? page : 128), 1, 1};
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  const CUtensorMapDataType type = c->type == DSPARK_TYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                               : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  for (int i = 0; i < 2; ++i) {
+    const int64_t* st = i ? v.vst : v.kst;
+    const cuuint64_t strides[3] = {(cuuint64_t)st[1], (cuuint64_t)st[2], (cuuint64_t)st[0]};
+    for (int d = 0; d < 3; ++d)
+      if (strides[d] == 0 || strides[d] >= ((cuuint64_t)1 << 40)) return;
+    if (h->encode(i ? &m->v : &m->k, type, 4, i ? v.v : v.k, dims, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return;
+  }
+  m->rows = (int)box[1];
 }
 
 int make_batch(const dspark_tree_batch* b, int page_size, bool rows, BatchView* out) {
@@ -132,6 +162,14 @@ int dspark_tree_create(const dspark_tree_config* cfg, dspark_tree_t* out) {
     e = cudaMalloc(&h->status, sizeof(int));
   }
   if (e == cudaSuccess) e = cudaMemset(h->status, 0, sizeof(int));
+  if (e == cudaSuccess) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
+    e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                         &found);
+    if (e == cudaSuccess && found == cudaDriverEntryPointSuccess)
+      h->encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }
   if (e == cudaSuccess) e = attend_setup(cfg->type == DSPARK_TYPE_F16, cfg->head_dim);
   if (e != cudaSuccess) {
     dspark_tree_destroy(h);
@@ -249,7 +287,9 @@ int dspark_tree_attend(dspark_tree_t h, const dspark_tree_cache* cache,
   a.part_of = h->part_of;
   a.part_rows = h->part_rows;
   a.status = h->status;
-  return cuda_code(attend_launch(a, h->cfg.type == DSPARK_TYPE_F16,
+  TileMaps maps;
+  make_maps(h, cache, a.c, &maps);
+  return cuda_code(attend_launch(a, maps, h->cfg.type == DSPARK_TYPE_F16,
                                  cache->type == DSPARK_TYPE_E4M3,
                                  static_cast<cudaStream_t>(stream)));
 }

@@ -86,21 +86,28 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 }
 
 // Every wait ends: past the limit the CTA's abort flag makes all its waits
-// return at once, the loops run on (all accesses stay in bounds), and the
-// status says so.
+// return at once, the loops run on without starting copies or products (all
+// accesses stay in bounds), and the status says so.
+//
+// A parity wait tells a phase from the next one only, so whoever waits on a
+// barrier waits for each of its phases in order.
 __device__ __forceinline__ void wait(Tail* s, uint64_t* bar, uint32_t parity, int* status) {
   if (ptx::mbar_try_wait(bar, parity)) return;
   const uint64_t t0 = globaltimer_ns();
   uint32_t spins = 0;
   while (!ptx::mbar_try_wait(bar, parity)) {
     if ((++spins & 63u) != 0u) continue;
-    if (*(volatile int*)&s->abort) return;
+    if (*(const volatile int*)&s->abort) return;
     if (globaltimer_ns() - t0 > kWaitLimitNs) {
       *(volatile int*)&s->abort = 1;
       set_status(status, DSPARK_ETIMEOUT);
       return;
     }
   }
+}
+
+__device__ __forceinline__ bool aborted(const Tail* s) {
+  return *(const volatile int*)&s->abort != 0;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -330,22 +337,62 @@ __device__ __forceinline__ Place place_of(const AttendArgs& a, int b, int pos, i
   return p;
 }
 
+// A tile of the CTA's share, in order.
+struct Cursor {
+  Walker w;
+  Segment s;
+  int t, seg;
+  bool more;
+
+  __device__ void init(const AttendArgs& a, const Tail* sh) {
+    w.init(a, sh);
+    more = w.next(a, &s);
+    t = s.t0;
+    seg = 0;
+  }
+  __device__ void next(const AttendArgs& a) {
+    if (++t < s.t1) return;
+    more = w.next(a, &s);
+    t = s.t0;
+    ++seg;
+  }
+};
+
+// 16-bit cache.  Tiles of context go by tiled copies, lane 0 of every warp
+// issuing its share of the boxes; tiles that reach into the draft (the last of
+// a request), and all tiles without a map, by 16-byte copies of the threads,
+// completed two slots later, so that rows past the end are zero and draft rows
+// of V can be looked through.
 template <bool F16, int DP>
-__device__ __forceinline__ void produce16(const AttendArgs& a, uint8_t* smem, Tail* sh) {
+__device__ __forceinline__ void produce16(const AttendArgs& a, const TileMaps& maps, uint8_t* smem,
+                                          Tail* sh) {
   using L = Layout<DP>;
   constexpr int kChunks = DP / 8;                // 16-byte chunks of a row
   constexpr int kRows = kProd / kChunks;         // rows a pass
   constexpr int kPasses = kKeys / kRows;
-  const int tid = threadIdx.x - kSoftWarps * 32, lane = threadIdx.x % 32;
+  const int tid = threadIdx.x - kSoftWarps * 32, lane = threadIdx.x % 32, warp = tid / 32;
   const int chunk = tid % kChunks, r0 = tid / kChunks;
   const bool in_dim = chunk * 8 < a.D;
+  const int pieces = maps.rows > 0 ? kKeys / maps.rows : 1;      // boxes along a tile's keys
+  const int piece = warp % pieces;               // this warp's, in one or two 64-element blocks
+  const int boxes = pieces * (DP / 64);
   uint8_t* ring = smem + L::kRing;
-  Walker w;
-  Segment s;
-  w.init(a, sh);
-  int n = 0, seg = 0;                            // slots issued, segments begun
+  Cursor c;
+  c.init(a, sh);
+  if (!c.more) return;
+  // the page of this warp's piece of the tile at the cursor, fetched a tile ahead
+  auto piece_page = [&]() {
+    const int pos = c.t * kKeys + piece * maps.rows;
+    int page = -1;
+    if (maps.rows > 0 && lane == 0 && c.more && (c.t + 1) * kKeys <= c.s.start)
+      page = __ldg(a.b.pages + (int64_t)c.s.b * a.b.pages_stride + a.c.page.div(pos));
+    return page;
+  };
+  int page_next = piece_page();
+  int n = 0;                                     // slots issued
+  uint32_t copied = 0;                           // bit i: slot n - 1 - i went by 16-byte copies
   // the V tile in flight: where it is and which of its positions are draft
-  int prev_pos = 0, prev_start = 0x7fffffff, prev_total = 0, prev_seg = 0;
+  int prev_pos = 0, prev_start = 0, prev_total = 0, prev_seg = 0;
   auto complete = [&](int slot, bool v) {        // slot's copies of this thread have landed
     if (v && prev_pos + kKeys > prev_start) {
 #pragma unroll 1
@@ -366,90 +413,125 @@ __device__ __forceinline__ void produce16(const AttendArgs& a, uint8_t* smem, Ta
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(&sh->full[slot % L::kSlots]);
   };
-  for (; w.next(a, &s); ++seg) {
-    const int total = s.start + s.rows;
-    for (int t = s.t0; t < s.t1; ++t) {
-      Place p[kPasses];
+  while (c.more) {
+    const int b = c.s.b, head = c.s.head, start = c.s.start, total = start + c.s.rows;
+    const int pos0 = c.t * kKeys, seg = c.seg, page = page_next;
+    c.next(a);
+    page_next = piece_page();
+    const bool tiled = maps.rows > 0 && pos0 + kKeys <= start;
+    Place p[kPasses];
+    if (!tiled) {
 #pragma unroll
-      for (int i = 0; i < kPasses; ++i)
-        p[i] = place_of(a, s.b, t * kKeys + r0 + i * kRows, total);
+      for (int i = 0; i < kPasses; ++i) p[i] = place_of(a, b, pos0 + r0 + i * kRows, total);
+    }
 #pragma unroll
-      for (int v = 0; v < 2; ++v, ++n) {
+    for (int v = 0; v < 2; ++v, ++n) {
+      uint64_t* full = &sh->full[n % L::kSlots];
+      uint8_t* dst = ring + (n % L::kSlots) * L::kTile;
+      if (tiled) {
+        if (lane == 0) {
+          wait(sh, &sh->empty[n % L::kSlots], ((n / L::kSlots) & 1) ^ 1, a.status);
+          // after an abort no copy may outlive the CTA: none is started
+          if (warp < boxes && !aborted(sh)) {
+            const bool two = boxes > kProdWarps;
+            ptx::mbar_expect_tx(full, (two ? 2 : 1) * maps.rows * 128);
+            const bool bad = (uint32_t)page >= (uint64_t)a.c.n_pages;
+            if (bad) set_status(a.status, DSPARK_EPAGES);
+            const int w = bad ? (int)a.c.n_pages : page;         // past the end: zeros
+            const int pos = pos0 + piece * maps.rows;
+            const int slot = pos - a.c.page.div(pos) * a.c.page.d;
+            for (int bx = warp; bx < boxes; bx += kProdWarps)
+              ptx::tma_load_4d(dst + (bx / pieces) * (kKeys * 128) + piece * maps.rows * 128,
+                               v ? &maps.v : &maps.k, (bx / pieces) * 64, slot, head, w, full);
+          } else {
+            ptx::mbar_arrive(full);
+          }
+        }
+        __syncwarp();
+      } else {
         wait(sh, &sh->empty[n % L::kSlots], ((n / L::kSlots) & 1) ^ 1, a.status);
-        uint8_t* dst = ring + (n % L::kSlots) * L::kTile;
         const int64_t* st = v ? a.c.vst : a.c.kst;
-        const uint8_t* src = (v ? a.c.v : a.c.k) + s.head * st[2] + chunk * 16;
+        const uint8_t* src = (v ? a.c.v : a.c.k) + head * st[2] + chunk * 16;
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
           const bool on = in_dim && p[i].page >= 0;
           const uint8_t* from = on ? src + p[i].page * st[0] + p[i].slot * st[1] : a.c.k;
           ptx::cp_async16_or_zero(dst + tile_offset(r0 + i * kRows, chunk), from, on);
         }
-        ptx::cp_async_commit();
-        if (n >= kLag) {
-          ptx::cp_async_wait_group<kLag>();
-          complete(n - kLag, v);
-        }
       }
-      prev_pos = t * kKeys;
-      prev_start = s.start;
-      prev_total = total;
-      prev_seg = seg;
+      ptx::cp_async_commit();
+      if (copied >> (kLag - 1) & 1) {
+        ptx::cp_async_wait_group<kLag>();
+        complete(n - kLag, v);
+      }
+      copied = copied << 1 | (tiled ? 0u : 1u);
     }
+    prev_pos = pos0;
+    prev_start = start;
+    prev_total = total;
+    prev_seg = seg;
   }
-  if (n > 0) {
-    ptx::cp_async_wait_group<1>();
+  ptx::cp_async_wait_group<0>();
+  if (copied & 1) {
     complete(n - 2, false);
-    ptx::cp_async_wait_group<0>();
     complete(n - 1, true);
   }
 }
 
+// e4m3 cache, through registers.  The tile after the one being converted is in
+// flight in registers, and the rows of the kAhead tiles after that are asked
+// for in L2.
 template <bool F16, int DP>
 __device__ __forceinline__ void produce8(const AttendArgs& a, uint8_t* smem, Tail* sh) {
   using L = Layout<DP>;
   constexpr int kChunks = DP / 16;               // 16-code chunks of a row
   constexpr int kRows = kProd / kChunks;
   constexpr int kPasses = kKeys / kRows;
+  constexpr int kAhead = 4;
+  static_assert(kProd == 2 * kKeys, "one row of K or V a thread");
   const int tid = threadIdx.x - kSoftWarps * 32, lane = threadIdx.x % 32;
   const int chunk = tid % kChunks, r0 = tid / kChunks;
   const bool in_dim = chunk * 16 < a.D;
   uint8_t* ring = smem + L::kRing;
-  Walker w;
-  Segment s;
-  w.init(a, sh);
-  bool more = w.next(a, &s);
-  int t = s.t0, seg = 0;                         // the tile to load next
+  Cursor c, far;                                 // the tile to load next; to ask L2 for next
+  c.init(a, sh);
+  if (!c.more) return;
+  far.init(a, sh);
+  auto ask = [&]() {
+    if (!far.more) return;
+    const bool v = tid >= kKeys;
+    const int64_t* st = v ? a.c.vst : a.c.kst;
+    const Place p = place_of(a, far.s.b, far.t * kKeys + tid % kKeys, far.s.start + far.s.rows);
+    if (p.page >= 0)
+      ptx::prefetch_l2((v ? a.c.v : a.c.k) + p.page * st[0] + p.slot * st[1] + far.s.head * st[2]);
+    far.next(a);
+  };
   uint4 x[2][kPasses];                           // K and V codes and scales of the tile in flight
   uint32_t byte[2][kPasses];
   auto load = [&](int v) {
     const int64_t* st = v ? a.c.vst : a.c.kst;
     const int64_t* ss = v ? a.c.vsst : a.c.ksst;
-    const uint8_t* src = (v ? a.c.v : a.c.k) + s.head * st[2] + chunk * 16;
-    const uint8_t* sc = (v ? a.c.vs : a.c.ks) + s.head * ss[2];
+    const uint8_t* src = (v ? a.c.v : a.c.k) + c.s.head * st[2] + chunk * 16;
+    const uint8_t* sc = (v ? a.c.vs : a.c.ks) + c.s.head * ss[2];
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-      const Place p = place_of(a, s.b, t * kKeys + r0 + i * kRows, s.start + s.rows);
+      const Place p = place_of(a, c.s.b, c.t * kKeys + r0 + i * kRows, c.s.start + c.s.rows);
       x[v][i] = make_uint4(0, 0, 0, 0);
       byte[v][i] = 127;
       if (in_dim && p.page >= 0) {
-        x[v][i] = __ldg(reinterpret_cast<const uint4*>(src + p.page * st[0] + p.slot * st[1]));
+        x[v][i] = ptx::ldg_nc_na(src + p.page * st[0] + p.slot * st[1]);
         byte[v][i] = __ldg(sc + p.page * ss[0] + p.slot * ss[1]);
       }
     }
   };
-  if (more) {
-    load(0);
-    load(1);
-  }
-  for (int n = 0; more;) {
+  load(0);
+  load(1);
+#pragma unroll 1
+  for (int i = 0; i <= kAhead; ++i) ask();
+  for (int n = 0; c.more;) {
     // the tile whose codes are in registers
-    const int pos0 = t * kKeys, start = s.start, this_seg = seg;
-    if (++t == s.t1) {
-      more = w.next(a, &s);
-      t = s.t0;
-      ++seg;
-    }
+    const int pos0 = c.t * kKeys, start = c.s.start, this_seg = c.seg;
+    c.next(a);
 #pragma unroll
     for (int v = 0; v < 2; ++v, ++n) {
       wait(sh, &sh->empty[n % L::kSlots], ((n / L::kSlots) & 1) ^ 1, a.status);
@@ -483,10 +565,11 @@ __device__ __forceinline__ void produce8(const AttendArgs& a, uint8_t* smem, Tai
         *reinterpret_cast<uint4*>(dst + tile_offset(row, 2 * chunk + odd)) = odd ? y[1] : y[0];
         *reinterpret_cast<uint4*>(dst + tile_offset(row, 2 * chunk + 1 - odd)) = odd ? y[0] : y[1];
       }
-      if (more) load(v);
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&sh->full[n % L::kSlots]);
+      if (c.more) load(v);
+      if (v == 0) ask();
     }
   }
 }
@@ -510,34 +593,44 @@ __device__ __forceinline__ void issue(const AttendArgs& a, uint8_t* smem, Tail* 
     const int n = s.t1 - s.t0, step = pair ? 1 : 2;
     const uint32_t q = ptx::smem_u32(smem) + (pair ? stream * L::kTile : 0);
     wait(sh, &sh->q_full, seg & 1, a.status);
-    for (int i = pair ? 0 : stream; i < n; i += step, ++count) {
+    for (int i = 0; i < n; ++i) {
       const uint32_t ks = slot0 + 2 * i, vs = ks + 1;
+      if (!pair && (i & 1) != stream) {          // the other stream's tile: its phases pass
+        wait(sh, &sh->full[ks % L::kSlots], (ks / L::kSlots) & 1, a.status);
+        wait(sh, &sh->full[vs % L::kSlots], (vs / L::kSlots) & 1, a.status);
+        continue;
+      }
       // S and P share columns: the last product that reads P is done first
       if (count > 0) wait(sh, &sh->o_done[stream], (count - 1) & 1, a.status);
       wait(sh, &sh->full[ks % L::kSlots], (ks / L::kSlots) & 1, a.status);
-      ptx::tc_fence_after();
-      const uint32_t k_addr = ring + (ks % L::kSlots) * L::kTile;
+      if (!aborted(sh)) {
+        ptx::tc_fence_after();
+        const uint32_t k_addr = ring + (ks % L::kSlots) * L::kTile;
 #pragma unroll
-      for (int k = 0; k < DP / 16; ++k) {
-        const uint32_t at = (k / 4) * (kKeys * 128) + (k % 4) * 32;
-        ptx::tc_mma_smem(tm_s, ptx::smem_desc_swizzle128(q + at, 16, 1024),
-                         ptx::smem_desc_swizzle128(k_addr + at, 16, 1024), kQK, k > 0);
+        for (int k = 0; k < DP / 16; ++k) {
+          const uint32_t at = (k / 4) * (kKeys * 128) + (k % 4) * 32;
+          ptx::tc_mma_smem(tm_s, ptx::smem_desc_swizzle128(q + at, 16, 1024),
+                           ptx::smem_desc_swizzle128(k_addr + at, 16, 1024), kQK, k > 0);
+        }
+        ptx::tc_commit(&sh->s_full[stream]);
+        ptx::tc_commit(&sh->empty[ks % L::kSlots]);
+        if (!pair) ptx::tc_commit(&sh->empty[ks % L::kSlots]);   // the other stream's share
       }
-      ptx::tc_commit(&sh->s_full[stream]);
-      ptx::tc_commit(&sh->empty[ks % L::kSlots]);
-      if (!pair) ptx::tc_commit(&sh->empty[ks % L::kSlots]);   // the other stream's share
       wait(sh, &sh->full[vs % L::kSlots], (vs / L::kSlots) & 1, a.status);
       wait(sh, &sh->p_full[stream], count & 1, a.status);
-      ptx::tc_fence_after();
-      const uint32_t v_addr = ring + (vs % L::kSlots) * L::kTile;
+      if (!aborted(sh)) {
+        ptx::tc_fence_after();
+        const uint32_t v_addr = ring + (vs % L::kSlots) * L::kTile;
 #pragma unroll
-      for (int k = 0; k < kKeys / 16; ++k)
-        ptx::tc_mma_tmem_a(tm_o, tm_s + 8 * k,
-                           ptx::smem_desc_swizzle128(v_addr + k * 2048, kKeys * 128, 1024), kPV,
-                           i >= step || k > 0);
-      ptx::tc_commit(&sh->o_done[stream]);
-      ptx::tc_commit(&sh->empty[vs % L::kSlots]);
-      if (!pair) ptx::tc_commit(&sh->empty[vs % L::kSlots]);
+        for (int k = 0; k < kKeys / 16; ++k)
+          ptx::tc_mma_tmem_a(tm_o, tm_s + 8 * k,
+                             ptx::smem_desc_swizzle128(v_addr + k * 2048, kKeys * 128, 1024), kPV,
+                             i >= step || k > 0);
+        ptx::tc_commit(&sh->o_done[stream]);
+        ptx::tc_commit(&sh->empty[vs % L::kSlots]);
+        if (!pair) ptx::tc_commit(&sh->empty[vs % L::kSlots]);
+      }
+      ++count;
     }
     slot0 += 2 * n;
     ptx::mbar_arrive(&sh->q_empty);
@@ -575,28 +668,158 @@ __device__ __noinline__ void add_nonfinite(const AttendArgs& a, const Segment& s
   }
 }
 
-template <bool F16, bool E4M3, int DP>
+// Two fp32 lanes at once.
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t x, float* lo, float* hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Raw scores to base-2 exponents.
+struct Score {
+  float sl2;        // |scale| log2(e)
+  float cap2;       // softcap log2(e)
+  float cap_in;     // 2 sl2 / softcap: tanh(y) = 1 - 2 / (2^(2 y log2(e)) + 1)
+};
+
+template <bool CAP>
+__device__ __forceinline__ float exponent(const Score& sc, float raw) {
+  return CAP ? sc.cap2 - 2.f * sc.cap2 * rcp(ex2(raw * sc.cap_in) + 1.f) : raw * sc.sl2;
+}
+
+// The largest raw score of the row's 128 (of those it sees).
+template <bool MASKED>
+__device__ __forceinline__ float tile_max(uint32_t tm_s, const uint32_t (&see)[4]) {
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t v[2][32];
+    ptx::tmem_ld32(tm_s + 64 * h, v[0]);
+    ptx::tmem_ld32(tm_s + 64 * h + 32, v[1]);
+    ptx::tmem_wait_ld32(v[0]);
+    ptx::tmem_wait_ld32(v[1]);
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        float x = __uint_as_float(v[c][k]);
+        if (MASKED) x = (see[2 * h + c] >> k) & 1 ? x : -INFINITY;
+        mx[k & 3] = fmaxf(mx[k & 3], x);
+      }
+  }
+  return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+}
+
+// Weights 2^(x - sub) of the row's 128 keys over their scores, rounded to the
+// 16-bit type; returns the sum of the unrounded ones.
+template <bool F16, bool CAP, bool MASKED>
+__device__ __forceinline__ float tile_weights(const Score& sc, uint32_t tm_s,
+                                              const uint32_t (&see)[4], float sub) {
+  uint64_t sum[2] = {0, 0};
+  const uint64_t mul = pack_f32x2(sc.sl2, sc.sl2), neg = pack_f32x2(-sub, -sub);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t v[2][32];
+    ptx::tmem_ld32(tm_s + 64 * h, v[0]);
+    ptx::tmem_ld32(tm_s + 64 * h + 32, v[1]);
+    ptx::tmem_wait_ld32(v[0]);
+    ptx::tmem_wait_ld32(v[1]);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      uint32_t pk[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const float r0 = __uint_as_float(v[c][2 * k]), r1 = __uint_as_float(v[c][2 * k + 1]);
+        float p0, p1;
+        if (CAP) {
+          p0 = exponent<true>(sc, r0) - sub;
+          p1 = exponent<true>(sc, r1) - sub;
+        } else {
+          unpack_f32x2(fma_f32x2(pack_f32x2(r0, r1), mul, neg), &p0, &p1);
+        }
+        p0 = ex2(p0);
+        p1 = ex2(p1);
+        if (MASKED) {
+          p0 = (see[2 * h + c] >> (2 * k)) & 1 ? p0 : 0.f;
+          p1 = (see[2 * h + c] >> (2 * k + 1)) & 1 ? p1 : 0.f;
+        }
+        sum[k & 1] = add_f32x2(sum[k & 1], pack_f32x2(p0, p1));
+        pk[k] = pack2<F16>(p0, p1);
+      }
+      ptx::tmem_st16(tm_s + 32 * h + 16 * c, pk);
+    }
+  }
+  float a, b;
+  unpack_f32x2(add_f32x2(sum[0], sum[1]), &a, &b);
+  return a + b;
+}
+
+// O of this row times `back`.
+template <int DP>
+__device__ __forceinline__ void scale_row(uint32_t tm_o, float back) {
+#pragma unroll 1
+  for (int c = 0; c < DP / 32; ++c) {
+    uint32_t v[32];
+    ptx::tmem_ld32(tm_o + 32 * c, v);
+    ptx::tmem_wait_ld32(v);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * back);
+    ptx::tmem_st32(tm_o + 32 * c, v);
+  }
+}
+
+// One tile of one row: S in tensor memory becomes P, m and l move on, O is
+// rescaled if m moved.
+template <bool F16, bool CAP, bool MASKED, int DP>
+__device__ __forceinline__ void softmax_tile(const Score& sc, uint32_t tm_s, uint32_t tm_o,
+                                             const uint32_t (&see)[4], bool first, float* mref,
+                                             float* l) {
+  constexpr float kShift = F16 ? 7.f : 0.f;
+  const float mx = tile_max<MASKED>(tm_s, see);
+  const float x_max = mx == -INFINITY ? -INFINITY : exponent<CAP>(sc, mx);
+  // the first visible key sets m; later ones move it when it has grown enough
+  const bool move = x_max > *mref + (*mref == -INFINITY ? 0.f : kShift + 8.f);
+  const float m_new = move ? x_max - kShift : *mref;
+  if (!first && __any_sync(0xffffffffu, move)) {
+    const float back = *mref == -INFINITY ? 0.f : ex2(*mref - m_new);
+    *l *= back;
+    scale_row<DP>(tm_o, back);
+  }
+  *mref = m_new;
+  *l += tile_weights<F16, CAP, MASKED>(sc, tm_s, see, m_new == -INFINITY ? 0.f : m_new);
+  ptx::tmem_wait_st();
+}
+
+template <bool F16, bool E4M3, bool CAP, int DP>
 __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail* sh) {
   using L = Layout<DP>;
-  constexpr float kShift = F16 ? 7.f : 0.f;
   const int wg = threadIdx.x / 128, lane_row = threadIdx.x % 128;
   const int warp = threadIdx.x / 32 % 4;
   const uint32_t lanes = (uint32_t)(warp * 32) << 16;
   const uint32_t tm_s = sh->tmem + lanes + wg * 128;
   const uint32_t tm_o = sh->tmem + lanes + 256;
-  const float sl2 = fabsf(a.scale) * kLog2e;
-  const bool cap = a.softcap > 0.f;
-  const float cap2 = a.softcap * kLog2e;
-  // tanh(y) = 1 - 2 / (e^(2y) + 1): 2 y log2(e) per raw score
-  const float cap_in = cap ? 2.f * sl2 / a.softcap : 0.f;
+  Score sc;
+  sc.sl2 = fabsf(a.scale) * kLog2e;
+  sc.cap2 = a.softcap * kLog2e;
+  sc.cap_in = CAP ? 2.f * sc.sl2 / a.softcap : 0.f;
   const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
-  auto score = [&](float raw) {
-    return cap ? cap2 - 2.f * cap2 * rcp(ex2(raw * cap_in) + 1.f) : raw * sl2;
-  };
   Walker w;
   Segment s;
   w.init(a, sh);
-  uint32_t count[2] = {0, 0};                    // tiles of the streams so far
+  uint32_t count = 0;                            // tiles of this stream so far
   for (uint32_t seg = 0; w.next(a, &s); ++seg) {
     const int rows = group_rows(a, s);
     const bool pair = rows > kKeys;
@@ -633,71 +856,22 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
     float mref = -INFINITY, l = 0.f;
     const int step = pair ? 1 : 2;
     for (int i = pair ? 0 : wg; i < n; i += step) {
-      wait(sh, &sh->s_full[wg], count[wg] & 1, a.status);
-      ++count[wg];
+      wait(sh, &sh->s_full[wg], count & 1, a.status);
+      ++count;
       ptx::tc_fence_after();
       if (warp_valid) {
         const int pos0 = (s.t0 + i) * kKeys;
         const bool masked = pos0 + kKeys > s.start;
         uint32_t see[4];
+        const uint32_t own_o = tm_o + wg * 128;
+        const bool first = i < step;
+        if (!masked && !CAP) {
+          softmax_tile<F16, false, false, DP>(sc, tm_s, own_o, see, first, &mref, &l);
+        } else {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          see[c] = masked ? sees_32(a, s, node, pos0 + 32 * c) : 0xffffffffu;
-        float mx = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[32];
-          ptx::tmem_ld32(tm_s + 32 * c, v);
-          ptx::tmem_wait_ld32(v);
-          if (masked) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              mx = fmaxf(mx, (see[c] >> k) & 1 ? __uint_as_float(v[k]) : -INFINITY);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(v[k]));
-          }
+          for (int c = 0; c < 4; ++c) see[c] = sees_32(a, s, node, pos0 + 32 * c);
+          softmax_tile<F16, CAP, true, DP>(sc, tm_s, own_o, see, first, &mref, &l);
         }
-        const float x_max = mx == -INFINITY ? -INFINITY : score(mx);
-        // the first tile sets m; later ones move it when it has grown enough
-        const bool move = x_max > mref + (mref == -INFINITY ? 0.f : kShift + 8.f);
-        const float m_new = move ? x_max - kShift : mref;
-        if (i >= step && __any_sync(0xffffffffu, move)) {
-          const float back = mref == -INFINITY ? 0.f : ex2(mref - m_new);
-          l *= back;
-#pragma unroll
-          for (int c = 0; c < DP / 32; ++c) {
-            uint32_t v[32];
-            ptx::tmem_ld32(tm_o + wg * 128 + 32 * c, v);
-            ptx::tmem_wait_ld32(v);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * back);
-            ptx::tmem_st32(tm_o + wg * 128 + 32 * c, v);
-          }
-        }
-        mref = m_new;
-        const float sub = mref == -INFINITY ? 0.f : mref;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[32], pk[16];
-          ptx::tmem_ld32(tm_s + 32 * c, v);
-          ptx::tmem_wait_ld32(v);
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const float raw = __uint_as_float(v[k]);
-            float p = cap ? ex2(score(raw) - sub) : ex2(fmaf(raw, sl2, -sub));
-            if (masked) p = (see[c] >> k) & 1 ? p : 0.f;
-            sum[k & 3] += p;
-            v[k] = __float_as_uint(p);
-          }
-#pragma unroll
-          for (int k = 0; k < 16; ++k)
-            pk[k] = pack2<F16>(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
-          ptx::tmem_st16(tm_s + 16 * c, pk);
-        }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        ptx::tmem_wait_st();
         ptx::tc_fence_before();
       }
       __syncwarp();
@@ -705,11 +879,10 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
     }
 
     // the segment's result
-    const int n0 = pair ? n : (n + 1) / 2, n1 = pair ? n : n / 2;
-    count[wg ^ 1] += wg ? n0 : n1;
-    if (count[0] > 0) wait(sh, &sh->o_done[0], (count[0] - 1) & 1, a.status);
-    if (count[1] > 0) wait(sh, &sh->o_done[1], (count[1] - 1) & 1, a.status);
+    const int n1 = n / 2;                        // the second stream's tiles, not in pairs
+    if (count > 0) wait(sh, &sh->o_done[wg], (count - 1) & 1, a.status);
     if (!pair) sh->ml[wg][lane_row] = make_float2(mref, l);
+    ptx::tc_fence_before();
     asm volatile("bar.sync 1, 256;" ::: "memory");
     ptx::tc_fence_after();
     float w0 = 1.f, w1 = 0.f;                    // weights of the two streams' O
@@ -840,7 +1013,8 @@ __device__ __forceinline__ void plan(const AttendArgs& a, Tail* sh) {
 }
 
 template <bool F16, bool E4M3, int DP>
-__global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_constant__ AttendArgs a) {
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ TileMaps maps) {
   extern __shared__ __align__(1024) uint8_t smem[];
   Tail* sh = reinterpret_cast<Tail*>(smem + Layout<DP>::kTail);
   const int warp = threadIdx.x / 32;
@@ -848,6 +1022,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   if (warp == kMmaWarp) {
     ptx::tmem_alloc(&sh->tmem, 512);
     ptx::tmem_relinquish();
+  }
+  if (!E4M3 && threadIdx.x == kSoftWarps * 32 && maps.rows > 0) {
+    ptx::prefetch_tensormap(&maps.k);
+    ptx::prefetch_tensormap(&maps.v);
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < 8; ++i) {
@@ -872,16 +1050,22 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   __syncthreads();
   ptx::tc_fence_after();
   if (warp < kSoftWarps) {
-    softmax<F16, E4M3, DP>(a, smem, sh);
+    if (a.softcap > 0.f) softmax<F16, E4M3, true, DP>(a, smem, sh);
+    else softmax<F16, E4M3, false, DP>(a, smem, sh);
   } else if (warp < kMmaWarp) {
     if (E4M3) produce8<F16, DP>(a, smem, sh);
-    else produce16<F16, DP>(a, smem, sh);
+    else produce16<F16, DP>(a, maps, smem, sh);
   } else if (threadIdx.x % 32 == 0) {
     issue<F16, DP>(a, smem, sh, warp - kMmaWarp);
   }
   __syncwarp();
   ptx::tc_fence_before();
   __syncthreads();
+  if (aborted(sh)) {                              // let what was started land
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+  }
+  __syncwarp();
   if (warp == kMmaWarp) ptx::tmem_dealloc(sh->tmem, 512);
 }
 
@@ -950,8 +1134,8 @@ constexpr size_t smem_bytes() {
 }
 
 template <bool F16, bool E4M3, int DP>
-cudaError_t launch(const AttendArgs& a, cudaStream_t stream) {
-  attend_kernel<F16, E4M3, DP><<<a.n_cta, kThreads, smem_bytes<DP>(), stream>>>(a);
+cudaError_t launch(const AttendArgs& a, const TileMaps& maps, cudaStream_t stream) {
+  attend_kernel<F16, E4M3, DP><<<a.n_cta, kThreads, smem_bytes<DP>(), stream>>>(a, maps);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // the join may be set up while the main kernel runs; it waits for it itself
@@ -985,17 +1169,18 @@ cudaError_t attend_setup(bool f16, int D) {
   return f16 ? setup<true, 128>() : setup<false, 128>();
 }
 
-cudaError_t attend_launch(const AttendArgs& a, bool f16, bool e4m3, cudaStream_t stream) {
+cudaError_t attend_launch(const AttendArgs& a, const TileMaps& maps, bool f16, bool e4m3,
+                          cudaStream_t stream) {
   const int sel = (f16 ? 4 : 0) + (e4m3 ? 2 : 0) + (padded_dim(a.D) == 128 ? 1 : 0);
   switch (sel) {
-    case 0: return launch<false, false, 64>(a, stream);
-    case 1: return launch<false, false, 128>(a, stream);
-    case 2: return launch<false, true, 64>(a, stream);
-    case 3: return launch<false, true, 128>(a, stream);
-    case 4: return launch<true, false, 64>(a, stream);
-    case 5: return launch<true, false, 128>(a, stream);
-    case 6: return launch<true, true, 64>(a, stream);
-    default: return launch<true, true, 128>(a, stream);
+    case 0: return launch<false, false, 64>(a, maps, stream);
+    case 1: return launch<false, false, 128>(a, maps, stream);
+    case 2: return launch<false, true, 64>(a, maps, stream);
+    case 3: return launch<false, true, 128>(a, maps, stream);
+    case 4: return launch<true, false, 64>(a, maps, stream);
+    case 5: return launch<true, false, 128>(a, maps, stream);
+    case 6: return launch<true, true, 64>(a, maps, stream);
+    default: return launch<true, true, 128>(a, maps, stream);
   }
 }
 

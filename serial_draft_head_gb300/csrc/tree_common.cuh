@@ -3,6 +3,7 @@
 // arguments of the launches (tree_cache.cu, tree_attend.cu).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -143,8 +144,16 @@ struct AttendArgs {
 inline int padded_dim(int D) { return D <= 64 ? 64 : 128; }
 constexpr int kGroupRows = 256;    // rows (nodes x heads of one group) of a work item
 
+// Tiled-copy maps of K and V of a 16-bit cache: {D, slot, head, page}, boxes of
+// 64 elements by `rows` slots, swizzled.  rows = 0: no map, 16-byte copies.
+struct TileMaps {
+  CUtensorMap k, v;
+  int rows;
+};
+
 cudaError_t attend_setup(bool f16, int D);
-cudaError_t attend_launch(const AttendArgs& a, bool f16, bool e4m3, cudaStream_t stream);
+cudaError_t attend_launch(const AttendArgs& a, const TileMaps& maps, bool f16, bool e4m3,
+                          cudaStream_t stream);
 
 // Packed rows of the cache calls: strides in bytes.
 struct RowsArgs {

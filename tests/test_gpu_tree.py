@@ -252,6 +252,21 @@ def test_attend_repeats_and_graph(tree):
         c.check(o3, l3)
 
 
+@pytest.mark.parametrize("page,cache", [(64, "16"), (16, "16"), (24, "16"), (64, "e4m3")])
+def test_attend_many_tiles_back_to_back(tree, page, cache):
+    """Long shares of every CTA, calls over several caches in a row without a wait between:
+    copies land late and out of order.  The same bits every time."""
+    cases = [Case(tree, 32, 8, 128, page, BF16, cache, [17], [40000 + 511 * i], seed=40 + i, spare=1,
+                  mask=None) for i in range(3)]
+    want = [c.attend() for c in cases]
+    cases[1].check(*want[1])
+    for _ in range(30):
+        got = [c.tree.attend(c.q, c.cache, c.pages, c.length, c.first) for c in cases * 4]
+        for i, (o, l) in enumerate(got):
+            assert torch.equal(o, want[i % 3][0]) and torch.equal(l, want[i % 3][1])
+    assert all(c.tree.status() == 0 for c in cases)
+
+
 def test_attend_empty_calls(tree):
     t = tree.Tree(4, 2, 64, BF16, max_requests=3, max_nodes=4)
     k = torch.zeros(2, 16, 2, 64, dtype=BF16, device="cuda")
