@@ -49,10 +49,24 @@ namespace {
 
 constexpr int kKeys = 128;              // keys of a tile
 constexpr int kSoftWarps = 8;
-constexpr int kProdWarps = 8;
-constexpr int kProd = kProdWarps * 32;
-constexpr int kThreads = (kSoftWarps + kProdWarps + 2) * 32;
-constexpr int kMmaWarp = kSoftWarps + kProdWarps;
+
+// Warps and registers.  The softmax groups take registers from the others: for
+// a 16-bit cache enough to hold a row of scores; for e4m3 the producers need
+// theirs to convert in, and the softmax reads its scores in two halves.
+template <bool E4M3>
+struct Roles {
+  static constexpr int kProdWarps = E4M3 ? 8 : 4;
+  static constexpr int kMmaWarp = kSoftWarps + kProdWarps;
+  static constexpr int kThreads = (kMmaWarp + 4) * 32;
+  static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
+  static constexpr int kSoftRegs = E4M3 ? 136 : 184;
+  static constexpr int kProdRegs = E4M3 ? 80 : 88;
+  static constexpr int kMmaRegs = E4M3 ? 48 : 56;
+  static constexpr int kSplit =
+      kSoftWarps * kSoftRegs + kProdWarps * kProdRegs + 4 * kMmaRegs;   // times 32
+  static_assert(kSplit * 32 <= kThreads * kLaunchRegs, "the split asks for more than there is");
+};
+
 constexpr int kLag = 2;                 // slots a producer issues ahead of the one it completes
 constexpr int kBadSets = 8;             // segments the producers can be ahead, rounded up
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
@@ -72,7 +86,7 @@ struct Tail {
   float2 ml[2][kKeys];
   uint32_t bad[kBadSets][DSPARK_TREE_MAX_NODES / 32];
   int64_t unit0, units, total;           // this CTA's share, and all units
-  int64_t warp_sum[kThreads / 32];
+  int64_t warp_sum[20];
   int b0;
   int64_t off0;
   uint32_t tmem;
@@ -322,18 +336,19 @@ struct Place {
   int page, slot;
 };
 
-// Page and slot of a position; positions past the end and bad pages: -1.
+// Page and slot of a position; positions past the end and bad pages: page -1.
+// Without branches around the load, so that several of them are in flight.
 __device__ __forceinline__ Place place_of(const AttendArgs& a, int b, int pos, int total) {
-  Place p{-1, 0};
-  if (pos < total) {
-    const int i = a.c.page.div(pos);
-    p.slot = pos - i * a.c.page.d;
-    p.page = __ldg(a.b.pages + (int64_t)b * a.b.pages_stride + i);
-    if ((uint32_t)p.page >= (uint64_t)a.c.n_pages) {
-      p.page = -1;
-      set_status(a.status, DSPARK_EPAGES);
-    }
+  Place p;
+  const int at = pos < total ? pos : total - 1;
+  const int i = a.c.page.div(at);
+  p.slot = at - i * a.c.page.d;
+  p.page = __ldg(a.b.pages + (int64_t)b * a.b.pages_stride + i);
+  if ((uint32_t)p.page >= (uint64_t)a.c.n_pages) {
+    p.page = -1;
+    set_status(a.status, DSPARK_EPAGES);
   }
+  if (pos >= total) p.page = -1;
   return p;
 }
 
@@ -367,28 +382,31 @@ template <bool F16, int DP>
 __device__ __forceinline__ void produce16(const AttendArgs& a, const TileMaps& maps, uint8_t* smem,
                                           Tail* sh) {
   using L = Layout<DP>;
+  constexpr int kProdWarps = Roles<false>::kProdWarps;
   constexpr int kChunks = DP / 8;                // 16-byte chunks of a row
-  constexpr int kRows = kProd / kChunks;         // rows a pass
+  constexpr int kRows = kProdWarps * 32 / kChunks;       // rows a pass
   constexpr int kPasses = kKeys / kRows;
   const int tid = threadIdx.x - kSoftWarps * 32, lane = threadIdx.x % 32, warp = tid / 32;
   const int chunk = tid % kChunks, r0 = tid / kChunks;
   const bool in_dim = chunk * 8 < a.D;
   const int pieces = maps.rows > 0 ? kKeys / maps.rows : 1;      // boxes along a tile's keys
-  const int piece = warp % pieces;               // this warp's, in one or two 64-element blocks
-  const int boxes = pieces * (DP / 64);
+  const int boxes = pieces * (DP / 64);          // of a tile; warp w issues w, w + 4, ...
   uint8_t* ring = smem + L::kRing;
   Cursor c;
   c.init(a, sh);
   if (!c.more) return;
-  // the page of this warp's piece of the tile at the cursor, fetched a tile ahead
-  auto piece_page = [&]() {
-    const int pos = c.t * kKeys + piece * maps.rows;
-    int page = -1;
-    if (maps.rows > 0 && lane == 0 && c.more && (c.t + 1) * kKeys <= c.s.start)
-      page = __ldg(a.b.pages + (int64_t)c.s.b * a.b.pages_stride + a.c.page.div(pos));
-    return page;
+  // the pages of this warp's boxes of the tile at the cursor, fetched a tile ahead: with
+  // eight pieces a warp's boxes lie in two of them, else in one
+  const int piece0 = warp % pieces, piece1 = (warp + kProdWarps) % pieces;
+  int next0 = -1, next1 = -1;
+  auto fetch_pages = [&]() {
+    if (maps.rows == 0 || lane != 0 || !c.more || (c.t + 1) * kKeys > c.s.start) return;
+    const int32_t* table = a.b.pages + (int64_t)c.s.b * a.b.pages_stride;
+    const int pos = c.t * kKeys;
+    next0 = __ldg(table + a.c.page.div(pos + piece0 * maps.rows));
+    if (piece1 != piece0) next1 = __ldg(table + a.c.page.div(pos + piece1 * maps.rows));
   };
-  int page_next = piece_page();
+  fetch_pages();
   int n = 0;                                     // slots issued
   uint32_t copied = 0;                           // bit i: slot n - 1 - i went by 16-byte copies
   // the V tile in flight: where it is and which of its positions are draft
@@ -415,15 +433,10 @@ __device__ __forceinline__ void produce16(const AttendArgs& a, const TileMaps& m
   };
   while (c.more) {
     const int b = c.s.b, head = c.s.head, start = c.s.start, total = start + c.s.rows;
-    const int pos0 = c.t * kKeys, seg = c.seg, page = page_next;
+    const int pos0 = c.t * kKeys, seg = c.seg, page0 = next0, page1 = next1;
     c.next(a);
-    page_next = piece_page();
+    fetch_pages();
     const bool tiled = maps.rows > 0 && pos0 + kKeys <= start;
-    Place p[kPasses];
-    if (!tiled) {
-#pragma unroll
-      for (int i = 0; i < kPasses; ++i) p[i] = place_of(a, b, pos0 + r0 + i * kRows, total);
-    }
 #pragma unroll
     for (int v = 0; v < 2; ++v, ++n) {
       uint64_t* full = &sh->full[n % L::kSlots];
@@ -432,17 +445,20 @@ __device__ __forceinline__ void produce16(const AttendArgs& a, const TileMaps& m
         if (lane == 0) {
           wait(sh, &sh->empty[n % L::kSlots], ((n / L::kSlots) & 1) ^ 1, a.status);
           // after an abort no copy may outlive the CTA: none is started
-          if (warp < boxes && !aborted(sh)) {
-            const bool two = boxes > kProdWarps;
-            ptx::mbar_expect_tx(full, (two ? 2 : 1) * maps.rows * 128);
-            const bool bad = (uint32_t)page >= (uint64_t)a.c.n_pages;
-            if (bad) set_status(a.status, DSPARK_EPAGES);
-            const int w = bad ? (int)a.c.n_pages : page;         // past the end: zeros
-            const int pos = pos0 + piece * maps.rows;
-            const int slot = pos - a.c.page.div(pos) * a.c.page.d;
-            for (int bx = warp; bx < boxes; bx += kProdWarps)
-              ptx::tma_load_4d(dst + (bx / pieces) * (kKeys * 128) + piece * maps.rows * 128,
-                               v ? &maps.v : &maps.k, (bx / pieces) * 64, slot, head, w, full);
+          const int mine = (boxes - warp + kProdWarps - 1) / kProdWarps;
+          if (mine > 0 && !aborted(sh)) {
+            ptx::mbar_expect_tx(full, mine * maps.rows * 128);
+            for (int bx = warp; bx < boxes; bx += kProdWarps) {
+              const int piece = bx % pieces, block = bx / pieces;
+              const int page = piece == piece0 ? page0 : page1;
+              const bool bad = (uint32_t)page >= (uint64_t)a.c.n_pages;
+              if (bad) set_status(a.status, DSPARK_EPAGES);
+              const int pos = pos0 + piece * maps.rows;
+              ptx::tma_load_4d(dst + block * (kKeys * 128) + piece * maps.rows * 128,
+                               v ? &maps.v : &maps.k, block * 64,
+                               pos - a.c.page.div(pos) * a.c.page.d, head,
+                               bad ? (int)a.c.n_pages : page, full);   // past the end: zeros
+            }
           } else {
             ptx::mbar_arrive(full);
           }
@@ -452,11 +468,18 @@ __device__ __forceinline__ void produce16(const AttendArgs& a, const TileMaps& m
         wait(sh, &sh->empty[n % L::kSlots], ((n / L::kSlots) & 1) ^ 1, a.status);
         const int64_t* st = v ? a.c.vst : a.c.kst;
         const uint8_t* src = (v ? a.c.v : a.c.k) + head * st[2] + chunk * 16;
+#pragma unroll 1
+        for (int i0 = 0; i0 < kPasses; i0 += 4) {
+          Place p[4];
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-          const bool on = in_dim && p[i].page >= 0;
-          const uint8_t* from = on ? src + p[i].page * st[0] + p[i].slot * st[1] : a.c.k;
-          ptx::cp_async16_or_zero(dst + tile_offset(r0 + i * kRows, chunk), from, on);
+          for (int i = 0; i < 4; ++i) p[i] = place_of(a, b, pos0 + r0 + (i0 + i) * kRows, total);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool on = in_dim && p[i].page >= 0;
+            const uint8_t* from = src + p[i].page * st[0] + p[i].slot * st[1];
+            ptx::cp_async16_or_zero(dst + tile_offset(r0 + (i0 + i) * kRows, chunk),
+                                    on ? from : a.c.k, on);
+          }
         }
       }
       ptx::cp_async_commit();
@@ -479,11 +502,12 @@ __device__ __forceinline__ void produce16(const AttendArgs& a, const TileMaps& m
 }
 
 // e4m3 cache, through registers.  The tile after the one being converted is in
-// flight in registers, and the rows of the kAhead tiles after that are asked
-// for in L2.
+// flight in registers, its page numbers were fetched a tile earlier, and the
+// rows of the kAhead tiles after it are asked for in L2.
 template <bool F16, int DP>
 __device__ __forceinline__ void produce8(const AttendArgs& a, uint8_t* smem, Tail* sh) {
   using L = Layout<DP>;
+  constexpr int kProd = Roles<true>::kProdWarps * 32;
   constexpr int kChunks = DP / 16;               // 16-code chunks of a row
   constexpr int kRows = kProd / kChunks;
   constexpr int kPasses = kKeys / kRows;
@@ -492,84 +516,118 @@ __device__ __forceinline__ void produce8(const AttendArgs& a, uint8_t* smem, Tai
   const int tid = threadIdx.x - kSoftWarps * 32, lane = threadIdx.x % 32;
   const int chunk = tid % kChunks, r0 = tid / kChunks;
   const bool in_dim = chunk * 16 < a.D;
+  // the upper half of a row's chunks stores its odd chunk first: the two
+  // 64-element blocks lie in the same banks
+  const int odd = chunk >= 4 ? 1 : 0;
+  const uint32_t to0 = tile_offset(r0, 2 * chunk + odd), to1 = tile_offset(r0, 2 * chunk + 1 - odd);
   uint8_t* ring = smem + L::kRing;
   Cursor c, far;                                 // the tile to load next; to ask L2 for next
   c.init(a, sh);
   if (!c.more) return;
   far.init(a, sh);
-  auto ask = [&]() {
-    if (!far.more) return;
-    const bool v = tid >= kKeys;
-    const int64_t* st = v ? a.c.vst : a.c.kst;
-    const Place p = place_of(a, far.s.b, far.t * kKeys + tid % kKeys, far.s.start + far.s.rows);
-    if (p.page >= 0)
-      ptx::prefetch_l2((v ? a.c.v : a.c.k) + p.page * st[0] + p.slot * st[1] + far.s.head * st[2]);
-    far.next(a);
+  // page numbers of this thread's rows of the tile at the cursor
+  int page[kPasses];
+  auto fetch_pages = [&]() {
+    if (!c.more) return;
+    const int32_t* table = a.b.pages + (int64_t)c.s.b * a.b.pages_stride;
+    const int last = c.s.start + c.s.rows - 1;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i)
+      page[i] = __ldg(table + a.c.page.div(min(c.t * kKeys + r0 + i * kRows, last)));
   };
-  uint4 x[2][kPasses];                           // K and V codes and scales of the tile in flight
-  uint32_t byte[2][kPasses];
+  // one row of K or V a thread, of the tile at the far cursor; its page was fetched before
+  int far_page = 0;
+  auto ask = [&](bool first) {
+    const bool v = tid >= kKeys;
+    if (!first && far.more) {
+      const int pos = min(far.t * kKeys + tid % kKeys, far.s.start + far.s.rows - 1);
+      const int64_t* st = v ? a.c.vst : a.c.kst;
+      if ((uint32_t)far_page < (uint64_t)a.c.n_pages)
+        ptx::prefetch_l2((v ? a.c.v : a.c.k) + far_page * st[0] + far.s.head * st[2] +
+                         (pos - a.c.page.div(pos) * a.c.page.d) * st[1]);
+      far.next(a);
+    }
+    if (far.more) {
+      const int pos = min(far.t * kKeys + tid % kKeys, far.s.start + far.s.rows - 1);
+      far_page = __ldg(a.b.pages + (int64_t)far.s.b * a.b.pages_stride + a.c.page.div(pos));
+    }
+  };
+  uint4 x[2][kPasses];                           // K and V codes of the tile in flight
+  uint32_t byte[2][kPasses];                     // and their scales
   auto load = [&](int v) {
     const int64_t* st = v ? a.c.vst : a.c.kst;
     const int64_t* ss = v ? a.c.vsst : a.c.ksst;
-    const uint8_t* src = (v ? a.c.v : a.c.k) + c.s.head * st[2] + chunk * 16;
+    const uint8_t* src = (v ? a.c.v : a.c.k) + c.s.head * st[2] + (in_dim ? chunk * 16 : 0);
     const uint8_t* sc = (v ? a.c.vs : a.c.ks) + c.s.head * ss[2];
+    const int last = c.s.start + c.s.rows - 1;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-      const Place p = place_of(a, c.s.b, c.t * kKeys + r0 + i * kRows, c.s.start + c.s.rows);
-      x[v][i] = make_uint4(0, 0, 0, 0);
-      byte[v][i] = 127;
-      if (in_dim && p.page >= 0) {
-        x[v][i] = ptx::ldg_nc_na(src + p.page * st[0] + p.slot * st[1]);
-        byte[v][i] = __ldg(sc + p.page * ss[0] + p.slot * ss[1]);
-      }
+      const int pos = min(c.t * kKeys + r0 + i * kRows, last);
+      const int slot = pos - a.c.page.div(pos) * a.c.page.d;
+      const bool bad = (uint32_t)page[i] >= (uint64_t)a.c.n_pages;
+      if (bad) set_status(a.status, DSPARK_EPAGES);
+      const int pg = bad ? 0 : page[i];
+      x[v][i] = ptx::ldg_nc_na(src + pg * st[0] + slot * st[1]);
+      byte[v][i] = __ldg(sc + pg * ss[0] + slot * ss[1]);
     }
   };
+  fetch_pages();
   load(0);
   load(1);
 #pragma unroll 1
-  for (int i = 0; i <= kAhead; ++i) ask();
+  for (int i = 0; i <= kAhead + 1; ++i) ask(i == 0);
   for (int n = 0; c.more;) {
     // the tile whose codes are in registers
     const int pos0 = c.t * kKeys, start = c.s.start, this_seg = c.seg;
+    const int rows = min(kKeys, start + c.s.rows - pos0);
     c.next(a);
+    fetch_pages();
 #pragma unroll
     for (int v = 0; v < 2; ++v, ++n) {
       wait(sh, &sh->empty[n % L::kSlots], ((n / L::kSlots) & 1) ^ 1, a.status);
       uint8_t* dst = ring + (n % L::kSlots) * L::kTile;
+      bool easy = true;
 #pragma unroll
       for (int i = 0; i < kPasses; ++i) {
-        const int row = r0 + i * kRows;
-        uint4 y[2];
-        if (easy_scale<F16>(byte[v][i])) {
+        easy &= easy_scale<F16>(byte[v][i]);
+        if (!in_dim || r0 + i * kRows >= rows) x[v][i] = make_uint4(0, 0, 0, 0);
+      }
+      if (easy) {
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
           const uint32_t m = scale_mul2<F16>(byte[v][i]);
           const uint2 c0 = scale_codes<F16>(x[v][i].x, m), c1 = scale_codes<F16>(x[v][i].y, m);
           const uint2 c2 = scale_codes<F16>(x[v][i].z, m), c3 = scale_codes<F16>(x[v][i].w, m);
-          y[0] = make_uint4(c0.x, c0.y, c1.x, c1.y);
-          y[1] = make_uint4(c2.x, c2.y, c3.x, c3.y);
-        } else {
-          const uint2 c0 = scale_codes_any<F16>(x[v][i].x, byte[v][i]);
-          const uint2 c1 = scale_codes_any<F16>(x[v][i].y, byte[v][i]);
-          const uint2 c2 = scale_codes_any<F16>(x[v][i].z, byte[v][i]);
-          const uint2 c3 = scale_codes_any<F16>(x[v][i].w, byte[v][i]);
-          y[0] = make_uint4(c0.x, c0.y, c1.x, c1.y);
-          y[1] = make_uint4(c2.x, c2.y, c3.x, c3.y);
-          const int j = pos0 + row - start;
+          const uint4 y0 = make_uint4(c0.x, c0.y, c1.x, c1.y);
+          const uint4 y1 = make_uint4(c2.x, c2.y, c3.x, c3.y);
+          *reinterpret_cast<uint4*>(dst + to0 + i * kRows * 128) = odd ? y1 : y0;
+          *reinterpret_cast<uint4*>(dst + to1 + i * kRows * 128) = odd ? y0 : y1;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+          // rows past the end stand for zeros whatever the scale of the row read for them
+          const uint32_t by = !in_dim || r0 + i * kRows >= rows ? 127 : byte[v][i];
+          const uint2 c0 = scale_codes_any<F16>(x[v][i].x, by);
+          const uint2 c1 = scale_codes_any<F16>(x[v][i].y, by);
+          const uint2 c2 = scale_codes_any<F16>(x[v][i].z, by);
+          const uint2 c3 = scale_codes_any<F16>(x[v][i].w, by);
+          uint4 y0 = make_uint4(c0.x, c0.y, c1.x, c1.y);
+          uint4 y1 = make_uint4(c2.x, c2.y, c3.x, c3.y);
+          const int j = pos0 + r0 + i * kRows - start;
           if (v && j >= 0) {
-            const bool b0 = zero_nonfinite<F16>(&y[0]), b1 = zero_nonfinite<F16>(&y[1]);
+            const bool b0 = zero_nonfinite<F16>(&y0), b1 = zero_nonfinite<F16>(&y1);
             if (b0 || b1) atomicOr(&sh->bad[this_seg % kBadSets][j >> 5], 1u << (j & 31));
           }
+          *reinterpret_cast<uint4*>(dst + to0 + i * kRows * 128) = odd ? y1 : y0;
+          *reinterpret_cast<uint4*>(dst + to1 + i * kRows * 128) = odd ? y0 : y1;
         }
-        // the upper half of a row's chunks stores its odd chunk first: the two
-        // 64-element blocks lie in the same banks
-        const int odd = chunk >= 4 ? 1 : 0;
-        *reinterpret_cast<uint4*>(dst + tile_offset(row, 2 * chunk + odd)) = odd ? y[1] : y[0];
-        *reinterpret_cast<uint4*>(dst + tile_offset(row, 2 * chunk + 1 - odd)) = odd ? y[0] : y[1];
       }
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&sh->full[n % L::kSlots]);
       if (c.more) load(v);
-      if (v == 0) ask();
+      if (v == 0) ask(false);
     }
   }
 }
@@ -700,73 +758,6 @@ __device__ __forceinline__ float exponent(const Score& sc, float raw) {
   return CAP ? sc.cap2 - 2.f * sc.cap2 * rcp(ex2(raw * sc.cap_in) + 1.f) : raw * sc.sl2;
 }
 
-// The largest raw score of the row's 128 (of those it sees).
-template <bool MASKED>
-__device__ __forceinline__ float tile_max(uint32_t tm_s, const uint32_t (&see)[4]) {
-  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t v[2][32];
-    ptx::tmem_ld32(tm_s + 64 * h, v[0]);
-    ptx::tmem_ld32(tm_s + 64 * h + 32, v[1]);
-    ptx::tmem_wait_ld32(v[0]);
-    ptx::tmem_wait_ld32(v[1]);
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
-#pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        float x = __uint_as_float(v[c][k]);
-        if (MASKED) x = (see[2 * h + c] >> k) & 1 ? x : -INFINITY;
-        mx[k & 3] = fmaxf(mx[k & 3], x);
-      }
-  }
-  return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-}
-
-// Weights 2^(x - sub) of the row's 128 keys over their scores, rounded to the
-// 16-bit type; returns the sum of the unrounded ones.
-template <bool F16, bool CAP, bool MASKED>
-__device__ __forceinline__ float tile_weights(const Score& sc, uint32_t tm_s,
-                                              const uint32_t (&see)[4], float sub) {
-  uint64_t sum[2] = {0, 0};
-  const uint64_t mul = pack_f32x2(sc.sl2, sc.sl2), neg = pack_f32x2(-sub, -sub);
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t v[2][32];
-    ptx::tmem_ld32(tm_s + 64 * h, v[0]);
-    ptx::tmem_ld32(tm_s + 64 * h + 32, v[1]);
-    ptx::tmem_wait_ld32(v[0]);
-    ptx::tmem_wait_ld32(v[1]);
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      uint32_t pk[16];
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const float r0 = __uint_as_float(v[c][2 * k]), r1 = __uint_as_float(v[c][2 * k + 1]);
-        float p0, p1;
-        if (CAP) {
-          p0 = exponent<true>(sc, r0) - sub;
-          p1 = exponent<true>(sc, r1) - sub;
-        } else {
-          unpack_f32x2(fma_f32x2(pack_f32x2(r0, r1), mul, neg), &p0, &p1);
-        }
-        p0 = ex2(p0);
-        p1 = ex2(p1);
-        if (MASKED) {
-          p0 = (see[2 * h + c] >> (2 * k)) & 1 ? p0 : 0.f;
-          p1 = (see[2 * h + c] >> (2 * k + 1)) & 1 ? p1 : 0.f;
-        }
-        sum[k & 1] = add_f32x2(sum[k & 1], pack_f32x2(p0, p1));
-        pk[k] = pack2<F16>(p0, p1);
-      }
-      ptx::tmem_st16(tm_s + 32 * h + 16 * c, pk);
-    }
-  }
-  float a, b;
-  unpack_f32x2(add_f32x2(sum[0], sum[1]), &a, &b);
-  return a + b;
-}
-
 // O of this row times `back`.
 template <int DP>
 __device__ __forceinline__ void scale_row(uint32_t tm_o, float back) {
@@ -781,15 +772,66 @@ __device__ __forceinline__ void scale_row(uint32_t tm_o, float back) {
   }
 }
 
+// Weights of 32 scores `v`, stored as P at tm_p; adds the unrounded ones to sum.
+template <bool F16, bool CAP, bool MASKED>
+__device__ __forceinline__ void weights_32(const Score& sc, const uint32_t (&v)[32], uint32_t see,
+                                           float sub, uint32_t tm_p, uint64_t (&sum)[2]) {
+  const uint64_t mul = pack_f32x2(sc.sl2, sc.sl2), neg = pack_f32x2(-sub, -sub);
+  uint32_t pk[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const float r0 = __uint_as_float(v[2 * k]), r1 = __uint_as_float(v[2 * k + 1]);
+    float p0, p1;
+    if (CAP) {
+      p0 = exponent<true>(sc, r0) - sub;
+      p1 = exponent<true>(sc, r1) - sub;
+    } else {
+      unpack_f32x2(fma_f32x2(pack_f32x2(r0, r1), mul, neg), &p0, &p1);
+    }
+    p0 = ex2(p0);
+    p1 = ex2(p1);
+    if (MASKED) {
+      p0 = (see >> (2 * k)) & 1 ? p0 : 0.f;
+      p1 = (see >> (2 * k + 1)) & 1 ? p1 : 0.f;
+    }
+    sum[k & 1] = add_f32x2(sum[k & 1], pack_f32x2(p0, p1));
+    pk[k] = pack2<F16>(p0, p1);
+  }
+  ptx::tmem_st16(tm_p, pk);
+}
+
+template <bool MASKED>
+__device__ __forceinline__ void max_32(const uint32_t (&v)[32], uint32_t see, float (&mx)[4]) {
+#pragma unroll
+  for (int k = 0; k < 32; ++k) {
+    float x = __uint_as_float(v[k]);
+    if (MASKED) x = (see >> k) & 1 ? x : -INFINITY;
+    mx[k & 3] = fmaxf(mx[k & 3], x);
+  }
+}
+
 // One tile of one row: S in tensor memory becomes P, m and l move on, O is
-// rescaled if m moved.
-template <bool F16, bool CAP, bool MASKED, int DP>
+// rescaled if m moved.  WIDE holds the row's 128 scores in registers; else
+// they are read twice, 64 at a time.
+template <bool F16, bool CAP, bool MASKED, bool WIDE, int DP>
 __device__ __forceinline__ void softmax_tile(const Score& sc, uint32_t tm_s, uint32_t tm_o,
                                              const uint32_t (&see)[4], bool first, float* mref,
                                              float* l) {
   constexpr float kShift = F16 ? 7.f : 0.f;
-  const float mx = tile_max<MASKED>(tm_s, see);
-  const float x_max = mx == -INFINITY ? -INFINITY : exponent<CAP>(sc, mx);
+  constexpr int kHold = WIDE ? 4 : 2;            // blocks of 32 scores held
+  uint32_t v[kHold][32];
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int h = 0; h < 4; h += kHold) {
+#pragma unroll
+    for (int c = 0; c < kHold; ++c) ptx::tmem_ld32(tm_s + 32 * (h + c), v[c]);
+#pragma unroll
+    for (int c = 0; c < kHold; ++c) ptx::tmem_wait_ld32(v[c]);
+#pragma unroll
+    for (int c = 0; c < kHold; ++c) max_32<MASKED>(v[c], see[h + c], mx);
+  }
+  const float raw_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+  const float x_max = raw_max == -INFINITY ? -INFINITY : exponent<CAP>(sc, raw_max);
   // the first visible key sets m; later ones move it when it has grown enough
   const bool move = x_max > *mref + (*mref == -INFINITY ? 0.f : kShift + 8.f);
   const float m_new = move ? x_max - kShift : *mref;
@@ -799,7 +841,23 @@ __device__ __forceinline__ void softmax_tile(const Score& sc, uint32_t tm_s, uin
     scale_row<DP>(tm_o, back);
   }
   *mref = m_new;
-  *l += tile_weights<F16, CAP, MASKED>(sc, tm_s, see, m_new == -INFINITY ? 0.f : m_new);
+  const float sub = m_new == -INFINITY ? 0.f : m_new;
+  uint64_t sum[2] = {0, 0};
+#pragma unroll
+  for (int h = 0; h < 4; h += kHold) {
+    if (!WIDE) {
+#pragma unroll
+      for (int c = 0; c < kHold; ++c) ptx::tmem_ld32(tm_s + 32 * (h + c), v[c]);
+#pragma unroll
+      for (int c = 0; c < kHold; ++c) ptx::tmem_wait_ld32(v[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < kHold; ++c)
+      weights_32<F16, CAP, MASKED>(sc, v[c], see[h + c], sub, tm_s + 16 * (h + c), sum);
+  }
+  float a, b;
+  unpack_f32x2(add_f32x2(sum[0], sum[1]), &a, &b);
+  *l += a + b;
   ptx::tmem_wait_st();
 }
 
@@ -827,22 +885,34 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
     // Q into shared memory, all 256 threads, when both MMA threads are past the last
     if (seg > 0) wait(sh, &sh->q_empty, (seg - 1) & 1, a.status);
     {
-      constexpr int kChunks = DP / 8;
+      constexpr int kChunks = DP / 8, kBatch = 8;
       const int q_rows = pair ? kGroupRows : kKeys;
-      for (int i = threadIdx.x; i < q_rows * kChunks; i += 256) {
-        const int r = i / kChunks, chunk = i % kChunks;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (r < rows && chunk * 8 < a.D) {
-          const int gr = s.group * kGroupRows + r, nd = a.group.div(gr);
-          const uint8_t* src = a.q + (int64_t)(s.row0 + nd) * a.q_row +
-                               (int64_t)(s.head * a.G + gr - nd * a.G) * a.q_head;
-          x = __ldg(reinterpret_cast<const uint4*>(src) + chunk);
-          x.x ^= flip;
-          x.y ^= flip;
-          x.z ^= flip;
-          x.w ^= flip;
+      const int chunk = threadIdx.x % kChunks;
+#pragma unroll 1
+      for (int i0 = threadIdx.x / kChunks; i0 < q_rows; i0 += kBatch * (256 / kChunks)) {
+        uint4 x[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int r = i0 + k * (256 / kChunks);
+          x[k] = make_uint4(0, 0, 0, 0);
+          if (r < rows && chunk * 8 < a.D) {
+            const int gr = s.group * kGroupRows + r, nd = a.group.div(gr);
+            const uint8_t* src = a.q + (int64_t)(s.row0 + nd) * a.q_row +
+                                 (int64_t)(s.head * a.G + gr - nd * a.G) * a.q_head;
+            x[k] = __ldg(reinterpret_cast<const uint4*>(src) + chunk);
+          }
         }
-        *reinterpret_cast<uint4*>(smem + (r / kKeys) * L::kTile + tile_offset(r % kKeys, chunk)) = x;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int r = i0 + k * (256 / kChunks);
+          x[k].x ^= flip;
+          x[k].y ^= flip;
+          x[k].z ^= flip;
+          x[k].w ^= flip;
+          if (r < q_rows)
+            *reinterpret_cast<uint4*>(smem + (r / kKeys) * L::kTile +
+                                      tile_offset(r % kKeys, chunk)) = x[k];
+        }
       }
       ptx::fence_proxy_async_smem();
       __syncwarp();
@@ -866,11 +936,11 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
         const uint32_t own_o = tm_o + wg * 128;
         const bool first = i < step;
         if (!masked && !CAP) {
-          softmax_tile<F16, false, false, DP>(sc, tm_s, own_o, see, first, &mref, &l);
+          softmax_tile<F16, false, false, !E4M3, DP>(sc, tm_s, own_o, see, first, &mref, &l);
         } else {
 #pragma unroll
           for (int c = 0; c < 4; ++c) see[c] = sees_32(a, s, node, pos0 + 32 * c);
-          softmax_tile<F16, CAP, true, DP>(sc, tm_s, own_o, see, first, &mref, &l);
+          softmax_tile<F16, CAP, true, !E4M3, DP>(sc, tm_s, own_o, see, first, &mref, &l);
         }
         ptx::tc_fence_before();
       }
@@ -962,6 +1032,7 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
 }
 
 // This CTA's share of the units: sums the requests' units in order.
+template <int kThreads>
 __device__ __forceinline__ void plan(const AttendArgs& a, Tail* sh) {
   constexpr int kPer = (DSPARK_TREE_MAX_REQUESTS + 511) / 512;
   int64_t mine[kPer], sum = 0;
@@ -1013,13 +1084,14 @@ __device__ __forceinline__ void plan(const AttendArgs& a, Tail* sh) {
 }
 
 template <bool F16, bool E4M3, int DP>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1)
     attend_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ TileMaps maps) {
+  using R = Roles<E4M3>;
   extern __shared__ __align__(1024) uint8_t smem[];
   Tail* sh = reinterpret_cast<Tail*>(smem + Layout<DP>::kTail);
   const int warp = threadIdx.x / 32;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (warp == kMmaWarp) {
+  if (warp == R::kMmaWarp) {
     ptx::tmem_alloc(&sh->tmem, 512);
     ptx::tmem_relinquish();
   }
@@ -1029,7 +1101,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < 8; ++i) {
-      ptx::mbar_init(&sh->full[i], kProdWarps);
+      ptx::mbar_init(&sh->full[i], R::kProdWarps);
       ptx::mbar_init(&sh->empty[i], 2);
     }
     ptx::mbar_init(&sh->q_full, kSoftWarps);
@@ -1043,20 +1115,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     sh->abort = 0;
     a.part_of[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
-  for (int i = threadIdx.x; i < kBadSets * (DSPARK_TREE_MAX_NODES / 32); i += kThreads)
+  for (int i = threadIdx.x; i < kBadSets * (DSPARK_TREE_MAX_NODES / 32); i += R::kThreads)
     (&sh->bad[0][0])[i] = 0;
-  plan(a, sh);
+  plan<R::kThreads>(a, sh);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   if (warp < kSoftWarps) {
+    ptx::more_registers<R::kSoftRegs>();
     if (a.softcap > 0.f) softmax<F16, E4M3, true, DP>(a, smem, sh);
     else softmax<F16, E4M3, false, DP>(a, smem, sh);
-  } else if (warp < kMmaWarp) {
+  } else if (warp < R::kMmaWarp) {
+    ptx::fewer_registers<R::kProdRegs>();
     if (E4M3) produce8<F16, DP>(a, smem, sh);
     else produce16<F16, DP>(a, maps, smem, sh);
-  } else if (threadIdx.x % 32 == 0) {
-    issue<F16, DP>(a, smem, sh, warp - kMmaWarp);
+  } else {
+    ptx::fewer_registers<R::kMmaRegs>();
+    if (warp < R::kMmaWarp + 2 && threadIdx.x % 32 == 0)
+      issue<F16, DP>(a, smem, sh, warp - R::kMmaWarp);
   }
   __syncwarp();
   ptx::tc_fence_before();
@@ -1066,7 +1142,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
   }
   __syncwarp();
-  if (warp == kMmaWarp) ptx::tmem_dealloc(sh->tmem, 512);
+  if (warp == R::kMmaWarp) ptx::tmem_dealloc(sh->tmem, 512);
 }
 
 // Joins the parts of the items that several CTAs share: block (c, y) takes rows
@@ -1135,7 +1211,8 @@ constexpr size_t smem_bytes() {
 
 template <bool F16, bool E4M3, int DP>
 cudaError_t launch(const AttendArgs& a, const TileMaps& maps, cudaStream_t stream) {
-  attend_kernel<F16, E4M3, DP><<<a.n_cta, kThreads, smem_bytes<DP>(), stream>>>(a, maps);
+  attend_kernel<F16, E4M3, DP>
+      <<<a.n_cta, Roles<E4M3>::kThreads, smem_bytes<DP>(), stream>>>(a, maps);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // the join may be set up while the main kernel runs; it waits for it itself
@@ -1151,22 +1228,30 @@ cudaError_t launch(const AttendArgs& a, const TileMaps& maps, cudaStream_t strea
   return cudaLaunchKernelEx(&cfg, join_kernel<F16, DP>, a);
 }
 
-template <bool F16, int DP>
+// Shared memory, and that the launch brings the registers that the roles split.
+template <bool F16, bool E4M3, int DP>
 cudaError_t setup() {
   static_assert(smem_bytes<DP>() <= 232448, "shared memory of an SM");
-  cudaError_t e = cudaFuncSetAttribute(attend_kernel<F16, false, DP>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem_bytes<DP>());
+  using R = Roles<E4M3>;
+  cudaFuncAttributes fa;
+  cudaError_t e = cudaFuncGetAttributes(&fa, attend_kernel<F16, E4M3, DP>);
   if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(attend_kernel<F16, true, DP>,
+  if (fa.numRegs * R::kThreads < R::kSplit * 32) return cudaErrorInvalidConfiguration;
+  return cudaFuncSetAttribute(attend_kernel<F16, E4M3, DP>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<DP>());
+}
+
+template <bool F16, int DP>
+cudaError_t setup_both() {
+  const cudaError_t e = setup<F16, false, DP>();
+  return e != cudaSuccess ? e : setup<F16, true, DP>();
 }
 
 }  // namespace
 
 cudaError_t attend_setup(bool f16, int D) {
-  if (padded_dim(D) == 64) return f16 ? setup<true, 64>() : setup<false, 64>();
-  return f16 ? setup<true, 128>() : setup<false, 128>();
+  if (padded_dim(D) == 64) return f16 ? setup_both<true, 64>() : setup_both<false, 64>();
+  return f16 ? setup_both<true, 128>() : setup_both<false, 128>();
 }
 
 cudaError_t attend_launch(const AttendArgs& a, const TileMaps& maps, bool f16, bool e4m3,
