@@ -166,14 +166,12 @@ __device__ __forceinline__ void prefetch_l2(const void* p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
-// Registers a thread of this warpgroup may use from here on (all four warps call it).
-template <int N>
-__device__ __forceinline__ void more_registers() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void fewer_registers() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+// Registers a thread of this warpgroup may use from here on (all four warps
+// call it), after a launch with FROM of them.
+template <int FROM, int TO>
+__device__ __forceinline__ void set_registers() {
+  if constexpr (TO > FROM) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(TO));
+  if constexpr (TO < FROM) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TO));
 }
 
 // Maximum of v over the 32 lanes of the (converged) warp.

@@ -59,8 +59,8 @@ struct Roles {
   static constexpr int kMmaWarp = kSoftWarps + kProdWarps;
   static constexpr int kThreads = (kMmaWarp + 4) * 32;
   static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
-  static constexpr int kSoftRegs = E4M3 ? 136 : 184;
-  static constexpr int kProdRegs = E4M3 ? 80 : 88;
+  static constexpr int kSoftRegs = E4M3 ? 112 : 184;
+  static constexpr int kProdRegs = E4M3 ? 104 : 88;
   static constexpr int kMmaRegs = E4M3 ? 48 : 56;
   static constexpr int kSplit =
       kSoftWarps * kSoftRegs + kProdWarps * kProdRegs + 4 * kMmaRegs;   // times 32
@@ -87,8 +87,7 @@ struct Tail {
   uint32_t bad[kBadSets][DSPARK_TREE_MAX_NODES / 32];
   int64_t unit0, units, total;           // this CTA's share, and all units
   int64_t warp_sum[20];
-  int b0;
-  int64_t off0;
+  int b0, head0, group0, t0;             // the share's first unit
   uint32_t tmem;
   int abort;
 };
@@ -159,6 +158,15 @@ __device__ __forceinline__ int64_t units_of(const AttendArgs& a, const Request& 
 // First unit of CTA i's share of `total` units over n CTAs.
 __device__ __forceinline__ int64_t share(int64_t total, int n, int i) { return total * i / n; }
 
+// The CTA whose share holds unit u.
+__device__ __noinline__ int holder(int64_t total, int n_cta, int64_t u) {
+  const int n = (int)(total < n_cta ? total : n_cta);
+  int c = (int)(u * n / total);
+  while (share(total, n, c + 1) <= u) ++c;
+  while (share(total, n, c) > u) --c;
+  return c;
+}
+
 // One CTA's part of an item: key tiles t0 .. t1-1 of `tiles`.
 struct Segment {
   int b, row0, rows, start, head, group, t0, t1, tiles;
@@ -174,13 +182,11 @@ struct Walker {
     left = s->units;
     unit = s->unit0;
     b = s->b0;
-    if (left <= 0) return;
+    head = s->head0;
+    group = s->group0;
+    t0 = s->t0;
     bool ok;
-    r = load_request(a, b, &ok);
-    const int64_t item = s->off0 / r.tiles;
-    t0 = (int)(s->off0 % r.tiles);
-    head = (int)(item / r.groups);
-    group = (int)(item % r.groups);
+    if (left > 0) r = load_request(a, b, &ok);
   }
 
   __device__ bool next(const AttendArgs& a, Segment* s) {
@@ -223,31 +229,28 @@ __device__ __forceinline__ int group_rows(const AttendArgs& a, const Segment& s)
   return n < kGroupRows ? n : kGroupRows;
 }
 
-// Word w of the draft positions that node `node` of the segment's request sees
-// (bits past the request's rows are clear).
-__device__ __forceinline__ uint32_t sees_word(const AttendArgs& a, const Segment& s, int node,
-                                              int w) {
-  const int left = s.rows - 32 * w;
-  if (w < 0 || left <= 0) return 0;
-  uint32_t m;
-  if (a.mask) {
-    m = __ldg(a.mask + (int64_t)(s.row0 + node) * a.mask_stride + w);
-  } else {
+// Visibility of the 128 positions from draft position j0 on (negative:
+// context): a bit a position, for a node with this mask row (null: a chain) of
+// a request with `rows` of them.
+__device__ __noinline__ uint4 sees_128(const uint32_t* mask_row, int rows, int node, int j0) {
+  auto word = [&](int w) {              // draft positions 32 w .. 32 w + 31
+    const int left = rows - 32 * w;
+    if (w < 0 || left <= 0) return 0u;
     const int n = node + 1 - 32 * w;
-    m = n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+    const uint32_t m = mask_row ? __ldg(mask_row + w)
+                                : n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+    return left >= 32 ? m : m & ((1u << left) - 1u);
+  };
+  uint32_t r[4];
+  const int sh = j0 & 31, w0 = j0 >> 5;          // floor: words w0 .. w0 + 4, shifted down by sh
+  uint32_t lo = w0 < 0 ? 0xffffffffu : word(w0);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const uint32_t hi = w0 + c + 1 < 0 ? 0xffffffffu : word(w0 + c + 1);
+    r[c] = __funnelshift_r(lo, hi, sh);
+    lo = hi;
   }
-  return left >= 32 ? m : m & ((1u << left) - 1u);
-}
-
-// Visibility of the 32 positions from `pos` on.
-__device__ __forceinline__ uint32_t sees_32(const AttendArgs& a, const Segment& s, int node,
-                                            int pos) {
-  const int j = pos - s.start;
-  if (j <= -32) return 0xffffffffu;
-  if (j < 0) return ((1u << -j) - 1u) | (sees_word(a, s, node, 0) << -j);
-  const int sh = j & 31;
-  const uint32_t lo = sees_word(a, s, node, j >> 5);
-  return sh ? (lo >> sh) | (sees_word(a, s, node, (j >> 5) + 1) << (32 - sh)) : lo;
+  return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 // ------------------------------------------------------------- producers --
@@ -278,9 +281,12 @@ __device__ __forceinline__ bool zero_nonfinite(uint4* x) {
   return any;
 }
 
-// Four e4m3 codes times 2^(byte - 127) in the 16-bit type, exact (see the
-// conditions at `easy_scale`).  bf16: sign and the seven other bits moved to
-// bf16's sign, exponent and mantissa fields stand for code * 2^-120.
+// Four e4m3 codes (bytes 0 .. 3) times 2^(byte - 127) in the 16-bit type, exact
+// for the scales of `easy_scale`.  bf16: a code's seven low bits moved to bf16's
+// exponent and mantissa fields stand for |code| 2^-120, the sign bit is put on
+// after the product; the pairs come as bytes (0, 2) and (1, 3), which needs no
+// byte permutation, so elements 1 and 2 of every four change places: Q is laid
+// out the same way, and O's columns change back at the end.
 template <bool F16>
 __device__ __forceinline__ uint2 scale_codes(uint32_t w, uint32_t mul2) {
   uint2 r;
@@ -292,16 +298,19 @@ __device__ __forceinline__ uint2 scale_codes(uint32_t w, uint32_t mul2) {
     r.x = *reinterpret_cast<const uint32_t*>(&x);
     r.y = *reinterpret_cast<const uint32_t*>(&y);
   } else {
-    const uint32_t lo = __byte_perm(w, 0, 0x1404), hi = __byte_perm(w, 0, 0x3424);
-    const uint32_t a = (lo & 0x80008000u) | ((lo >> 4) & 0x07f007f0u);
-    const uint32_t b = (hi & 0x80008000u) | ((hi >> 4) & 0x07f007f0u);
+    const uint32_t even = (w << 4) & 0x07f007f0u, odd = (w >> 4) & 0x07f007f0u;
     const __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(&mul2);
-    const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), m);
-    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&b), m);
-    r.x = *reinterpret_cast<const uint32_t*>(&x);
-    r.y = *reinterpret_cast<const uint32_t*>(&y);
+    const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&even), m);
+    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&odd), m);
+    r.x = *reinterpret_cast<const uint32_t*>(&x) ^ ((w << 8) & 0x80008000u);
+    r.y = *reinterpret_cast<const uint32_t*>(&y) ^ (w & 0x80008000u);
   }
   return r;
+}
+
+// The order above of four elements (two packed pairs).
+__device__ __forceinline__ uint2 swap_middle(uint2 x) {
+  return make_uint2(__byte_perm(x.x, x.y, 0x5410), __byte_perm(x.x, x.y, 0x7632));
 }
 
 // Scales whose product with any code is a finite number of the 16-bit type and
@@ -313,7 +322,7 @@ __device__ __forceinline__ bool easy_scale(uint32_t byte) {
 
 template <bool F16>
 __device__ __forceinline__ uint32_t scale_mul2(uint32_t byte) {
-  return (F16 ? (byte - 112) << 10 : (byte + 120) << 7) * 0x00010001u;
+  return F16 ? (byte - 112) * 0x04000400u : byte * 0x00800080u + 120u * 0x00800080u;
 }
 
 // Any other scale: through fp32, rounded and saturated as the cache reads back.
@@ -321,9 +330,10 @@ template <bool F16>
 __device__ __noinline__ uint2 scale_codes_any(uint32_t w, uint32_t byte) {
   const float s = scale_value(byte);
   const float2 x = e4m3x2_to_float2(w & 0xffffu), y = e4m3x2_to_float2(w >> 16);
-  return make_uint2(
+  const uint2 r = make_uint2(
       pack2<F16>(saturate16<F16>(x.x * s), saturate16<F16>(x.y * s)),
       pack2<F16>(saturate16<F16>(y.x * s), saturate16<F16>(y.y * s)));
+  return F16 ? r : swap_middle(r);
 }
 
 // Byte offset of (row, 16-byte chunk) in a tile: 64-element blocks of 128 rows.
@@ -332,81 +342,82 @@ __device__ __forceinline__ uint32_t tile_offset(int row, int chunk) {
          (uint32_t)((chunk ^ row) & 7) * 16;
 }
 
-struct Place {
-  int page, slot;
-};
-
-// Page and slot of a position; positions past the end and bad pages: page -1.
-// Without branches around the load, so that several of them are in flight.
-__device__ __forceinline__ Place place_of(const AttendArgs& a, int b, int pos, int total) {
-  Place p;
-  const int at = pos < total ? pos : total - 1;
-  const int i = a.c.page.div(at);
-  p.slot = at - i * a.c.page.d;
-  p.page = __ldg(a.b.pages + (int64_t)b * a.b.pages_stride + i);
-  if ((uint32_t)p.page >= (uint64_t)a.c.n_pages) {
-    p.page = -1;
-    set_status(a.status, DSPARK_EPAGES);
-  }
-  if (pos >= total) p.page = -1;
-  return p;
-}
-
-// A tile of the CTA's share, in order.
+// The tiles of the CTA's share, in order.
 struct Cursor {
-  Walker w;
-  Segment s;
-  int t, seg;
-  bool more;
+  int b, head, group, t, seg;           // seg: segments begun before this one
+  int rows, start, tiles, groups;       // of the request
+  int64_t left;                         // tiles from this one on
 
-  __device__ void init(const AttendArgs& a, const Tail* sh) {
-    w.init(a, sh);
-    more = w.next(a, &s);
-    t = s.t0;
-    seg = 0;
+  __device__ void load(const AttendArgs& a) {
+    bool ok;
+    const Request r = load_request(a, b, &ok);
+    rows = r.rows;
+    start = r.start;
+    tiles = r.tiles;
+    groups = r.groups;
   }
+  __device__ void init(const AttendArgs& a, const Tail* s) {
+    left = s->units;
+    b = s->b0;
+    head = s->head0;
+    group = s->group0;
+    t = s->t0;
+    seg = 0;
+    if (left > 0) load(a);
+  }
+  __device__ __forceinline__ bool more() const { return left > 0; }
+  __device__ __forceinline__ int total() const { return start + rows; }
   __device__ void next(const AttendArgs& a) {
-    if (++t < s.t1) return;
-    more = w.next(a, &s);
-    t = s.t0;
+    --left;
+    if (++t < tiles) return;
+    t = 0;
     ++seg;
+    if (++group < groups) return;
+    group = 0;
+    if (++head < a.Hkv) return;
+    head = 0;
+    if (left <= 0) return;
+    do {
+      ++b;
+      load(a);
+    } while (rows == 0 && b + 1 < a.b.B);
+    if (rows == 0) left = 0;            // the arrays changed under the kernel
   }
 };
 
-// 16-bit cache.  Tiles of context go by tiled copies, lane 0 of every warp
-// issuing its share of the boxes; tiles that reach into the draft (the last of
-// a request), and all tiles without a map, by 16-byte copies of the threads,
-// completed two slots later, so that rows past the end are zero and draft rows
-// of V can be looked through.
+// 16-bit cache.  With a map (see make_maps for when), tiles of context go by
+// tiled copies, lane 0 of every warp issuing its share of the boxes; tiles that
+// reach into the draft (the last of a request), and all tiles without a map, by
+// 16-byte copies, completed two slots later, so that rows past the end are zero
+// and draft rows of V can be looked through.  A warp copies 32 rows of the
+// tile; each lane looks one row's page up, a tile ahead, and hands it round.
 template <bool F16, int DP>
 __device__ __forceinline__ void produce16(const AttendArgs& a, const TileMaps& maps, uint8_t* smem,
                                           Tail* sh) {
   using L = Layout<DP>;
-  constexpr int kProdWarps = Roles<false>::kProdWarps;
+  constexpr int kWarps = Roles<false>::kProdWarps;
   constexpr int kChunks = DP / 8;                // 16-byte chunks of a row
-  constexpr int kRows = kProdWarps * 32 / kChunks;       // rows a pass
-  constexpr int kPasses = kKeys / kRows;
-  const int tid = threadIdx.x - kSoftWarps * 32, lane = threadIdx.x % 32, warp = tid / 32;
-  const int chunk = tid % kChunks, r0 = tid / kChunks;
+  constexpr int kSub = 32 / kChunks;             // rows of one copy instruction
+  static_assert(kWarps * 32 == kKeys, "32 rows a warp");
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32 - kSoftWarps;
+  const int chunk = lane % kChunks, sub = lane / kChunks;
   const bool in_dim = chunk * 8 < a.D;
-  const int pieces = maps.rows > 0 ? kKeys / maps.rows : 1;      // boxes along a tile's keys
+  const int pieces = maps.rows > 0 ? kKeys / maps.rows : 0;      // boxes along a tile's keys
   const int boxes = pieces * (DP / 64);          // of a tile; warp w issues w, w + 4, ...
   uint8_t* ring = smem + L::kRing;
   Cursor c;
   c.init(a, sh);
-  if (!c.more) return;
-  // the pages of this warp's boxes of the tile at the cursor, fetched a tile ahead: with
-  // eight pieces a warp's boxes lie in two of them, else in one
-  const int piece0 = warp % pieces, piece1 = (warp + kProdWarps) % pieces;
-  int next0 = -1, next1 = -1;
-  auto fetch_pages = [&]() {
-    if (maps.rows == 0 || lane != 0 || !c.more || (c.t + 1) * kKeys > c.s.start) return;
-    const int32_t* table = a.b.pages + (int64_t)c.s.b * a.b.pages_stride;
-    const int pos = c.t * kKeys;
-    next0 = __ldg(table + a.c.page.div(pos + piece0 * maps.rows));
-    if (piece1 != piece0) next1 = __ldg(table + a.c.page.div(pos + piece1 * maps.rows));
+  if (!c.more()) return;
+  // the page of this lane's row (tiled: of the warp's box) of the tile at the cursor
+  int page_next = 0;
+  auto fetch_page = [&]() {
+    if (!c.more()) return;
+    const bool tiled = maps.rows > 0 && (c.t + 1) * kKeys <= c.start;
+    const int row = tiled ? warp % pieces * maps.rows : warp * 32 + lane;
+    const int pos = min(c.t * kKeys + row, c.total() - 1);
+    page_next = __ldg(a.b.pages + (int64_t)c.b * a.b.pages_stride + a.c.page.div(pos));
   };
-  fetch_pages();
+  fetch_page();
   int n = 0;                                     // slots issued
   uint32_t copied = 0;                           // bit i: slot n - 1 - i went by 16-byte copies
   // the V tile in flight: where it is and which of its positions are draft
@@ -414,8 +425,8 @@ __device__ __forceinline__ void produce16(const AttendArgs& a, const TileMaps& m
   auto complete = [&](int slot, bool v) {        // slot's copies of this thread have landed
     if (v && prev_pos + kKeys > prev_start) {
 #pragma unroll 1
-      for (int i = 0; i < kPasses; ++i) {
-        const int row = r0 + i * kRows, pos = prev_pos + row;
+      for (int i = sub; i < 32; i += kSub) {
+        const int row = warp * 32 + i, pos = prev_pos + row;
         if (pos < prev_start || pos >= prev_total) continue;
         uint4* p = reinterpret_cast<uint4*>(ring + (slot % L::kSlots) * L::kTile +
                                             tile_offset(row, chunk));
@@ -426,60 +437,56 @@ __device__ __forceinline__ void produce16(const AttendArgs& a, const TileMaps& m
           atomicOr(&sh->bad[prev_seg % kBadSets][j >> 5], 1u << (j & 31));
         }
       }
+      __syncwarp();
     }
     ptx::fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(&sh->full[slot % L::kSlots]);
   };
-  while (c.more) {
-    const int b = c.s.b, head = c.s.head, start = c.s.start, total = start + c.s.rows;
-    const int pos0 = c.t * kKeys, seg = c.seg, page0 = next0, page1 = next1;
-    c.next(a);
-    fetch_pages();
+  while (c.more()) {
+    const int head = c.head, start = c.start, total = c.total(), seg = c.seg;
+    const int pos0 = c.t * kKeys;
     const bool tiled = maps.rows > 0 && pos0 + kKeys <= start;
-#pragma unroll
+    int page = page_next;
+    if ((uint32_t)page >= (uint64_t)a.c.n_pages) {
+      set_status(a.status, DSPARK_EPAGES);
+      page = -1;
+    }
+    c.next(a);
+    fetch_page();
+    const int my_pos = pos0 + (tiled ? warp % pieces * maps.rows : warp * 32 + lane);
+    const int my_slot = my_pos - a.c.page.div(my_pos) * a.c.page.d;
+    if (my_pos >= total) page = -1;
+#pragma unroll 1
     for (int v = 0; v < 2; ++v, ++n) {
       uint64_t* full = &sh->full[n % L::kSlots];
       uint8_t* dst = ring + (n % L::kSlots) * L::kTile;
+      wait(sh, &sh->empty[n % L::kSlots], ((n / L::kSlots) & 1) ^ 1, a.status);
       if (tiled) {
         if (lane == 0) {
-          wait(sh, &sh->empty[n % L::kSlots], ((n / L::kSlots) & 1) ^ 1, a.status);
           // after an abort no copy may outlive the CTA: none is started
-          const int mine = (boxes - warp + kProdWarps - 1) / kProdWarps;
-          if (mine > 0 && !aborted(sh)) {
-            ptx::mbar_expect_tx(full, mine * maps.rows * 128);
-            for (int bx = warp; bx < boxes; bx += kProdWarps) {
-              const int piece = bx % pieces, block = bx / pieces;
-              const int page = piece == piece0 ? page0 : page1;
-              const bool bad = (uint32_t)page >= (uint64_t)a.c.n_pages;
-              if (bad) set_status(a.status, DSPARK_EPAGES);
-              const int pos = pos0 + piece * maps.rows;
-              ptx::tma_load_4d(dst + block * (kKeys * 128) + piece * maps.rows * 128,
-                               v ? &maps.v : &maps.k, block * 64,
-                               pos - a.c.page.div(pos) * a.c.page.d, head,
-                               bad ? (int)a.c.n_pages : page, full);   // past the end: zeros
-            }
+          if (warp < boxes && !aborted(sh)) {
+            ptx::mbar_expect_tx(full, maps.rows * 128);
+            const int block = warp / pieces;
+            ptx::tma_load_4d(dst + block * (kKeys * 128) + warp % pieces * maps.rows * 128,
+                             v ? &maps.v : &maps.k, block * 64, my_slot, head,
+                             page < 0 ? (int)a.c.n_pages : page, full);   // past the end: zeros
           } else {
             ptx::mbar_arrive(full);
           }
         }
         __syncwarp();
       } else {
-        wait(sh, &sh->empty[n % L::kSlots], ((n / L::kSlots) & 1) ^ 1, a.status);
-        const int64_t* st = v ? a.c.vst : a.c.kst;
-        const uint8_t* src = (v ? a.c.v : a.c.k) + head * st[2] + chunk * 16;
-#pragma unroll 1
-        for (int i0 = 0; i0 < kPasses; i0 += 4) {
-          Place p[4];
+        const int64_t st0 = v ? a.c.vst[0] : a.c.kst[0], st1 = v ? a.c.vst[1] : a.c.kst[1];
+        const uint8_t* src = v ? a.c.v + head * a.c.vst[2] : a.c.k + head * a.c.kst[2];
+        src += chunk * 16;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) p[i] = place_of(a, b, pos0 + r0 + (i0 + i) * kRows, total);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const bool on = in_dim && p[i].page >= 0;
-            const uint8_t* from = src + p[i].page * st[0] + p[i].slot * st[1];
-            ptx::cp_async16_or_zero(dst + tile_offset(r0 + (i0 + i) * kRows, chunk),
-                                    on ? from : a.c.k, on);
-          }
+        for (int i = 0; i < 32; i += kSub) {
+          const int p = __shfl_sync(0xffffffffu, page, i + sub);
+          const int s = __shfl_sync(0xffffffffu, my_slot, i + sub);
+          const bool on = in_dim && p >= 0;
+          ptx::cp_async16_or_zero(dst + tile_offset(warp * 32 + i + sub, chunk),
+                                  on ? src + p * st0 + s * st1 : a.c.k, on);
         }
       }
       ptx::cp_async_commit();
@@ -501,135 +508,164 @@ __device__ __forceinline__ void produce16(const AttendArgs& a, const TileMaps& m
   }
 }
 
-// e4m3 cache, through registers.  The tile after the one being converted is in
-// flight in registers, its page numbers were fetched a tile earlier, and the
-// rows of the kAhead tiles after it are asked for in L2.
+// e4m3 cache, through registers.  A half tile (K or V) is converted while the
+// next two are in flight in registers (three sets, used in turn); their pages
+// were looked up half a tile earlier, and the rows kAhead tiles on are asked for
+// in L2, one row of K or V a thread.
 template <bool F16, int DP>
 __device__ __forceinline__ void produce8(const AttendArgs& a, uint8_t* smem, Tail* sh) {
   using L = Layout<DP>;
-  constexpr int kProd = Roles<true>::kProdWarps * 32;
+  constexpr int kWarps = Roles<true>::kProdWarps;
   constexpr int kChunks = DP / 16;               // 16-code chunks of a row
-  constexpr int kRows = kProd / kChunks;
+  constexpr int kWarpRows = 32 / kChunks;
+  constexpr int kRows = kWarps * kWarpRows;      // rows a pass
   constexpr int kPasses = kKeys / kRows;
   constexpr int kAhead = 4;
-  static_assert(kProd == 2 * kKeys, "one row of K or V a thread");
-  const int tid = threadIdx.x - kSoftWarps * 32, lane = threadIdx.x % 32;
-  const int chunk = tid % kChunks, r0 = tid / kChunks;
+  static_assert(kWarps * 32 == 2 * kKeys, "one row of K or V a thread");
+  const int tid = threadIdx.x - kSoftWarps * 32, lane = tid % 32, warp = tid / 32;
+  // eight lanes store to two neighbouring rows, four 32-byte chunks of one
+  // 64-element block each: all banks once
+  const int chunk = (lane & 3) | (DP == 128 ? (lane >> 1) & 4 : 0);
+  const int r0 = warp * kWarpRows +
+                 (DP == 128 ? ((lane >> 2) & 1) | ((lane >> 3) & 2) : lane >> 2);
   const bool in_dim = chunk * 16 < a.D;
-  // the upper half of a row's chunks stores its odd chunk first: the two
-  // 64-element blocks lie in the same banks
-  const int odd = chunk >= 4 ? 1 : 0;
-  const uint32_t to0 = tile_offset(r0, 2 * chunk + odd), to1 = tile_offset(r0, 2 * chunk + 1 - odd);
+  const uint32_t to0 = tile_offset(r0, 2 * chunk), to1 = tile_offset(r0, 2 * chunk + 1);
   uint8_t* ring = smem + L::kRing;
-  Cursor c, far;                                 // the tile to load next; to ask L2 for next
+  Cursor c;                                      // the tile whose pages are looked up
   c.init(a, sh);
-  if (!c.more) return;
-  far.init(a, sh);
-  // page numbers of this thread's rows of the tile at the cursor
-  int page[kPasses];
+  if (!c.more()) return;
+  struct Tile {
+    int head, rows, draft, seg;                  // rows that exist; the first of the draft
+  };
+  auto tile_at = [&]() {
+    return Tile{c.head, min(kKeys, c.total() - c.t * kKeys), c.start - c.t * kKeys, c.seg};
+  };
+  uint32_t page[kPasses], worst = 0;
+  int slot[kPasses];
   auto fetch_pages = [&]() {
-    if (!c.more) return;
-    const int32_t* table = a.b.pages + (int64_t)c.s.b * a.b.pages_stride;
-    const int last = c.s.start + c.s.rows - 1;
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i)
-      page[i] = __ldg(table + a.c.page.div(min(c.t * kKeys + r0 + i * kRows, last)));
-  };
-  // one row of K or V a thread, of the tile at the far cursor; its page was fetched before
-  int far_page = 0;
-  auto ask = [&](bool first) {
-    const bool v = tid >= kKeys;
-    if (!first && far.more) {
-      const int pos = min(far.t * kKeys + tid % kKeys, far.s.start + far.s.rows - 1);
-      const int64_t* st = v ? a.c.vst : a.c.kst;
-      if ((uint32_t)far_page < (uint64_t)a.c.n_pages)
-        ptx::prefetch_l2((v ? a.c.v : a.c.k) + far_page * st[0] + far.s.head * st[2] +
-                         (pos - a.c.page.div(pos) * a.c.page.d) * st[1]);
-      far.next(a);
-    }
-    if (far.more) {
-      const int pos = min(far.t * kKeys + tid % kKeys, far.s.start + far.s.rows - 1);
-      far_page = __ldg(a.b.pages + (int64_t)far.s.b * a.b.pages_stride + a.c.page.div(pos));
-    }
-  };
-  uint4 x[2][kPasses];                           // K and V codes of the tile in flight
-  uint32_t byte[2][kPasses];                     // and their scales
-  auto load = [&](int v) {
-    const int64_t* st = v ? a.c.vst : a.c.kst;
-    const int64_t* ss = v ? a.c.vsst : a.c.ksst;
-    const uint8_t* src = (v ? a.c.v : a.c.k) + c.s.head * st[2] + (in_dim ? chunk * 16 : 0);
-    const uint8_t* sc = (v ? a.c.vs : a.c.ks) + c.s.head * ss[2];
-    const int last = c.s.start + c.s.rows - 1;
+    const int32_t* table = a.b.pages + (int64_t)c.b * a.b.pages_stride;
+    const int last = c.total() - 1;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-      const int pos = min(c.t * kKeys + r0 + i * kRows, last);
-      const int slot = pos - a.c.page.div(pos) * a.c.page.d;
-      const bool bad = (uint32_t)page[i] >= (uint64_t)a.c.n_pages;
-      if (bad) set_status(a.status, DSPARK_EPAGES);
-      const int pg = bad ? 0 : page[i];
-      x[v][i] = ptx::ldg_nc_na(src + pg * st[0] + slot * st[1]);
-      byte[v][i] = __ldg(sc + pg * ss[0] + slot * ss[1]);
+      const int pos = min(c.t * kKeys + r0 + i * kRows, last), at = a.c.page.div(pos);
+      page[i] = (uint32_t)__ldg(table + at);
+      slot[i] = pos - at * a.c.page.d;
     }
   };
-  fetch_pages();
-  load(0);
-  load(1);
-#pragma unroll 1
-  for (int i = 0; i <= kAhead + 1; ++i) ask(i == 0);
-  for (int n = 0; c.more;) {
-    // the tile whose codes are in registers
-    const int pos0 = c.t * kKeys, start = c.s.start, this_seg = c.seg;
-    const int rows = min(kKeys, start + c.s.rows - pos0);
-    c.next(a);
-    fetch_pages();
+  // rows of the same request kAhead tiles on, across a head's end
+  auto ask = [&]() {
+    int t = c.t + kAhead, head = c.head;
+    if (t >= c.tiles) {
+      t -= c.tiles;
+      ++head;
+    }
+    if (head >= a.Hkv || t >= c.tiles) return;
+    const int pos = min(t * kKeys + tid % kKeys, c.total() - 1), at = a.c.page.div(pos);
+    const uint32_t p = (uint32_t)__ldg(a.b.pages + (int64_t)c.b * a.b.pages_stride + at);
+    if (p >= (uint64_t)a.c.n_pages) return;
+    const int64_t s = pos - at * a.c.page.d;
+    ptx::prefetch_l2(tid >= kKeys
+                         ? a.c.v + p * a.c.vst[0] + s * a.c.vst[1] + head * a.c.vst[2]
+                         : a.c.k + p * a.c.kst[0] + s * a.c.kst[1] + head * a.c.kst[2]);
+  };
+  uint4 x[3][kPasses];
+  uint32_t byte[3][kPasses];
+  const uint32_t top_page = (uint32_t)(a.c.n_pages - 1);
+  auto load = [&](int set, bool v, int head) {
+    const uint8_t* src = (v ? a.c.v + head * a.c.vst[2] : a.c.k + head * a.c.kst[2]) +
+                         (in_dim ? chunk * 16 : 0);
+    const uint8_t* sc = v ? a.c.vs + head * a.c.vsst[2] : a.c.ks + head * a.c.ksst[2];
+    const int64_t st0 = v ? a.c.vst[0] : a.c.kst[0], st1 = v ? a.c.vst[1] : a.c.kst[1];
+    const int64_t ss0 = v ? a.c.vsst[0] : a.c.ksst[0], ss1 = v ? a.c.vsst[1] : a.c.ksst[1];
 #pragma unroll
-    for (int v = 0; v < 2; ++v, ++n) {
-      wait(sh, &sh->empty[n % L::kSlots], ((n / L::kSlots) & 1) ^ 1, a.status);
-      uint8_t* dst = ring + (n % L::kSlots) * L::kTile;
-      bool easy = true;
+    for (int i = 0; i < kPasses; ++i) {
+      const uint32_t p = min(page[i], top_page); // a bad page is reported at the end
+      worst = max(worst, page[i]);
+      x[set][i] = ptx::ldg_nc_na(src + p * st0 + slot[i] * st1);
+      byte[set][i] = __ldg(sc + p * ss0 + slot[i] * ss1);
+    }
+  };
+  int n = 0;
+  auto convert = [&](int set, bool v, const Tile& tile) {
+    wait(sh, &sh->empty[n % L::kSlots], ((n / L::kSlots) & 1) ^ 1, a.status);
+    uint8_t* dst = ring + (n % L::kSlots) * L::kTile;
+    if (tile.rows < kKeys || a.D < DP) {         // rows and elements past the end are zeros
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i)
+        if (!in_dim || r0 + i * kRows >= tile.rows) {
+          x[set][i] = make_uint4(0, 0, 0, 0);
+          byte[set][i] = 127;
+        }
+    }
+    bool easy = true;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) easy &= easy_scale<F16>(byte[set][i]);
+    if (easy) {
 #pragma unroll
       for (int i = 0; i < kPasses; ++i) {
-        easy &= easy_scale<F16>(byte[v][i]);
-        if (!in_dim || r0 + i * kRows >= rows) x[v][i] = make_uint4(0, 0, 0, 0);
+        const uint32_t m = scale_mul2<F16>(byte[set][i]);
+        const uint2 c0 = scale_codes<F16>(x[set][i].x, m), c1 = scale_codes<F16>(x[set][i].y, m);
+        const uint2 c2 = scale_codes<F16>(x[set][i].z, m), c3 = scale_codes<F16>(x[set][i].w, m);
+        *reinterpret_cast<uint4*>(dst + to0 + i * kRows * 128) = make_uint4(c0.x, c0.y, c1.x, c1.y);
+        *reinterpret_cast<uint4*>(dst + to1 + i * kRows * 128) = make_uint4(c2.x, c2.y, c3.x, c3.y);
       }
-      if (easy) {
+    } else {
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-          const uint32_t m = scale_mul2<F16>(byte[v][i]);
-          const uint2 c0 = scale_codes<F16>(x[v][i].x, m), c1 = scale_codes<F16>(x[v][i].y, m);
-          const uint2 c2 = scale_codes<F16>(x[v][i].z, m), c3 = scale_codes<F16>(x[v][i].w, m);
-          const uint4 y0 = make_uint4(c0.x, c0.y, c1.x, c1.y);
-          const uint4 y1 = make_uint4(c2.x, c2.y, c3.x, c3.y);
-          *reinterpret_cast<uint4*>(dst + to0 + i * kRows * 128) = odd ? y1 : y0;
-          *reinterpret_cast<uint4*>(dst + to1 + i * kRows * 128) = odd ? y0 : y1;
+      for (int i = 0; i < kPasses; ++i) {
+        const uint2 c0 = scale_codes_any<F16>(x[set][i].x, byte[set][i]);
+        const uint2 c1 = scale_codes_any<F16>(x[set][i].y, byte[set][i]);
+        const uint2 c2 = scale_codes_any<F16>(x[set][i].z, byte[set][i]);
+        const uint2 c3 = scale_codes_any<F16>(x[set][i].w, byte[set][i]);
+        uint4 y0 = make_uint4(c0.x, c0.y, c1.x, c1.y), y1 = make_uint4(c2.x, c2.y, c3.x, c3.y);
+        const int j = r0 + i * kRows - tile.draft;
+        if (v && j >= 0) {
+          const bool b0 = zero_nonfinite<F16>(&y0), b1 = zero_nonfinite<F16>(&y1);
+          if (b0 || b1) atomicOr(&sh->bad[tile.seg % kBadSets][j >> 5], 1u << (j & 31));
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-          // rows past the end stand for zeros whatever the scale of the row read for them
-          const uint32_t by = !in_dim || r0 + i * kRows >= rows ? 127 : byte[v][i];
-          const uint2 c0 = scale_codes_any<F16>(x[v][i].x, by);
-          const uint2 c1 = scale_codes_any<F16>(x[v][i].y, by);
-          const uint2 c2 = scale_codes_any<F16>(x[v][i].z, by);
-          const uint2 c3 = scale_codes_any<F16>(x[v][i].w, by);
-          uint4 y0 = make_uint4(c0.x, c0.y, c1.x, c1.y);
-          uint4 y1 = make_uint4(c2.x, c2.y, c3.x, c3.y);
-          const int j = pos0 + r0 + i * kRows - start;
-          if (v && j >= 0) {
-            const bool b0 = zero_nonfinite<F16>(&y0), b1 = zero_nonfinite<F16>(&y1);
-            if (b0 || b1) atomicOr(&sh->bad[this_seg % kBadSets][j >> 5], 1u << (j & 31));
-          }
-          *reinterpret_cast<uint4*>(dst + to0 + i * kRows * 128) = odd ? y1 : y0;
-          *reinterpret_cast<uint4*>(dst + to1 + i * kRows * 128) = odd ? y0 : y1;
-        }
+        *reinterpret_cast<uint4*>(dst + to0 + i * kRows * 128) = y0;
+        *reinterpret_cast<uint4*>(dst + to1 + i * kRows * 128) = y1;
       }
-      ptx::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&sh->full[n % L::kSlots]);
-      if (c.more) load(v);
-      if (v == 0) ask(false);
     }
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&sh->full[n % L::kSlots]);
+    ++n;
+  };
+  fetch_pages();
+  Tile cur = tile_at();
+  load(0, false, cur.head);
+  load(1, true, cur.head);
+  c.next(a);
+  bool more = c.more();
+  Tile nxt = cur;
+  if (more) {
+    fetch_pages();
+    nxt = tile_at();
   }
+  // K of the tile in set k, V in set v, set f free; false after the last tile
+  auto step = [&](int k, int v, int f) {
+    if (more) load(f, false, nxt.head);
+    convert(k, false, cur);
+    if (more) load(k, true, nxt.head);
+    const bool last = !more;
+    const Tile was = cur;
+    cur = nxt;
+    if (more) {
+      c.next(a);
+      more = c.more();
+      if (more) {
+        fetch_pages();
+        nxt = tile_at();
+        ask();
+      }
+    }
+    convert(v, true, was);
+    return !last;
+  };
+#pragma unroll 1
+  while (step(0, 1, 2) && step(2, 0, 1) && step(1, 2, 0)) {
+  }
+  if (worst > top_page) set_status(a.status, DSPARK_EPAGES);
 }
 
 // ------------------------------------------------------------------- MMA --
@@ -698,30 +734,32 @@ __device__ __forceinline__ void issue(const AttendArgs& a, uint8_t* smem, Tail* 
 
 // --------------------------------------------------------------- softmax --
 
+// Adds the non-finite elements of the draft rows of V that a row sees to its
+// result, which the calling thread has just written (columns d0 .. d1 - 1): what
+// 0 < p times them comes to.  The result: 16-bit values (out), or the part's
+// fp32 ones (column d at part[(d / 4) * stride + d % 4]).
 template <bool F16, bool E4M3>
-__device__ __forceinline__ float value_at(const AttendArgs& a, const Segment& s, int pos, int d) {
-  const Place p = place_of(a, s.b, pos, s.start + s.rows);
-  if (p.page < 0) return 0.f;
-  const uint8_t* row = a.c.v + p.page * a.c.vst[0] + p.slot * a.c.vst[1] + s.head * a.c.vst[2];
-  if (!E4M3) return to_float<F16>(reinterpret_cast<const uint16_t*>(row)[d]);
-  const uint8_t byte = a.c.vs[p.page * a.c.vsst[0] + p.slot * a.c.vsst[1] + s.head * a.c.vsst[2]];
-  return saturate16<F16>(e4m3x2_to_float2(row[d]).x * scale_value(byte));
-}
-
-// Adds the non-finite elements of the draft rows of V that this row sees to
-// columns d0 .. d0 + 31 of its O: what 0 < p times them comes to.
-template <bool F16, bool E4M3>
-__device__ __noinline__ void add_nonfinite(const AttendArgs& a, const Segment& s,
-                                           const uint32_t* bad, int node, int d0, float* o) {
-  for (int w = 0; w < DSPARK_TREE_MAX_NODES / 32; ++w) {
-    uint32_t m = bad[w] != 0 ? bad[w] & sees_word(a, s, node, w) : 0u;
-    while (m != 0) {
-      const int j = 32 * w + __ffs(m) - 1;
-      m &= m - 1;
-      for (int d = 0; d < 32 && d0 + d < a.D; ++d) {
-        const float v = value_at<F16, E4M3>(a, s, s.start + j, d0 + d);
-        if (!isfinite(v)) o[d] += v;
-      }
+__device__ __noinline__ void add_nonfinite(const AttendArgs& a, const uint32_t* bad,
+                                           const uint32_t* mask_row, int b, int rows, int start,
+                                           int head, int node, int d0, int d1, uint16_t* out,
+                                           float* part, int64_t stride) {
+#pragma unroll 1
+  for (int j = 0; j < rows; ++j) {
+    const bool see = mask_row ? mask_row[j >> 5] >> (j & 31) & 1 : j <= node;
+    if (!see || !(bad[j >> 5] >> (j & 31) & 1)) continue;
+    int64_t page;
+    int slot;
+    if (!locate(a.c, a.b, b, start + j, &page, &slot)) continue;
+    const uint8_t* v = a.c.v + page * a.c.vst[0] + slot * a.c.vst[1] + head * a.c.vst[2];
+    float scale = 1.f;
+    if (E4M3) scale = scale_value(a.c.vs[page * a.c.vsst[0] + slot * a.c.vsst[1] + head * a.c.vsst[2]]);
+#pragma unroll 1
+    for (int d = d0; d < d1; ++d) {
+      const float x = E4M3 ? saturate16<F16>(e4m3x2_to_float2(v[d]).x * scale)
+                           : to_float<F16>(reinterpret_cast<const uint16_t*>(v)[d]);
+      if (isfinite(x)) continue;
+      if (out) out[d] = (uint16_t)pack2<F16>(to_float<F16>(out[d]) + x, 0.f);
+      else part[(d >> 2) * stride + (d & 3)] += x;
     }
   }
 }
@@ -749,18 +787,17 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
 // Raw scores to base-2 exponents.
 struct Score {
   float sl2;        // |scale| log2(e)
-  float cap2;       // softcap log2(e)
+  float cap2;       // softcap log2(e), 0 without a cap
   float cap_in;     // 2 sl2 / softcap: tanh(y) = 1 - 2 / (2^(2 y log2(e)) + 1)
 };
 
-template <bool CAP>
-__device__ __forceinline__ float exponent(const Score& sc, float raw) {
-  return CAP ? sc.cap2 - 2.f * sc.cap2 * rcp(ex2(raw * sc.cap_in) + 1.f) : raw * sc.sl2;
+__device__ __forceinline__ float capped(const Score& sc, float raw) {
+  return sc.cap2 - 2.f * sc.cap2 * rcp(ex2(raw * sc.cap_in) + 1.f);
 }
 
 // O of this row times `back`.
 template <int DP>
-__device__ __forceinline__ void scale_row(uint32_t tm_o, float back) {
+__device__ __noinline__ void scale_row(uint32_t tm_o, float back) {
 #pragma unroll 1
   for (int c = 0; c < DP / 32; ++c) {
     uint32_t v[32];
@@ -772,52 +809,28 @@ __device__ __forceinline__ void scale_row(uint32_t tm_o, float back) {
   }
 }
 
-// Weights of 32 scores `v`, stored as P at tm_p; adds the unrounded ones to sum.
-template <bool F16, bool CAP, bool MASKED>
-__device__ __forceinline__ void weights_32(const Score& sc, const uint32_t (&v)[32], uint32_t see,
-                                           float sub, uint32_t tm_p, uint64_t (&sum)[2]) {
-  const uint64_t mul = pack_f32x2(sc.sl2, sc.sl2), neg = pack_f32x2(-sub, -sub);
-  uint32_t pk[16];
-#pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    const float r0 = __uint_as_float(v[2 * k]), r1 = __uint_as_float(v[2 * k + 1]);
-    float p0, p1;
-    if (CAP) {
-      p0 = exponent<true>(sc, r0) - sub;
-      p1 = exponent<true>(sc, r1) - sub;
-    } else {
-      unpack_f32x2(fma_f32x2(pack_f32x2(r0, r1), mul, neg), &p0, &p1);
-    }
-    p0 = ex2(p0);
-    p1 = ex2(p1);
-    if (MASKED) {
-      p0 = (see >> (2 * k)) & 1 ? p0 : 0.f;
-      p1 = (see >> (2 * k + 1)) & 1 ? p1 : 0.f;
-    }
-    sum[k & 1] = add_f32x2(sum[k & 1], pack_f32x2(p0, p1));
-    pk[k] = pack2<F16>(p0, p1);
-  }
-  ptx::tmem_st16(tm_p, pk);
-}
-
-template <bool MASKED>
-__device__ __forceinline__ void max_32(const uint32_t (&v)[32], uint32_t see, float (&mx)[4]) {
-#pragma unroll
-  for (int k = 0; k < 32; ++k) {
-    float x = __uint_as_float(v[k]);
-    if (MASKED) x = (see >> k) & 1 ? x : -INFINITY;
-    mx[k & 3] = fmaxf(mx[k & 3], x);
-  }
-}
-
-// One tile of one row: S in tensor memory becomes P, m and l move on, O is
-// rescaled if m moved.  WIDE holds the row's 128 scores in registers; else
-// they are read twice, 64 at a time.
-template <bool F16, bool CAP, bool MASKED, bool WIDE, int DP>
-__device__ __forceinline__ void softmax_tile(const Score& sc, uint32_t tm_s, uint32_t tm_o,
-                                             const uint32_t (&see)[4], bool first, float* mref,
-                                             float* l) {
+// The row's m after a tile whose largest exponent is x_max; l and O follow if it
+// moves: the first visible key sets it, later ones when it has grown enough.
+template <bool F16, int DP>
+__device__ __forceinline__ float move_reference(float x_max, bool first, uint32_t tm_o, float mref,
+                                                float* l) {
   constexpr float kShift = F16 ? 7.f : 0.f;
+  const bool move = x_max > mref + (mref == -INFINITY ? 0.f : kShift + 8.f);
+  const float m_new = move ? x_max - kShift : mref;
+  if (!first && __any_sync(0xffffffffu, move)) {
+    const float back = mref == -INFINITY ? 0.f : ex2(mref - m_new);
+    *l *= back;
+    scale_row<DP>(tm_o, back);
+  }
+  return m_new;
+}
+
+// One tile of one row: S in tensor memory becomes P, m and l move on.  All 128
+// keys are visible and scores are not capped.  WIDE holds the row's scores in
+// registers; else they are read twice, 64 at a time.
+template <bool F16, bool WIDE, int DP>
+__device__ __forceinline__ void softmax_tile(float sl2, uint32_t tm_s, uint32_t tm_o, bool first,
+                                             float* mref, float* l) {
   constexpr int kHold = WIDE ? 4 : 2;            // blocks of 32 scores held
   uint32_t v[kHold][32];
   float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -828,20 +841,15 @@ __device__ __forceinline__ void softmax_tile(const Score& sc, uint32_t tm_s, uin
 #pragma unroll
     for (int c = 0; c < kHold; ++c) ptx::tmem_wait_ld32(v[c]);
 #pragma unroll
-    for (int c = 0; c < kHold; ++c) max_32<MASKED>(v[c], see[h + c], mx);
+    for (int c = 0; c < kHold; ++c)
+#pragma unroll
+      for (int k = 0; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(v[c][k]));
   }
   const float raw_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-  const float x_max = raw_max == -INFINITY ? -INFINITY : exponent<CAP>(sc, raw_max);
-  // the first visible key sets m; later ones move it when it has grown enough
-  const bool move = x_max > *mref + (*mref == -INFINITY ? 0.f : kShift + 8.f);
-  const float m_new = move ? x_max - kShift : *mref;
-  if (!first && __any_sync(0xffffffffu, move)) {
-    const float back = *mref == -INFINITY ? 0.f : ex2(*mref - m_new);
-    *l *= back;
-    scale_row<DP>(tm_o, back);
-  }
-  *mref = m_new;
-  const float sub = m_new == -INFINITY ? 0.f : m_new;
+  const float x_max = raw_max == -INFINITY ? -INFINITY : raw_max * sl2;
+  *mref = move_reference<F16, DP>(x_max, first, tm_o, *mref, l);
+  const float sub = *mref == -INFINITY ? 0.f : *mref;
+  const uint64_t mul = pack_f32x2(sl2, sl2), neg = pack_f32x2(-sub, -sub);
   uint64_t sum[2] = {0, 0};
 #pragma unroll
   for (int h = 0; h < 4; h += kHold) {
@@ -852,8 +860,20 @@ __device__ __forceinline__ void softmax_tile(const Score& sc, uint32_t tm_s, uin
       for (int c = 0; c < kHold; ++c) ptx::tmem_wait_ld32(v[c]);
     }
 #pragma unroll
-    for (int c = 0; c < kHold; ++c)
-      weights_32<F16, CAP, MASKED>(sc, v[c], see[h + c], sub, tm_s + 16 * (h + c), sum);
+    for (int c = 0; c < kHold; ++c) {
+      uint32_t pk[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        float p0, p1;
+        unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[c][2 * k]),
+                                          __uint_as_float(v[c][2 * k + 1])), mul, neg), &p0, &p1);
+        p0 = ex2(p0);
+        p1 = ex2(p1);
+        sum[k & 1] = add_f32x2(sum[k & 1], pack_f32x2(p0, p1));
+        pk[k] = pack2<F16>(p0, p1);
+      }
+      ptx::tmem_st16(tm_s + 16 * (h + c), pk);
+    }
   }
   float a, b;
   unpack_f32x2(add_f32x2(sum[0], sum[1]), &a, &b);
@@ -861,7 +881,59 @@ __device__ __forceinline__ void softmax_tile(const Score& sc, uint32_t tm_s, uin
   ptx::tmem_wait_st();
 }
 
-template <bool F16, bool E4M3, bool CAP, int DP>
+// The same for tiles with invisible keys (see: a bit a key) or capped scores,
+// 32 keys at a time.  Returns {m, l}.
+template <bool F16, int DP>
+__device__ __noinline__ float2 softmax_tile_any(Score sc, uint32_t tm_s, uint32_t tm_o, uint4 see,
+                                                bool first, float mref, float l) {
+  const bool cap = sc.cap2 > 0.f;
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    const uint32_t m = c == 0 ? see.x : c == 1 ? see.y : c == 2 ? see.z : see.w;
+    uint32_t v[32];
+    ptx::tmem_ld32(tm_s + 32 * c, v);
+    ptx::tmem_wait_ld32(v);
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+      mx[k & 3] = fmaxf(mx[k & 3], (m >> k) & 1 ? __uint_as_float(v[k]) : -INFINITY);
+  }
+  const float raw_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+  float x_max = raw_max == -INFINITY ? -INFINITY : raw_max * sc.sl2;
+  if (cap && raw_max != -INFINITY) x_max = capped(sc, raw_max);
+  mref = move_reference<F16, DP>(x_max, first, tm_o, mref, &l);
+  const float sub = mref == -INFINITY ? 0.f : mref;
+  float sum[2] = {0.f, 0.f};
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    const uint32_t m = c == 0 ? see.x : c == 1 ? see.y : c == 2 ? see.z : see.w;
+    uint32_t v[32], pk[16];
+    ptx::tmem_ld32(tm_s + 32 * c, v);
+    ptx::tmem_wait_ld32(v);
+    if (cap) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        v[k] = __float_as_uint(capped(sc, __uint_as_float(v[k])) - sub);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        v[k] = __float_as_uint(fmaf(__uint_as_float(v[k]), sc.sl2, -sub));
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const float p0 = (m >> (2 * k)) & 1 ? ex2(__uint_as_float(v[2 * k])) : 0.f;
+      const float p1 = (m >> (2 * k + 1)) & 1 ? ex2(__uint_as_float(v[2 * k + 1])) : 0.f;
+      sum[0] += p0;
+      sum[1] += p1;
+      pk[k] = pack2<F16>(p0, p1);
+    }
+    ptx::tmem_st16(tm_s + 16 * c, pk);
+  }
+  ptx::tmem_wait_st();
+  return make_float2(mref, l + (sum[0] + sum[1]));
+}
+
+template <bool F16, bool E4M3, int DP>
 __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail* sh) {
   using L = Layout<DP>;
   const int wg = threadIdx.x / 128, lane_row = threadIdx.x % 128;
@@ -872,7 +944,7 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
   Score sc;
   sc.sl2 = fabsf(a.scale) * kLog2e;
   sc.cap2 = a.softcap * kLog2e;
-  sc.cap_in = CAP ? 2.f * sc.sl2 / a.softcap : 0.f;
+  sc.cap_in = a.softcap > 0.f ? 2.f * sc.sl2 / a.softcap : 0.f;
   const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
   Walker w;
   Segment s;
@@ -909,6 +981,11 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
           x[k].y ^= flip;
           x[k].z ^= flip;
           x[k].w ^= flip;
+          if (E4M3 && !F16) {
+            const uint2 lo = swap_middle(make_uint2(x[k].x, x[k].y));
+            const uint2 hi = swap_middle(make_uint2(x[k].z, x[k].w));
+            x[k] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+          }
           if (r < q_rows)
             *reinterpret_cast<uint4*>(smem + (r / kKeys) * L::kTile +
                                       tile_offset(r % kKeys, chunk)) = x[k];
@@ -923,6 +1000,8 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
     const bool warp_valid = local - threadIdx.x % 32 < rows;
     const int grow = s.group * kGroupRows + (valid ? local : 0);
     const int node = a.group.div(grow);
+    const uint32_t* mask_row =
+        a.mask ? a.mask + (int64_t)(s.row0 + node) * a.mask_stride : nullptr;
     float mref = -INFINITY, l = 0.f;
     const int step = pair ? 1 : 2;
     for (int i = pair ? 0 : wg; i < n; i += step) {
@@ -932,15 +1011,18 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
       if (warp_valid) {
         const int pos0 = (s.t0 + i) * kKeys;
         const bool masked = pos0 + kKeys > s.start;
-        uint32_t see[4];
         const uint32_t own_o = tm_o + wg * 128;
         const bool first = i < step;
-        if (!masked && !CAP) {
-          softmax_tile<F16, false, false, !E4M3, DP>(sc, tm_s, own_o, see, first, &mref, &l);
+        if (!masked && sc.cap2 == 0.f) {
+          softmax_tile<F16, !E4M3, DP>(sc.sl2, tm_s, own_o, first, &mref, &l);
         } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) see[c] = sees_32(a, s, node, pos0 + 32 * c);
-          softmax_tile<F16, CAP, true, !E4M3, DP>(sc, tm_s, own_o, see, first, &mref, &l);
+          const float2 r = softmax_tile_any<F16, DP>(
+              sc, tm_s, own_o,
+              masked ? sees_128(mask_row, s.rows, node, pos0 - s.start)
+                     : make_uint4(~0u, ~0u, ~0u, ~0u),
+              first, mref, l);
+          mref = r.x;
+          l = r.y;
         }
         ptx::tc_fence_before();
       }
@@ -989,7 +1071,14 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = fmaf(__uint_as_float(v[k]), w1, o[k]);
         }
-        if (any_bad != 0) add_nonfinite<F16, E4M3>(a, s, bad, node, 32 * c, o);
+        if (E4M3 && !F16) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 4) {
+            const float y = o[k + 1];
+            o[k + 1] = o[k + 2];
+            o[k + 2] = y;
+          }
+        }
         if (valid && whole) {
           uint4* dst = reinterpret_cast<uint4*>(a.out + out_row * a.D + 32 * c);
 #pragma unroll
@@ -1010,19 +1099,24 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
         }
         __syncwarp();
       }
+      if (valid && any_bad != 0)
+        add_nonfinite<F16, E4M3>(
+            a, bad, mask_row, s.b, s.rows, s.start, s.head, node, 32 * c0, min(32 * c1, a.D),
+            whole ? a.out + out_row * a.D : nullptr,
+            a.part_o + ((int64_t)part * (DP / 4) * a.part_rows + local) * 4,
+            (int64_t)a.part_rows * 4);
+      __syncwarp();
       if (valid && (pair || wg == 0)) {
         if (!whole) a.part_ml[(int64_t)part * a.part_rows + local] = make_float2(mref, l);
         else if (a.lse) a.lse[out_row] = l == 0.f ? -INFINITY : (mref + log2f(l)) * kLn2;
       }
     }
-    if (!whole && s.t0 == 0 && threadIdx.x == 0) {
-      // the item's other parts lie in the CTAs up to the one that holds its last unit
-      const int64_t last = s.item_end - 1;
-      const int n_cta = (int)(sh->total < a.n_cta ? sh->total : a.n_cta);
-      int c = (int)(last * n_cta / sh->total);
-      while (share(sh->total, n_cta, c + 1) <= last) ++c;
-      while (share(sh->total, n_cta, c) > last) --c;
-      a.part_of[blockIdx.x] = make_int4(s.b, s.head, s.group, c - (int)blockIdx.x + 1);
+    if (!whole && threadIdx.x == 0) {
+      // the CTAs that share the item: from the one with its first unit to that with its last
+      const int first = holder(sh->total, a.n_cta, s.item_end - s.tiles);
+      const int last = holder(sh->total, a.n_cta, s.item_end - 1);
+      a.part_of[part] = make_int4(s.b, (int)((uint32_t)s.head << 16 | s.group), first,
+                                   last - first + 1);
     }
     ptx::tc_fence_before();
     asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -1076,8 +1170,14 @@ __device__ __forceinline__ void plan(const AttendArgs& a, Tail* sh) {
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     if (u1 > u0 && u0 >= before && u0 < before + mine[k]) {
-      sh->b0 = threadIdx.x * per + k;
-      sh->off0 = u0 - before;
+      const int b = threadIdx.x * per + k;
+      bool ok;
+      const Request r = load_request(a, b, &ok);
+      const int64_t item = (u0 - before) / r.tiles;
+      sh->b0 = b;
+      sh->t0 = (int)(u0 - before - item * r.tiles);
+      sh->head0 = (int)(item / r.groups);
+      sh->group0 = (int)(item % r.groups);
     }
     before += mine[k];
   }
@@ -1113,7 +1213,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1)
     }
     ptx::fence_mbar_init();
     sh->abort = 0;
-    a.part_of[blockIdx.x] = make_int4(0, 0, 0, 0);
+    a.part_of[2 * blockIdx.x] = a.part_of[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
   }
   for (int i = threadIdx.x; i < kBadSets * (DSPARK_TREE_MAX_NODES / 32); i += R::kThreads)
     (&sh->bad[0][0])[i] = 0;
@@ -1122,15 +1222,14 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   if (warp < kSoftWarps) {
-    ptx::more_registers<R::kSoftRegs>();
-    if (a.softcap > 0.f) softmax<F16, E4M3, true, DP>(a, smem, sh);
-    else softmax<F16, E4M3, false, DP>(a, smem, sh);
+    ptx::set_registers<R::kLaunchRegs, R::kSoftRegs>();
+    softmax<F16, E4M3, DP>(a, smem, sh);
   } else if (warp < R::kMmaWarp) {
-    ptx::fewer_registers<R::kProdRegs>();
+    ptx::set_registers<R::kLaunchRegs, R::kProdRegs>();
     if (E4M3) produce8<F16, DP>(a, smem, sh);
     else produce16<F16, DP>(a, maps, smem, sh);
   } else {
-    ptx::fewer_registers<R::kMmaRegs>();
+    ptx::set_registers<R::kLaunchRegs, R::kMmaRegs>();
     if (warp < R::kMmaWarp + 2 && threadIdx.x % 32 == 0)
       issue<F16, DP>(a, smem, sh, warp - R::kMmaWarp);
   }
@@ -1145,63 +1244,91 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1)
   if (warp == R::kMmaWarp) ptx::tmem_dealloc(sh->tmem, 512);
 }
 
-// Joins the parts of the items that several CTAs share: block (c, y) takes rows
-// 32 y .. of the item whose first part CTA c left.  The parts are added in the
-// order of the keys, so the result does not depend on timing.
+// Joins the parts of the items that several CTAs share.  An item of P parts has
+// P x kJoinSplit blocks: block (p, y) of a part's slot p takes every (P x
+// kJoinSplit)-th piece of 32 rows by 16 columns.  Its eight warps take every
+// eighth part, lane = row, and are then added in order, so the result does not
+// depend on timing.
 constexpr int kJoinThreads = 256;
+constexpr int kJoinSplit = 4;
 
 template <bool F16, int DP>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttendArgs a) {
+  __shared__ float4 part_sum[8][4][32];
+  __shared__ float2 part_ml[8][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 of = a.part_of[blockIdx.x];
-  if (of.w == 0) return;
+  const int parts = of.w;
+  if (parts == 0) return;
   bool ok;
   const Request r = load_request(a, of.x, &ok);
-  const int local = blockIdx.y * 32 + threadIdx.x % 32;
-  const int grow = of.z * kGroupRows + local;
-  if (local >= kGroupRows || grow >= r.rows * a.G) return;
-  const int node = a.group.div(grow);
-  const int64_t out_row = (int64_t)(r.row0 + node) * a.Hq + of.y * a.G + grow - node * a.G;
-  const int p0 = 2 * blockIdx.x + 1, parts = of.w;
-  auto part = [&](int i) { return i == 0 ? p0 : p0 - 1 + 2 * i; };   // slot 0 of the later CTAs
-  float m = -INFINITY;
-#pragma unroll 4
-  for (int i = 0; i < parts; ++i)
-    m = fmaxf(m, a.part_ml[(int64_t)part(i) * a.part_rows + local].x);
-  const float sub = m == -INFINITY ? 0.f : m;
-  float l = 0.f;
-  constexpr int kEach = DP / 4 / (kJoinThreads / 32);       // float4 columns a thread
-  float4 o[kEach];
+  const int head = (int)((uint32_t)of.y >> 16), group = of.y & 0xffff, first = of.z;
+  const int rows = min(kGroupRows, r.rows * a.G - group * kGroupRows);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int pieces = (rows + 31) / 32 * (DP / 16);
+  // this block's place among the item's: which part's slot, and y
+  const int mine = ((int)blockIdx.x / 2 - first) * kJoinSplit + blockIdx.y;
+  for (int piece = mine; piece < pieces; piece += parts * kJoinSplit) {
+    const int c4 = piece % (DP / 16) * 4, local = piece / (DP / 16) * 32 + lane;   // float4 column
+    float m = -INFINITY, l = 0.f;
+    float4 o[4];
 #pragma unroll
-  for (int k = 0; k < kEach; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  const int g0 = threadIdx.x / 32;
-#pragma unroll 2
-  for (int i = 0; i < parts; ++i) {
-    const float2 ml = a.part_ml[(int64_t)part(i) * a.part_rows + local];
-    const float w = ex2(ml.x - sub);
-    l = fmaf(ml.y, w, l);
-    const float4* src = reinterpret_cast<const float4*>(a.part_o) +
-                        (int64_t)part(i) * (DP / 4) * a.part_rows + local;
+    for (int k = 0; k < 4; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = warp; i < parts; i += 8) {
+      const int64_t part = 2 * (first + i) + (i == 0 ? 1 : 0);
+      const float2 ml = a.part_ml[part * a.part_rows + local];
+      const float4* src = reinterpret_cast<const float4*>(a.part_o) +
+                          (part * (DP / 4) + c4) * a.part_rows + local;
+      float4 x[4];
 #pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-      const float4 x = src[(int64_t)(g0 + k * (kJoinThreads / 32)) * a.part_rows];
-      o[k].x = fmaf(x.x, w, o[k].x);
-      o[k].y = fmaf(x.y, w, o[k].y);
-      o[k].z = fmaf(x.z, w, o[k].z);
-      o[k].w = fmaf(x.w, w, o[k].w);
+      for (int k = 0; k < 4; ++k) x[k] = src[(int64_t)k * a.part_rows];
+      const float m_new = fmaxf(m, ml.x), sub = m_new == -INFINITY ? 0.f : m_new;
+      const float wo = ex2(m - sub), wx = ex2(ml.x - sub);
+      m = m_new;
+      l = l * wo + ml.y * wx;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        o[k].x = o[k].x * wo + x[k].x * wx;
+        o[k].y = o[k].y * wo + x[k].y * wx;
+        o[k].z = o[k].z * wo + x[k].z * wx;
+        o[k].w = o[k].w * wo + x[k].w * wx;
+      }
     }
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-  for (int k = 0; k < kEach; ++k) {
-    const int d = 4 * (g0 + k * (kJoinThreads / 32));
-    if (d >= a.D) continue;
-    const uint2 y = l == 0.f ? make_uint2(0u, 0u)
-                             : make_uint2(pack2<F16>(o[k].x * inv, o[k].y * inv),
-                                          pack2<F16>(o[k].z * inv, o[k].w * inv));
-    *reinterpret_cast<uint2*>(a.out + out_row * a.D + d) = y;
+    for (int k = 0; k < 4; ++k) part_sum[warp][k][lane] = o[k];
+    part_ml[warp][lane] = make_float2(m, l);
+    __syncthreads();
+    const int grow = group * kGroupRows + local;
+    if (warp < 4 && local < rows) {              // warp k finishes float4 column c4 + k
+      const int live = min(8, parts);
+      m = -INFINITY;
+      for (int i = 0; i < live; ++i) m = fmaxf(m, part_ml[i][lane].x);
+      const float sub = m == -INFINITY ? 0.f : m;
+      l = 0.f;
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = 0; i < live; ++i) {
+        const float w = ex2(part_ml[i][lane].x - sub);
+        const float4 x = part_sum[i][warp][lane];
+        l = fmaf(part_ml[i][lane].y, w, l);
+        s.x = fmaf(x.x, w, s.x);
+        s.y = fmaf(x.y, w, s.y);
+        s.z = fmaf(x.z, w, s.z);
+        s.w = fmaf(x.w, w, s.w);
+      }
+      const int node = a.group.div(grow);
+      const int64_t out_row = (int64_t)(r.row0 + node) * a.Hq + head * a.G + grow - node * a.G;
+      const int d = 4 * (c4 + warp);
+      if (d < a.D) {
+        const float inv = 1.f / l;
+        *reinterpret_cast<uint2*>(a.out + out_row * a.D + d) =
+            l == 0.f ? make_uint2(0u, 0u)
+                     : make_uint2(pack2<F16>(s.x * inv, s.y * inv),
+                                  pack2<F16>(s.z * inv, s.w * inv));
+      }
+      if (d == 0 && a.lse) a.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    }
+    __syncthreads();
   }
-  if (g0 == 0 && a.lse) a.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 template <int DP>
@@ -1220,7 +1347,7 @@ cudaError_t launch(const AttendArgs& a, const TileMaps& maps, cudaStream_t strea
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(a.n_cta, (a.part_rows + 31) / 32);
+  cfg.gridDim = dim3(2 * a.n_cta, kJoinSplit);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cfg.attrs = &attr;
@@ -1236,15 +1363,21 @@ cudaError_t setup() {
   cudaFuncAttributes fa;
   cudaError_t e = cudaFuncGetAttributes(&fa, attend_kernel<F16, E4M3, DP>);
   if (e != cudaSuccess) return e;
-  if (fa.numRegs * R::kThreads < R::kSplit * 32) return cudaErrorInvalidConfiguration;
+  if (fa.numRegs != R::kLaunchRegs) return cudaErrorInvalidConfiguration;
   return cudaFuncSetAttribute(attend_kernel<F16, E4M3, DP>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<DP>());
 }
 
+// The join keeps the main kernel's split of shared memory and L1: another would
+// have the SMs drained and set up anew between the two.
 template <bool F16, int DP>
 cudaError_t setup_both() {
-  const cudaError_t e = setup<F16, false, DP>();
-  return e != cudaSuccess ? e : setup<F16, true, DP>();
+  cudaError_t e = setup<F16, false, DP>();
+  if (e == cudaSuccess) e = setup<F16, true, DP>();
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(join_kernel<F16, DP>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+  return e;
 }
 
 }  // namespace

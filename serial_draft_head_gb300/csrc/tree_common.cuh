@@ -135,7 +135,7 @@ struct AttendArgs {
   // part_rows rows: O (fp32, [D / 4][part_rows][4]) and {m, l} a row
   float* part_o;
   float2* part_ml;
-  int4* part_of;             // per CTA: {request, head << 8 | row group, parts, 0} it starts
+  int4* part_of;             // per part: {request, head << 16 | row group, first CTA, parts}
   int part_rows;
   int* status;
 };
