@@ -59,8 +59,8 @@ struct Roles {
   static constexpr int kMmaWarp = kSoftWarps + kProdWarps;
   static constexpr int kThreads = (kMmaWarp + 4) * 32;
   static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
-  static constexpr int kSoftRegs = E4M3 ? 112 : 184;
-  static constexpr int kProdRegs = E4M3 ? 104 : 88;
+  static constexpr int kSoftRegs = E4M3 ? 120 : 184;
+  static constexpr int kProdRegs = E4M3 ? 96 : 88;
   static constexpr int kMmaRegs = E4M3 ? 48 : 56;
   static constexpr int kSplit =
       kSoftWarps * kSoftRegs + kProdWarps * kProdRegs + 4 * kMmaRegs;   // times 32
@@ -104,8 +104,7 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 //
 // A parity wait tells a phase from the next one only, so whoever waits on a
 // barrier waits for each of its phases in order.
-__device__ __forceinline__ void wait(Tail* s, uint64_t* bar, uint32_t parity, int* status) {
-  if (ptx::mbar_try_wait(bar, parity)) return;
+__device__ __forceinline__ void wait_long(Tail* s, uint64_t* bar, uint32_t parity, int* status) {
   const uint64_t t0 = globaltimer_ns();
   uint32_t spins = 0;
   while (!ptx::mbar_try_wait(bar, parity)) {
@@ -117,6 +116,10 @@ __device__ __forceinline__ void wait(Tail* s, uint64_t* bar, uint32_t parity, in
       return;
     }
   }
+}
+
+__device__ __forceinline__ void wait(Tail* s, uint64_t* bar, uint32_t parity, int* status) {
+  if (!ptx::mbar_try_wait(bar, parity)) wait_long(s, bar, parity, status);
 }
 
 __device__ __forceinline__ bool aborted(const Tail* s) {
@@ -508,10 +511,27 @@ __device__ __forceinline__ void produce16(const AttendArgs& a, const TileMaps& m
   }
 }
 
+// A chunk of 16 codes whose scale is not easy, stored at p0 and p1.  Non-finite
+// elements of a draft row of V are zeroed and noted (bad: its bit's word).
+template <bool F16>
+__device__ __noinline__ void store_any(uint4 x, uint32_t byte, uint8_t* p0, uint8_t* p1,
+                                       uint32_t* bad, uint32_t bit) {
+  const uint2 c0 = scale_codes_any<F16>(x.x, byte), c1 = scale_codes_any<F16>(x.y, byte);
+  const uint2 c2 = scale_codes_any<F16>(x.z, byte), c3 = scale_codes_any<F16>(x.w, byte);
+  uint4 y0 = make_uint4(c0.x, c0.y, c1.x, c1.y), y1 = make_uint4(c2.x, c2.y, c3.x, c3.y);
+  if (bad) {
+    const bool b0 = zero_nonfinite<F16>(&y0), b1 = zero_nonfinite<F16>(&y1);
+    if (b0 || b1) atomicOr(bad, bit);
+  }
+  *reinterpret_cast<uint4*>(p0) = y0;
+  *reinterpret_cast<uint4*>(p1) = y1;
+}
+
 // e4m3 cache, through registers.  A half tile (K or V) is converted while the
-// next two are in flight in registers (three sets, used in turn); their pages
-// were looked up half a tile earlier, and the rows kAhead tiles on are asked for
-// in L2, one row of K or V a thread.
+// next is in flight in registers; pages are looked up two half tiles earlier,
+// and the rows kAhead tiles on are asked for in L2, one row of K or V a thread.
+// The loop is one half tile: unrolled over register sets it outgrew the
+// instruction cache.
 template <bool F16, int DP>
 __device__ __forceinline__ void produce8(const AttendArgs& a, uint8_t* smem, Tail* sh) {
   using L = Layout<DP>;
@@ -531,7 +551,7 @@ __device__ __forceinline__ void produce8(const AttendArgs& a, uint8_t* smem, Tai
   const bool in_dim = chunk * 16 < a.D;
   const uint32_t to0 = tile_offset(r0, 2 * chunk), to1 = tile_offset(r0, 2 * chunk + 1);
   uint8_t* ring = smem + L::kRing;
-  Cursor c;                                      // the tile whose pages are looked up
+  Cursor c;                                      // the tile after the one in `page`
   c.init(a, sh);
   if (!c.more()) return;
   struct Tile {
@@ -568,10 +588,10 @@ __device__ __forceinline__ void produce8(const AttendArgs& a, uint8_t* smem, Tai
                          ? a.c.v + p * a.c.vst[0] + s * a.c.vst[1] + head * a.c.vst[2]
                          : a.c.k + p * a.c.kst[0] + s * a.c.kst[1] + head * a.c.kst[2]);
   };
-  uint4 x[3][kPasses];
-  uint32_t byte[3][kPasses];
+  uint4 x[kPasses], x_next[kPasses];
+  uint32_t byte[kPasses], byte_next[kPasses];
   const uint32_t top_page = (uint32_t)(a.c.n_pages - 1);
-  auto load = [&](int set, bool v, int head) {
+  auto load = [&](bool v, int head) {
     const uint8_t* src = (v ? a.c.v + head * a.c.vst[2] : a.c.k + head * a.c.kst[2]) +
                          (in_dim ? chunk * 16 : 0);
     const uint8_t* sc = v ? a.c.vs + head * a.c.vsst[2] : a.c.ks + head * a.c.ksst[2];
@@ -581,89 +601,71 @@ __device__ __forceinline__ void produce8(const AttendArgs& a, uint8_t* smem, Tai
     for (int i = 0; i < kPasses; ++i) {
       const uint32_t p = min(page[i], top_page); // a bad page is reported at the end
       worst = max(worst, page[i]);
-      x[set][i] = ptx::ldg_nc_na(src + p * st0 + slot[i] * st1);
-      byte[set][i] = __ldg(sc + p * ss0 + slot[i] * ss1);
+      x_next[i] = ptx::ldg_nc_na(src + p * st0 + slot[i] * st1);
+      byte_next[i] = __ldg(sc + p * ss0 + slot[i] * ss1);
     }
   };
-  int n = 0;
-  auto convert = [&](int set, bool v, const Tile& tile) {
+  fetch_pages();
+  Tile cur = tile_at();
+  load(false, cur.head);
+  bool more = true;                              // another half tile after the one in x_next
+#pragma unroll 1
+  for (int n = 0; more; ++n) {
+    const bool v = n & 1;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      x[i] = x_next[i];
+      byte[i] = byte_next[i];
+    }
+    const Tile tile = cur;
+    if (!v) {
+      load(true, cur.head);                      // V of the same tile, then the next tile's pages
+      c.next(a);
+      if (c.more()) {
+        fetch_pages();
+        ask();
+      }
+    } else {
+      more = c.more();
+      if (more) {
+        cur = tile_at();
+        load(false, cur.head);
+      }
+    }
     wait(sh, &sh->empty[n % L::kSlots], ((n / L::kSlots) & 1) ^ 1, a.status);
     uint8_t* dst = ring + (n % L::kSlots) * L::kTile;
     if (tile.rows < kKeys || a.D < DP) {         // rows and elements past the end are zeros
 #pragma unroll
       for (int i = 0; i < kPasses; ++i)
         if (!in_dim || r0 + i * kRows >= tile.rows) {
-          x[set][i] = make_uint4(0, 0, 0, 0);
-          byte[set][i] = 127;
+          x[i] = make_uint4(0, 0, 0, 0);
+          byte[i] = 127;
         }
     }
     bool easy = true;
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) easy &= easy_scale<F16>(byte[set][i]);
+    for (int i = 0; i < kPasses; ++i) easy &= easy_scale<F16>(byte[i]);
     if (easy) {
 #pragma unroll
       for (int i = 0; i < kPasses; ++i) {
-        const uint32_t m = scale_mul2<F16>(byte[set][i]);
-        const uint2 c0 = scale_codes<F16>(x[set][i].x, m), c1 = scale_codes<F16>(x[set][i].y, m);
-        const uint2 c2 = scale_codes<F16>(x[set][i].z, m), c3 = scale_codes<F16>(x[set][i].w, m);
+        const uint32_t m = scale_mul2<F16>(byte[i]);
+        const uint2 c0 = scale_codes<F16>(x[i].x, m), c1 = scale_codes<F16>(x[i].y, m);
+        const uint2 c2 = scale_codes<F16>(x[i].z, m), c3 = scale_codes<F16>(x[i].w, m);
         *reinterpret_cast<uint4*>(dst + to0 + i * kRows * 128) = make_uint4(c0.x, c0.y, c1.x, c1.y);
         *reinterpret_cast<uint4*>(dst + to1 + i * kRows * 128) = make_uint4(c2.x, c2.y, c3.x, c3.y);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < kPasses; ++i) {
-        const uint2 c0 = scale_codes_any<F16>(x[set][i].x, byte[set][i]);
-        const uint2 c1 = scale_codes_any<F16>(x[set][i].y, byte[set][i]);
-        const uint2 c2 = scale_codes_any<F16>(x[set][i].z, byte[set][i]);
-        const uint2 c3 = scale_codes_any<F16>(x[set][i].w, byte[set][i]);
-        uint4 y0 = make_uint4(c0.x, c0.y, c1.x, c1.y), y1 = make_uint4(c2.x, c2.y, c3.x, c3.y);
         const int j = r0 + i * kRows - tile.draft;
-        if (v && j >= 0) {
-          const bool b0 = zero_nonfinite<F16>(&y0), b1 = zero_nonfinite<F16>(&y1);
-          if (b0 || b1) atomicOr(&sh->bad[tile.seg % kBadSets][j >> 5], 1u << (j & 31));
-        }
-        *reinterpret_cast<uint4*>(dst + to0 + i * kRows * 128) = y0;
-        *reinterpret_cast<uint4*>(dst + to1 + i * kRows * 128) = y1;
+        const bool draft = v && j >= 0;
+        store_any<F16>(x[i], byte[i], dst + to0 + i * kRows * 128, dst + to1 + i * kRows * 128,
+                       draft ? &sh->bad[tile.seg % kBadSets][j >> 5] : nullptr, 1u << (j & 31));
       }
     }
     ptx::fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(&sh->full[n % L::kSlots]);
-    ++n;
-  };
-  fetch_pages();
-  Tile cur = tile_at();
-  load(0, false, cur.head);
-  load(1, true, cur.head);
-  c.next(a);
-  bool more = c.more();
-  Tile nxt = cur;
-  if (more) {
-    fetch_pages();
-    nxt = tile_at();
-  }
-  // K of the tile in set k, V in set v, set f free; false after the last tile
-  auto step = [&](int k, int v, int f) {
-    if (more) load(f, false, nxt.head);
-    convert(k, false, cur);
-    if (more) load(k, true, nxt.head);
-    const bool last = !more;
-    const Tile was = cur;
-    cur = nxt;
-    if (more) {
-      c.next(a);
-      more = c.more();
-      if (more) {
-        fetch_pages();
-        nxt = tile_at();
-        ask();
-      }
-    }
-    convert(v, true, was);
-    return !last;
-  };
-#pragma unroll 1
-  while (step(0, 1, 2) && step(2, 0, 1) && step(1, 2, 0)) {
   }
   if (worst > top_page) set_status(a.status, DSPARK_EPAGES);
 }
@@ -700,7 +702,7 @@ __device__ __forceinline__ void issue(const AttendArgs& a, uint8_t* smem, Tail* 
       if (!aborted(sh)) {
         ptx::tc_fence_after();
         const uint32_t k_addr = ring + (ks % L::kSlots) * L::kTile;
-#pragma unroll
+#pragma unroll 4
         for (int k = 0; k < DP / 16; ++k) {
           const uint32_t at = (k / 4) * (kKeys * 128) + (k % 4) * 32;
           ptx::tc_mma_smem(tm_s, ptx::smem_desc_swizzle128(q + at, 16, 1024),
@@ -715,7 +717,7 @@ __device__ __forceinline__ void issue(const AttendArgs& a, uint8_t* smem, Tail* 
       if (!aborted(sh)) {
         ptx::tc_fence_after();
         const uint32_t v_addr = ring + (vs % L::kSlots) * L::kTile;
-#pragma unroll
+#pragma unroll 4
         for (int k = 0; k < kKeys / 16; ++k)
           ptx::tc_mma_tmem_a(tm_o, tm_s + 8 * k,
                              ptx::smem_desc_swizzle128(v_addr + k * 2048, kKeys * 128, 1024), kPV,
@@ -834,7 +836,7 @@ __device__ __forceinline__ void softmax_tile(float sl2, uint32_t tm_s, uint32_t 
   constexpr int kHold = WIDE ? 4 : 2;            // blocks of 32 scores held
   uint32_t v[kHold][32];
   float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
+#pragma unroll 1
   for (int h = 0; h < 4; h += kHold) {
 #pragma unroll
     for (int c = 0; c < kHold; ++c) ptx::tmem_ld32(tm_s + 32 * (h + c), v[c]);
@@ -851,7 +853,7 @@ __device__ __forceinline__ void softmax_tile(float sl2, uint32_t tm_s, uint32_t 
   const float sub = *mref == -INFINITY ? 0.f : *mref;
   const uint64_t mul = pack_f32x2(sl2, sl2), neg = pack_f32x2(-sub, -sub);
   uint64_t sum[2] = {0, 0};
-#pragma unroll
+#pragma unroll 1
   for (int h = 0; h < 4; h += kHold) {
     if (!WIDE) {
 #pragma unroll
