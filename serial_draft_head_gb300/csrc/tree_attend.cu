@@ -672,6 +672,8 @@ __device__ __forceinline__ void produce8(const AttendArgs& a, uint8_t* smem, Tai
 
 // ------------------------------------------------------------------- MMA --
 
+// One warp a stream; all lanes run the loop and one issues, so that descriptors
+// stay in uniform registers.
 template <bool F16, int DP>
 __device__ __forceinline__ void issue(const AttendArgs& a, uint8_t* smem, Tail* sh, int stream) {
   using L = Layout<DP>;
@@ -687,49 +689,53 @@ __device__ __forceinline__ void issue(const AttendArgs& a, uint8_t* smem, Tail* 
   for (uint32_t seg = 0; w.next(a, &s); ++seg) {
     const bool pair = group_rows(a, s) > kKeys;
     const int n = s.t1 - s.t0, step = pair ? 1 : 2;
-    const uint32_t q = ptx::smem_u32(smem) + (pair ? stream * L::kTile : 0);
+    const uint64_t q_desc = ptx::smem_desc_swizzle128(
+        ptx::smem_u32(smem) + (pair ? stream * L::kTile : 0), 16, 1024);
     wait(sh, &sh->q_full, seg & 1, a.status);
     for (int i = 0; i < n; ++i) {
       const uint32_t ks = slot0 + 2 * i, vs = ks + 1;
-      if (!pair && (i & 1) != stream) {          // the other stream's tile: its phases pass
-        wait(sh, &sh->full[ks % L::kSlots], (ks / L::kSlots) & 1, a.status);
-        wait(sh, &sh->full[vs % L::kSlots], (vs / L::kSlots) & 1, a.status);
-        continue;
-      }
+      const bool own = pair || (i & 1) == stream;         // else the phases only pass
       // S and P share columns: the last product that reads P is done first
-      if (count > 0) wait(sh, &sh->o_done[stream], (count - 1) & 1, a.status);
+      if (own && count > 0) wait(sh, &sh->o_done[stream], (count - 1) & 1, a.status);
       wait(sh, &sh->full[ks % L::kSlots], (ks / L::kSlots) & 1, a.status);
-      if (!aborted(sh)) {
+      if (own && !aborted(sh)) {
         ptx::tc_fence_after();
-        const uint32_t k_addr = ring + (ks % L::kSlots) * L::kTile;
-#pragma unroll 4
-        for (int k = 0; k < DP / 16; ++k) {
-          const uint32_t at = (k / 4) * (kKeys * 128) + (k % 4) * 32;
-          ptx::tc_mma_smem(tm_s, ptx::smem_desc_swizzle128(q + at, 16, 1024),
-                           ptx::smem_desc_swizzle128(k_addr + at, 16, 1024), kQK, k > 0);
+        const uint64_t k_desc =
+            ptx::smem_desc_swizzle128(ring + (ks % L::kSlots) * L::kTile, 16, 1024);
+        if (ptx::elect_one()) {
+#pragma unroll
+          for (int k = 0; k < DP / 16; ++k) {
+            const uint64_t at = (k / 4) * (kKeys * 128 / 16) + (k % 4) * 2;
+            ptx::tc_mma_smem(tm_s, q_desc + at, k_desc + at, kQK, k > 0);
+          }
+          ptx::tc_commit(&sh->s_full[stream]);
+          ptx::tc_commit(&sh->empty[ks % L::kSlots]);
+          if (!pair) ptx::tc_commit(&sh->empty[ks % L::kSlots]);   // the other stream's share
         }
-        ptx::tc_commit(&sh->s_full[stream]);
-        ptx::tc_commit(&sh->empty[ks % L::kSlots]);
-        if (!pair) ptx::tc_commit(&sh->empty[ks % L::kSlots]);   // the other stream's share
+        __syncwarp();
       }
       wait(sh, &sh->full[vs % L::kSlots], (vs / L::kSlots) & 1, a.status);
+      if (!own) continue;
       wait(sh, &sh->p_full[stream], count & 1, a.status);
       if (!aborted(sh)) {
         ptx::tc_fence_after();
-        const uint32_t v_addr = ring + (vs % L::kSlots) * L::kTile;
-#pragma unroll 4
-        for (int k = 0; k < kKeys / 16; ++k)
-          ptx::tc_mma_tmem_a(tm_o, tm_s + 8 * k,
-                             ptx::smem_desc_swizzle128(v_addr + k * 2048, kKeys * 128, 1024), kPV,
-                             i >= step || k > 0);
-        ptx::tc_commit(&sh->o_done[stream]);
-        ptx::tc_commit(&sh->empty[vs % L::kSlots]);
-        if (!pair) ptx::tc_commit(&sh->empty[vs % L::kSlots]);
+        const uint64_t v_desc = ptx::smem_desc_swizzle128(
+            ring + (vs % L::kSlots) * L::kTile, kKeys * 128, 1024);
+        if (ptx::elect_one()) {
+#pragma unroll
+          for (int k = 0; k < kKeys / 16; ++k)
+            ptx::tc_mma_tmem_a(tm_o, tm_s + 8 * k, v_desc + k * (2048 / 16), kPV,
+                               i >= step || k > 0);
+          ptx::tc_commit(&sh->o_done[stream]);
+          ptx::tc_commit(&sh->empty[vs % L::kSlots]);
+          if (!pair) ptx::tc_commit(&sh->empty[vs % L::kSlots]);
+        }
+        __syncwarp();
       }
       ++count;
     }
     slot0 += 2 * n;
-    ptx::mbar_arrive(&sh->q_empty);
+    if (threadIdx.x % 32 == 0) ptx::mbar_arrive(&sh->q_empty);
   }
   if (count > 0) wait(sh, &sh->o_done[stream], (count - 1) & 1, a.status);
 }
@@ -766,7 +772,7 @@ __device__ __noinline__ void add_nonfinite(const AttendArgs& a, const uint32_t* 
   }
 }
 
-// Two fp32 lanes at once.
+// Two fp32 values at once.
 __device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
@@ -780,12 +786,6 @@ __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 // Raw scores to base-2 exponents.
 struct Score {
   float sl2;        // |scale| log2(e)
@@ -799,7 +799,7 @@ __device__ __forceinline__ float capped(const Score& sc, float raw) {
 
 // O of this row times `back`.
 template <int DP>
-__device__ __noinline__ void scale_row(uint32_t tm_o, float back) {
+__device__ __forceinline__ void scale_row(uint32_t tm_o, float back) {
 #pragma unroll 1
   for (int c = 0; c < DP / 32; ++c) {
     uint32_t v[32];
@@ -827,64 +827,48 @@ __device__ __forceinline__ float move_reference(float x_max, bool first, uint32_
   return m_new;
 }
 
-// One tile of one row: S in tensor memory becomes P, m and l move on.  All 128
-// keys are visible and scores are not capped.  WIDE holds the row's scores in
-// registers; else they are read twice, 64 at a time.
-template <bool F16, bool WIDE, int DP>
-__device__ __forceinline__ void softmax_tile(float sl2, uint32_t tm_s, uint32_t tm_o, bool first,
-                                             float* mref, float* l) {
-  constexpr int kHold = WIDE ? 4 : 2;            // blocks of 32 scores held
-  uint32_t v[kHold][32];
-  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-  for (int h = 0; h < 4; h += kHold) {
+// One tile of one row whose 128 keys are all visible, scores not capped, m
+// set: P over S, and l.  The weights go by m as it stands while the maximum is
+// taken beside them, so nothing waits for it; if it has outgrown m in any row of
+// the warp, S is still there and the tile is done again by softmax_tile_any
+// (false).  WIDE loads the next 32 scores while these are worked on.
+template <bool F16, bool WIDE>
+__device__ __forceinline__ bool softmax_tile(float sl2, uint32_t tm_s, float mref, float* l) {
+  constexpr float kShift = F16 ? 7.f : 0.f;
+  constexpr int kBuf = WIDE ? 2 : 1;
+  uint32_t v[kBuf][32], pk[4][16];
+  float mx[2] = {-INFINITY, -INFINITY}, sum[4] = {0.f, 0.f, 0.f, 0.f};
+  const uint64_t mul = pack_f32x2(sl2, sl2), neg = pack_f32x2(-mref, -mref);
+  ptx::tmem_ld32(tm_s, v[0]);
 #pragma unroll
-    for (int c = 0; c < kHold; ++c) ptx::tmem_ld32(tm_s + 32 * (h + c), v[c]);
+  for (int c = 0; c < 4; ++c) {
+    uint32_t (&x)[32] = v[c % kBuf];
+    ptx::tmem_wait_ld32(x);
+    if (WIDE && c < 3) ptx::tmem_ld32(tm_s + 32 * (c + 1), v[(c + 1) % kBuf]);
 #pragma unroll
-    for (int c = 0; c < kHold; ++c) ptx::tmem_wait_ld32(v[c]);
-#pragma unroll
-    for (int c = 0; c < kHold; ++c)
-#pragma unroll
-      for (int k = 0; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(v[c][k]));
-  }
-  const float raw_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-  const float x_max = raw_max == -INFINITY ? -INFINITY : raw_max * sl2;
-  *mref = move_reference<F16, DP>(x_max, first, tm_o, *mref, l);
-  const float sub = *mref == -INFINITY ? 0.f : *mref;
-  const uint64_t mul = pack_f32x2(sl2, sl2), neg = pack_f32x2(-sub, -sub);
-  uint64_t sum[2] = {0, 0};
-#pragma unroll 1
-  for (int h = 0; h < 4; h += kHold) {
-    if (!WIDE) {
-#pragma unroll
-      for (int c = 0; c < kHold; ++c) ptx::tmem_ld32(tm_s + 32 * (h + c), v[c]);
-#pragma unroll
-      for (int c = 0; c < kHold; ++c) ptx::tmem_wait_ld32(v[c]);
+    for (int k = 0; k < 16; ++k) {
+      const float r0 = __uint_as_float(x[2 * k]), r1 = __uint_as_float(x[2 * k + 1]);
+      mx[k & 1] = fmaxf(mx[k & 1], fmaxf(r0, r1));
+      float p0, p1;
+      unpack_f32x2(fma_f32x2(pack_f32x2(r0, r1), mul, neg), &p0, &p1);
+      p0 = ex2(p0);
+      p1 = ex2(p1);
+      sum[2 * k & 3] += p0;
+      sum[(2 * k + 1) & 3] += p1;
+      pk[c][k] = pack2<F16>(p0, p1);
     }
-#pragma unroll
-    for (int c = 0; c < kHold; ++c) {
-      uint32_t pk[16];
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        float p0, p1;
-        unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[c][2 * k]),
-                                          __uint_as_float(v[c][2 * k + 1])), mul, neg), &p0, &p1);
-        p0 = ex2(p0);
-        p1 = ex2(p1);
-        sum[k & 1] = add_f32x2(sum[k & 1], pack_f32x2(p0, p1));
-        pk[k] = pack2<F16>(p0, p1);
-      }
-      ptx::tmem_st16(tm_s + 16 * (h + c), pk);
-    }
+    if (!WIDE && c < 3) ptx::tmem_ld32(tm_s + 32 * (c + 1), v[0]);
   }
-  float a, b;
-  unpack_f32x2(add_f32x2(sum[0], sum[1]), &a, &b);
-  *l += a + b;
+  if (__any_sync(0xffffffffu, fmaxf(mx[0], mx[1]) * sl2 > mref + (kShift + 8.f))) return false;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) ptx::tmem_st16(tm_s + 16 * c, pk[c]);
+  *l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
   ptx::tmem_wait_st();
+  return true;
 }
 
-// The same for tiles with invisible keys (see: a bit a key) or capped scores,
-// 32 keys at a time.  Returns {m, l}.
+// Any tile of one row, also with invisible keys (see: a bit a key), capped
+// scores, or a maximum that moves m; 32 keys at a time.  Returns {m, l}.
 template <bool F16, int DP>
 __device__ __noinline__ float2 softmax_tile_any(Score sc, uint32_t tm_s, uint32_t tm_o, uint4 see,
                                                 bool first, float mref, float l) {
@@ -1013,16 +997,14 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
       if (warp_valid) {
         const int pos0 = (s.t0 + i) * kKeys;
         const bool masked = pos0 + kKeys > s.start;
-        const uint32_t own_o = tm_o + wg * 128;
-        const bool first = i < step;
-        if (!masked && sc.cap2 == 0.f) {
-          softmax_tile<F16, !E4M3, DP>(sc.sl2, tm_s, own_o, first, &mref, &l);
-        } else {
+        const bool plain = !masked && sc.cap2 == 0.f && i >= step &&
+                           !__any_sync(0xffffffffu, mref == -INFINITY);
+        if (!plain || !softmax_tile<F16, !E4M3>(sc.sl2, tm_s, mref, &l)) {
           const float2 r = softmax_tile_any<F16, DP>(
-              sc, tm_s, own_o,
+              sc, tm_s, tm_o + wg * 128,
               masked ? sees_128(mask_row, s.rows, node, pos0 - s.start)
                      : make_uint4(~0u, ~0u, ~0u, ~0u),
-              first, mref, l);
+              i < step, mref, l);
           mref = r.x;
           l = r.y;
         }
@@ -1232,8 +1214,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1)
     else produce16<F16, DP>(a, maps, smem, sh);
   } else {
     ptx::set_registers<R::kLaunchRegs, R::kMmaRegs>();
-    if (warp < R::kMmaWarp + 2 && threadIdx.x % 32 == 0)
-      issue<F16, DP>(a, smem, sh, warp - R::kMmaWarp);
+    if (warp < R::kMmaWarp + 2) issue<F16, DP>(a, smem, sh, warp - R::kMmaWarp);
   }
   __syncwarp();
   ptx::tc_fence_before();
