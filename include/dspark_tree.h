@@ -82,8 +82,10 @@ struct dspark_tree_config {
  * A paged cache: k and v are [n_pages, page_size, kv_heads, head_dim] of
  * `type` (the handle's type or DSPARK_TYPE_E4M3), head_dim contiguous, the
  * other strides free: {page, slot, head} in elements.  Base addresses and
- * strides are multiples of 16 bytes.  k_scale and v_scale, e4m3 only, are
- * bytes [n_pages, page_size, kv_heads] with strides of their own.
+ * strides are multiples of 16 bytes, those of pages and slots below 2^31
+ * bytes.  k_scale and v_scale, e4m3 only, are bytes [n_pages, page_size,
+ * kv_heads] with strides of their own.  NaN codes stand under byte 255 only,
+ * as dspark_tree_write leaves them.
  */
 struct dspark_tree_cache {
     void *k, *v;

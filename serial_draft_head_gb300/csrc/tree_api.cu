@@ -50,20 +50,21 @@ int make_cache(const dspark_tree* h, const dspark_tree_cache* c, CacheView* out)
   if (e4m3 && (!c->k_scale || !c->v_scale || h->cfg.head_dim % 16)) return DSPARK_EINVAL;
   if (c->n_pages < 1 || c->n_pages >= ((int64_t)1 << 31) || c->page_size < 1) return DSPARK_EINVAL;
   if (!aligned16(c->k) || !aligned16(c->v)) return DSPARK_EINVAL;
-  out->k = static_cast<uint8_t*>(c->k);
-  out->v = static_cast<uint8_t*>(c->v);
-  out->ks = e4m3 ? c->k_scale : nullptr;
-  out->vs = e4m3 ? c->v_scale : nullptr;
-  for (int i = 0; i < 3; ++i) {
-    if (!stride_ok(c->k_stride[i], es) || !stride_ok(c->v_stride[i], es)) return DSPARK_EINVAL;
-    out->kst[i] = c->k_stride[i] * es;
-    out->vst[i] = c->v_stride[i] * es;
-    out->ksst[i] = out->vsst[i] = 0;
-    if (e4m3) {
-      if (c->k_scale_stride[i] < 0 || c->v_scale_stride[i] < 0) return DSPARK_EINVAL;
-      out->ksst[i] = c->k_scale_stride[i];
-      out->vsst[i] = c->v_scale_stride[i];
+  for (int v = 0; v < 2; ++v) {
+    const int64_t* st = v ? c->v_stride : c->k_stride;
+    const int64_t* ss = v ? c->v_scale_stride : c->k_scale_stride;
+    for (int i = 0; i < 3; ++i) {
+      if (!stride_ok(st[i], es)) return DSPARK_EINVAL;
+      if (e4m3 && (ss[i] < 0 || ss[i] > ((int64_t)1 << 40))) return DSPARK_EINVAL;
+      // pages and slots lie within 2 GB strides (see Rows); heads may be further apart
+      if (i < 2 && (st[i] * es >= ((int64_t)1 << 31) || (e4m3 && ss[i] >= ((int64_t)1 << 31))))
+        return DSPARK_EINVAL;
     }
+    out->x[v] = {static_cast<uint8_t*>(v ? c->v : c->k), st[2] * es, (uint32_t)(st[0] * es),
+                 (uint32_t)(st[1] * es)};
+    out->scale[v] = {nullptr, 0, 0, 0};
+    if (e4m3)
+      out->scale[v] = {v ? c->v_scale : c->k_scale, ss[2], (uint32_t)ss[0], (uint32_t)ss[1]};
   }
   out->n_pages = c->n_pages;
   out->page = FastDiv::of(c->page_size);
@@ -86,11 +87,11 @@ void make_maps(const dspark_tree* h, const dspark_tree_cache* c, const CacheView
   const CUtensorMapDataType type = c->type == DSPARK_TYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                                : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   for (int i = 0; i < 2; ++i) {
-    const int64_t* st = i ? v.vst : v.kst;
-    const cuuint64_t strides[3] = {(cuuint64_t)st[1], (cuuint64_t)st[2], (cuuint64_t)st[0]};
+    const Rows& r = v.x[i];
+    const cuuint64_t strides[3] = {r.slot, (cuuint64_t)r.head, r.page};
     for (int d = 0; d < 3; ++d)
       if (strides[d] == 0 || strides[d] >= ((cuuint64_t)1 << 40)) return;
-    if (h->encode(i ? &m->v : &m->k, type, 4, i ? v.v : v.k, dims, strides, box, one,
+    if (h->encode(i ? &m->v : &m->k, type, 4, r.p, dims, strides, box, one,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
@@ -193,13 +194,13 @@ int dspark_tree_write(dspark_tree_t h, const dspark_tree_cache* cache,
   if (!k || !v || !k_stride || !v_stride || !aligned16(k) || !aligned16(v)) return DSPARK_EINVAL;
   for (int i = 0; i < 2; ++i)
     if (!stride_ok(k_stride[i], 2) || !stride_ok(v_stride[i], 2)) return DSPARK_EINVAL;
-  a.k = static_cast<const uint8_t*>(k);
-  a.v = static_cast<const uint8_t*>(v);
-  a.k_row = k_stride[0] * 2;
-  a.k_head = k_stride[1] * 2;
-  a.v_row = v_stride[0] * 2;
-  a.v_head = v_stride[1] * 2;
+  for (int i = 0; i < 2; ++i) {
+    a.src[i] = static_cast<const uint8_t*>(i ? v : k);
+    a.src_row[i] = (i ? v_stride : k_stride)[0] * 2;
+    a.src_head[i] = (i ? v_stride : k_stride)[1] * 2;
+  }
   a.Hkv = h->cfg.kv_heads;
+  a.kv2 = FastDiv::of(2 * a.Hkv);
   a.D = h->cfg.head_dim;
   a.status = h->status;
   return cuda_code(write_launch(a, h->cfg.type == DSPARK_TYPE_F16,
@@ -217,9 +218,10 @@ int dspark_tree_read(dspark_tree_t h, const dspark_tree_cache* cache,
   if (rc != DSPARK_OK) return rc;
   if (a.b.B == 0) return DSPARK_OK;
   if (!out_k || !out_v || !aligned16(out_k) || !aligned16(out_v)) return DSPARK_EINVAL;
-  a.out_k = static_cast<uint16_t*>(out_k);
-  a.out_v = static_cast<uint16_t*>(out_v);
+  a.out[0] = static_cast<uint16_t*>(out_k);
+  a.out[1] = static_cast<uint16_t*>(out_v);
   a.Hkv = h->cfg.kv_heads;
+  a.kv2 = FastDiv::of(2 * a.Hkv);
   a.D = h->cfg.head_dim;
   a.status = h->status;
   return cuda_code(read_launch(a, h->cfg.type == DSPARK_TYPE_F16,

@@ -81,6 +81,18 @@ struct Layout {
   static constexpr int kTail = kRing + kSlots * kTile;
 };
 
+// A place in the ring and the parity of its fills.
+template <int SLOTS>
+struct RingPos {
+  uint32_t slot = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == SLOTS) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+};
+
 struct Tail {
   uint64_t full[8], empty[8], q_full, q_empty, s_full[2], p_full[2], o_done[2];
   float2 ml[2][kKeys];
@@ -284,50 +296,6 @@ __device__ __forceinline__ bool zero_nonfinite(uint4* x) {
   return any;
 }
 
-// Four e4m3 codes (bytes 0 .. 3) times 2^(byte - 127) in the 16-bit type, exact
-// for the scales of `easy_scale`.  bf16: a code's seven low bits moved to bf16's
-// exponent and mantissa fields stand for |code| 2^-120, the sign bit is put on
-// after the product; the pairs come as bytes (0, 2) and (1, 3), which needs no
-// byte permutation, so elements 1 and 2 of every four change places: Q is laid
-// out the same way, and O's columns change back at the end.
-template <bool F16>
-__device__ __forceinline__ uint2 scale_codes(uint32_t w, uint32_t mul2) {
-  uint2 r;
-  if (F16) {
-    const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
-    const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
-    const __half2 m = *reinterpret_cast<const __half2*>(&mul2);
-    const __half2 x = __hmul2(__half2(lo), m), y = __hmul2(__half2(hi), m);
-    r.x = *reinterpret_cast<const uint32_t*>(&x);
-    r.y = *reinterpret_cast<const uint32_t*>(&y);
-  } else {
-    const uint32_t even = (w << 4) & 0x07f007f0u, odd = (w >> 4) & 0x07f007f0u;
-    const __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(&mul2);
-    const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&even), m);
-    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&odd), m);
-    r.x = *reinterpret_cast<const uint32_t*>(&x) ^ ((w << 8) & 0x80008000u);
-    r.y = *reinterpret_cast<const uint32_t*>(&y) ^ (w & 0x80008000u);
-  }
-  return r;
-}
-
-// The order above of four elements (two packed pairs).
-__device__ __forceinline__ uint2 swap_middle(uint2 x) {
-  return make_uint2(__byte_perm(x.x, x.y, 0x5410), __byte_perm(x.x, x.y, 0x7632));
-}
-
-// Scales whose product with any code is a finite number of the 16-bit type and
-// whose multiplier is one too: 2^(byte - 7) for bf16, 2^(byte - 127) for f16.
-template <bool F16>
-__device__ __forceinline__ bool easy_scale(uint32_t byte) {
-  return byte <= 134 && (!F16 || byte >= 113);
-}
-
-template <bool F16>
-__device__ __forceinline__ uint32_t scale_mul2(uint32_t byte) {
-  return F16 ? (byte - 112) * 0x04000400u : byte * 0x00800080u + 120u * 0x00800080u;
-}
-
 // Any other scale: through fp32, rounded and saturated as the cache reads back.
 template <bool F16>
 __device__ __noinline__ uint2 scale_codes_any(uint32_t w, uint32_t byte) {
@@ -421,18 +389,18 @@ __device__ __forceinline__ void produce16(const AttendArgs& a, const TileMaps& m
     page_next = __ldg(a.b.pages + (int64_t)c.b * a.b.pages_stride + a.c.page.div(pos));
   };
   fetch_page();
-  int n = 0;                                     // slots issued
-  uint32_t copied = 0;                           // bit i: slot n - 1 - i went by 16-byte copies
+  RingPos<L::kSlots> at;
+  uint32_t copied = 0;                           // bit i: the slot i + 1 before went by 16-byte copies
   // the V tile in flight: where it is and which of its positions are draft
   int prev_pos = 0, prev_start = 0, prev_total = 0, prev_seg = 0;
-  auto complete = [&](int slot, bool v) {        // slot's copies of this thread have landed
+  auto complete = [&](int back, bool v) {        // this thread's copies `back` slots ago have landed
+    const uint32_t slot = at.slot >= (uint32_t)back ? at.slot - back : at.slot + L::kSlots - back;
     if (v && prev_pos + kKeys > prev_start) {
 #pragma unroll 1
       for (int i = sub; i < 32; i += kSub) {
         const int row = warp * 32 + i, pos = prev_pos + row;
         if (pos < prev_start || pos >= prev_total) continue;
-        uint4* p = reinterpret_cast<uint4*>(ring + (slot % L::kSlots) * L::kTile +
-                                            tile_offset(row, chunk));
+        uint4* p = reinterpret_cast<uint4*>(ring + slot * L::kTile + tile_offset(row, chunk));
         uint4 x = *p;
         if (zero_nonfinite<F16>(&x)) {
           *p = x;
@@ -444,7 +412,7 @@ __device__ __forceinline__ void produce16(const AttendArgs& a, const TileMaps& m
     }
     ptx::fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(&sh->full[slot % L::kSlots]);
+    if (lane == 0) ptx::mbar_arrive(&sh->full[slot]);
   };
   while (c.more()) {
     const int head = c.head, start = c.start, total = c.total(), seg = c.seg;
@@ -461,10 +429,10 @@ __device__ __forceinline__ void produce16(const AttendArgs& a, const TileMaps& m
     const int my_slot = my_pos - a.c.page.div(my_pos) * a.c.page.d;
     if (my_pos >= total) page = -1;
 #pragma unroll 1
-    for (int v = 0; v < 2; ++v, ++n) {
-      uint64_t* full = &sh->full[n % L::kSlots];
-      uint8_t* dst = ring + (n % L::kSlots) * L::kTile;
-      wait(sh, &sh->empty[n % L::kSlots], ((n / L::kSlots) & 1) ^ 1, a.status);
+    for (int v = 0; v < 2; ++v) {
+      uint64_t* full = &sh->full[at.slot];
+      uint8_t* dst = ring + at.slot * L::kTile;
+      wait(sh, &sh->empty[at.slot], at.phase ^ 1, a.status);
       if (tiled) {
         if (lane == 0) {
           // after an abort no copy may outlive the CTA: none is started
@@ -480,24 +448,24 @@ __device__ __forceinline__ void produce16(const AttendArgs& a, const TileMaps& m
         }
         __syncwarp();
       } else {
-        const int64_t st0 = v ? a.c.vst[0] : a.c.kst[0], st1 = v ? a.c.vst[1] : a.c.kst[1];
-        const uint8_t* src = v ? a.c.v + head * a.c.vst[2] : a.c.k + head * a.c.kst[2];
-        src += chunk * 16;
+        const Rows rows = a.c.x[v];
+        const uint8_t* src = rows.of_head(head) + chunk * 16;
 #pragma unroll
         for (int i = 0; i < 32; i += kSub) {
           const int p = __shfl_sync(0xffffffffu, page, i + sub);
           const int s = __shfl_sync(0xffffffffu, my_slot, i + sub);
           const bool on = in_dim && p >= 0;
           ptx::cp_async16_or_zero(dst + tile_offset(warp * 32 + i + sub, chunk),
-                                  on ? src + p * st0 + s * st1 : a.c.k, on);
+                                  on ? src + rows.offset(p, s) : rows.p, on);
         }
       }
       ptx::cp_async_commit();
       if (copied >> (kLag - 1) & 1) {
         ptx::cp_async_wait_group<kLag>();
-        complete(n - kLag, v);
+        complete(kLag, v);
       }
       copied = copied << 1 | (tiled ? 0u : 1u);
+      at.next();
     }
     prev_pos = pos0;
     prev_start = start;
@@ -506,8 +474,8 @@ __device__ __forceinline__ void produce16(const AttendArgs& a, const TileMaps& m
   }
   ptx::cp_async_wait_group<0>();
   if (copied & 1) {
-    complete(n - 2, false);
-    complete(n - 1, true);
+    complete(2, false);
+    complete(1, true);
   }
 }
 
@@ -572,6 +540,7 @@ __device__ __forceinline__ void produce8(const AttendArgs& a, uint8_t* smem, Tai
       slot[i] = pos - at * a.c.page.d;
     }
   };
+  RingPos<L::kSlots> at;
   // rows of the same request kAhead tiles on, across a head's end
   auto ask = [&]() {
     int t = c.t + kAhead, head = c.head;
@@ -583,26 +552,23 @@ __device__ __forceinline__ void produce8(const AttendArgs& a, uint8_t* smem, Tai
     const int pos = min(t * kKeys + tid % kKeys, c.total() - 1), at = a.c.page.div(pos);
     const uint32_t p = (uint32_t)__ldg(a.b.pages + (int64_t)c.b * a.b.pages_stride + at);
     if (p >= (uint64_t)a.c.n_pages) return;
-    const int64_t s = pos - at * a.c.page.d;
-    ptx::prefetch_l2(tid >= kKeys
-                         ? a.c.v + p * a.c.vst[0] + s * a.c.vst[1] + head * a.c.vst[2]
-                         : a.c.k + p * a.c.kst[0] + s * a.c.kst[1] + head * a.c.kst[2]);
+    ptx::prefetch_l2(a.c.x[tid >= kKeys].at(p, pos - at * a.c.page.d, head));
   };
   uint4 x[kPasses], x_next[kPasses];
   uint32_t byte[kPasses], byte_next[kPasses];
   const uint32_t top_page = (uint32_t)(a.c.n_pages - 1);
   auto load = [&](bool v, int head) {
-    const uint8_t* src = (v ? a.c.v + head * a.c.vst[2] : a.c.k + head * a.c.kst[2]) +
-                         (in_dim ? chunk * 16 : 0);
-    const uint8_t* sc = v ? a.c.vs + head * a.c.vsst[2] : a.c.ks + head * a.c.ksst[2];
-    const int64_t st0 = v ? a.c.vst[0] : a.c.kst[0], st1 = v ? a.c.vst[1] : a.c.kst[1];
-    const int64_t ss0 = v ? a.c.vsst[0] : a.c.ksst[0], ss1 = v ? a.c.vsst[1] : a.c.ksst[1];
+    const Rows rows = a.c.x[v], scales = a.c.scale[v];
+    const uint8_t* src = rows.of_head(head) + (in_dim ? chunk * 16 : 0);
+    const uint8_t* sc = scales.of_head(head);
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-      const uint32_t p = min(page[i], top_page); // a bad page is reported at the end
-      worst = max(worst, page[i]);
-      x_next[i] = ptx::ldg_nc_na(src + p * st0 + slot[i] * st1);
-      byte_next[i] = __ldg(sc + p * ss0 + slot[i] * ss1);
+      if (!v) {                                  // a bad page is reported at the end
+        worst = max(worst, page[i]);
+        page[i] = min(page[i], top_page);
+      }
+      x_next[i] = ptx::ldg_nc_na(src + rows.offset(page[i], slot[i]));
+      byte_next[i] = __ldg(sc + scales.offset(page[i], slot[i]));
     }
   };
   fetch_pages();
@@ -610,8 +576,7 @@ __device__ __forceinline__ void produce8(const AttendArgs& a, uint8_t* smem, Tai
   load(false, cur.head);
   bool more = true;                              // another half tile after the one in x_next
 #pragma unroll 1
-  for (int n = 0; more; ++n) {
-    const bool v = n & 1;
+  for (bool v = false; more; v = !v, at.next()) {
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
       x[i] = x_next[i];
@@ -632,8 +597,8 @@ __device__ __forceinline__ void produce8(const AttendArgs& a, uint8_t* smem, Tai
         load(false, cur.head);
       }
     }
-    wait(sh, &sh->empty[n % L::kSlots], ((n / L::kSlots) & 1) ^ 1, a.status);
-    uint8_t* dst = ring + (n % L::kSlots) * L::kTile;
+    wait(sh, &sh->empty[at.slot], at.phase ^ 1, a.status);
+    uint8_t* dst = ring + at.slot * L::kTile;
     if (tile.rows < kKeys || a.D < DP) {         // rows and elements past the end are zeros
 #pragma unroll
       for (int i = 0; i < kPasses; ++i)
@@ -665,7 +630,7 @@ __device__ __forceinline__ void produce8(const AttendArgs& a, uint8_t* smem, Tai
     }
     ptx::fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(&sh->full[n % L::kSlots]);
+    if (lane == 0) ptx::mbar_arrive(&sh->full[at.slot]);
   }
   if (worst > top_page) set_status(a.status, DSPARK_EPAGES);
 }
@@ -685,7 +650,8 @@ __device__ __forceinline__ void issue(const AttendArgs& a, uint8_t* smem, Tail* 
   Walker w;
   Segment s;
   w.init(a, sh);
-  uint32_t slot0 = 0, count = 0;                 // the segment's first slot; own tiles so far
+  RingPos<L::kSlots> at;
+  uint32_t count = 0;                            // own tiles so far
   for (uint32_t seg = 0; w.next(a, &s); ++seg) {
     const bool pair = group_rows(a, s) > kKeys;
     const int n = s.t1 - s.t0, step = pair ? 1 : 2;
@@ -693,15 +659,14 @@ __device__ __forceinline__ void issue(const AttendArgs& a, uint8_t* smem, Tail* 
         ptx::smem_u32(smem) + (pair ? stream * L::kTile : 0), 16, 1024);
     wait(sh, &sh->q_full, seg & 1, a.status);
     for (int i = 0; i < n; ++i) {
-      const uint32_t ks = slot0 + 2 * i, vs = ks + 1;
       const bool own = pair || (i & 1) == stream;         // else the phases only pass
       // S and P share columns: the last product that reads P is done first
       if (own && count > 0) wait(sh, &sh->o_done[stream], (count - 1) & 1, a.status);
-      wait(sh, &sh->full[ks % L::kSlots], (ks / L::kSlots) & 1, a.status);
+      wait(sh, &sh->full[at.slot], at.phase, a.status);
       if (own && !aborted(sh)) {
         ptx::tc_fence_after();
         const uint64_t k_desc =
-            ptx::smem_desc_swizzle128(ring + (ks % L::kSlots) * L::kTile, 16, 1024);
+            ptx::smem_desc_swizzle128(ring + at.slot * L::kTile, 16, 1024);
         if (ptx::elect_one()) {
 #pragma unroll
           for (int k = 0; k < DP / 16; ++k) {
@@ -709,32 +674,34 @@ __device__ __forceinline__ void issue(const AttendArgs& a, uint8_t* smem, Tail* 
             ptx::tc_mma_smem(tm_s, q_desc + at, k_desc + at, kQK, k > 0);
           }
           ptx::tc_commit(&sh->s_full[stream]);
-          ptx::tc_commit(&sh->empty[ks % L::kSlots]);
-          if (!pair) ptx::tc_commit(&sh->empty[ks % L::kSlots]);   // the other stream's share
+          ptx::tc_commit(&sh->empty[at.slot]);
+          if (!pair) ptx::tc_commit(&sh->empty[at.slot]);          // the other stream's share
         }
         __syncwarp();
       }
-      wait(sh, &sh->full[vs % L::kSlots], (vs / L::kSlots) & 1, a.status);
+      at.next();
+      const uint32_t vs = at.slot;
+      wait(sh, &sh->full[vs], at.phase, a.status);
+      at.next();
       if (!own) continue;
       wait(sh, &sh->p_full[stream], count & 1, a.status);
       if (!aborted(sh)) {
         ptx::tc_fence_after();
         const uint64_t v_desc = ptx::smem_desc_swizzle128(
-            ring + (vs % L::kSlots) * L::kTile, kKeys * 128, 1024);
+            ring + vs * L::kTile, kKeys * 128, 1024);
         if (ptx::elect_one()) {
 #pragma unroll
           for (int k = 0; k < kKeys / 16; ++k)
             ptx::tc_mma_tmem_a(tm_o, tm_s + 8 * k, v_desc + k * (2048 / 16), kPV,
                                i >= step || k > 0);
           ptx::tc_commit(&sh->o_done[stream]);
-          ptx::tc_commit(&sh->empty[vs % L::kSlots]);
-          if (!pair) ptx::tc_commit(&sh->empty[vs % L::kSlots]);
+          ptx::tc_commit(&sh->empty[vs]);
+          if (!pair) ptx::tc_commit(&sh->empty[vs]);
         }
         __syncwarp();
       }
       ++count;
     }
-    slot0 += 2 * n;
     if (threadIdx.x % 32 == 0) ptx::mbar_arrive(&sh->q_empty);
   }
   if (count > 0) wait(sh, &sh->o_done[stream], (count - 1) & 1, a.status);
@@ -758,9 +725,9 @@ __device__ __noinline__ void add_nonfinite(const AttendArgs& a, const uint32_t* 
     int64_t page;
     int slot;
     if (!locate(a.c, a.b, b, start + j, &page, &slot)) continue;
-    const uint8_t* v = a.c.v + page * a.c.vst[0] + slot * a.c.vst[1] + head * a.c.vst[2];
+    const uint8_t* v = a.c.x[1].at((uint32_t)page, slot, head);
     float scale = 1.f;
-    if (E4M3) scale = scale_value(a.c.vs[page * a.c.vsst[0] + slot * a.c.vsst[1] + head * a.c.vsst[2]]);
+    if (E4M3) scale = scale_value(*a.c.scale[1].at((uint32_t)page, slot, head));
 #pragma unroll 1
     for (int d = d0; d < d1; ++d) {
       const float x = E4M3 ? saturate16<F16>(e4m3x2_to_float2(v[d]).x * scale)

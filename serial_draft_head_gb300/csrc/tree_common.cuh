@@ -16,31 +16,43 @@ namespace dspark {
 namespace tree {
 
 // n / d for 0 <= n < 2^31 by one multiplication: with L = ceil(log2 d) and
-// mul = ceil(2^(31+L) / d) < 2^32 + 1, floor(n * mul / 2^(31+L)) is exact.
+// mul = ceil(2^(31+L) / d) < 2^32, floor(n * mul / 2^(31+L)) is exact.
 struct FastDiv {
-  uint64_t mul;
-  int shift;
+  uint32_t mul;
+  int shift;                 // L
   int d;
   __host__ static FastDiv of(int d) {
     FastDiv f;
     int L = 0;
     while (((int64_t)1 << L) < d) ++L;
-    f.shift = 31 + L;
-    f.mul = (((uint64_t)1 << f.shift) + (uint64_t)d - 1) / (uint64_t)d;
+    f.shift = L;
+    f.mul = (uint32_t)((((uint64_t)1 << (31 + L)) + (uint64_t)d - 1) / (uint64_t)d);
     f.d = d;
     return f;
   }
   __device__ __forceinline__ int div(int n) const {
-    return (int)(((uint64_t)(uint32_t)n * mul) >> shift);
+    return (int)(__umulhi((uint32_t)n << 1, mul) >> shift);
   }
 };
 
-// The cache with strides in bytes.
+// Rows of one array of the cache, strides in bytes.  Those of pages and slots
+// are below 2^31, so an offset is two 32 x 32 -> 64 bit products.
+struct Rows {
+  uint8_t* p;
+  int64_t head;
+  uint32_t page, slot;
+  __device__ __forceinline__ uint8_t* of_head(int h) const { return p + h * head; }
+  __device__ __forceinline__ uint64_t offset(uint32_t pg, uint32_t sl) const {
+    return (uint64_t)pg * page + (uint64_t)sl * slot;
+  }
+  __device__ __forceinline__ uint8_t* at(uint32_t pg, uint32_t sl, int h) const {
+    return of_head(h) + offset(pg, sl);
+  }
+};
+
 struct CacheView {
-  uint8_t *k, *v;
-  uint8_t *ks, *vs;          // scale bytes, e4m3 only
-  int64_t kst[3], vst[3];    // page, slot, head
-  int64_t ksst[3], vsst[3];
+  Rows x[2];                 // K, V
+  Rows scale[2];             // their scale bytes, e4m3 only
   int64_t n_pages;
   FastDiv page;
 };
@@ -116,6 +128,50 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t codes) {
   return __half22float2(__half2(r));
 }
 
+// Four e4m3 codes (bytes 0 .. 3) times 2^(byte - 127) in the 16-bit type, exact
+// for the scales of `easy_scale`.  bf16: a code's seven low bits moved to bf16's
+// exponent and mantissa fields stand for |code| 2^-120, the sign bit is put on
+// after the product; the pairs come as bytes (0, 2) and (1, 3), which needs no
+// byte permutation, so elements 1 and 2 of every four change places (attend lays
+// Q out the same way, and O's columns change back at the end).
+template <bool F16>
+__device__ __forceinline__ uint2 scale_codes(uint32_t w, uint32_t mul2) {
+  uint2 r;
+  if (F16) {
+    const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
+    const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
+    const __half2 m = *reinterpret_cast<const __half2*>(&mul2);
+    const __half2 x = __hmul2(__half2(lo), m), y = __hmul2(__half2(hi), m);
+    r.x = *reinterpret_cast<const uint32_t*>(&x);
+    r.y = *reinterpret_cast<const uint32_t*>(&y);
+  } else {
+    const uint32_t even = (w << 4) & 0x07f007f0u, odd = (w >> 4) & 0x07f007f0u;
+    const __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(&mul2);
+    const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&even), m);
+    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&odd), m);
+    r.x = *reinterpret_cast<const uint32_t*>(&x) ^ ((w << 8) & 0x80008000u);
+    r.y = *reinterpret_cast<const uint32_t*>(&y) ^ (w & 0x80008000u);
+  }
+  return r;
+}
+
+// The order above of four elements (two packed pairs).
+__device__ __forceinline__ uint2 swap_middle(uint2 x) {
+  return make_uint2(__byte_perm(x.x, x.y, 0x5410), __byte_perm(x.x, x.y, 0x7632));
+}
+
+// Scales whose product with any code is a finite number of the 16-bit type and
+// whose multiplier is one too: 2^(byte - 7) for bf16, 2^(byte - 127) for f16.
+template <bool F16>
+__device__ __forceinline__ bool easy_scale(uint32_t byte) {
+  return byte <= 134 && (!F16 || byte >= 113);
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t scale_mul2(uint32_t byte) {
+  return F16 ? (byte - 112) * 0x04000400u : byte * 0x00800080u + 120u * 0x00800080u;
+}
+
 struct AttendArgs {
   CacheView c;
   BatchView b;
@@ -159,10 +215,11 @@ cudaError_t attend_launch(const AttendArgs& a, const TileMaps& maps, bool f16, b
 struct RowsArgs {
   CacheView c;
   BatchView b;
-  const uint8_t *k, *v;      // write: source rows
-  int64_t k_row, k_head, v_row, v_head;
-  uint16_t *out_k, *out_v;   // read: destination rows
+  const uint8_t* src[2];     // write: K and V rows
+  int64_t src_row[2], src_head[2];
+  uint16_t* out[2];          // read: destination rows
   int Hkv, D;
+  FastDiv kv2;               // by 2 Hkv, the cached rows of a token
   int* status;
 };
 
