@@ -148,14 +148,20 @@ int dspark_tree_create(const dspark_tree_config* cfg, dspark_tree_t* out) {
   h->device = dev;
   h->sm_count = sms;
   h->cfg = *cfg;
-  // two parts a CTA: the item it finishes for an earlier CTA, and the one it leaves to a later
+  // two parts a worker: the item it finishes for an earlier one, and the one it
+  // leaves to a later; as much as any of the kernels needs
   const int G = cfg->q_heads / cfg->kv_heads;
   const int64_t rows = (int64_t)cfg->max_nodes * G;
   h->part_rows = rows >= kGroupRows ? kGroupRows : (int)((rows + 31) / 32 * 32);
-  const size_t n = (size_t)2 * sms * h->part_rows;
-  const size_t o_bytes = n * padded_dim(cfg->head_dim) * sizeof(float);
-  const size_t ml_bytes = n * sizeof(float2);
-  e = cudaMalloc(&h->parts, o_bytes + ml_bytes + (size_t)2 * sms * sizeof(int4));
+  size_t n_parts = (size_t)2 * sms, n_rows = n_parts * h->part_rows;
+  for (int tiles = 1; tiles <= 2; ++tiles) {
+    const size_t n = (size_t)2 * few_workers(sms, tiles);
+    if (n > n_parts) n_parts = n;
+    if (n * 16 * tiles > n_rows) n_rows = n * 16 * tiles;
+  }
+  const size_t o_bytes = n_rows * padded_dim(cfg->head_dim) * sizeof(float);
+  const size_t ml_bytes = n_rows * sizeof(float2);
+  e = cudaMalloc(&h->parts, o_bytes + ml_bytes + n_parts * sizeof(int4));
   if (e == cudaSuccess) {
     uint8_t* p = static_cast<uint8_t*>(h->parts);
     h->part_o = reinterpret_cast<float*>(p);
@@ -173,6 +179,7 @@ int dspark_tree_create(const dspark_tree_config* cfg, dspark_tree_t* out) {
       h->encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   }
   if (e == cudaSuccess) e = attend_setup(cfg->type == DSPARK_TYPE_F16, cfg->head_dim);
+  if (e == cudaSuccess) e = few_setup(cfg->type == DSPARK_TYPE_F16, cfg->head_dim);
   if (e != cudaSuccess) {
     dspark_tree_destroy(h);
     return cuda_code(e);
@@ -290,6 +297,13 @@ int dspark_tree_attend(dspark_tree_t h, const dspark_tree_cache* cache,
   a.part_of = h->part_of;
   a.part_rows = h->part_rows;
   a.status = h->status;
+  // At most 32 rows a cached head on average: the kernel for few rows (any number
+  // of rows is right in either).
+  const int64_t rows = (int64_t)a.b.N * a.G;
+  if (rows <= (int64_t)32 * a.b.B)
+    return cuda_code(few_launch(a, rows <= (int64_t)16 * a.b.B ? 1 : 2,
+                                h->cfg.type == DSPARK_TYPE_F16, cache->type == DSPARK_TYPE_E4M3,
+                                static_cast<cudaStream_t>(stream)));
   TileMaps maps;
   make_maps(h, cache, a.c, &maps);
   return cuda_code(attend_launch(a, maps, h->cfg.type == DSPARK_TYPE_F16,

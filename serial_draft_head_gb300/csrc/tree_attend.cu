@@ -1,23 +1,7 @@
-// tree_attend.cu -- attention of drafted rows over a paged cache on tcgen05.
-//
-// Per cached head the rows that read it are (node, query head of the group):
-// T * G of them.  A work item is (request, cached head, up to 256 of its rows)
-// over all its keys, cut into tiles of 128 keys; a tile of one item is a unit.
-// The units of all items, in order, are split evenly over one CTA per SM: the
-// lengths are known on the device only, so every CTA sums them up itself.  An
-// item that lies inside one CTA's share is finished there; one that several
-// CTAs share leaves parts (unnormalised O, maximum, sum), joined by a second
-// kernel in a fixed order.
-//
-// Mathematics, per row, one pass over the tiles in the base-2 exponent:
-//   x_j = log2(e) * scale * q.k_j              (capped: log2(e) c tanh(s / c))
-//   p_j = 2^(x_j - m),  l = sum p_j,  O = sum p_j v_j
-// m follows the running maximum lazily: it moves, and O and l are rescaled,
-// only when the maximum has grown by more than 8, so p <= 2^8: O and l in fp32
-// keep their relative precision, and the read-modify-write of O is rare.  p is
-// rounded once to the 16-bit type for the second product (half a unit, as the
-// result itself is rounded); l sums the unrounded p.  For f16 m carries -7, so
-// that weights down to 2^-21 of the largest stay normal numbers.
+// tree_attend.cu -- attention of drafted rows over a paged cache on tcgen05, for
+// more than 32 rows a cached head (tree_attend_few.cu has the others).  Items
+// are 256 rows by tiles of 128 keys, a worker is a CTA, one a SM (tree_items.cuh
+// says how the work is cut, and the mathematics).
 //
 // Roles of the 18 warps: 8 softmax warps in two groups of 128 threads (thread =
 // row = tensor-memory lane), 8 producer warps, 2 MMA warps (one thread each).
@@ -38,10 +22,7 @@
 // Keys past the end are zero rows and masked; draft rows of V that are not
 // finite would reach every row of the product (0 * NaN), so such elements are
 // zeroed in the ring and noted, and added at the end to the rows that see them.
-#include <math.h>
-
-#include "tc_ptx.cuh"
-#include "tree_common.cuh"
+#include "tree_items.cuh"
 
 namespace dspark {
 namespace tree {
@@ -70,8 +51,10 @@ struct Roles {
 constexpr int kLag = 2;                 // slots a producer issues ahead of the one it completes
 constexpr int kBadSets = 8;             // segments the producers can be ahead, rounded up
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
+using Item = Work<kKeys, kGroupRows>;
+using Segment = Item::Segment;
+using Walker = Item::Walker;
+using Cursor = Item::Cursor;
 
 template <int DP>
 struct Layout {
@@ -97,9 +80,8 @@ struct Tail {
   uint64_t full[8], empty[8], q_full, q_empty, s_full[2], p_full[2], o_done[2];
   float2 ml[2][kKeys];
   uint32_t bad[kBadSets][DSPARK_TREE_MAX_NODES / 32];
-  int64_t unit0, units, total;           // this CTA's share, and all units
+  Share share;
   int64_t warp_sum[20];
-  int b0, head0, group0, t0;             // the share's first unit
   uint32_t tmem;
   int abort;
 };
@@ -138,223 +120,19 @@ __device__ __forceinline__ bool aborted(const Tail* s) {
   return *(const volatile int*)&s->abort != 0;
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ float rcp(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Rows of request b as attend takes them (0 if they do not fit), key tiles and
-// row groups.
-struct Request {
-  int row0, rows, start, tiles, groups;
-};
-
-__device__ __forceinline__ Request load_request(const AttendArgs& a, int b, bool* ok) {
-  Request r;
-  *ok = request_rows(a.b, b, &r.row0, &r.rows, &r.start) && r.rows <= a.max_nodes &&
-        (!a.mask || r.rows <= 32 * a.mask_words);
-  if (!*ok) r.rows = 0;
-  r.tiles = (r.start + r.rows + kKeys - 1) / kKeys;
-  r.groups = (r.rows * a.G + kGroupRows - 1) / kGroupRows;
-  return r;
-}
-
-__device__ __forceinline__ int64_t units_of(const AttendArgs& a, const Request& r) {
-  return r.rows == 0 ? 0 : (int64_t)r.tiles * r.groups * a.Hkv;
-}
-
-// First unit of CTA i's share of `total` units over n CTAs.
-__device__ __forceinline__ int64_t share(int64_t total, int n, int i) { return total * i / n; }
-
-// The CTA whose share holds unit u.
-__device__ __noinline__ int holder(int64_t total, int n_cta, int64_t u) {
-  const int n = (int)(total < n_cta ? total : n_cta);
-  int c = (int)(u * n / total);
-  while (share(total, n, c + 1) <= u) ++c;
-  while (share(total, n, c) > u) --c;
-  return c;
-}
-
-// One CTA's part of an item: key tiles t0 .. t1-1 of `tiles`.
-struct Segment {
-  int b, row0, rows, start, head, group, t0, t1, tiles;
-  int64_t item_end;                     // unit after the item's last
-};
-
-struct Walker {
-  Request r;
-  int b, head, group, t0;
-  int64_t left, unit;
-
-  __device__ void init(const AttendArgs& a, const Tail* s) {
-    left = s->units;
-    unit = s->unit0;
-    b = s->b0;
-    head = s->head0;
-    group = s->group0;
-    t0 = s->t0;
-    bool ok;
-    if (left > 0) r = load_request(a, b, &ok);
-  }
-
-  __device__ bool next(const AttendArgs& a, Segment* s) {
-    if (left <= 0) return false;
-    const int64_t rest = r.tiles - t0;
-    const int n = (int)(rest < left ? rest : left);
-    s->b = b;
-    s->row0 = r.row0;
-    s->rows = r.rows;
-    s->start = r.start;
-    s->head = head;
-    s->group = group;
-    s->t0 = t0;
-    s->t1 = t0 + n;
-    s->tiles = r.tiles;
-    s->item_end = unit + rest;
-    left -= n;
-    unit += n;
-    t0 += n;
-    if (t0 == r.tiles) {
-      t0 = 0;
-      if (++group == r.groups) {
-        group = 0;
-        if (++head == a.Hkv) {
-          head = 0;
-          bool ok;
-          if (left > 0) do {
-              r = load_request(a, ++b, &ok);
-            } while (r.rows == 0 && b + 1 < a.b.B);
-          if (r.rows == 0) left = 0;    // the arrays changed under the kernel
-        }
-      }
-    }
-    return true;
-  }
-};
-
-__device__ __forceinline__ int group_rows(const AttendArgs& a, const Segment& s) {
-  const int n = s.rows * a.G - s.group * kGroupRows;
-  return n < kGroupRows ? n : kGroupRows;
-}
-
-// Visibility of the 128 positions from draft position j0 on (negative:
-// context): a bit a position, for a node with this mask row (null: a chain) of
-// a request with `rows` of them.
+// Visibility of the 128 positions from draft position j0 on.
 __device__ __noinline__ uint4 sees_128(const uint32_t* mask_row, int rows, int node, int j0) {
-  auto word = [&](int w) {              // draft positions 32 w .. 32 w + 31
-    const int left = rows - 32 * w;
-    if (w < 0 || left <= 0) return 0u;
-    const int n = node + 1 - 32 * w;
-    const uint32_t m = mask_row ? __ldg(mask_row + w)
-                                : n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
-    return left >= 32 ? m : m & ((1u << left) - 1u);
-  };
-  uint32_t r[4];
-  const int sh = j0 & 31, w0 = j0 >> 5;          // floor: words w0 .. w0 + 4, shifted down by sh
-  uint32_t lo = w0 < 0 ? 0xffffffffu : word(w0);
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const uint32_t hi = w0 + c + 1 < 0 ? 0xffffffffu : word(w0 + c + 1);
-    r[c] = __funnelshift_r(lo, hi, sh);
-    lo = hi;
-  }
-  return make_uint4(r[0], r[1], r[2], r[3]);
+  return make_uint4(sees_32(mask_row, rows, node, j0), sees_32(mask_row, rows, node, j0 + 32),
+                    sees_32(mask_row, rows, node, j0 + 64), sees_32(mask_row, rows, node, j0 + 96));
 }
 
 // ------------------------------------------------------------- producers --
-
-template <bool F16>
-__device__ __forceinline__ bool nonfinite16(uint32_t x) {
-  constexpr uint32_t e = F16 ? 0x7c00u : 0x7f80u;
-  return (x & e) == e;
-}
-
-// Zeroes the non-finite elements of a 16-byte chunk; true if there were any.
-template <bool F16>
-__device__ __forceinline__ bool zero_nonfinite(uint4* x) {
-  uint32_t w[4] = {x->x, x->y, x->z, x->w};
-  bool any = false;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (nonfinite16<F16>(w[i])) {
-      w[i] &= 0xffff0000u;
-      any = true;
-    }
-    if (nonfinite16<F16>(w[i] >> 16)) {
-      w[i] &= 0x0000ffffu;
-      any = true;
-    }
-  }
-  if (any) *x = make_uint4(w[0], w[1], w[2], w[3]);
-  return any;
-}
-
-// Any other scale: through fp32, rounded and saturated as the cache reads back.
-template <bool F16>
-__device__ __noinline__ uint2 scale_codes_any(uint32_t w, uint32_t byte) {
-  const float s = scale_value(byte);
-  const float2 x = e4m3x2_to_float2(w & 0xffffu), y = e4m3x2_to_float2(w >> 16);
-  const uint2 r = make_uint2(
-      pack2<F16>(saturate16<F16>(x.x * s), saturate16<F16>(x.y * s)),
-      pack2<F16>(saturate16<F16>(y.x * s), saturate16<F16>(y.y * s)));
-  return F16 ? r : swap_middle(r);
-}
 
 // Byte offset of (row, 16-byte chunk) in a tile: 64-element blocks of 128 rows.
 __device__ __forceinline__ uint32_t tile_offset(int row, int chunk) {
   return (uint32_t)(chunk >> 3) * (kKeys * 128) + (uint32_t)row * 128 +
          (uint32_t)((chunk ^ row) & 7) * 16;
 }
-
-// The tiles of the CTA's share, in order.
-struct Cursor {
-  int b, head, group, t, seg;           // seg: segments begun before this one
-  int rows, start, tiles, groups;       // of the request
-  int64_t left;                         // tiles from this one on
-
-  __device__ void load(const AttendArgs& a) {
-    bool ok;
-    const Request r = load_request(a, b, &ok);
-    rows = r.rows;
-    start = r.start;
-    tiles = r.tiles;
-    groups = r.groups;
-  }
-  __device__ void init(const AttendArgs& a, const Tail* s) {
-    left = s->units;
-    b = s->b0;
-    head = s->head0;
-    group = s->group0;
-    t = s->t0;
-    seg = 0;
-    if (left > 0) load(a);
-  }
-  __device__ __forceinline__ bool more() const { return left > 0; }
-  __device__ __forceinline__ int total() const { return start + rows; }
-  __device__ void next(const AttendArgs& a) {
-    --left;
-    if (++t < tiles) return;
-    t = 0;
-    ++seg;
-    if (++group < groups) return;
-    group = 0;
-    if (++head < a.Hkv) return;
-    head = 0;
-    if (left <= 0) return;
-    do {
-      ++b;
-      load(a);
-    } while (rows == 0 && b + 1 < a.b.B);
-    if (rows == 0) left = 0;            // the arrays changed under the kernel
-  }
-};
 
 // 16-bit cache.  With a map (see make_maps for when), tiles of context go by
 // tiled copies, lane 0 of every warp issuing its share of the boxes; tiles that
@@ -377,7 +155,7 @@ __device__ __forceinline__ void produce16(const AttendArgs& a, const TileMaps& m
   const int boxes = pieces * (DP / 64);          // of a tile; warp w issues w, w + 4, ...
   uint8_t* ring = smem + L::kRing;
   Cursor c;
-  c.init(a, sh);
+  c.init(a, sh->share);
   if (!c.more()) return;
   // the page of this lane's row (tiled: of the warp's box) of the tile at the cursor
   int page_next = 0;
@@ -520,7 +298,7 @@ __device__ __forceinline__ void produce8(const AttendArgs& a, uint8_t* smem, Tai
   const uint32_t to0 = tile_offset(r0, 2 * chunk), to1 = tile_offset(r0, 2 * chunk + 1);
   uint8_t* ring = smem + L::kRing;
   Cursor c;                                      // the tile after the one in `page`
-  c.init(a, sh);
+  c.init(a, sh->share);
   if (!c.more()) return;
   struct Tile {
     int head, rows, draft, seg;                  // rows that exist; the first of the draft
@@ -649,11 +427,11 @@ __device__ __forceinline__ void issue(const AttendArgs& a, uint8_t* smem, Tail* 
   const uint32_t ring = ptx::smem_u32(smem + L::kRing);
   Walker w;
   Segment s;
-  w.init(a, sh);
+  w.init(a, sh->share);
   RingPos<L::kSlots> at;
   uint32_t count = 0;                            // own tiles so far
   for (uint32_t seg = 0; w.next(a, &s); ++seg) {
-    const bool pair = group_rows(a, s) > kKeys;
+    const bool pair = Item::group_rows(a, s) > kKeys;
     const int n = s.t1 - s.t0, step = pair ? 1 : 2;
     const uint64_t q_desc = ptx::smem_desc_swizzle128(
         ptx::smem_u32(smem) + (pair ? stream * L::kTile : 0), 16, 1024);
@@ -709,10 +487,10 @@ __device__ __forceinline__ void issue(const AttendArgs& a, uint8_t* smem, Tail* 
 
 // --------------------------------------------------------------- softmax --
 
-// Adds the non-finite elements of the draft rows of V that a row sees to its
-// result, which the calling thread has just written (columns d0 .. d1 - 1): what
-// 0 < p times them comes to.  The result: 16-bit values (out), or the part's
-// fp32 ones (column d at part[(d / 4) * stride + d % 4]).
+// Adds to a row's result, which the calling thread has just written (columns d0
+// .. d1 - 1), the non-finite elements of the draft rows of V that it sees: what
+// 0 < p times them comes to.  The result: 16-bit values (out), or the part's fp32
+// ones (column d at part[(d / 4) * stride + d % 4]).
 template <bool F16, bool E4M3>
 __device__ __noinline__ void add_nonfinite(const AttendArgs& a, const uint32_t* bad,
                                            const uint32_t* mask_row, int b, int rows, int start,
@@ -720,18 +498,10 @@ __device__ __noinline__ void add_nonfinite(const AttendArgs& a, const uint32_t* 
                                            float* part, int64_t stride) {
 #pragma unroll 1
   for (int j = 0; j < rows; ++j) {
-    const bool see = mask_row ? mask_row[j >> 5] >> (j & 31) & 1 : j <= node;
-    if (!see || !(bad[j >> 5] >> (j & 31) & 1)) continue;
-    int64_t page;
-    int slot;
-    if (!locate(a.c, a.b, b, start + j, &page, &slot)) continue;
-    const uint8_t* v = a.c.x[1].at((uint32_t)page, slot, head);
-    float scale = 1.f;
-    if (E4M3) scale = scale_value(*a.c.scale[1].at((uint32_t)page, slot, head));
+    if (!(sees_word(mask_row, rows, node, j >> 5) & bad[j >> 5] & (1u << (j & 31)))) continue;
 #pragma unroll 1
     for (int d = d0; d < d1; ++d) {
-      const float x = E4M3 ? saturate16<F16>(e4m3x2_to_float2(v[d]).x * scale)
-                           : to_float<F16>(reinterpret_cast<const uint16_t*>(v)[d]);
+      const float x = bad_value<F16, E4M3>(a, b, start + j, head, d);
       if (isfinite(x)) continue;
       if (out) out[d] = (uint16_t)pack2<F16>(to_float<F16>(out[d]) + x, 0.f);
       else part[(d >> 2) * stride + (d & 3)] += x;
@@ -753,17 +523,6 @@ __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-// Raw scores to base-2 exponents.
-struct Score {
-  float sl2;        // |scale| log2(e)
-  float cap2;       // softcap log2(e), 0 without a cap
-  float cap_in;     // 2 sl2 / softcap: tanh(y) = 1 - 2 / (2^(2 y log2(e)) + 1)
-};
-
-__device__ __forceinline__ float capped(const Score& sc, float raw) {
-  return sc.cap2 - 2.f * sc.cap2 * rcp(ex2(raw * sc.cap_in) + 1.f);
-}
-
 // O of this row times `back`.
 template <int DP>
 __device__ __forceinline__ void scale_row(uint32_t tm_o, float back) {
@@ -894,17 +653,14 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
   const uint32_t lanes = (uint32_t)(warp * 32) << 16;
   const uint32_t tm_s = sh->tmem + lanes + wg * 128;
   const uint32_t tm_o = sh->tmem + lanes + 256;
-  Score sc;
-  sc.sl2 = fabsf(a.scale) * kLog2e;
-  sc.cap2 = a.softcap * kLog2e;
-  sc.cap_in = a.softcap > 0.f ? 2.f * sc.sl2 / a.softcap : 0.f;
+  const Score sc = Score::of(a);
   const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
   Walker w;
   Segment s;
-  w.init(a, sh);
+  w.init(a, sh->share);
   uint32_t count = 0;                            // tiles of this stream so far
   for (uint32_t seg = 0; w.next(a, &s); ++seg) {
-    const int rows = group_rows(a, s);
+    const int rows = Item::group_rows(a, s);
     const bool pair = rows > kKeys;
     const int n = s.t1 - s.t0;
     // Q into shared memory, all 256 threads, when both MMA threads are past the last
@@ -997,7 +753,7 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
       w1 = n1 > 0 ? ex2(x1.x - sub) : 0.f;
       l = w0 * x0.y + (n1 > 0 ? w1 * x1.y : 0.f);
     }
-    const bool whole = s.t0 == 0 && s.t1 == s.tiles;
+    const bool whole = s.whole();
     const int part = 2 * blockIdx.x + (s.t0 == 0 ? 1 : 0);
     const uint32_t* bad = sh->bad[seg % kBadSets];
     uint32_t any_bad = 0;
@@ -1062,75 +818,12 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
         else if (a.lse) a.lse[out_row] = l == 0.f ? -INFINITY : (mref + log2f(l)) * kLn2;
       }
     }
-    if (!whole && threadIdx.x == 0) {
-      // the CTAs that share the item: from the one with its first unit to that with its last
-      const int first = holder(sh->total, a.n_cta, s.item_end - s.tiles);
-      const int last = holder(sh->total, a.n_cta, s.item_end - 1);
-      a.part_of[part] = make_int4(s.b, (int)((uint32_t)s.head << 16 | s.group), first,
-                                   last - first + 1);
-    }
+    if (!whole && threadIdx.x == 0)
+      a.part_of[part] = Item::part_of(s, sh->share.total, a.n_cta);
     ptx::tc_fence_before();
     asm volatile("bar.sync 1, 256;" ::: "memory");
     if (any_bad != 0 && threadIdx.x < DSPARK_TREE_MAX_NODES / 32)
       sh->bad[seg % kBadSets][threadIdx.x] = 0;
-  }
-}
-
-// This CTA's share of the units: sums the requests' units in order.
-template <int kThreads>
-__device__ __forceinline__ void plan(const AttendArgs& a, Tail* sh) {
-  constexpr int kPer = (DSPARK_TREE_MAX_REQUESTS + 511) / 512;
-  int64_t mine[kPer], sum = 0;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int per = (a.b.B + 511) / 512;
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const int b = threadIdx.x * per + k;
-    mine[k] = 0;
-    if (k < per && threadIdx.x < 512 && b < a.b.B) {
-      bool ok;
-      mine[k] = units_of(a, load_request(a, b, &ok));
-      if (!ok && blockIdx.x == 0) set_status(a.status, DSPARK_EPAGES);
-    }
-    sum += mine[k];
-  }
-  int64_t incl = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) sh->warp_sum[warp] = incl;
-  __syncthreads();
-  int64_t before = incl - sum, total = 0;
-#pragma unroll
-  for (int k = 0; k < kThreads / 32; ++k) {
-    const int64_t y = sh->warp_sum[k];
-    if (k < warp) before += y;
-    total += y;
-  }
-  const int n = (int)(total < a.n_cta ? total : a.n_cta);
-  const int cta = blockIdx.x;
-  const int64_t u0 = cta < n ? share(total, n, cta) : total;
-  const int64_t u1 = cta < n ? share(total, n, cta + 1) : total;
-  if (threadIdx.x == 0) {
-    sh->unit0 = u0;
-    sh->units = u1 - u0;
-    sh->total = total;
-  }
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    if (u1 > u0 && u0 >= before && u0 < before + mine[k]) {
-      const int b = threadIdx.x * per + k;
-      bool ok;
-      const Request r = load_request(a, b, &ok);
-      const int64_t item = (u0 - before) / r.tiles;
-      sh->b0 = b;
-      sh->t0 = (int)(u0 - before - item * r.tiles);
-      sh->head0 = (int)(item / r.groups);
-      sh->group0 = (int)(item % r.groups);
-    }
-    before += mine[k];
   }
 }
 
@@ -1168,7 +861,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1)
   }
   for (int i = threadIdx.x; i < kBadSets * (DSPARK_TREE_MAX_NODES / 32); i += R::kThreads)
     (&sh->bad[0][0])[i] = 0;
-  plan<R::kThreads>(a, sh);
+  Item::plan<R::kThreads, 1>(a, blockIdx.x, 1, a.n_cta, &sh->share, sh->warp_sum);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -1208,11 +901,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   __shared__ float2 part_ml[8][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 of = a.part_of[blockIdx.x];
-  const int parts = of.w;
+  const int parts = of.w >> 16, first = of.w & 0xffff, head = of.y, group = of.z;
   if (parts == 0) return;
   bool ok;
-  const Request r = load_request(a, of.x, &ok);
-  const int head = (int)((uint32_t)of.y >> 16), group = of.y & 0xffff, first = of.z;
+  const Item::Request r = Item::load_request(a, of.x, &ok);
   const int rows = min(kGroupRows, r.rows * a.G - group * kGroupRows);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int pieces = (rows + 31) / 32 * (DP / 16);

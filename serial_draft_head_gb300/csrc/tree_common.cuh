@@ -191,7 +191,7 @@ struct AttendArgs {
   // part_rows rows: O (fp32, [D / 4][part_rows][4]) and {m, l} a row
   float* part_o;
   float2* part_ml;
-  int4* part_of;             // per part: {request, head << 16 | row group, first CTA, parts}
+  int4* part_of;             // per part: {request, head, row group, first worker | parts << 16}
   int part_rows;
   int* status;
 };
@@ -206,6 +206,12 @@ struct TileMaps {
   CUtensorMap k, v;
   int rows;
 };
+
+// attend_few: at most 32 rows a cached head, on mma.sync (tree_attend_few.cu).
+// Its workers are warps; `tiles` is 1 or 2 row tiles of 16.
+int few_workers(int n_cta, int tiles);
+cudaError_t few_setup(bool f16, int D);
+cudaError_t few_launch(const AttendArgs& a, int tiles, bool f16, bool e4m3, cudaStream_t stream);
 
 cudaError_t attend_setup(bool f16, int D);
 cudaError_t attend_launch(const AttendArgs& a, const TileMaps& maps, bool f16, bool e4m3,

@@ -1,0 +1,366 @@
+// tree_items.cuh -- how both attention kernels cut their work, and the parts of
+// the softmax they share.
+//
+// Per cached head the rows that read it are (node, query head of the group):
+// T * G of them.  A work item is (request, cached head, up to ROWS of its rows)
+// over all its keys, cut into tiles of KEYS keys; a tile of one item is a unit.
+// The units of all items, in order, are split evenly over the workers (CTAs or
+// warps): the lengths are known on the device only, so every CTA sums them up
+// itself.  An item that lies inside one worker's share is finished there; one
+// that several workers share leaves parts (unnormalised O, maximum, sum), joined
+// by a second kernel in the order of the keys.
+//
+// Mathematics, per row, one pass over the tiles in the base-2 exponent:
+//   x_j = log2(e) * scale * q.k_j              (capped: log2(e) c tanh(s / c))
+//   p_j = 2^(x_j - m),  l = sum p_j,  O = sum p_j v_j
+// m follows the running maximum lazily: it moves, and O and l are rescaled,
+// only when the maximum has grown by more than 8, so p <= 2^8: O and l in fp32
+// keep their relative precision, and the rescaling of O is rare.  p is rounded
+// once to the 16-bit type for the second product (half a unit, as the result
+// itself is rounded); l sums the unrounded p.  For f16 m carries -7, so that
+// weights down to 2^-21 of the largest stay normal numbers.
+#pragma once
+
+#include <math.h>
+
+#include "tc_ptx.cuh"
+#include "tree_common.cuh"
+
+namespace dspark {
+namespace tree {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Raw scores to base-2 exponents.
+struct Score {
+  float sl2;        // |scale| log2(e): a negative scale turns Q's signs
+  float cap2;       // softcap log2(e), 0 without a cap
+  float cap_in;     // 2 sl2 / softcap: tanh(y) = 1 - 2 / (2^(2 y log2(e)) + 1)
+
+  __device__ static Score of(const AttendArgs& a) {
+    Score s;
+    s.sl2 = fabsf(a.scale) * kLog2e;
+    s.cap2 = a.softcap * kLog2e;
+    s.cap_in = a.softcap > 0.f ? 2.f * s.sl2 / a.softcap : 0.f;
+    return s;
+  }
+};
+
+__device__ __forceinline__ float capped(const Score& sc, float raw) {
+  return sc.cap2 - 2.f * sc.cap2 * rcp(ex2(raw * sc.cap_in) + 1.f);
+}
+
+// First unit of worker i's share of `total` units over n workers.
+__device__ __forceinline__ int64_t share_start(int64_t total, int n, int i) { return total * i / n; }
+
+// The worker whose share holds unit u.
+static __device__ __noinline__ int holder(int64_t total, int workers, int64_t u) {
+  const int n = (int)(total < workers ? total : workers);
+  int c = (int)(u * n / total);
+  while (share_start(total, n, c + 1) <= u) ++c;
+  while (share_start(total, n, c) > u) --c;
+  return c;
+}
+
+// A worker's share: its units, all units, and the place of its first.
+struct Share {
+  int64_t unit0, units, total;
+  int b0, head0, group0, t0;
+};
+
+template <int KEYS, int ROWS>
+struct Work {
+  // Rows of request b as attend takes them (0 if they do not fit), key tiles and
+  // row groups.
+  struct Request {
+    int row0, rows, start, tiles, groups;
+  };
+
+  __device__ static __forceinline__ Request load_request(const AttendArgs& a, int b, bool* ok) {
+    Request r;
+    *ok = request_rows(a.b, b, &r.row0, &r.rows, &r.start) && r.rows <= a.max_nodes &&
+          (!a.mask || r.rows <= 32 * a.mask_words);
+    if (!*ok) r.rows = 0;
+    r.tiles = (int)(((int64_t)r.start + r.rows + KEYS - 1) / KEYS);
+    r.groups = (r.rows * a.G + ROWS - 1) / ROWS;
+    return r;
+  }
+
+  // The shares of workers worker0 + i * stride, i < COUNT, of `workers`, by all
+  // THREADS threads of the CTA: sums the requests' units in order.
+  template <int THREADS, int COUNT>
+  __device__ static __forceinline__ void plan(const AttendArgs& a, int worker0, int stride,
+                                              int workers, Share* shares, int64_t* warp_sum) {
+    constexpr int kPer = (DSPARK_TREE_MAX_REQUESTS + THREADS - 1) / THREADS;
+    int64_t mine[kPer], sum = 0;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int per = (a.b.B + THREADS - 1) / THREADS;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int b = threadIdx.x * per + k;
+      mine[k] = 0;
+      if (k < per && b < a.b.B) {
+        bool ok;
+        const Request r = load_request(a, b, &ok);
+        if (ok && r.rows > 0) mine[k] = (int64_t)r.tiles * r.groups * a.Hkv;
+        if (!ok && blockIdx.x == 0) set_status(a.status, DSPARK_EPAGES);
+      }
+      sum += mine[k];
+    }
+    int64_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int64_t before = incl - sum, total = 0;
+#pragma unroll
+    for (int k = 0; k < THREADS / 32; ++k) {
+      const int64_t y = warp_sum[k];
+      if (k < warp) before += y;
+      total += y;
+    }
+    const int n = (int)(total < workers ? total : workers);
+    if ((int)threadIdx.x < COUNT) {
+      const int w = worker0 + threadIdx.x * stride;
+      const int64_t u0 = w < n ? share_start(total, n, w) : total;
+      shares[threadIdx.x].unit0 = u0;
+      shares[threadIdx.x].units = (w < n ? share_start(total, n, w + 1) : total) - u0;
+      shares[threadIdx.x].total = total;
+    }
+    // the thread whose requests hold a share's first unit writes its place
+    for (int i = 0; i < COUNT; ++i) {
+      const int w = worker0 + i * stride;
+      if (w >= n) break;
+      const int64_t u0 = share_start(total, n, w);
+      if (u0 < before || u0 >= before + sum) continue;
+      int64_t at = before;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        if (u0 >= at && u0 < at + mine[k]) {
+          const int b = threadIdx.x * per + k;
+          bool ok;
+          const Request r = load_request(a, b, &ok);
+          const int64_t item = (u0 - at) / r.tiles;
+          shares[i].b0 = b;
+          shares[i].t0 = (int)(u0 - at - item * r.tiles);
+          shares[i].head0 = (int)(item / r.groups);
+          shares[i].group0 = (int)(item % r.groups);
+        }
+        at += mine[k];
+      }
+    }
+    __syncthreads();
+  }
+
+  // One worker's part of an item: key tiles t0 .. t1-1 of `tiles`.
+  struct Segment {
+    int b, row0, rows, start, head, group, t0, t1, tiles;
+    int64_t item_end;                   // unit after the item's last
+    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
+  };
+
+  struct Walker {
+    Request r;
+    int b, head, group, t0;
+    int64_t left, unit;
+
+    __device__ void init(const AttendArgs& a, const Share& s) {
+      left = s.units;
+      unit = s.unit0;
+      b = s.b0;
+      head = s.head0;
+      group = s.group0;
+      t0 = s.t0;
+      bool ok;
+      if (left > 0) r = load_request(a, b, &ok);
+    }
+
+    __device__ bool next(const AttendArgs& a, Segment* s) {
+      if (left <= 0) return false;
+      const int64_t rest = r.tiles - t0;
+      const int n = (int)(rest < left ? rest : left);
+      s->b = b;
+      s->row0 = r.row0;
+      s->rows = r.rows;
+      s->start = r.start;
+      s->head = head;
+      s->group = group;
+      s->t0 = t0;
+      s->t1 = t0 + n;
+      s->tiles = r.tiles;
+      s->item_end = unit + rest;
+      left -= n;
+      unit += n;
+      t0 += n;
+      if (t0 == r.tiles) {
+        t0 = 0;
+        if (++group == r.groups) {
+          group = 0;
+          if (++head == a.Hkv) {
+            head = 0;
+            bool ok;
+            if (left > 0) do {
+                r = load_request(a, ++b, &ok);
+              } while (r.rows == 0 && b + 1 < a.b.B);
+            if (r.rows == 0) left = 0;  // the arrays changed under the kernel
+          }
+        }
+      }
+      return true;
+    }
+  };
+
+  // The tiles of a share, in order.
+  struct Cursor {
+    int b, head, group, t, seg;         // seg: segments begun before this one
+    int rows, start, tiles, groups;     // of the request
+    int64_t left;                       // tiles from this one on
+
+    __device__ void load(const AttendArgs& a) {
+      bool ok;
+      const Request r = load_request(a, b, &ok);
+      rows = r.rows;
+      start = r.start;
+      tiles = r.tiles;
+      groups = r.groups;
+    }
+    __device__ void init(const AttendArgs& a, const Share& s) {
+      left = s.units;
+      b = s.b0;
+      head = s.head0;
+      group = s.group0;
+      t = s.t0;
+      seg = 0;
+      if (left > 0) load(a);
+    }
+    __device__ __forceinline__ bool more() const { return left > 0; }
+    __device__ __forceinline__ int total() const { return start + rows; }
+    __device__ void next(const AttendArgs& a) {
+      --left;
+      if (++t < tiles) return;
+      t = 0;
+      ++seg;
+      if (++group < groups) return;
+      group = 0;
+      if (++head < a.Hkv) return;
+      head = 0;
+      if (left <= 0) return;
+      do {
+        ++b;
+        load(a);
+      } while (rows == 0 && b + 1 < a.b.B);
+      if (rows == 0) left = 0;          // the arrays changed under the kernel
+    }
+  };
+
+  __device__ static __forceinline__ int group_rows(const AttendArgs& a, const Segment& s) {
+    const int n = s.rows * a.G - s.group * ROWS;
+    return n < ROWS ? n : ROWS;
+  }
+
+  // What the join needs of a part: the workers that share the item, from the one
+  // with its first unit to that with its last.
+  __device__ static __forceinline__ int4 part_of(const Segment& s, int64_t total, int workers) {
+    const int first = holder(total, workers, s.item_end - s.tiles);
+    const int last = holder(total, workers, s.item_end - 1);
+    return make_int4(s.b, s.head, s.group, first | (last - first + 1) << 16);
+  }
+};
+
+// Draft positions 32 w .. 32 w + 31 that a node sees: its mask row (null: a
+// chain) of a request with `rows` nodes.
+__device__ __forceinline__ uint32_t sees_word(const uint32_t* mask_row, int rows, int node,
+                                              int w) {
+  const int left = rows - 32 * w;
+  if (w < 0 || left <= 0) return 0u;
+  const int n = node + 1 - 32 * w;
+  const uint32_t m = mask_row ? __ldg(mask_row + w)
+                              : n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+  return left >= 32 ? m : m & ((1u << left) - 1u);
+}
+
+// Visibility of the 32 positions from draft position j0 on (negative: context).
+static __device__ __noinline__ uint32_t sees_32(const uint32_t* mask_row, int rows, int node, int j0) {
+  const int w = j0 >> 5;                         // floor
+  const uint32_t lo = w < 0 ? 0xffffffffu : sees_word(mask_row, rows, node, w);
+  const uint32_t hi = w + 1 < 0 ? 0xffffffffu : sees_word(mask_row, rows, node, w + 1);
+  return __funnelshift_r(lo, hi, j0 & 31);
+}
+
+template <bool F16>
+__device__ __forceinline__ bool nonfinite16(uint32_t x) {
+  constexpr uint32_t e = F16 ? 0x7c00u : 0x7f80u;
+  return (x & e) == e;
+}
+
+// Zeroes the non-finite elements of two packed ones; true if there were any.
+template <bool F16>
+__device__ __forceinline__ bool zero_nonfinite(uint32_t* w) {
+  bool any = false;
+  if (nonfinite16<F16>(*w)) {
+    *w &= 0xffff0000u;
+    any = true;
+  }
+  if (nonfinite16<F16>(*w >> 16)) {
+    *w &= 0x0000ffffu;
+    any = true;
+  }
+  return any;
+}
+
+template <bool F16>
+__device__ __forceinline__ bool zero_nonfinite(uint4* x) {
+  bool any = zero_nonfinite<F16>(&x->x);
+  any |= zero_nonfinite<F16>(&x->y);
+  any |= zero_nonfinite<F16>(&x->z);
+  any |= zero_nonfinite<F16>(&x->w);
+  return any;
+}
+
+// Four codes times any scale: through fp32, rounded and saturated as the cache
+// reads back, in the order of scale_codes.
+template <bool F16>
+static __device__ __noinline__ uint2 scale_codes_any(uint32_t w, uint32_t byte) {
+  const float s = scale_value(byte);
+  const float2 x = e4m3x2_to_float2(w & 0xffffu), y = e4m3x2_to_float2(w >> 16);
+  const uint2 r = make_uint2(
+      pack2<F16>(saturate16<F16>(x.x * s), saturate16<F16>(x.y * s)),
+      pack2<F16>(saturate16<F16>(y.x * s), saturate16<F16>(y.y * s)));
+  return F16 ? r : swap_middle(r);
+}
+
+// Draft rows of V that are not finite would reach every row of the product
+// (0 * NaN): their elements enter it as zeros, are noted (bad: a bit a node), and
+// added here to the results that see them, which the calling thread has just
+// written (columns d0 .. d1 - 1): what 0 < p times them comes to.  The result:
+// 16-bit values (out), or a part's fp32 ones (column d at part[index(d)], stride
+// and step given).
+template <bool F16, bool E4M3>
+__device__ __forceinline__ float bad_value(const AttendArgs& a, int b, int pos, int head, int d) {
+  int64_t page;
+  int slot;
+  if (!locate(a.c, a.b, b, pos, &page, &slot)) return 0.f;
+  const uint8_t* v = a.c.x[1].at((uint32_t)page, slot, head);
+  if (!E4M3) return to_float<F16>(reinterpret_cast<const uint16_t*>(v)[d]);
+  return saturate16<F16>(e4m3x2_to_float2(v[d]).x *
+                         scale_value(*a.c.scale[1].at((uint32_t)page, slot, head)));
+}
+
+}  // namespace tree
+}  // namespace dspark
