@@ -153,12 +153,7 @@ int dspark_tree_create(const dspark_tree_config* cfg, dspark_tree_t* out) {
   const int G = cfg->q_heads / cfg->kv_heads;
   const int64_t rows = (int64_t)cfg->max_nodes * G;
   h->part_rows = rows >= kGroupRows ? kGroupRows : (int)((rows + 31) / 32 * 32);
-  size_t n_parts = (size_t)2 * sms, n_rows = n_parts * h->part_rows;
-  for (int tiles = 1; tiles <= 2; ++tiles) {
-    const size_t n = (size_t)2 * few_workers(sms, tiles);
-    if (n > n_parts) n_parts = n;
-    if (n * 16 * tiles > n_rows) n_rows = n * 16 * tiles;
-  }
+  const size_t n_parts = (size_t)2 * sms, n_rows = n_parts * h->part_rows;
   const size_t o_bytes = n_rows * padded_dim(cfg->head_dim) * sizeof(float);
   const size_t ml_bytes = n_rows * sizeof(float2);
   e = cudaMalloc(&h->parts, o_bytes + ml_bytes + n_parts * sizeof(int4));

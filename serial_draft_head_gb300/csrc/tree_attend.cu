@@ -51,7 +51,8 @@ struct Roles {
 constexpr int kLag = 2;                 // slots a producer issues ahead of the one it completes
 constexpr int kBadSets = 8;             // segments the producers can be ahead, rounded up
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
-using Item = Work<kKeys, kGroupRows>;
+// An item's Q, result and way into the loop take as long as about three tiles.
+using Item = Work<kKeys, kGroupRows, 3>;
 using Segment = Item::Segment;
 using Walker = Item::Walker;
 using Cursor = Item::Cursor;

@@ -1,18 +1,19 @@
 // tree_attend_few.cu -- attention of few drafted rows (at most 32 a cached head:
 // single tokens, short chains) over a paged cache.
 //
-// A worker is a warp, alone with its items (16 or 32 rows by blocks of 16 keys;
-// tree_items.cuh says how the work is cut, and the mathematics): no barriers,
-// nothing handed between warps.  With so few rows K and V are used once from
-// where they land, and the memory rate bounds the kernel; tcgen05 tiles of 128
-// rows would be mostly padding, and what they need round them (rings, barriers,
-// tensor memory) cost more than the products.  So the products are mma.sync
-// m16n8k16, fed from registers:
+// Items are 16 or 32 rows by blocks of 16 keys, a worker is a CTA (tree_items.cuh
+// says how the work is cut, and the mathematics).  The warps of a CTA take a
+// segment's blocks in turn, each with its own O, m and l, and meet at its end.
+// With so few rows K and V are used once from where they land, and the memory
+// rate bounds the kernel; tcgen05 tiles of 128 rows would be mostly padding, and
+// what they need round them (a ring handed between warps, barriers, tensor
+// memory) cost more than the products.  So the products are mma.sync m16n8k16,
+// fed from registers:
 //
 //  - S = Q K^T: lane (g, q) = (lane / 4, lane % 4) holds B of key g and four
 //    elements of it a step.  The order of the elements along the head is free as
 //    long as Q has the same: lane q takes 16-byte chunks q, q + 4, ... of the row
-//    as they lie, and Q's A operand is loaded by the same chunks.
+//    as they lie, and Q's A operand is laid out by the same chunks.
 //  - O = P V: P's A operand is S's accumulator, packed.  B of lane (g, q) is keys
 //    2q, 2q + 1, 2q + 8, 2q + 9 at column g of every 8-column tile; the columns'
 //    order is free too, so lane g takes 16-byte chunks g (and g + 8) of the four
@@ -20,8 +21,14 @@
 //
 // So every thread reads just the 16-byte chunks that it copied itself: the ring
 // in shared memory (cp.async, a stage is 16 keys of K and V) needs no barrier,
-// only the thread's own wait.  e4m3 codes are converted in registers, the scale
-// multiplied in (exact in bf16).
+// only the thread's own wait.
+//
+// e4m3: the products are f16, which holds every code, one conversion for two
+// codes.  K's scale goes on the scores (fp32).  V's goes into the codes: exact in
+// f16 for scales 2^-14 .. 2^7; blocks with others take the second product in the
+// handle's type, code times scale as the cache reads back.  bf16 rows of Q are
+// brought to f16 by a power of two a row (exact for elements down to 2^-32 of the
+// row's largest, below that to 2^-40 of it).
 #include "tree_items.cuh"
 
 namespace dspark {
@@ -29,27 +36,36 @@ namespace tree {
 namespace {
 
 constexpr int kBlock = 16;              // keys of a block, and of a ring stage
+constexpr int kExtra = 14;              // blocks that an item's other work takes as long as
 
 template <bool E4M3, int DP, int MT>
 struct Few {
   static constexpr int kRows = 16 * MT;
-  // as many warps as hold their O, Q and S in registers
-  static constexpr int kWarps = MT == 1 ? 12 : 8;
+  // as many warps as hold their O and S in registers and their ring in shared memory
+  static constexpr int kWarps = MT == 2 ? 8 : E4M3 ? 12 : 10;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kBytes = DP * (E4M3 ? 1 : 2);     // of a cached row
   static constexpr int kKCopies = kBytes / 64;           // 16-byte chunks a lane, of a row of K
   static constexpr int kVBytes = kBytes / 8;             // bytes a lane, of a row of V
   static constexpr int kStage = 2 * kBlock * kBytes;
   static constexpr int kVPart = kBlock * kBytes;         // V's place in a stage
-  static constexpr int kStages = 16384 / kStage < 6 ? 16384 / kStage : 6;
-  static constexpr int kRing = kStages * kStage;
-  static constexpr int kQ = MT == 1 ? 0 : kRows * DP * 2;        // two row tiles: Q in shared memory
-  static constexpr int kScales = kRing + kQ;             // [stage][K 16, V 16]
-  static constexpr int kBad = kScales + kStages * 32;
-  static constexpr int kWarpBytes = kBad + DSPARK_TREE_MAX_NODES / 8;
-  static constexpr int kShares = kWarps * kWarpBytes;
-  static constexpr int kSums = kShares + kWarps * (int)sizeof(Share);
-  static constexpr int kSmem = kSums + kWarps * 8;
+  static constexpr int kStages = kStage == 8192 ? 2 : 3;
+  static constexpr int kTiles = DP / 8;                  // column tiles of O, per row tile
+  static constexpr int kMerge = MT * kTiles / 2;         // accumulator tiles merged at a time
+  static constexpr int kRing = kStages * kStage;         // of a warp
+  static constexpr int kQ = kWarps * kRing;              // Q, then the result: [rows][DP] 16-bit
+  static constexpr int kBuf = kQ + kRows * DP * 2;       // [warp][kMerge][lane] float4
+  static constexpr int kScales = kBuf + kWarps * kMerge * 512;   // [warp][stage][K 16, V 16]
+  static constexpr int kSmem = kScales + kWarps * kStages * 32;
+};
+
+struct FewState {
+  float2 ml[16][32];                    // [warp][row]
+  float row_mul[32];                    // a row's factor on the raw scores
+  uint32_t bad[DSPARK_TREE_MAX_NODES / 32];
+  int64_t sums[16];
+  Share share;
+  int live;                             // there is a segment
 };
 
 // Column d of the result: its place in the accumulators, n = 2 q + e and tile.
@@ -82,11 +98,12 @@ __device__ __noinline__ uint4 pair_codes_any(uint32_t wa, uint32_t byte_a, uint3
                     __byte_perm(x.y, y.y, 0x5410), __byte_perm(x.y, y.y, 0x7632));
 }
 
-// Two codes of two keys (half 0 or 1 of words wa, wb), as two pairs of keys.
-template <bool F16>
-__device__ __forceinline__ uint2 pair_codes(uint32_t wa, uint32_t wb, int half, uint32_t mul2) {
-  const uint32_t sel = F16 ? (half ? 0x7362 : 0x5140) : (half ? 0x7632 : 0x5410);
-  return scale_codes<F16>(__byte_perm(wa, wb, sel), mul2);
+// Four codes as f16.
+__device__ __forceinline__ uint2 codes_f16(uint32_t w) {
+  const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
+  const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
+  const __half2 x(lo), y(hi);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
 }
 
 // Adds to a row's result, written by this warp, the non-finite elements of the
@@ -114,38 +131,101 @@ __device__ __noinline__ void add_nonfinite(const AttendArgs& a, const uint32_t* 
   }
 }
 
+// The blocks of one warp in order: of every segment those t0 + warp, t0 + warp +
+// warps, ...
+template <class Item>
+struct BlockCursor {
+  int b, head, group, t, end;           // end: of the segment
+  int rows, start, tiles, groups;
+  int64_t after;                        // units of the share after this segment
+  bool more;
+
+  __device__ void load(const AttendArgs& a) {
+    bool ok;
+    const typename Item::Request r = Item::load_request(a, b, &ok);
+    rows = r.rows;
+    start = r.start;
+    tiles = r.tiles;
+    groups = r.groups;
+  }
+  __device__ void settle(const AttendArgs& a, int warp) {     // past the ends of segments
+    while (t >= end) {
+      if (after <= kExtra) {            // no more tiles in the share
+        more = false;
+        return;
+      }
+      if (++group == groups) {
+        group = 0;
+        if (++head == a.Hkv) {
+          head = 0;
+          do {
+            if (++b >= a.b.B) {         // the arrays changed under the kernel
+              more = false;
+              return;
+            }
+            load(a);
+          } while (rows == 0);
+        }
+      }
+      after -= kExtra;
+      end = (int)(after < tiles ? after : tiles);
+      after -= end;
+      t = warp;
+    }
+  }
+  __device__ void init(const AttendArgs& a, const Share& s, int warp) {
+    more = s.units > 0;
+    if (!more) return;
+    b = s.b0;
+    head = s.head0;
+    group = s.group0;
+    load(a);
+    const int64_t rest = tiles - s.t0;
+    const int n = (int)(rest < s.units ? rest : s.units);
+    end = s.t0 + n;                     // below 0: the share ends before the tiles
+    t = max(s.t0, 0) + warp;
+    after = s.units - n;
+    settle(a, warp);
+  }
+  __device__ void next(const AttendArgs& a, int warp, int warps) {
+    t += warps;
+    if (t >= end) settle(a, warp);
+  }
+};
+
 template <bool F16, bool E4M3, int DP, int MT>
 __global__ void __launch_bounds__(Few<E4M3, DP, MT>::kThreads, 1)
     few_kernel(const __grid_constant__ AttendArgs a) {
   using L = Few<E4M3, DP, MT>;
-  using Item = Work<kBlock, L::kRows>;
-  constexpr int kTiles = DP / 8;                 // column tiles of O
+  using Item = Work<kBlock, L::kRows, kExtra>;
+  constexpr bool kHalf = F16 || E4M3;            // the products' type is f16
+  constexpr int kTiles = L::kTiles;
   constexpr int kQChunks = DP / 32;              // 16-byte chunks of a row of Q a lane
-  constexpr float kShift = F16 ? 7.f : 0.f;
+  constexpr float kShift = kHalf ? 7.f : 0.f;
   extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ FewState st;
+  __shared__ typename Item::Walker walker;
+  __shared__ typename Item::Segment s;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane >> 2, q = lane & 3;
-  uint8_t* ring = smem + warp * L::kWarpBytes;
-  uint4* q_mem = reinterpret_cast<uint4*>(ring + L::kRing);
-  uint8_t* scales = ring + L::kScales;
-  uint32_t* bad = reinterpret_cast<uint32_t*>(ring + L::kBad);
-  Share* shares = reinterpret_cast<Share*>(smem + L::kShares);
+  uint8_t* ring = smem + warp * L::kRing;
+  uint4* q_mem = reinterpret_cast<uint4*>(smem + L::kQ);
+  uint8_t* scales = smem + L::kScales + warp * L::kStages * 32;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int worker = warp * a.n_cta + blockIdx.x, workers = a.n_cta * L::kWarps;
-  if (lane < 2) a.part_of[2 * worker + lane] = make_int4(0, 0, 0, 0);
-  if (lane < DSPARK_TREE_MAX_NODES / 32) bad[lane] = 0;
-  Item::template plan<L::kThreads, L::kWarps>(a, blockIdx.x, a.n_cta, workers, shares,
-                                              reinterpret_cast<int64_t*>(smem + L::kSums));
-  const Share& share = shares[warp];
+  if (threadIdx.x < 2) a.part_of[2 * blockIdx.x + threadIdx.x] = make_int4(0, 0, 0, 0);
+  if (threadIdx.x < DSPARK_TREE_MAX_NODES / 32) st.bad[threadIdx.x] = 0;
+  Item::template plan<L::kThreads, 1>(a, blockIdx.x, 1, a.n_cta, &st.share, st.sums);
 
-  // ---- the copies' side: blocks in order, kStages - 1 ahead of the products
-  typename Item::Cursor c;
-  c.init(a, share);
+  // ---- the copies' side: the warp's blocks in order, kStages - 1 ahead of the products
+  BlockCursor<Item> c;
+  c.init(a, st.share, warp);
   const uint32_t top_page = (uint32_t)(a.c.n_pages - 1);
-  uint32_t page = 0, worst = 0;                  // lane % 16: the page of its key of the next block
+  const bool even = a.c.page.d % kBlock == 0;    // a block lies in one page
+  uint32_t page = 0, worst = 0;                  // of the next block: its page, or that of key lane % 16
   auto look = [&]() {
-    if (!c.more()) return;
-    const int pos = min(c.t * kBlock + lane % 16, c.total() - 1);
-    page = (uint32_t)__ldg(a.b.pages + (int64_t)c.b * a.b.pages_stride + a.c.page.div(pos));
+    if (!c.more) return;
+    const int pos = c.t * kBlock + (even ? 0 : lane % 16);
+    page = (uint32_t)__ldg(a.b.pages + (int64_t)c.b * a.b.pages_stride +
+                           a.c.page.div(min(pos, c.start + c.rows - 1)));
   };
   look();
   int stage_in = 0, scale_stage = -1;
@@ -154,27 +234,33 @@ __global__ void __launch_bounds__(Few<E4M3, DP, MT>::kThreads, 1)
     // the scales of the block before have landed: lanes 0 .. 15 K's, 16 .. 31 V's
     if (E4M3 && scale_stage >= 0) scales[scale_stage * 32 + lane] = (uint8_t)scale_byte;
     scale_stage = -1;
-    if (c.more()) {
-      const int pos0 = c.t * kBlock, total = c.total(), head = c.head;
-      const int pos = min(pos0 + lane % 16, total - 1);
-      const int slot = pos - a.c.page.div(pos) * a.c.page.d;
+    if (c.more) {
+      const int pos0 = c.t * kBlock, total = c.start + c.rows, head = c.head;
+      const bool full = pos0 + kBlock <= total;
       worst = max(worst, page);                  // a bad page is reported at the end
       const uint32_t pg = min(page, top_page);
+      const int pos = even ? pos0 : min(pos0 + lane % 16, total - 1);
+      const int slot = pos - a.c.page.div(pos) * a.c.page.d;   // of the block, or of key lane % 16
       if (E4M3) {
-        scale_byte = __ldg(a.c.scale[lane / 16].at(pg, slot, head));
+        scale_byte = __ldg(a.c.scale[lane / 16].at(pg, even ? slot + lane % 16 : slot, head));
         scale_stage = stage_in;
       }
-      c.next(a);
+      c.next(a, warp, L::kWarps);
       look();
       uint8_t* dst = ring + stage_in * L::kStage + lane * 16;
       const Rows& kr = a.c.x[0];
       const uint8_t* k = kr.of_head(head) + q * 16;
+      if (even) k += kr.offset(pg, slot + g);
 #pragma unroll
       for (int kg = 0; kg < 2; ++kg) {
-        const uint32_t p = __shfl_sync(0xffffffffu, pg, g + 8 * kg);
-        const int s = __shfl_sync(0xffffffffu, slot, g + 8 * kg);
-        const uint8_t* src = k + kr.offset(p, s);
-        const bool on = pos0 + g + 8 * kg < total;
+        const uint8_t* src;
+        if (even) {
+          src = k + (uint64_t)(8 * kg) * kr.slot;
+        } else {
+          const uint32_t p = __shfl_sync(0xffffffffu, pg, g + 8 * kg);
+          src = k + kr.offset(p, __shfl_sync(0xffffffffu, slot, g + 8 * kg));
+        }
+        const bool on = full || pos0 + g + 8 * kg < total;
 #pragma unroll
         for (int i = 0; i < L::kKCopies; ++i)
           ptx::cp_async16_or_zero(dst + (kg * L::kKCopies + i) * 512, src + i * 64,
@@ -182,13 +268,18 @@ __global__ void __launch_bounds__(Few<E4M3, DP, MT>::kThreads, 1)
       }
       const Rows& vr = a.c.x[1];
       const uint8_t* v = vr.of_head(head) + g * (L::kVBytes < 16 ? 8 : 16);
+      if (even) v += vr.offset(pg, slot + 2 * q);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
-        const int key = 2 * q + (kk & 1) + 8 * (kk >> 1);
-        const uint32_t p = __shfl_sync(0xffffffffu, pg, key);
-        const int s = __shfl_sync(0xffffffffu, slot, key);
-        const uint8_t* src = v + vr.offset(p, s);
-        const bool on = pos0 + key < total;
+        const int off = (kk & 1) + 8 * (kk >> 1), key = 2 * q + off;
+        const uint8_t* src;
+        if (even) {
+          src = v + (uint64_t)off * vr.slot;
+        } else {
+          const uint32_t p = __shfl_sync(0xffffffffu, pg, key);
+          src = v + vr.offset(p, __shfl_sync(0xffffffffu, slot, key));
+        }
+        const bool on = full || pos0 + key < total;
         if (L::kVBytes < 16) {                   // e4m3, 64 elements: 8 codes a lane
           ptx::cp_async8_or_zero(ring + stage_in * L::kStage + L::kVPart + (kk * 32 + lane) * 8,
                                  src, on && g * 8 < a.D);
@@ -209,60 +300,82 @@ __global__ void __launch_bounds__(Few<E4M3, DP, MT>::kThreads, 1)
 
   // ---- the products' side
   const Score sc = Score::of(a);
+  const bool cap = sc.cap2 > 0.f;
   const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
-  typename Item::Walker w;
-  typename Item::Segment s;
-  w.init(a, share);
+  if (threadIdx.x == 0) {
+    walker.init(a, st.share);
+    st.live = walker.next(a, &s);
+  }
+  __syncthreads();
   int stage = 0;
-  while (w.next(a, &s)) {
+  while (st.live) {
     const int rows = Item::group_rows(a, s);
-    int node[MT][2];
-    int64_t out_row[MT][2];
-    bool valid[MT][2];
-    uint4 qf[MT == 1 ? 2 : 1][MT == 1 ? kQChunks : 1];
+    // Q: a warp for every eight rows, lane (g, q) the chunks that meet its K
+    if (warp < 2 * MT) {
+      const int row = 8 * warp + g;
+      const int grow = s.group * L::kRows + (row < rows ? row : 0), nd = a.group.div(grow);
+      const uint8_t* src = a.q + (int64_t)(s.row0 + nd) * a.q_row +
+                           (int64_t)(s.head * a.G + grow - nd * a.G) * a.q_head;
+      uint4 x[kQChunks];
+      uint32_t big = 0;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+      for (int j = 0; j < kQChunks; ++j) {
+        const int chunk = E4M3 ? 8 * (j / 2) + 2 * q + j % 2 : 4 * j + q;
+        x[j] = make_uint4(0, 0, 0, 0);
+        if (row < rows && chunk * 8 < a.D) x[j] = __ldg(reinterpret_cast<const uint4*>(src) + chunk);
+        if (E4M3 && !F16) {
+          const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = 16 * mt + 8 * h + g;
-        valid[mt][h] = row < rows;
-        const int grow = s.group * L::kRows + (valid[mt][h] ? row : 0);
-        node[mt][h] = a.group.div(grow);
-        const int qh = s.head * a.G + grow - node[mt][h] * a.G;
-        out_row[mt][h] = (int64_t)(s.row0 + node[mt][h]) * a.Hq + qh;
-        const uint8_t* src = a.q + (int64_t)(s.row0 + node[mt][h]) * a.q_row + qh * a.q_head;
+          for (int k = 0; k < 4; ++k)
+            big = max(big, max((w[k] & 0x7fffu) << 16, w[k] & 0x7fff0000u));
+        }
+        x[j].x ^= flip;
+        x[j].y ^= flip;
+        x[j].z ^= flip;
+        x[j].w ^= flip;
+      }
+      float row_mul = cap ? 1.f : sc.sl2;
+      if (E4M3 && !F16) {
+        // the row's largest magnitude to [2^14, 2^15): r a power of two, exact
+        big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        const int e = (int)(big >> 23);
+        const int up = big == 0 || e == 255 ? 0 : min(127 + 14 - e, 126);
+        const float r = __uint_as_float((uint32_t)(127 + up) << 23);
+        const float down = __uint_as_float((uint32_t)(127 - up) << 23);
+        row_mul *= down;
 #pragma unroll
         for (int j = 0; j < kQChunks; ++j) {
-          // the chunk of 8 elements that meets this lane's j-th half chunk of codes, or chunk, of K
-          const int chunk = E4M3 ? 8 * (j / 2) + 2 * q + j % 2 : 4 * j + q;
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (valid[mt][h] && chunk * 8 < a.D) x = __ldg(reinterpret_cast<const uint4*>(src) + chunk);
-          x.x ^= flip;
-          x.y ^= flip;
-          x.z ^= flip;
-          x.w ^= flip;
-          if (E4M3 && !F16) {
-            const uint2 lo = swap_middle(make_uint2(x.x, x.y)), hi = swap_middle(make_uint2(x.z, x.w));
-            x = make_uint4(lo.x, lo.y, hi.x, hi.y);
-          }
-          if (MT == 1) qf[h][j] = x;
-          else q_mem[((mt * 2 + h) * kQChunks + j) * 32 + lane] = x;
+          uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            w[k] = pack2<true>(to_float<false>((uint16_t)w[k]) * r,
+                               to_float<false>((uint16_t)(w[k] >> 16)) * r);
+          x[j] = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
-    float o[MT][kTiles][4], mref[MT][2], l[MT][2];
+      if (q == 0) st.row_mul[row] = row_mul;
+#pragma unroll
+      for (int j = 0; j < kQChunks; ++j) q_mem[(warp * kQChunks + j) * 32 + lane] = x[j];
+    }
+    __syncthreads();
+    float o[MT][kTiles][4], mref[MT][2], l[MT][2], row_mul[MT][2];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      mref[mt][0] = mref[mt][1] = -INFINITY;
-      l[mt][0] = l[mt][1] = 0.f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        mref[mt][h] = -INFINITY;
+        l[mt][h] = 0.f;
+        row_mul[mt][h] = st.row_mul[16 * mt + 8 * h + g];
+      }
 #pragma unroll
       for (int t = 0; t < kTiles; ++t)
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[mt][t][k] = 0.f;
     }
-    bool any_bad = false;
-
+    const int t1 = s.t1, start = s.start;
 #pragma unroll 1
-    for (int t = s.t0; t < s.t1; ++t) {
+    for (int t = s.t0 + warp; t < t1; t += L::kWarps) {
       issue();
       ptx::cp_async_wait_group<L::kStages - 1>();
       __syncwarp();
@@ -272,22 +385,7 @@ __global__ void __launch_bounds__(Few<E4M3, DP, MT>::kThreads, 1)
                              lane * (L::kVBytes < 16 ? 8 : 16);
       if (++stage == L::kStages) stage = 0;
       const int pos0 = t * kBlock;
-      const bool masked = pos0 + kBlock > s.start;
-      uint32_t kb[2], vb[4];                     // scale bytes of this lane's keys
-      bool easy = true;
-      if (E4M3) {
-        kb[0] = sb[g];
-        kb[1] = sb[g + 8];
-        const uint32_t v01 = *reinterpret_cast<const uint16_t*>(sb + 16 + 2 * q);
-        const uint32_t v23 = *reinterpret_cast<const uint16_t*>(sb + 24 + 2 * q);
-        vb[0] = v01 & 0xff;
-        vb[1] = v01 >> 8;
-        vb[2] = v23 & 0xff;
-        vb[3] = v23 >> 8;
-        easy = __all_sync(0xffffffffu, easy_scale<F16>(kb[0]) && easy_scale<F16>(kb[1]) &&
-                                           easy_scale<F16>(vb[0]) && easy_scale<F16>(vb[1]) &&
-                                           easy_scale<F16>(vb[2]) && easy_scale<F16>(vb[3]));
-      }
+      const bool masked = pos0 + kBlock > start;
       // S: a lane's rows g and g + 8, keys 2q, 2q + 1 of both groups of eight
       float x[MT][2][4];
 #pragma unroll
@@ -304,40 +402,41 @@ __global__ void __launch_bounds__(Few<E4M3, DP, MT>::kThreads, 1)
           kc[kg] = *reinterpret_cast<const uint4*>(src + (kg * L::kKCopies + i) * 512);
 #pragma unroll
         for (int hc = 0; hc < (E4M3 ? 2 : 1); ++hc) {      // a chunk of Q: two steps
-          uint4 qa[MT], qb[MT];
+          uint2 b0[2], b1[2];                              // B of the two steps
+#pragma unroll
+          for (int kg = 0; kg < 2; ++kg) {
+            if (E4M3) {
+              b0[kg] = codes_f16(hc ? kc[kg].z : kc[kg].x);
+              b1[kg] = codes_f16(hc ? kc[kg].w : kc[kg].y);
+            } else {
+              b0[kg] = make_uint2(kc[kg].x, kc[kg].y);
+              b1[kg] = make_uint2(kc[kg].z, kc[kg].w);
+            }
+          }
           const int j = E4M3 ? 2 * i + hc : i;
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
-            qa[mt] = MT == 1 ? qf[0][MT == 1 ? j : 0] : q_mem[(mt * 2 * kQChunks + j) * 32 + lane];
-            qb[mt] = MT == 1 ? qf[MT == 1 ? 1 : 0][MT == 1 ? j : 0]
-                             : q_mem[((mt * 2 + 1) * kQChunks + j) * 32 + lane];
-          }
+            const uint4 qa = q_mem[((2 * mt) * kQChunks + j) * 32 + lane];
+            const uint4 qb = q_mem[((2 * mt + 1) * kQChunks + j) * 32 + lane];
 #pragma unroll
-          for (int kg = 0; kg < 2; ++kg) {
-            uint2 b0, b1;                        // B of the two steps
-            if (E4M3) {
-              const uint32_t w0 = hc ? kc[kg].z : kc[kg].x, w1 = hc ? kc[kg].w : kc[kg].y;
-              if (easy) {
-                const uint32_t m = scale_mul2<F16>(kb[kg]);
-                b0 = scale_codes<F16>(w0, m);
-                b1 = scale_codes<F16>(w1, m);
-              } else {
-                b0 = scale_codes_any<F16>(w0, kb[kg]);
-                b1 = scale_codes_any<F16>(w1, kb[kg]);
-              }
-            } else {
-              b0 = make_uint2(kc[kg].x, kc[kg].y);
-              b1 = make_uint2(kc[kg].z, kc[kg].w);
-            }
+            for (int kg = 0; kg < 2; ++kg)
+              mma<kHalf>(x[mt][kg], qa.x, qb.x, qa.y, qb.y, b0[kg].x, b0[kg].y);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              mma<F16>(x[mt][kg], qa[mt].x, qb[mt].x, qa[mt].y, qb[mt].y, b0.x, b0.y);
-              mma<F16>(x[mt][kg], qa[mt].z, qb[mt].z, qa[mt].w, qb[mt].w, b1.x, b1.y);
-            }
+            for (int kg = 0; kg < 2; ++kg)
+              mma<kHalf>(x[mt][kg], qa.z, qb.z, qa.w, qb.w, b1[kg].x, b1[kg].y);
           }
         }
       }
       // exponents, and whether a row's m has to move
+      float ks[4] = {1.f, 1.f, 1.f, 1.f};        // K's scales of keys 2q, 2q + 1, 2q + 8, 2q + 9
+      if (E4M3) {
+        const uint32_t k01 = *reinterpret_cast<const uint16_t*>(sb + 2 * q);
+        const uint32_t k23 = *reinterpret_cast<const uint16_t*>(sb + 8 + 2 * q);
+        ks[0] = __uint_as_float((k01 & 0xff) << 23);
+        ks[1] = __uint_as_float((k01 >> 8) << 23);
+        ks[2] = __uint_as_float((k23 & 0xff) << 23);
+        ks[3] = __uint_as_float((k23 >> 8) << 23);
+      }
       uint32_t see[MT][2];
       bool over = false;
 #pragma unroll
@@ -345,17 +444,21 @@ __global__ void __launch_bounds__(Few<E4M3, DP, MT>::kThreads, 1)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           see[mt][h] = 0xffffffffu;
-          if (masked)
-            see[mt][h] = sees_32(a.mask ? a.mask + (int64_t)(s.row0 + node[mt][h]) * a.mask_stride
-                                        : nullptr,
-                                 s.rows, node[mt][h], pos0 - s.start) >> (2 * q);
+          if (masked) {
+            const int row = 16 * mt + 8 * h + g;
+            const int nd = a.group.div(s.group * L::kRows + (row < rows ? row : 0));
+            see[mt][h] =
+                sees_32(a.mask ? a.mask + (int64_t)(s.row0 + nd) * a.mask_stride : nullptr, s.rows,
+                        nd, pos0 - start) >> (2 * q);
+          }
           float mx = -INFINITY;
 #pragma unroll
           for (int kg = 0; kg < 2; ++kg)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               float& v = x[mt][kg][2 * h + e];
-              v = sc.cap2 > 0.f ? capped(sc, v) : v * sc.sl2;
+              v *= E4M3 ? row_mul[mt][h] * ks[2 * kg + e] : row_mul[mt][h];
+              if (cap) v = capped(sc, v);
               if (!masked || (see[mt][h] >> (8 * kg + e)) & 1) mx = fmaxf(mx, v);
             }
           over |= mx > mref[mt][h] + (mref[mt][h] == -INFINITY ? 0.f : kShift + 8.f);
@@ -396,19 +499,27 @@ __global__ void __launch_bounds__(Few<E4M3, DP, MT>::kThreads, 1)
           const float sub = mref[mt][h] == -INFINITY ? 0.f : mref[mt][h];
 #pragma unroll
           for (int kg = 0; kg < 2; ++kg) {
-            float w0 = ex2(x[mt][kg][2 * h] - sub), w1 = ex2(x[mt][kg][2 * h + 1] - sub);
+            float &w0 = x[mt][kg][2 * h], &w1 = x[mt][kg][2 * h + 1];
+            w0 = ex2(w0 - sub);
+            w1 = ex2(w1 - sub);
             if (masked) {
               w0 = (see[mt][h] >> (8 * kg)) & 1 ? w0 : 0.f;
               w1 = (see[mt][h] >> (8 * kg + 1)) & 1 ? w1 : 0.f;
             }
             l[mt][h] += w0 + w1;
-            p[mt][2 * kg + h] = pack2<F16>(w0, w1);
+            p[mt][2 * kg + h] = pack2<kHalf>(w0, w1);
           }
         }
       // O += P V
-      const int draft = s.start - pos0;          // first key of the block that is draft
+      const int draft = start - pos0;            // first key of the block that is draft
       if (E4M3) {
-        uint32_t vw[4][4];
+        uint32_t vw[4][4], vb[4];
+        const uint32_t v01 = *reinterpret_cast<const uint16_t*>(sb + 16 + 2 * q);
+        const uint32_t v23 = *reinterpret_cast<const uint16_t*>(sb + 24 + 2 * q);
+        vb[0] = v01 & 0xff;
+        vb[1] = v01 >> 8;
+        vb[2] = v23 & 0xff;
+        vb[3] = v23 >> 8;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
           if (L::kVBytes < 16) {
@@ -427,44 +538,47 @@ __global__ void __launch_bounds__(Few<E4M3, DP, MT>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < L::kVBytes / 4; ++i) vw[kk][i] = 0;
             vb[kk] = 127;
-            if (pos0 + key < s.start + s.rows) {
-              atomicOr(&bad[(key - draft) >> 5], 1u << ((key - draft) & 31));
-              any_bad = true;
-            }
+            if (pos0 + key < start + s.rows)
+              atomicOr(&st.bad[(key - draft) >> 5], 1u << ((key - draft) & 31));
           }
         }
-        const uint32_t m01 = (scale_mul2<F16>(vb[0]) & 0xffffu) | (scale_mul2<F16>(vb[1]) << 16);
-        const uint32_t m23 = (scale_mul2<F16>(vb[2]) & 0xffffu) | (scale_mul2<F16>(vb[3]) << 16);
+        const bool easy = __all_sync(0xffffffffu, easy_scale<true>(vb[0]) && easy_scale<true>(vb[1]) &&
+                                                      easy_scale<true>(vb[2]) && easy_scale<true>(vb[3]));
+        if (easy) {
+          const uint32_t m01 = (scale_mul2<true>(vb[0]) & 0xffffu) | (scale_mul2<true>(vb[1]) << 16);
+          const uint32_t m23 = (scale_mul2<true>(vb[2]) & 0xffffu) | (scale_mul2<true>(vb[3]) << 16);
 #pragma unroll
-        for (int i = 0; i < L::kVBytes / 4; ++i) {
-          uint32_t b0[4], b1[4];
-          if (easy) {
+          for (int i = 0; i < L::kVBytes / 4; ++i)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint2 y = pair_codes<F16>(vw[0][i], vw[1][i], h, m01);
-              const uint2 z = pair_codes<F16>(vw[2][i], vw[3][i], h, m23);
-              b0[2 * h] = y.x;
-              b0[2 * h + 1] = y.y;
-              b1[2 * h] = z.x;
-              b1[2 * h + 1] = z.y;
-            }
-          } else {
-            const uint4 y = pair_codes_any<F16>(vw[0][i], vb[0], vw[1][i], vb[1]);
-            const uint4 z = pair_codes_any<F16>(vw[2][i], vb[2], vw[3][i], vb[3]);
-            b0[0] = y.x;
-            b0[1] = y.y;
-            b0[2] = y.z;
-            b0[3] = y.w;
-            b1[0] = z.x;
-            b1[1] = z.y;
-            b1[2] = z.z;
-            b1[3] = z.w;
-          }
+              const uint32_t sel = h ? 0x7362 : 0x5140;    // two codes of two keys, key by key
+              const uint2 y = scale_codes<true>(__byte_perm(vw[0][i], vw[1][i], sel), m01);
+              const uint2 z = scale_codes<true>(__byte_perm(vw[2][i], vw[3][i], sel), m23);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
+              for (int mt = 0; mt < MT; ++mt) {
+                mma<true>(o[mt][4 * i + 2 * h], p[mt][0], p[mt][1], p[mt][2], p[mt][3], y.x, z.x);
+                mma<true>(o[mt][4 * i + 2 * h + 1], p[mt][0], p[mt][1], p[mt][2], p[mt][3], y.y, z.y);
+              }
+            }
+        } else {
+          if (!F16) {                            // weights in the handle's type
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
-              mma<F16>(o[mt][4 * i + k], p[mt][0], p[mt][1], p[mt][2], p[mt][3], b0[k], b1[k]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                p[mt][k] = pack2<false>(x[mt][k / 2][2 * (k % 2)], x[mt][k / 2][2 * (k % 2) + 1]);
+          }
+#pragma unroll
+          for (int i = 0; i < L::kVBytes / 4; ++i) {
+            const uint4 y = pair_codes_any<F16>(vw[0][i], vb[0], vw[1][i], vb[1]);
+            const uint4 z = pair_codes_any<F16>(vw[2][i], vb[2], vw[3][i], vb[3]);
+            const uint32_t b0[4] = {y.x, y.y, y.z, y.w}, b1[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt)
+                mma<F16>(o[mt][4 * i + k], p[mt][0], p[mt][1], p[mt][2], p[mt][3], b0[k], b1[k]);
+          }
         }
       } else {
 #pragma unroll
@@ -475,10 +589,8 @@ __global__ void __launch_bounds__(Few<E4M3, DP, MT>::kThreads, 1)
             uint4 y = *reinterpret_cast<const uint4*>(v_src + (kk * (DP / 64) + cc) * 512);
             if (masked) {
               const int key = 2 * q + (kk & 1) + 8 * (kk >> 1);
-              if (key >= draft && pos0 + key < s.start + s.rows && zero_nonfinite<F16>(&y)) {
-                atomicOr(&bad[(key - draft) >> 5], 1u << ((key - draft) & 31));
-                any_bad = true;
-              }
+              if (key >= draft && pos0 + key < start + s.rows && zero_nonfinite<F16>(&y))
+                atomicOr(&st.bad[(key - draft) >> 5], 1u << ((key - draft) & 31));
             }
             vw[kk][0] = y.x;
             vw[kk][1] = y.y;
@@ -500,78 +612,139 @@ __global__ void __launch_bounds__(Few<E4M3, DP, MT>::kThreads, 1)
       }
     }
 
-    // the segment's result
+    // the warps meet: O, m and l of the segment.  First everybody's m and l ...
     const bool whole = s.whole();
-    const int64_t part = 2 * worker + (s.t0 == 0 ? 1 : 0);
-    float* part_o = a.part_o + part * (L::kRows * DP);
+    const int64_t part = 2 * blockIdx.x + (s.t0 == 0 ? 1 : 0);
+    float4* buf = reinterpret_cast<float4*>(smem + L::kBuf);
+    const int live = min(L::kWarps, s.t1 - s.t0);          // warps that had a block
+    float weight[MT][2];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float sum = l[mt][h];
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        const float inv = 1.f / sum;
-        if (whole && valid[mt][h]) {
-          uint16_t* out = a.out + out_row[mt][h] * a.D;
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int c8 = 0; c8 < kTiles / 8; ++c8) {
-              const int d = E4M3 ? (DP / 8) * (2 * q + e) + 8 * c8 : 8 * (2 * q + e) + 64 * c8;
-              uint32_t y[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                y[k] = sum == 0.f ? 0u
-                                  : pack2<F16>(o[mt][8 * c8 + 2 * k][2 * h + e] * inv,
-                                               o[mt][8 * c8 + 2 * k + 1][2 * h + e] * inv);
-              if (d < a.D) *reinterpret_cast<uint4*>(out + d) = make_uint4(y[0], y[1], y[2], y[3]);
-            }
-          if (q == 0 && a.lse)
-            a.lse[out_row[mt][h]] = sum == 0.f ? -INFINITY : (mref[mt][h] + log2f(sum)) * kLn2;
-        }
-        if (!whole && q == 0)
-          a.part_ml[part * L::kRows + 16 * mt + 8 * h + g] = make_float2(mref[mt][h], sum);
+        if (q == 0) st.ml[warp][16 * mt + 8 * h + g] = make_float2(mref[mt][h], sum);
       }
-      if (!whole) {
+    __syncthreads();
+    // ... then every warp's O by its weight, half of the accumulator tiles at a time
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t)
-          reinterpret_cast<float4*>(part_o)[(mt * kTiles + t) * 32 + lane] =
-              make_float4(o[mt][t][0], o[mt][t][1], o[mt][t][2], o[mt][t][3]);
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float top = -INFINITY;
+        for (int i = 0; i < live; ++i) top = fmaxf(top, st.ml[i][16 * mt + 8 * h + g].x);
+        weight[mt][h] = ex2(mref[mt][h] - (top == -INFINITY ? 0.f : top));
+      }
+#pragma unroll
+    for (int pass = 0; pass < 2; ++pass) {
+      if (warp < live) {
+#pragma unroll
+        for (int k = 0; k < L::kMerge; ++k) {
+          const int tile = pass * L::kMerge + k, mt = tile / kTiles;
+          const float* v = o[mt][tile % kTiles];
+          buf[(warp * L::kMerge + k) * 32 + lane] =
+              make_float4(v[0] * weight[mt][0], v[1] * weight[mt][0], v[2] * weight[mt][1],
+                          v[3] * weight[mt][1]);
+        }
+      }
+      __syncthreads();
+#pragma unroll 1
+      for (int k = warp; k < L::kMerge; k += L::kWarps) {
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int i = 0; i < live; ++i) {
+          const float4 v = buf[(i * L::kMerge + k) * 32 + lane];
+          y.x += v.x;
+          y.y += v.y;
+          y.z += v.z;
+          y.w += v.w;
+        }
+        const int tile = pass * L::kMerge + k, mt = tile / kTiles;
+        if (!whole) {
+          reinterpret_cast<float4*>(a.part_o + part * (L::kRows * DP))[tile * 32 + lane] = y;
+        } else {
+          // as 16-bit rows in Q's place
+          uint16_t* out = reinterpret_cast<uint16_t*>(q_mem);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int row = 16 * mt + 8 * h + g;
+            float top = -INFINITY, sum = 0.f;
+            for (int i = 0; i < live; ++i) top = fmaxf(top, st.ml[i][row].x);
+            const float sub = top == -INFINITY ? 0.f : top;
+            for (int i = 0; i < live; ++i) sum = fmaf(st.ml[i][row].y, ex2(st.ml[i][row].x - sub), sum);
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const float r0 = sum == 0.f ? 0.f : (h ? y.z : y.x) * inv;
+            const float r1 = sum == 0.f ? 0.f : (h ? y.w : y.y) * inv;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int n = 2 * q + e, ct = tile % kTiles;
+              const int d = E4M3 ? (DP / 8) * n + ct : 8 * n + ct % 8 + ct / 8 * 64;
+              out[row * DP + d] = (uint16_t)pack2<F16>(e ? r1 : r0, 0.f);
+            }
+          }
+        }
+      }
+      __syncthreads();
+    }
+    if (threadIdx.x < L::kRows && (int)threadIdx.x < rows) {
+      const int row = threadIdx.x;
+      float top = -INFINITY, sum = 0.f;
+      for (int i = 0; i < live; ++i) top = fmaxf(top, st.ml[i][row].x);
+      const float sub = top == -INFINITY ? 0.f : top;
+      for (int i = 0; i < live; ++i) sum = fmaf(st.ml[i][row].y, ex2(st.ml[i][row].x - sub), sum);
+      if (!whole) {
+        a.part_ml[part * L::kRows + row] = make_float2(top, sum);
+      } else if (a.lse) {
+        const int grow = s.group * L::kRows + row, nd = a.group.div(grow);
+        a.lse[(int64_t)(s.row0 + nd) * a.Hq + s.head * a.G + grow - nd * a.G] =
+            sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
       }
     }
-    if (!whole && lane == 0) a.part_of[part] = Item::part_of(s, share.total, workers);
-    if (__any_sync(0xffffffffu, any_bad)) {
-      __syncwarp();
-#pragma unroll 1
-      for (int i = 0; i < 2 * MT; ++i) {         // one lane a row
-        const int row = 8 * i + g;
-        if (q != 0 || row >= rows) continue;
+    if (whole) {
+      for (int i = threadIdx.x; i < rows * (DP / 8); i += L::kThreads) {
+        const int row = i / (DP / 8), chunk = i % (DP / 8);
         const int grow = s.group * L::kRows + row, nd = a.group.div(grow);
+        if (chunk * 8 < a.D)
+          reinterpret_cast<uint4*>(
+              a.out + ((int64_t)(s.row0 + nd) * a.Hq + s.head * a.G + grow - nd * a.G) * a.D)[chunk] =
+              q_mem[i];
+      }
+    }
+    if (!whole && threadIdx.x == 0) a.part_of[part] = Item::part_of(s, st.share.total, a.n_cta);
+    uint32_t any_bad = 0;
+#pragma unroll
+    for (int k = 0; k < DSPARK_TREE_MAX_NODES / 32; ++k) any_bad |= st.bad[k];
+    __syncthreads();
+    if (any_bad != 0) {
+      if (threadIdx.x < L::kRows && (int)threadIdx.x < rows) {
+        const int grow = s.group * L::kRows + threadIdx.x, nd = a.group.div(grow);
         add_nonfinite<F16, E4M3, DP>(
-            a, bad, a.mask ? a.mask + (int64_t)(s.row0 + nd) * a.mask_stride : nullptr, s.b, s.rows,
+            a, st.bad, a.mask ? a.mask + (int64_t)(s.row0 + nd) * a.mask_stride : nullptr, s.b, s.rows,
             s.start, s.head, nd,
             whole ? a.out + ((int64_t)(s.row0 + nd) * a.Hq + s.head * a.G + grow - nd * a.G) * a.D
                   : nullptr,
-            part_o, row);
+            a.part_o + part * (L::kRows * DP), threadIdx.x);
       }
-      __syncwarp();
-      if (lane < DSPARK_TREE_MAX_NODES / 32) bad[lane] = 0;
-      __syncwarp();
+      __syncthreads();
+      if (threadIdx.x < DSPARK_TREE_MAX_NODES / 32) st.bad[threadIdx.x] = 0;
     }
+    if (threadIdx.x == 0) st.live = walker.next(a, &s);
+    __syncthreads();
   }
   ptx::cp_async_wait_group<0>();
   if (worst > top_page) set_status(a.status, DSPARK_EPAGES);
 }
 
-// Joins the parts of the items that several warps share: an item of P parts has
-// P blocks, which take its pieces of four accumulator tiles in turn; the eight
-// warps of a block take every eighth part and are then added in order.
+// Joins the parts of the items that several CTAs share: an item of P parts has P
+// blocks, which take its pieces of four accumulator tiles in turn; the eight warps
+// of a block take every eighth part and are then added in order.
 constexpr int kJoinThreads = 256;
 
 template <bool F16, bool E4M3, int DP, int MT>
 __global__ void __launch_bounds__(kJoinThreads) few_join_kernel(const __grid_constant__ AttendArgs a) {
-  using Item = Work<kBlock, 16 * MT>;
+  using Item = Work<kBlock, 16 * MT, kExtra>;
   constexpr int kTiles = DP / 8, kRows = 16 * MT;
   __shared__ float4 sum_o[8][4][32];
   __shared__ float2 sum_ml[8][2][32];
@@ -668,7 +841,7 @@ cudaError_t launch(const AttendArgs& a, cudaStream_t stream) {
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(2 * few_workers(a.n_cta, MT));
+  cfg.gridDim = dim3(2 * a.n_cta);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cfg.attrs = &attr;
@@ -679,7 +852,7 @@ cudaError_t launch(const AttendArgs& a, cudaStream_t stream) {
 template <bool F16, bool E4M3, int DP, int MT>
 cudaError_t setup() {
   using L = Few<E4M3, DP, MT>;
-  static_assert(L::kSmem <= 232448, "shared memory of an SM");
+  static_assert(L::kSmem + sizeof(FewState) + 256 <= 232448, "shared memory of an SM");
   cudaError_t e = cudaFuncSetAttribute(few_kernel<F16, E4M3, DP, MT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (e != cudaSuccess) return e;
@@ -707,10 +880,6 @@ cudaError_t launch_for(const AttendArgs& a, int tiles, cudaStream_t stream) {
 }
 
 }  // namespace
-
-int few_workers(int n_cta, int tiles) {
-  return n_cta * (tiles == 1 ? Few<false, 128, 1>::kWarps : Few<false, 128, 2>::kWarps);
-}
 
 cudaError_t few_setup(bool f16, int D) {
   if (padded_dim(D) == 64) return f16 ? setup_all<true, 64>() : setup_all<false, 64>();

@@ -208,8 +208,7 @@ struct TileMaps {
 };
 
 // attend_few: at most 32 rows a cached head, on mma.sync (tree_attend_few.cu).
-// Its workers are warps; `tiles` is 1 or 2 row tiles of 16.
-int few_workers(int n_cta, int tiles);
+// `tiles`: 1 or 2 row tiles of 16.
 cudaError_t few_setup(bool f16, int D);
 cudaError_t few_launch(const AttendArgs& a, int tiles, bool f16, bool e4m3, cudaStream_t stream);
 

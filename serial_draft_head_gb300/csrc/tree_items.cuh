@@ -3,10 +3,12 @@
 //
 // Per cached head the rows that read it are (node, query head of the group):
 // T * G of them.  A work item is (request, cached head, up to ROWS of its rows)
-// over all its keys, cut into tiles of KEYS keys; a tile of one item is a unit.
-// The units of all items, in order, are split evenly over the workers (CTAs or
-// warps): the lengths are known on the device only, so every CTA sums them up
-// itself.  An item that lies inside one worker's share is finished there; one
+// over all its keys, cut into tiles of KEYS keys; a tile of one item is a unit,
+// and so that short items do not pile up on one worker, EXTRA more units stand
+// before an item's first for what it costs beside its tiles (Q, the result, the
+// way into the loop).  The units of all items, in order, are split evenly over
+// the workers (one CTA a SM): the lengths are known on the device only, so every
+// CTA sums them up itself.  An item that lies inside one worker's share is finished there; one
 // that several workers share leaves parts (unnormalised O, maximum, sum), joined
 // by a second kernel in the order of the keys.
 //
@@ -75,13 +77,14 @@ static __device__ __noinline__ int holder(int64_t total, int workers, int64_t u)
   return c;
 }
 
-// A worker's share: its units, all units, and the place of its first.
+// A worker's share: its units, all units, and the place of its first (t0 < 0: one
+// of the units before an item's tiles).
 struct Share {
   int64_t unit0, units, total;
   int b0, head0, group0, t0;
 };
 
-template <int KEYS, int ROWS>
+template <int KEYS, int ROWS, int EXTRA>
 struct Work {
   // Rows of request b as attend takes them (0 if they do not fit), key tiles and
   // row groups.
@@ -115,7 +118,7 @@ struct Work {
       if (k < per && b < a.b.B) {
         bool ok;
         const Request r = load_request(a, b, &ok);
-        if (ok && r.rows > 0) mine[k] = (int64_t)r.tiles * r.groups * a.Hkv;
+        if (ok && r.rows > 0) mine[k] = (int64_t)(r.tiles + EXTRA) * r.groups * a.Hkv;
         if (!ok && blockIdx.x == 0) set_status(a.status, DSPARK_EPAGES);
       }
       sum += mine[k];
@@ -156,9 +159,9 @@ struct Work {
           const int b = threadIdx.x * per + k;
           bool ok;
           const Request r = load_request(a, b, &ok);
-          const int64_t item = (u0 - at) / r.tiles;
+          const int64_t item = (u0 - at) / (r.tiles + EXTRA);
           shares[i].b0 = b;
-          shares[i].t0 = (int)(u0 - at - item * r.tiles);
+          shares[i].t0 = (int)(u0 - at - item * (r.tiles + EXTRA)) - EXTRA;
           shares[i].head0 = (int)(item / r.groups);
           shares[i].group0 = (int)(item % r.groups);
         }
@@ -192,37 +195,39 @@ struct Work {
     }
 
     __device__ bool next(const AttendArgs& a, Segment* s) {
-      if (left <= 0) return false;
-      const int64_t rest = r.tiles - t0;
-      const int n = (int)(rest < left ? rest : left);
-      s->b = b;
-      s->row0 = r.row0;
-      s->rows = r.rows;
-      s->start = r.start;
-      s->head = head;
-      s->group = group;
-      s->t0 = t0;
-      s->t1 = t0 + n;
-      s->tiles = r.tiles;
-      s->item_end = unit + rest;
-      left -= n;
-      unit += n;
-      t0 += n;
-      if (t0 == r.tiles) {
-        t0 = 0;
-        if (++group == r.groups) {
-          group = 0;
-          if (++head == a.Hkv) {
-            head = 0;
-            bool ok;
-            if (left > 0) do {
-                r = load_request(a, ++b, &ok);
-              } while (r.rows == 0 && b + 1 < a.b.B);
-            if (r.rows == 0) left = 0;  // the arrays changed under the kernel
+      while (left > 0) {
+        const int64_t rest = r.tiles - t0;
+        const int n = (int)(rest < left ? rest : left);
+        s->b = b;
+        s->row0 = r.row0;
+        s->rows = r.rows;
+        s->start = r.start;
+        s->head = head;
+        s->group = group;
+        s->t0 = t0 > 0 ? t0 : 0;
+        s->t1 = t0 + n;
+        s->tiles = r.tiles;
+        s->item_end = unit + rest;
+        left -= n;
+        unit += n;
+        t0 += n;
+        if (t0 == r.tiles) {
+          t0 = -EXTRA;
+          if (++group == r.groups) {
+            group = 0;
+            if (++head == a.Hkv) {
+              head = 0;
+              bool ok;
+              if (left > 0) do {
+                  r = load_request(a, ++b, &ok);
+                } while (r.rows == 0 && b + 1 < a.b.B);
+              if (r.rows == 0) left = 0;  // the arrays changed under the kernel
+            }
           }
         }
+        if (s->t1 > s->t0) return true;   // else no more than units before the tiles
       }
-      return true;
+      return false;
     }
   };
 
@@ -248,13 +253,21 @@ struct Work {
       t = s.t0;
       seg = 0;
       if (left > 0) load(a);
+      skip();
+    }
+    __device__ __forceinline__ void skip() {      // the units before an item's tiles
+      if (t < 0) {
+        left += t;
+        t = 0;
+      }
     }
     __device__ __forceinline__ bool more() const { return left > 0; }
     __device__ __forceinline__ int total() const { return start + rows; }
     __device__ void next(const AttendArgs& a) {
       --left;
       if (++t < tiles) return;
-      t = 0;
+      t = -EXTRA;
+      skip();
       ++seg;
       if (++group < groups) return;
       group = 0;
