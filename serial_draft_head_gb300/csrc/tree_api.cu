@@ -292,12 +292,11 @@ int dspark_tree_attend(dspark_tree_t h, const dspark_tree_cache* cache,
   a.part_of = h->part_of;
   a.part_rows = h->part_rows;
   a.status = h->status;
-  // At most 32 rows a cached head on average: the kernel for few rows (any number
+  // At most 16 rows a cached head on average: the kernel for few rows (any number
   // of rows is right in either).
-  const int64_t rows = (int64_t)a.b.N * a.G;
-  if (rows <= (int64_t)32 * a.b.B)
-    return cuda_code(few_launch(a, rows <= (int64_t)16 * a.b.B ? 1 : 2,
-                                h->cfg.type == DSPARK_TYPE_F16, cache->type == DSPARK_TYPE_E4M3,
+  if ((int64_t)a.b.N * a.G <= (int64_t)16 * a.b.B)
+    return cuda_code(few_launch(a, h->cfg.type == DSPARK_TYPE_F16,
+                                cache->type == DSPARK_TYPE_E4M3,
                                 static_cast<cudaStream_t>(stream)));
   TileMaps maps;
   make_maps(h, cache, a.c, &maps);

@@ -1,5 +1,5 @@
 // tree_attend.cu -- attention of drafted rows over a paged cache on tcgen05, for
-// more than 32 rows a cached head (tree_attend_few.cu has the others).  Items
+// more than 16 rows a cached head (tree_attend_few.cu has the others).  Items
 // are 256 rows by tiles of 128 keys, a worker is a CTA, one a SM (tree_items.cuh
 // says how the work is cut, and the mathematics).
 //

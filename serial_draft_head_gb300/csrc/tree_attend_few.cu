@@ -1,7 +1,7 @@
-// tree_attend_few.cu -- attention of few drafted rows (at most 32 a cached head:
+// tree_attend_few.cu -- attention of few drafted rows (at most 16 a cached head:
 // single tokens, short chains) over a paged cache.
 //
-// Items are 16 or 32 rows by blocks of 16 keys, a worker is a CTA (tree_items.cuh
+// Items are 16 rows by blocks of 16 (e4m3: 32) keys, a worker is a CTA (tree_items.cuh
 // says how the work is cut, and the mathematics).  The warps of a CTA take a
 // segment's blocks in turn, each with its own O, m and l, and meet at its end.
 // With so few rows K and V are used once from where they land, and the memory
@@ -20,7 +20,7 @@
 //    rows, and pairs of keys are put together by byte permutations.
 //
 // So every thread reads just the 16-byte chunks that it copied itself: the ring
-// in shared memory (cp.async, a stage is 16 keys of K and V) needs no barrier,
+// in shared memory (cp.async, a stage is a block of K and V) needs no barrier,
 // only the thread's own wait.
 //
 // e4m3: the products are f16, which holds every code, one conversion for two
@@ -35,37 +35,40 @@ namespace dspark {
 namespace tree {
 namespace {
 
-constexpr int kBlock = 16;              // keys of a block, and of a ring stage
-constexpr int kExtra = 14;              // blocks that an item's other work takes as long as
-
-template <bool E4M3, int DP, int MT>
+template <bool E4M3, int DP>
 struct Few {
-  static constexpr int kRows = 16 * MT;
-  // as many warps as hold their O and S in registers and their ring in shared memory
-  static constexpr int kWarps = MT == 2 ? 8 : E4M3 ? 12 : 10;
+  static constexpr int kRows = 16;
+  // e4m3: what a block costs beside its data is spread over twice the keys
+  static constexpr int kBlock = E4M3 ? 32 : 16;
+  static constexpr int kExtra = E4M3 ? 10 : 8;           // blocks an item's other work takes as long as
+  static constexpr int kWarps = E4M3 ? 12 : 10;          // as many as registers and rings allow
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kBytes = DP * (E4M3 ? 1 : 2);     // of a cached row
+  static constexpr int kGroups = kBlock / 8;             // of eight keys
   static constexpr int kKCopies = kBytes / 64;           // 16-byte chunks a lane, of a row of K
   static constexpr int kVBytes = kBytes / 8;             // bytes a lane, of a row of V
   static constexpr int kStage = 2 * kBlock * kBytes;
   static constexpr int kVPart = kBlock * kBytes;         // V's place in a stage
   static constexpr int kStages = kStage == 8192 ? 2 : 3;
-  static constexpr int kTiles = DP / 8;                  // column tiles of O, per row tile
-  static constexpr int kMerge = MT * kTiles / 2;         // accumulator tiles merged at a time
+  static constexpr int kTiles = DP / 8;                  // column tiles of O
+  static constexpr int kMerge = 4;                       // of them merged at a time
   static constexpr int kRing = kStages * kStage;         // of a warp
-  static constexpr int kQ = kWarps * kRing;              // Q, then the result: [rows][DP] 16-bit
+  static constexpr int kQ = kWarps * kRing;
+  static constexpr int kOut = kQ;                        // the result in Q's place: [rows][DP]
   static constexpr int kBuf = kQ + kRows * DP * 2;       // [warp][kMerge][lane] float4
-  static constexpr int kScales = kBuf + kWarps * kMerge * 512;   // [warp][stage][K 16, V 16]
-  static constexpr int kSmem = kScales + kWarps * kStages * 32;
+  static constexpr int kScales = kBuf + kWarps * kMerge * 512;   // [warp][stage][K, V][key]
+  static constexpr int kSmem = kScales + kWarps * kStages * 2 * kBlock;
+  using Item = Work<kBlock, kRows, kExtra>;
 };
 
 struct FewState {
-  float2 ml[16][32];                    // [warp][row]
-  float row_mul[32];                    // a row's factor on the raw scores
+  float2 ml[16][16];                    // [warp][row]
+  float2 fin[16];                       // a row's m of all warps, and 1 / l (l = 0: 0)
+  float row_mul[16];                    // a row's factor on the raw scores
   uint32_t bad[DSPARK_TREE_MAX_NODES / 32];
   int64_t sums[16];
   Share share;
-  int live;                             // there is a segment
+  int live[2];                          // there is a segment; the next one
 };
 
 // Column d of the result: its place in the accumulators, n = 2 q + e and tile.
@@ -133,7 +136,7 @@ __device__ __noinline__ void add_nonfinite(const AttendArgs& a, const uint32_t* 
 
 // The blocks of one warp in order: of every segment those t0 + warp, t0 + warp +
 // warps, ...
-template <class Item>
+template <class Item, int EXTRA>
 struct BlockCursor {
   int b, head, group, t, end;           // end: of the segment
   int rows, start, tiles, groups;
@@ -150,7 +153,7 @@ struct BlockCursor {
   }
   __device__ void settle(const AttendArgs& a, int warp) {     // past the ends of segments
     while (t >= end) {
-      if (after <= kExtra) {            // no more tiles in the share
+      if (after <= EXTRA) {             // no more tiles in the share
         more = false;
         return;
       }
@@ -167,7 +170,7 @@ struct BlockCursor {
           } while (rows == 0);
         }
       }
-      after -= kExtra;
+      after -= EXTRA;
       end = (int)(after < tiles ? after : tiles);
       after -= end;
       t = warp;
@@ -193,56 +196,63 @@ struct BlockCursor {
   }
 };
 
-template <bool F16, bool E4M3, int DP, int MT>
-__global__ void __launch_bounds__(Few<E4M3, DP, MT>::kThreads, 1)
+template <bool F16, bool E4M3, int DP>
+__global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
     few_kernel(const __grid_constant__ AttendArgs a) {
-  using L = Few<E4M3, DP, MT>;
-  using Item = Work<kBlock, L::kRows, kExtra>;
+  using L = Few<E4M3, DP>;
+  using Item = typename L::Item;
+  using Segment = typename Item::Segment;
   constexpr bool kHalf = F16 || E4M3;            // the products' type is f16
-  constexpr int kTiles = L::kTiles;
+  constexpr int kTiles = L::kTiles, kGroups = L::kGroups, kBlock = L::kBlock;
   constexpr int kQChunks = DP / 32;              // 16-byte chunks of a row of Q a lane
+  constexpr int kQWarp = L::kWarps - 2;          // the two warps that bring Q, eight rows each
   constexpr float kShift = kHalf ? 7.f : 0.f;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ FewState st;
   __shared__ typename Item::Walker walker;
-  __shared__ typename Item::Segment s;
+  __shared__ Segment segments[2];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane >> 2, q = lane & 3;
   uint8_t* ring = smem + warp * L::kRing;
   uint4* q_mem = reinterpret_cast<uint4*>(smem + L::kQ);
-  uint8_t* scales = smem + L::kScales + warp * L::kStages * 32;
+  uint8_t* scales = smem + L::kScales + warp * L::kStages * 2 * kBlock;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x < 2) a.part_of[2 * blockIdx.x + threadIdx.x] = make_int4(0, 0, 0, 0);
   if (threadIdx.x < DSPARK_TREE_MAX_NODES / 32) st.bad[threadIdx.x] = 0;
   Item::template plan<L::kThreads, 1>(a, blockIdx.x, 1, a.n_cta, &st.share, st.sums);
 
   // ---- the copies' side: the warp's blocks in order, kStages - 1 ahead of the products
-  BlockCursor<Item> c;
+  BlockCursor<Item, L::kExtra> c;
   c.init(a, st.share, warp);
   const uint32_t top_page = (uint32_t)(a.c.n_pages - 1);
   const bool even = a.c.page.d % kBlock == 0;    // a block lies in one page
-  uint32_t page = 0, worst = 0;                  // of the next block: its page, or that of key lane % 16
+  uint32_t page = 0, worst = 0;                  // of the next block: its page, or that of key lane
   auto look = [&]() {
     if (!c.more) return;
-    const int pos = c.t * kBlock + (even ? 0 : lane % 16);
+    const int pos = c.t * kBlock + (even ? 0 : lane % kBlock);
     page = (uint32_t)__ldg(a.b.pages + (int64_t)c.b * a.b.pages_stride +
                            a.c.page.div(min(pos, c.start + c.rows - 1)));
   };
   look();
   int stage_in = 0, scale_stage = -1;
-  uint32_t scale_byte = 0;
+  uint32_t k_byte = 0, v_byte = 0;
   auto issue = [&]() {
-    // the scales of the block before have landed: lanes 0 .. 15 K's, 16 .. 31 V's
-    if (E4M3 && scale_stage >= 0) scales[scale_stage * 32 + lane] = (uint8_t)scale_byte;
+    // the scales of the block before have landed: lane = key
+    if (E4M3 && scale_stage >= 0) {
+      scales[scale_stage * 2 * kBlock + lane] = (uint8_t)k_byte;
+      scales[scale_stage * 2 * kBlock + kBlock + lane] = (uint8_t)v_byte;
+    }
     scale_stage = -1;
     if (c.more) {
       const int pos0 = c.t * kBlock, total = c.start + c.rows, head = c.head;
       const bool full = pos0 + kBlock <= total;
       worst = max(worst, page);                  // a bad page is reported at the end
       const uint32_t pg = min(page, top_page);
-      const int pos = even ? pos0 : min(pos0 + lane % 16, total - 1);
-      const int slot = pos - a.c.page.div(pos) * a.c.page.d;   // of the block, or of key lane % 16
+      const int pos = even ? pos0 : min(pos0 + lane % kBlock, total - 1);
+      const int slot = pos - a.c.page.div(pos) * a.c.page.d;   // of the block, or of key lane
       if (E4M3) {
-        scale_byte = __ldg(a.c.scale[lane / 16].at(pg, even ? slot + lane % 16 : slot, head));
+        const int key_slot = even ? slot + lane : slot;
+        k_byte = __ldg(a.c.scale[0].at(pg, key_slot, head));
+        v_byte = __ldg(a.c.scale[1].at(pg, key_slot, head));
         scale_stage = stage_in;
       }
       c.next(a, warp, L::kWarps);
@@ -252,7 +262,7 @@ __global__ void __launch_bounds__(Few<E4M3, DP, MT>::kThreads, 1)
       const uint8_t* k = kr.of_head(head) + q * 16;
       if (even) k += kr.offset(pg, slot + g);
 #pragma unroll
-      for (int kg = 0; kg < 2; ++kg) {
+      for (int kg = 0; kg < kGroups; ++kg) {
         const uint8_t* src;
         if (even) {
           src = k + (uint64_t)(8 * kg) * kr.slot;
@@ -270,7 +280,7 @@ __global__ void __launch_bounds__(Few<E4M3, DP, MT>::kThreads, 1)
       const uint8_t* v = vr.of_head(head) + g * (L::kVBytes < 16 ? 8 : 16);
       if (even) v += vr.offset(pg, slot + 2 * q);
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
+      for (int kk = 0; kk < kBlock / 4; ++kk) {
         const int off = (kk & 1) + 8 * (kk >> 1), key = 2 * q + off;
         const uint8_t* src;
         if (even) {
@@ -295,116 +305,114 @@ __global__ void __launch_bounds__(Few<E4M3, DP, MT>::kThreads, 1)
     ptx::cp_async_commit();
     if (++stage_in == L::kStages) stage_in = 0;
   };
-#pragma unroll 1
-  for (int i = 0; i < L::kStages - 1; ++i) issue();
 
-  // ---- the products' side
+  // ---- Q of a segment: lane (g, q) of two warps the chunks that meet its K
   const Score sc = Score::of(a);
   const bool cap = sc.cap2 > 0.f;
-  const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
-  if (threadIdx.x == 0) {
-    walker.init(a, st.share);
-    st.live = walker.next(a, &s);
-  }
-  __syncthreads();
-  int stage = 0;
-  while (st.live) {
+  const int q_row = 8 * (warp - kQWarp) + g;
+  uint4 qx[kQChunks];
+  auto load_q = [&](const Segment& s) {
     const int rows = Item::group_rows(a, s);
-    // Q: a warp for every eight rows, lane (g, q) the chunks that meet its K
-    if (warp < 2 * MT) {
-      const int row = 8 * warp + g;
-      const int grow = s.group * L::kRows + (row < rows ? row : 0), nd = a.group.div(grow);
-      const uint8_t* src = a.q + (int64_t)(s.row0 + nd) * a.q_row +
-                           (int64_t)(s.head * a.G + grow - nd * a.G) * a.q_head;
-      uint4 x[kQChunks];
+    const int grow = s.group * L::kRows + (q_row < rows ? q_row : 0), nd = a.group.div(grow);
+    const uint8_t* src = a.q + (int64_t)(s.row0 + nd) * a.q_row +
+                         (int64_t)(s.head * a.G + grow - nd * a.G) * a.q_head;
+#pragma unroll
+    for (int j = 0; j < kQChunks; ++j) {
+      const int chunk = E4M3 ? 8 * (j / 2) + 2 * q + j % 2 : 4 * j + q;
+      qx[j] = make_uint4(0, 0, 0, 0);
+      if (q_row < rows && chunk * 8 < a.D)
+        qx[j] = __ldg(reinterpret_cast<const uint4*>(src) + chunk);
+    }
+  };
+  auto store_q = [&]() {
+    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+    float row_mul = cap ? 1.f : sc.sl2, r = 1.f;
+    if (E4M3 && !F16) {
+      // the row's largest magnitude to [2^14, 2^15): r a power of two, exact
       uint32_t big = 0;
 #pragma unroll
       for (int j = 0; j < kQChunks; ++j) {
-        const int chunk = E4M3 ? 8 * (j / 2) + 2 * q + j % 2 : 4 * j + q;
-        x[j] = make_uint4(0, 0, 0, 0);
-        if (row < rows && chunk * 8 < a.D) x[j] = __ldg(reinterpret_cast<const uint4*>(src) + chunk);
-        if (E4M3 && !F16) {
-          const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+        const uint32_t w[4] = {qx[j].x, qx[j].y, qx[j].z, qx[j].w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            big = max(big, max((w[k] & 0x7fffu) << 16, w[k] & 0x7fff0000u));
-        }
-        x[j].x ^= flip;
-        x[j].y ^= flip;
-        x[j].z ^= flip;
-        x[j].w ^= flip;
+        for (int k = 0; k < 4; ++k) big = max(big, max((w[k] & 0x7fffu) << 16, w[k] & 0x7fff0000u));
       }
-      float row_mul = cap ? 1.f : sc.sl2;
+      big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      const int e = (int)(big >> 23);
+      const int up = big == 0 || e == 255 ? 0 : min(127 + 14 - e, 126);
+      r = __uint_as_float((uint32_t)(127 + up) << 23);
+      row_mul *= __uint_as_float((uint32_t)(127 - up) << 23);
+    }
+    if (q == 0) st.row_mul[q_row] = row_mul;
+#pragma unroll
+    for (int j = 0; j < kQChunks; ++j) {
+      uint32_t w[4] = {qx[j].x ^ flip, qx[j].y ^ flip, qx[j].z ^ flip, qx[j].w ^ flip};
       if (E4M3 && !F16) {
-        // the row's largest magnitude to [2^14, 2^15): r a power of two, exact
-        big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
-        big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-        const int e = (int)(big >> 23);
-        const int up = big == 0 || e == 255 ? 0 : min(127 + 14 - e, 126);
-        const float r = __uint_as_float((uint32_t)(127 + up) << 23);
-        const float down = __uint_as_float((uint32_t)(127 - up) << 23);
-        row_mul *= down;
 #pragma unroll
-        for (int j = 0; j < kQChunks; ++j) {
-          uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            w[k] = pack2<true>(to_float<false>((uint16_t)w[k]) * r,
-                               to_float<false>((uint16_t)(w[k] >> 16)) * r);
-          x[j] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+        for (int k = 0; k < 4; ++k)
+          w[k] = pack2<true>(to_float<false>((uint16_t)w[k]) * r,
+                             to_float<false>((uint16_t)(w[k] >> 16)) * r);
       }
-      if (q == 0) st.row_mul[row] = row_mul;
-#pragma unroll
-      for (int j = 0; j < kQChunks; ++j) q_mem[(warp * kQChunks + j) * 32 + lane] = x[j];
+      q_mem[((warp - kQWarp) * kQChunks + j) * 32 + lane] = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    __syncthreads();
-    float o[MT][kTiles][4], mref[MT][2], l[MT][2], row_mul[MT][2];
+  };
+  if (threadIdx.x == 0) {
+    walker.init(a, st.share);
+    st.live[0] = walker.next(a, &segments[0]);
+  }
+#pragma unroll 1
+  for (int i = 0; i < L::kStages - 1; ++i) issue();
+  __syncthreads();
+  if (st.live[0] && warp >= kQWarp) {
+    load_q(segments[0]);
+    store_q();
+  }
+  __syncthreads();
+
+  // ---- the products' side
+  int stage = 0, cur = 0;
+  while (st.live[cur]) {
+    const Segment& s = segments[cur];
+    const int rows = Item::group_rows(a, s), t1 = s.t1, start = s.start;
+    float o[kTiles][4], mref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    const float row_mul[2] = {st.row_mul[g], st.row_mul[g + 8]};
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        mref[mt][h] = -INFINITY;
-        l[mt][h] = 0.f;
-        row_mul[mt][h] = st.row_mul[16 * mt + 8 * h + g];
-      }
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[mt][t][k] = 0.f;
-    }
-    const int t1 = s.t1, start = s.start;
+      for (int k = 0; k < 4; ++k) o[t][k] = 0.f;
+    // the segment after this one, meanwhile
+    if (threadIdx.x == L::kThreads - 1) st.live[cur ^ 1] = walker.next(a, &segments[cur ^ 1]);
 #pragma unroll 1
     for (int t = s.t0 + warp; t < t1; t += L::kWarps) {
       issue();
       ptx::cp_async_wait_group<L::kStages - 1>();
       __syncwarp();
       const uint8_t* src = ring + stage * L::kStage + lane * 16;
-      const uint8_t* sb = scales + stage * 32;
+      const uint8_t* sb = scales + stage * 2 * kBlock;
       const uint8_t* v_src = ring + stage * L::kStage + L::kVPart +
                              lane * (L::kVBytes < 16 ? 8 : 16);
       if (++stage == L::kStages) stage = 0;
       const int pos0 = t * kBlock;
       const bool masked = pos0 + kBlock > start;
-      // S: a lane's rows g and g + 8, keys 2q, 2q + 1 of both groups of eight
-      float x[MT][2][4];
+      // S: a lane's rows g and g + 8, keys 2q, 2q + 1 of every group of eight
+      float x[kGroups][4];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int kg = 0; kg < kGroups; ++kg)
 #pragma unroll
-        for (int kg = 0; kg < 2; ++kg)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) x[mt][kg][k] = 0.f;
+        for (int k = 0; k < 4; ++k) x[kg][k] = 0.f;
 #pragma unroll
       for (int i = 0; i < L::kKCopies; ++i) {
-        uint4 kc[2];
+        uint4 kc[kGroups];
 #pragma unroll
-        for (int kg = 0; kg < 2; ++kg)
+        for (int kg = 0; kg < kGroups; ++kg)
           kc[kg] = *reinterpret_cast<const uint4*>(src + (kg * L::kKCopies + i) * 512);
 #pragma unroll
         for (int hc = 0; hc < (E4M3 ? 2 : 1); ++hc) {      // a chunk of Q: two steps
-          uint2 b0[2], b1[2];                              // B of the two steps
+          const int j = E4M3 ? 2 * i + hc : i;
+          const uint4 qa = q_mem[j * 32 + lane], qb = q_mem[(kQChunks + j) * 32 + lane];
+          uint2 b0[kGroups], b1[kGroups];                  // B of the two steps
 #pragma unroll
-          for (int kg = 0; kg < 2; ++kg) {
+          for (int kg = 0; kg < kGroups; ++kg) {
             if (E4M3) {
               b0[kg] = codes_f16(hc ? kc[kg].z : kc[kg].x);
               b1[kg] = codes_f16(hc ? kc[kg].w : kc[kg].y);
@@ -413,325 +421,279 @@ __global__ void __launch_bounds__(Few<E4M3, DP, MT>::kThreads, 1)
               b1[kg] = make_uint2(kc[kg].z, kc[kg].w);
             }
           }
-          const int j = E4M3 ? 2 * i + hc : i;
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            const uint4 qa = q_mem[((2 * mt) * kQChunks + j) * 32 + lane];
-            const uint4 qb = q_mem[((2 * mt + 1) * kQChunks + j) * 32 + lane];
+          for (int kg = 0; kg < kGroups; ++kg)
+            mma<kHalf>(x[kg], qa.x, qb.x, qa.y, qb.y, b0[kg].x, b0[kg].y);
 #pragma unroll
-            for (int kg = 0; kg < 2; ++kg)
-              mma<kHalf>(x[mt][kg], qa.x, qb.x, qa.y, qb.y, b0[kg].x, b0[kg].y);
-#pragma unroll
-            for (int kg = 0; kg < 2; ++kg)
-              mma<kHalf>(x[mt][kg], qa.z, qb.z, qa.w, qb.w, b1[kg].x, b1[kg].y);
-          }
+          for (int kg = 0; kg < kGroups; ++kg)
+            mma<kHalf>(x[kg], qa.z, qb.z, qa.w, qb.w, b1[kg].x, b1[kg].y);
         }
       }
       // exponents, and whether a row's m has to move
-      float ks[4] = {1.f, 1.f, 1.f, 1.f};        // K's scales of keys 2q, 2q + 1, 2q + 8, 2q + 9
-      if (E4M3) {
-        const uint32_t k01 = *reinterpret_cast<const uint16_t*>(sb + 2 * q);
-        const uint32_t k23 = *reinterpret_cast<const uint16_t*>(sb + 8 + 2 * q);
-        ks[0] = __uint_as_float((k01 & 0xff) << 23);
-        ks[1] = __uint_as_float((k01 >> 8) << 23);
-        ks[2] = __uint_as_float((k23 & 0xff) << 23);
-        ks[3] = __uint_as_float((k23 >> 8) << 23);
-      }
-      uint32_t see[MT][2];
-      bool over = false;
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      uint32_t see[2] = {0xffffffffu, 0xffffffffu};
+      if (masked) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          see[mt][h] = 0xffffffffu;
-          if (masked) {
-            const int row = 16 * mt + 8 * h + g;
-            const int nd = a.group.div(s.group * L::kRows + (row < rows ? row : 0));
-            see[mt][h] =
-                sees_32(a.mask ? a.mask + (int64_t)(s.row0 + nd) * a.mask_stride : nullptr, s.rows,
-                        nd, pos0 - start) >> (2 * q);
-          }
-          float mx = -INFINITY;
-#pragma unroll
-          for (int kg = 0; kg < 2; ++kg)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float& v = x[mt][kg][2 * h + e];
-              v *= E4M3 ? row_mul[mt][h] * ks[2 * kg + e] : row_mul[mt][h];
-              if (cap) v = capped(sc, v);
-              if (!masked || (see[mt][h] >> (8 * kg + e)) & 1) mx = fmaxf(mx, v);
-            }
-          over |= mx > mref[mt][h] + (mref[mt][h] == -INFINITY ? 0.f : kShift + 8.f);
+          const int row = 8 * h + g;
+          const int nd = a.group.div(s.group * L::kRows + (row < rows ? row : 0));
+          see[h] = sees_32(a.mask ? a.mask + (int64_t)(s.row0 + nd) * a.mask_stride : nullptr,
+                           s.rows, nd, pos0 - start) >> (2 * q);
         }
+      }
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int kg = 0; kg < kGroups; ++kg) {
+        float ks[2] = {1.f, 1.f};                // K's scales of keys 2q, 2q + 1 of the group
+        if (E4M3) {
+          const uint32_t k01 = *reinterpret_cast<const uint16_t*>(sb + 8 * kg + 2 * q);
+          ks[0] = __uint_as_float((k01 & 0xff) << 23);
+          ks[1] = __uint_as_float((k01 >> 8) << 23);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float& v = x[kg][2 * h + e];
+            v *= E4M3 ? row_mul[h] * ks[e] : row_mul[h];
+            if (cap) v = capped(sc, v);
+            if (!masked || (see[h] >> (8 * kg + e)) & 1) mx[h] = fmaxf(mx[h], v);
+          }
+      }
+      const bool over = mx[0] > mref[0] + (mref[0] == -INFINITY ? 0.f : kShift + 8.f) ||
+                        mx[1] > mref[1] + (mref[1] == -INFINITY ? 0.f : kShift + 8.f);
       if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int h = 0; h < 2; ++h) {
+          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+          const float old = mref[h];
+          if (mx[h] > old + (old == -INFINITY ? 0.f : kShift + 8.f)) {
+            mref[h] = mx[h] - kShift;
+            const float back = old == -INFINITY ? 0.f : ex2(old - mref[h]);
+            l[h] *= back;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float mx = -INFINITY;
-#pragma unroll
-            for (int kg = 0; kg < 2; ++kg)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if (!masked || (see[mt][h] >> (8 * kg + e)) & 1)
-                  mx = fmaxf(mx, x[mt][kg][2 * h + e]);
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const float old = mref[mt][h];
-            if (mx > old + (old == -INFINITY ? 0.f : kShift + 8.f)) {
-              mref[mt][h] = mx - kShift;
-              const float back = old == -INFINITY ? 0.f : ex2(old - mref[mt][h]);
-              l[mt][h] *= back;
-#pragma unroll
-              for (int c8 = 0; c8 < kTiles; ++c8) {
-                o[mt][c8][2 * h] *= back;
-                o[mt][c8][2 * h + 1] *= back;
-              }
+            for (int t8 = 0; t8 < kTiles; ++t8) {
+              o[t8][2 * h] *= back;
+              o[t8][2 * h + 1] *= back;
             }
           }
+        }
       }
       // weights, as the A operand of the second product
-      uint32_t p[MT][4];
+      uint32_t p[kGroups / 2][4];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int h = 0; h < 2; ++h) {
+        const float sub = mref[h] == -INFINITY ? 0.f : mref[h];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float sub = mref[mt][h] == -INFINITY ? 0.f : mref[mt][h];
-#pragma unroll
-          for (int kg = 0; kg < 2; ++kg) {
-            float &w0 = x[mt][kg][2 * h], &w1 = x[mt][kg][2 * h + 1];
-            w0 = ex2(w0 - sub);
-            w1 = ex2(w1 - sub);
-            if (masked) {
-              w0 = (see[mt][h] >> (8 * kg)) & 1 ? w0 : 0.f;
-              w1 = (see[mt][h] >> (8 * kg + 1)) & 1 ? w1 : 0.f;
-            }
-            l[mt][h] += w0 + w1;
-            p[mt][2 * kg + h] = pack2<kHalf>(w0, w1);
+        for (int kg = 0; kg < kGroups; ++kg) {
+          float &w0 = x[kg][2 * h], &w1 = x[kg][2 * h + 1];
+          w0 = ex2(w0 - sub);
+          w1 = ex2(w1 - sub);
+          if (masked) {
+            w0 = (see[h] >> (8 * kg)) & 1 ? w0 : 0.f;
+            w1 = (see[h] >> (8 * kg + 1)) & 1 ? w1 : 0.f;
           }
+          l[h] += w0 + w1;
+          p[kg / 2][2 * (kg % 2) + h] = pack2<kHalf>(w0, w1);
         }
-      // O += P V
-      const int draft = start - pos0;            // first key of the block that is draft
-      if (E4M3) {
-        uint32_t vw[4][4], vb[4];
-        const uint32_t v01 = *reinterpret_cast<const uint16_t*>(sb + 16 + 2 * q);
-        const uint32_t v23 = *reinterpret_cast<const uint16_t*>(sb + 24 + 2 * q);
-        vb[0] = v01 & 0xff;
-        vb[1] = v01 >> 8;
-        vb[2] = v23 & 0xff;
-        vb[3] = v23 >> 8;
+      }
+      // O += P V, 16 keys at a time
+      const int draft = start - pos0, last = start + s.rows - pos0;   // in the block
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          if (L::kVBytes < 16) {
-            const uint2 y = *reinterpret_cast<const uint2*>(v_src + kk * 256);
-            vw[kk][0] = y.x;
-            vw[kk][1] = y.y;
-          } else {
-            const uint4 y = *reinterpret_cast<const uint4*>(v_src + kk * 512);
-            vw[kk][0] = y.x;
-            vw[kk][1] = y.y;
-            vw[kk][2] = y.z;
-            vw[kk][3] = y.w;
-          }
-          const int key = 2 * q + (kk & 1) + 8 * (kk >> 1);
-          if (masked && vb[kk] == 255 && key >= draft) {   // draft, or past the end
-#pragma unroll
-            for (int i = 0; i < L::kVBytes / 4; ++i) vw[kk][i] = 0;
-            vb[kk] = 127;
-            if (pos0 + key < start + s.rows)
-              atomicOr(&st.bad[(key - draft) >> 5], 1u << ((key - draft) & 31));
-          }
-        }
-        const bool easy = __all_sync(0xffffffffu, easy_scale<true>(vb[0]) && easy_scale<true>(vb[1]) &&
-                                                      easy_scale<true>(vb[2]) && easy_scale<true>(vb[3]));
-        if (easy) {
-          const uint32_t m01 = (scale_mul2<true>(vb[0]) & 0xffffu) | (scale_mul2<true>(vb[1]) << 16);
-          const uint32_t m23 = (scale_mul2<true>(vb[2]) & 0xffffu) | (scale_mul2<true>(vb[3]) << 16);
-#pragma unroll
-          for (int i = 0; i < L::kVBytes / 4; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t sel = h ? 0x7362 : 0x5140;    // two codes of two keys, key by key
-              const uint2 y = scale_codes<true>(__byte_perm(vw[0][i], vw[1][i], sel), m01);
-              const uint2 z = scale_codes<true>(__byte_perm(vw[2][i], vw[3][i], sel), m23);
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) {
-                mma<true>(o[mt][4 * i + 2 * h], p[mt][0], p[mt][1], p[mt][2], p[mt][3], y.x, z.x);
-                mma<true>(o[mt][4 * i + 2 * h + 1], p[mt][0], p[mt][1], p[mt][2], p[mt][3], y.y, z.y);
-              }
-            }
-        } else {
-          if (!F16) {                            // weights in the handle's type
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                p[mt][k] = pack2<false>(x[mt][k / 2][2 * (k % 2)], x[mt][k / 2][2 * (k % 2) + 1]);
-          }
-#pragma unroll
-          for (int i = 0; i < L::kVBytes / 4; ++i) {
-            const uint4 y = pair_codes_any<F16>(vw[0][i], vb[0], vw[1][i], vb[1]);
-            const uint4 z = pair_codes_any<F16>(vw[2][i], vb[2], vw[3][i], vb[3]);
-            const uint32_t b0[4] = {y.x, y.y, y.z, y.w}, b1[4] = {z.x, z.y, z.z, z.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt)
-                mma<F16>(o[mt][4 * i + k], p[mt][0], p[mt][1], p[mt][2], p[mt][3], b0[k], b1[k]);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int cc = 0; cc < DP / 64; ++cc) {
-          uint32_t vw[4][4];
+      for (int ks = 0; ks < kGroups / 2; ++ks) {
+        if (E4M3) {
+          uint32_t vw[4][4], vb[4];
+          const uint32_t v01 = *reinterpret_cast<const uint16_t*>(sb + kBlock + 16 * ks + 2 * q);
+          const uint32_t v23 = *reinterpret_cast<const uint16_t*>(sb + kBlock + 16 * ks + 8 + 2 * q);
+          vb[0] = v01 & 0xff;
+          vb[1] = v01 >> 8;
+          vb[2] = v23 & 0xff;
+          vb[3] = v23 >> 8;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
-            uint4 y = *reinterpret_cast<const uint4*>(v_src + (kk * (DP / 64) + cc) * 512);
-            if (masked) {
-              const int key = 2 * q + (kk & 1) + 8 * (kk >> 1);
-              if (key >= draft && pos0 + key < start + s.rows && zero_nonfinite<F16>(&y))
-                atomicOr(&st.bad[(key - draft) >> 5], 1u << ((key - draft) & 31));
+            if (L::kVBytes < 16) {
+              const uint2 y = *reinterpret_cast<const uint2*>(v_src + (4 * ks + kk) * 256);
+              vw[kk][0] = y.x;
+              vw[kk][1] = y.y;
+            } else {
+              const uint4 y = *reinterpret_cast<const uint4*>(v_src + (4 * ks + kk) * 512);
+              vw[kk][0] = y.x;
+              vw[kk][1] = y.y;
+              vw[kk][2] = y.z;
+              vw[kk][3] = y.w;
             }
-            vw[kk][0] = y.x;
-            vw[kk][1] = y.y;
-            vw[kk][2] = y.z;
-            vw[kk][3] = y.w;
+            const int key = 16 * ks + 2 * q + (kk & 1) + 8 * (kk >> 1);
+            if (masked && vb[kk] == 255 && key >= draft) {   // draft, or past the end
+#pragma unroll
+              for (int i = 0; i < L::kVBytes / 4; ++i) vw[kk][i] = 0;
+              vb[kk] = 127;
+              if (key < last) atomicOr(&st.bad[(key - draft) >> 5], 1u << ((key - draft) & 31));
+            }
           }
+          const bool easy =
+              __all_sync(0xffffffffu, easy_scale<true>(vb[0]) && easy_scale<true>(vb[1]) &&
+                                          easy_scale<true>(vb[2]) && easy_scale<true>(vb[3]));
+          if (easy) {
+            const uint32_t m01 =
+                (scale_mul2<true>(vb[0]) & 0xffffu) | (scale_mul2<true>(vb[1]) << 16);
+            const uint32_t m23 =
+                (scale_mul2<true>(vb[2]) & 0xffffu) | (scale_mul2<true>(vb[3]) << 16);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < L::kVBytes / 4; ++i)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t sel = h ? 0x7632 : 0x5410;
-              const uint32_t b0 = __byte_perm(vw[0][i], vw[1][i], sel);
-              const uint32_t b1 = __byte_perm(vw[2][i], vw[3][i], sel);
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t sel = h ? 0x7362 : 0x5140;  // two codes of two keys, key by key
+                const uint2 y = scale_codes<true>(__byte_perm(vw[0][i], vw[1][i], sel), m01);
+                const uint2 z = scale_codes<true>(__byte_perm(vw[2][i], vw[3][i], sel), m23);
+                mma<true>(o[4 * i + 2 * h], p[ks][0], p[ks][1], p[ks][2], p[ks][3], y.x, z.x);
+                mma<true>(o[4 * i + 2 * h + 1], p[ks][0], p[ks][1], p[ks][2], p[ks][3], y.y, z.y);
+              }
+          } else {
+            if (!F16) {                          // weights in the handle's type
 #pragma unroll
-              for (int mt = 0; mt < MT; ++mt)
-                mma<F16>(o[mt][8 * cc + 2 * i + h], p[mt][0], p[mt][1], p[mt][2], p[mt][3], b0, b1);
+              for (int k = 0; k < 4; ++k)
+                p[ks][k] = pack2<false>(x[2 * ks + k / 2][2 * (k % 2)],
+                                        x[2 * ks + k / 2][2 * (k % 2) + 1]);
             }
+#pragma unroll
+            for (int i = 0; i < L::kVBytes / 4; ++i) {
+              const uint4 y = pair_codes_any<F16>(vw[0][i], vb[0], vw[1][i], vb[1]);
+              const uint4 z = pair_codes_any<F16>(vw[2][i], vb[2], vw[3][i], vb[3]);
+              const uint32_t b0[4] = {y.x, y.y, y.z, y.w}, b1[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma<F16>(o[4 * i + k], p[ks][0], p[ks][1], p[ks][2], p[ks][3], b0[k], b1[k]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int cc = 0; cc < DP / 64; ++cc) {
+            uint32_t vw[4][4];
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              uint4 y = *reinterpret_cast<const uint4*>(v_src + ((4 * ks + kk) * (DP / 64) + cc) * 512);
+              if (masked) {
+                const int key = 16 * ks + 2 * q + (kk & 1) + 8 * (kk >> 1);
+                if (key >= draft && key < last && zero_nonfinite<F16>(&y))
+                  atomicOr(&st.bad[(key - draft) >> 5], 1u << ((key - draft) & 31));
+              }
+              vw[kk][0] = y.x;
+              vw[kk][1] = y.y;
+              vw[kk][2] = y.z;
+              vw[kk][3] = y.w;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t sel = h ? 0x7632 : 0x5410;
+                mma<F16>(o[8 * cc + 2 * i + h], p[ks][0], p[ks][1], p[ks][2], p[ks][3],
+                         __byte_perm(vw[0][i], vw[1][i], sel), __byte_perm(vw[2][i], vw[3][i], sel));
+              }
+          }
         }
       }
     }
 
-    // the warps meet: O, m and l of the segment.  First everybody's m and l ...
+    // the warps meet: O, m and l of the segment
     const bool whole = s.whole();
     const int64_t part = 2 * blockIdx.x + (s.t0 == 0 ? 1 : 0);
-    float4* buf = reinterpret_cast<float4*>(smem + L::kBuf);
     const int live = min(L::kWarps, s.t1 - s.t0);          // warps that had a block
-    float weight[MT][2];
+    float4* buf = reinterpret_cast<float4*>(smem + L::kBuf);
+    uint16_t* out = reinterpret_cast<uint16_t*>(smem + L::kOut);
+    auto out_row = [&](int row) {
+      const int grow = s.group * L::kRows + row, nd = a.group.div(grow);
+      return (int64_t)(s.row0 + nd) * a.Hq + s.head * a.G + grow - nd * a.G;
+    };
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float sum = l[mt][h];
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        if (q == 0) st.ml[warp][16 * mt + 8 * h + g] = make_float2(mref[mt][h], sum);
-      }
+    for (int h = 0; h < 2; ++h) {
+      float sum = l[h];
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      if (q == 0) st.ml[warp][8 * h + g] = make_float2(mref[h], sum);
+    }
     __syncthreads();
-    // ... then every warp's O by its weight, half of the accumulator tiles at a time
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float top = -INFINITY;
-        for (int i = 0; i < live; ++i) top = fmaxf(top, st.ml[i][16 * mt + 8 * h + g].x);
-        weight[mt][h] = ex2(mref[mt][h] - (top == -INFINITY ? 0.f : top));
+    const bool next_live = st.live[cur ^ 1];
+    if (warp == 0 && lane < L::kRows) {          // a row a lane: m and l of all warps
+      float top = -INFINITY, sum = 0.f;
+      for (int i = 0; i < live; ++i) top = fmaxf(top, st.ml[i][lane].x);
+      const float sub = top == -INFINITY ? 0.f : top;
+      for (int i = 0; i < live; ++i) sum = fmaf(st.ml[i][lane].y, ex2(st.ml[i][lane].x - sub), sum);
+      st.fin[lane] = make_float2(sub, sum == 0.f ? 0.f : 1.f / sum);
+      if (lane < rows) {
+        if (!whole) a.part_ml[part * L::kRows + lane] = make_float2(top, sum);
+        else if (a.lse) a.lse[out_row(lane)] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
       }
+    }
+    if (next_live && warp >= kQWarp) load_q(segments[cur ^ 1]);
+    __syncthreads();
+    // every warp's O by its weight, kMerge accumulator tiles at a time
+    const float w0 = ex2(mref[0] - st.fin[g].x), w1 = ex2(mref[1] - st.fin[g + 8].x);
 #pragma unroll
-    for (int pass = 0; pass < 2; ++pass) {
+    for (int pass = 0; pass < kTiles / L::kMerge; ++pass) {
       if (warp < live) {
 #pragma unroll
         for (int k = 0; k < L::kMerge; ++k) {
-          const int tile = pass * L::kMerge + k, mt = tile / kTiles;
-          const float* v = o[mt][tile % kTiles];
+          const float* v = o[pass * L::kMerge + k];
           buf[(warp * L::kMerge + k) * 32 + lane] =
-              make_float4(v[0] * weight[mt][0], v[1] * weight[mt][0], v[2] * weight[mt][1],
-                          v[3] * weight[mt][1]);
+              make_float4(v[0] * w0, v[1] * w0, v[2] * w1, v[3] * w1);
         }
       }
       __syncthreads();
-#pragma unroll 1
-      for (int k = warp; k < L::kMerge; k += L::kWarps) {
+      if (warp < L::kMerge) {
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
         for (int i = 0; i < live; ++i) {
-          const float4 v = buf[(i * L::kMerge + k) * 32 + lane];
+          const float4 v = buf[(i * L::kMerge + warp) * 32 + lane];
           y.x += v.x;
           y.y += v.y;
           y.z += v.z;
           y.w += v.w;
         }
-        const int tile = pass * L::kMerge + k, mt = tile / kTiles;
+        const int tile = pass * L::kMerge + warp;
         if (!whole) {
           reinterpret_cast<float4*>(a.part_o + part * (L::kRows * DP))[tile * 32 + lane] = y;
         } else {
-          // as 16-bit rows in Q's place
-          uint16_t* out = reinterpret_cast<uint16_t*>(q_mem);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int row = 16 * mt + 8 * h + g;
-            float top = -INFINITY, sum = 0.f;
-            for (int i = 0; i < live; ++i) top = fmaxf(top, st.ml[i][row].x);
-            const float sub = top == -INFINITY ? 0.f : top;
-            for (int i = 0; i < live; ++i) sum = fmaf(st.ml[i][row].y, ex2(st.ml[i][row].x - sub), sum);
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            const float r0 = sum == 0.f ? 0.f : (h ? y.z : y.x) * inv;
-            const float r1 = sum == 0.f ? 0.f : (h ? y.w : y.y) * inv;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int n = 2 * q + e, ct = tile % kTiles;
-              const int d = E4M3 ? (DP / 8) * n + ct : 8 * n + ct % 8 + ct / 8 * 64;
-              out[row * DP + d] = (uint16_t)pack2<F16>(e ? r1 : r0, 0.f);
-            }
-          }
+          // l = 0: every weight was 0, and so is O
+          const float i0 = st.fin[g].y, i1 = st.fin[g + 8].y;
+          const int d0 = E4M3 ? (DP / 8) * 2 * q + tile : 16 * q + tile % 8 + tile / 8 * 64;
+          const int d1 = d0 + (E4M3 ? DP / 8 : 8);
+          out[g * DP + d0] = (uint16_t)pack2<F16>(y.x * i0, 0.f);
+          out[g * DP + d1] = (uint16_t)pack2<F16>(y.y * i0, 0.f);
+          out[(g + 8) * DP + d0] = (uint16_t)pack2<F16>(y.z * i1, 0.f);
+          out[(g + 8) * DP + d1] = (uint16_t)pack2<F16>(y.w * i1, 0.f);
         }
       }
       __syncthreads();
     }
-    if (threadIdx.x < L::kRows && (int)threadIdx.x < rows) {
-      const int row = threadIdx.x;
-      float top = -INFINITY, sum = 0.f;
-      for (int i = 0; i < live; ++i) top = fmaxf(top, st.ml[i][row].x);
-      const float sub = top == -INFINITY ? 0.f : top;
-      for (int i = 0; i < live; ++i) sum = fmaf(st.ml[i][row].y, ex2(st.ml[i][row].x - sub), sum);
-      if (!whole) {
-        a.part_ml[part * L::kRows + row] = make_float2(top, sum);
-      } else if (a.lse) {
-        const int grow = s.group * L::kRows + row, nd = a.group.div(grow);
-        a.lse[(int64_t)(s.row0 + nd) * a.Hq + s.head * a.G + grow - nd * a.G] =
-            sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-      }
-    }
     if (whole) {
       for (int i = threadIdx.x; i < rows * (DP / 8); i += L::kThreads) {
         const int row = i / (DP / 8), chunk = i % (DP / 8);
-        const int grow = s.group * L::kRows + row, nd = a.group.div(grow);
         if (chunk * 8 < a.D)
-          reinterpret_cast<uint4*>(
-              a.out + ((int64_t)(s.row0 + nd) * a.Hq + s.head * a.G + grow - nd * a.G) * a.D)[chunk] =
-              q_mem[i];
+          reinterpret_cast<uint4*>(a.out + out_row(row) * a.D)[chunk] =
+              reinterpret_cast<const uint4*>(out)[i];
       }
+    } else if (threadIdx.x == 0) {
+      a.part_of[part] = Item::part_of(s, st.share.total, a.n_cta);
     }
-    if (!whole && threadIdx.x == 0) a.part_of[part] = Item::part_of(s, st.share.total, a.n_cta);
     uint32_t any_bad = 0;
 #pragma unroll
     for (int k = 0; k < DSPARK_TREE_MAX_NODES / 32; ++k) any_bad |= st.bad[k];
     __syncthreads();
+    if (next_live && warp >= kQWarp) store_q();
     if (any_bad != 0) {
       if (threadIdx.x < L::kRows && (int)threadIdx.x < rows) {
-        const int grow = s.group * L::kRows + threadIdx.x, nd = a.group.div(grow);
+        const int nd = a.group.div(s.group * L::kRows + threadIdx.x);
         add_nonfinite<F16, E4M3, DP>(
             a, st.bad, a.mask ? a.mask + (int64_t)(s.row0 + nd) * a.mask_stride : nullptr, s.b, s.rows,
-            s.start, s.head, nd,
-            whole ? a.out + ((int64_t)(s.row0 + nd) * a.Hq + s.head * a.G + grow - nd * a.G) * a.D
-                  : nullptr,
+            s.start, s.head, nd, whole ? a.out + out_row(threadIdx.x) * a.D : nullptr,
             a.part_o + part * (L::kRows * DP), threadIdx.x);
       }
       __syncthreads();
       if (threadIdx.x < DSPARK_TREE_MAX_NODES / 32) st.bad[threadIdx.x] = 0;
     }
-    if (threadIdx.x == 0) st.live = walker.next(a, &s);
     __syncthreads();
+    cur ^= 1;
   }
   ptx::cp_async_wait_group<0>();
   if (worst > top_page) set_status(a.status, DSPARK_EPAGES);
@@ -742,10 +704,11 @@ __global__ void __launch_bounds__(Few<E4M3, DP, MT>::kThreads, 1)
 // of a block take every eighth part and are then added in order.
 constexpr int kJoinThreads = 256;
 
-template <bool F16, bool E4M3, int DP, int MT>
+template <bool F16, bool E4M3, int DP>
 __global__ void __launch_bounds__(kJoinThreads) few_join_kernel(const __grid_constant__ AttendArgs a) {
-  using Item = Work<kBlock, 16 * MT, kExtra>;
-  constexpr int kTiles = DP / 8, kRows = 16 * MT;
+  using L = Few<E4M3, DP>;
+  using Item = typename L::Item;
+  constexpr int kTiles = L::kTiles, kRows = L::kRows;
   __shared__ float4 sum_o[8][4][32];
   __shared__ float2 sum_ml[8][2][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -756,8 +719,7 @@ __global__ void __launch_bounds__(kJoinThreads) few_join_kernel(const __grid_con
   const typename Item::Request r = Item::load_request(a, of.x, &ok);
   const int rows = min(kRows, r.rows * a.G - group * kRows);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane >> 2, q = lane & 3;
-  for (int piece = (int)blockIdx.x / 2 - first; piece < MT * kTiles / 4; piece += parts) {
-    const int mt = piece * 4 / kTiles;
+  for (int piece = (int)blockIdx.x / 2 - first; piece < kTiles / 4; piece += parts) {
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     float4 o[4];
 #pragma unroll
@@ -772,7 +734,7 @@ __global__ void __launch_bounds__(kJoinThreads) few_join_kernel(const __grid_con
 #pragma unroll
       for (int k = 0; k < 4; ++k) x[k] = src[k * 32];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) ml[h] = a.part_ml[part * kRows + 16 * mt + 8 * h + g];
+      for (int h = 0; h < 2; ++h) ml[h] = a.part_ml[part * kRows + 8 * h + g];
       float wo[2], wx[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -796,10 +758,10 @@ __global__ void __launch_bounds__(kJoinThreads) few_join_kernel(const __grid_con
     for (int h = 0; h < 2; ++h) sum_ml[warp][h][lane] = make_float2(m[h], l[h]);
     __syncthreads();
     if (warp < 4) {                              // warp k finishes tile k of the piece
-      const int live = min(8, parts), tile = (piece * 4 + warp) % kTiles;
+      const int live = min(8, parts), tile = piece * 4 + warp;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int row = 16 * mt + 8 * h + g;
+        const int row = 8 * h + g;
         if (row >= rows) continue;
         float top = -INFINITY;
         for (int i = 0; i < live; ++i) top = fmaxf(top, sum_ml[i][h][lane].x);
@@ -822,7 +784,7 @@ __global__ void __launch_bounds__(kJoinThreads) few_join_kernel(const __grid_con
           if (d < a.D)
             a.out[out_row * a.D + d] = sum == 0.f ? 0 : (uint16_t)pack2<F16>(y[e] * inv, 0.f);
         }
-        if (piece % (kTiles / 4) == 0 && warp == 0 && q == 0 && a.lse)
+        if (tile == 0 && q == 0 && a.lse)
           a.lse[out_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
       }
     }
@@ -830,10 +792,10 @@ __global__ void __launch_bounds__(kJoinThreads) few_join_kernel(const __grid_con
   }
 }
 
-template <bool F16, bool E4M3, int DP, int MT>
+template <bool F16, bool E4M3, int DP>
 cudaError_t launch(const AttendArgs& a, cudaStream_t stream) {
-  using L = Few<E4M3, DP, MT>;
-  few_kernel<F16, E4M3, DP, MT><<<a.n_cta, L::kThreads, L::kSmem, stream>>>(a);
+  using L = Few<E4M3, DP>;
+  few_kernel<F16, E4M3, DP><<<a.n_cta, L::kThreads, L::kSmem, stream>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // the join may be set up while the main kernel runs; it waits for it itself
@@ -846,49 +808,44 @@ cudaError_t launch(const AttendArgs& a, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, few_join_kernel<F16, E4M3, DP, MT>, a);
+  return cudaLaunchKernelEx(&cfg, few_join_kernel<F16, E4M3, DP>, a);
 }
 
-template <bool F16, bool E4M3, int DP, int MT>
+template <bool F16, bool E4M3, int DP>
 cudaError_t setup() {
-  using L = Few<E4M3, DP, MT>;
-  static_assert(L::kSmem + sizeof(FewState) + 256 <= 232448, "shared memory of an SM");
-  cudaError_t e = cudaFuncSetAttribute(few_kernel<F16, E4M3, DP, MT>,
+  using L = Few<E4M3, DP>;
+  static_assert(L::kSmem + sizeof(FewState) + 512 <= 232448, "shared memory of an SM");
+  cudaError_t e = cudaFuncSetAttribute(few_kernel<F16, E4M3, DP>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (e != cudaSuccess) return e;
   // the main kernel's split of shared memory and L1: another would have the SMs
   // drained and set up anew between the two
-  return cudaFuncSetAttribute(few_join_kernel<F16, E4M3, DP, MT>,
+  return cudaFuncSetAttribute(few_join_kernel<F16, E4M3, DP>,
                               cudaFuncAttributePreferredSharedMemoryCarveout,
                               cudaSharedmemCarveoutMaxShared);
 }
 
 template <bool F16, int DP>
-cudaError_t setup_all() {
-  cudaError_t e = setup<F16, false, DP, 1>();
-  if (e == cudaSuccess) e = setup<F16, false, DP, 2>();
-  if (e == cudaSuccess) e = setup<F16, true, DP, 1>();
-  if (e == cudaSuccess) e = setup<F16, true, DP, 2>();
-  return e;
+cudaError_t setup_both() {
+  const cudaError_t e = setup<F16, false, DP>();
+  return e != cudaSuccess ? e : setup<F16, true, DP>();
 }
 
 template <bool F16, bool E4M3>
-cudaError_t launch_for(const AttendArgs& a, int tiles, cudaStream_t stream) {
-  if (padded_dim(a.D) == 64)
-    return tiles == 1 ? launch<F16, E4M3, 64, 1>(a, stream) : launch<F16, E4M3, 64, 2>(a, stream);
-  return tiles == 1 ? launch<F16, E4M3, 128, 1>(a, stream) : launch<F16, E4M3, 128, 2>(a, stream);
+cudaError_t launch_for(const AttendArgs& a, cudaStream_t stream) {
+  return padded_dim(a.D) == 64 ? launch<F16, E4M3, 64>(a, stream) : launch<F16, E4M3, 128>(a, stream);
 }
 
 }  // namespace
 
 cudaError_t few_setup(bool f16, int D) {
-  if (padded_dim(D) == 64) return f16 ? setup_all<true, 64>() : setup_all<false, 64>();
-  return f16 ? setup_all<true, 128>() : setup_all<false, 128>();
+  if (padded_dim(D) == 64) return f16 ? setup_both<true, 64>() : setup_both<false, 64>();
+  return f16 ? setup_both<true, 128>() : setup_both<false, 128>();
 }
 
-cudaError_t few_launch(const AttendArgs& a, int tiles, bool f16, bool e4m3, cudaStream_t stream) {
-  if (f16) return e4m3 ? launch_for<true, true>(a, tiles, stream) : launch_for<true, false>(a, tiles, stream);
-  return e4m3 ? launch_for<false, true>(a, tiles, stream) : launch_for<false, false>(a, tiles, stream);
+cudaError_t few_launch(const AttendArgs& a, bool f16, bool e4m3, cudaStream_t stream) {
+  if (f16) return e4m3 ? launch_for<true, true>(a, stream) : launch_for<true, false>(a, stream);
+  return e4m3 ? launch_for<false, true>(a, stream) : launch_for<false, false>(a, stream);
 }
 
 }  // namespace tree

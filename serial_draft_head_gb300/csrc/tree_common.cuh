@@ -207,10 +207,9 @@ struct TileMaps {
   int rows;
 };
 
-// attend_few: at most 32 rows a cached head, on mma.sync (tree_attend_few.cu).
-// `tiles`: 1 or 2 row tiles of 16.
+// At most 16 rows a cached head, on mma.sync (tree_attend_few.cu).
 cudaError_t few_setup(bool f16, int D);
-cudaError_t few_launch(const AttendArgs& a, int tiles, bool f16, bool e4m3, cudaStream_t stream);
+cudaError_t few_launch(const AttendArgs& a, bool f16, bool e4m3, cudaStream_t stream);
 
 cudaError_t attend_setup(bool f16, int D);
 cudaError_t attend_launch(const AttendArgs& a, const TileMaps& maps, bool f16, bool e4m3,
