@@ -56,8 +56,10 @@ struct Few {
   static constexpr int kQ = kWarps * kRing;
   static constexpr int kOut = kQ;                        // the result in Q's place: [rows][DP]
   static constexpr int kBuf = kQ + kRows * DP * 2;       // [warp][kMerge][lane] float4
-  static constexpr int kScales = kBuf + kWarps * kMerge * 512;   // [warp][stage][K, V][key]
-  static constexpr int kSmem = kScales + kWarps * kStages * 2 * kBlock;
+  // the scales of a stage: K's as bf16, V's as f16 (0 where it is none) and as bytes
+  static constexpr int kScaleBytes = E4M3 ? 5 * kBlock : 0;
+  static constexpr int kScales = kBuf + kWarps * kMerge * 512;   // [warp][stage]
+  static constexpr int kSmem = kScales + kWarps * kStages * kScaleBytes;
   using Item = Work<kBlock, kRows, kExtra>;
 };
 
@@ -101,13 +103,6 @@ __device__ __noinline__ uint4 pair_codes_any(uint32_t wa, uint32_t byte_a, uint3
                     __byte_perm(x.y, y.y, 0x5410), __byte_perm(x.y, y.y, 0x7632));
 }
 
-// Four codes as f16.
-__device__ __forceinline__ uint2 codes_f16(uint32_t w) {
-  const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
-  const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
-  const __half2 x(lo), y(hi);
-  return make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-}
 
 // Adds to a row's result, written by this warp, the non-finite elements of the
 // draft rows of V that it sees: 16-bit values (out), or the part's accumulators.
@@ -214,7 +209,7 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane >> 2, q = lane & 3;
   uint8_t* ring = smem + warp * L::kRing;
   uint4* q_mem = reinterpret_cast<uint4*>(smem + L::kQ);
-  uint8_t* scales = smem + L::kScales + warp * L::kStages * 2 * kBlock;
+  uint8_t* scales = smem + L::kScales + warp * L::kStages * L::kScaleBytes;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x < 2) a.part_of[2 * blockIdx.x + threadIdx.x] = make_int4(0, 0, 0, 0);
   if (threadIdx.x < DSPARK_TREE_MAX_NODES / 32) st.bad[threadIdx.x] = 0;
@@ -234,12 +229,18 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
   };
   look();
   int stage_in = 0, scale_stage = -1;
-  uint32_t k_byte = 0, v_byte = 0;
+  uint32_t k_byte = 0, v_byte = 0, easy_stages = 0;     // bit: all of V's scales in the stage are easy
   auto issue = [&]() {
     // the scales of the block before have landed: lane = key
     if (E4M3 && scale_stage >= 0) {
-      scales[scale_stage * 2 * kBlock + lane] = (uint8_t)k_byte;
-      scales[scale_stage * 2 * kBlock + kBlock + lane] = (uint8_t)v_byte;
+      uint8_t* sb = scales + scale_stage * L::kScaleBytes;
+      reinterpret_cast<uint16_t*>(sb)[lane] = (uint16_t)(k_byte << 7);
+      const bool easy = easy_scale<true>(v_byte);
+      reinterpret_cast<uint16_t*>(sb + 2 * kBlock)[lane] =
+          (uint16_t)(easy ? scale_mul2<true>(v_byte) : 0u);
+      sb[4 * kBlock + lane] = (uint8_t)v_byte;
+      easy_stages = easy_stages & ~(1u << scale_stage) |
+                    (__all_sync(0xffffffffu, easy) ? 1u << scale_stage : 0u);
     }
     scale_stage = -1;
     if (c.more) {
@@ -258,9 +259,27 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
       c.next(a, warp, L::kWarps);
       look();
       uint8_t* dst = ring + stage_in * L::kStage + lane * 16;
-      const Rows& kr = a.c.x[0];
+      const Rows &kr = a.c.x[0], &vr = a.c.x[1];
       const uint8_t* k = kr.of_head(head) + q * 16;
-      if (even) k += kr.offset(pg, slot + g);
+      const uint8_t* v = vr.of_head(head) + g * (L::kVBytes < 16 ? 8 : 16);
+      if (even) {
+        k += kr.offset(pg, slot + g);
+        v += vr.offset(pg, slot + 2 * q);
+      }
+      if (even && full && a.D == DP && L::kVBytes >= 16) {       // the common case, no predicates
+#pragma unroll
+        for (int kg = 0; kg < kGroups; ++kg)
+#pragma unroll
+          for (int i = 0; i < L::kKCopies; ++i)
+            ptx::cp_async16(dst + (kg * L::kKCopies + i) * 512,
+                            k + (uint64_t)(8 * kg) * kr.slot + i * 64);
+#pragma unroll
+        for (int kk = 0; kk < kBlock / 4; ++kk)
+#pragma unroll
+          for (int i = 0; i < L::kVBytes / 16; ++i)
+            ptx::cp_async16(dst + L::kVPart + (kk * (L::kVBytes / 16) + i) * 512,
+                            v + (uint64_t)((kk & 1) + 8 * (kk >> 1)) * vr.slot + i * 128);
+      } else {
 #pragma unroll
       for (int kg = 0; kg < kGroups; ++kg) {
         const uint8_t* src;
@@ -276,9 +295,6 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
           ptx::cp_async16_or_zero(dst + (kg * L::kKCopies + i) * 512, src + i * 64,
                                   on && (4 * i + q) * 16 < a.D * (E4M3 ? 1 : 2));
       }
-      const Rows& vr = a.c.x[1];
-      const uint8_t* v = vr.of_head(head) + g * (L::kVBytes < 16 ? 8 : 16);
-      if (even) v += vr.offset(pg, slot + 2 * q);
 #pragma unroll
       for (int kk = 0; kk < kBlock / 4; ++kk) {
         const int off = (kk & 1) + 8 * (kk >> 1), key = 2 * q + off;
@@ -300,6 +316,7 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
                                     src + i * 128,
                                     on && (g + 8 * i) * 16 < a.D * (E4M3 ? 1 : 2));
         }
+      }
       }
     }
     ptx::cp_async_commit();
@@ -388,7 +405,8 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
       ptx::cp_async_wait_group<L::kStages - 1>();
       __syncwarp();
       const uint8_t* src = ring + stage * L::kStage + lane * 16;
-      const uint8_t* sb = scales + stage * 2 * kBlock;
+      const uint8_t* sb = scales + stage * L::kScaleBytes;
+      const bool easy = !E4M3 || easy_stages >> stage & 1;
       const uint8_t* v_src = ring + stage * L::kStage + L::kVPart +
                              lane * (L::kVBytes < 16 ? 8 : 16);
       if (++stage == L::kStages) stage = 0;
@@ -414,8 +432,8 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
 #pragma unroll
           for (int kg = 0; kg < kGroups; ++kg) {
             if (E4M3) {
-              b0[kg] = codes_f16(hc ? kc[kg].z : kc[kg].x);
-              b1[kg] = codes_f16(hc ? kc[kg].w : kc[kg].y);
+              b0[kg] = e4m3x4_to_f16(hc ? kc[kg].z : kc[kg].x);
+              b1[kg] = e4m3x4_to_f16(hc ? kc[kg].w : kc[kg].y);
             } else {
               b0[kg] = make_uint2(kc[kg].x, kc[kg].y);
               b1[kg] = make_uint2(kc[kg].z, kc[kg].w);
@@ -429,36 +447,44 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
             mma<kHalf>(x[kg], qa.z, qb.z, qa.w, qb.w, b1[kg].x, b1[kg].y);
         }
       }
-      // exponents, and whether a row's m has to move
-      uint32_t see[2] = {0xffffffffu, 0xffffffffu};
+      // scores by K's scales (x times row_mul is the exponent), invisible ones -infinity
+      if (E4M3) {
+#pragma unroll
+        for (int kg = 0; kg < kGroups; ++kg) {
+          const uint32_t k01 = reinterpret_cast<const uint32_t*>(sb)[4 * kg + q];
+          const float s0 = __uint_as_float(k01 << 16), s1 = __uint_as_float(k01 & 0xffff0000u);
+          x[kg][0] *= s0;
+          x[kg][1] *= s1;
+          x[kg][2] *= s0;
+          x[kg][3] *= s1;
+        }
+      }
       if (masked) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int row = 8 * h + g;
           const int nd = a.group.div(s.group * L::kRows + (row < rows ? row : 0));
-          see[h] = sees_32(a.mask ? a.mask + (int64_t)(s.row0 + nd) * a.mask_stride : nullptr,
-                           s.rows, nd, pos0 - start) >> (2 * q);
+          const uint32_t see =
+              sees_32(a.mask ? a.mask + (int64_t)(s.row0 + nd) * a.mask_stride : nullptr, s.rows,
+                      nd, pos0 - start) >> (2 * q);
+#pragma unroll
+          for (int kg = 0; kg < kGroups; ++kg)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (!((see >> (8 * kg + e)) & 1)) x[kg][2 * h + e] = -INFINITY;
         }
       }
-      float mx[2] = {-INFINITY, -INFINITY};
+      float mx[2];
 #pragma unroll
-      for (int kg = 0; kg < kGroups; ++kg) {
-        float ks[2] = {1.f, 1.f};                // K's scales of keys 2q, 2q + 1 of the group
-        if (E4M3) {
-          const uint32_t k01 = *reinterpret_cast<const uint16_t*>(sb + 8 * kg + 2 * q);
-          ks[0] = __uint_as_float((k01 & 0xff) << 23);
-          ks[1] = __uint_as_float((k01 >> 8) << 23);
-        }
+      for (int h = 0; h < 2; ++h) {
+        mx[h] = fmaxf(x[0][2 * h], x[0][2 * h + 1]);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float& v = x[kg][2 * h + e];
-            v *= E4M3 ? row_mul[h] * ks[e] : row_mul[h];
-            if (cap) v = capped(sc, v);
-            if (!masked || (see[h] >> (8 * kg + e)) & 1) mx[h] = fmaxf(mx[h], v);
-          }
+        for (int kg = 1; kg < kGroups; ++kg)
+          mx[h] = fmaxf(mx[h], fmaxf(x[kg][2 * h], x[kg][2 * h + 1]));
+        mx[h] = mx[h] == -INFINITY ? -INFINITY : mx[h] * row_mul[h];
+        if (cap && mx[h] != -INFINITY) mx[h] = capped(sc, mx[h]);
       }
+      // the first visible key sets a row's m, later ones when the maximum has grown enough
       const bool over = mx[0] > mref[0] + (mref[0] == -INFINITY ? 0.f : kShift + 8.f) ||
                         mx[1] > mref[1] + (mref[1] == -INFINITY ? 0.f : kShift + 8.f);
       if (__any_sync(0xffffffffu, over)) {
@@ -484,15 +510,26 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const float sub = mref[h] == -INFINITY ? 0.f : mref[h];
+        if (cap) {
+#pragma unroll
+          for (int kg = 0; kg < kGroups; ++kg)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float& v = x[kg][2 * h + e];
+              v = v == -INFINITY ? v : capped(sc, v * row_mul[h]) - sub;
+            }
+        } else {
+#pragma unroll
+          for (int kg = 0; kg < kGroups; ++kg)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              x[kg][2 * h + e] = fmaf(x[kg][2 * h + e], row_mul[h], -sub);
+        }
 #pragma unroll
         for (int kg = 0; kg < kGroups; ++kg) {
           float &w0 = x[kg][2 * h], &w1 = x[kg][2 * h + 1];
-          w0 = ex2(w0 - sub);
-          w1 = ex2(w1 - sub);
-          if (masked) {
-            w0 = (see[h] >> (8 * kg)) & 1 ? w0 : 0.f;
-            w1 = (see[h] >> (8 * kg + 1)) & 1 ? w1 : 0.f;
-          }
+          w0 = ex2(w0);
+          w1 = ex2(w1);
           l[h] += w0 + w1;
           p[kg / 2][2 * (kg % 2) + h] = pack2<kHalf>(w0, w1);
         }
@@ -502,13 +539,7 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
 #pragma unroll
       for (int ks = 0; ks < kGroups / 2; ++ks) {
         if (E4M3) {
-          uint32_t vw[4][4], vb[4];
-          const uint32_t v01 = *reinterpret_cast<const uint16_t*>(sb + kBlock + 16 * ks + 2 * q);
-          const uint32_t v23 = *reinterpret_cast<const uint16_t*>(sb + kBlock + 16 * ks + 8 + 2 * q);
-          vb[0] = v01 & 0xff;
-          vb[1] = v01 >> 8;
-          vb[2] = v23 & 0xff;
-          vb[3] = v23 >> 8;
+          uint32_t vw[4][4];
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             if (L::kVBytes < 16) {
@@ -522,22 +553,10 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
               vw[kk][2] = y.z;
               vw[kk][3] = y.w;
             }
-            const int key = 16 * ks + 2 * q + (kk & 1) + 8 * (kk >> 1);
-            if (masked && vb[kk] == 255 && key >= draft) {   // draft, or past the end
-#pragma unroll
-              for (int i = 0; i < L::kVBytes / 4; ++i) vw[kk][i] = 0;
-              vb[kk] = 127;
-              if (key < last) atomicOr(&st.bad[(key - draft) >> 5], 1u << ((key - draft) & 31));
-            }
           }
-          const bool easy =
-              __all_sync(0xffffffffu, easy_scale<true>(vb[0]) && easy_scale<true>(vb[1]) &&
-                                          easy_scale<true>(vb[2]) && easy_scale<true>(vb[3]));
           if (easy) {
-            const uint32_t m01 =
-                (scale_mul2<true>(vb[0]) & 0xffffu) | (scale_mul2<true>(vb[1]) << 16);
-            const uint32_t m23 =
-                (scale_mul2<true>(vb[2]) & 0xffffu) | (scale_mul2<true>(vb[3]) << 16);
+            const uint32_t* sv = reinterpret_cast<const uint32_t*>(sb + 2 * kBlock) + 8 * ks + q;
+            const uint32_t m01 = sv[0], m23 = sv[4];
 #pragma unroll
             for (int i = 0; i < L::kVBytes / 4; ++i)
 #pragma unroll
@@ -549,6 +568,18 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
                 mma<true>(o[4 * i + 2 * h + 1], p[ks][0], p[ks][1], p[ks][2], p[ks][3], y.y, z.y);
               }
           } else {
+            uint32_t vb[4];
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              const int key = 16 * ks + 2 * q + (kk & 1) + 8 * (kk >> 1);
+              vb[kk] = sb[4 * kBlock + key];
+              if (masked && vb[kk] == 255 && key >= draft) {   // draft, or past the end
+#pragma unroll
+                for (int i = 0; i < L::kVBytes / 4; ++i) vw[kk][i] = 0;
+                vb[kk] = 127;
+                if (key < last) atomicOr(&st.bad[(key - draft) >> 5], 1u << ((key - draft) & 31));
+              }
+            }
             if (!F16) {                          // weights in the handle's type
 #pragma unroll
               for (int k = 0; k < 4; ++k)

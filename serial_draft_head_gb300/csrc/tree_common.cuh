@@ -122,6 +122,18 @@ __device__ __forceinline__ float saturate16(float x) {
   return fabsf(x) > top ? copysignf(top, x) : x;
 }
 
+// Four e4m3 codes as f16, exactly.
+__device__ __forceinline__ uint2 e4m3x4_to_f16(uint32_t w) {
+  uint2 r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "mov.b32 {lo, hi}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+      : "=r"(r.x), "=r"(r.y)
+      : "r"(w));
+  return r;
+}
+
 // Two e4m3 codes to floats.
 __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t codes) {
   const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
@@ -138,10 +150,10 @@ template <bool F16>
 __device__ __forceinline__ uint2 scale_codes(uint32_t w, uint32_t mul2) {
   uint2 r;
   if (F16) {
-    const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
-    const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
+    const uint2 c = e4m3x4_to_f16(w);
     const __half2 m = *reinterpret_cast<const __half2*>(&mul2);
-    const __half2 x = __hmul2(__half2(lo), m), y = __hmul2(__half2(hi), m);
+    const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&c.x), m);
+    const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&c.y), m);
     r.x = *reinterpret_cast<const uint32_t*>(&x);
     r.y = *reinterpret_cast<const uint32_t*>(&y);
   } else {
