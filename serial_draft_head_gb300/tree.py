@@ -14,11 +14,12 @@ handle are ordered by the caller, and a call given `stream` works on that
 stream: its inputs have to be ready there.  There is no fallback.
 """
 import ctypes
+import struct
 
 import torch
 
 from . import walk
-from .walk import OK, WalkError, _check  # noqa: F401
+from .walk import WalkError, _check
 
 TYPE_BF16 = 0
 TYPE_F16 = 1
@@ -55,6 +56,11 @@ class dspark_tree_batch(ctypes.Structure):
                 ("pages_stride", ctypes.c_int64), ("max_pages", ctypes.c_int), ("B", ctypes.c_int),
                 ("N", ctypes.c_int)]
 
+
+_pack_batch = struct.Struct("@PPPqiii").pack_into      # dspark_tree_batch
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") \
+    else lambda index: torch.cuda.current_stream(index).cuda_stream
+_int32 = torch.int32
 
 _lib = None
 
@@ -113,6 +119,7 @@ class KVCache:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.device, self.dtype = k.device, k.dtype
         self.kv_heads, self.head_dim = k.shape[2], k.shape[3]
+        self.key = (k.get_device(), self.kv_heads, self.head_dim, self.dtype)
         self.c = c
         self.ref = ctypes.byref(c)
 
@@ -148,6 +155,9 @@ class Tree:
         _need(dtype in (torch.bfloat16, torch.float16), "rows are bf16 or f16")
         self.device = torch.device("cuda", torch.cuda.current_device()) if device is None \
             else torch.device(device)
+        _need(self.device.type == "cuda", "the handle's device is a CUDA device")
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
         self.q_heads, self.kv_heads, self.head_dim, self.dtype = q_heads, kv_heads, head_dim, dtype
         cfg = dspark_tree_config(q_heads, kv_heads, head_dim, _TYPES[dtype], max_requests,
                                  max_nodes)
@@ -157,49 +167,59 @@ class Tree:
             _check(self.lib.dspark_tree_create(ctypes.byref(cfg), ctypes.byref(h)),
                    "dspark_tree_create")
         self.h = h.value
+        self._index = self.device.index
+        self._key = (self._index, kv_heads, head_dim, dtype)
+        self._key_e4m3 = (self._index, kv_heads, head_dim, torch.float8_e4m3fn)
+        self._scale = head_dim ** -0.5
         self._batch = dspark_tree_batch()
+        self._batch_mem = (ctypes.c_char * ctypes.sizeof(self._batch)).from_buffer(self._batch)
         self._batch_ref = ctypes.byref(self._batch)
+        self._s0, self._s1 = _i64x2(), _i64x2()
 
-    # ---- argument marshalling ----
+    # ---- argument marshalling: a few microseconds a call matter here ----
 
     def _cache(self, cache):
-        _need(cache.device == self.device and cache.kv_heads == self.kv_heads
-              and cache.head_dim == self.head_dim
-              and cache.dtype in (self.dtype, torch.float8_e4m3fn),
-              "the cache has the handle's device, heads, head_dim and type (or e4m3)")
+        if cache.key != self._key and cache.key != self._key_e4m3:
+            raise ValueError("the cache has the handle's device, heads, head_dim and type (or e4m3)")
         return cache.ref
 
-    def _ints(self, t, dim, what):
-        _need(t.dtype == torch.int32 and t.device == self.device and t.dim() == dim
-              and (t.stride(dim - 1) == 1 or t.shape[dim - 1] <= 1), what)
-        return t.data_ptr()
-
     def _requests(self, pages, start, first, n_rows):
-        b = self._batch
-        b.pages = self._ints(pages, 2, "pages is int32 [B, P] on the handle's device")
-        b.start = self._ints(start, 1, "lengths are int32 [B] on the handle's device")
-        b.B, b.max_pages = pages.shape
-        b.pages_stride = pages.stride(0)
-        _need(start.shape[0] == b.B, "pages and lengths have one row a request")
+        i = self._index
+        if not (pages.dtype is _int32 and pages.get_device() == i and pages.dim() == 2
+                and start.dtype is _int32 and start.get_device() == i and start.dim() == 1):
+            raise ValueError("pages is int32 [B, P] and lengths int32 [B], on the handle's device")
+        B, width = pages.shape
+        row, one = pages.stride()
+        if (one != 1 and width > 1) or start.shape[0] != B or (B > 1 and start.stride(0) != 1):
+            raise ValueError("pages and lengths have one row a request, entries next to each other")
+        f = 0
         if first is not None:
-            b.first = self._ints(first, 1, "first is int32 [B + 1] on the handle's device")
-            _need(first.shape[0] == b.B + 1, "first has B + 1 entries")
-        b.N = n_rows
+            if not (first.dtype is _int32 and first.get_device() == i and first.dim() == 1
+                    and first.shape[0] == B + 1 and (B == 0 or first.stride(0) == 1)):
+                raise ValueError("first is int32 [B + 1] on the handle's device")
+            f = first.data_ptr()
+        _pack_batch(self._batch_mem, 0, pages.data_ptr(), start.data_ptr(), f, row, width, B, n_rows)
         return self._batch_ref
 
-    def _rows(self, t, heads, what):
-        _need(t.dtype == self.dtype and t.device == self.device and t.dim() == 3
-              and t.shape[1] == heads and t.shape[2] == self.head_dim and t.stride(2) == 1, what)
-        return _i64x2(t.stride(0), t.stride(1))
+    def _rows(self, t, heads, strides, what):
+        if not (t.dtype is self.dtype and t.get_device() == self._index and t.dim() == 3):
+            raise ValueError(what)
+        n, h, d = t.shape
+        s0, s1, s2 = t.stride()
+        if h != heads or d != self.head_dim or (s2 != 1 and d > 1):
+            raise ValueError(what)
+        strides[0], strides[1] = s0, s1
+        return n
 
     def _out(self, t, shape, dtype, what):
-        _need(t.dtype == dtype and t.device == self.device and tuple(t.shape) == shape
-              and t.is_contiguous(), what)
+        if not (t.dtype is dtype and t.get_device() == self._index and t.shape == shape
+                and t.is_contiguous()):
+            raise ValueError(what)
         return t
 
     def _stream(self, stream):
         if stream is None:
-            return torch.cuda.current_stream(self.device).cuda_stream
+            return _raw_stream(self._index)
         return walk._stream(stream)
 
     def _empty(self, shape, dtype, stream):
@@ -213,35 +233,48 @@ class Tree:
 
     def write(self, cache, pages, start, first, k, v, stream=None):
         """Rows first[b] + i of k and v [N, kv_heads, head_dim] to positions start[b] + i."""
-        ks = self._rows(k, self.kv_heads, "k is [N, kv_heads, head_dim] of the handle's type")
-        vs = self._rows(v, self.kv_heads, "v is [N, kv_heads, head_dim] of the handle's type")
-        _need(k.shape[0] == v.shape[0], "k and v have as many rows")
-        _check(self.lib.dspark_tree_write(
-            self.h, self._cache(cache), self._requests(pages, start, first, k.shape[0]),
-            k.data_ptr(), ks, v.data_ptr(), vs, self._stream(stream)), "dspark_tree_write")
+        n = self._rows(k, self.kv_heads, self._s0, "k is [N, kv_heads, head_dim] of the handle's type")
+        if self._rows(v, self.kv_heads, self._s1,
+                      "v is [N, kv_heads, head_dim] of the handle's type") != n:
+            raise ValueError("k and v have as many rows")
+        rc = self.lib.dspark_tree_write(
+            self.h, self._cache(cache), self._requests(pages, start, first, n), k.data_ptr(),
+            self._s0, v.data_ptr(), self._s1, self._stream(stream))
+        if rc:
+            raise WalkError(rc, "dspark_tree_write")
 
     def read(self, cache, pages, start, first, n_rows, out=None, stream=None):
         """Positions start[b] + i to rows first[b] + i of (k, v) [n_rows, kv_heads, head_dim]."""
         shape = (n_rows, self.kv_heads, self.head_dim)
         if out is None:
-            out = tuple(self._empty(shape, self.dtype, stream) for _ in range(2))
-        k, v = (self._out(t, shape, self.dtype, "out is two contiguous [n_rows, kv_heads, "
-                          "head_dim] tensors of the handle's type") for t in out)
-        _check(self.lib.dspark_tree_read(
-            self.h, self._cache(cache), self._requests(pages, start, first, n_rows),
-            k.data_ptr(), v.data_ptr(), self._stream(stream)), "dspark_tree_read")
+            k, v = self._empty(shape, self.dtype, stream), self._empty(shape, self.dtype, stream)
+        else:
+            k, v = (self._out(t, shape, self.dtype, "out is two contiguous [n_rows, kv_heads, "
+                              "head_dim] tensors of the handle's type") for t in out)
+        rc = self.lib.dspark_tree_read(
+            self.h, self._cache(cache), self._requests(pages, start, first, n_rows), k.data_ptr(),
+            v.data_ptr(), self._stream(stream))
+        if rc:
+            raise WalkError(rc, "dspark_tree_read")
         return k, v
 
     def keep(self, cache, pages, start, path, count, stream=None):
         """Position start[b] + path[b, i] moves to start[b] + i for i < count[b]; path int32
         [B, P'], strictly ascending in its first count[b] entries."""
-        p = self._ints(path, 2, "path is int32 [B, n] on the handle's device")
-        c = self._ints(count, 1, "count is int32 [B] on the handle's device")
+        i = self._index
+        if not (path.dtype is _int32 and path.get_device() == i and path.dim() == 2
+                and count.dtype is _int32 and count.get_device() == i and count.dim() == 1):
+            raise ValueError("path is int32 [B, n] and count int32 [B], on the handle's device")
         batch = self._requests(pages, start, None, 0)
-        _need(path.shape[0] == count.shape[0] == pages.shape[0], "one path and count a request")
-        _check(self.lib.dspark_tree_keep(
-            self.h, self._cache(cache), batch, p, path.stride(0),
-            path.shape[1], c, self._stream(stream)), "dspark_tree_keep")
+        n, width = path.shape
+        row, one = path.stride()
+        if not (n == count.shape[0] == pages.shape[0] and (one == 1 or width <= 1)
+                and (n <= 1 or count.stride(0) == 1)):
+            raise ValueError("one path and count a request, entries next to each other")
+        rc = self.lib.dspark_tree_keep(self.h, self._cache(cache), batch, path.data_ptr(), row, width,
+                                       count.data_ptr(), self._stream(stream))
+        if rc:
+            raise WalkError(rc, "dspark_tree_keep")
 
     def attend(self, q, cache, pages, length, first, mask=None, scale=None, softcap=0.0, out=None,
                lse=None, stream=None):
@@ -249,22 +282,31 @@ class Tree:
         length[b] + T_b - 1 of their requests.  mask int32 [N, words] (see `ancestor_bits`) or
         None for chains.  scale: 1 / sqrt(head_dim) unless given.  softcap c > 0: scores become
         c tanh(s / c).  Returns (out [N, q_heads, head_dim], lse float32 [N, q_heads])."""
-        qs = self._rows(q, self.q_heads, "q is [N, q_heads, head_dim] of the handle's type")
-        n = q.shape[0]
-        out = self._empty(q.shape, self.dtype, stream) if out is None else \
-            self._out(out, tuple(q.shape), self.dtype, "out is like q, contiguous")
-        lse = self._empty((n, self.q_heads), torch.float32, stream) if lse is None else \
+        n = self._rows(q, self.q_heads, self._s0, "q is [N, q_heads, head_dim] of the handle's type")
+        shape = q.shape
+        if out is None:
+            out = self._empty(shape, self.dtype, stream)
+        else:
+            self._out(out, shape, self.dtype, "out is like q, contiguous")
+        if lse is None:
+            lse = self._empty((n, self.q_heads), torch.float32, stream)
+        else:
             self._out(lse, (n, self.q_heads), torch.float32, "lse is float32 [N, q_heads]")
         m, ms, mw = None, 0, 0
         if mask is not None:
-            m = self._ints(mask, 2, "mask is int32 [N, words] on the handle's device")
-            _need(mask.shape[0] == n, "mask has a row for every row of q")
-            mw = mask.shape[1]
-            ms = mask.stride(0)
-        _check(self.lib.dspark_tree_attend(
-            self.h, self._cache(cache), self._requests(pages, length, first, n), q.data_ptr(), qs,
-            m, ms, mw, self.head_dim ** -0.5 if scale is None else scale, softcap,
-            out.data_ptr(), lse.data_ptr(), self._stream(stream)), "dspark_tree_attend")
+            if not (mask.dtype is _int32 and mask.get_device() == self._index and mask.dim() == 2
+                    and mask.shape[0] == n):
+                raise ValueError("mask is int32 [N, words] on the handle's device")
+            m, mw = mask.data_ptr(), mask.shape[1]
+            ms, one = mask.stride()
+            if one != 1 and mw > 1:
+                raise ValueError("a mask row's words lie next to each other")
+        rc = self.lib.dspark_tree_attend(
+            self.h, self._cache(cache), self._requests(pages, length, first, n), q.data_ptr(),
+            self._s0, m, ms, mw, self._scale if scale is None else scale, softcap, out.data_ptr(),
+            lse.data_ptr(), self._stream(stream))
+        if rc:
+            raise WalkError(rc, "dspark_tree_attend")
         return out, lse
 
     def status(self, stream=None):

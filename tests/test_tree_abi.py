@@ -78,3 +78,12 @@ def test_ancestor_bits():
         assert bits == [1 if j <= i else 0 for j in range(96)]
     with pytest.raises(ValueError):
         tree.ancestor_bits(torch.tensor([0], dtype=torch.int32), first[:1].new_tensor([0, 1]))
+
+
+def test_batch_is_packed_as_the_struct_lies():
+    from serial_draft_head_gb300 import tree
+    b = tree.dspark_tree_batch()
+    mem = (ctypes.c_char * ctypes.sizeof(b)).from_buffer(b)
+    tree._pack_batch(mem, 0, 11, 12, 13, -14, 15, 16, 17)
+    assert (b.pages, b.start, b.first, b.pages_stride, b.max_pages, b.B, b.N) == \
+        (11, 12, 13, -14, 15, 16, 17)
