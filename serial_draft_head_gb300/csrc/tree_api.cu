@@ -15,7 +15,7 @@ struct dspark_tree {
   int device = 0;
   int sm_count = 0;
   dspark_tree_config cfg{};
-  int* status = nullptr;
+  int* status = nullptr;          // and after it a count a SM (AttendArgs::arrived)
   void* parts = nullptr;          // attend's workspace
   float* part_o = nullptr;
   float2* part_ml = nullptr;
@@ -162,9 +162,9 @@ int dspark_tree_create(const dspark_tree_config* cfg, dspark_tree_t* out) {
     h->part_o = reinterpret_cast<float*>(p);
     h->part_ml = reinterpret_cast<float2*>(p + o_bytes);
     h->part_of = reinterpret_cast<int4*>(p + o_bytes + ml_bytes);
-    e = cudaMalloc(&h->status, sizeof(int));
+    e = cudaMalloc(&h->status, (1 + sms) * sizeof(int));
   }
-  if (e == cudaSuccess) e = cudaMemset(h->status, 0, sizeof(int));
+  if (e == cudaSuccess) e = cudaMemset(h->status, 0, (1 + sms) * sizeof(int));
   if (e == cudaSuccess) {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
@@ -291,6 +291,7 @@ int dspark_tree_attend(dspark_tree_t h, const dspark_tree_cache* cache,
   a.part_ml = h->part_ml;
   a.part_of = h->part_of;
   a.part_rows = h->part_rows;
+  a.arrived = h->status + 1;
   a.status = h->status;
   // At most 16 rows a cached head on average: the kernel for few rows (any number
   // of rows is right in either).
@@ -310,7 +311,7 @@ int dspark_tree_status(dspark_tree_t h, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int st = 0;
   cudaError_t e = cudaMemcpyAsync(&st, h->status, sizeof(int), cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaMemsetAsync(h->status, 0, sizeof(int), s);
+  if (e == cudaSuccess) e = cudaMemsetAsync(h->status, 0, (1 + h->sm_count) * sizeof(int), s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   return e == cudaSuccess ? st : cuda_code(e);
 }

@@ -71,6 +71,7 @@ struct FewState {
   int64_t sums[16];
   Share share;
   int live[2];                          // there is a segment; the next one
+  int join;                             // an item to join: first worker | parts << 16
 };
 
 // Column d of the result: its place in the accumulators, n = 2 q + e and tile.
@@ -125,6 +126,101 @@ __device__ __noinline__ void add_nonfinite(const AttendArgs& a, const uint32_t* 
         const int lane = row % 8 * 4 + n / 2;
         part[((row / 16 * (DP / 8) + tile) * 32 + lane) * 4 + (row / 8 % 2) * 2 + n % 2] += x;
       }
+    }
+  }
+}
+
+// Joins the `parts` parts of an item that several CTAs share, the first of them
+// worker `first`'s: a warp has a piece of four accumulator tiles and every
+// kSplit-th part; the warps of a piece are then added in order, so that the
+// result does not depend on which CTA came last.
+template <bool F16, bool E4M3, int DP>
+__device__ __noinline__ void join_parts(const AttendArgs& a, FewState& st, float4* sum_o, int first,
+                                        int parts, int row0, int head, int group, int rows) {
+  using L = Few<E4M3, DP>;
+  constexpr int kRows = L::kRows, kPieces = L::kTiles / 4, kSplit = L::kWarps / kPieces;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane >> 2, q = lane & 3;
+  const int piece = warp % kPieces, split = warp / kPieces;
+  if (split < kSplit) {
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float4 o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = split; i < parts; i += kSplit) {
+      const int64_t part = 2 * (first + i) + (i == 0 ? 1 : 0);
+      const float4* src = reinterpret_cast<const float4*>(a.part_o + part * (kRows * DP)) +
+                          piece * 4 * 32 + lane;
+      float4 x[4];
+      float2 ml[2];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = __ldcg(src + k * 32);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) ml[h] = __ldcg(a.part_ml + part * kRows + 8 * h + g);
+      float wo[2], wx[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (8 * h + g >= rows) ml[h] = make_float2(-INFINITY, 0.f);     // no part has the row
+        const float m_new = fmaxf(m[h], ml[h].x), sub = m_new == -INFINITY ? 0.f : m_new;
+        wo[h] = ex2(m[h] - sub);
+        wx[h] = ex2(ml[h].x - sub);
+        m[h] = m_new;
+        l[h] = l[h] * wo[h] + ml[h].y * wx[h];
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        o[k].x = o[k].x * wo[0] + x[k].x * wx[0];
+        o[k].y = o[k].y * wo[0] + x[k].y * wx[0];
+        o[k].z = o[k].z * wo[1] + x[k].z * wx[1];
+        o[k].w = o[k].w * wo[1] + x[k].w * wx[1];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sum_o[(warp * 4 + k) * 32 + lane] = o[k];
+    if (piece == 0 && q == 0) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) st.ml[split][8 * h + g] = make_float2(m[h], l[h]);
+    }
+  }
+  __syncthreads();
+  const int live = min(kSplit, parts);
+#pragma unroll 1
+  for (int tile = warp; tile < L::kTiles; tile += L::kWarps) {
+    float4 x[kSplit];
+#pragma unroll
+    for (int i = 0; i < kSplit; ++i)
+      x[i] = sum_o[((i * kPieces + tile / 4) * 4 + tile % 4) * 32 + lane];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = 8 * h + g;
+      if (row >= rows) continue;
+      float top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kSplit; ++i)
+        if (i < live) top = fmaxf(top, st.ml[i][row].x);
+      const float sub = top == -INFINITY ? 0.f : top;
+      float sum = 0.f, y[2] = {0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < kSplit; ++i) {
+        if (i >= live) continue;
+        const float2 ml = st.ml[i][row];
+        const float w = ex2(ml.x - sub);
+        sum = fmaf(ml.y, w, sum);
+        y[0] = fmaf(h ? x[i].z : x[i].x, w, y[0]);
+        y[1] = fmaf(h ? x[i].w : x[i].y, w, y[1]);
+      }
+      const int grow = group * kRows + row, node = a.group.div(grow);
+      const int64_t out_row = (int64_t)(row0 + node) * a.Hq + head * a.G + grow - node * a.G;
+      const float inv = 1.f / sum;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int n = 2 * q + e;
+        const int d = E4M3 ? (DP / 8) * n + tile : 8 * n + tile % 8 + tile / 8 * 64;
+        if (d < a.D)
+          a.out[out_row * a.D + d] = sum == 0.f ? 0 : (uint16_t)pack2<F16>(y[e] * inv, 0.f);
+      }
+      if (tile == 0 && q == 0 && a.lse)
+        a.lse[out_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
     }
   }
 }
@@ -210,8 +306,6 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
   uint8_t* ring = smem + warp * L::kRing;
   uint4* q_mem = reinterpret_cast<uint4*>(smem + L::kQ);
   uint8_t* scales = smem + L::kScales + warp * L::kStages * L::kScaleBytes;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (threadIdx.x < 2) a.part_of[2 * blockIdx.x + threadIdx.x] = make_int4(0, 0, 0, 0);
   if (threadIdx.x < DSPARK_TREE_MAX_NODES / 32) st.bad[threadIdx.x] = 0;
   Item::template plan<L::kThreads, 1>(a, blockIdx.x, 1, a.n_cta, &st.share, st.sums);
 
@@ -704,8 +798,6 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
           reinterpret_cast<uint4*>(a.out + out_row(row) * a.D)[chunk] =
               reinterpret_cast<const uint4*>(out)[i];
       }
-    } else if (threadIdx.x == 0) {
-      a.part_of[part] = Item::part_of(s, st.share.total, a.n_cta);
     }
     uint32_t any_bad = 0;
 #pragma unroll
@@ -723,6 +815,22 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
       __syncthreads();
       if (threadIdx.x < DSPARK_TREE_MAX_NODES / 32) st.bad[threadIdx.x] = 0;
     }
+    if (!whole) {
+      // the last CTA to leave its part of the item joins them all
+      if (threadIdx.x == 0) {
+        const int w = Item::part_of(s, st.share.total, a.n_cta).w;
+        int* count = a.arrived + (w & 0xffff);
+        __threadfence();
+        const bool last = atomicAdd(count, 1) == (w >> 16) - 1;
+        if (last) *count = 0;
+        __threadfence();
+        st.join = last ? w : 0;
+      }
+      __syncthreads();
+      if (st.join)
+        join_parts<F16, E4M3, DP>(a, st, buf, st.join & 0xffff, st.join >> 16, s.row0, s.head,
+                                  s.group, rows);
+    }
     __syncthreads();
     cur ^= 1;
   }
@@ -730,130 +838,19 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
   if (worst > top_page) set_status(a.status, DSPARK_EPAGES);
 }
 
-// Joins the parts of the items that several CTAs share: an item of P parts has P
-// blocks, which take its pieces of four accumulator tiles in turn; the eight warps
-// of a block take every eighth part and are then added in order.
-constexpr int kJoinThreads = 256;
-
-template <bool F16, bool E4M3, int DP>
-__global__ void __launch_bounds__(kJoinThreads) few_join_kernel(const __grid_constant__ AttendArgs a) {
-  using L = Few<E4M3, DP>;
-  using Item = typename L::Item;
-  constexpr int kTiles = L::kTiles, kRows = L::kRows;
-  __shared__ float4 sum_o[8][4][32];
-  __shared__ float2 sum_ml[8][2][32];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 of = a.part_of[blockIdx.x];
-  const int parts = of.w >> 16, first = of.w & 0xffff, head = of.y, group = of.z;
-  if (parts == 0) return;
-  bool ok;
-  const typename Item::Request r = Item::load_request(a, of.x, &ok);
-  const int rows = min(kRows, r.rows * a.G - group * kRows);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane >> 2, q = lane & 3;
-  for (int piece = (int)blockIdx.x / 2 - first; piece < kTiles / 4; piece += parts) {
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float4 o[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-    for (int i = warp; i < parts; i += 8) {
-      const int64_t part = 2 * (first + i) + (i == 0 ? 1 : 0);
-      const float4* src = reinterpret_cast<const float4*>(a.part_o + part * (kRows * DP)) +
-                          piece * 4 * 32 + lane;
-      float4 x[4];
-      float2 ml[2];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] = src[k * 32];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) ml[h] = a.part_ml[part * kRows + 8 * h + g];
-      float wo[2], wx[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float m_new = fmaxf(m[h], ml[h].x), sub = m_new == -INFINITY ? 0.f : m_new;
-        wo[h] = ex2(m[h] - sub);
-        wx[h] = ex2(ml[h].x - sub);
-        m[h] = m_new;
-        l[h] = l[h] * wo[h] + ml[h].y * wx[h];
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        o[k].x = o[k].x * wo[0] + x[k].x * wx[0];
-        o[k].y = o[k].y * wo[0] + x[k].y * wx[0];
-        o[k].z = o[k].z * wo[1] + x[k].z * wx[1];
-        o[k].w = o[k].w * wo[1] + x[k].w * wx[1];
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) sum_o[warp][k][lane] = o[k];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) sum_ml[warp][h][lane] = make_float2(m[h], l[h]);
-    __syncthreads();
-    if (warp < 4) {                              // warp k finishes tile k of the piece
-      const int live = min(8, parts), tile = piece * 4 + warp;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = 8 * h + g;
-        if (row >= rows) continue;
-        float top = -INFINITY;
-        for (int i = 0; i < live; ++i) top = fmaxf(top, sum_ml[i][h][lane].x);
-        const float sub = top == -INFINITY ? 0.f : top;
-        float sum = 0.f, y[2] = {0.f, 0.f};
-        for (int i = 0; i < live; ++i) {
-          const float w = ex2(sum_ml[i][h][lane].x - sub);
-          const float4 x = sum_o[i][warp][lane];
-          sum = fmaf(sum_ml[i][h][lane].y, w, sum);
-          y[0] = fmaf(h ? x.z : x.x, w, y[0]);
-          y[1] = fmaf(h ? x.w : x.y, w, y[1]);
-        }
-        const int grow = group * kRows + row, node = a.group.div(grow);
-        const int64_t out_row = (int64_t)(r.row0 + node) * a.Hq + head * a.G + grow - node * a.G;
-        const float inv = 1.f / sum;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int n = 2 * q + e;
-          const int d = E4M3 ? (DP / 8) * n + tile : 8 * n + tile % 8 + tile / 8 * 64;
-          if (d < a.D)
-            a.out[out_row * a.D + d] = sum == 0.f ? 0 : (uint16_t)pack2<F16>(y[e] * inv, 0.f);
-        }
-        if (tile == 0 && q == 0 && a.lse)
-          a.lse[out_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-      }
-    }
-    __syncthreads();
-  }
-}
-
 template <bool F16, bool E4M3, int DP>
 cudaError_t launch(const AttendArgs& a, cudaStream_t stream) {
   using L = Few<E4M3, DP>;
   few_kernel<F16, E4M3, DP><<<a.n_cta, L::kThreads, L::kSmem, stream>>>(a);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  // the join may be set up while the main kernel runs; it waits for it itself
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(2 * a.n_cta);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, few_join_kernel<F16, E4M3, DP>, a);
+  return cudaGetLastError();
 }
 
 template <bool F16, bool E4M3, int DP>
 cudaError_t setup() {
   using L = Few<E4M3, DP>;
   static_assert(L::kSmem + sizeof(FewState) + 512 <= 232448, "shared memory of an SM");
-  cudaError_t e = cudaFuncSetAttribute(few_kernel<F16, E4M3, DP>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
-  if (e != cudaSuccess) return e;
-  // the main kernel's split of shared memory and L1: another would have the SMs
-  // drained and set up anew between the two
-  return cudaFuncSetAttribute(few_join_kernel<F16, E4M3, DP>,
-                              cudaFuncAttributePreferredSharedMemoryCarveout,
-                              cudaSharedmemCarveoutMaxShared);
+  return cudaFuncSetAttribute(few_kernel<F16, E4M3, DP>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
 }
 
 template <bool F16, int DP>

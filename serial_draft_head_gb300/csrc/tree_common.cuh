@@ -205,6 +205,7 @@ struct AttendArgs {
   float2* part_ml;
   int4* part_of;             // per part: {request, head, row group, first worker | parts << 16}
   int part_rows;
+  int* arrived;              // few rows: parts written of the item whose first is a worker's, 0 between calls
   int* status;
 };
 
