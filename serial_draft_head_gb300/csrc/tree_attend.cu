@@ -29,6 +29,7 @@ namespace tree {
 namespace {
 
 constexpr int kKeys = 128;              // keys of a tile
+constexpr int kHalf = 64;               // of them in one step of the softmax
 constexpr int kSoftWarps = 8;
 
 // Warps and registers.  The softmax groups take registers from the others: for
@@ -78,7 +79,8 @@ struct RingPos {
 };
 
 struct Tail {
-  uint64_t full[8], empty[8], q_full, q_empty, s_full[2], p_full[2], o_done[2];
+  uint64_t full[8], empty[8], q_full, q_empty;
+  uint64_t s_full[2][2], p_full[2][2], o_done[2][2];      // [stream][half of the tile]
   float2 ml[2][kKeys];
   uint32_t bad[kBadSets][DSPARK_TREE_MAX_NODES / 32];
   Share share;
@@ -121,10 +123,14 @@ __device__ __forceinline__ bool aborted(const Tail* s) {
   return *(const volatile int*)&s->abort != 0;
 }
 
-// Visibility of the 128 positions from draft position j0 on.
+// Visibility of the 128 positions from draft position j0 on (negative: context).
 __device__ __noinline__ uint4 sees_128(const uint32_t* mask_row, int rows, int node, int j0) {
-  return make_uint4(sees_32(mask_row, rows, node, j0), sees_32(mask_row, rows, node, j0 + 32),
-                    sees_32(mask_row, rows, node, j0 + 64), sees_32(mask_row, rows, node, j0 + 96));
+  const int w = j0 >> 5;                         // floor
+  uint32_t x[5];
+#pragma unroll
+  for (int k = 0; k < 5; ++k) x[k] = w + k < 0 ? 0xffffffffu : sees_word(mask_row, rows, node, w + k);
+  return make_uint4(__funnelshift_r(x[0], x[1], j0 & 31), __funnelshift_r(x[1], x[2], j0 & 31),
+                    __funnelshift_r(x[2], x[3], j0 & 31), __funnelshift_r(x[3], x[4], j0 & 31));
 }
 
 // ------------------------------------------------------------- producers --
@@ -423,6 +429,7 @@ __device__ __forceinline__ void issue(const AttendArgs& a, uint8_t* smem, Tail* 
   using L = Layout<DP>;
   constexpr uint32_t kTypes = F16 ? (1u << 7) | (1u << 10) : 0u;   // bf16 fields, cleared for f16
   constexpr uint32_t kQK = ptx::idesc_bf16_f32(128, kKeys) & ~kTypes;
+  constexpr uint32_t kQKHalf = ptx::idesc_bf16_f32(128, kHalf) & ~kTypes;
   constexpr uint32_t kPV = (ptx::idesc_bf16_f32(128, DP) & ~kTypes) | (1u << 16);  // B N-major
   const uint32_t tm_s = sh->tmem + stream * 128, tm_o = sh->tmem + 256 + stream * 128;
   const uint32_t ring = ptx::smem_u32(smem + L::kRing);
@@ -430,60 +437,116 @@ __device__ __forceinline__ void issue(const AttendArgs& a, uint8_t* smem, Tail* 
   Segment s;
   w.init(a, sh->share);
   RingPos<L::kSlots> at;
-  uint32_t count = 0;                            // own tiles so far
+  uint32_t count[2] = {0, 0};                    // products so far, of h
+  bool pair = false;
+  uint64_t q_desc = 0;
+  // the next slot of the ring, filled; also those that are only passed: every phase
+  // is waited for in order
+  auto take = [&]() {
+    const uint32_t slot = at.slot;
+    wait(sh, &sh->full[slot], at.phase, a.status);
+    at.next();
+    return slot;
+  };
+  auto filled = [&]() {                          // whether the next slot is
+    return __any_sync(0xffffffffu, ptx::mbar_test_wait(&sh->full[at.slot], at.phase)) != 0;
+  };
+  auto release = [&](uint32_t slot) {
+    ptx::tc_commit(&sh->empty[slot]);
+    if (!pair) ptx::tc_commit(&sh->empty[slot]);           // the other stream's share
+  };
+  auto scores = [&](uint32_t slot, int h, bool all) {      // S of half a tile, or of all of it
+    if (!aborted(sh)) {
+      ptx::tc_fence_after();
+      const uint64_t k_desc =
+          ptx::smem_desc_swizzle128(ring + slot * L::kTile + h * (kHalf * 128), 16, 1024);
+      const uint32_t type = all ? kQK : kQKHalf;
+      if (ptx::elect_one()) {
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k)
+          ptx::tc_mma_smem(tm_s + h * kHalf, q_desc + (k / 4) * (kKeys * 128 / 16) + (k % 4) * 2,
+                           k_desc + (k / 4) * (kKeys * 128 / 16) + (k % 4) * 2, type, k > 0);
+        ptx::tc_commit(&sh->s_full[stream][h]);
+        if (all && pair) ptx::tc_commit(&sh->s_full[stream][1]);
+        if (all || h == 1) release(slot);
+      }
+      __syncwarp();
+    }
+  };
+  // O += P V of half a tile, or of all of it (h = 0), and the wait for it
+  auto values = [&](uint32_t slot, int h, bool add) {
+    const uint32_t phase = count[h]++ & 1;
+    wait(sh, &sh->p_full[stream][h], phase, a.status);
+    if (!aborted(sh)) {
+      ptx::tc_fence_after();
+      const uint64_t v_desc =
+          ptx::smem_desc_swizzle128(ring + slot * L::kTile + h * (kHalf * 128), kKeys * 128, 1024);
+      if (ptx::elect_one()) {
+#pragma unroll
+        for (int k = 0; k < kHalf / 16; ++k)
+          ptx::tc_mma_tmem_a(tm_o, tm_s + h * kHalf + 8 * k, v_desc + k * (2048 / 16), kPV,
+                             add || k > 0);
+        if (!pair) {
+#pragma unroll
+          for (int k = kHalf / 16; k < kKeys / 16; ++k)
+            ptx::tc_mma_tmem_a(tm_o, tm_s + 8 * k, v_desc + k * (2048 / 16), kPV, true);
+        }
+        ptx::tc_commit(&sh->o_done[stream][h]);
+        if (!pair || h == 1) release(slot);
+      }
+      __syncwarp();
+    }
+    wait(sh, &sh->o_done[stream][h], phase, a.status);
+  };
   for (uint32_t seg = 0; w.next(a, &s); ++seg) {
-    const bool pair = Item::group_rows(a, s) > kKeys;
-    const int n = s.t1 - s.t0, step = pair ? 1 : 2;
-    const uint64_t q_desc = ptx::smem_desc_swizzle128(
-        ptx::smem_u32(smem) + (pair ? stream * L::kTile : 0), 16, 1024);
+    pair = Item::group_rows(a, s) > kKeys;
+    const int n = s.t1 - s.t0;
+    q_desc = ptx::smem_desc_swizzle128(ptx::smem_u32(smem) + (pair ? stream * L::kTile : 0), 16,
+                                       1024);
     wait(sh, &sh->q_full, seg & 1, a.status);
-    for (int i = 0; i < n; ++i) {
-      const bool own = pair || (i & 1) == stream;         // else the phases only pass
-      // S and P share columns: the last product that reads P is done first
-      if (own && count > 0) wait(sh, &sh->o_done[stream], (count - 1) & 1, a.status);
-      wait(sh, &sh->full[at.slot], at.phase, a.status);
-      if (own && !aborted(sh)) {
-        ptx::tc_fence_after();
-        const uint64_t k_desc =
-            ptx::smem_desc_swizzle128(ring + at.slot * L::kTile, 16, 1024);
-        if (ptx::elect_one()) {
-#pragma unroll
-          for (int k = 0; k < DP / 16; ++k) {
-            const uint64_t at = (k / 4) * (kKeys * 128 / 16) + (k % 4) * 2;
-            ptx::tc_mma_smem(tm_s, q_desc + at, k_desc + at, kQK, k > 0);
-          }
-          ptx::tc_commit(&sh->s_full[stream]);
-          ptx::tc_commit(&sh->empty[at.slot]);
-          if (!pair) ptx::tc_commit(&sh->empty[at.slot]);          // the other stream's share
+    if (pair) {
+      // S and P share columns, so the next S of a half follows the product that read
+      // its P: made while the softmax works on the other half, unless K has not come
+      // (the producers may need this tile's V slot to get there)
+      uint32_t k_slot = take();
+      scores(k_slot, 0, true);
+      for (int i = 0;; ++i) {
+        const uint32_t v_slot = take();
+        values(v_slot, 0, i > 0);
+        const bool early = i + 1 < n && filled();
+        if (early) {
+          k_slot = take();
+          scores(k_slot, 0, false);
         }
-        __syncwarp();
+        values(v_slot, 1, true);
+        if (i + 1 == n) break;
+        if (!early) k_slot = take();
+        scores(k_slot, early ? 1 : 0, !early);
       }
-      at.next();
-      const uint32_t vs = at.slot;
-      wait(sh, &sh->full[vs], at.phase, a.status);
-      at.next();
-      if (!own) continue;
-      wait(sh, &sh->p_full[stream], count & 1, a.status);
-      if (!aborted(sh)) {
-        ptx::tc_fence_after();
-        const uint64_t v_desc = ptx::smem_desc_swizzle128(
-            ring + vs * L::kTile, kKeys * 128, 1024);
-        if (ptx::elect_one()) {
-#pragma unroll
-          for (int k = 0; k < kKeys / 16; ++k)
-            ptx::tc_mma_tmem_a(tm_o, tm_s + 8 * k, v_desc + k * (2048 / 16), kPV,
-                               i >= step || k > 0);
-          ptx::tc_commit(&sh->o_done[stream]);
-          ptx::tc_commit(&sh->empty[vs]);
-          if (!pair) ptx::tc_commit(&sh->empty[vs]);
-        }
-        __syncwarp();
+    } else {
+      // a tile at a time: nothing but V's slot is held, and the ring's depth, which
+      // is what counts with few rows, is the copies'
+      for (int i = 0; i < n; ++i) {
+        const uint32_t k_slot = take();
+        const bool own = (i & 1) == stream;
+        if (own) scores(k_slot, 0, true);
+        const uint32_t v_slot = take();
+        if (own) values(v_slot, 0, i > 1);
       }
-      ++count;
     }
     if (threadIdx.x % 32 == 0) ptx::mbar_arrive(&sh->q_empty);
   }
-  if (count > 0) wait(sh, &sh->o_done[stream], (count - 1) & 1, a.status);
+}
+
+// The parts' places for the join, by a warp that has nothing else to do (1.1 us of
+// divisions).
+__device__ __forceinline__ void place_parts(const AttendArgs& a, Tail* sh) {
+  Walker w;
+  Segment s;
+  w.init(a, sh->share);
+  while (w.next(a, &s))
+    if (threadIdx.x % 32 == 0 && !s.whole())
+      a.part_of[2 * blockIdx.x + (s.t0 == 0 ? 1 : 0)] = Item::part_of(s, sh->share.total, a.n_cta);
 }
 
 // --------------------------------------------------------------- softmax --
@@ -524,6 +587,11 @@ __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 // O of this row times `back`.
 template <int DP>
 __device__ __forceinline__ void scale_row(uint32_t tm_o, float back) {
@@ -538,15 +606,19 @@ __device__ __forceinline__ void scale_row(uint32_t tm_o, float back) {
   }
 }
 
-// The row's m after a tile whose largest exponent is x_max; l and O follow if it
-// moves: the first visible key sets it, later ones when it has grown enough.
+// The row's m after keys whose largest exponent is x_max; l and O follow if it
+// moves: the first visible key sets it, later ones when it has grown enough.  O
+// is free to scale once the last product is done (o_done, null before the first).
 template <bool F16, int DP>
-__device__ __forceinline__ float move_reference(float x_max, bool first, uint32_t tm_o, float mref,
-                                                float* l) {
+__device__ __forceinline__ float move_reference(float x_max, Tail* sh, uint64_t* o_done,
+                                                uint32_t parity, int* status, uint32_t tm_o,
+                                                float mref, float* l) {
   constexpr float kShift = F16 ? 7.f : 0.f;
   const bool move = x_max > mref + (mref == -INFINITY ? 0.f : kShift + 8.f);
   const float m_new = move ? x_max - kShift : mref;
-  if (!first && __any_sync(0xffffffffu, move)) {
+  if (o_done && __any_sync(0xffffffffu, move)) {
+    wait(sh, o_done, parity, status);
+    ptx::tc_fence_after();
     const float back = mref == -INFINITY ? 0.f : ex2(mref - m_new);
     *l *= back;
     scale_row<DP>(tm_o, back);
@@ -554,24 +626,23 @@ __device__ __forceinline__ float move_reference(float x_max, bool first, uint32_
   return m_new;
 }
 
-// One tile of one row whose 128 keys are all visible, scores not capped, m
+// KEYS keys (a tile or half) of one row that are all visible, scores not capped, m
 // set: P over S, and l.  The weights go by m as it stands while the maximum is
 // taken beside them, so nothing waits for it; if it has outgrown m in any row of
-// the warp, S is still there and the tile is done again by softmax_tile_any
-// (false).  WIDE loads the next 32 scores while these are worked on.
-template <bool F16, bool WIDE>
-__device__ __forceinline__ bool softmax_tile(float sl2, uint32_t tm_s, float mref, float* l) {
+// the warp, S is still there and they are done again by softmax_any (false).  WIDE loads the next 32 scores while these are worked on.
+template <bool F16, bool WIDE, int KEYS>
+__device__ __forceinline__ bool softmax_plain(float sl2, uint32_t tm_s, float mref, float* l) {
   constexpr float kShift = F16 ? 7.f : 0.f;
-  constexpr int kBuf = WIDE ? 2 : 1;
-  uint32_t v[kBuf][32], pk[4][16];
+  constexpr int kBuf = WIDE ? 2 : 1, kChunks = KEYS / 32;
+  uint32_t v[kBuf][32], pk[kChunks][16];
   float mx[2] = {-INFINITY, -INFINITY}, sum[4] = {0.f, 0.f, 0.f, 0.f};
   const uint64_t mul = pack_f32x2(sl2, sl2), neg = pack_f32x2(-mref, -mref);
   ptx::tmem_ld32(tm_s, v[0]);
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < kChunks; ++c) {
     uint32_t (&x)[32] = v[c % kBuf];
     ptx::tmem_wait_ld32(x);
-    if (WIDE && c < 3) ptx::tmem_ld32(tm_s + 32 * (c + 1), v[(c + 1) % kBuf]);
+    if (WIDE && c < kChunks - 1) ptx::tmem_ld32(tm_s + 32 * (c + 1), v[(c + 1) % kBuf]);
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
       const float r0 = __uint_as_float(x[2 * k]), r1 = __uint_as_float(x[2 * k + 1]);
@@ -584,25 +655,26 @@ __device__ __forceinline__ bool softmax_tile(float sl2, uint32_t tm_s, float mre
       sum[(2 * k + 1) & 3] += p1;
       pk[c][k] = pack2<F16>(p0, p1);
     }
-    if (!WIDE && c < 3) ptx::tmem_ld32(tm_s + 32 * (c + 1), v[0]);
+    if (!WIDE && c < kChunks - 1) ptx::tmem_ld32(tm_s + 32 * (c + 1), v[0]);
   }
   if (__any_sync(0xffffffffu, fmaxf(mx[0], mx[1]) * sl2 > mref + (kShift + 8.f))) return false;
 #pragma unroll
-  for (int c = 0; c < 4; ++c) ptx::tmem_st16(tm_s + 16 * c, pk[c]);
+  for (int c = 0; c < kChunks; ++c) ptx::tmem_st16(tm_s + 16 * c, pk[c]);
   *l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
   ptx::tmem_wait_st();
   return true;
 }
 
-// Any tile of one row, also with invisible keys (see: a bit a key), capped
+// 64 or 128 keys of one row, also with invisible keys (see: a bit a key), capped
 // scores, or a maximum that moves m; 32 keys at a time.  Returns {m, l}.
 template <bool F16, int DP>
-__device__ __noinline__ float2 softmax_tile_any(Score sc, uint32_t tm_s, uint32_t tm_o, uint4 see,
-                                                bool first, float mref, float l) {
+__device__ __noinline__ float2 softmax_any(Score sc, Tail* sh, uint64_t* o_done, uint32_t parity,
+                                           int* status, uint32_t tm_s, uint32_t tm_o, int keys,
+                                           uint4 see, float mref, float l) {
   const bool cap = sc.cap2 > 0.f;
-  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, mn[2] = {INFINITY, INFINITY};
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < keys / 32; ++c) {
     const uint32_t m = c == 0 ? see.x : c == 1 ? see.y : c == 2 ? see.z : see.w;
     uint32_t v[32];
     ptx::tmem_ld32(tm_s + 32 * c, v);
@@ -610,20 +682,50 @@ __device__ __noinline__ float2 softmax_tile_any(Score sc, uint32_t tm_s, uint32_
 #pragma unroll
     for (int k = 0; k < 32; ++k)
       mx[k & 3] = fmaxf(mx[k & 3], (m >> k) & 1 ? __uint_as_float(v[k]) : -INFINITY);
+    if (cap) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        mn[k & 1] = fminf(mn[k & 1], (m >> k) & 1 ? __uint_as_float(v[k]) : INFINITY);
+    }
   }
   const float raw_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
   float x_max = raw_max == -INFINITY ? -INFINITY : raw_max * sc.sl2;
   if (cap && raw_max != -INFINITY) x_max = capped(sc, raw_max);
-  mref = move_reference<F16, DP>(x_max, first, tm_o, mref, &l);
+  mref = move_reference<F16, DP>(x_max, sh, o_done, parity, status, tm_o, mref, &l);
   const float sub = mref == -INFINITY ? 0.f : mref;
+  // Far from the cap (|y| <= 0.75 for y = s / c, in all rows of the warp) tanh(y) / y
+  // is a polynomial in y^2, fitted to it by weighted least squares to 3e-8: no
+  // special functions but the weight's own (2.0 us for 64 keys went to 1.2).
+  const float big = raw_max == -INFINITY ? 0.f : fmaxf(fabsf(raw_max), fabsf(fminf(mn[0], mn[1])));
+  const bool small = cap && __all_sync(0xffffffffu, big * sc.cap_y <= 0.75f);
+  constexpr float kTanh[6] = {1.f,           -0.333329588f, 0.133254066f,
+                              -0.0533444323f, 0.0195829086f, -0.00471625756f};
+  uint64_t coef[6];
+#pragma unroll
+  for (int i = 0; i < 6; ++i) coef[i] = pack_f32x2(sc.cap2 * kTanh[i], sc.cap2 * kTanh[i]);
+  const uint64_t neg = pack_f32x2(-sub, -sub);
   float sum[2] = {0.f, 0.f};
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < keys / 32; ++c) {
     const uint32_t m = c == 0 ? see.x : c == 1 ? see.y : c == 2 ? see.z : see.w;
     uint32_t v[32], pk[16];
     ptx::tmem_ld32(tm_s + 32 * c, v);
     ptx::tmem_wait_ld32(v);
-    if (cap) {
+    if (small) {
+#pragma unroll
+      for (int k = 0; k < 32; k += 2) {
+        const uint64_t y = mul_f32x2(pack_f32x2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])),
+                                     pack_f32x2(sc.cap_y, sc.cap_y));
+        const uint64_t u = mul_f32x2(y, y);
+        uint64_t t = coef[5];
+#pragma unroll
+        for (int i = 4; i >= 0; --i) t = fma_f32x2(t, u, coef[i]);
+        float x0, x1;
+        unpack_f32x2(fma_f32x2(y, t, neg), &x0, &x1);
+        v[k] = __float_as_uint(x0);
+        v[k + 1] = __float_as_uint(x1);
+      }
+    } else if (cap) {
 #pragma unroll
       for (int k = 0; k < 32; ++k)
         v[k] = __float_as_uint(capped(sc, __uint_as_float(v[k])) - sub);
@@ -659,46 +761,43 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
   Walker w;
   Segment s;
   w.init(a, sh->share);
-  uint32_t count = 0;                            // tiles of this stream so far
+  uint32_t count0 = 0, count1 = 0;               // steps of this stream so far, of h
   for (uint32_t seg = 0; w.next(a, &s); ++seg) {
     const int rows = Item::group_rows(a, s);
     const bool pair = rows > kKeys;
     const int n = s.t1 - s.t0;
-    // Q into shared memory, all 256 threads, when both MMA threads are past the last
-    if (seg > 0) wait(sh, &sh->q_empty, (seg - 1) & 1, a.status);
+    // Q into shared memory, all 256 threads
     {
-      constexpr int kChunks = DP / 8, kBatch = 8;
-      const int q_rows = pair ? kGroupRows : kKeys;
-      const int chunk = threadIdx.x % kChunks;
+      constexpr int kChunks = DP / 8, kStep = 256 / kChunks;
+      const int q_rows = pair ? kGroupRows : kKeys, chunk = threadIdx.x % kChunks;
+      const bool in_dim = chunk * 8 < a.D;
+      auto place = [&](int r) {
+        return reinterpret_cast<uint4*>(smem + (r / kKeys) * L::kTile +
+                                        tile_offset(r % kKeys, chunk));
+      };
+#pragma unroll 2
+      for (int r = threadIdx.x / kChunks; r < q_rows; r += kStep) {
+        const bool on = in_dim && r < rows;
+        const int gr = s.group * kGroupRows + (on ? r : 0), nd = a.group.div(gr);
+        const uint8_t* src = a.q + (int64_t)(s.row0 + nd) * a.q_row +
+                             (int64_t)(s.head * a.G + gr - nd * a.G) * a.q_head;
+        ptx::cp_async16_or_zero(place(r), on ? src + chunk * 16 : src, on);
+      }
+      ptx::cp_async_commit();
+      ptx::cp_async_wait_group<0>();
+      if ((E4M3 && !F16) || flip) {              // each thread the chunks that it copied
 #pragma unroll 1
-      for (int i0 = threadIdx.x / kChunks; i0 < q_rows; i0 += kBatch * (256 / kChunks)) {
-        uint4 x[kBatch];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int r = i0 + k * (256 / kChunks);
-          x[k] = make_uint4(0, 0, 0, 0);
-          if (r < rows && chunk * 8 < a.D) {
-            const int gr = s.group * kGroupRows + r, nd = a.group.div(gr);
-            const uint8_t* src = a.q + (int64_t)(s.row0 + nd) * a.q_row +
-                                 (int64_t)(s.head * a.G + gr - nd * a.G) * a.q_head;
-            x[k] = __ldg(reinterpret_cast<const uint4*>(src) + chunk);
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int r = i0 + k * (256 / kChunks);
-          x[k].x ^= flip;
-          x[k].y ^= flip;
-          x[k].z ^= flip;
-          x[k].w ^= flip;
+        for (int r = threadIdx.x / kChunks; r < q_rows; r += kStep) {
+          uint4 x = *place(r);
+          x.x ^= flip;
+          x.y ^= flip;
+          x.z ^= flip;
+          x.w ^= flip;
           if (E4M3 && !F16) {
-            const uint2 lo = swap_middle(make_uint2(x[k].x, x[k].y));
-            const uint2 hi = swap_middle(make_uint2(x[k].z, x[k].w));
-            x[k] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            const uint2 lo = swap_middle(make_uint2(x.x, x.y)), hi = swap_middle(make_uint2(x.z, x.w));
+            x = make_uint4(lo.x, lo.y, hi.x, hi.y);
           }
-          if (r < q_rows)
-            *reinterpret_cast<uint4*>(smem + (r / kKeys) * L::kTile +
-                                      tile_offset(r % kKeys, chunk)) = x[k];
+          *place(r) = x;
         }
       }
       ptx::fence_proxy_async_smem();
@@ -714,33 +813,45 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
         a.mask ? a.mask + (int64_t)(s.row0 + node) * a.mask_stride : nullptr;
     float mref = -INFINITY, l = 0.f;
     const int step = pair ? 1 : 2;
+    const int keys = pair ? kHalf : kKeys;       // of one step
     for (int i = pair ? 0 : wg; i < n; i += step) {
-      wait(sh, &sh->s_full[wg], count & 1, a.status);
-      ++count;
-      ptx::tc_fence_after();
-      if (warp_valid) {
-        const int pos0 = (s.t0 + i) * kKeys;
-        const bool masked = pos0 + kKeys > s.start;
-        const bool plain = !masked && sc.cap2 == 0.f && i >= step &&
-                           !__any_sync(0xffffffffu, mref == -INFINITY);
-        if (!plain || !softmax_tile<F16, !E4M3>(sc.sl2, tm_s, mref, &l)) {
-          const float2 r = softmax_tile_any<F16, DP>(
-              sc, tm_s, tm_o + wg * 128,
-              masked ? sees_128(mask_row, s.rows, node, pos0 - s.start)
-                     : make_uint4(~0u, ~0u, ~0u, ~0u),
-              i < step, mref, l);
-          mref = r.x;
-          l = r.y;
+#pragma unroll 1
+      for (int h = 0; h < (pair ? 2 : 1); ++h) {
+        wait(sh, &sh->s_full[wg][h], (h ? count1 : count0) & 1, a.status);
+        ptx::tc_fence_after();
+        if (warp_valid) {
+          const int pos0 = (s.t0 + i) * kKeys + h * kHalf;
+          const bool masked = pos0 + keys > s.start;
+          bool done = !masked && sc.cap2 == 0.f && !__any_sync(0xffffffffu, mref == -INFINITY);
+          if (done)
+            done = pair ? softmax_plain<F16, !E4M3, kHalf>(sc.sl2, tm_s + h * kHalf, mref, &l)
+                        : softmax_plain<F16, !E4M3, kKeys>(sc.sl2, tm_s, mref, &l);
+          if (!done) {
+            // the product before this one
+            const int before = pair ? h ^ 1 : 0;
+            const uint32_t phase = (before ? count1 : count0) - 1;
+            const float2 r = softmax_any<F16, DP>(
+                sc, sh, h == 1 || i >= step ? &sh->o_done[wg][before] : nullptr, phase & 1, a.status,
+                tm_s + h * kHalf, tm_o + wg * 128, keys,
+                masked ? sees_128(mask_row, s.rows, node, pos0 - s.start)
+                       : make_uint4(~0u, ~0u, ~0u, ~0u),
+                mref, l);
+            mref = r.x;
+            l = r.y;
+          }
+          ptx::tc_fence_before();
         }
-        ptx::tc_fence_before();
+        __syncwarp();
+        if (threadIdx.x % 32 == 0) ptx::mbar_arrive(&sh->p_full[wg][h]);
+        if (h == 0) ++count0;
+        else ++count1;
       }
-      __syncwarp();
-      if (threadIdx.x % 32 == 0) ptx::mbar_arrive(&sh->p_full[wg]);
     }
 
     // the segment's result
     const int n1 = n / 2;                        // the second stream's tiles, not in pairs
-    if (count > 0) wait(sh, &sh->o_done[wg], (count - 1) & 1, a.status);
+    if (pair || wg < n) wait(sh, &sh->o_done[wg][0], (count0 - 1) & 1, a.status);
+    if (pair) wait(sh, &sh->o_done[wg][1], (count1 - 1) & 1, a.status);
     if (!pair) sh->ml[wg][lane_row] = make_float2(mref, l);
     ptx::tc_fence_before();
     asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -754,6 +865,7 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
       w1 = n1 > 0 ? ex2(x1.x - sub) : 0.f;
       l = w0 * x0.y + (n1 > 0 ? w1 * x1.y : 0.f);
     }
+    wait(sh, &sh->q_empty, seg & 1, a.status);   // both MMA warps are past it
     const bool whole = s.whole();
     const int part = 2 * blockIdx.x + (s.t0 == 0 ? 1 : 0);
     const uint32_t* bad = sh->bad[seg % kBadSets];
@@ -765,6 +877,10 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
       const int64_t out_row = (int64_t)(s.row0 + node) * a.Hq + s.head * a.G + grow - node * a.G;
       // pair: a group its own row tile, all columns; else both tiles, half the columns
       const int c0 = pair ? 0 : wg * (DP / 64), c1 = pair ? DP / 32 : c0 + DP / 64;
+      // 16-byte chunks of a row here: kPer places, of which not in pairs half is used
+      constexpr int kPer = DP / 8;
+      const int lane = threadIdx.x % 32;
+      uint4* q_rows = reinterpret_cast<uint4*>(smem) + (threadIdx.x / 32) * 32 * kPer;
 #pragma unroll 1
       for (int c = c0; c < c1; ++c) {
         uint32_t v[32];
@@ -787,15 +903,14 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
             o[k + 2] = y;
           }
         }
-        if (valid && whole) {
-          uint4* dst = reinterpret_cast<uint4*>(a.out + out_row * a.D + 32 * c);
+        if (whole) {                             // to the warp's rows in Q's place
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             uint32_t x[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               x[e] = l == 0.f ? 0u : pack2<F16>(o[8 * k + 2 * e] * inv, o[8 * k + 2 * e + 1] * inv);
-            if (32 * c + 8 * k < a.D) dst[k] = make_uint4(x[0], x[1], x[2], x[3]);
+            q_rows[lane * kPer + (4 * (c - c0) + k ^ lane % kPer)] = make_uint4(x[0], x[1], x[2], x[3]);
           }
         } else if (valid) {
           float4* dst = reinterpret_cast<float4*>(a.part_o) +
@@ -804,6 +919,18 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
           for (int k = 0; k < 8; ++k)
             dst[(int64_t)k * a.part_rows] =
                 make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        }
+        __syncwarp();
+      }
+      if (whole) {                               // whole rows at a time to memory
+        const int per = 4 * (c1 - c0), n_chunks = per * min(32, rows - (local - lane));
+#pragma unroll 4
+        for (int k = lane; k < 32 * per; k += 32) {
+          const int r = k / per, chunk = k % per;
+          const int64_t to = __shfl_sync(0xffffffffu, out_row, r);
+          if (k < n_chunks && (4 * c0 + chunk) * 8 < a.D)
+            reinterpret_cast<uint4*>(a.out + to * a.D)[4 * c0 + chunk] =
+                q_rows[r * kPer + (chunk ^ r % kPer)];
         }
         __syncwarp();
       }
@@ -819,8 +946,6 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
         else if (a.lse) a.lse[out_row] = l == 0.f ? -INFINITY : (mref + log2f(l)) * kLn2;
       }
     }
-    if (!whole && threadIdx.x == 0)
-      a.part_of[part] = Item::part_of(s, sh->share.total, a.n_cta);
     ptx::tc_fence_before();
     asm volatile("bar.sync 1, 256;" ::: "memory");
     if (any_bad != 0 && threadIdx.x < DSPARK_TREE_MAX_NODES / 32)
@@ -852,9 +977,11 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1)
     ptx::mbar_init(&sh->q_full, kSoftWarps);
     ptx::mbar_init(&sh->q_empty, 2);
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&sh->s_full[i], 1);
-      ptx::mbar_init(&sh->p_full[i], 4);
-      ptx::mbar_init(&sh->o_done[i], 1);
+      for (int h = 0; h < 2; ++h) {
+        ptx::mbar_init(&sh->s_full[i][h], 1);
+        ptx::mbar_init(&sh->p_full[i][h], 4);
+        ptx::mbar_init(&sh->o_done[i][h], 1);
+      }
     }
     ptx::fence_mbar_init();
     sh->abort = 0;
@@ -876,6 +1003,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1)
   } else {
     ptx::set_registers<R::kLaunchRegs, R::kMmaRegs>();
     if (warp < R::kMmaWarp + 2) issue<F16, DP>(a, smem, sh, warp - R::kMmaWarp);
+    else if (warp == R::kMmaWarp + 2) place_parts(a, sh);
   }
   __syncwarp();
   ptx::tc_fence_before();
@@ -888,36 +1016,26 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1)
   if (warp == R::kMmaWarp) ptx::tmem_dealloc(sh->tmem, 512);
 }
 
-// Joins the parts of the items that several CTAs share.  An item of P parts has
-// P x kJoinSplit blocks: block (p, y) of a part's slot p takes every (P x
-// kJoinSplit)-th piece of 32 rows by 16 columns.  Its eight warps take every
-// eighth part, lane = row, and are then added in order, so the result does not
-// depend on timing.
+// Joins the parts of the items that several CTAs share, in pieces of 32 rows (lane
+// = row) by 16 columns.  An item of P parts has P x kJoinSplit blocks: block (p, y)
+// of a part's slot p takes every (P x kJoinSplit)-th of its pieces, or of groups of
+// eight where one warp joins a piece alone (up to kJoinAlone parts).  With more
+// parts the warps of a block take every eighth one and are then added in order:
+// the result does not depend on timing.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinSplit = 4;
+constexpr int kJoinAlone = 4;
 
-template <bool F16, int DP>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttendArgs a) {
-  __shared__ float4 part_sum[8][4][32];
-  __shared__ float2 part_ml[8][32];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 of = a.part_of[blockIdx.x];
-  const int parts = of.w >> 16, first = of.w & 0xffff, head = of.y, group = of.z;
-  if (parts == 0) return;
-  bool ok;
-  const Item::Request r = Item::load_request(a, of.x, &ok);
-  const int rows = min(kGroupRows, r.rows * a.G - group * kGroupRows);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int pieces = (rows + 31) / 32 * (DP / 16);
-  // this block's place among the item's: which part's slot, and y
-  const int mine = ((int)blockIdx.x / 2 - first) * kJoinSplit + blockIdx.y;
-  for (int piece = mine; piece < pieces; piece += parts * kJoinSplit) {
-    const int c4 = piece % (DP / 16) * 4, local = piece / (DP / 16) * 32 + lane;   // float4 column
-    float m = -INFINITY, l = 0.f;
-    float4 o[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = warp; i < parts; i += 8) {
+struct JoinSum {
+  float m = -INFINITY, l = 0.f;
+  float4 o[4] = {};
+
+  // adds parts first + i, first + i + step, ... below `parts`
+  template <int DP, int UNROLL>
+  __device__ __forceinline__ void add(const AttendArgs& a, int first, int parts, int i, int step,
+                                      int c4, int local) {
+#pragma unroll UNROLL
+    for (; i < parts; i += step) {
       const int64_t part = 2 * (first + i) + (i == 0 ? 1 : 0);
       const float2 ml = a.part_ml[part * a.part_rows + local];
       const float4* src = reinterpret_cast<const float4*>(a.part_o) +
@@ -937,37 +1055,73 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         o[k].w = o[k].w * wo + x[k].w * wx;
       }
     }
+  }
+};
+
+template <bool F16>
+__device__ __forceinline__ uint2 join_pack(float4 s, float l) {
+  if (l == 0.f) return make_uint2(0u, 0u);
+  const float inv = 1.f / l;
+  return make_uint2(pack2<F16>(s.x * inv, s.y * inv), pack2<F16>(s.z * inv, s.w * inv));
+}
+
+template <bool F16, int DP>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttendArgs a) {
+  __shared__ float4 part_sum[8][4][32];
+  __shared__ float2 part_ml[8][32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 of = a.part_of[blockIdx.x];
+  const int parts = of.w >> 16, first = of.w & 0xffff, head = of.y, group = of.z;
+  if (parts == 0) return;
+  bool ok;
+  const Item::Request r = Item::load_request(a, of.x, &ok);
+  const int rows = min(kGroupRows, r.rows * a.G - group * kGroupRows);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int pieces = (rows + 31) / 32 * (DP / 16);
+  // this block's place among the item's: which part's slot, and y
+  const int mine = ((int)blockIdx.x / 2 - first) * kJoinSplit + blockIdx.y;
+  const bool alone = parts <= kJoinAlone;
+  const int step = parts * kJoinSplit * (alone ? 8 : 1);
+  for (int piece = alone ? mine * 8 + warp : mine; piece < pieces; piece += step) {
+    const int c4 = piece % (DP / 16) * 4, local = piece / (DP / 16) * 32 + lane;   // float4 column
+    const int grow = group * kGroupRows + local, node = a.group.div(grow);
+    const int64_t out_row = (int64_t)(r.row0 + node) * a.Hq + head * a.G + grow - node * a.G;
+    JoinSum s;
+    if (alone) {
+      s.add<DP, 2>(a, first, parts, 0, 1, c4, local);
+      if (local >= rows) continue;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) part_sum[warp][k][lane] = o[k];
-    part_ml[warp][lane] = make_float2(m, l);
+      for (int k = 0; k < 4; k += 2) {
+        const uint2 x = join_pack<F16>(s.o[k], s.l), y = join_pack<F16>(s.o[k + 1], s.l);
+        if (4 * (c4 + k) < a.D)
+          *reinterpret_cast<uint4*>(a.out + out_row * a.D + 4 * (c4 + k)) =
+              make_uint4(x.x, x.y, y.x, y.y);
+      }
+      if (c4 == 0 && a.lse) a.lse[out_row] = s.l == 0.f ? -INFINITY : (s.m + log2f(s.l)) * kLn2;
+      continue;
+    }
+    s.add<DP, 1>(a, first, parts, warp, 8, c4, local);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) part_sum[warp][k][lane] = s.o[k];
+    part_ml[warp][lane] = make_float2(s.m, s.l);
     __syncthreads();
-    const int grow = group * kGroupRows + local;
     if (warp < 4 && local < rows) {              // warp k finishes float4 column c4 + k
       const int live = min(8, parts);
-      m = -INFINITY;
+      float m = -INFINITY, l = 0.f;
       for (int i = 0; i < live; ++i) m = fmaxf(m, part_ml[i][lane].x);
       const float sub = m == -INFINITY ? 0.f : m;
-      l = 0.f;
-      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int i = 0; i < live; ++i) {
         const float w = ex2(part_ml[i][lane].x - sub);
         const float4 x = part_sum[i][warp][lane];
         l = fmaf(part_ml[i][lane].y, w, l);
-        s.x = fmaf(x.x, w, s.x);
-        s.y = fmaf(x.y, w, s.y);
-        s.z = fmaf(x.z, w, s.z);
-        s.w = fmaf(x.w, w, s.w);
+        y.x = fmaf(x.x, w, y.x);
+        y.y = fmaf(x.y, w, y.y);
+        y.z = fmaf(x.z, w, y.z);
+        y.w = fmaf(x.w, w, y.w);
       }
-      const int node = a.group.div(grow);
-      const int64_t out_row = (int64_t)(r.row0 + node) * a.Hq + head * a.G + grow - node * a.G;
       const int d = 4 * (c4 + warp);
-      if (d < a.D) {
-        const float inv = 1.f / l;
-        *reinterpret_cast<uint2*>(a.out + out_row * a.D + d) =
-            l == 0.f ? make_uint2(0u, 0u)
-                     : make_uint2(pack2<F16>(s.x * inv, s.y * inv),
-                                  pack2<F16>(s.z * inv, s.w * inv));
-      }
+      if (d < a.D) *reinterpret_cast<uint2*>(a.out + out_row * a.D + d) = join_pack<F16>(y, l);
       if (d == 0 && a.lse) a.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     }
     __syncthreads();

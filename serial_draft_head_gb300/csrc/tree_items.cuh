@@ -51,12 +51,14 @@ struct Score {
   float sl2;        // |scale| log2(e): a negative scale turns Q's signs
   float cap2;       // softcap log2(e), 0 without a cap
   float cap_in;     // 2 sl2 / softcap: tanh(y) = 1 - 2 / (2^(2 y log2(e)) + 1)
+  float cap_y;      // |scale| / softcap
 
   __device__ static Score of(const AttendArgs& a) {
     Score s;
     s.sl2 = fabsf(a.scale) * kLog2e;
     s.cap2 = a.softcap * kLog2e;
     s.cap_in = a.softcap > 0.f ? 2.f * s.sl2 / a.softcap : 0.f;
+    s.cap_y = a.softcap > 0.f ? fabsf(a.scale) / a.softcap : 0.f;
     return s;
   }
 };
@@ -67,6 +69,11 @@ __device__ __forceinline__ float capped(const Score& sc, float raw) {
 
 // First unit of worker i's share of `total` units over n workers.
 __device__ __forceinline__ int64_t share_start(int64_t total, int n, int i) { return total * i / n; }
+
+// The same out of line: code that is met cold costs a few hundred cycles a line.
+static __device__ __noinline__ int64_t share_start_far(int64_t total, int n, int i) {
+  return share_start(total, n, i);
+}
 
 // The worker whose share holds unit u.
 static __device__ __noinline__ int holder(int64_t total, int workers, int64_t u) {
@@ -141,16 +148,16 @@ struct Work {
     const int n = (int)(total < workers ? total : workers);
     if ((int)threadIdx.x < COUNT) {
       const int w = worker0 + threadIdx.x * stride;
-      const int64_t u0 = w < n ? share_start(total, n, w) : total;
+      const int64_t u0 = w < n ? share_start_far(total, n, w) : total;
       shares[threadIdx.x].unit0 = u0;
-      shares[threadIdx.x].units = (w < n ? share_start(total, n, w + 1) : total) - u0;
+      shares[threadIdx.x].units = (w < n ? share_start_far(total, n, w + 1) : total) - u0;
       shares[threadIdx.x].total = total;
     }
     // the thread whose requests hold a share's first unit writes its place
     for (int i = 0; i < COUNT; ++i) {
       const int w = worker0 + i * stride;
       if (w >= n) break;
-      const int64_t u0 = share_start(total, n, w);
+      const int64_t u0 = share_start_far(total, n, w);
       if (u0 < before || u0 >= before + sum) continue;
       int64_t at = before;
 #pragma unroll
