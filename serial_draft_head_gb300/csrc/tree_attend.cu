@@ -679,14 +679,13 @@ __device__ __noinline__ float2 softmax_any(Score sc, Tail* sh, uint64_t* o_done,
     uint32_t v[32];
     ptx::tmem_ld32(tm_s + 32 * c, v);
     ptx::tmem_wait_ld32(v);
+    if (cap) {                                   // invisible ones too: see `small`
+#pragma unroll
+      for (int k = 0; k < 32; ++k) mn[k & 1] = fminf(mn[k & 1], __uint_as_float(v[k]));
+    }
 #pragma unroll
     for (int k = 0; k < 32; ++k)
       mx[k & 3] = fmaxf(mx[k & 3], (m >> k) & 1 ? __uint_as_float(v[k]) : -INFINITY);
-    if (cap) {
-#pragma unroll
-      for (int k = 0; k < 32; ++k)
-        mn[k & 1] = fminf(mn[k & 1], (m >> k) & 1 ? __uint_as_float(v[k]) : INFINITY);
-    }
   }
   const float raw_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
   float x_max = raw_max == -INFINITY ? -INFINITY : raw_max * sc.sl2;
