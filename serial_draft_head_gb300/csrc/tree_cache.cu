@@ -16,7 +16,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxTok = 16;        // tokens per block
-constexpr int kBatch = 4;          // rows in flight a thread
+constexpr int kBatch = 2;          // rows in flight a thread
 
 struct Token {
   int page, slot;                  // page -1: left out
@@ -69,63 +69,77 @@ __device__ __forceinline__ Place place_of_row(const RowsArgs& a, int r, int rows
   return p;
 }
 
-// LANES (8 or 16) lanes a row, 8 elements each.
+// LANES lanes a row, 16 bytes of the cache each (8 elements, or 16 codes).
 template <bool F16, bool E4M3, int LANES>
 __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__ RowsArgs a,
                                                          int tok) {
   __shared__ Token toks[kMaxTok];
   constexpr int kGroups = kThreads / LANES;
+  constexpr int kLoads = E4M3 ? 2 : 1;             // 16-byte chunks of the row a lane
   const int n0 = blockIdx.x * tok;
   const int n_tok = min(tok, a.b.N - n0);
   find_tokens(a, n0, n_tok, toks);
   const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
-  const bool in_row = lane * 8 < a.D;
+  const bool in_row = lane * 8 * kLoads < a.D;
   const int rows = n_tok * a.Hkv * 2;
   // whole warps stay in the loop: the shuffles need every lane
   for (int r0 = 0; r0 < rows; r0 += kGroups * kBatch) {
-    uint4 x[kBatch];
+    uint4 x[kBatch][kLoads];
     Place p[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       p[i] = place_of_row(a, r0 + group + i * kGroups, rows, toks);
-      x[i] = make_uint4(0, 0, 0, 0);
-      if (p[i].on && in_row)
-        x[i] = __ldg(reinterpret_cast<const uint4*>(
-                         a.src[p[i].v] + (int64_t)(n0 + p[i].tok) * a.src_row[p[i].v] +
-                         p[i].head * a.src_head[p[i].v]) + lane);
+      const uint4* src = reinterpret_cast<const uint4*>(
+                             a.src[p[i].v] + (int64_t)(n0 + p[i].tok) * a.src_row[p[i].v] +
+                             p[i].head * a.src_head[p[i].v]) + lane * kLoads;
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) {
+        x[i][k] = make_uint4(0, 0, 0, 0);
+        if (p[i].on && in_row) x[i][k] = __ldg(src + k);
+      }
     }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
       uint8_t* dst = a.c.x[p[i].v].at(p[i].t.page, p[i].t.slot, p[i].head);
       if (!E4M3) {
-        if (p[i].on && in_row) reinterpret_cast<uint4*>(dst)[lane] = x[i];
+        if (p[i].on && in_row) reinterpret_cast<uint4*>(dst)[lane] = x[i][0];
         continue;
       }
-      float f[8];
-      uint32_t big = 0;
+      uint32_t w[4 * kLoads];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        f[k] = to_float<F16>((uint16_t)(w[k / 2] >> (16 * (k & 1))));
-        big = max(big, __float_as_uint(f[k]) & 0x7fffffffu);   // ordered as magnitudes, NaN last
+      for (int k = 0; k < kLoads; ++k) {
+        w[4 * k] = x[i][k].x;
+        w[4 * k + 1] = x[i][k].y;
+        w[4 * k + 2] = x[i][k].z;
+        w[4 * k + 3] = x[i][k].w;
       }
+      uint32_t big2 = 0;                           // magnitudes in order, NaN last
+#pragma unroll
+      for (int k = 0; k < 4 * kLoads; ++k) big2 = __vmaxu2(big2, w[k] & 0x7fff7fffu);
 #pragma unroll
       for (int o = LANES / 2; o > 0; o >>= 1)
-        big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+        big2 = __vmaxu2(big2, __shfl_xor_sync(0xffffffffu, big2, o));
+      const uint32_t big = __float_as_uint(to_float<F16>((uint16_t)max(big2 & 0xffffu, big2 >> 16)));
       // a = m 2^x, 448 = 1.75 2^8: e = x - 8, one more where m > 1.75
       const int field = (int)(big >> 23);
       int byte = field - 8 + ((big & 0x7fffffu) > 0x600000u ? 1 : 0);
       byte = field == 255 ? 255 : max(byte, 0);
       const float inv = __uint_as_float((uint32_t)(254 - (byte == 255 ? 127 : byte)) << 23);
-      uint32_t code[2] = {0, 0};
+      uint32_t code[2 * kLoads];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < 4 * kLoads; ++k) {
         const __nv_fp8x2_storage_t c2 = __nv_cvt_float2_to_fp8x2(
-            make_float2(f[2 * k] * inv, f[2 * k + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-        code[k / 2] |= (uint32_t)c2 << (16 * (k & 1));
+            make_float2(to_float<F16>((uint16_t)w[k]) * inv, to_float<F16>((uint16_t)(w[k] >> 16)) * inv),
+            __NV_SATFINITE, __NV_E4M3);
+        code[k / 2] = k % 2 ? code[k / 2] | (uint32_t)c2 << 16 : (uint32_t)c2;
       }
-      if (byte == 255) code[0] = code[1] = 0x7f7f7f7fu;
-      if (p[i].on && in_row) reinterpret_cast<uint2*>(dst)[lane] = make_uint2(code[0], code[1]);
+      if (byte == 255) {
+#pragma unroll
+        for (int k = 0; k < 2 * kLoads; ++k) code[k] = 0x7f7f7f7fu;
+      }
+      if (p[i].on && in_row)
+        reinterpret_cast<uint4*>(dst)[lane] =
+            make_uint4(code[0], code[1], code[kLoads], code[2 * kLoads - 1]);
       if (p[i].on && lane == 0)
         *a.c.scale[p[i].v].at(p[i].t.page, p[i].t.slot, p[i].head) = (uint8_t)byte;
     }
@@ -270,8 +284,9 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constan
 
 template <bool F16, bool E4M3>
 void launch_write(const RowsArgs& a, int grid, int tok, cudaStream_t stream) {
-  if (a.D <= 64) write_kernel<F16, E4M3, 8><<<grid, kThreads, 0, stream>>>(a, tok);
-  else write_kernel<F16, E4M3, 16><<<grid, kThreads, 0, stream>>>(a, tok);
+  constexpr int kEach = E4M3 ? 16 : 8;
+  if (a.D <= 64) write_kernel<F16, E4M3, 64 / kEach><<<grid, kThreads, 0, stream>>>(a, tok);
+  else write_kernel<F16, E4M3, 128 / kEach><<<grid, kThreads, 0, stream>>>(a, tok);
 }
 
 template <bool F16, bool E4M3>
