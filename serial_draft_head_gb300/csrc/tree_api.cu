@@ -293,9 +293,13 @@ int dspark_tree_attend(dspark_tree_t h, const dspark_tree_cache* cache,
   a.part_rows = h->part_rows;
   a.arrived = h->status + 1;
   a.status = h->status;
-  // At most 16 rows a cached head on average: the kernel for few rows (any number
-  // of rows is right in either).
-  if ((int64_t)a.b.N * a.G <= (int64_t)16 * a.b.B)
+  // Few rows a cached head on average: the kernel that has tiles of 16 of them (any
+  // number of rows is right in either).  16 requests of 300 to 6,000 tokens, 8 heads,
+  // us here / there: 16-bit 4 rows 57 / 63, 16 rows 58.5 / 63.5, 20 rows 100 / 64 (K
+  // and V read twice); e4m3, which the other kernel has to convert through shared
+  // memory, 4 rows 45 / 69, 16 rows 46 / 76, 32 rows 74 / 78.
+  const int few_rows = cache->type == DSPARK_TYPE_E4M3 ? 32 : 16;
+  if ((int64_t)a.b.N * a.G <= (int64_t)few_rows * a.b.B)
     return cuda_code(few_launch(a, h->cfg.type == DSPARK_TYPE_F16,
                                 cache->type == DSPARK_TYPE_E4M3,
                                 static_cast<cudaStream_t>(stream)));

@@ -1023,7 +1023,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1)
 // the result does not depend on timing.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinSplit = 4;
-constexpr int kJoinAlone = 4;
+constexpr int kJoinAlone = 8;
 
 struct JoinSum {
   float m = -INFINITY, l = 0.f;
