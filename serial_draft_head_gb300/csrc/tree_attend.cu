@@ -546,7 +546,7 @@ __device__ __forceinline__ void place_parts(const AttendArgs& a, Tail* sh) {
   w.init(a, sh->share);
   while (w.next(a, &s))
     if (threadIdx.x % 32 == 0 && !s.whole())
-      a.part_of[2 * blockIdx.x + (s.t0 == 0 ? 1 : 0)] = Item::part_of(s, sh->share.total, a.n_cta);
+      a.part_of[2 * blockIdx.x + (s.t0 == 0 ? 1 : 0)] = Item::part_of(s, sh->share.cut);
 }
 
 // --------------------------------------------------------------- softmax --
@@ -988,7 +988,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1)
   }
   for (int i = threadIdx.x; i < kBadSets * (DSPARK_TREE_MAX_NODES / 32); i += R::kThreads)
     (&sh->bad[0][0])[i] = 0;
-  Item::plan<R::kThreads, 1>(a, blockIdx.x, 1, a.n_cta, &sh->share, sh->warp_sum);
+  Item::plan<R::kThreads>(a, &sh->share, sh->warp_sum);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();

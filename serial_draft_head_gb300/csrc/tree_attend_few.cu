@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
   uint4* q_mem = reinterpret_cast<uint4*>(smem + L::kQ);
   uint8_t* scales = smem + L::kScales + warp * L::kStages * L::kScaleBytes;
   if (threadIdx.x < DSPARK_TREE_MAX_NODES / 32) st.bad[threadIdx.x] = 0;
-  Item::template plan<L::kThreads, 1>(a, blockIdx.x, 1, a.n_cta, &st.share, st.sums);
+  Item::template plan<L::kThreads>(a, &st.share, st.sums);
 
   // ---- the copies' side: the warp's blocks in order, kStages - 1 ahead of the products
   BlockCursor<Item, L::kExtra> c;
@@ -820,7 +820,7 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
     if (!whole) {
       // the last CTA to leave its part of the item joins them all
       if (threadIdx.x == 0) {
-        const int w = Item::part_of(s, st.share.total, a.n_cta).w;
+        const int w = Item::part_of(s, st.share.cut).w;
         int* count = a.arrived + (w & 0xffff);
         __threadfence();
         const bool last = atomicAdd(count, 1) == (w >> 16) - 1;
