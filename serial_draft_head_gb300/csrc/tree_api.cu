@@ -72,9 +72,10 @@ int make_cache(const dspark_tree* h, const dspark_tree_cache* c, CacheView* out)
 }
 
 // Tiled-copy maps of a 16-bit cache whose pages cut a 128-key tile into one or
-// two boxes (a box of 64 slots by 64 elements is 8 KB; with 16-slot pages a tile
-// took 32 boxes of 2 KB and 6,000 cycles, twice what the 16-byte copies take).
-// Others, and strides the maps do not take, have none.
+// two boxes.  With 64-slot pages, by maps / by 16-byte copies: 17 nodes over 131,000
+// tokens 102 / 138 us, 64 requests of 64 nodes 402 / 479 us.  With 16-slot pages a
+// tile would be 32 boxes of 2 KB, which took 6,000 cycles, twice the copies' time:
+// those, and strides that a map does not take, have none.
 void make_maps(const dspark_tree* h, const dspark_tree_cache* c, const CacheView& v, TileMaps* m) {
   m->rows = 0;
   const int page = c->page_size;

@@ -1,27 +1,43 @@
 // tree_attend.cu -- attention of drafted rows over a paged cache on tcgen05, for
-// more than 16 rows a cached head (tree_attend_few.cu has the others).  Items
-// are 256 rows by tiles of 128 keys, a worker is a CTA, one a SM (tree_items.cuh
-// says how the work is cut, and the mathematics).
+// more rows a cached head than tree_attend_few.cu takes.  Items are 256 rows by
+// tiles of 128 keys, a worker is a CTA, one a SM (tree_items.cuh says how the
+// work is cut, and the mathematics).
 //
-// Roles of the 18 warps: 8 softmax warps in two groups of 128 threads (thread =
-// row = tensor-memory lane), 8 producer warps, 2 MMA warps (one thread each).
-// Two streams share the ring of key and value tiles: with more than 128 rows
-// each stream owns a row tile and both read every key tile; with fewer, the
-// streams take alternate key tiles of the one row tile and are joined at the
-// end.  Per stream: S = Q K^T (tcgen05, both operands in shared memory) into
+// Warps: 8 of softmax in two groups of 128 threads (thread = row = tensor-memory
+// lane), then the producers (4 for a 16-bit cache, 8 for e4m3), then a group of 4
+// of which two issue products, one a stream, and a third works out where the
+// parts lie.  Two streams share the ring of key and value tiles: with more than
+// 128 rows (a pair) each stream owns a row tile and both read every key tile;
+// with fewer, the streams take alternate key tiles of the one row tile and are
+// joined at the end.  Per stream: S = Q K^T (both operands in shared memory) into
 // tensor memory, softmax there, P written over S, O += P V with P read from
-// tensor memory.  One stream's softmax runs beside the other's products.
+// tensor memory.
+//
+// S and P share columns and tensor memory is full, so the next S cannot be made
+// before P has been used.  A pair therefore goes by halves of 64 keys: one half's
+// S is made while the softmax is at the other (64 requests of 64 nodes, 4,096 to
+// 8,192 tokens: 400 us, 426 with whole tiles).  Alternate tiles stay whole: with
+// few rows the copies bound, and halves hold their slots longer (63 us against 75
+// for 16 requests of 8 nodes).
 //
 // Tensor memory (512 columns): S/P of the streams at 0 and 128, O at 256 and
-// 384.  Shared memory: two Q tiles and the ring, rows of 64 elements (128
-// bytes) swizzled in atoms of 8 rows; K is read K-major, V (same layout)
-// N-major.  The producers copy any strides and page size: 16-byte cp.async for
-// a 16-bit cache; e4m3 through registers, the scale multiplied in (exact in
-// bf16), so everything after the ring is the same.
+// 384.  Shared memory: two Q tiles (the result leaves through their place, a row
+// at a time) and the ring, rows of 64 elements (128 bytes) swizzled in atoms of 8
+// rows; K is read K-major, V (same layout) N-major.  A 16-bit cache comes by
+// tiled copies where pages allow (make_maps), else by 16-byte copies of any
+// strides and page size; e4m3 through registers, the scale multiplied in (exact
+// in bf16), so everything after the ring is the same.
 //
 // Keys past the end are zero rows and masked; draft rows of V that are not
 // finite would reach every row of the product (0 * NaN), so such elements are
 // zeroed in the ring and noted, and added at the end to the rows that see them.
+//
+// What bounds it.  64 x 64 as above (414 GFLOP, 1.7 GB): 400 us, 1.0 PFLOP/s, the
+// tensor pipe active 47% of the time and the issue slots 48%: the rest is the
+// chain softmax - product - next S of two streams, and 15 us an item for Q, the
+// masked tiles and the result.  17 nodes over 131,000 tokens: 103 us, 5.2 TB/s.
+// 16 requests of 8 nodes: 63 us, 2.8 TB/s, the ring's five slots against the
+// copies' latency (long scoreboard 7.5 of 15 warp cycles an issue).
 #include "tree_items.cuh"
 
 namespace dspark {
@@ -52,7 +68,8 @@ struct Roles {
 constexpr int kLag = 2;                 // slots a producer issues ahead of the one it completes
 constexpr int kBadSets = 8;             // segments the producers can be ahead, rounded up
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
-// An item's Q, result and way into the loop take as long as about three tiles.
+// An item's Q, result and way into the loop take as long as about three tiles (16
+// requests of 8 nodes: 1 65 us, 3 63, 6 68; 13 trees over e4m3: 49.7, 49.6, 55.6).
 using Item = Work<kKeys, kGroupRows, 3>;
 using Segment = Item::Segment;
 using Walker = Item::Walker;
@@ -1020,7 +1037,9 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1)
 // of a part's slot p takes every (P x kJoinSplit)-th of its pieces, or of groups of
 // eight where one warp joins a piece alone (up to kJoinAlone parts).  With more
 // parts the warps of a block take every eighth one and are then added in order:
-// the result does not depend on timing.
+// the result does not depend on timing.  Alone for none / 4 / 8 / any number: 13
+// trees 58.8 / 49.8 / 47.9 / 48.2 us, 64 x 64 431 / 404 / 405 / 397 (up to 3 parts),
+// 17 nodes over 131,000 tokens (20 parts) 106 / 102.7 / 102.7 / 114.3.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinSplit = 4;
 constexpr int kJoinAlone = 8;

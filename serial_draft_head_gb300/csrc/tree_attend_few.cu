@@ -1,5 +1,5 @@
-// tree_attend_few.cu -- attention of few drafted rows (at most 16 a cached head:
-// single tokens, short chains) over a paged cache.
+// tree_attend_few.cu -- attention of few drafted rows (single tokens, short
+// chains: dspark_tree_attend has the rule) over a paged cache.
 //
 // Items are 16 rows by blocks of 16 (e4m3: 32) keys, a worker is a CTA (tree_items.cuh
 // says how the work is cut, and the mathematics).  The warps of a CTA take a
@@ -29,6 +29,14 @@
 // handle's type, code times scale as the cache reads back.  bf16 rows of Q are
 // brought to f16 by a power of two a row (exact for elements down to 2^-32 of the
 // row's largest, below that to 2^-40 of it).
+//
+// What bounds it.  128 single tokens of 500 to 9,000 over e4m3 (64 heads on 8):
+// 318 us, 3.7 TB/s; DRAM at 1.04 times the cache's bytes, 840 warp instructions a
+// block of 32 keys (conversions, the products, V's scales), issued at 34% of the
+// slots by the three warps a scheduler that registers and rings leave, held by
+// fixed latencies.  The same over bf16 up to 5,000 tokens: 299 us, 4.8 TB/s.  One
+// token over 517: 12 us on the device, a chain of dependent steps (lengths, page,
+// K, the warps' meeting, the other CTAs' parts).
 #include "tree_items.cuh"
 
 namespace dspark {

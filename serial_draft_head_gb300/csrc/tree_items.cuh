@@ -8,9 +8,11 @@
 // before an item's first for what it costs beside its tiles (Q, the result, the
 // way into the loop).  The units of all items, in order, are split evenly over
 // the workers (one CTA a SM): the lengths are known on the device only, so every
-// CTA sums them up itself.  An item that lies inside one worker's share is finished there; one
-// that several workers share leaves parts (unnormalised O, maximum, sum), joined
-// by a second kernel in the order of the keys.
+// CTA sums them up itself.  An item that lies inside one worker's share is
+// finished there; one that several workers share leaves parts (unnormalised O,
+// maximum, sum), joined in an order that does not depend on timing: by the CTA
+// that is last to leave its part (few rows: 16 rows a part), or by a second kernel
+// over all SMs (tcgen05: up to 256 rows a part, and 20 parts an item).
 //
 // Mathematics, per row, one pass over the tiles in the base-2 exponent:
 //   x_j = log2(e) * scale * q.k_j              (capped: log2(e) c tanh(s / c))
