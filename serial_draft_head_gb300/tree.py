@@ -34,7 +34,6 @@ _TYPES = {torch.bfloat16: TYPE_BF16, torch.float16: TYPE_F16, torch.float8_e4m3f
 EXPORTS = ["dspark_tree_create", "dspark_tree_write", "dspark_tree_read", "dspark_tree_keep",
            "dspark_tree_attend", "dspark_tree_status", "dspark_tree_destroy"]
 
-_i64x2 = ctypes.c_int64 * 2
 _i64x3 = ctypes.c_int64 * 3
 
 
@@ -58,6 +57,7 @@ class dspark_tree_batch(ctypes.Structure):
 
 
 _pack_batch = struct.Struct("@PPPqiii").pack_into      # dspark_tree_batch
+_pack_strides = struct.Struct("@qq").pack_into
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") \
     else lambda index: torch.cuda.current_stream(index).cuda_stream
 _int32 = torch.int32
@@ -71,14 +71,12 @@ def load():
     if _lib is None:
         L = walk.load()
         vp, i64, i32, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
-        pc, pb = ctypes.POINTER(dspark_tree_cache), ctypes.POINTER(dspark_tree_batch)
+        # structs and arrays go by address: ctypes converts an int fastest
         L.dspark_tree_create.argtypes = [ctypes.POINTER(dspark_tree_config), ctypes.POINTER(vp)]
-        L.dspark_tree_write.argtypes = [vp, pc, pb, vp, ctypes.POINTER(i64), vp,
-                                        ctypes.POINTER(i64), vp]
-        L.dspark_tree_read.argtypes = [vp, pc, pb, vp, vp, vp]
-        L.dspark_tree_keep.argtypes = [vp, pc, pb, vp, i64, i32, vp, vp]
-        L.dspark_tree_attend.argtypes = [vp, pc, pb, vp, ctypes.POINTER(i64), vp, i64, i32, f32,
-                                         f32, vp, vp, vp]
+        L.dspark_tree_write.argtypes = [vp] * 8
+        L.dspark_tree_read.argtypes = [vp] * 6
+        L.dspark_tree_keep.argtypes = [vp, vp, vp, vp, i64, i32, vp, vp]
+        L.dspark_tree_attend.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, f32, f32, vp, vp, vp]
         L.dspark_tree_status.argtypes = [vp, vp]
         L.dspark_tree_destroy.argtypes = [vp]
         for name in EXPORTS:
@@ -121,7 +119,7 @@ class KVCache:
         self.kv_heads, self.head_dim = k.shape[2], k.shape[3]
         self.key = (k.get_device(), self.kv_heads, self.head_dim, self.dtype)
         self.c = c
-        self.ref = ctypes.byref(c)
+        self.address = ctypes.addressof(c)
 
 
 def ancestor_bits(parent, first):
@@ -173,42 +171,51 @@ class Tree:
         self._scale = head_dim ** -0.5
         self._batch = dspark_tree_batch()
         self._batch_mem = (ctypes.c_char * ctypes.sizeof(self._batch)).from_buffer(self._batch)
-        self._batch_ref = ctypes.byref(self._batch)
-        self._s0, self._s1 = _i64x2(), _i64x2()
+        self._batch_at = ctypes.addressof(self._batch)
+        self._strides = (ctypes.c_char * 32)()       # two rows' {token, head}
+        self._s0 = ctypes.addressof(self._strides)
+        self._s1 = self._s0 + 16
 
     # ---- argument marshalling: a few microseconds a call matter here ----
 
     def _cache(self, cache):
         if cache.key != self._key and cache.key != self._key_e4m3:
             raise ValueError("the cache has the handle's device, heads, head_dim and type (or e4m3)")
-        return cache.ref
+        return cache.address
 
     def _requests(self, pages, start, first, n_rows):
         i = self._index
-        if not (pages.dtype is _int32 and pages.get_device() == i and pages.dim() == 2
-                and start.dtype is _int32 and start.get_device() == i and start.dim() == 1):
+        try:
+            B, width = pages.shape
+            row, one = pages.stride()
+            n, = start.shape
+            step, = start.stride()
+        except ValueError:
+            n = B = -1
+        if not (n == B >= 0 and pages.dtype is _int32 and start.dtype is _int32
+                and pages.get_device() == i and start.get_device() == i):
             raise ValueError("pages is int32 [B, P] and lengths int32 [B], on the handle's device")
-        B, width = pages.shape
-        row, one = pages.stride()
-        if (one != 1 and width > 1) or start.shape[0] != B or (B > 1 and start.stride(0) != 1):
+        if (one != 1 and width > 1) or (step != 1 and B > 1):
             raise ValueError("pages and lengths have one row a request, entries next to each other")
         f = 0
         if first is not None:
-            if not (first.dtype is _int32 and first.get_device() == i and first.dim() == 1
-                    and first.shape[0] == B + 1 and (B == 0 or first.stride(0) == 1)):
+            if not (first.dtype is _int32 and first.get_device() == i and first.shape == (B + 1,)
+                    and (B == 0 or first.stride(0) == 1)):
                 raise ValueError("first is int32 [B + 1] on the handle's device")
             f = first.data_ptr()
         _pack_batch(self._batch_mem, 0, pages.data_ptr(), start.data_ptr(), f, row, width, B, n_rows)
-        return self._batch_ref
+        return self._batch_at
 
-    def _rows(self, t, heads, strides, what):
-        if not (t.dtype is self.dtype and t.get_device() == self._index and t.dim() == 3):
+    def _rows(self, t, heads, at, what):
+        try:
+            n, h, d = t.shape
+            s0, s1, s2 = t.stride()
+        except ValueError:
+            raise ValueError(what) from None
+        if not (h == heads and d == self.head_dim and (s2 == 1 or d == 1)
+                and t.dtype is self.dtype and t.get_device() == self._index):
             raise ValueError(what)
-        n, h, d = t.shape
-        s0, s1, s2 = t.stride()
-        if h != heads or d != self.head_dim or (s2 != 1 and d > 1):
-            raise ValueError(what)
-        strides[0], strides[1] = s0, s1
+        _pack_strides(self._strides, at, s0, s1)
         return n
 
     def _out(self, t, shape, dtype, what):
@@ -233,8 +240,8 @@ class Tree:
 
     def write(self, cache, pages, start, first, k, v, stream=None):
         """Rows first[b] + i of k and v [N, kv_heads, head_dim] to positions start[b] + i."""
-        n = self._rows(k, self.kv_heads, self._s0, "k is [N, kv_heads, head_dim] of the handle's type")
-        if self._rows(v, self.kv_heads, self._s1,
+        n = self._rows(k, self.kv_heads, 0, "k is [N, kv_heads, head_dim] of the handle's type")
+        if self._rows(v, self.kv_heads, 16,
                       "v is [N, kv_heads, head_dim] of the handle's type") != n:
             raise ValueError("k and v have as many rows")
         rc = self.lib.dspark_tree_write(
@@ -262,14 +269,18 @@ class Tree:
         """Position start[b] + path[b, i] moves to start[b] + i for i < count[b]; path int32
         [B, P'], strictly ascending in its first count[b] entries."""
         i = self._index
-        if not (path.dtype is _int32 and path.get_device() == i and path.dim() == 2
-                and count.dtype is _int32 and count.get_device() == i and count.dim() == 1):
+        try:
+            n, width = path.shape
+            row, one = path.stride()
+            m, = count.shape
+            step, = count.stride()
+        except ValueError:
+            n, m = -1, -2
+        if not (n >= 0 and path.dtype is _int32 and path.get_device() == i
+                and count.dtype is _int32 and count.get_device() == i):
             raise ValueError("path is int32 [B, n] and count int32 [B], on the handle's device")
         batch = self._requests(pages, start, None, 0)
-        n, width = path.shape
-        row, one = path.stride()
-        if not (n == count.shape[0] == pages.shape[0] and (one == 1 or width <= 1)
-                and (n <= 1 or count.stride(0) == 1)):
+        if not (n == m == len(pages) and (one == 1 or width <= 1) and (step == 1 or n <= 1)):
             raise ValueError("one path and count a request, entries next to each other")
         rc = self.lib.dspark_tree_keep(self.h, self._cache(cache), batch, path.data_ptr(), row, width,
                                        count.data_ptr(), self._stream(stream))
@@ -282,7 +293,7 @@ class Tree:
         length[b] + T_b - 1 of their requests.  mask int32 [N, words] (see `ancestor_bits`) or
         None for chains.  scale: 1 / sqrt(head_dim) unless given.  softcap c > 0: scores become
         c tanh(s / c).  Returns (out [N, q_heads, head_dim], lse float32 [N, q_heads])."""
-        n = self._rows(q, self.q_heads, self._s0, "q is [N, q_heads, head_dim] of the handle's type")
+        n = self._rows(q, self.q_heads, 0, "q is [N, q_heads, head_dim] of the handle's type")
         shape = q.shape
         if out is None:
             out = self._empty(shape, self.dtype, stream)
