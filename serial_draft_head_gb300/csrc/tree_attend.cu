@@ -976,6 +976,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   Tail* sh = reinterpret_cast<Tail*>(smem + Layout<DP>::kTail);
   const int warp = threadIdx.x / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == R::kMmaWarp) {
     ptx::tmem_alloc(&sh->tmem, 512);
@@ -1153,20 +1154,23 @@ constexpr size_t smem_bytes() {
 
 template <bool F16, bool E4M3, int DP>
 cudaError_t launch(const AttendArgs& a, const TileMaps& maps, cudaStream_t stream) {
-  attend_kernel<F16, E4M3, DP>
-      <<<a.n_cta, Roles<E4M3>::kThreads, smem_bytes<DP>(), stream>>>(a, maps);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  // the join may be set up while the main kernel runs; it waits for it itself
+  // either kernel is set up while the one before it ends (the join: runs), and waits
+  // for it itself
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(2 * a.n_cta, kJoinSplit);
-  cfg.blockDim = dim3(kJoinThreads);
+  cfg.gridDim = dim3(a.n_cta);
+  cfg.blockDim = dim3(Roles<E4M3>::kThreads);
+  cfg.dynamicSmemBytes = smem_bytes<DP>();
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, attend_kernel<F16, E4M3, DP>, a, maps);
+  if (e != cudaSuccess) return e;
+  cfg.dynamicSmemBytes = 0;
+  cfg.gridDim = dim3(2 * a.n_cta, kJoinSplit);
+  cfg.blockDim = dim3(kJoinThreads);
   return cudaLaunchKernelEx(&cfg, join_kernel<F16, DP>, a);
 }
 

@@ -316,6 +316,7 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
   uint8_t* ring = smem + warp * L::kRing;
   uint4* q_mem = reinterpret_cast<uint4*>(smem + L::kQ);
   uint8_t* scales = smem + L::kScales + warp * L::kStages * L::kScaleBytes;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (threadIdx.x < DSPARK_TREE_MAX_NODES / 32) st.bad[threadIdx.x] = 0;
   Item::template plan<L::kThreads>(a, &st.share, st.sums);
 
@@ -851,8 +852,19 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
 template <bool F16, bool E4M3, int DP>
 cudaError_t launch(const AttendArgs& a, cudaStream_t stream) {
   using L = Few<E4M3, DP>;
-  few_kernel<F16, E4M3, DP><<<a.n_cta, L::kThreads, L::kSmem, stream>>>(a);
-  return cudaGetLastError();
+  // set up while the kernel before it in the stream ends, which it waits for before
+  // it reads anything (calls in a row: 14.3 to 12.3 us for 1 token)
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(a.n_cta);
+  cfg.blockDim = dim3(L::kThreads);
+  cfg.dynamicSmemBytes = L::kSmem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, few_kernel<F16, E4M3, DP>, a);
 }
 
 template <bool F16, bool E4M3, int DP>
