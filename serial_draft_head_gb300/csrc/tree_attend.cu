@@ -16,8 +16,8 @@
 // S and P share columns and tensor memory is full, so the next S cannot be made
 // before P has been used.  A pair therefore goes by halves of 64 keys: one half's
 // S is made while the softmax is at the other (64 requests of 64 nodes, 4,096 to
-// 8,192 tokens: 400 us, 426 with whole tiles).  Alternate tiles stay whole: with
-// few rows the copies bound, and halves hold their slots longer (63 us against 75
+// 8,192 tokens: 402 us, 426 with whole tiles).  Alternate tiles stay whole: with
+// few rows the copies bound, and halves hold their slots longer (64 us against 75
 // for 16 requests of 8 nodes).
 //
 // Tensor memory (512 columns): S/P of the streams at 0 and 128, O at 256 and
@@ -32,11 +32,11 @@
 // finite would reach every row of the product (0 * NaN), so such elements are
 // zeroed in the ring and noted, and added at the end to the rows that see them.
 //
-// What bounds it.  64 x 64 as above (414 GFLOP, 1.7 GB): 400 us, 1.0 PFLOP/s, the
+// What bounds it.  64 x 64 as above (414 GFLOP, 1.7 GB): 400 to 415 us, 1.0 PFLOP/s, the
 // tensor pipe active 47% of the time and the issue slots 48%: the rest is the
 // chain softmax - product - next S of two streams, and 15 us an item for Q, the
-// masked tiles and the result.  17 nodes over 131,000 tokens: 103 us, 5.2 TB/s.
-// 16 requests of 8 nodes: 63 us, 2.8 TB/s, the ring's five slots against the
+// masked tiles and the result.  17 nodes over 131,000 tokens: 101 us, 5.3 TB/s.
+// 16 requests of 8 nodes: 61 us, 2.9 TB/s, the ring's five slots against the
 // copies' latency (long scoreboard 7.5 of 15 warp cycles an issue).
 #include "tree_items.cuh"
 

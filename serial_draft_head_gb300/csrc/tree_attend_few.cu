@@ -31,10 +31,10 @@
 // row's largest, below that to 2^-40 of it).
 //
 // What bounds it.  128 single tokens of 500 to 9,000 over e4m3 (64 heads on 8):
-// 318 us, 3.7 TB/s; DRAM at 1.04 times the cache's bytes, 840 warp instructions a
+// 315 us, 3.7 TB/s; DRAM at 1.04 times the cache's bytes, 840 warp instructions a
 // block of 32 keys (conversions, the products, V's scales), issued at 34% of the
 // slots by the three warps a scheduler that registers and rings leave, held by
-// fixed latencies.  The same over bf16 up to 5,000 tokens: 299 us, 4.8 TB/s.  One
+// fixed latencies.  The same over bf16 up to 5,000 tokens: 293 us, 4.9 TB/s.  One
 // token over 517: 12 us on the device, a chain of dependent steps (lengths, page,
 // K, the warps' meeting, the other CTAs' parts).
 #include "tree_items.cuh"
