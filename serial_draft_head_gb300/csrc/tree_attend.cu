@@ -116,8 +116,10 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 // return at once, the loops run on without starting copies or products (all
 // accesses stay in bounds), and the status says so.
 //
-// A parity wait tells a phase from the next one only, so whoever waits on a
-// barrier waits for each of its phases in order.
+// A parity wait tells a phase from the next one only.  So whoever waits on a
+// barrier waits for each of its phases in order (or knows that the one before is
+// over), and no phase can end before all lanes that wait for the one before it
+// have seen that: what ends it depends on an arrival of theirs.
 __device__ __forceinline__ void wait_long(Tail* s, uint64_t* bar, uint32_t parity, int* status) {
   const uint64_t t0 = globaltimer_ns();
   uint32_t spins = 0;
@@ -236,6 +238,7 @@ __device__ __forceinline__ void produce16(const AttendArgs& a, const TileMaps& m
       uint8_t* dst = ring + at.slot * L::kTile;
       wait(sh, &sh->empty[at.slot], at.phase ^ 1, a.status);
       if (tiled) {
+        __syncwarp();                            // every lane's wait is over
         if (lane == 0) {
           // after an abort no copy may outlive the CTA: none is started
           if (warp < boxes && !aborted(sh)) {
@@ -468,9 +471,13 @@ __device__ __forceinline__ void issue(const AttendArgs& a, uint8_t* smem, Tail* 
   auto filled = [&]() {                          // whether the next slot is
     return __any_sync(0xffffffffu, ptx::mbar_test_wait(&sh->full[at.slot], at.phase)) != 0;
   };
-  auto release = [&](uint32_t slot) {
-    ptx::tc_commit(&sh->empty[slot]);
-    if (!pair) ptx::tc_commit(&sh->empty[slot]);           // the other stream's share
+  // a slot is free when both streams have let go of it: by the products that read
+  // it, or, for one that is only passed, by this warp after its wait.  So no slot
+  // is refilled, and no phase runs on, before both have seen it filled.
+  auto release = [&](uint32_t slot) { ptx::tc_commit(&sh->empty[slot]); };
+  auto pass = [&](uint32_t slot) {
+    __syncwarp();                                // every lane's wait is over
+    if (threadIdx.x % 32 == 0) ptx::mbar_arrive(&sh->empty[slot]);
   };
   auto scores = [&](uint32_t slot, int h, bool all) {      // S of half a tile, or of all of it
     if (!aborted(sh)) {
@@ -547,8 +554,10 @@ __device__ __forceinline__ void issue(const AttendArgs& a, uint8_t* smem, Tail* 
         const uint32_t k_slot = take();
         const bool own = (i & 1) == stream;
         if (own) scores(k_slot, 0, true);
+        else pass(k_slot);
         const uint32_t v_slot = take();
         if (own) values(v_slot, 0, i > 1);
+        else pass(v_slot);
       }
     }
     if (threadIdx.x % 32 == 0) ptx::mbar_arrive(&sh->q_empty);

@@ -1,0 +1,32 @@
+"""The draft-check operators at their edges: barriers' phases under load, streams, sizes near what
+indexes hold, masked and visible values that are not finite, scales and caps of any size."""
+import math
+
+import pytest
+import torch
+
+import tree_reference as ref
+from test_gpu_tree import BF16, E4M3, F16, Case, tree  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("D,page,cache", [(128, 64, "16"), (128, 16, "16"), (64, 64, "16"), (64, 24, "16"),
+                                          (128, 64, "e4m3"), (64, 24, "e4m3")])
+def test_attend_alternate_tiles_back_to_back(tree, D, page, cache):
+    """One row tile (two streams in turn over the same ring): segments of one tile to many, so that a
+    stream passes slots quickly while the other works; calls in a row without a wait.  The same bits
+    every time, and no wait runs out."""
+    T = [9, 14, 30, 9, 11, 25]
+    cases = [Case(tree, 8, 2, D, page, BF16, cache, T, L, seed=200 + i, spare=1)
+             for i, L in enumerate([[0, 100, 129, 20000, 5, 640], [7000, 1, 260, 130, 131, 9000],
+                                    [120, 119, 118, 117, 116, 115]])]
+    want = []
+    for c in cases:
+        want.append(c.attend())
+        c.check(*want[-1])
+    for _ in range(40):
+        got = [c.tree.attend(c.q, c.cache, c.pages, c.length, c.first, mask=c.mask) for c in cases * 3]
+        for i, (o, l) in enumerate(got):
+            assert torch.equal(o, want[i % 3][0]) and torch.equal(l, want[i % 3][1])
+    assert all(c.tree.status() == 0 for c in cases)
