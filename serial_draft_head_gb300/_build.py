@@ -1,5 +1,6 @@
 """Build the CUDA library (libdspark_walk.so) in-tree with nvcc for sm_103a."""
 import os
+import re
 import shutil
 import subprocess
 from concurrent.futures import ThreadPoolExecutor
@@ -28,6 +29,22 @@ def _deps():
     return files
 
 
+def check_registers(log):
+    """Kernels whose warps hand registers to each other (setmaxnreg) count on a number of them at
+    launch, which `__launch_bounds__` sets and their name ends with: `log`, the assembler's report
+    (-Xptxas -v), has to give each of them that number.  Returns how many kernels there were."""
+    found = re.findall(r"Compiling entry function '(\w+)'.*?Used (\d+) registers", log, flags=re.S)
+    counted = 0
+    for name, used in found:
+        want = re.search(r"attend_kernelI(?:L[a-z]\w+?E)*Li(\d+)EEE", name)
+        if want:
+            counted += 1
+            if int(want.group(1)) != int(used):
+                raise RuntimeError("%s counts on %s registers a thread at launch, the compiler gave "
+                                   "it %s" % (name, want.group(1), used))
+    return counted
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile every .cu under csrc/ and link the shared library."""
     if not force and os.path.exists(LIB):
@@ -36,9 +53,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
             return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
     flags = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
-                    "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
-    if verbose:
-        flags += ["-Xptxas", "-v"]
+                    "--expt-relaxed-constexpr", "-Xptxas", "-v", "-I", os.path.join(ROOT, "include")]
 
     def compile_one(src):
         obj = os.path.join(OUT_DIR, os.path.basename(src)[:-3] + ".o")
@@ -46,6 +61,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         res = subprocess.run(cmd, capture_output=True, text=True)
         if res.returncode != 0:
             raise RuntimeError("nvcc failed on %s:\n%s" % (src, res.stderr))
+        check_registers(res.stderr)
         return obj, res.stderr
 
     with ThreadPoolExecutor(max_workers=min(8, len(sources()))) as ex:

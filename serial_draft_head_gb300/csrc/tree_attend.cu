@@ -978,7 +978,9 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
   }
 }
 
-template <bool F16, bool E4M3, int DP>
+// REGS: the registers a thread that the roles' split counts on at launch.  In the
+// kernel's name, where the build checks it against what the compiler gave.
+template <bool F16, bool E4M3, int DP, int REGS>
 __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1)
     attend_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ TileMaps maps) {
   using R = Roles<E4M3>;
@@ -1020,14 +1022,14 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   if (warp < kSoftWarps) {
-    ptx::set_registers<R::kLaunchRegs, R::kSoftRegs>();
+    ptx::set_registers<REGS, R::kSoftRegs>();
     softmax<F16, E4M3, DP>(a, smem, sh);
   } else if (warp < R::kMmaWarp) {
-    ptx::set_registers<R::kLaunchRegs, R::kProdRegs>();
+    ptx::set_registers<REGS, R::kProdRegs>();
     if (E4M3) produce8<F16, DP>(a, smem, sh);
     else produce16<F16, DP>(a, maps, smem, sh);
   } else {
-    ptx::set_registers<R::kLaunchRegs, R::kMmaRegs>();
+    ptx::set_registers<REGS, R::kMmaRegs>();
     if (warp < R::kMmaWarp + 2) issue<F16, DP>(a, smem, sh, warp - R::kMmaWarp);
     else if (warp == R::kMmaWarp + 2) place_parts(a, sh);
   }
@@ -1175,7 +1177,8 @@ cudaError_t launch(const AttendArgs& a, const TileMaps& maps, cudaStream_t strea
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, attend_kernel<F16, E4M3, DP>, a, maps);
+  cudaError_t e = cudaLaunchKernelEx(
+      &cfg, attend_kernel<F16, E4M3, DP, Roles<E4M3>::kLaunchRegs>, a, maps);
   if (e != cudaSuccess) return e;
   cfg.dynamicSmemBytes = 0;
   cfg.gridDim = dim3(2 * a.n_cta, kJoinSplit);
@@ -1183,16 +1186,10 @@ cudaError_t launch(const AttendArgs& a, const TileMaps& maps, cudaStream_t strea
   return cudaLaunchKernelEx(&cfg, join_kernel<F16, DP>, a);
 }
 
-// Shared memory, and that the launch brings the registers that the roles split.
 template <bool F16, bool E4M3, int DP>
 cudaError_t setup() {
   static_assert(smem_bytes<DP>() <= 232448, "shared memory of an SM");
-  using R = Roles<E4M3>;
-  cudaFuncAttributes fa;
-  cudaError_t e = cudaFuncGetAttributes(&fa, attend_kernel<F16, E4M3, DP>);
-  if (e != cudaSuccess) return e;
-  if (fa.numRegs != R::kLaunchRegs) return cudaErrorInvalidConfiguration;
-  return cudaFuncSetAttribute(attend_kernel<F16, E4M3, DP>,
+  return cudaFuncSetAttribute(attend_kernel<F16, E4M3, DP, Roles<E4M3>::kLaunchRegs>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<DP>());
 }
 
