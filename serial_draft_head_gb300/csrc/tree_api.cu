@@ -35,6 +35,18 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 bool stride_ok(int64_t s, int es) { return s >= 0 && s <= ((int64_t)1 << 40) && s * es % 16 == 0; }
 
+// Zeroes device memory before it returns, on a stream of its own: a memset alone is
+// not waited for by the host, and kernels on streams of all kinds come after it.
+cudaError_t clear(void* p, size_t bytes) {
+  cudaStream_t s = nullptr;
+  cudaError_t e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+  if (e != cudaSuccess) return e;
+  e = cudaMemsetAsync(p, 0, bytes, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  const cudaError_t d = cudaStreamDestroy(s);
+  return e != cudaSuccess ? e : d;
+}
+
 // The calls work on the current device: it has to be the handle's.
 int check_device(const dspark_tree* h) {
   int dev = -1;
@@ -165,7 +177,7 @@ int dspark_tree_create(const dspark_tree_config* cfg, dspark_tree_t* out) {
     h->part_of = reinterpret_cast<int4*>(p + o_bytes + ml_bytes);
     e = cudaMalloc(&h->status, (1 + sms) * sizeof(int));
   }
-  if (e == cudaSuccess) e = cudaMemset(h->status, 0, (1 + sms) * sizeof(int));
+  if (e == cudaSuccess) e = clear(h->status, (1 + sms) * sizeof(int));
   if (e == cudaSuccess) {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;

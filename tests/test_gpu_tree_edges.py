@@ -30,3 +30,24 @@ def test_attend_alternate_tiles_back_to_back(tree, D, page, cache):
         for i, (o, l) in enumerate(got):
             assert torch.equal(o, want[i % 3][0]) and torch.equal(l, want[i % 3][1])
     assert all(c.tree.status() == 0 for c in cases)
+
+
+def test_attend_at_once_on_a_side_stream_of_a_new_handle(tree):
+    """A handle made while the default stream is busy, and used on another stream at once: items of
+    many parts go by counts that the making of the handle has cleared."""
+    c = Case(tree, 8, 2, 128, 16, BF16, "16", [1, 2, 1], [20000, 37, 900], seed=210)
+    out, lse = c.attend()
+    c.check(out, lse)
+    x = torch.randn(8192, 8192, device="cuda").to(BF16)
+    y = torch.empty_like(x)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for _ in range(40):                        # some 20 ms of queue
+            torch.matmul(x, x, out=y)
+        t = tree.Tree(8, 2, 128, BF16, max_requests=3, max_nodes=2)
+        o2, l2 = t.attend(c.q, c.cache, c.pages, c.length, c.first, mask=c.mask, stream=side)
+        side.synchronize()
+        assert torch.equal(out, o2) and torch.equal(lse, l2)
+        assert t.status(stream=side) == 0
+        t.close()

@@ -1,0 +1,47 @@
+"""What the tree operators' C calls ask of the CUDA runtime, against a fake of it (no GPU)."""
+import json
+import os
+import subprocess
+import sys
+
+import pytest
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+
+
+@pytest.fixture(scope="session")
+def calls(tmp_path_factory):
+    """Runs a list of calls (see fake_tree.py); the results and each call's log."""
+    from serial_draft_head_gb300 import tree, walk
+    tree.load()
+    fake = str(tmp_path_factory.mktemp("fake") / "fake_cudart.so")
+    subprocess.run(["gcc", "-shared", "-fPIC", "-O1", "-o", fake, os.path.join(HERE, "fake_cudart.c")],
+                   check=True)
+
+    def run(what):
+        res = subprocess.run([sys.executable, os.path.join(HERE, "fake_tree.py"), walk.library_path(), fake],
+                             input=json.dumps(what), capture_output=True, text=True, timeout=120)
+        assert res.returncode == 0, res.stderr
+        return json.loads(res.stdout)
+
+    return run
+
+
+def create(**kw):
+    from serial_draft_head_gb300 import tree
+    cfg = tree.dspark_tree_config(**{**dict(q_heads=8, kv_heads=2, head_dim=64, type=0, max_requests=4,
+                                            max_nodes=64), **kw})
+    return ["dspark_tree_create", {"bytes": bytes(cfg).hex()}, "out"]
+
+
+def test_create_returns_with_its_memory_cleared(calls):
+    """The status word and the counts that kernels on any stream go by are zero before the handle is
+    there to be used: what clears them has been waited for, and waits for no work of others."""
+    (rc, log), = calls([create()])
+    assert rc == 0
+    cleared = [i for i, line in enumerate(log) if line.startswith("memset")]
+    assert cleared
+    for i in cleared:
+        stream = log[i].split()[2]
+        assert any(line.startswith("synchronise stream %s " % stream) for line in log[i:])
+        assert stream != "0" and not any(line.startswith("synchronise all") for line in log)
