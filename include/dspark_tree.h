@@ -64,6 +64,7 @@ extern "C" {
 #define DSPARK_TREE_MAX_HEAD_DIM 128
 #define DSPARK_TREE_MAX_REQUESTS 1024
 #define DSPARK_TREE_MAX_NODES 256
+#define DSPARK_TREE_MAX_LENGTH 2147483392 /* cached rows of a request, 2^31 - 256 */
 
 typedef struct dspark_tree dspark_tree;
 typedef dspark_tree *dspark_tree_t;
@@ -100,7 +101,8 @@ struct dspark_tree_cache {
 /*
  * The requests of one call, all arrays on the device: pages int32, max_pages
  * entries a request, the requests' rows pages_stride entries apart (max_pages *
- * page_size < 2^31), start int32 [B] (the position of the request's first row), first
+ * page_size < 2^31; positions from DSPARK_TREE_MAX_LENGTH on are not used), start int32 [B]
+ * (the position of the request's first row), first
  * int32 [B + 1] (the request's rows are first[b] .. first[b+1]-1 of the packed
  * arrays).  N: rows of the packed arrays.
  */

@@ -127,7 +127,8 @@ int make_batch(const dspark_tree_batch* b, int page_size, bool rows, BatchView* 
   out->start = b->start;
   out->first = b->first;
   out->pages_stride = b->pages_stride;
-  out->max_pos = max_pos;
+  // a tile of keys past the last position still has a 32-bit place
+  out->max_pos = max_pos < DSPARK_TREE_MAX_LENGTH ? max_pos : DSPARK_TREE_MAX_LENGTH;
   out->B = b->B;
   out->N = rows ? b->N : 0;
   return DSPARK_OK;

@@ -62,7 +62,7 @@ struct BatchView {
   const int32_t* start;
   const int32_t* first;
   int64_t pages_stride;
-  int64_t max_pos;           // max_pages * page_size < 2^31
+  int64_t max_pos;           // max_pages * page_size, at most DSPARK_TREE_MAX_LENGTH
   int B, N;
 };
 

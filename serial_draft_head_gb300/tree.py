@@ -28,6 +28,7 @@ TYPE_E4M3 = 2
 TREE_MAX_HEAD_DIM = 128
 TREE_MAX_REQUESTS = 1024
 TREE_MAX_NODES = 256
+TREE_MAX_LENGTH = 2147483392
 
 _TYPES = {torch.bfloat16: TYPE_BF16, torch.float16: TYPE_F16, torch.float8_e4m3fn: TYPE_E4M3}
 

@@ -51,3 +51,27 @@ def test_attend_at_once_on_a_side_stream_of_a_new_handle(tree):
         assert torch.equal(out, o2) and torch.equal(lse, l2)
         assert t.status(stream=side) == 0
         t.close()
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_attend_positions_near_what_an_index_holds(tree, T):
+    """All positions are one slot (strides of zero), so that a cache of 2^31 - 1 rows fits: a request
+    that would end past the longest length is left out and reported, its neighbour runs."""
+    from serial_draft_head_gb300 import walk
+    g = torch.Generator(device="cuda")
+    g.manual_seed(220)
+    slots, most = 2 ** 31 - 1, tree.TREE_MAX_LENGTH
+    k, v, q = (torch.randn(n, 1, 64, generator=g, device="cuda").to(BF16) for n in (1, 1, 2 * T))
+    cache = tree.KVCache(k[:, None].expand(1, slots, 1, 64), v[:, None].expand(1, slots, 1, 64))
+    t = tree.Tree(1, 1, 64, BF16, max_requests=2, max_nodes=T)
+    pages = torch.zeros(2, 1, dtype=torch.int32, device="cuda")
+    first = torch.tensor([0, T, 2 * T], dtype=torch.int32, device="cuda")
+    s = (q.double() @ k[0, 0].double() / 8)[:, 0]
+    for past in (slots - T, most - T + 1):
+        length = torch.tensor([past, 77], dtype=torch.int32, device="cuda")
+        out = torch.full((2 * T, 1, 64), 5.0, dtype=BF16, device="cuda")
+        _, lse = t.attend(q, cache, pages, length, first, out=out)
+        assert t.status() == walk.EPAGES
+        assert (out[:T] == 5).all() and torch.equal(out[T:], v.expand(T, 1, 64))
+        n = 78 + torch.arange(T, device="cuda")
+        assert (lse[T:, 0].double() - s[T:] - n.double().log()).abs().max() < 1e-4
