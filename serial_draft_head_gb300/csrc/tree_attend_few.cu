@@ -564,19 +564,19 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
           x[kg][3] *= s1;
         }
       }
+      uint32_t see[2] = {~0u, ~0u};              // bit 8 kg + e: rows g and g + 8 see the key
       if (masked) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int row = 8 * h + g;
           const int nd = a.group.div(s.group * L::kRows + (row < rows ? row : 0));
-          const uint32_t see =
-              sees_32(a.mask ? a.mask + (int64_t)(s.row0 + nd) * a.mask_stride : nullptr, s.rows,
-                      nd, pos0 - start) >> (2 * q);
+          see[h] = sees_32(a.mask ? a.mask + (int64_t)(s.row0 + nd) * a.mask_stride : nullptr, s.rows,
+                           nd, pos0 - start) >> (2 * q);
 #pragma unroll
           for (int kg = 0; kg < kGroups; ++kg)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-              if (!((see >> (8 * kg + e)) & 1)) x[kg][2 * h + e] = -INFINITY;
+              if (!((see[h] >> (8 * kg + e)) & 1)) x[kg][2 * h + e] = -INFINITY;
         }
       }
       float mx[2];
@@ -631,10 +631,21 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
               x[kg][2 * h + e] = fmaf(x[kg][2 * h + e], row_mul[h], -sub);
         }
 #pragma unroll
+        for (int kg = 0; kg < kGroups; ++kg)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) x[kg][2 * h + e] = ex2(x[kg][2 * h + e]);
+        // by the bits: an invisible key's exponent can be anything (-infinity times a
+        // scale of zero)
+        if (masked) {
+#pragma unroll
+          for (int kg = 0; kg < kGroups; ++kg)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (!((see[h] >> (8 * kg + e)) & 1)) x[kg][2 * h + e] = 0.f;
+        }
+#pragma unroll
         for (int kg = 0; kg < kGroups; ++kg) {
-          float &w0 = x[kg][2 * h], &w1 = x[kg][2 * h + 1];
-          w0 = ex2(w0);
-          w1 = ex2(w1);
+          const float w0 = x[kg][2 * h], w1 = x[kg][2 * h + 1];
           l[h] += w0 + w1;
           p[kg / 2][2 * (kg % 2) + h] = pack2<kHalf>(w0, w1);
         }

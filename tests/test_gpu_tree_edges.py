@@ -75,3 +75,18 @@ def test_attend_positions_near_what_an_index_holds(tree, T):
         assert (out[:T] == 5).all() and torch.equal(out[T:], v.expand(T, 1, 64))
         n = 78 + torch.arange(T, device="cuda")
         assert (lse[T:, 0].double() - s[T:] - n.double().log()).abs().max() < 1e-4
+
+
+# ---------------------------------------------------------------- scores --
+
+FEW = [1, 3, 2]                     # 2 to 6 rows a cached head of 2 query heads
+TILES = [30, 100]
+
+
+@pytest.mark.parametrize("T", [FEW, [4] * 3, TILES])
+@pytest.mark.parametrize("dtype,cache", [(BF16, "16"), (F16, "16"), (BF16, "e4m3"), (F16, "e4m3")])
+@pytest.mark.parametrize("scale", [0.0, -0.3, 2.0])
+def test_attend_scale_of_any_sign_and_zero(tree, T, dtype, cache, scale):
+    """Totals that end inside a block, in both kernels; a scale of zero weighs all visible keys alike."""
+    c = Case(tree, 4, 2, 64, 20, dtype, cache, T, [200, 45, 0][:len(T)], seed=230)
+    c.check(*c.attend(scale=scale), scale=scale)
