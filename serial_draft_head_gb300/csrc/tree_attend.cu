@@ -698,36 +698,28 @@ __device__ __noinline__ float2 softmax_any(Score sc, Tail* sh, uint64_t* o_done,
                                            int* status, uint32_t tm_s, uint32_t tm_o, int keys,
                                            uint4 see, float mref, float l) {
   const bool cap = sc.cap2 > 0.f;
-  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, mn[2] = {INFINITY, INFINITY};
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
   for (int c = 0; c < keys / 32; ++c) {
     const uint32_t m = c == 0 ? see.x : c == 1 ? see.y : c == 2 ? see.z : see.w;
     uint32_t v[32];
     ptx::tmem_ld32(tm_s + 32 * c, v);
     ptx::tmem_wait_ld32(v);
-    if (cap) {                                   // invisible ones too: see `small`
-#pragma unroll
-      for (int k = 0; k < 32; ++k) mn[k & 1] = fminf(mn[k & 1], __uint_as_float(v[k]));
-    }
 #pragma unroll
     for (int k = 0; k < 32; ++k)
       mx[k & 3] = fmaxf(mx[k & 3], (m >> k) & 1 ? __uint_as_float(v[k]) : -INFINITY);
   }
   const float raw_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
   float x_max = raw_max == -INFINITY ? -INFINITY : raw_max * sc.sl2;
-  if (cap && raw_max != -INFINITY) x_max = capped(sc, raw_max);
+  if (cap && raw_max != -INFINITY) x_max = capped(sc, raw_max, 0.f);
   mref = move_reference<F16, DP>(x_max, sh, o_done, parity, status, tm_o, mref, &l);
   const float sub = mref == -INFINITY ? 0.f : mref;
-  // Far from the cap (|y| <= 0.75 for y = s / c, in all rows of the warp) tanh(y) / y
-  // is a polynomial in y^2, fitted to it by weighted least squares to 3e-8: no
-  // special functions but the weight's own (2.0 us for 64 keys went to 1.2).
-  const float big = raw_max == -INFINITY ? 0.f : fmaxf(fabsf(raw_max), fabsf(fminf(mn[0], mn[1])));
-  const bool small = cap && __all_sync(0xffffffffu, big * sc.cap_y <= 0.75f);
-  constexpr float kTanh[6] = {1.f,           -0.333329588f, 0.133254066f,
-                              -0.0533444323f, 0.0195829086f, -0.00471625756f};
+  // capped_near, two scores at once: no special functions but the weight's own where
+  // 8 keys are far from the cap in all rows of the warp
   uint64_t coef[6];
 #pragma unroll
-  for (int i = 0; i < 6; ++i) coef[i] = pack_f32x2(sc.cap2 * kTanh[i], sc.cap2 * kTanh[i]);
+  for (int i = 0; i < 6; ++i)
+    coef[i] = pack_f32x2(sc.cap2 * tanh_coef(i), sc.cap2 * tanh_coef(i));
   const uint64_t neg = pack_f32x2(-sub, -sub);
   float sum[2] = {0.f, 0.f};
 #pragma unroll 1
@@ -736,24 +728,31 @@ __device__ __noinline__ float2 softmax_any(Score sc, Tail* sh, uint64_t* o_done,
     uint32_t v[32], pk[16];
     ptx::tmem_ld32(tm_s + 32 * c, v);
     ptx::tmem_wait_ld32(v);
-    if (small) {
+    if (cap) {
 #pragma unroll
-      for (int k = 0; k < 32; k += 2) {
-        const uint64_t y = mul_f32x2(pack_f32x2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])),
-                                     pack_f32x2(sc.cap_y, sc.cap_y));
-        const uint64_t u = mul_f32x2(y, y);
-        uint64_t t = coef[5];
+      for (int k0 = 0; k0 < 32; k0 += 8) {
+        float x[8], big = 0.f;
 #pragma unroll
-        for (int i = 4; i >= 0; --i) t = fma_f32x2(t, u, coef[i]);
-        float x0, x1;
-        unpack_f32x2(fma_f32x2(y, t, neg), &x0, &x1);
-        v[k] = __float_as_uint(x0);
-        v[k + 1] = __float_as_uint(x1);
+        for (int k = 0; k < 8; k += 2) {
+          const float r0 = __uint_as_float(v[k0 + k]), r1 = __uint_as_float(v[k0 + k + 1]);
+          big = fmaxf(big, fmaxf(fabsf(r0), fabsf(r1)));
+          const uint64_t y = mul_f32x2(pack_f32x2(r0, r1), pack_f32x2(sc.cap_y, sc.cap_y));
+          const uint64_t u = mul_f32x2(y, y);
+          uint64_t t = coef[5];
+#pragma unroll
+          for (int i = 4; i >= 0; --i) t = fma_f32x2(t, u, coef[i]);
+          unpack_f32x2(fma_f32x2(y, t, neg), &x[k], &x[k + 1]);
+        }
+        if (__any_sync(0xffffffffu, past_near(sc, big))) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float raw = __uint_as_float(v[k0 + k]);
+            if (past_near(sc, raw)) x[k] = capped_past(sc, raw, sub);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k0 + k] = __float_as_uint(x[k]);
       }
-    } else if (cap) {
-#pragma unroll
-      for (int k = 0; k < 32; ++k)
-        v[k] = __float_as_uint(capped(sc, __uint_as_float(v[k])) - sub);
     } else {
 #pragma unroll
       for (int k = 0; k < 32; ++k)

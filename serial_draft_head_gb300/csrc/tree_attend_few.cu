@@ -297,7 +297,10 @@ struct BlockCursor {
   }
 };
 
-template <bool F16, bool E4M3, int DP>
+// CAP: scores are capped.  A kernel of its own, for the capped form's code in the loop
+// costs other calls: 64 single tokens of 500 to 6,800 over a 16-bit cache, no cap, 210
+// us with it, 196 without; capped 222 (scores all far from the cap), 228 (near it).
+template <bool F16, bool E4M3, int DP, bool CAP>
 __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
     few_kernel(const __grid_constant__ AttendArgs a) {
   using L = Few<E4M3, DP>;
@@ -430,7 +433,6 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
 
   // ---- Q of a segment: lane (g, q) of two warps the chunks that meet its K
   const Score sc = Score::of(a);
-  const bool cap = sc.cap2 > 0.f;
   const int q_row = 8 * (warp - kQWarp) + g;
   uint4 qx[kQChunks];
   auto load_q = [&](const Segment& s) {
@@ -448,7 +450,7 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
   };
   auto store_q = [&]() {
     const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
-    float row_mul = cap ? 1.f : sc.sl2, r = 1.f;
+    float row_mul = CAP ? 1.f : sc.sl2, r = 1.f;
     if (E4M3 && !F16) {
       // the row's largest magnitude to [2^14, 2^15): r a power of two, exact
       uint32_t big = 0;
@@ -587,7 +589,7 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
         for (int kg = 1; kg < kGroups; ++kg)
           mx[h] = fmaxf(mx[h], fmaxf(x[kg][2 * h], x[kg][2 * h + 1]));
         mx[h] = mx[h] == -INFINITY ? -INFINITY : mx[h] * row_mul[h];
-        if (cap && mx[h] != -INFINITY) mx[h] = capped(sc, mx[h]);
+        if (CAP && mx[h] != -INFINITY) mx[h] = capped(sc, mx[h], 0.f);
       }
       // the first visible key sets a row's m, later ones when the maximum has grown enough
       const bool over = mx[0] > mref[0] + (mref[0] == -INFINITY ? 0.f : kShift + 8.f) ||
@@ -611,25 +613,33 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
         }
       }
       // weights, as the A operand of the second product
+      const float sub[2] = {mref[0] == -INFINITY ? 0.f : mref[0],
+                            mref[1] == -INFINITY ? 0.f : mref[1]};
+      if (!CAP) {
+#pragma unroll
+        for (int kg = 0; kg < kGroups; ++kg)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[kg][k] = fmaf(x[kg][k], row_mul[k / 2], -sub[k / 2]);
+      } else {
+#pragma unroll
+        for (int kg = 0; kg < kGroups; ++kg) {
+          float raw[4], big = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            raw[k] = x[kg][k] * row_mul[k / 2];
+            big = fmaxf(big, fabsf(raw[k]));
+            x[kg][k] = capped_near(sc, raw[k], sub[k / 2]);
+          }
+          if (__any_sync(0xffffffffu, past_near(sc, big))) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (past_near(sc, raw[k])) x[kg][k] = capped_past(sc, raw[k], sub[k / 2]);
+          }
+        }
+      }
       uint32_t p[kGroups / 2][4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float sub = mref[h] == -INFINITY ? 0.f : mref[h];
-        if (cap) {
-#pragma unroll
-          for (int kg = 0; kg < kGroups; ++kg)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float& v = x[kg][2 * h + e];
-              v = v == -INFINITY ? v : capped(sc, v * row_mul[h]) - sub;
-            }
-        } else {
-#pragma unroll
-          for (int kg = 0; kg < kGroups; ++kg)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              x[kg][2 * h + e] = fmaf(x[kg][2 * h + e], row_mul[h], -sub);
-        }
 #pragma unroll
         for (int kg = 0; kg < kGroups; ++kg)
 #pragma unroll
@@ -860,7 +870,7 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
   if (worst > top_page) set_status(a.status, DSPARK_EPAGES);
 }
 
-template <bool F16, bool E4M3, int DP>
+template <bool F16, bool E4M3, int DP, bool CAP>
 cudaError_t launch(const AttendArgs& a, cudaStream_t stream) {
   using L = Few<E4M3, DP>;
   // set up while the kernel before it in the stream ends, which it waits for before
@@ -875,14 +885,17 @@ cudaError_t launch(const AttendArgs& a, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, few_kernel<F16, E4M3, DP>, a);
+  return cudaLaunchKernelEx(&cfg, few_kernel<F16, E4M3, DP, CAP>, a);
 }
 
 template <bool F16, bool E4M3, int DP>
 cudaError_t setup() {
   using L = Few<E4M3, DP>;
   static_assert(L::kSmem + sizeof(FewState) + 512 <= 232448, "shared memory of an SM");
-  return cudaFuncSetAttribute(few_kernel<F16, E4M3, DP>,
+  const cudaError_t e = cudaFuncSetAttribute(
+      few_kernel<F16, E4M3, DP, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(few_kernel<F16, E4M3, DP, true>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
 }
 
@@ -892,9 +905,16 @@ cudaError_t setup_both() {
   return e != cudaSuccess ? e : setup<F16, true, DP>();
 }
 
+template <bool F16, bool E4M3, int DP>
+cudaError_t launch_cap(const AttendArgs& a, cudaStream_t stream) {
+  return a.softcap > 0.f ? launch<F16, E4M3, DP, true>(a, stream)
+                         : launch<F16, E4M3, DP, false>(a, stream);
+}
+
 template <bool F16, bool E4M3>
 cudaError_t launch_for(const AttendArgs& a, cudaStream_t stream) {
-  return padded_dim(a.D) == 64 ? launch<F16, E4M3, 64>(a, stream) : launch<F16, E4M3, 128>(a, stream);
+  return padded_dim(a.D) == 64 ? launch_cap<F16, E4M3, 64>(a, stream)
+                               : launch_cap<F16, E4M3, 128>(a, stream);
 }
 
 }  // namespace

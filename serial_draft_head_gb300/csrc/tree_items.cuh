@@ -48,7 +48,8 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
-// Raw scores to base-2 exponents.
+// Raw scores to base-2 exponents.  Caps beyond 2^100 or below 2^-100 do to scores in
+// fp32 what those do.
 struct Score {
   float sl2;        // |scale| log2(e): a negative scale turns Q's signs
   float cap2;       // softcap log2(e), 0 without a cap
@@ -57,16 +58,47 @@ struct Score {
 
   __device__ static Score of(const AttendArgs& a) {
     Score s;
+    const float c = fminf(fmaxf(a.softcap, 0x1p-100f), 0x1p100f);
     s.sl2 = fabsf(a.scale) * kLog2e;
-    s.cap2 = a.softcap * kLog2e;
-    s.cap_in = a.softcap > 0.f ? 2.f * s.sl2 / a.softcap : 0.f;
-    s.cap_y = a.softcap > 0.f ? fabsf(a.scale) / a.softcap : 0.f;
+    s.cap2 = a.softcap > 0.f ? c * kLog2e : 0.f;
+    s.cap_in = 2.f * s.sl2 / c;
+    s.cap_y = fabsf(a.scale) / c;
     return s;
   }
 };
 
-__device__ __forceinline__ float capped(const Score& sc, float raw) {
-  return sc.cap2 - 2.f * sc.cap2 * rcp(ex2(raw * sc.cap_in) + 1.f);
+// Up to |y| = 0.75 (y = s / c) tanh(y) / y is a polynomial in y^2, fitted to it by
+// weighted least squares, within 6.5e-8 of it, so that a score keeps its relative
+// precision under any cap.  Past that, c - 2c / (e^2y + 1) does; below, its
+// difference would cancel (c 2^-22 off whatever the score).
+constexpr float kNearCap = 0.75f;
+__device__ __forceinline__ constexpr float tanh_coef(int i) {
+  constexpr float k[6] = {1.f,           -0.333329588f, 0.133254066f,
+                          -0.0533444323f, 0.0195829086f, -0.00471625756f};
+  return k[i];
+}
+
+// A capped score's exponent less `sub` in the two forms.  Which one it gets goes by
+// the score alone, so a row's weights do not depend on the rows and keys beside it;
+// that a whole warp needs only the first saves the second's special functions.
+__device__ __forceinline__ float capped_near(const Score& sc, float raw, float sub) {
+  const float y = raw * sc.cap_y, u = y * y;
+  float t = sc.cap2 * tanh_coef(5);
+#pragma unroll
+  for (int i = 4; i >= 0; --i) t = fmaf(t, u, sc.cap2 * tanh_coef(i));
+  return fmaf(y, t, -sub);
+}
+
+__device__ __forceinline__ float capped_past(const Score& sc, float raw, float sub) {
+  return sc.cap2 - 2.f * sc.cap2 * rcp(ex2(raw * sc.cap_in) + 1.f) - sub;
+}
+
+__device__ __forceinline__ bool past_near(const Score& sc, float raw) {
+  return fabsf(raw * sc.cap_y) > kNearCap;
+}
+
+__device__ __forceinline__ float capped(const Score& sc, float raw, float sub) {
+  return past_near(sc, raw) ? capped_past(sc, raw, sub) : capped_near(sc, raw, sub);
 }
 
 // a / b for a >= 0, b > 0: 32-bit arithmetic where that does.

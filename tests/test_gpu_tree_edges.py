@@ -90,3 +90,59 @@ def test_attend_scale_of_any_sign_and_zero(tree, T, dtype, cache, scale):
     """Totals that end inside a block, in both kernels; a scale of zero weighs all visible keys alike."""
     c = Case(tree, 4, 2, 64, 20, dtype, cache, T, [200, 45, 0][:len(T)], seed=230)
     c.check(*c.attend(scale=scale), scale=scale)
+
+
+def check_capped(c, out, lse, scale, softcap, sums=None, mask=None):
+    """Against the definition, by bounds that do not grow with the cap: `ref.bounds` of uncapped scores, and
+    2^-20 of a score for the cap itself (tanh(y) / y or 1 - 2 / (e^2y + 1), each a few roundings), which
+    counts like a score's other error: twice in a weight, once more in lse."""
+    keep, c.mask = c.mask, c.mask if mask is None else mask
+    want, want_lse, weight, own = ref.attend(c.q, c.k, c.v, c.ks, c.vs, c.pages, c.page, c.length, c.first,
+                                             c.mask, scale, softcap)
+    c.mask = keep
+    sums = own if sums is None else sums
+    tol, tol_lse = ref.bounds(want, weight, sums, c.D, c.dtype, 0.0)
+    extra = 2.0 ** -20 * sums.clamp(max=softcap)
+    tol, tol_lse = tol + 2 * extra[..., None] * weight, tol_lse + 3 * extra
+    off, far = (out.double() - want).abs() - tol, (lse.double() - want_lse).abs() - tol_lse
+    assert (off <= 0).all(), "out is %g past its bound" % off.max()
+    assert (far <= 0).all(), "lse is %g past its bound" % far.max()
+
+
+@pytest.mark.parametrize("T", [FEW, TILES])
+@pytest.mark.parametrize("dtype,cache", [(BF16, "16"), (F16, "16"), (BF16, "e4m3"), (F16, "e4m3")])
+@pytest.mark.parametrize("softcap", [8.0, 50.0, 1e4, 1e6, 1e8, 1e20, 3e38, 1e-3, 1e-38])
+def test_attend_cap_of_any_size(tree, T, dtype, cache, softcap):
+    """Scores of about 10 keep their precision under any cap."""
+    c = Case(tree, 4, 2, 64, 20, dtype, cache, T, [200, 45, 0][:len(T)], seed=231)
+    out, lse = c.attend(scale=1.25, softcap=softcap)
+    check_capped(c, out, lse, 1.25, softcap)
+
+
+@pytest.mark.parametrize("T", [FEW, TILES])
+@pytest.mark.parametrize("cache", ["16", "e4m3"])
+def test_attend_scores_near_the_cap_beside_small_ones(tree, T, cache):
+    """One key far below the others, near the cap: its weight is nothing, the others keep theirs."""
+    c = Case(tree, 4, 2, 64, 20, BF16, cache, T, [200, 45, 0][:len(T)], seed=232, mask=None)
+    c.q[:, :, 0] = 1.0
+    for b, n in enumerate(c.L):                    # the last node of each request
+        p = n + T[b] - 1
+        page, slot = c.pages[b, p // 20].long(), p % 20
+        row = torch.zeros(64, device="cuda")
+        row[0] = -2.0 ** 19
+        if cache == "e4m3":
+            code, byte = ref.quantise(row[None])
+            c.k[page, slot] = code.float().to(E4M3)
+            c.ks[page, slot] = byte
+        else:
+            c.k[page, slot] = row.to(BF16)
+    words = (max(T) + 31) // 32
+    c.mask = torch.full((c.N, words), -1, dtype=torch.int32, device="cuda")
+    without = c.mask.clone()
+    for b, t in enumerate(T):
+        rows = slice(int(c.first[b]), int(c.first[b + 1]))
+        if t > 1 or c.L[b] > 0:
+            without[rows, (t - 1) // 32] ^= torch.tensor(1 << (t - 1) % 32, dtype=torch.int64).int().item() \
+                if (t - 1) % 32 < 31 else -2 ** 31
+    out, lse = c.attend(scale=1.0, softcap=1e6)
+    check_capped(c, out, lse, 1.0, 1e6, mask=without)
