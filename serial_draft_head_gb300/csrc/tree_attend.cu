@@ -698,6 +698,7 @@ __device__ __noinline__ float2 softmax_any(Score sc, Tail* sh, uint64_t* o_done,
                                            int* status, uint32_t tm_s, uint32_t tm_o, int keys,
                                            uint4 see, float mref, float l) {
   const bool cap = sc.cap2 > 0.f;
+  uint32_t any = 0;                              // whether the row sees one of the keys
   float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
   for (int c = 0; c < keys / 32; ++c) {
@@ -705,13 +706,15 @@ __device__ __noinline__ float2 softmax_any(Score sc, Tail* sh, uint64_t* o_done,
     uint32_t v[32];
     ptx::tmem_ld32(tm_s + 32 * c, v);
     ptx::tmem_wait_ld32(v);
+    any |= m;
 #pragma unroll
     for (int k = 0; k < 32; ++k)
       mx[k & 3] = fmaxf(mx[k & 3], (m >> k) & 1 ? __uint_as_float(v[k]) : -INFINITY);
   }
   const float raw_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
   float x_max = raw_max == -INFINITY ? -INFINITY : raw_max * sc.sl2;
-  if (cap && raw_max != -INFINITY) x_max = capped(sc, raw_max, 0.f);
+  // a visible score of -infinity is the cap's negative, an invisible one nothing
+  if (cap && any != 0) x_max = capped(sc, raw_max, 0.f);
   mref = move_reference<F16, DP>(x_max, sh, o_done, parity, status, tm_o, mref, &l);
   const float sub = mref == -INFINITY ? 0.f : mref;
   // capped_near, two scores at once: no special functions but the weight's own where

@@ -589,7 +589,9 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
         for (int kg = 1; kg < kGroups; ++kg)
           mx[h] = fmaxf(mx[h], fmaxf(x[kg][2 * h], x[kg][2 * h + 1]));
         mx[h] = mx[h] == -INFINITY ? -INFINITY : mx[h] * row_mul[h];
-        if (CAP && mx[h] != -INFINITY) mx[h] = capped(sc, mx[h], 0.f);
+        // a visible score of -infinity is the cap's negative, an invisible one nothing
+        constexpr uint32_t kMine = kGroups == 4 ? 0x03030303u : 0x0303u;
+        if (CAP && (see[h] & kMine) != 0) mx[h] = capped(sc, mx[h], 0.f);
       }
       // the first visible key sets a row's m, later ones when the maximum has grown enough
       const bool over = mx[0] > mref[0] + (mref[0] == -INFINITY ? 0.f : kShift + 8.f) ||

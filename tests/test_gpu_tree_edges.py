@@ -146,3 +146,21 @@ def test_attend_scores_near_the_cap_beside_small_ones(tree, T, cache):
                 if (t - 1) % 32 < 31 else -2 ** 31
     out, lse = c.attend(scale=1.0, softcap=1e6)
     check_capped(c, out, lse, 1.0, 1e6, mask=without)
+
+
+@pytest.mark.parametrize("T,L", [([1, 3, 2, 1], [200, 45, 1, 0]), ([30, 100, 40], [200, 1, 0])])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf])
+def test_attend_infinite_scores_meet_the_cap(tree, T, L, dtype, bad):
+    """A score of either infinity is the cap or its negative, where nothing else is visible too."""
+    c = Case(tree, 4, 2, 64, 20, dtype, "16", T, L, seed=233, mask="tree")
+    def put(x):  # noqa: E306
+        for b, n in enumerate(L):                  # the request's first key, and its last node
+            for p in (0, n + T[b] - 1):
+                c.k[c.pages[b, p // 20].long(), p % 20, :, 5] = x
+    put(0.0)
+    sums = ref.attend(c.q, c.k, c.v, None, None, c.pages, 20, c.length, c.first, c.mask, 0.2, 2.0)[3]
+    put(bad)
+    assert (c.q[:, :, 5] != 0).all()
+    out, lse = c.attend(scale=0.2, softcap=2.0)
+    check_capped(c, out, lse, 0.2, 2.0, sums=sums)
