@@ -342,7 +342,8 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
     // the scales of the block before have landed: lane = key
     if (E4M3 && scale_stage >= 0) {
       uint8_t* sb = scales + scale_stage * L::kScaleBytes;
-      reinterpret_cast<uint16_t*>(sb)[lane] = (uint16_t)(k_byte << 7);
+      // 2^(byte - 127), of byte 0 a subnormal number
+      reinterpret_cast<uint16_t*>(sb)[lane] = (uint16_t)(k_byte == 0 ? 0x40u : k_byte << 7);
       const bool easy = easy_scale<true>(v_byte);
       reinterpret_cast<uint16_t*>(sb + 2 * kBlock)[lane] =
           (uint16_t)(easy ? scale_mul2<true>(v_byte) : 0u);

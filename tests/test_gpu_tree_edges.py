@@ -164,3 +164,12 @@ def test_attend_infinite_scores_meet_the_cap(tree, T, L, dtype, bad):
     assert (c.q[:, :, 5] != 0).all()
     out, lse = c.attend(scale=0.2, softcap=2.0)
     check_capped(c, out, lse, 0.2, 2.0, sums=sums)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_attend_smallest_scale_of_keys(tree, D):
+    """Keys under scale byte 0, 2^-127, with queries that reach them."""
+    c = Case(tree, 4, 2, D, 20, BF16, "e4m3", FEW, [200, 45, 0], seed=234)
+    c.ks[c.ks != 255] = 0
+    c.q = (c.q.float() * 2.0 ** 118).to(BF16)
+    c.check(*c.attend(scale=0.25), scale=0.25)
