@@ -25,9 +25,9 @@
 //
 // e4m3: the products are f16, which holds every code, one conversion for two
 // codes.  K's scale goes on the scores (fp32).  V's goes into the codes: exact in
-// f16 for scales 2^-14 .. 2^7; blocks with others take the second product in the
-// handle's type, code times scale as the cache reads back.  bf16 rows of Q are
-// brought to f16 by a power of two a row (exact for elements down to 2^-32 of the
+// f16 for scales 2^-14 .. 2^7; keys with others get a product of their own in the
+// handle's type, code times scale as the cache reads back (64 single tokens with such
+// a key in every block: 318 us, without 173).  bf16 rows of Q are brought to f16 by a power of two a row (exact for elements down to 2^-32 of the
 // row's largest, below that to 2^-40 of it).
 //
 // What bounds it.  128 single tokens of 500 to 9,000 over e4m3 (64 heads on 8):
@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
               vw[kk][3] = y.w;
             }
           }
-          if (easy) {
+          auto product = [&]() {                 // by f16 scales
             const uint32_t* sv = reinterpret_cast<const uint32_t*>(sb + 2 * kBlock) + 8 * ks + q;
             const uint32_t m01 = sv[0], m23 = sv[4];
 #pragma unroll
@@ -696,7 +696,13 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
                 mma<true>(o[4 * i + 2 * h], p[ks][0], p[ks][1], p[ks][2], p[ks][3], y.x, z.x);
                 mma<true>(o[4 * i + 2 * h + 1], p[ks][0], p[ks][1], p[ks][2], p[ks][3], y.y, z.y);
               }
+          };
+          if (easy) {
+            product();
           } else {
+            // keys whose scale is not easy count nothing in this product (their f16 scale
+            // is 0) and alone in one more, in the handle's type: how a row's weights are
+            // rounded does not go by keys that it does not see
             uint32_t vb[4];
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
@@ -708,6 +714,13 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
                 vb[kk] = 127;
                 if (key < last) atomicOr(&st.bad[(key - draft) >> 5], 1u << ((key - draft) & 31));
               }
+            }
+            product();
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              if (!easy_scale<true>(vb[kk])) continue;
+#pragma unroll
+              for (int i = 0; i < L::kVBytes / 4; ++i) vw[kk][i] = 0;
             }
             if (!F16) {                          // weights in the handle's type
 #pragma unroll

@@ -173,3 +173,69 @@ def test_attend_smallest_scale_of_keys(tree, D):
     c.ks[c.ks != 255] = 0
     c.q = (c.q.float() * 2.0 ** 118).to(BF16)
     c.check(*c.attend(scale=0.25), scale=0.25)
+
+
+# -------------------------------------------------- invisible rows of the draft --
+
+
+@pytest.mark.parametrize("T,L", [([3, 2], [130, 20]), ([4, 3, 2], [3000, 0, 7]), ([1, 5], [500, 33]),
+                                 ([9, 150], [130, 20]), ([40, 20], [5000, 250])])
+@pytest.mark.parametrize("dtype,cache", [(BF16, "16"), (F16, "16"), (BF16, "e4m3"), (F16, "e4m3")])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("where", ["k", "v"])
+def test_attend_invisible_rows_hold_anything_in_both_kernels(tree, T, L, dtype, cache, bad, where):
+    """What a node holds reaches the nodes that see it and no other: few rows and tiles, items in one
+    piece and in parts, every type."""
+    if cache == "e4m3" and not math.isnan(bad):
+        pytest.skip("an e4m3 row that is not finite is NaN")
+    c = Case(tree, 4, 2, 64, 20, dtype, cache, T, L, seed=235, mask=None)
+    parent = torch.tensor([-1 if i == 0 else 0 for t in T for i in range(t)], dtype=torch.int32, device="cuda")
+    c.mask = tree.ancestor_bits(parent, c.first)   # all nodes are children of node 0
+    nodes = [(b, j) for b, t in enumerate(T) for j in {t - 1, t // 2} if j > 0]
+    clean_out, clean_lse = c.attend()
+    for b, j in nodes:
+        p = L[b] + j
+        page, slot = c.pages[b, p // 20].long(), p % 20
+        if cache == "e4m3":
+            getattr(c, where).view(torch.uint8)[page, slot] = 0x7f
+            getattr(c, where + "s")[page, slot] = 255
+        else:
+            getattr(c, where)[page, slot, :, 3] = bad
+    out, lse = c.attend()
+    hit = torch.zeros(c.N, dtype=torch.bool, device="cuda")
+    for b, j in nodes:
+        hit[int(c.first[b]) + j] = True
+    assert torch.equal(out[~hit], clean_out[~hit]) and torch.equal(lse[~hit], clean_lse[~hit])
+    if where == "v":
+        assert torch.equal(lse[hit], clean_lse[hit])
+        if cache == "e4m3":
+            assert torch.isnan(out[hit]).all()
+        else:
+            got = out[hit][..., 3].float()
+            assert torch.isnan(got).all() if math.isnan(bad) else (got == bad).all()
+            other = [i for i in range(64) if i != 3]
+            assert torch.equal(out[hit][..., other], clean_out[hit][..., other])
+    elif math.isnan(bad):
+        assert torch.isnan(out[hit]).all() and torch.isnan(lse[hit]).all()
+
+
+@pytest.mark.parametrize("T,L", [([3, 2], [130, 20]), ([4, 3, 2], [3000, 0, 7]), ([40, 20], [600, 250])])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("byte", [0, 60, 112, 135, 150])
+def test_attend_scales_of_invisible_rows(tree, T, L, dtype, byte):
+    """The scale that an invisible row of the draft has (finite in the rows' type) changes no bit."""
+    if dtype == F16 and byte > 134:
+        byte = 134
+    c = Case(tree, 4, 2, 64, 20, dtype, "e4m3", T, L, seed=236, mask=None)
+    parent = torch.tensor([-1 if i == 0 else 0 for t in T for i in range(t)], dtype=torch.int32, device="cuda")
+    c.mask = tree.ancestor_bits(parent, c.first)
+    clean_out, clean_lse = c.attend()
+    hit = torch.zeros(c.N, dtype=torch.bool, device="cuda")
+    for b, t in enumerate(T):
+        p = L[b] + t - 1
+        page, slot = c.pages[b, p // 20].long(), p % 20
+        c.ks[page, slot] = byte
+        c.vs[page, slot] = byte
+        hit[int(c.first[b]) + t - 1] = True
+    out, lse = c.attend()
+    assert torch.equal(out[~hit], clean_out[~hit]) and torch.equal(lse[~hit], clean_lse[~hit])
