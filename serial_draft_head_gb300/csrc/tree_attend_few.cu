@@ -27,8 +27,9 @@
 // codes.  K's scale goes on the scores (fp32).  V's goes into the codes: exact in
 // f16 for scales 2^-14 .. 2^7; keys with others get a product of their own in the
 // handle's type, code times scale as the cache reads back (64 single tokens with such
-// a key in every block: 318 us, without 173).  bf16 rows of Q are brought to f16 by a power of two a row (exact for elements down to 2^-32 of the
-// row's largest, below that to 2^-40 of it).
+// a key in every block: 318 us, without 173).  bf16 rows of Q are brought to f16 by a
+// power of two a row (exact for elements down to 2^-32 of the row's largest, below
+// that to 2^-40 of it).
 //
 // What bounds it.  128 single tokens of 500 to 9,000 over e4m3 (64 heads on 8):
 // 315 us, 3.7 TB/s; DRAM at 1.04 times the cache's bytes, 840 warp instructions a

@@ -29,26 +29,31 @@ struct Token {
   int page, slot;                  // page -1: left out
 };
 
-// The block's tokens n0 .. n0 + n_tok - 1: the request of row n is the last b
-// with first[b] <= n.  All threads count the requests before the block's first
-// row, then each token's thread walks on from there.
+// The block's tokens n0 .. n0 + n_tok - 1.  All threads look at all requests, each by
+// itself, so that one whose numbers do not fit hides no other and is reported if it
+// has no rows, too; a token's request is the one that holds its row (the last, if
+// ranges overlap).
 __device__ __forceinline__ void find_tokens(const RowsArgs& a, int n0, int n_tok, Token* toks) {
-  int before = 0;
-  for (int b = 0; b < a.b.B; b += kThreads) {
-    const bool in = b + (int)threadIdx.x < a.b.B && __ldg(a.b.first + b + threadIdx.x) <= n0;
-    before += __syncthreads_count(in);
-  }
-  if ((int)threadIdx.x < n_tok) {
-    const int n = n0 + threadIdx.x;
-    Token t{-1, 0};
-    int b = max(before - 1, 0);
-    while (b + 1 < a.b.B && __ldg(a.b.first + b + 1) <= n) ++b;
+  __shared__ int owner[kMaxTok];
+  if ((int)threadIdx.x < n_tok) owner[threadIdx.x] = -1;
+  __syncthreads();
+  for (int b = threadIdx.x; b < a.b.B; b += kThreads) {
     int row0, rows, start;
-    int64_t page;
-    if (!request_rows(a.b, b, &row0, &rows, &start)) {
+    if (request_rows(a.b, b, &row0, &rows, &start)) {
+      const int end = min(row0 + rows, n0 + n_tok);
+      for (int n = max(row0, n0); n < end; ++n) atomicMax(&owner[n - n0], b);
+    } else if (blockIdx.x == 0) {
       set_status(a.status, DSPARK_EPAGES);
-    } else if (n >= row0 && n < row0 + rows) {   // else a row of no request
-      if (locate(a.c, a.b, b, start + (n - row0), &page, &t.slot)) t.page = (int)page;
+    }
+  }
+  __syncthreads();
+  if ((int)threadIdx.x < n_tok) {
+    const int b = owner[threadIdx.x];
+    Token t{-1, 0};
+    if (b >= 0) {                                  // else a row of no request
+      int64_t page;
+      const int pos = a.b.start[b] + (n0 + (int)threadIdx.x - a.b.first[b]);
+      if (locate(a.c, a.b, b, pos, &page, &t.slot)) t.page = (int)page;
       else set_status(a.status, DSPARK_EPAGES);
     }
     toks[threadIdx.x] = t;

@@ -239,3 +239,65 @@ def test_attend_scales_of_invisible_rows(tree, T, L, dtype, byte):
         hit[int(c.first[b]) + t - 1] = True
     out, lse = c.attend()
     assert torch.equal(out[~hit], clean_out[~hit]) and torch.equal(lse[~hit], clean_lse[~hit])
+
+
+# ------------------------------------------------------------- arguments --
+
+
+FIRSTS = [[0, 2 ** 31 - 1, 9, 15], [0, -1, 9, 15], [3, 1, 9, 15], [0, 12, 9, 15], [0, 4, 2, 15]]
+
+
+@pytest.mark.parametrize("first", FIRSTS)
+@pytest.mark.parametrize("cache", ["16", "e4m3"])
+def test_a_bad_row_range_leaves_the_other_requests_alone(tree, first, cache):
+    """Requests behind one whose rows are out of range are written, read and attended to."""
+    from serial_draft_head_gb300 import walk
+    T, L = [9, 9, 6], [40, 50, 60]
+    c = Case(tree, 4, 2, 64, 16, BF16, cache, T, L, seed=253, garbage=None, mask=None)
+    c.tree = tree.Tree(4, 2, 64, BF16, max_requests=3, max_nodes=16)
+    N = 15
+    f = torch.tensor(first, dtype=torch.int32, device="cuda")
+    ok = [0 <= a <= b <= N for a, b in zip(first, first[1:])]
+    assert not all(ok) and ok[2]
+    new = torch.randn(N, 2, 64, generator=c.g, device="cuda").to(BF16)
+    c.tree.write(c.cache, c.pages, c.length, f, new, new)
+    assert c.tree.status() == walk.EPAGES
+    code, byte = ref.quantise(new)
+    want = (code * ref.scale_of(byte)[..., None]).to(BF16) if cache == "e4m3" else new
+    alone = torch.tensor([0, first[3] - first[2]], dtype=torch.int32, device="cuda")
+    rows = slice(first[2], first[3])
+    got = c.tree.read(c.cache, c.pages[2:], c.length[2:], alone, first[3] - first[2])
+    assert c.tree.status() == 0
+    assert all(torch.equal(x, want[rows]) for x in got)
+    back = tuple(torch.full((N, 2, 64), 5.0, dtype=BF16, device="cuda") for _ in range(2))
+    c.tree.read(c.cache, c.pages, c.length, f, N, out=back)
+    assert c.tree.status() == walk.EPAGES
+    assert all(torch.equal(x[rows], want[rows]) for x in back)
+    q = torch.randn(N, 4, 64, generator=c.g, device="cuda").to(BF16)
+    out, _ = c.tree.attend(q, c.cache, c.pages, c.length, f)
+    assert c.tree.status() == walk.EPAGES
+    one, _ = c.tree.attend(q[rows], c.cache, c.pages[2:], c.length[2:], alone)
+    assert c.tree.status() == 0
+    if all(b <= first[2] for a, b, o in zip(first[:2], first[1:], ok) if o):
+        # rows of one request only; the kernel's choice goes by all requests' rows: within roundings
+        assert (out[rows].double() - one.double()).abs().max() < 2.0 ** -6
+
+
+def test_cache_calls_report_bad_requests_without_rows(tree):
+    """As attend does: a request that has no rows but numbers that do not fit."""
+    from serial_draft_head_gb300 import walk
+    c = Case(tree, 2, 2, 64, 16, BF16, "e4m3", [4, 0, 5], [40, 7, 50], seed=254, garbage=None, mask=None)
+    new = torch.randn(9, 2, 64, generator=c.g, device="cuda").to(BF16)
+    for length in (-1, 1 << 20):
+        bad = c.length.clone()
+        bad[1] = length
+        c.tree.write(c.cache, c.pages, bad, c.first, new, new)
+        assert c.tree.status() == walk.EPAGES
+        k, v = c.tree.read(c.cache, c.pages, bad, c.first, 9)
+        assert c.tree.status() == walk.EPAGES
+        code, byte = ref.quantise(new)
+        want = (code * ref.scale_of(byte)[..., None]).to(BF16)
+        assert torch.equal(k, want) and torch.equal(v, want)
+        q = torch.randn(9, 2, 64, generator=c.g, device="cuda").to(BF16)
+        c.tree.attend(q, c.cache, c.pages, bad, c.first)
+        assert c.tree.status() == walk.EPAGES
