@@ -38,7 +38,8 @@
  *
  * Conventions as in dspark_walk.h: 0 or a negative DSPARK_E* code, nothing
  * traps, calls on one handle are ordered by the caller, `stream` is a
- * cudaStream_t of the handle's device, launches are graph-capturable.  Sizes
+ * cudaStream_t of the handle's device (which need not be the current one),
+ * launches are graph-capturable.  Sizes
  * that only the device knows (start, first, pages, path, count) are checked
  * there: a request that fails is left out (its rows and cache stay as they
  * were) and dspark_tree_status then returns DSPARK_EPAGES.  Where only an entry

@@ -47,12 +47,26 @@ cudaError_t clear(void* p, size_t bytes) {
   return e != cudaSuccess ? e : d;
 }
 
-// The calls work on the current device: it has to be the handle's.
-int check_device(const dspark_tree* h) {
-  int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess) return DSPARK_ECUDA;
-  return dev == h->device ? DSPARK_OK : DSPARK_EINVAL;
-}
+// The handle's device is current while a call runs; the caller's is afterwards.
+class OnDevice {
+ public:
+  explicit OnDevice(const dspark_tree* h) {
+    int now = 0;
+    if (cudaGetDevice(&now) != cudaSuccess) return;
+    ok_ = now == h->device || cudaSetDevice(h->device) == cudaSuccess;
+    if (ok_ && now != h->device) before_ = now;
+  }
+  ~OnDevice() {
+    if (before_ >= 0) cudaSetDevice(before_);
+  }
+  OnDevice(const OnDevice&) = delete;
+  OnDevice& operator=(const OnDevice&) = delete;
+  int code() const { return ok_ ? DSPARK_OK : DSPARK_ECUDA; }
+
+ private:
+  bool ok_ = false;
+  int before_ = -1;
+};
 
 int make_cache(const dspark_tree* h, const dspark_tree_cache* c, CacheView* out) {
   if (!c || !c->k || !c->v) return DSPARK_EINVAL;
@@ -202,7 +216,8 @@ int dspark_tree_write(dspark_tree_t h, const dspark_tree_cache* cache,
                       const void* v, const int64_t* v_stride, void* stream) {
   if (!h) return DSPARK_EINVAL;
   RowsArgs a{};
-  int rc = check_device(h);
+  const OnDevice on(h);
+  int rc = on.code();
   if (rc == DSPARK_OK) rc = make_cache(h, cache, &a.c);
   if (rc == DSPARK_OK) rc = make_batch(batch, cache->page_size, true, &a.b);
   if (rc != DSPARK_OK) return rc;
@@ -228,7 +243,8 @@ int dspark_tree_read(dspark_tree_t h, const dspark_tree_cache* cache,
                      const dspark_tree_batch* batch, void* out_k, void* out_v, void* stream) {
   if (!h) return DSPARK_EINVAL;
   RowsArgs a{};
-  int rc = check_device(h);
+  const OnDevice on(h);
+  int rc = on.code();
   if (rc == DSPARK_OK) rc = make_cache(h, cache, &a.c);
   if (rc == DSPARK_OK) rc = make_batch(batch, cache->page_size, true, &a.b);
   if (rc != DSPARK_OK) return rc;
@@ -250,7 +266,8 @@ int dspark_tree_keep(dspark_tree_t h, const dspark_tree_cache* cache,
                      int max_path, const int32_t* count, void* stream) {
   if (!h) return DSPARK_EINVAL;
   KeepArgs a{};
-  int rc = check_device(h);
+  const OnDevice on(h);
+  int rc = on.code();
   if (rc == DSPARK_OK) rc = make_cache(h, cache, &a.c);
   if (rc == DSPARK_OK) rc = make_batch(batch, cache->page_size, false, &a.b);
   if (rc != DSPARK_OK) return rc;
@@ -274,7 +291,8 @@ int dspark_tree_attend(dspark_tree_t h, const dspark_tree_cache* cache,
                        float softcap, void* out, float* lse, void* stream) {
   if (!h) return DSPARK_EINVAL;
   AttendArgs a{};
-  int rc = check_device(h);
+  const OnDevice on(h);
+  int rc = on.code();
   if (rc == DSPARK_OK) rc = make_cache(h, cache, &a.c);
   if (rc == DSPARK_OK) rc = make_batch(batch, cache->page_size, true, &a.b);
   if (rc != DSPARK_OK) return rc;
@@ -326,6 +344,8 @@ int dspark_tree_attend(dspark_tree_t h, const dspark_tree_cache* cache,
 
 int dspark_tree_status(dspark_tree_t h, void* stream) {
   if (!h) return DSPARK_EINVAL;
+  const OnDevice on(h);
+  if (on.code() != DSPARK_OK) return on.code();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int st = 0;
   cudaError_t e = cudaMemcpyAsync(&st, h->status, sizeof(int), cudaMemcpyDeviceToHost, s);
@@ -336,7 +356,8 @@ int dspark_tree_status(dspark_tree_t h, void* stream) {
 
 int dspark_tree_destroy(dspark_tree_t h) {
   if (!h) return DSPARK_EINVAL;
-  const int rc = cuda_code(cudaDeviceSynchronize());
+  const OnDevice on(h);
+  const int rc = on.code() != DSPARK_OK ? on.code() : cuda_code(cudaDeviceSynchronize());
   if (h->status) cudaFree(h->status);
   if (h->parts) cudaFree(h->parts);
   delete h;

@@ -233,7 +233,8 @@ class Tree:
     def _empty(self, shape, dtype, stream):
         if stream is None:
             return torch.empty(shape, dtype=dtype, device=self.device)
-        s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+        s = torch.cuda.ExternalStream(stream, device=self.device) if isinstance(stream, int) \
+            else stream
         with torch.cuda.stream(s):           # the block belongs to the stream that fills it
             return torch.empty(shape, dtype=dtype, device=self.device)
 

@@ -67,7 +67,9 @@ int cudaLaunchKernelExC(const void *config, const void *f, void **args) {
   return note("launch on %d\n", current);
 }
 typedef struct { unsigned x, y, z; } dim3;
-int cudaLaunchKernel(const void *f, dim3 grid, dim3 block, void **args, size_t smem, void *s) {
-  (void)f, (void)args, (void)smem, (void)s;
+/* what the compiler makes of <<< >>> */
+int __cudaGetKernel(void **kernel, const void *f) { return *kernel = (void *)f, 0; }
+int __cudaLaunchKernel(void *kernel, dim3 grid, dim3 block, void **args, size_t smem, void *s) {
+  (void)kernel, (void)args, (void)smem, (void)s;
   return note("launch grid %u %u %u block %u on %d\n", grid.x, grid.y, grid.z, block.x, current);
 }

@@ -45,3 +45,31 @@ def test_create_returns_with_its_memory_cleared(calls):
         stream = log[i].split()[2]
         assert any(line.startswith("synchronise stream %s " % stream) for line in log[i:])
         assert stream != "0" and not any(line.startswith("synchronise all") for line in log)
+
+
+def operators(B=2, N=8):
+    """One call of each operator on a handle of `create()`, over a 16-bit cache."""
+    from serial_draft_head_gb300 import tree
+    at = 1 << 20                                   # any address: nothing is launched
+    cache = tree.dspark_tree_cache(k=at, v=at, n_pages=9, page_size=16, type=0)
+    cache.k_stride[:] = cache.v_stride[:] = (16 * 128, 128, 64)
+    batch = tree.dspark_tree_batch(pages=at, start=at, first=at, pages_stride=4, max_pages=4, B=B, N=N)
+    strides = {"bytes": bytes((tree.ctypes.c_int64 * 2)(512, 64)).hex()}
+    c, b = {"bytes": bytes(cache).hex()}, {"bytes": bytes(batch).hex()}
+    return [["dspark_tree_write", "handle", c, b, at, strides, at, strides, None],
+            ["dspark_tree_read", "handle", c, b, at, at, None],
+            ["dspark_tree_keep", "handle", c, b, at, 3, 3, at, None],
+            ["dspark_tree_attend", "handle", c, b, at, strides, None, 0, 0, 0.125, 0.0, at, at, None]]
+
+
+def test_calls_work_on_the_handles_device(calls):
+    """Whichever device is current: each call launches on the handle's and leaves the other current."""
+    what = operators() + [["dspark_tree_status", "handle", None], ["dspark_tree_destroy", "handle"]]
+    for now in (0, 1):
+        done = calls([["device", 1], create(), ["device", now]] + what)[3:]
+        for (name, *_), (rc, log) in zip(what, done):
+            assert rc == 0, name
+            work = [line for line in log if " on " in line]
+            assert work and all(line.endswith(" on 1") for line in work), (name, log)
+            devices = [line for line in log if line.startswith("device")]
+            assert devices == ([] if now == 1 else ["device 1", "device 0"]), (name, log)
