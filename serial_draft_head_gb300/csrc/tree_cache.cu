@@ -239,7 +239,7 @@ constexpr int kKeepBatch = 8;
 // before its stores.  So no two threads touch the same bytes and nothing waits.
 __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constant__ KeepArgs a) {
   __shared__ uint2 from[DSPARK_TREE_MAX_NODES], to[DSPARK_TREE_MAX_NODES];   // page, slot
-  const int b = blockIdx.y;
+  const int b = blockIdx.x;                        // the grid's long direction
   const int n = a.count[b], start = a.b.start[b];
   bool bad = n < 0 || n > a.max_path || start < 0;
   if (!bad) {
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constan
     return;
   }
   const int parts = a.row_bytes / 16, chunks = parts * a.Hkv;    // of K; as many of V
-  const int c = blockIdx.x * kKeepThreads + threadIdx.x;
+  const int c = blockIdx.y * kKeepThreads + threadIdx.x;
   if (c < 2 * chunks) {
     const int v = c >= chunks;
     const int cc = c - v * chunks, head = cc / parts;
@@ -347,7 +347,7 @@ cudaError_t read_launch(const RowsArgs& a, bool f16, bool e4m3, int sm_count,
 
 cudaError_t keep_launch(const KeepArgs& a, cudaStream_t stream) {
   const int columns = a.row_bytes / 16 * a.Hkv * 2 + (a.scales ? 2 * a.Hkv : 0);
-  const dim3 grid((columns + kKeepThreads - 1) / kKeepThreads, a.b.B);
+  const dim3 grid(a.b.B, (columns + kKeepThreads - 1) / kKeepThreads);
   keep_kernel<<<grid, kKeepThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }

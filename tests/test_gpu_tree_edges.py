@@ -301,3 +301,22 @@ def test_cache_calls_report_bad_requests_without_rows(tree):
         q = torch.randn(9, 2, 64, generator=c.g, device="cuda").to(BF16)
         c.tree.attend(q, c.cache, c.pages, bad, c.first)
         assert c.tree.status() == walk.EPAGES
+
+
+def test_keep_of_many_requests(tree):
+    """More requests than a grid is wide in its second direction."""
+    B, page, Hkv, D = 70001, 4, 1, 16
+    g = torch.Generator(device="cuda")
+    g.manual_seed(255)
+    t = tree.Tree(1, Hkv, D)
+    k = torch.randn(B, page, Hkv, D, generator=g, device="cuda").to(BF16)
+    v = torch.randn(B, page, Hkv, D, generator=g, device="cuda").to(BF16)
+    want = [x.clone() for x in (k, v)]
+    for x in want:
+        x[:, 1] = x[:, 3]
+    pages = torch.randperm(B, generator=g, device="cuda").int()[:, None].contiguous()
+    start = torch.ones(B, dtype=torch.int32, device="cuda")
+    path = torch.full((B, 1), 2, dtype=torch.int32, device="cuda")
+    t.keep(tree.KVCache(k, v), pages, start, path, torch.ones_like(start))
+    assert t.status() == 0
+    assert torch.equal(k, want[0]) and torch.equal(v, want[1])
