@@ -217,6 +217,9 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
   }
 }
 
+// N is at least 1, and up to 2^31 - 1.
+int blocks_of(const RowsArgs& a, int tok) { return (a.b.N - 1) / tok + 1; }
+
 // Tokens per block: 16 where that still gives every SM four blocks, fewer for
 // small calls, so that their rows spread over the SMs, as long as a block's
 // threads all have a row.  Device time, spread / 16 a block: 128 tokens of 16 rows
@@ -225,7 +228,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
 int tokens_per_block(const RowsArgs& a, int lanes, int sm_count) {
   const int pass = kThreads / lanes;             // rows
   int tok = kMaxTok;
-  while (tok > 1 && (a.b.N + tok - 1) / tok < 4 * sm_count && tok / 2 * 2 * a.Hkv >= pass) tok >>= 1;
+  while (tok > 1 && blocks_of(a, tok) < 4 * sm_count && tok / 2 * 2 * a.Hkv >= pass) tok >>= 1;
   return tok;
 }
 
@@ -301,13 +304,13 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constan
 template <bool F16, bool E4M3, int LANES>
 void launch_write(const RowsArgs& a, int sm_count, cudaStream_t stream) {
   const int tok = tokens_per_block(a, LANES, sm_count);
-  write_kernel<F16, E4M3, LANES><<<(a.b.N + tok - 1) / tok, kThreads, 0, stream>>>(a, tok);
+  write_kernel<F16, E4M3, LANES><<<blocks_of(a, tok), kThreads, 0, stream>>>(a, tok);
 }
 
 template <bool F16, bool E4M3, int LANES>
 void launch_read(const RowsArgs& a, int sm_count, cudaStream_t stream) {
   const int tok = tokens_per_block(a, LANES, sm_count);
-  read_kernel<F16, E4M3, LANES><<<(a.b.N + tok - 1) / tok, kThreads, 0, stream>>>(a, tok);
+  read_kernel<F16, E4M3, LANES><<<blocks_of(a, tok), kThreads, 0, stream>>>(a, tok);
 }
 
 // Half the lanes for heads of up to 64 elements: lanes without elements cost as

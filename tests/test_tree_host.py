@@ -76,12 +76,12 @@ def test_calls_work_on_the_handles_device(calls):
 
 
 def test_grids_fit_the_device(calls):
-    """Any number of requests: a grid is at most 65,535 wide in its second direction."""
+    """Any number of requests and rows: a grid is at most 65,535 wide in its second direction."""
     def launch(what):  # noqa: E306
         (rc, _), (rc2, log), (rc3, _) = calls([create(kv_heads=kv, q_heads=kv), what, ["dspark_tree_destroy", "handle"]])
         assert (rc, rc2, rc3) == (0, 0, 0)
         return [tuple(int(x) for x in line.split()[2:5]) for line in log if line.startswith("launch grid")]
-    for B, N in ((70001, 8), (2 ** 31 - 1, 1)):
+    for B, N in ((70001, 8), (2 ** 31 - 1, 1), (1, 2 ** 31 - 1)):
         for kv in (1, 8, 65535):
             for what in operators(B, N)[:3]:
                 for x, y, z in launch(what):
