@@ -311,6 +311,8 @@ class Tree:
                     and mask.shape[0] == n):
                 raise ValueError("mask is int32 [N, words] on the handle's device")
             m, mw = mask.data_ptr(), mask.shape[1]
+            if mw < 1 and n > 0:                  # its address would be null: a chain
+                raise ValueError("mask has a word a row at least")
             ms, one = mask.stride()
             if one != 1 and mw > 1:
                 raise ValueError("a mask row's words lie next to each other")

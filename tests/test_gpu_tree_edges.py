@@ -244,6 +244,13 @@ def test_attend_scales_of_invisible_rows(tree, T, L, dtype, byte):
 # ------------------------------------------------------------- arguments --
 
 
+def test_attend_refuses_a_mask_without_words(tree):
+    c = Case(tree, 4, 2, 64, 16, BF16, "16", [4], [40], seed=250)
+    with pytest.raises((ValueError, tree.WalkError)):
+        c.tree.attend(c.q, c.cache, c.pages, c.length, c.first, mask=c.mask[:, :0])
+    assert c.tree.status() == 0
+
+
 FIRSTS = [[0, 2 ** 31 - 1, 9, 15], [0, -1, 9, 15], [3, 1, 9, 15], [0, 12, 9, 15], [0, 4, 2, 15]]
 
 
