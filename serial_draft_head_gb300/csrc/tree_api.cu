@@ -307,7 +307,9 @@ int dspark_tree_attend(dspark_tree_t h, const dspark_tree_cache* cache,
   a.q_head = q_stride[1] * 2;
   a.mask = mask;
   a.mask_stride = mask_stride;
-  a.mask_words = mask ? mask_words : 0;
+  // no more than nodes need, so that the bits of a row are a small number
+  constexpr int kWords = (DSPARK_TREE_MAX_NODES + 31) / 32;
+  a.mask_words = !mask ? 0 : mask_words < kWords ? mask_words : kWords;
   a.scale = scale;
   a.softcap = softcap;
   a.out = static_cast<uint16_t*>(out);

@@ -251,6 +251,19 @@ def test_attend_refuses_a_mask_without_words(tree):
     assert c.tree.status() == 0
 
 
+def test_attend_takes_a_mask_of_many_words(tree):
+    """More words a row than nodes need, as many as 2^26."""
+    for T in (1, 20):
+        c = Case(tree, 4, 2, 64, 16, BF16, "16", [T], [40], seed=251)
+        out, lse = c.attend()
+        wide = torch.zeros(T, 1 << 26, dtype=torch.int32, device="cuda")
+        wide[:, :1] = c.mask
+        o2, l2 = c.tree.attend(c.q, c.cache, c.pages, c.length, c.first, mask=wide)
+        assert c.tree.status() == 0
+        assert torch.equal(out, o2) and torch.equal(lse, l2)
+        del wide
+
+
 FIRSTS = [[0, 2 ** 31 - 1, 9, 15], [0, -1, 9, 15], [3, 1, 9, 15], [0, 12, 9, 15], [0, 4, 2, 15]]
 
 
