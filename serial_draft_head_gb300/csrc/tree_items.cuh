@@ -107,7 +107,7 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
   return a / b;
 }
 
-// `total` units over the workers that get any, evenly: those with one more than
+// `total` units over the workers that get any (one at least), evenly: those with one more than
 // the others lie between them, so that where the items are alike and divide the
 // workers (one long request: 8 heads on 152 SMs) no share crosses an item's end
 // (99 us for 17 rows over 131,000 tokens; 103.5 with the longer shares first).
@@ -118,8 +118,8 @@ struct Cut {
   __device__ static __forceinline__ Cut of(int64_t total, int n_cta) {
     Cut c;
     c.total = total;
-    c.workers = (int)(total < n_cta ? total : n_cta);
-    c.per = total == 0 ? 0 : quotient(total, c.workers);
+    c.workers = (int)(total < n_cta ? max(total, (int64_t)1) : n_cta);   // one without units
+    c.per = quotient(total, c.workers);
     c.rest = (int)(total - c.per * c.workers);
     return c;
   }

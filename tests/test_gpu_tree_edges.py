@@ -264,6 +264,17 @@ def test_attend_takes_a_mask_of_many_words(tree):
         del wide
 
 
+@pytest.mark.parametrize("T", [2, 40])
+def test_attend_where_no_request_has_rows(tree, T):
+    """All requests fail, or none has a row: nothing is written."""
+    from serial_draft_head_gb300 import walk
+    c = Case(tree, 4, 2, 64, 16, BF16, "16", [T, T], [40, 9], seed=252)
+    for length, first, code in ((-1, c.first, walk.EPAGES), (3, torch.zeros_like(c.first), 0)):
+        out = torch.full_like(c.q, 3.0)
+        c.tree.attend(c.q, c.cache, c.pages, torch.full_like(c.length, length), first, mask=c.mask, out=out)
+        assert c.tree.status() == code and (out == 3).all()
+
+
 FIRSTS = [[0, 2 ** 31 - 1, 9, 15], [0, -1, 9, 15], [3, 1, 9, 15], [0, 12, 9, 15], [0, 4, 2, 15]]
 
 
