@@ -10,19 +10,20 @@
 // the workers (one CTA a SM): the lengths are known on the device only, so every
 // CTA sums them up itself.  An item that lies inside one worker's share is
 // finished there; one that several workers share leaves parts (unnormalised O,
-// maximum, sum), joined in an order that does not depend on timing: by the CTA
-// that is last to leave its part (few rows: 16 rows a part), or by a second kernel
-// over all SMs (tcgen05: up to 256 rows a part, and 20 parts an item).
+// maximum, sum), at most one a worker, joined in an order that does not depend on
+// timing: by the CTA that is last to leave its part (few rows: 16 rows a part), or by
+// a second kernel over all SMs (tcgen05: up to 256 rows a part).
 //
 // Mathematics, per row, one pass over the tiles in the base-2 exponent:
 //   x_j = log2(e) * scale * q.k_j              (capped: log2(e) c tanh(s / c))
 //   p_j = 2^(x_j - m),  l = sum p_j,  O = sum p_j v_j
-// m follows the running maximum lazily: it moves, and O and l are rescaled,
-// only when the maximum has grown by more than 8, so p <= 2^8: O and l in fp32
-// keep their relative precision, and the rescaling of O is rare.  p is rounded
-// once to the 16-bit type for the second product (half a unit, as the result
-// itself is rounded); l sums the unrounded p.  For f16 m carries -7, so that
-// weights down to 2^-21 of the largest stay normal numbers.
+// m follows the running maximum lazily: it moves, and O and l are rescaled, only when
+// the maximum has grown by more than 8, so p <= 2^8, and the rescaling of O is rare.
+// For products in f16 m stands 7 below the maximum that set it, so that weights down
+// to 2^-21 of the largest stay normal numbers: p <= 2^15 then, and f16 ends at 65,504.
+// O and l in fp32 keep their relative precision.  p is rounded once to the 16-bit type
+// for the second product (half a unit, as the result itself is rounded); l sums the
+// unrounded p.
 #pragma once
 
 #include <math.h>

@@ -241,6 +241,20 @@ def test_attend_scales_of_invisible_rows(tree, T, L, dtype, byte):
     assert torch.equal(out[~hit], clean_out[~hit]) and torch.equal(lse[~hit], clean_lse[~hit])
 
 
+# -------------------------------------------------------------- parts --
+
+
+@pytest.mark.parametrize("T,cache", [(1, "16"), (4, "e4m3"), (20, "16"), (60, "16"), (40, "e4m3")])
+def test_attend_one_item_over_all_workers(tree, T, cache):
+    """One cached head and a long context: an item of as many parts as there are SMs."""
+    c = Case(tree, 4, 1, 64, 16, BF16, cache, [T], [60000], seed=240)
+    out, lse = c.attend()
+    c.check(out, lse)
+    for _ in range(5):
+        o2, l2 = c.attend()
+        assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
 # ------------------------------------------------------------- arguments --
 
 
