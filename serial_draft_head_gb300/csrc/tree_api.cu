@@ -329,11 +329,12 @@ int dspark_tree_attend(dspark_tree_t h, const dspark_tree_cache* cache,
   a.status = h->status;
   // Few rows a cached head on average: the kernel that has tiles of 16 of them (any
   // number of rows is right in either).  16 requests of 300 to 6,000 tokens, 8 heads,
-  // us here / there: 16-bit 4 rows 57 / 63, 16 rows 58.5 / 63.5, 20 rows 100 / 64 (K
-  // and V read twice); e4m3, which the other kernel has to convert through shared
-  // memory, 4 rows 45 / 69, 16 rows 46 / 76, 32 rows 74 / 78.
-  const int few_rows = cache->type == DSPARK_TYPE_E4M3 ? 32 : 16;
-  if ((int64_t)a.b.N * a.G <= (int64_t)few_rows * a.b.B)
+  // us here / there.  16-slot pages, 16-bit: 4 rows 56 / 67, 16 rows 57 / 67, 20 rows
+  // 96 / 67 (K and V read twice); e4m3, which the other kernel has to convert through
+  // shared memory: 4 rows 42 / 65, 16 rows 44 / 66, 20 rows 70 / 66.  64-slot pages,
+  // which the other kernel takes by tiled copies, 16-bit: 16 rows 56 / 55, 20 rows
+  // 95 / 56; e4m3: 16 rows 50 / 66, 20 rows 84 / 66.
+  if ((int64_t)a.b.N * a.G <= (int64_t)16 * a.b.B)
     return cuda_code(few_launch(a, h->cfg.type == DSPARK_TYPE_F16,
                                 cache->type == DSPARK_TYPE_E4M3,
                                 static_cast<cudaStream_t>(stream)));
