@@ -333,7 +333,7 @@ int dspark_tree_attend(dspark_tree_t h, const dspark_tree_cache* cache,
   // 96 / 67 (K and V read twice); e4m3, which the other kernel has to convert through
   // shared memory: 4 rows 42 / 65, 16 rows 44 / 66, 20 rows 70 / 66.  64-slot pages,
   // which the other kernel takes by tiled copies, 16-bit: 16 rows 56 / 55, 20 rows
-  // 95 / 56; e4m3: 16 rows 50 / 66, 20 rows 84 / 66.
+  // 95 / 56; e4m3: 16 rows 43 / 66.
   if ((int64_t)a.b.N * a.G <= (int64_t)16 * a.b.B)
     return cuda_code(few_launch(a, h->cfg.type == DSPARK_TYPE_F16,
                                 cache->type == DSPARK_TYPE_E4M3,

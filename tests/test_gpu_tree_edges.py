@@ -365,3 +365,22 @@ def test_keep_of_many_requests(tree):
     t.keep(tree.KVCache(k, v), pages, start, path, torch.ones_like(start))
     assert t.status() == 0
     assert torch.equal(k, want[0]) and torch.equal(v, want[1])
+
+
+@pytest.mark.parametrize("T,L", [([1], [600]), ([2, 3], [45, 0]), ([20], [600])])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_attend_slots_past_the_end_change_no_bit(tree, T, L, dtype):
+    """Codes and scales of a page's slots that a request has not reached."""
+    c = Case(tree, 4, 2, 64, 64, dtype, "e4m3", T, L, seed=256, garbage=None)
+    out, lse = c.attend()
+    free = torch.ones(c.n_pages, 64, dtype=torch.bool, device="cuda")
+    for b in range(c.B):
+        at = torch.arange(L[b] + T[b], device="cuda")
+        free[c.pages[b][at // 64].long(), at % 64] = False
+    for code, byte in ((0, 0), (0x7f, 255), (0x55, 200), (0x7e, 254)):
+        for x in (c.k, c.v):
+            x.view(torch.uint8)[free] = code
+        for x in (c.ks, c.vs):
+            x[free] = byte
+        o2, l2 = c.attend()
+        assert torch.equal(out, o2) and torch.equal(lse, l2)
