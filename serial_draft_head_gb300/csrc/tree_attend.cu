@@ -16,7 +16,7 @@
 // S and P share columns and tensor memory is full, so the next S cannot be made
 // before P has been used.  A pair therefore goes by halves of 64 keys: one half's
 // S is made while the softmax is at the other (64 requests of 64 nodes, 4,096 to
-// 8,192 tokens: 402 us, 426 with whole tiles).  Alternate tiles stay whole: with
+// 8,192 tokens: 402 us at the time, 426 with whole tiles).  Alternate tiles stay whole: with
 // few rows the copies bound, and halves hold their slots longer (64 us against 75
 // for 16 requests of 8 nodes).
 //
@@ -32,12 +32,12 @@
 // finite would reach every row of the product (0 * NaN), so such elements are
 // zeroed in the ring and noted, and added at the end to the rows that see them.
 //
-// What bounds it.  64 x 64 as above (414 GFLOP, 1.7 GB): 400 to 415 us, 1.0 PFLOP/s, the
-// tensor pipe active 47% of the time and the issue slots 48%: the rest is the
+// What bounds it.  64 x 64 as above (414 GFLOP, 1.7 GB): 407 to 422 us, 1.0 PFLOP/s, the
+// tensor pipe active 50% of the time and the issue slots 50%: the rest is the
 // chain softmax - product - next S of two streams, and 15 us an item for Q, the
-// masked tiles and the result.  17 nodes over 131,000 tokens: 101 us, 5.3 TB/s.
-// 16 requests of 8 nodes: 61 us, 2.9 TB/s, the ring's five slots against the
-// copies' latency (long scoreboard 7.5 of 15 warp cycles an issue).
+// masked tiles and the result.  17 nodes over 131,000 tokens: 99 us, 5.4 TB/s.
+// 16 requests of 8 nodes: 60 us, 2.9 TB/s, the ring's five slots against the
+// copies' latency (long scoreboard 7.2 of 14 warp cycles an issue).
 #include "tree_items.cuh"
 
 namespace dspark {
@@ -717,13 +717,43 @@ __device__ __noinline__ float2 softmax_any(Score sc, Tail* sh, uint64_t* o_done,
   if (cap && any != 0) x_max = capped(sc, raw_max, 0.f);
   mref = move_reference<F16, DP>(x_max, sh, o_done, parity, status, tm_o, mref, &l);
   const float sub = mref == -INFINITY ? 0.f : mref;
-  // capped_near, two scores at once: no special functions but the weight's own where
-  // 8 keys are far from the cap in all rows of the warp
+  // coefficients of capped_near.  No special functions but the weight's own where all
+  // of 8 keys are far from the cap in all rows of the warp; 16 requests of 64 nodes, 300
+  // to 6,000 tokens, 16-bit: 130 us where all are, 168 where in all groups some are not
+  // (no cap 84).
   uint64_t coef[6];
 #pragma unroll
   for (int i = 0; i < 6; ++i)
     coef[i] = pack_f32x2(sc.cap2 * tanh_coef(i), sc.cap2 * tanh_coef(i));
   const uint64_t neg = pack_f32x2(-sub, -sub);
+  const float past0 = sc.cap2 - sub;
+  // scores k0 .. k0 + n - 1 to exponents, two at once, by capped_near; `both`: those
+  // past it by capped_past
+  auto cap_pairs = [&](uint32_t (&v)[32], int k0, int n, bool both) {
+#pragma unroll
+    for (int k = k0; k < k0 + n; k += 2) {
+      const uint64_t raw = pack_f32x2(__uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+      const uint64_t y = mul_f32x2(raw, pack_f32x2(sc.cap_y, sc.cap_y));
+      const uint64_t u = mul_f32x2(y, y);
+      uint64_t t = coef[5];
+#pragma unroll
+      for (int i = 4; i >= 0; --i) t = fma_f32x2(t, u, coef[i]);
+      float x[2];
+      unpack_f32x2(fma_f32x2(y, t, neg), &x[0], &x[1]);
+      if (both) {
+        float z[2], yy[2], r[2];
+        unpack_f32x2(mul_f32x2(raw, pack_f32x2(sc.cap_in, sc.cap_in)), &z[0], &z[1]);
+        unpack_f32x2(y, &yy[0], &yy[1]);
+        const uint64_t d = pack_f32x2(rcp(ex2(z[0]) + 1.f), rcp(ex2(z[1]) + 1.f));
+        unpack_f32x2(fma_f32x2(d, pack_f32x2(-2.f * sc.cap2, -2.f * sc.cap2),
+                               pack_f32x2(past0, past0)), &r[0], &r[1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) x[e] = fabsf(yy[e]) > kNearCap ? r[e] : x[e];
+      }
+      v[k] = __float_as_uint(x[0]);
+      v[k + 1] = __float_as_uint(x[1]);
+    }
+  };
   float sum[2] = {0.f, 0.f};
 #pragma unroll 1
   for (int c = 0; c < keys / 32; ++c) {
@@ -732,29 +762,17 @@ __device__ __noinline__ float2 softmax_any(Score sc, Tail* sh, uint64_t* o_done,
     ptx::tmem_ld32(tm_s + 32 * c, v);
     ptx::tmem_wait_ld32(v);
     if (cap) {
+      float big[4] = {0.f, 0.f, 0.f, 0.f};       // of 8 keys each
 #pragma unroll
-      for (int k0 = 0; k0 < 32; k0 += 8) {
-        float x[8], big = 0.f;
+      for (int k = 0; k < 32; ++k) big[k / 8] = fmaxf(big[k / 8], fabsf(__uint_as_float(v[k])));
+      if (!__any_sync(0xffffffffu, past_near(sc, fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]))))) {
+        cap_pairs(v, 0, 32, false);
+      } else {
 #pragma unroll
-        for (int k = 0; k < 8; k += 2) {
-          const float r0 = __uint_as_float(v[k0 + k]), r1 = __uint_as_float(v[k0 + k + 1]);
-          big = fmaxf(big, fmaxf(fabsf(r0), fabsf(r1)));
-          const uint64_t y = mul_f32x2(pack_f32x2(r0, r1), pack_f32x2(sc.cap_y, sc.cap_y));
-          const uint64_t u = mul_f32x2(y, y);
-          uint64_t t = coef[5];
-#pragma unroll
-          for (int i = 4; i >= 0; --i) t = fma_f32x2(t, u, coef[i]);
-          unpack_f32x2(fma_f32x2(y, t, neg), &x[k], &x[k + 1]);
+        for (int k0 = 0; k0 < 32; k0 += 8) {
+          if (__any_sync(0xffffffffu, past_near(sc, big[k0 / 8]))) cap_pairs(v, k0, 8, true);
+          else cap_pairs(v, k0, 8, false);
         }
-        if (__any_sync(0xffffffffu, past_near(sc, big))) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float raw = __uint_as_float(v[k0 + k]);
-            if (past_near(sc, raw)) x[k] = capped_past(sc, raw, sub);
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k0 + k] = __float_as_uint(x[k]);
       }
     } else {
 #pragma unroll
@@ -1167,8 +1185,8 @@ constexpr size_t smem_bytes() {
 
 template <bool F16, bool E4M3, int DP>
 cudaError_t launch(const AttendArgs& a, const TileMaps& maps, cudaStream_t stream) {
-  // either kernel is set up while the one before it ends (the join: runs), and waits
-  // for it itself
+  // either kernel is launched while the one before it ends (the join: runs), and waits
+  // for it itself before anything else
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;

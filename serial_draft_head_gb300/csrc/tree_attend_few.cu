@@ -32,7 +32,7 @@
 // that to 2^-40 of it).
 //
 // What bounds it.  128 single tokens of 500 to 9,000 over e4m3 (64 heads on 8):
-// 315 us, 3.7 TB/s; DRAM at 1.04 times the cache's bytes, 840 warp instructions a
+// 317 us, 3.7 TB/s; DRAM at 1.04 times the cache's bytes, 850 warp instructions a
 // block of 32 keys (conversions, the products, V's scales), issued at 34% of the
 // slots by the three warps a scheduler that registers and rings leave, held by
 // fixed latencies.  The same over bf16 up to 5,000 tokens: 293 us, 4.9 TB/s.  One
@@ -639,8 +639,10 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
           }
           if (__any_sync(0xffffffffu, past_near(sc, big))) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (past_near(sc, raw[k])) x[kg][k] = capped_past(sc, raw[k], sub[k / 2]);
+            for (int k = 0; k < 4; ++k) {
+              const float past = capped_past(sc, raw[k], sub[k / 2]);
+              if (past_near(sc, raw[k])) x[kg][k] = past;
+            }
           }
         }
       }
@@ -893,8 +895,8 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
 template <bool F16, bool E4M3, int DP, bool CAP>
 cudaError_t launch(const AttendArgs& a, cudaStream_t stream) {
   using L = Few<E4M3, DP>;
-  // set up while the kernel before it in the stream ends, which it waits for before
-  // it reads anything (calls in a row: 14.3 to 12.3 us for 1 token)
+  // launched while the kernel before it in the stream ends, which it waits for before
+  // anything else (calls in a row: 14.3 to 12.3 us for 1 token)
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
