@@ -34,7 +34,10 @@
  *     out = sum_j softmax(s)_j v_j,  lse = ln sum_j e^(s_j)
  *
  * A row that sees nothing gets out = 0 and lse = -infinity.  Keys and values
- * at invisible positions do not affect a row, whatever they hold.
+ * at invisible positions do not affect a row, whatever they hold.  Sums, maxima
+ * and out are fp32 until out is rounded; the weights e^(s - m) are rounded once to
+ * a 16-bit type for their product with v: the handle's, or f16 where the cache is
+ * e4m3 and the rows are few.  Any finite scale, and any cap from 0 on.
  *
  * Conventions as in dspark_walk.h: 0 or a negative DSPARK_E* code, nothing
  * traps, calls on one handle are ordered by the caller, `stream` is a
@@ -102,10 +105,11 @@ struct dspark_tree_cache {
 /*
  * The requests of one call, all arrays on the device: pages int32, max_pages
  * entries a request, the requests' rows pages_stride entries apart (max_pages *
- * page_size < 2^31; positions from DSPARK_TREE_MAX_LENGTH on are not used), start int32 [B]
- * (the position of the request's first row), first
- * int32 [B + 1] (the request's rows are first[b] .. first[b+1]-1 of the packed
- * arrays).  N: rows of the packed arrays.
+ * page_size < 2^31; positions from DSPARK_TREE_MAX_LENGTH on are not used), start
+ * int32 [B] (the position of the request's first row), first int32 [B + 1] (the
+ * request's rows are first[b] .. first[b+1]-1 of the packed arrays; no two requests
+ * have a row in common).  None of them changes while a call runs.  N: rows of the
+ * packed arrays.
  */
 struct dspark_tree_batch {
     const int32_t *pages;

@@ -37,7 +37,7 @@
 // chain softmax - product - next S of two streams, and 15 us an item for Q, the
 // masked tiles and the result.  17 nodes over 131,000 tokens: 99 us, 5.4 TB/s.
 // 16 requests of 8 nodes: 60 us, 2.9 TB/s, the ring's five slots against the
-// copies' latency (long scoreboard 7.2 of 14 warp cycles an issue).
+// copies' latency (long scoreboard 7.2 of 15 warp cycles an issue).
 #include "tree_items.cuh"
 
 namespace dspark {

@@ -9,11 +9,12 @@
 // up once per token and block, into shared memory.
 //
 // Prompts of 901 to 8,191 tokens (26,600 in all, 8 heads of 128) written as e4m3:
-// 33.4 us, 4.9 TB/s of bytes read and written; 46,800 tokens read back: 52 us, 5.6.
-// Writing is issued at 56% of the slots: a lane takes two chunks of the row, so that
+// 33.1 us, 5.0 TB/s of bytes read and written; 46,800 tokens read back: 51.3 us, 5.6.
+// Writing is issued at 55% of the slots: a lane takes two chunks of the row, so that
 // what a row costs beside its elements is spread over 16 of them (one chunk: 43.4).
-// 128 tokens take 2.7 us on the device, a path of 17 rows in each of 128 requests 6
-// us with the call: launches.
+// 16-bit, 36,900 tokens: 49.6 us written, 50.8 read, 6.1 and 5.9 TB/s.  128 tokens take
+// 2.7 us on the device (16-bit 2.3), a path of 17 rows in each of 128 requests 7 us with
+// the call: launches.
 #include "tc_ptx.cuh"
 #include "tree_common.cuh"
 

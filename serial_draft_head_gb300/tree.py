@@ -127,7 +127,8 @@ def ancestor_bits(parent, first):
     """The mask words of trees: parent int32 [N], each node's parent as its place within its own
     request's rows (smaller than the node's own; -1: a root, whose parent is the context), first
     int32 [B + 1].  Returns int32 [N, ceil(T / 32)] with T the most nodes of a request: a node
-    sees itself and its ancestors.  Host arithmetic on small arrays; the result is on parent's
+    sees itself and its ancestors.  Host arithmetic (some ms for 64 trees of 64 nodes), and it
+    waits for arrays on the device: not for inside a captured graph.  The result is on parent's
     device."""
     device = parent.device
     parent, first = parent.cpu().long().tolist(), first.cpu().long().tolist()
