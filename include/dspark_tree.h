@@ -23,6 +23,20 @@
  * is one rounding of x, and makes every value exact in bf16 (but those past
  * its range).
  *
+ * A row in 4 bits is held as e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6, and a sign in
+ * the top bit; two a byte, the even element in the low half) and a byte for each
+ * 16 elements, bits 14 .. 7 of the block's scale as an f16:
+ *
+ *     a    = max |x| of the block
+ *     s    = the smallest f16 with three mantissa bits with a <= 6 s, at most 10240
+ *     code = e2m1_rne(x / s), at most 6 in size,   byte = f16 bits of s >> 7,
+ *     value = code * s
+ *
+ * (a = 0: byte 0.  A block that holds a NaN or an infinity: byte 255, codes 0, and
+ * it reads back as NaN.  Bytes 227 to 254 are not written; what a block under one
+ * reads as is not specified.)  A value has six significant bits and is exact in f16
+ * and in bf16.
+ *
  * Attention: node i of request b (row first[b] + i of q) with query head h
  * reads cached head h / (q_heads / kv_heads) at positions 0 .. start[b]-1 (the
  * context: all visible) and start[b] + j, j < T_b (the draft: visible if bit
@@ -37,7 +51,10 @@
  * at invisible positions do not affect a row, whatever they hold.  Sums, maxima
  * and out are fp32 until out is rounded; the weights e^(s - m) are rounded once to
  * a 16-bit type for their product with v: the handle's, or f16 where the cache is
- * e4m3 and the rows are few.  Any finite scale, and any cap from 0 on.
+ * e2m1, or e4m3 and the rows are few.  Over e4m3 with few rows and over e2m1, rows of
+ * q in bf16 are brought to f16 by a power of two each, exact for elements down to 2^-32
+ * of the row's largest and to 2^-40 of that below.  Any finite scale, and any cap from
+ * 0 on.
  *
  * Conventions as in dspark_walk.h: 0 or a negative DSPARK_E* code, nothing
  * traps, calls on one handle are ordered by the caller, `stream` is a
@@ -63,6 +80,7 @@ extern "C" {
 #define DSPARK_TYPE_BF16 0
 #define DSPARK_TYPE_F16 1
 #define DSPARK_TYPE_E4M3 2 /* cache only */
+#define DSPARK_TYPE_E2M1 3 /* cache only */
 
 /* Largest sizes of a handle. */
 #define DSPARK_TREE_MAX_HEAD_DIM 128
@@ -77,7 +95,7 @@ typedef dspark_tree *dspark_tree_t;
 struct dspark_tree_config {
     int q_heads;      /* query heads, a multiple of kv_heads */
     int kv_heads;     /* cached heads */
-    int head_dim;     /* a multiple of 8 (of 16 with an e4m3 cache), at most 128 */
+    int head_dim;     /* a multiple of 8 (e4m3 cache: 16, e2m1: 32), at most 128 */
     int type;         /* DSPARK_TYPE_BF16 or DSPARK_TYPE_F16: q, k, v, out */
     int max_requests; /* largest B of an attend call, at most 1024 */
     int max_nodes;    /* most nodes of one request in an attend call, at most 256 */
@@ -85,12 +103,14 @@ struct dspark_tree_config {
 
 /*
  * A paged cache: k and v are [n_pages, page_size, kv_heads, head_dim] of
- * `type` (the handle's type or DSPARK_TYPE_E4M3), head_dim contiguous, the
- * other strides free: {page, slot, head} in elements.  Base addresses and
- * strides are multiples of 16 bytes, those of pages and slots below 2^31
- * bytes.  k_scale and v_scale, e4m3 only, are bytes [n_pages, page_size,
- * kv_heads] with strides of their own.  NaN codes stand under byte 255 only,
- * as dspark_tree_write leaves them.
+ * `type` (the handle's type, DSPARK_TYPE_E4M3 or DSPARK_TYPE_E2M1), head_dim
+ * contiguous, the other strides free: {page, slot, head} in elements (e2m1: in
+ * bytes).  Base addresses and strides are multiples of 16 bytes, those of pages and
+ * slots below 2^31 bytes.  k_scale and v_scale: e4m3, bytes [n_pages, page_size,
+ * kv_heads] with strides of their own; e2m1, bytes [n_pages, page_size, kv_heads,
+ * head_dim / 16], the last contiguous, addresses and the other strides multiples of
+ * the largest power of two in head_dim / 16.  NaN codes stand under byte 255 only, as
+ * dspark_tree_write leaves them.
  */
 struct dspark_tree_cache {
     void *k, *v;
@@ -138,7 +158,7 @@ int dspark_tree_write(dspark_tree_t h, const struct dspark_tree_cache *cache,
 
 /*
  * Positions start[b] + i of the cache into rows of out_k and out_v
- * ([N, kv_heads, head_dim] contiguous, 16-byte aligned): code * 2^e rounded
+ * ([N, kv_heads, head_dim] contiguous, 16-byte aligned): code times scale rounded
  * once to the handle's type; values past its range become the largest finite
  * one.
  */

@@ -70,10 +70,13 @@ class OnDevice {
 
 int make_cache(const dspark_tree* h, const dspark_tree_cache* c, CacheView* out) {
   if (!c || !c->k || !c->v) return DSPARK_EINVAL;
-  if (c->type != h->cfg.type && c->type != DSPARK_TYPE_E4M3) return DSPARK_EINVAL;
-  const bool e4m3 = c->type == DSPARK_TYPE_E4M3;
-  const int es = e4m3 ? 1 : 2;
-  if (e4m3 && (!c->k_scale || !c->v_scale || h->cfg.head_dim % 16)) return DSPARK_EINVAL;
+  const bool e2m1 = c->type == DSPARK_TYPE_E2M1, scaled = e2m1 || c->type == DSPARK_TYPE_E4M3;
+  if (c->type != h->cfg.type && !scaled) return DSPARK_EINVAL;
+  const int es = scaled ? 1 : 2;
+  if (scaled && (!c->k_scale || !c->v_scale || h->cfg.head_dim % (e2m1 ? 32 : 16)))
+    return DSPARK_EINVAL;
+  // bytes that a row's scales are read by at once: 8, 4 or 2
+  const int64_t together = e2m1 ? h->cfg.head_dim / 16 & -(h->cfg.head_dim / 16) : 1;
   if (c->n_pages < 1 || c->n_pages >= ((int64_t)1 << 31) || c->page_size < 1) return DSPARK_EINVAL;
   if (!aligned16(c->k) || !aligned16(c->v)) return DSPARK_EINVAL;
   for (int v = 0; v < 2; ++v) {
@@ -81,20 +84,27 @@ int make_cache(const dspark_tree* h, const dspark_tree_cache* c, CacheView* out)
     const int64_t* ss = v ? c->v_scale_stride : c->k_scale_stride;
     for (int i = 0; i < 3; ++i) {
       if (!stride_ok(st[i], es)) return DSPARK_EINVAL;
-      if (e4m3 && (ss[i] < 0 || ss[i] > ((int64_t)1 << 40))) return DSPARK_EINVAL;
+      if (scaled && (ss[i] < 0 || ss[i] > ((int64_t)1 << 40) || ss[i] % together))
+        return DSPARK_EINVAL;
       // pages and slots lie within 2 GB strides (see Rows); heads may be further apart
-      if (i < 2 && (st[i] * es >= ((int64_t)1 << 31) || (e4m3 && ss[i] >= ((int64_t)1 << 31))))
+      if (i < 2 && (st[i] * es >= ((int64_t)1 << 31) || (scaled && ss[i] >= ((int64_t)1 << 31))))
         return DSPARK_EINVAL;
     }
+    if (scaled && reinterpret_cast<uintptr_t>(v ? c->v_scale : c->k_scale) % together)
+      return DSPARK_EINVAL;
     out->x[v] = {static_cast<uint8_t*>(v ? c->v : c->k), st[2] * es, (uint32_t)(st[0] * es),
                  (uint32_t)(st[1] * es)};
     out->scale[v] = {nullptr, 0, 0, 0};
-    if (e4m3)
+    if (scaled)
       out->scale[v] = {v ? c->v_scale : c->k_scale, ss[2], (uint32_t)ss[0], (uint32_t)ss[1]};
   }
   out->n_pages = c->n_pages;
   out->page = FastDiv::of(c->page_size);
   return DSPARK_OK;
+}
+
+Held held_as(const dspark_tree_cache* c) {
+  return c->type == DSPARK_TYPE_E4M3 ? kE4M3 : c->type == DSPARK_TYPE_E2M1 ? kE2M1 : k16;
 }
 
 // Tiled-copy maps of a 16-bit cache whose pages cut a 128-key tile into one or
@@ -105,7 +115,7 @@ int make_cache(const dspark_tree* h, const dspark_tree_cache* c, CacheView* out)
 void make_maps(const dspark_tree* h, const dspark_tree_cache* c, const CacheView& v, TileMaps* m) {
   m->rows = 0;
   const int page = c->page_size;
-  if (c->type == DSPARK_TYPE_E4M3 || !h->encode) return;
+  if (held_as(c) != k16 || !h->encode) return;
   if (page % 128 != 0 && page != 64) return;
   const cuuint64_t dims[4] = {(cuuint64_t)h->cfg.head_dim, (cuuint64_t)page,
                               (cuuint64_t)h->cfg.kv_heads, (cuuint64_t)c->n_pages};
@@ -203,6 +213,7 @@ int dspark_tree_create(const dspark_tree_config* cfg, dspark_tree_t* out) {
   }
   if (e == cudaSuccess) e = attend_setup(cfg->type == DSPARK_TYPE_F16, cfg->head_dim);
   if (e == cudaSuccess) e = few_setup(cfg->type == DSPARK_TYPE_F16, cfg->head_dim);
+  if (e == cudaSuccess) e = few4_setup(cfg->type == DSPARK_TYPE_F16, cfg->head_dim);
   if (e != cudaSuccess) {
     dspark_tree_destroy(h);
     return cuda_code(e);
@@ -234,8 +245,7 @@ int dspark_tree_write(dspark_tree_t h, const dspark_tree_cache* cache,
   a.kv2 = FastDiv::of(2 * a.Hkv);
   a.D = h->cfg.head_dim;
   a.status = h->status;
-  return cuda_code(write_launch(a, h->cfg.type == DSPARK_TYPE_F16,
-                                cache->type == DSPARK_TYPE_E4M3, h->sm_count,
+  return cuda_code(write_launch(a, h->cfg.type == DSPARK_TYPE_F16, held_as(cache), h->sm_count,
                                 static_cast<cudaStream_t>(stream)));
 }
 
@@ -256,8 +266,7 @@ int dspark_tree_read(dspark_tree_t h, const dspark_tree_cache* cache,
   a.kv2 = FastDiv::of(2 * a.Hkv);
   a.D = h->cfg.head_dim;
   a.status = h->status;
-  return cuda_code(read_launch(a, h->cfg.type == DSPARK_TYPE_F16,
-                               cache->type == DSPARK_TYPE_E4M3, h->sm_count,
+  return cuda_code(read_launch(a, h->cfg.type == DSPARK_TYPE_F16, held_as(cache), h->sm_count,
                                static_cast<cudaStream_t>(stream)));
 }
 
@@ -279,8 +288,9 @@ int dspark_tree_keep(dspark_tree_t h, const dspark_tree_cache* cache,
   a.path_stride = path_stride;
   a.max_path = max_path;
   a.Hkv = h->cfg.kv_heads;
-  a.scales = cache->type == DSPARK_TYPE_E4M3;
-  a.row_bytes = h->cfg.head_dim * (a.scales ? 1 : 2);
+  const Held held = held_as(cache);
+  a.scale_bytes = held == kE4M3 ? 1 : held == kE2M1 ? h->cfg.head_dim / 16 : 0;
+  a.row_bytes = held == kE2M1 ? h->cfg.head_dim / 2 : h->cfg.head_dim * (held == kE4M3 ? 1 : 2);
   a.status = h->status;
   return cuda_code(keep_launch(a, static_cast<cudaStream_t>(stream)));
 }
@@ -327,6 +337,9 @@ int dspark_tree_attend(dspark_tree_t h, const dspark_tree_cache* cache,
   a.part_rows = h->part_rows;
   a.arrived = h->status + 1;
   a.status = h->status;
+  if (held_as(cache) == kE2M1)
+    return cuda_code(few4_launch(a, h->cfg.type == DSPARK_TYPE_F16,
+                                 static_cast<cudaStream_t>(stream)));
   // Few rows a cached head on average: the kernel that has tiles of 16 of them (any
   // number of rows is right in either).  16 requests of 300 to 6,000 tokens, 8 heads,
   // us here / there.  16-slot pages, 16-bit: 4 rows 56 / 67, 16 rows 57 / 67, 20 rows

@@ -236,68 +236,6 @@ __device__ __noinline__ void join_parts(const AttendArgs& a, FewState& st, float
   }
 }
 
-// The blocks of one warp in order: of every segment those t0 + warp, t0 + warp +
-// warps, ...
-template <class Item, int EXTRA>
-struct BlockCursor {
-  int b, head, group, t, end;           // end: of the segment
-  int rows, start, tiles, groups;
-  int64_t after;                        // units of the share after this segment
-  bool more;
-
-  __device__ void load(const AttendArgs& a) {
-    bool ok;
-    const typename Item::Request r = Item::load_request(a, b, &ok);
-    rows = r.rows;
-    start = r.start;
-    tiles = r.tiles;
-    groups = r.groups;
-  }
-  __device__ void settle(const AttendArgs& a, int warp) {     // past the ends of segments
-    while (t >= end) {
-      if (after <= EXTRA) {             // no more tiles in the share
-        more = false;
-        return;
-      }
-      if (++group == groups) {
-        group = 0;
-        if (++head == a.Hkv) {
-          head = 0;
-          do {
-            if (++b >= a.b.B) {         // the arrays changed under the kernel
-              more = false;
-              return;
-            }
-            load(a);
-          } while (rows == 0);
-        }
-      }
-      after -= EXTRA;
-      end = (int)(after < tiles ? after : tiles);
-      after -= end;
-      t = warp;
-    }
-  }
-  __device__ void init(const AttendArgs& a, const Share& s, int warp) {
-    more = s.units > 0;
-    if (!more) return;
-    b = s.b0;
-    head = s.head0;
-    group = s.group0;
-    load(a);
-    const int64_t rest = tiles - s.t0;
-    const int n = (int)(rest < s.units ? rest : s.units);
-    end = s.t0 + n;                     // below 0: the share ends before the tiles
-    t = max(s.t0, 0) + warp;
-    after = s.units - n;
-    settle(a, warp);
-  }
-  __device__ void next(const AttendArgs& a, int warp, int warps) {
-    t += warps;
-    if (t >= end) settle(a, warp);
-  }
-};
-
 // CAP: scores are capped.  A kernel of its own, for the capped form's code in the loop
 // costs other calls: 64 single tokens of 500 to 6,800 over a 16-bit cache, no cap, 210
 // us with it, 196 without; capped 222 (scores all far from the cap), 228 (near it).

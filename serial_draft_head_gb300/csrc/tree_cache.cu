@@ -82,13 +82,43 @@ __device__ __forceinline__ Place place_of_row(const RowsArgs& a, int r, int rows
   return p;
 }
 
-// LANES lanes a row, 16 bytes of the cache each (8 elements, or 16 codes).
-template <bool F16, bool E4M3, int LANES>
+// A block of 16 elements to e2m1 codes and its scale byte (the header has the rule).
+// x / s only has to fall on the right side of the codes' borders: x has 11 significant
+// bits at most and a border times s seven, so x / s is on a border or 2^-13 away from
+// it, and the product by fl(1 / s), off by 2^-21, rounded to a multiple of 2^-16 (by
+// adding 192 and taking it off again) is on the border or the same side of it.
+template <bool F16>
+__device__ __forceinline__ uint2 block_to_e2m1(const uint32_t (&w)[8], uint32_t* byte) {
+  uint32_t big2 = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) big2 = __vmaxu2(big2, w[k] & 0x7fff7fffu);
+  const uint32_t big = __float_as_uint(to_float<F16>((uint16_t)max(big2 & 0xffffu, big2 >> 16)));
+  const bool bad = big >= 0x7f800000u;
+  *byte = bad ? 255u : e2m1_scale_byte(big);
+  const float s = __half2float(__ushort_as_half((uint16_t)(*byte << 7)));
+  const float inv = *byte == 0 || bad ? 0.f : 1.f / s;
+  uint32_t code[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float y[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint16_t x = (uint16_t)(w[4 * h + k / 2] >> (16 * (k & 1)));
+      y[k] = fmaf(to_float<F16>(x), inv, 192.f) - 192.f;
+    }
+    code[h] = float8_to_e2m1(y);
+  }
+  return bad ? make_uint2(0u, 0u) : make_uint2(code[0], code[1]);
+}
+
+// LANES lanes a row, 16 bytes of the cache each (8 elements, or 16 codes; e2m1: 8
+// bytes, 16 codes).
+template <bool F16, Held HELD, int LANES>
 __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__ RowsArgs a,
                                                          int tok) {
   __shared__ Token toks[kMaxTok];
   constexpr int kGroups = kThreads / LANES;
-  constexpr int kLoads = E4M3 ? 2 : 1;             // 16-byte chunks of the row a lane
+  constexpr int kLoads = HELD == k16 ? 1 : 2;      // 16-byte chunks of the row a lane
   const int n0 = blockIdx.x * tok;
   const int n_tok = min(tok, a.b.N - n0);
   find_tokens(a, n0, n_tok, toks);
@@ -114,8 +144,19 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       uint8_t* dst = a.c.x[p[i].v].at(p[i].t.page, p[i].t.slot, p[i].head);
-      if (!E4M3) {
+      if (HELD == k16) {
         if (p[i].on && in_row) reinterpret_cast<uint4*>(dst)[lane] = x[i][0];
+        continue;
+      }
+      if constexpr (HELD == kE2M1) {               // a lane has a block of its own
+        const uint32_t block[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w,
+                                   x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
+        uint32_t byte;
+        const uint2 code = block_to_e2m1<F16>(block, &byte);
+        if (p[i].on && in_row) {
+          reinterpret_cast<uint2*>(dst)[lane] = code;
+          a.c.scale[p[i].v].at(p[i].t.page, p[i].t.slot, p[i].head)[lane] = (uint8_t)byte;
+        }
         continue;
       }
       uint32_t w[4 * kLoads];
@@ -159,13 +200,13 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__
   }
 }
 
-// LANES lanes a row, 16 bytes of the cache each (8 elements, or 16 codes).
-template <bool F16, bool E4M3, int LANES>
+// LANES lanes a row, as they write it.
+template <bool F16, Held HELD, int LANES>
 __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ RowsArgs a,
                                                         int tok) {
   __shared__ Token toks[kMaxTok];
   constexpr int kGroups = kThreads / LANES;
-  constexpr int kEach = E4M3 ? 16 : 8;
+  constexpr int kEach = HELD == k16 ? 8 : 16;
   const int n0 = blockIdx.x * tok;
   const int n_tok = min(tok, a.b.N - n0);
   find_tokens(a, n0, n_tok, toks);
@@ -181,8 +222,16 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
       p[i] = place_of_row(a, r0 + group + i * kGroups, rows, toks);
       byte[i] = 127;
       if (p[i].on) {
-        x[i] = ptx::ldg_nc_na(a.c.x[p[i].v].at(p[i].t.page, p[i].t.slot, p[i].head) + lane * 16);
-        if (E4M3) byte[i] = __ldg(a.c.scale[p[i].v].at(p[i].t.page, p[i].t.slot, p[i].head));
+        const uint8_t* src = a.c.x[p[i].v].at(p[i].t.page, p[i].t.slot, p[i].head);
+        const uint8_t* scale = a.c.scale[p[i].v].at(p[i].t.page, p[i].t.slot, p[i].head);
+        if (HELD == kE2M1) {
+          const uint2 y = __ldg(reinterpret_cast<const uint2*>(src) + lane);
+          x[i] = make_uint4(y.x, y.y, 0, 0);
+          byte[i] = __ldg(scale + lane);
+        } else {
+          x[i] = ptx::ldg_nc_na(src + lane * 16);
+          if (HELD == kE4M3) byte[i] = __ldg(scale);
+        }
       }
     }
 #pragma unroll
@@ -190,8 +239,25 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
       if (!p[i].on) continue;
       uint16_t* out = a.out[p[i].v] + ((int64_t)(n0 + p[i].tok) * a.Hkv + p[i].head) * a.D;
       uint4* dst = reinterpret_cast<uint4*>(out + lane * kEach);
-      if (!E4M3) {
+      if (HELD == k16) {
         *dst = x[i];
+        continue;
+      }
+      if constexpr (HELD == kE2M1) {
+        // every value is exact in f16, and the bf16 that it becomes is exact too
+        const uint32_t s2 = byte[i] * 0x00800080u;
+        const uint4 lo = e2m1x8_to_f16(x[i].x), hi = e2m1x8_to_f16(x[i].y);
+        uint32_t y[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          y[k] = mul_f16x2(y[k], s2);
+          if (!F16) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&y[k]));
+            y[k] = pack2<false>(f.x, f.y);
+          }
+        }
+        dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
+        dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
         continue;
       }
       const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
@@ -286,10 +352,11 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constan
     }
   }
   const int s = c - 2 * chunks;                    // the scale bytes' columns follow
-  if (a.scales && s >= 0 && s < 2 * a.Hkv) {
-    const int v = s >= a.Hkv;
+  const int bytes = a.scale_bytes * a.Hkv;         // of K
+  if (s >= 0 && s < 2 * bytes) {
+    const int v = s >= bytes, ss = s - v * bytes, head = ss / a.scale_bytes;
     const Rows rows = a.c.scale[v];
-    uint8_t* base = rows.of_head(s - v * a.Hkv);
+    uint8_t* base = rows.of_head(head) + (ss - head * a.scale_bytes);
     for (int i0 = 0; i0 < n; i0 += kKeepBatch) {
       uint8_t x[kKeepBatch];
 #pragma unroll
@@ -302,55 +369,59 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constan
   }
 }
 
-template <bool F16, bool E4M3, int LANES>
+template <bool F16, Held HELD, int LANES>
 void launch_write(const RowsArgs& a, int sm_count, cudaStream_t stream) {
   const int tok = tokens_per_block(a, LANES, sm_count);
-  write_kernel<F16, E4M3, LANES><<<blocks_of(a, tok), kThreads, 0, stream>>>(a, tok);
+  write_kernel<F16, HELD, LANES><<<blocks_of(a, tok), kThreads, 0, stream>>>(a, tok);
 }
 
-template <bool F16, bool E4M3, int LANES>
+template <bool F16, Held HELD, int LANES>
 void launch_read(const RowsArgs& a, int sm_count, cudaStream_t stream) {
   const int tok = tokens_per_block(a, LANES, sm_count);
-  read_kernel<F16, E4M3, LANES><<<blocks_of(a, tok), kThreads, 0, stream>>>(a, tok);
+  read_kernel<F16, HELD, LANES><<<blocks_of(a, tok), kThreads, 0, stream>>>(a, tok);
 }
 
 // Half the lanes for heads of up to 64 elements: lanes without elements cost as
 // much as the others (prompts over e4m3: 19.4 us against 27.8 with those of 128).
-template <bool F16, bool E4M3>
+template <bool F16, Held HELD>
 void write_for(const RowsArgs& a, int sm_count, cudaStream_t stream) {
-  constexpr int kEach = E4M3 ? 16 : 8;
-  if (a.D <= 64) launch_write<F16, E4M3, 64 / kEach>(a, sm_count, stream);
-  else launch_write<F16, E4M3, 128 / kEach>(a, sm_count, stream);
+  constexpr int kEach = HELD == k16 ? 8 : 16;
+  if (a.D <= 64) launch_write<F16, HELD, 64 / kEach>(a, sm_count, stream);
+  else launch_write<F16, HELD, 128 / kEach>(a, sm_count, stream);
 }
 
-template <bool F16, bool E4M3>
+template <bool F16, Held HELD>
 void read_for(const RowsArgs& a, int sm_count, cudaStream_t stream) {
-  constexpr int kEach = E4M3 ? 16 : 8;
-  if (a.D <= 64) launch_read<F16, E4M3, 64 / kEach>(a, sm_count, stream);
-  else launch_read<F16, E4M3, 128 / kEach>(a, sm_count, stream);
+  constexpr int kEach = HELD == k16 ? 8 : 16;
+  if (a.D <= 64) launch_read<F16, HELD, 64 / kEach>(a, sm_count, stream);
+  else launch_read<F16, HELD, 128 / kEach>(a, sm_count, stream);
 }
 
 }  // namespace
 
 // A 16-bit cache holds the rows' own bits, whichever of the two types.
-cudaError_t write_launch(const RowsArgs& a, bool f16, bool e4m3, int sm_count,
+cudaError_t write_launch(const RowsArgs& a, bool f16, Held held, int sm_count,
                          cudaStream_t stream) {
-  if (!e4m3) write_for<false, false>(a, sm_count, stream);
-  else if (f16) write_for<true, true>(a, sm_count, stream);
-  else write_for<false, true>(a, sm_count, stream);
+  if (held == k16) write_for<false, k16>(a, sm_count, stream);
+  else if (held == kE4M3 && f16) write_for<true, kE4M3>(a, sm_count, stream);
+  else if (held == kE4M3) write_for<false, kE4M3>(a, sm_count, stream);
+  else if (f16) write_for<true, kE2M1>(a, sm_count, stream);
+  else write_for<false, kE2M1>(a, sm_count, stream);
   return cudaGetLastError();
 }
 
-cudaError_t read_launch(const RowsArgs& a, bool f16, bool e4m3, int sm_count,
+cudaError_t read_launch(const RowsArgs& a, bool f16, Held held, int sm_count,
                         cudaStream_t stream) {
-  if (!e4m3) read_for<false, false>(a, sm_count, stream);
-  else if (f16) read_for<true, true>(a, sm_count, stream);
-  else read_for<false, true>(a, sm_count, stream);
+  if (held == k16) read_for<false, k16>(a, sm_count, stream);
+  else if (held == kE4M3 && f16) read_for<true, kE4M3>(a, sm_count, stream);
+  else if (held == kE4M3) read_for<false, kE4M3>(a, sm_count, stream);
+  else if (f16) read_for<true, kE2M1>(a, sm_count, stream);
+  else read_for<false, kE2M1>(a, sm_count, stream);
   return cudaGetLastError();
 }
 
 cudaError_t keep_launch(const KeepArgs& a, cudaStream_t stream) {
-  const int columns = a.row_bytes / 16 * a.Hkv * 2 + (a.scales ? 2 * a.Hkv : 0);
+  const int columns = (a.row_bytes / 16 + a.scale_bytes) * a.Hkv * 2;
   const dim3 grid(a.b.B, (columns + kKeepThreads - 1) / kKeepThreads);
   keep_kernel<<<grid, kKeepThreads, 0, stream>>>(a);
   return cudaGetLastError();

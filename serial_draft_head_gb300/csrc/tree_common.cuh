@@ -50,9 +50,13 @@ struct Rows {
   }
 };
 
+// How the cache holds a row: 16-bit values, e4m3 codes under one scale, or e2m1 codes
+// under a scale for each 16.
+enum Held { k16, kE4M3, kE2M1 };
+
 struct CacheView {
   Rows x[2];                 // K, V
-  Rows scale[2];             // their scale bytes, e4m3 only
+  Rows scale[2];             // their scale bytes, not 16-bit
   int64_t n_pages;
   FastDiv page;
 };
@@ -184,6 +188,58 @@ __device__ __forceinline__ uint32_t scale_mul2(uint32_t byte) {
   return F16 ? (byte - 112) * 0x04000400u : byte * 0x00800080u + 120u * 0x00800080u;
 }
 
+// Four e2m1 codes' pairs: byte i of a word, two codes, as f16x2, exactly.
+__device__ __forceinline__ uint4 e2m1x8_to_f16(uint32_t w) {
+  uint4 r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+      : "r"(w));
+  return r;
+}
+
+// Eight floats, at most 6 in size after rounding, to e2m1 codes, nearest even, the
+// first in the low half of byte 0.
+__device__ __forceinline__ uint32_t float8_to_e2m1(const float (&x)[8]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// The last scale byte of a block of e2m1 codes that is written, 10240.
+constexpr uint32_t kTopScale = 226;
+
+// The scale byte of a block of 16 elements whose largest magnitude's float bits are
+// `big` (finite): the smallest s of three mantissa bits with 6 s >= a.  The product
+// by fl(1/6) = (1 + 2^-25) / 6 rounds to s where a = 6 s, 1.875 * 2^-25 being less than
+// half of 2^-23; elsewhere a, of 11 significant bits at most, is 2^-11 of itself away
+// from 6 s.
+__device__ __forceinline__ uint32_t e2m1_scale_byte(uint32_t big) {
+  const float t = __uint_as_float(big) * (1.f / 6.f);
+  // from 2^-14 on: exponent and three bits, rounded up; below, multiples of 2^-17
+  const uint32_t bits = __float_as_uint(t);
+  const uint32_t normal = ((bits + 0xfffffu) >> 20) - ((127u - 15u) << 3);
+  const uint32_t small = (uint32_t)ceilf(t * 0x1p17f);
+  return min(bits >= 0x38800000u ? normal : small, kTopScale);
+}
+
 struct AttendArgs {
   CacheView c;
   BatchView b;
@@ -222,6 +278,10 @@ struct TileMaps {
   int rows;
 };
 
+// e2m1 cache, few rows a cached head (tree_attend_few4.cu).
+cudaError_t few4_setup(bool f16, int D);
+cudaError_t few4_launch(const AttendArgs& a, bool f16, cudaStream_t stream);
+
 // Few rows a cached head, on mma.sync (tree_attend_few.cu).
 cudaError_t few_setup(bool f16, int D);
 cudaError_t few_launch(const AttendArgs& a, bool f16, bool e4m3, cudaStream_t stream);
@@ -242,9 +302,9 @@ struct RowsArgs {
   int* status;
 };
 
-cudaError_t write_launch(const RowsArgs& a, bool f16, bool e4m3, int sm_count,
+cudaError_t write_launch(const RowsArgs& a, bool f16, Held held, int sm_count,
                          cudaStream_t stream);
-cudaError_t read_launch(const RowsArgs& a, bool f16, bool e4m3, int sm_count,
+cudaError_t read_launch(const RowsArgs& a, bool f16, Held held, int sm_count,
                         cudaStream_t stream);
 
 struct KeepArgs {
@@ -255,7 +315,7 @@ struct KeepArgs {
   int64_t path_stride;
   int max_path;
   int Hkv, row_bytes;        // bytes of one head's row
-  bool scales;
+  int scale_bytes;           // and of its scales
   int* status;
 };
 

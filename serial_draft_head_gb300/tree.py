@@ -1,7 +1,7 @@
 """Thin ctypes binding of include/dspark_tree.h: the target model's check of
 drafted tokens over a paged key/value cache.
 
-    cache = KVCache(k, v)                        # or KVCache(k_e4m3, v_e4m3, k_scale, v_scale)
+    cache = KVCache(k, v)                        # or KVCache(codes_k, codes_v, k_scale, v_scale)
     tree = Tree(q_heads, kv_heads, head_dim, max_requests=B, max_nodes=T)
     tree.write(cache, pages, length, first, k, v)             # the draft's keys and values
     out, lse = tree.attend(q, cache, pages, length, first, mask=ancestor_bits(parent, first))
@@ -24,13 +24,15 @@ from .walk import WalkError, _check
 TYPE_BF16 = 0
 TYPE_F16 = 1
 TYPE_E4M3 = 2
+TYPE_E2M1 = 3
 
 TREE_MAX_HEAD_DIM = 128
 TREE_MAX_REQUESTS = 1024
 TREE_MAX_NODES = 256
 TREE_MAX_LENGTH = 2147483392
 
-_TYPES = {torch.bfloat16: TYPE_BF16, torch.float16: TYPE_F16, torch.float8_e4m3fn: TYPE_E4M3}
+_TYPES = {torch.bfloat16: TYPE_BF16, torch.float16: TYPE_F16, torch.float8_e4m3fn: TYPE_E4M3,
+          torch.uint8: TYPE_E2M1}
 
 EXPORTS = ["dspark_tree_create", "dspark_tree_write", "dspark_tree_read", "dspark_tree_keep",
            "dspark_tree_attend", "dspark_tree_status", "dspark_tree_destroy"]
@@ -92,35 +94,58 @@ def _need(ok, what):
 
 
 class KVCache:
-    """A paged cache: k and v [n_pages, page_size, kv_heads, head_dim], bfloat16, float16 or
-    float8_e4m3fn (then with uint8 scales [n_pages, page_size, kv_heads]).  Any strides that are
-    multiples of 16 bytes, head_dim contiguous.  Holds the tensors, not copies of them."""
+    """A paged cache: k and v [n_pages, page_size, kv_heads, head_dim], bfloat16, float16,
+    float8_e4m3fn (then with uint8 scales [n_pages, page_size, kv_heads]), or 4 bits an element:
+    uint8 [n_pages, page_size, kv_heads, head_dim / 2], two e2m1 codes a byte, with uint8 scales
+    [n_pages, page_size, kv_heads, head_dim / 16].  Any strides that are multiples of 16 bytes
+    (scales of e2m1: of the largest power of two in head_dim / 16), the last dimension contiguous.
+    Holds the tensors, not copies of them."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         _need(k.is_cuda and v.is_cuda and k.device == v.device, "k and v are on one CUDA device")
         _need(k.dim() == 4 and k.shape == v.shape, "k and v are [n_pages, page_size, heads, dim]")
-        _need(k.dtype in _TYPES and v.dtype == k.dtype, "k and v are bf16, f16 or e4m3")
+        _need(k.dtype in _TYPES and v.dtype == k.dtype, "k and v are bf16, f16, e4m3 or uint8 (e2m1)")
         _need(k.stride(3) == 1 and v.stride(3) == 1, "head_dim is contiguous")
-        e4m3 = k.dtype == torch.float8_e4m3fn
-        _need((k_scale is not None) == e4m3 and (v_scale is not None) == e4m3,
-              "an e4m3 cache, and no other, has scales")
+        e4m3, e2m1 = k.dtype == torch.float8_e4m3fn, k.dtype == torch.uint8
+        _need((k_scale is not None) == (e4m3 or e2m1) and (v_scale is not None) == (e4m3 or e2m1),
+              "an e4m3 or e2m1 cache, and no other, has scales")
         c = dspark_tree_cache(k=k.data_ptr(), v=v.data_ptr(), n_pages=k.shape[0],
                               page_size=k.shape[1], type=_TYPES[k.dtype])
         c.k_stride[:] = k.stride()[:3]
         c.v_stride[:] = v.stride()[:3]
-        if e4m3:
+        self.kv_heads, self.head_dim = k.shape[2], k.shape[3] * (2 if e2m1 else 1)
+        if e4m3 or e2m1:
+            shape = k.shape[:3] if e4m3 else k.shape[:3] + (self.head_dim // 16,)
             for s in (k_scale, v_scale):
-                _need(s.device == k.device and s.dtype == torch.uint8 and s.shape == k.shape[:3],
-                      "scales are uint8 [n_pages, page_size, heads]")
+                _need(s.device == k.device and s.dtype == torch.uint8 and s.shape == shape,
+                      "scales are uint8 [n_pages, page_size, heads], of e2m1 [.., head_dim / 16]")
+                _need(e4m3 or s.shape[3] <= 1 or s.stride(3) == 1, "a row's scales are contiguous")
             c.k_scale, c.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
-            c.k_scale_stride[:] = k_scale.stride()
-            c.v_scale_stride[:] = v_scale.stride()
+            c.k_scale_stride[:] = k_scale.stride()[:3]
+            c.v_scale_stride[:] = v_scale.stride()[:3]
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.device, self.dtype = k.device, k.dtype
-        self.kv_heads, self.head_dim = k.shape[2], k.shape[3]
         self.key = (k.get_device(), self.kv_heads, self.head_dim, self.dtype)
         self.c = c
         self.address = ctypes.addressof(c)
+
+    @classmethod
+    def zeros(cls, n_pages, page_size, kv_heads, head_dim, dtype, device="cuda"):
+        """A cache of zeros; dtype torch.uint8: e2m1.  A page holds the slots of one head next to
+        each other, as attention reads them (e2m1: a head's scales of 16 slots are 128 bytes that
+        way, and 8 bytes of every 64 with the heads of a slot next to each other)."""
+        _need(dtype in _TYPES, "a cache is bf16, f16, e4m3 or uint8 (e2m1)")
+        e2m1 = dtype == torch.uint8
+
+        def rows(*last, of=torch.uint8):
+            return torch.zeros(n_pages, kv_heads, page_size, *last, dtype=of, device=device).transpose(1, 2)
+
+        x = [rows(head_dim // 2 if e2m1 else head_dim, of=dtype) for _ in range(2)]
+        if e2m1:
+            return cls(*x, rows(head_dim // 16), rows(head_dim // 16))
+        if dtype == torch.float8_e4m3fn:
+            return cls(*x, rows(), rows())
+        return cls(*x)
 
 
 def ancestor_bits(parent, first):
@@ -168,8 +193,8 @@ class Tree:
                    "dspark_tree_create")
         self.h = h.value
         self._index = self.device.index
-        self._key = (self._index, kv_heads, head_dim, dtype)
-        self._key_e4m3 = (self._index, kv_heads, head_dim, torch.float8_e4m3fn)
+        self._keys = {(self._index, kv_heads, head_dim, t)
+                      for t in (dtype, torch.float8_e4m3fn, torch.uint8)}
         self._scale = head_dim ** -0.5
         self._batch = dspark_tree_batch()
         self._batch_mem = (ctypes.c_char * ctypes.sizeof(self._batch)).from_buffer(self._batch)
@@ -181,8 +206,8 @@ class Tree:
     # ---- argument marshalling: a few microseconds a call matter here ----
 
     def _cache(self, cache):
-        if cache.key != self._key and cache.key != self._key_e4m3:
-            raise ValueError("the cache has the handle's device, heads, head_dim and type (or e4m3)")
+        if cache.key not in self._keys:
+            raise ValueError("the cache has the handle's device, heads, head_dim and type (or e4m3, e2m1)")
         return cache.address
 
     def _requests(self, pages, start, first, n_rows):
