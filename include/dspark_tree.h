@@ -8,7 +8,9 @@
  *  2. lets every drafted token attend to the cached context and to its own
  *     ancestors in the draft (dspark_tree_attend),
  *  3. keeps the accepted path's rows of the cache (dspark_tree_keep).
- * dspark_tree_read gives cached rows back in the model's type.
+ * dspark_tree_read gives cached rows back in the model's type.  dspark_tree_place is
+ * the first step for a model that norms and rotates its query and key heads: it does that
+ * on the way into the cache.  dspark_pages.h has the page tables and slots.
  *
  * The cache is paged: position p of request b is slot p % page_size of page
  * pages[b][p / page_size].  A quantised row (one token, one head) is held as
@@ -189,6 +191,53 @@ int dspark_tree_attend(dspark_tree_t h, const struct dspark_tree_cache *cache,
                        const int64_t *q_stride, const uint32_t *mask, int64_t mask_stride,
                        int mask_words, float scale, float softcap, void *out, float *lse,
                        void *stream);
+
+/*
+ * Norms of query and key heads, and the rotation by a token's position.  A row x of
+ * head_dim elements (a multiple of 16) becomes, in fp32 with one rounding at the end:
+ *
+ *     y_d = x_d / sqrt(mean x^2 + eps) * norm_d         (without norm: y = x)
+ *     t   = 2 pi position turns_i / 2^64                 pair i = (a, b):
+ *     y_a, y_b = y_a cos t - y_b sin t, y_b cos t + y_a sin t
+ *
+ * for the pairs i < rotary_dim / 2 (rotary_dim a multiple of 16, from 0 to head_dim):
+ * elements i and i + rotary_dim / 2, or, interleaved, 2 i and 2 i + 1.  The elements
+ * past rotary_dim are not turned.  Arrays on the device: turns [rotary_dim / 2], the
+ * turns of a position as fractions of 2^64 (whole turns do not count), norms fp32
+ * [head_dim], 16-byte aligned.
+ */
+struct dspark_tree_rotation {
+    const uint64_t *turns;
+    const float *q_norm; /* or null: no norm */
+    const float *k_norm; /* or null */
+    float eps;
+    int rotary_dim;
+    int interleaved;
+};
+
+/*
+ * Rows of q [N, q_heads, head_dim] and k [N, kv_heads, head_dim] (strides {row, head}
+ * in elements, 16-byte multiples) to out_q and out_k, contiguous, 16-byte aligned.
+ * position int32 [N], of any sign.
+ */
+int dspark_tree_rotate(dspark_tree_t h, const struct dspark_tree_rotation *rotation,
+                       const int32_t *position, int N, const void *q, const int64_t *q_stride,
+                       const void *k, const int64_t *k_stride, void *out_q, void *out_k,
+                       void *stream);
+
+/*
+ * The same with k and v on their way into the cache: rows of k, normed, rotated and
+ * rounded, and of v as they are, go to slot[n] of the cache (page slot / page_size, place
+ * slot % page_size; int32 [N], no two rows in the same slot), quantised where it is, as
+ * dspark_tree_rotate and then dspark_tree_write leave them.  A row whose slot is below 0
+ * is left out: out_q and the cache stay as they were there.  So is one past the cache, and
+ * dspark_tree_status then returns DSPARK_EPAGES.  n_pages * page_size < 2^31.
+ */
+int dspark_tree_place(dspark_tree_t h, const struct dspark_tree_cache *cache, const int32_t *slot,
+                      const struct dspark_tree_rotation *rotation, const int32_t *position, int N,
+                      const void *q, const int64_t *q_stride, const void *k,
+                      const int64_t *k_stride, const void *v, const int64_t *v_stride, void *out_q,
+                      void *stream);
 
 /* Wait for the stream; return and clear the handle's device status. */
 int dspark_tree_status(dspark_tree_t h, void *stream);

@@ -24,7 +24,7 @@ def sources():
 
 def _deps():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files += [os.path.join(ROOT, "include", f) for f in ("dspark_walk.h", "dspark_tree.h")]
+    files += [os.path.join(ROOT, "include", f) for f in ("dspark_walk.h", "dspark_tree.h", "dspark_pages.h")]
     files.append(os.path.abspath(__file__))
     return files
 

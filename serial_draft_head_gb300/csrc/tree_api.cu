@@ -158,6 +158,35 @@ int make_batch(const dspark_tree_batch* b, int page_size, bool rows, BatchView* 
   return DSPARK_OK;
 }
 
+int make_rotation(const dspark_tree* h, const dspark_tree_rotation* r, int N, RotateArgs* a) {
+  if (!r || N < 0) return DSPARK_EINVAL;
+  const int D = h->cfg.head_dim, R = r->rotary_dim;
+  if (D % 16 || R < 0 || R > D || R % 16 || (R > 0 && !r->turns)) return DSPARK_EINVAL;
+  if (!isfinite(r->eps) || r->eps < 0.f || !aligned16(r->q_norm) || !aligned16(r->k_norm))
+    return DSPARK_EINVAL;
+  a->turns = r->turns;
+  a->q_norm = r->q_norm;
+  a->k_norm = r->k_norm;
+  a->eps = r->eps;
+  a->inv_dim = 1.f / (float)D;
+  a->pairs = r->interleaved != 0;
+  a->N = N;
+  a->Hq = h->cfg.q_heads;
+  a->Hkv = h->cfg.kv_heads;
+  a->D = D;
+  a->R = R;
+  a->status = h->status;
+  return DSPARK_OK;
+}
+
+bool source(RotateArgs* a, int i, const void* x, const int64_t* stride) {
+  if (!x || !stride || !aligned16(x) || !stride_ok(stride[0], 2) || !stride_ok(stride[1], 2)) return false;
+  a->src[i] = static_cast<const uint8_t*>(x);
+  a->src_row[i] = stride[0] * 2;
+  a->src_head[i] = stride[1] * 2;
+  return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -356,6 +385,49 @@ int dspark_tree_attend(dspark_tree_t h, const dspark_tree_cache* cache,
   return cuda_code(attend_launch(a, maps, h->cfg.type == DSPARK_TYPE_F16,
                                  cache->type == DSPARK_TYPE_E4M3,
                                  static_cast<cudaStream_t>(stream)));
+}
+
+int dspark_tree_rotate(dspark_tree_t h, const dspark_tree_rotation* rotation, const int32_t* position,
+                       int N, const void* q, const int64_t* q_stride, const void* k,
+                       const int64_t* k_stride, void* out_q, void* out_k, void* stream) {
+  if (!h) return DSPARK_EINVAL;
+  RotateArgs a{};
+  const OnDevice on(h);
+  int rc = on.code();
+  if (rc == DSPARK_OK) rc = make_rotation(h, rotation, N, &a);
+  if (rc != DSPARK_OK) return rc;
+  if (N == 0) return DSPARK_OK;
+  if (!position || !out_q || !out_k || !aligned16(out_q) || !aligned16(out_k)) return DSPARK_EINVAL;
+  if (!source(&a, 0, q, q_stride) || !source(&a, 1, k, k_stride)) return DSPARK_EINVAL;
+  a.position = position;
+  a.out_q = static_cast<uint16_t*>(out_q);
+  a.out_k = static_cast<uint16_t*>(out_k);
+  return cuda_code(rotate_launch(a, false, h->cfg.type == DSPARK_TYPE_F16, k16, h->sm_count,
+                                 static_cast<cudaStream_t>(stream)));
+}
+
+int dspark_tree_place(dspark_tree_t h, const dspark_tree_cache* cache, const int32_t* slot,
+                      const dspark_tree_rotation* rotation, const int32_t* position, int N,
+                      const void* q, const int64_t* q_stride, const void* k, const int64_t* k_stride,
+                      const void* v, const int64_t* v_stride, void* out_q, void* stream) {
+  if (!h) return DSPARK_EINVAL;
+  RotateArgs a{};
+  const OnDevice on(h);
+  int rc = on.code();
+  if (rc == DSPARK_OK) rc = make_cache(h, cache, &a.c);
+  if (rc == DSPARK_OK) rc = make_rotation(h, rotation, N, &a);
+  if (rc != DSPARK_OK) return rc;
+  a.slots = cache->n_pages * cache->page_size;
+  if (a.slots >= ((int64_t)1 << 31)) return DSPARK_EINVAL;
+  if (N == 0) return DSPARK_OK;
+  if (!position || !slot || !out_q || !aligned16(out_q)) return DSPARK_EINVAL;
+  if (!source(&a, 0, q, q_stride) || !source(&a, 1, k, k_stride) || !source(&a, 2, v, v_stride))
+    return DSPARK_EINVAL;
+  a.position = position;
+  a.slot = slot;
+  a.out_q = static_cast<uint16_t*>(out_q);
+  return cuda_code(rotate_launch(a, true, h->cfg.type == DSPARK_TYPE_F16, held_as(cache),
+                                 h->sm_count, static_cast<cudaStream_t>(stream)));
 }
 
 int dspark_tree_status(dspark_tree_t h, void* stream) {

@@ -321,5 +321,25 @@ struct KeepArgs {
 
 cudaError_t keep_launch(const KeepArgs& a, cudaStream_t stream);
 
+// Norms and rotation (tree_rotate.cu): strides in bytes.
+struct RotateArgs {
+  CacheView c;               // place only
+  const uint8_t* src[3];     // rows of q, k and v
+  int64_t src_row[3], src_head[3];
+  uint16_t *out_q, *out_k;
+  const int32_t* position;
+  const int32_t* slot;       // place only; below 0: left out
+  int64_t slots;             // of the cache
+  const uint64_t* turns;
+  const float *q_norm, *k_norm;    // null: no norm
+  float eps, inv_dim;
+  int N, Hq, Hkv, D, R;
+  bool pairs;                // neighbours turn with each other, else halves
+  int* status;
+};
+
+cudaError_t rotate_launch(const RotateArgs& a, bool place, bool f16, Held held, int sm_count,
+                          cudaStream_t stream);
+
 }  // namespace tree
 }  // namespace dspark

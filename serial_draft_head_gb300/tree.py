@@ -14,7 +14,9 @@ handle are ordered by the caller, and a call given `stream` works on that
 stream: its inputs have to be ready there.  There is no fallback.
 """
 import ctypes
+import math
 import struct
+from fractions import Fraction
 
 import torch
 
@@ -35,7 +37,8 @@ _TYPES = {torch.bfloat16: TYPE_BF16, torch.float16: TYPE_F16, torch.float8_e4m3f
           torch.uint8: TYPE_E2M1}
 
 EXPORTS = ["dspark_tree_create", "dspark_tree_write", "dspark_tree_read", "dspark_tree_keep",
-           "dspark_tree_attend", "dspark_tree_status", "dspark_tree_destroy"]
+           "dspark_tree_attend", "dspark_tree_rotate", "dspark_tree_place", "dspark_tree_status",
+           "dspark_tree_destroy"]
 
 _i64x3 = ctypes.c_int64 * 3
 
@@ -59,6 +62,11 @@ class dspark_tree_batch(ctypes.Structure):
                 ("N", ctypes.c_int)]
 
 
+class dspark_tree_rotation(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int)]
+
+
 _pack_batch = struct.Struct("@PPPqiii").pack_into      # dspark_tree_batch
 _pack_strides = struct.Struct("@qq").pack_into
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") \
@@ -80,6 +88,8 @@ def load():
         L.dspark_tree_read.argtypes = [vp] * 6
         L.dspark_tree_keep.argtypes = [vp, vp, vp, vp, i64, i32, vp, vp]
         L.dspark_tree_attend.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, f32, f32, vp, vp, vp]
+        L.dspark_tree_rotate.argtypes = [vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp]
+        L.dspark_tree_place.argtypes = [vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp]
         L.dspark_tree_status.argtypes = [vp, vp]
         L.dspark_tree_destroy.argtypes = [vp]
         for name in EXPORTS:
@@ -148,6 +158,48 @@ class KVCache:
         return cls(*x)
 
 
+# 1 / (2 pi), to 2^-150
+_TURN = Fraction(15915494309189533576888376337251436203445964574, 10 ** 47)
+
+
+class Rotation:
+    """How query and key heads are normed and turned (see `Tree.rotate`): `freq` [R / 2], radians a
+    position of every pair (any real numbers, taken as float64), or None: no rotation; q_norm and
+    k_norm [head_dim] or None: no norm; pairs are elements i and i + R / 2, or, `interleaved`, 2 i
+    and 2 i + 1.  Copies what it is given, on the host where needed: made once, not in a graph."""
+
+    def __init__(self, head_dim, freq=None, q_norm=None, k_norm=None, eps=1e-6, interleaved=False,
+                 device=None):
+        device = torch.device("cuda", torch.cuda.current_device()) if device is None \
+            else torch.device(device)
+        _need(device.type == "cuda", "the rotation's device is a CUDA device")
+        if device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        f = [] if freq is None else torch.as_tensor(freq, dtype=torch.float64).cpu()
+        if freq is not None:
+            _need(f.dim() == 1 and bool(torch.isfinite(f).all()), "freq is [R / 2], finite")
+            f = f.tolist()
+        _need(head_dim % 16 == 0 and len(f) % 8 == 0 and 2 * len(f) <= head_dim,
+              "head_dim and R are multiples of 16, R at most head_dim")
+        _need(eps >= 0.0 and math.isfinite(eps), "eps is a number from 0 on")
+        turns = [round((Fraction(x) * _TURN % 1) * 2 ** 64) % 2 ** 64 for x in f]
+        self.turns = torch.tensor([x - 2 ** 64 if x >= 2 ** 63 else x for x in turns],
+                                  dtype=torch.int64).to(device)
+        norms = []
+        for w in (q_norm, k_norm):
+            if w is not None:
+                _need(tuple(w.shape) == (head_dim,), "a norm is [head_dim]")
+                w = w.detach().to(device=device, dtype=torch.float32, copy=True).contiguous()
+            norms.append(w)
+        self.q_norm, self.k_norm = norms
+        self.head_dim, self.key = head_dim, (device.index, head_dim)
+        self.c = dspark_tree_rotation(self.turns.data_ptr() if turns else None,
+                                      *(None if w is None else w.data_ptr() for w in norms), eps,
+                                      2 * len(f), int(bool(interleaved)))
+        self.address = ctypes.addressof(self.c)
+        torch.cuda.current_stream(device).synchronize()      # ready for calls on any stream
+
+
 def ancestor_bits(parent, first):
     """The mask words of trees: parent int32 [N], each node's parent as its place within its own
     request's rows (smaller than the node's own; -1: a root, whose parent is the context), first
@@ -199,9 +251,10 @@ class Tree:
         self._batch = dspark_tree_batch()
         self._batch_mem = (ctypes.c_char * ctypes.sizeof(self._batch)).from_buffer(self._batch)
         self._batch_at = ctypes.addressof(self._batch)
-        self._strides = (ctypes.c_char * 32)()       # two rows' {token, head}
+        self._strides = (ctypes.c_char * 48)()       # three rows' {token, head}
         self._s0 = ctypes.addressof(self._strides)
         self._s1 = self._s0 + 16
+        self._s2 = self._s0 + 32
 
     # ---- argument marshalling: a few microseconds a call matter here ----
 
@@ -314,6 +367,56 @@ class Tree:
                                        count.data_ptr(), self._stream(stream))
         if rc:
             raise WalkError(rc, "dspark_tree_keep")
+
+    def _turning(self, rotation, position, n):
+        if rotation.key != (self._index, self.head_dim):
+            raise ValueError("the rotation has the handle's device and head_dim")
+        if not (position.dtype is _int32 and position.get_device() == self._index
+                and position.shape == (n,) and (n <= 1 or position.stride(0) == 1)):
+            raise ValueError("position is int32 [N] on the handle's device, its entries next to each other")
+        return rotation.address
+
+    def rotate(self, q, k, position, rotation, out=None, stream=None):
+        """Norms and rotation (`Rotation`) of q [N, q_heads, head_dim] and k [N, kv_heads, head_dim]
+        by position int32 [N]; returns new (q, k).  fp32 inside, one rounding."""
+        n = self._rows(q, self.q_heads, 0, "q is [N, q_heads, head_dim] of the handle's type")
+        if self._rows(k, self.kv_heads, 16, "k is [N, kv_heads, head_dim] of the handle's type") != n:
+            raise ValueError("q and k have as many rows")
+        if out is None:
+            out_q, out_k = (self._empty(x.shape, self.dtype, stream) for x in (q, k))
+        else:
+            out_q, out_k = (self._out(y, x.shape, self.dtype, "out is two contiguous tensors like q and k")
+                            for x, y in zip((q, k), out))
+        rc = self.lib.dspark_tree_rotate(
+            self.h, self._turning(rotation, position, n), position.data_ptr(), n, q.data_ptr(), self._s0,
+            k.data_ptr(), self._s1, out_q.data_ptr(), out_k.data_ptr(), self._stream(stream))
+        if rc:
+            raise WalkError(rc, "dspark_tree_rotate")
+        return out_q, out_k
+
+    def place(self, cache, slot, q, k, v, position, rotation, out=None, stream=None):
+        """`rotate`, with k and v [N, kv_heads, head_dim] going to the cache at slot int32 [N] (page
+        slot // page_size, place slot % page_size; see `Pages.grow`), quantised where it is, as
+        rotate and then write leave them.  Returns the new q.  Rows with a slot below 0 are left
+        out: the cache and their rows of q stay as they were."""
+        n = self._rows(q, self.q_heads, 0, "q is [N, q_heads, head_dim] of the handle's type")
+        for x, at in ((k, 16), (v, 32)):
+            if self._rows(x, self.kv_heads, at, "k and v are [N, kv_heads, head_dim] of the handle's type") != n:
+                raise ValueError("q, k and v have as many rows")
+        if not (slot.dtype is _int32 and slot.get_device() == self._index and slot.shape == (n,)
+                and (n <= 1 or slot.stride(0) == 1)):
+            raise ValueError("slot is int32 [N] on the handle's device, its entries next to each other")
+        if out is None:
+            out = self._empty(q.shape, self.dtype, stream)
+        else:
+            self._out(out, q.shape, self.dtype, "out is like q, contiguous")
+        rc = self.lib.dspark_tree_place(
+            self.h, self._cache(cache), slot.data_ptr(), self._turning(rotation, position, n),
+            position.data_ptr(), n, q.data_ptr(), self._s0, k.data_ptr(), self._s1, v.data_ptr(), self._s2,
+            out.data_ptr(), self._stream(stream))
+        if rc:
+            raise WalkError(rc, "dspark_tree_place")
+        return out
 
     def attend(self, q, cache, pages, length, first, mask=None, scale=None, softcap=0.0, out=None,
                lse=None, stream=None):
