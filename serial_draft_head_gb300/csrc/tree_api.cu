@@ -243,6 +243,7 @@ int dspark_tree_create(const dspark_tree_config* cfg, dspark_tree_t* out) {
   if (e == cudaSuccess) e = attend_setup(cfg->type == DSPARK_TYPE_F16, cfg->head_dim);
   if (e == cudaSuccess) e = few_setup(cfg->type == DSPARK_TYPE_F16, cfg->head_dim);
   if (e == cudaSuccess) e = few4_setup(cfg->type == DSPARK_TYPE_F16, cfg->head_dim);
+  if (e == cudaSuccess) e = attend4_setup(cfg->type == DSPARK_TYPE_F16, cfg->head_dim);
   if (e != cudaSuccess) {
     dspark_tree_destroy(h);
     return cuda_code(e);
@@ -366,17 +367,20 @@ int dspark_tree_attend(dspark_tree_t h, const dspark_tree_cache* cache,
   a.part_rows = h->part_rows;
   a.arrived = h->status + 1;
   a.status = h->status;
-  if (held_as(cache) == kE2M1)
-    return cuda_code(few4_launch(a, h->cfg.type == DSPARK_TYPE_F16,
-                                 static_cast<cudaStream_t>(stream)));
-  // Few rows a cached head on average: the kernel that has tiles of 16 of them (any
+  // Few rows a cached head on average: the kernels that have tiles of 16 of them (any
   // number of rows is right in either).  16 requests of 300 to 6,000 tokens, 8 heads,
   // us here / there.  16-slot pages, 16-bit: 4 rows 56 / 67, 16 rows 57 / 67, 20 rows
   // 96 / 67 (K and V read twice); e4m3, which the other kernel has to convert through
   // shared memory: 4 rows 42 / 65, 16 rows 44 / 66, 20 rows 70 / 66.  64-slot pages,
   // which the other kernel takes by tiled copies, 16-bit: 16 rows 56 / 55, 20 rows
   // 95 / 56; e4m3: 16 rows 43 / 66.
-  if ((int64_t)a.b.N * a.G <= (int64_t)16 * a.b.B)
+  const bool few = (int64_t)a.b.N * a.G <= (int64_t)16 * a.b.B;
+  if (held_as(cache) == kE2M1) {
+    const bool f16 = h->cfg.type == DSPARK_TYPE_F16;
+    return cuda_code(few ? few4_launch(a, f16, static_cast<cudaStream_t>(stream))
+                         : attend4_launch(a, f16, static_cast<cudaStream_t>(stream)));
+  }
+  if (few)
     return cuda_code(few_launch(a, h->cfg.type == DSPARK_TYPE_F16,
                                 cache->type == DSPARK_TYPE_E4M3,
                                 static_cast<cudaStream_t>(stream)));

@@ -128,7 +128,7 @@ __device__ __noinline__ void add_nonfinite(const AttendArgs& a, const uint32_t* 
     if (!(sees_word(mask_row, rows, node, j >> 5) & bad[j >> 5] & (1u << (j & 31)))) continue;
 #pragma unroll 1
     for (int d = 0; d < a.D; ++d) {
-      const float x = bad_value<F16, E4M3>(a, b, start + j, head, d);
+      const float x = bad_value<F16, E4M3 ? kE4M3 : k16>(a, b, start + j, head, d);
       if (isfinite(x)) continue;
       if (out) {
         out[d] = (uint16_t)pack2<F16>(to_float<F16>(out[d]) + x, 0.f);

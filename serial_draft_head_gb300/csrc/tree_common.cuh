@@ -282,6 +282,10 @@ struct TileMaps {
 cudaError_t few4_setup(bool f16, int D);
 cudaError_t few4_launch(const AttendArgs& a, bool f16, cudaStream_t stream);
 
+// e2m1 cache, more rows (tree_attend4.cu).
+cudaError_t attend4_setup(bool f16, int D);
+cudaError_t attend4_launch(const AttendArgs& a, bool f16, cudaStream_t stream);
+
 // Few rows a cached head, on mma.sync (tree_attend_few.cu).
 cudaError_t few_setup(bool f16, int D);
 cudaError_t few_launch(const AttendArgs& a, bool f16, bool e4m3, cudaStream_t stream);

@@ -66,6 +66,12 @@ struct Score {
     s.cap_y = fabsf(a.scale) / c;
     return s;
   }
+  // for scores that `back`, a power of two, makes those of the rows
+  __device__ __forceinline__ void scores_times(float back) {
+    sl2 *= back;
+    cap_in *= back;
+    cap_y *= back;
+  }
 };
 
 // Up to |y| = 0.75 (y = s / c) tanh(y) / y is a polynomial in y^2, fitted to it by
@@ -480,13 +486,15 @@ static __device__ __noinline__ uint2 scale_codes_any(uint32_t w, uint32_t byte) 
 // written (columns d0 .. d1 - 1): what 0 < p times them comes to.  The result:
 // 16-bit values (out), or a part's fp32 ones (column d at part[index(d)], stride
 // and step given).
-template <bool F16, bool E4M3>
+template <bool F16, int HELD>
 __device__ __forceinline__ float bad_value(const AttendArgs& a, int b, int pos, int head, int d) {
   int64_t page;
   int slot;
   if (!locate(a.c, a.b, b, pos, &page, &slot)) return 0.f;
   const uint8_t* v = a.c.x[1].at((uint32_t)page, slot, head);
-  if (!E4M3) return to_float<F16>(reinterpret_cast<const uint16_t*>(v)[d]);
+  if (HELD == k16) return to_float<F16>(reinterpret_cast<const uint16_t*>(v)[d]);
+  if (HELD == kE2M1)                               // a number does not count here
+    return a.c.scale[1].at((uint32_t)page, slot, head)[d / 16] > kTopScale ? __uint_as_float(0x7fffffffu) : 0.f;
   return saturate16<F16>(e4m3x2_to_float2(v[d]).x *
                          scale_value(*a.c.scale[1].at((uint32_t)page, slot, head)));
 }
