@@ -53,10 +53,9 @@
  * at invisible positions do not affect a row, whatever they hold.  Sums, maxima
  * and out are fp32 until out is rounded; the weights e^(s - m) are rounded once to
  * a 16-bit type for their product with v: the handle's, or f16 where the cache is
- * e2m1, or e4m3 and the rows are few.  Over e4m3 with few rows and over e2m1, rows of
- * q in bf16 are brought to f16 by a power of two each, exact for elements down to 2^-32
- * of the row's largest and to 2^-40 of that below.  Any finite scale, and any cap from
- * 0 on.
+ * e4m3 or e2m1 and the rows are few (rows of q in bf16 are then brought to f16 by a
+ * power of two each, exact for elements down to 2^-32 of the row's largest and to 2^-40
+ * of that below).  Any finite scale, and any cap from 0 on.
  *
  * Conventions as in dspark_walk.h: 0 or a negative DSPARK_E* code, nothing
  * traps, calls on one handle are ordered by the caller, `stream` is a

@@ -26,8 +26,8 @@
 // rows; K is read K-major, V (same layout) N-major.  A 16-bit cache comes by
 // tiled copies where pages allow (make_maps), else by 16-byte copies of any
 // strides and page size; e4m3 through registers, the scale multiplied in (exact
-// in bf16), so everything after the ring is the same; e2m1 too, to f16, where every
-// value is exact, and with rows of Q in bf16 brought to f16 by a power of two each.
+// in bf16), so everything after the ring is the same; e2m1 too, whose values are exact in
+// both types.
 //
 // Keys past the end are zero rows and masked; draft rows of V that are not
 // finite would reach every row of the product (0 * NaN), so such elements are
@@ -102,7 +102,6 @@ struct Tail {
   uint64_t full[8], empty[8], q_full, q_empty;
   uint64_t s_full[2][2], p_full[2][2], o_done[2][2];      // [stream][half of the tile]
   float2 ml[2][kKeys];
-  uint8_t q_back[kGroupRows];           // 2^(byte - 127) brings a row's scores back (e2m1, bf16)
   uint32_t bad[kBadSets][DSPARK_TREE_MAX_NODES / 32];
   Share share;
   int64_t warp_sum[20];
@@ -445,8 +444,11 @@ __device__ __forceinline__ void produce8(const AttendArgs& a, uint8_t* smem, Tai
 }
 
 // e2m1 cache, through registers, as e4m3: a lane has the 16 codes of a block, 8 bytes,
-// and their scale.  The product with it is exact and needs no other way.
-template <int DP>
+// of several rows, and multiplies them by their scale, exactly.  A warp has 16 rows of the
+// tile; two lanes look a row's page up, ask for half of its scales each, and hand both
+// round.  K and V have registers of their own, so that what is asked for is used a whole
+// tile later.
+template <bool F16, int DP>
 __device__ __forceinline__ void produce4(const AttendArgs& a, uint8_t* smem, Tail* sh) {
   using L = Layout<DP>;
   constexpr int kWarps = Roles<true>::kProdWarps;
@@ -456,15 +458,20 @@ __device__ __forceinline__ void produce4(const AttendArgs& a, uint8_t* smem, Tai
   constexpr int kPasses = kKeys / kRows;
   constexpr int kAhead = 4;
   static_assert(kWarps * 32 == 2 * kKeys, "one row of K or V a thread");
+  static_assert(kPasses * kWarpRows == 16, "16 rows a warp");
   const int tid = threadIdx.x - kSoftWarps * 32, lane = tid % 32, warp = tid / 32;
   // as in produce8: eight lanes store to all banks once
   const int chunk = (lane & 3) | (DP == 128 ? (lane >> 1) & 4 : 0);
-  const int r0 = warp * kWarpRows +
-                 (DP == 128 ? ((lane >> 2) & 1) | ((lane >> 3) & 2) : lane >> 2);
+  const int w0 = DP == 128 ? ((lane >> 2) & 1) | ((lane >> 3) & 2) : lane >> 2;
+  const int r0 = warp * kWarpRows + w0;
   const bool in_dim = chunk * 16 < a.D;
   const uint32_t to0 = tile_offset(r0, 2 * chunk), to1 = tile_offset(r0, 2 * chunk + 1);
+  // row lane / 2 of the warp's, and which half of its scales
+  const int own = lane / 2, half = lane & 1;
+  const int own_row = own / kWarpRows * kRows + warp * kWarpRows + own % kWarpRows;
+  const bool own_in = half * 64 < a.D;
   uint8_t* ring = smem + L::kRing;
-  Cursor c;                                      // the tile after the one in `page`
+  Cursor c;                                      // the tile whose loads come next
   c.init(a, sh->share);
   if (!c.more()) return;
   struct Tile {
@@ -473,108 +480,116 @@ __device__ __forceinline__ void produce4(const AttendArgs& a, uint8_t* smem, Tai
   auto tile_at = [&]() {
     return Tile{c.head, min(kKeys, c.total() - c.t * kKeys), c.start - c.t * kKeys, c.seg};
   };
-  uint32_t page[kPasses], worst = 0;
-  int slot[kPasses];
-  auto fetch_pages = [&]() {
-    const int32_t* table = a.b.pages + (int64_t)c.b * a.b.pages_stride;
-    const int last = c.total() - 1;
+  const uint32_t top_page = (uint32_t)(a.c.n_pages - 1);
+  uint32_t page = 0, worst = 0;
+  int slot = 0;
+  auto fetch_page = [&]() {
+    const int pos = min(c.t * kKeys + own_row, c.total() - 1), at = a.c.page.div(pos);
+    page = (uint32_t)__ldg(a.b.pages + (int64_t)c.b * a.b.pages_stride + at);
+    slot = pos - at * a.c.page.d;
+  };
+  // rows of the same request kAhead tiles on, across a head's end, are asked for in L2, a
+  // tile after their pages have been looked up
+  uint32_t ask_page = ~0u;
+  int ask_slot = 0, ask_head = 0;
+  auto ask = [&]() {
+    if (ask_page <= top_page) {
+      ptx::prefetch_l2(a.c.x[tid >= kKeys].at(ask_page, ask_slot, ask_head));
+      ptx::prefetch_l2(a.c.scale[tid >= kKeys].at(ask_page, ask_slot, ask_head));
+    }
+    ask_page = ~0u;
+    int t = c.t + kAhead;
+    ask_head = c.head;
+    if (t >= c.tiles) {
+      t -= c.tiles;
+      ++ask_head;
+    }
+    if (ask_head >= a.Hkv || t >= c.tiles) return;
+    const int pos = min(t * kKeys + tid % kKeys, c.total() - 1), at = a.c.page.div(pos);
+    ask_page = (uint32_t)__ldg(a.b.pages + (int64_t)c.b * a.b.pages_stride + at);
+    ask_slot = pos - at * a.c.page.d;
+  };
+  struct Part {
+    uint2 x[kPasses];
+    uint32_t scales;                             // four bytes of row `own`
+  };
+  auto load = [&](Part& part, int v, int head) {
+    const Rows rows = a.c.x[v];
+    const uint8_t* src = rows.of_head(head) + (in_dim ? chunk * 8 : 0);
+    const uint8_t* sc = a.c.scale[v].at(page, slot, head) + (own_in ? half * 4 : 0);
+    if (a.D % 64 == 0) {
+      part.scales = __ldg(reinterpret_cast<const uint32_t*>(sc));
+    } else {                                     // heads of 32 and 96: two bytes at their end
+      part.scales = __ldg(reinterpret_cast<const uint16_t*>(sc));
+      if (half * 64 + 32 < a.D)
+        part.scales |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(sc) + 1) << 16;
+    }
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-      const int pos = min(c.t * kKeys + r0 + i * kRows, last), at = a.c.page.div(pos);
-      page[i] = (uint32_t)__ldg(table + at);
-      slot[i] = pos - at * a.c.page.d;
+      const int from = 2 * (i * kWarpRows + w0);
+      const uint32_t p = __shfl_sync(0xffffffffu, page, from);
+      const int s = __shfl_sync(0xffffffffu, slot, from);
+      part.x[i] = __ldg(reinterpret_cast<const uint2*>(src + rows.offset(p, s)));
     }
   };
   RingPos<L::kSlots> at;
-  // rows of the same request kAhead tiles on, across a head's end
-  auto ask = [&]() {
-    int t = c.t + kAhead, head = c.head;
-    if (t >= c.tiles) {
-      t -= c.tiles;
-      ++head;
-    }
-    if (head >= a.Hkv || t >= c.tiles) return;
-    const int pos = min(t * kKeys + tid % kKeys, c.total() - 1), at = a.c.page.div(pos);
-    const uint32_t p = (uint32_t)__ldg(a.b.pages + (int64_t)c.b * a.b.pages_stride + at);
-    if (p >= (uint64_t)a.c.n_pages) return;
-    ptx::prefetch_l2(a.c.x[tid >= kKeys].at(p, pos - at * a.c.page.d, head));
-    ptx::prefetch_l2(a.c.scale[tid >= kKeys].at(p, pos - at * a.c.page.d, head));
-  };
-  uint2 x[kPasses], x_next[kPasses];
-  uint32_t byte[kPasses], byte_next[kPasses];
-  const uint32_t top_page = (uint32_t)(a.c.n_pages - 1);
-  auto load = [&](bool v, int head) {
-    const Rows rows = a.c.x[v], scales = a.c.scale[v];
-    const uint8_t* src = rows.of_head(head) + (in_dim ? chunk * 8 : 0);
-    const uint8_t* sc = scales.of_head(head) + (in_dim ? chunk : 0);
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      if (!v) {                                  // a bad page is reported at the end
-        worst = max(worst, page[i]);
-        page[i] = min(page[i], top_page);
-      }
-      x_next[i] = __ldg(reinterpret_cast<const uint2*>(src + rows.offset(page[i], slot[i])));
-      byte_next[i] = __ldg(sc + scales.offset(page[i], slot[i]));
-    }
-  };
-  fetch_pages();
-  Tile cur = tile_at();
-  load(false, cur.head);
-  bool more = true;                              // another half tile after the one in x_next
-#pragma unroll 1
-  for (bool v = false; more; v = !v, at.next()) {
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      x[i] = x_next[i];
-      byte[i] = byte_next[i];
-    }
-    const Tile tile = cur;
-    if (!v) {
-      load(true, cur.head);                      // V of the same tile, then the next tile's pages
-      c.next(a);
-      if (c.more()) {
-        fetch_pages();
-        ask();
-      }
-    } else {
-      more = c.more();
-      if (more) {
-        cur = tile_at();
-        load(false, cur.head);
+  auto convert = [&](const Part& part, bool v, const Tile& tile) {
+    uint32_t scales = part.scales;
+    if (own_row >= tile.rows) scales = 0;        // rows past the end are zeros
+    if (v && tile.draft < kKeys) {               // draft rows: zeros for blocks that are no numbers
+      const uint32_t over = __vcmpgtu4(scales, kTopScale * 0x01010101u);
+      const int j = own_row - tile.draft;
+      if (j >= 0 && over != 0) {
+        scales &= ~over;
+        atomicOr(&sh->bad[tile.seg % kBadSets][j >> 5], 1u << (j & 31));
       }
     }
     wait(sh, &sh->empty[at.slot], at.phase ^ 1, a.status);
     uint8_t* dst = ring + at.slot * L::kTile;
-    if (tile.rows < kKeys || a.D < DP) {         // rows and elements past the end are zeros
-#pragma unroll
-      for (int i = 0; i < kPasses; ++i)
-        if (!in_dim || r0 + i * kRows >= tile.rows) {
-          x[i] = make_uint2(0, 0);
-          byte[i] = 0;
-        }
-    }
-    if (v && tile.draft < kKeys) {               // draft rows: zeros for blocks that are no numbers
-#pragma unroll
-      for (int i = 0; i < kPasses; ++i) {
-        const int j = r0 + i * kRows - tile.draft;
-        if (j >= 0 && byte[i] > kTopScale) {
-          byte[i] = 0;
-          atomicOr(&sh->bad[tile.seg % kBadSets][j >> 5], 1u << (j & 31));
-        }
-      }
-    }
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-      const uint32_t s = byte[i] * 0x00800080u;  // the scale twice
-      const uint4 y = e2m1x8_to_f16(x[i].x), z = e2m1x8_to_f16(x[i].y);
-      *reinterpret_cast<uint4*>(dst + to0 + i * kRows * 128) =
-          make_uint4(mul_f16x2(y.x, s), mul_f16x2(y.y, s), mul_f16x2(y.z, s), mul_f16x2(y.w, s));
-      *reinterpret_cast<uint4*>(dst + to1 + i * kRows * 128) =
-          make_uint4(mul_f16x2(z.x, s), mul_f16x2(z.y, s), mul_f16x2(z.z, s), mul_f16x2(z.w, s));
+      const uint32_t four = __shfl_sync(0xffffffffu, scales, 2 * (i * kWarpRows + w0) + chunk / 4);
+      const uint32_t s = e2m1_mul2<F16>(in_dim ? four >> (chunk % 4 * 8) & 0xffu : 0u);
+      *reinterpret_cast<uint4*>(dst + to0 + i * kRows * 128) = e2m1x8_times<F16>(part.x[i].x, s);
+      *reinterpret_cast<uint4*>(dst + to1 + i * kRows * 128) = e2m1x8_times<F16>(part.x[i].y, s);
     }
     ptx::fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(&sh->full[at.slot]);
+    at.next();
+  };
+  Part k, v;
+  auto clamp_page = [&]() {                      // a bad page is reported at the end
+    worst = max(worst, page);
+    page = min(page, top_page);
+  };
+  fetch_page();
+  clamp_page();
+  Tile cur = tile_at();
+  load(k, 0, cur.head);
+  load(v, 1, cur.head);
+  c.next(a);
+  bool more = c.more();
+  if (more) fetch_page();
+#pragma unroll 1
+  while (true) {
+    Tile next = cur;
+    if (more) {
+      next = tile_at();
+      ask();
+    }
+    convert(k, false, cur);
+    if (more) {
+      clamp_page();
+      load(k, 0, next.head);
+    }
+    convert(v, true, cur);
+    if (!more) break;
+    load(v, 1, next.head);
+    cur = next;
+    c.next(a);
+    more = c.more();
+    if (more) fetch_page();
   }
   if (worst > top_page) set_status(a.status, DSPARK_EPAGES);
 }
@@ -771,15 +786,24 @@ __device__ __forceinline__ void scale_row(uint32_t tm_o, float back) {
   }
 }
 
+// How far a row's maximum may grow past the one that set m before m moves.  Over e2m1
+// codes in bf16 as far as O and l in fp32 bear (2^64 times 2^16 times 2^31 keys): a weight
+// has bf16's relative precision whatever its size, and what moves m costs (64 x 64 with
+// a key in 50 eight times the others: 8 607 us, 64 495).  In f16 no further than f16 goes.
+template <bool F16, int HELD>
+constexpr float grow_limit() {
+  return HELD == kE2M1 && !F16 ? 64.f : 8.f;
+}
+
 // The row's m after keys whose largest exponent is x_max; l and O follow if it
 // moves: the first visible key sets it, later ones when it has grown enough.  O
 // is free to scale once the last product is done (o_done, null before the first).
-template <bool F16, int DP>
+template <bool F16, int HELD, int DP>
 __device__ __forceinline__ float move_reference(float x_max, Tail* sh, uint64_t* o_done,
                                                 uint32_t parity, int* status, uint32_t tm_o,
                                                 float mref, float* l) {
   constexpr float kShift = F16 ? 7.f : 0.f;
-  const bool move = x_max > mref + (mref == -INFINITY ? 0.f : kShift + 8.f);
+  const bool move = x_max > mref + (mref == -INFINITY ? 0.f : kShift + grow_limit<F16, HELD>());
   const float m_new = move ? x_max - kShift : mref;
   if (o_done && __any_sync(0xffffffffu, move)) {
     wait(sh, o_done, parity, status);
@@ -794,10 +818,13 @@ __device__ __forceinline__ float move_reference(float x_max, Tail* sh, uint64_t*
 // KEYS keys (a tile or half) of one row that are all visible, scores not capped, m
 // set: P over S, and l.  The weights go by m as it stands while the maximum is
 // taken beside them, so nothing waits for it; if it has outgrown m in any row of
-// the warp, S is still there and they are done again by softmax_any (false).  WIDE loads the next 32 scores while these are worked on.
-template <bool F16, bool WIDE, int KEYS>
-__device__ __forceinline__ bool softmax_plain(float sl2, uint32_t tm_s, float mref, float* l) {
+// the warp, S is still there and they are done again (false; x_max is the row's largest
+// exponent).  A 16-bit cache: the next 32 scores are loaded while these are worked on.
+template <bool F16, int HELD, int KEYS>
+__device__ __forceinline__ bool softmax_plain(float sl2, uint32_t tm_s, float mref, float* l,
+                                              float* x_max) {
   constexpr float kShift = F16 ? 7.f : 0.f;
+  constexpr bool WIDE = HELD == k16;
   constexpr int kBuf = WIDE ? 2 : 1, kChunks = KEYS / 32;
   uint32_t v[kBuf][32], pk[kChunks][16];
   float mx[2] = {-INFINITY, -INFINITY}, sum[4] = {0.f, 0.f, 0.f, 0.f};
@@ -822,7 +849,8 @@ __device__ __forceinline__ bool softmax_plain(float sl2, uint32_t tm_s, float mr
     }
     if (!WIDE && c < kChunks - 1) ptx::tmem_ld32(tm_s + 32 * (c + 1), v[0]);
   }
-  if (__any_sync(0xffffffffu, fmaxf(mx[0], mx[1]) * sl2 > mref + (kShift + 8.f))) return false;
+  *x_max = fmaxf(mx[0], mx[1]) * sl2;
+  if (__any_sync(0xffffffffu, *x_max > mref + (kShift + grow_limit<F16, HELD>()))) return false;
 #pragma unroll
   for (int c = 0; c < kChunks; ++c) ptx::tmem_st16(tm_s + 16 * c, pk[c]);
   *l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
@@ -832,7 +860,7 @@ __device__ __forceinline__ bool softmax_plain(float sl2, uint32_t tm_s, float mr
 
 // 64 or 128 keys of one row, also with invisible keys (see: a bit a key), capped
 // scores, or a maximum that moves m; 32 keys at a time.  Returns {m, l}.
-template <bool F16, int DP>
+template <bool F16, int HELD, int DP>
 __device__ __noinline__ float2 softmax_any(Score sc, Tail* sh, uint64_t* o_done, uint32_t parity,
                                            int* status, uint32_t tm_s, uint32_t tm_o, int keys,
                                            uint4 see, float mref, float l) {
@@ -854,7 +882,7 @@ __device__ __noinline__ float2 softmax_any(Score sc, Tail* sh, uint64_t* o_done,
   float x_max = raw_max == -INFINITY ? -INFINITY : raw_max * sc.sl2;
   // a visible score of -infinity is the cap's negative, an invisible one nothing
   if (cap && any != 0) x_max = capped(sc, raw_max, 0.f);
-  mref = move_reference<F16, DP>(x_max, sh, o_done, parity, status, tm_o, mref, &l);
+  mref = move_reference<F16, HELD, DP>(x_max, sh, o_done, parity, status, tm_o, mref, &l);
   const float sub = mref == -INFINITY ? 0.f : mref;
   // coefficients of capped_near.  No special functions but the weight's own where all
   // of 8 keys are far from the cap in all rows of the warp; 16 requests of 64 nodes, 300
@@ -935,15 +963,13 @@ __device__ __noinline__ float2 softmax_any(Score sc, Tail* sh, uint64_t* o_done,
 template <bool F16, int HELD, int DP>
 __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail* sh) {
   using L = Layout<DP>;
-  constexpr bool kHalfMath = F16 || HELD == kE2M1;       // the products' type is f16
-  constexpr bool kToHalf = !F16 && HELD == kE2M1;        // Q is brought to it
   constexpr bool kSwapped = !F16 && HELD == kE4M3;       // the codes' order (scale_codes)
   const int wg = threadIdx.x / 128, lane_row = threadIdx.x % 128;
   const int warp = threadIdx.x / 32 % 4;
   const uint32_t lanes = (uint32_t)(warp * 32) << 16;
   const uint32_t tm_s = sh->tmem + lanes + wg * 128;
   const uint32_t tm_o = sh->tmem + lanes + 256;
-  const Score all = Score::of(a);
+  const Score sc = Score::of(a);
   const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
   Walker w;
   Segment s;
@@ -972,7 +998,7 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
       }
       ptx::cp_async_commit();
       ptx::cp_async_wait_group<0>();
-      if (kSwapped || kToHalf || flip) {         // each thread the chunks that it copied
+      if (kSwapped || flip) {                    // each thread the chunks that it copied
 #pragma unroll 1
         for (int r = threadIdx.x / kChunks; r < q_rows; r += kStep) {
           uint4 x = *place(r);
@@ -984,22 +1010,6 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
             const uint2 lo = swap_middle(make_uint2(x.x, x.y)), hi = swap_middle(make_uint2(x.z, x.w));
             x = make_uint4(lo.x, lo.y, hi.x, hi.y);
           }
-          if (kToHalf) {
-            // the row's largest magnitude to [2^14, 2^15) by a power of two, exact
-            uint32_t y[4] = {x.x, x.y, x.z, x.w}, big = 0;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) big = max(big, max((y[k] & 0x7fffu) << 16, y[k] & 0x7fff0000u));
-#pragma unroll
-            for (int o = kChunks / 2; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
-            const int e = (int)(big >> 23), up = big == 0 || e == 255 ? 0 : min(127 + 14 - e, 126);
-            const float mul = __uint_as_float((uint32_t)(127 + up) << 23);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              y[k] = pack2<true>(to_float<false>((uint16_t)y[k]) * mul,
-                                 to_float<false>((uint16_t)(y[k] >> 16)) * mul);
-            x = make_uint4(y[0], y[1], y[2], y[3]);
-            if (chunk == 0) sh->q_back[r] = (uint8_t)(127 - up);
-          }
           *place(r) = x;
         }
       }
@@ -1008,11 +1018,6 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
       if (threadIdx.x % 32 == 0) ptx::mbar_arrive(&sh->q_full);
     }
     const int local = (pair ? wg * kKeys : 0) + lane_row;        // row of the group
-    Score sc = all;
-    if (kToHalf) {
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      sc.scores_times(__uint_as_float((uint32_t)sh->q_back[local] << 23));
-    }
     const bool valid = local < rows;
     const bool warp_valid = local - threadIdx.x % 32 < rows;
     const int grow = s.group * kGroupRows + (valid ? local : 0);
@@ -1031,16 +1036,26 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
           const int pos0 = (s.t0 + i) * kKeys + h * kHalf;
           const bool masked = pos0 + keys > s.start;
           bool done = !masked && sc.cap2 == 0.f && !__any_sync(0xffffffffu, mref == -INFINITY);
-          if (done)
-            done = pair ? softmax_plain<kHalfMath, HELD == k16, kHalf>(sc.sl2, tm_s + h * kHalf, mref, &l)
-                        : softmax_plain<kHalfMath, HELD == k16, kKeys>(sc.sl2, tm_s, mref, &l);
+          // the product before this one
+          const int before = pair ? h ^ 1 : 0;
+          const uint32_t phase = (before ? count1 : count0) - 1;
+          uint64_t* o_done = h == 1 || i >= step ? &sh->o_done[wg][before] : nullptr;
+          if (done) {
+            float x_max;
+            auto plain = [&]() {
+              return pair ? softmax_plain<F16, HELD, kHalf>(sc.sl2, tm_s + h * kHalf, mref, &l, &x_max)
+                          : softmax_plain<F16, HELD, kKeys>(sc.sl2, tm_s, mref, &l, &x_max);
+            };
+            done = plain();
+            if (HELD == kE2M1 && !done) {        // as long as m follows, the second time it fits
+              mref = move_reference<F16, HELD, DP>(x_max, sh, o_done, phase & 1, a.status, tm_o + wg * 128,
+                                                   mref, &l);
+              done = plain();
+            }
+          }
           if (!done) {
-            // the product before this one
-            const int before = pair ? h ^ 1 : 0;
-            const uint32_t phase = (before ? count1 : count0) - 1;
-            const float2 r = softmax_any<kHalfMath, DP>(
-                sc, sh, h == 1 || i >= step ? &sh->o_done[wg][before] : nullptr, phase & 1, a.status,
-                tm_s + h * kHalf, tm_o + wg * 128, keys,
+            const float2 r = softmax_any<F16, HELD, DP>(
+                sc, sh, o_done, phase & 1, a.status, tm_s + h * kHalf, tm_o + wg * 128, keys,
                 masked ? sees_128(mask_row, s.rows, node, pos0 - s.start)
                        : make_uint4(~0u, ~0u, ~0u, ~0u),
                 mref, l);
@@ -1209,13 +1224,13 @@ __global__ void __launch_bounds__(Roles<HELD != k16>::kThreads, 1)
     softmax<F16, HELD, DP>(a, smem, sh);
   } else if (warp < R::kMmaWarp) {
     ptx::set_registers<REGS, R::kProdRegs>();
-    if (HELD == kE2M1) produce4<DP>(a, smem, sh);
+    if (HELD == kE2M1) produce4<F16, DP>(a, smem, sh);
     else if (HELD == kE4M3) produce8<F16, DP>(a, smem, sh);
     else produce16<F16, DP>(a, maps, smem, sh);
   } else {
     ptx::set_registers<REGS, R::kMmaRegs>();
     if (warp < R::kMmaWarp + 2)
-      issue<F16 || HELD == kE2M1, DP>(a, smem, sh, warp - R::kMmaWarp);
+      issue<F16, DP>(a, smem, sh, warp - R::kMmaWarp);
     else if (warp == R::kMmaWarp + 2) place_parts(a, sh);
   }
   __syncwarp();

@@ -223,6 +223,34 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// Eight e2m1 codes times their scale in the 16-bit type, exactly; `mul2` is e2m1_mul2 of
+// the scale's byte.  bf16: a code as f16, its exponent and mantissa moved down to bf16's
+// place, stands for itself times 2^-112, which the multiplier has back.
+template <bool F16>
+__device__ __forceinline__ uint32_t e2m1_mul2(uint32_t byte) {
+  if (F16) return byte * 0x00800080u;
+  const float s = __half2float(__ushort_as_half((uint16_t)(byte << 7))) * 0x1p112f;
+  return __byte_perm(__float_as_uint(s), 0, 0x3232);
+}
+
+template <bool F16>
+__device__ __forceinline__ uint4 e2m1x8_times(uint32_t w, uint32_t mul2) {
+  const uint4 c = e2m1x8_to_f16(w);
+  uint32_t x[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (F16) {
+      x[k] = mul_f16x2(x[k], mul2);
+    } else {
+      const uint32_t y = (x[k] >> 3 & 0x0fff0fffu) | (x[k] & 0x80008000u);
+      const __nv_bfloat162 z = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y),
+                                       *reinterpret_cast<const __nv_bfloat162*>(&mul2));
+      x[k] = *reinterpret_cast<const uint32_t*>(&z);
+    }
+  }
+  return make_uint4(x[0], x[1], x[2], x[3]);
+}
+
 // The last scale byte of a block of e2m1 codes that is written, 10240.
 constexpr uint32_t kTopScale = 226;
 

@@ -66,12 +66,6 @@ struct Score {
     s.cap_y = fabsf(a.scale) / c;
     return s;
   }
-  // for scores that `back`, a power of two, makes those of the rows
-  __device__ __forceinline__ void scores_times(float back) {
-    sl2 *= back;
-    cap_in *= back;
-    cap_y *= back;
-  }
 };
 
 // Up to |y| = 0.75 (y = s / c) tanh(y) / y is a polynomial in y^2, fitted to it by

@@ -52,15 +52,17 @@ def values(codes, byte):
     return unpack(codes) * scale_of(byte).repeat_interleave(16, -1)
 
 
-def bounds(out, weight, sums, D, dtype, softcap, keys, q_max, k_max, v_max):
+def bounds(out, weight, sums, D, dtype, softcap, keys, q_max, k_max, v_max, many):
     """What out and lse may be off by, from the formats alone.
 
     A score: D products added in 32 bits, each addition within 2^-23 (it may truncate); bf16 rows of q
     are exact in f16 but for elements below 2^-32 of the row's largest, which are off by 2^-40 of that;
     the cap adds 2^-21 of it.  A weight e^(s - m): the score's error twice (s and m), 2^-21 of the
     exponential and 2^-22 of its argument; then one rounding to f16, half a unit, or half of f16's
-    smallest number, 2^-25, beside a largest weight of 2^7 at least.  The result: one rounding."""
-    half, f16 = torch.finfo(dtype).eps / 2, 2.0 ** -11
+    smallest number, 2^-25, beside a largest weight of 2^7 at least; or, for many rows, to the handle's
+    type (`many`).  The result: one rounding."""
+    half = torch.finfo(dtype).eps / 2
+    f16 = half if many else 2.0 ** -11
     score = (D + 4) * 2.0 ** -23 * sums + (softcap or 0.0) * 2.0 ** -21 + D * 2.0 ** -40 * q_max * k_max
     top = torch.clamp(sums, max=softcap) if softcap else sums
     p = 2 * score + 2.0 ** -21 + 2.0 ** -22 * top
