@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <math.h>
 
+#include <algorithm>
 #include <new>
 
 #include "../../include/dspark_tree.h"
@@ -15,7 +16,7 @@ struct dspark_tree {
   int device = 0;
   int sm_count = 0;
   dspark_tree_config cfg{};
-  int* status = nullptr;          // and after it a count a SM (AttendArgs::arrived)
+  int* status = nullptr;          // and after it a count a worker (AttendArgs::arrived)
   void* parts = nullptr;          // attend's workspace
   float* part_o = nullptr;
   float2* part_ml = nullptr;
@@ -30,6 +31,8 @@ int cuda_code(cudaError_t e) {
   if (e == cudaSuccess) return DSPARK_OK;
   return e == cudaErrorMemoryAllocation ? DSPARK_ENOMEM : DSPARK_ECUDA;
 }
+
+size_t status_bytes(const dspark_tree* h) { return (1 + kFew4Workers * h->sm_count) * sizeof(int); }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -220,7 +223,8 @@ int dspark_tree_create(const dspark_tree_config* cfg, dspark_tree_t* out) {
   const int G = cfg->q_heads / cfg->kv_heads;
   const int64_t rows = (int64_t)cfg->max_nodes * G;
   h->part_rows = rows >= kGroupRows ? kGroupRows : (int)((rows + 31) / 32 * 32);
-  const size_t n_parts = (size_t)2 * sms, n_rows = n_parts * h->part_rows;
+  const size_t n_parts = (size_t)2 * sms;
+  const size_t n_rows = std::max(n_parts * h->part_rows, (size_t)kFew4PartRows * sms);
   const size_t o_bytes = n_rows * padded_dim(cfg->head_dim) * sizeof(float);
   const size_t ml_bytes = n_rows * sizeof(float2);
   e = cudaMalloc(&h->parts, o_bytes + ml_bytes + n_parts * sizeof(int4));
@@ -229,9 +233,9 @@ int dspark_tree_create(const dspark_tree_config* cfg, dspark_tree_t* out) {
     h->part_o = reinterpret_cast<float*>(p);
     h->part_ml = reinterpret_cast<float2*>(p + o_bytes);
     h->part_of = reinterpret_cast<int4*>(p + o_bytes + ml_bytes);
-    e = cudaMalloc(&h->status, (1 + sms) * sizeof(int));
+    e = cudaMalloc(&h->status, status_bytes(h));
   }
-  if (e == cudaSuccess) e = clear(h->status, (1 + sms) * sizeof(int));
+  if (e == cudaSuccess) e = clear(h->status, status_bytes(h));
   if (e == cudaSuccess) {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
@@ -242,7 +246,7 @@ int dspark_tree_create(const dspark_tree_config* cfg, dspark_tree_t* out) {
   }
   if (e == cudaSuccess) e = attend_setup(cfg->type == DSPARK_TYPE_F16, cfg->head_dim);
   if (e == cudaSuccess) e = few_setup(cfg->type == DSPARK_TYPE_F16, cfg->head_dim);
-  if (e == cudaSuccess) e = few4_setup(cfg->type == DSPARK_TYPE_F16, cfg->head_dim);
+  if (e == cudaSuccess) e = few4_setup(cfg->head_dim);
   if (e == cudaSuccess) e = attend4_setup(cfg->type == DSPARK_TYPE_F16, cfg->head_dim);
   if (e != cudaSuccess) {
     dspark_tree_destroy(h);
@@ -376,9 +380,9 @@ int dspark_tree_attend(dspark_tree_t h, const dspark_tree_cache* cache,
   // 95 / 56; e4m3: 16 rows 43 / 66.
   const bool few = (int64_t)a.b.N * a.G <= (int64_t)16 * a.b.B;
   if (held_as(cache) == kE2M1) {
-    const bool f16 = h->cfg.type == DSPARK_TYPE_F16;
-    return cuda_code(few ? few4_launch(a, f16, static_cast<cudaStream_t>(stream))
-                         : attend4_launch(a, f16, static_cast<cudaStream_t>(stream)));
+    a.f16 = h->cfg.type == DSPARK_TYPE_F16;
+    return cuda_code(few ? few4_launch(a, static_cast<cudaStream_t>(stream))
+                         : attend4_launch(a, a.f16, static_cast<cudaStream_t>(stream)));
   }
   if (few)
     return cuda_code(few_launch(a, h->cfg.type == DSPARK_TYPE_F16,
@@ -441,7 +445,7 @@ int dspark_tree_status(dspark_tree_t h, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int st = 0;
   cudaError_t e = cudaMemcpyAsync(&st, h->status, sizeof(int), cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaMemsetAsync(h->status, 0, (1 + h->sm_count) * sizeof(int), s);
+  if (e == cudaSuccess) e = cudaMemsetAsync(h->status, 0, status_bytes(h), s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   return e == cudaSuccess ? st : cuda_code(e);
 }

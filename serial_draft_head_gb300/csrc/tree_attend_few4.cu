@@ -1,748 +1,70 @@
-// tree_attend_few4.cu -- attention of few drafted rows (single tokens, short chains:
-// dspark_tree_attend has the rule) over a paged cache in 4 bits.
-//
-// Items are 8 or 16 rows by blocks of 32 keys, a worker is a CTA (tree_items.cuh says
-// how the work is cut, and the mathematics).  The warps of a CTA take a segment's
-// blocks in turn, each with its own O, m and l, and meet at its end.
-//
-// A cached row of 128 elements is 72 bytes, so what bounds the kernel is less the memory
-// than what is done to every element on the way to the products (f16 mma.sync
-// m16n8k16): one conversion for two codes, one multiplication by their scales, exact.
-// The products stand the other way round than those of tree_attend_few.cu: keys (for S)
-// and columns of V (for O) are the 16 rows of A, the drafted rows the 8 columns of B, so
-// that eight rows (a single token of a group of eight heads) fill a tile and O takes half
-// the registers.
-//
-//  - S^T = K Q^T: lane (g, q) = (lane / 4, lane % 4) holds keys g and g + 8 of A.  The
-//    order of the elements along the head is free as long as Q has the same: lane q takes
-//    the q-th quarter of a row, two blocks under a scale each, as it lies.
-//  - P^T's B operand is S^T's accumulator, packed and transposed by movmatrix.
-//  - O^T = V^T P^T: A of lane (g, q) is column g and g + 8 of keys 2q, 2q + 1, 2q + 8,
-//    2q + 9; the columns' order is free too, so lane g takes the g-th eighth of the rows,
-//    one block, puts two keys' codes into bytes by four logic operations for 16, and
-//    multiplies by the two keys' scales, which are a pair as ldmatrix hands them out
-//    transposed.
-//
-// Rows of Q are brought to f16 by a power of two a row.
-#include "tree_items.cuh"
+// tree_attend_few4.cu -- tree_attend_few4.cuh for heads of up to 64 elements, and the choice among
+// its forms.
+#include "tree_attend_few4.cuh"
 
 namespace dspark {
 namespace tree {
+
+cudaError_t few4_setup128();
+cudaError_t few4_launch128(const AttendArgs& a, bool two, bool alone, bool bulk, cudaStream_t stream);
+
 namespace {
 
-// DP: head dimension as laid out, 64 or 128; NT: tiles of eight rows.
-template <int DP, int NT>
-struct Few4 {
-  static constexpr int kRows = 8 * NT;
-  static constexpr int kBlock = 32;
-  static constexpr int kGroups = kBlock / 8;             // of eight keys
-  // units an item counts beside its blocks, for Q, the first copies and the warps'
-  // meeting
-  static constexpr int kExtra = 20;
-  static constexpr int kWarps = NT == 1 ? 16 : 12;
-  static constexpr int kThreads = kWarps * 32;
-  static constexpr int kBytes = DP / 2;                  // of a row of codes
-  static constexpr int kChunks = kBytes / 16;            // 16-byte copies of a row
-  static constexpr int kRowsAtOnce = 32 / kChunks;       // rows of one copy instruction
-  static constexpr int kCopies = kBlock / kRowsAtOnce;
-  static constexpr int kWords = kBytes / 16;             // 32-bit words a lane, of a row of K
-  static constexpr int kVPart = kBlock * kBytes;         // V's place in a stage
-  static constexpr int kStage = 2 * kVPart;
-  static constexpr int kStages = 2;
-  static constexpr int kTiles = DP / 16;                 // of O^T
-  static constexpr int kScale = kStages * kStage;        // a block's scales as f16: [K, V][key][8]
-  static constexpr int kRing = kScale + 2 * kBlock * 16; // of a warp
-  static constexpr int kQ = kWarps * kRing;              // [NT][DP / 32][lane] 16 bytes
-  static constexpr int kMerge = kQ + kRows * DP * 2;     // [warp][row][kHalf + 4] floats
-  static constexpr int kHalf = DP / 2;                   // columns merged at a time
-  static constexpr int kMergeRow = kHalf + 4;
-  static constexpr int kSmem = kMerge + kWarps * kRows * kMergeRow * 4;
-  using Item = Work<kBlock, kRows, kExtra>;
-};
-
-constexpr int kMaxWorkers = 256;        // SMs; a part's weights a row fit the merge's place
-
-struct Few4State {
-  float2 ml[16][16];                    // [warp][row]
-  float2 fin[16];                       // a row's m of all warps, and 1 / l (l = 0: 0)
-  float row_mul[16];                    // a row's factor on the raw scores
-  uint32_t bad[DSPARK_TREE_MAX_NODES / 32];
-  int64_t sums[16];
-  Share share;
-  int live[2];                          // there is a segment; the next one
-  int join;                             // an item to join: first worker | parts << 16
-};
-
-// The 8x8 matrix of 16-bit elements that a warp holds, transposed.
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
-  uint32_t r;
-  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
-  return r;
+cudaError_t setup64() {
+  cudaError_t e = setup<64, 1, 16, false, false>();
+  if (e == cudaSuccess) e = setup<64, 1, 16, false, true>();
+  if (e == cudaSuccess) e = setup<64, 1, 16, true, false>();
+  if (e == cudaSuccess) e = setup<64, 1, 16, true, true>();
+  if (e == cudaSuccess) e = setup<64, 1, 4, true, false>();
+  if (e == cudaSuccess) e = setup<64, 2, 12, false, false>();
+  if (e == cudaSuccess) e = setup<64, 2, 12, false, true>();
+  if (e == cudaSuccess) e = setup<64, 2, 12, true, false>();
+  if (e == cudaSuccess) e = setup<64, 2, 12, true, true>();
+  if (e == cudaSuccess) e = setup<64, 2, 4, true, false>();
+  return e;
 }
 
-__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t saddr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(saddr)
-               : "memory");
-}
-
-// The scale bytes of a row, as many as its elements have blocks.
-__device__ __forceinline__ uint2 load_scales(const uint8_t* p, int D) {
-  uint2 r = make_uint2(0u, 0u);
-  if (D == 128) {
-    r = __ldg(reinterpret_cast<const uint2*>(p));
-  } else if (D == 64) {
-    r.x = __ldg(reinterpret_cast<const uint32_t*>(p));
-  } else {
-    const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
-    r.x = __ldg(h);
-    if (D == 96) {
-      r.x |= (uint32_t)__ldg(h + 1) << 16;
-      r.y = __ldg(h + 2);
-    }
+cudaError_t launch64(const AttendArgs& a, bool two, bool alone, bool bulk, cudaStream_t stream) {
+  const bool cap = a.softcap > 0.f;
+  if (!bulk) {
+    if (two) return cap ? launch<64, 2, 12, false, true>(a, stream) : launch<64, 2, 12, false, false>(a, stream);
+    return cap ? launch<64, 1, 16, false, true>(a, stream) : launch<64, 1, 16, false, false>(a, stream);
   }
-  return r;
-}
-
-// Eight f16 scales for the eight 16-byte-eighths of a row of 128 elements (64: each of
-// four blocks twice).
-template <int DP>
-__device__ __forceinline__ uint4 spread_scales(uint2 b) {
-  if (DP == 128)
-    return make_uint4(__byte_perm(b.x, 0, 0x4140) << 7, __byte_perm(b.x, 0, 0x4342) << 7,
-                      __byte_perm(b.y, 0, 0x4140) << 7, __byte_perm(b.y, 0, 0x4342) << 7);
-  return make_uint4(__byte_perm(b.x, 0, 0x4040) << 7, __byte_perm(b.x, 0, 0x4141) << 7,
-                    __byte_perm(b.x, 0, 0x4242) << 7, __byte_perm(b.x, 0, 0x4343) << 7);
-}
-
-// Whether one of a row's scale bytes is past those of numbers; and those, as 0.
-__device__ __forceinline__ bool zero_nonnumbers(uint32_t* w) {
-  const uint32_t over = __vcmpgtu4(*w, kTopScale * 0x01010101u);
-  *w &= ~over;
-  return over != 0;
-}
-
-// Overwrites a row's result, written by this CTA, with NaN where a draft row of V that
-// it sees has a block that is none: 16-bit values (out), or the part's floats.
-__device__ __noinline__ void add_nan(const AttendArgs& a, const uint32_t* bad,
-                                     const uint32_t* mask_row, int b, int rows, int start, int head,
-                                     int node, uint16_t* out, float* part) {
-#pragma unroll 1
-  for (int j = 0; j < rows; ++j) {
-    if (!(sees_word(mask_row, rows, node, j >> 5) & bad[j >> 5] & (1u << (j & 31)))) continue;
-    int64_t page;
-    int slot;
-    if (!locate(a.c, a.b, b, start + j, &page, &slot)) continue;
-    const uint8_t* s = a.c.scale[1].at((uint32_t)page, slot, head);
-#pragma unroll 1
-    for (int d = 0; d < a.D; ++d) {
-      if (s[d / 16] <= kTopScale) continue;
-      if (out) out[d] = 0x7fffu;                 // NaN in f16 and in bf16
-      else part[d] = __uint_as_float(0x7fffffffu);
-    }
+  if (two) {
+    if (cap) return launch<64, 2, 12, true, true>(a, stream);
+    return alone ? launch<64, 2, 12, true, false>(a, stream) : launch<64, 2, 4, true, false>(a, stream);
   }
+  if (cap) return launch<64, 1, 16, true, true>(a, stream);
+  return alone ? launch<64, 1, 16, true, false>(a, stream) : launch<64, 1, 4, true, false>(a, stream);
 }
 
-// Joins the `parts` parts of an item that several CTAs share, the first of them worker
-// `first`'s: a part's weight a row, then the sum over the parts in order, so that the
-// result does not depend on which CTA came last.
-template <bool F16, int DP, int NT>
-__device__ __noinline__ void join_parts(const AttendArgs& a, Few4State& st, float* weight, int first,
-                                        int parts, int row0, int head, int group, int rows) {
-  using L = Few4<DP, NT>;
-  constexpr int kRows = L::kRows;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  auto part_at = [&](int i) { return (int64_t)2 * (first + i) + (i == 0 ? 1 : 0); };
-  auto out_row = [&](int row) {
-    const int grow = group * kRows + row, node = a.group.div(grow);
-    return (int64_t)(row0 + node) * a.Hq + head * a.G + grow - node * a.G;
-  };
-  for (int row = warp; row < rows; row += L::kWarps) {
-    float top = -INFINITY, sum = 0.f;
-    for (int i = lane; i < parts; i += 32) top = fmaxf(top, __ldcg(a.part_ml + part_at(i) * kRows + row).x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float sub = top == -INFINITY ? 0.f : top;
-    for (int i = lane; i < parts; i += 32) {
-      const float2 ml = __ldcg(a.part_ml + part_at(i) * kRows + row);
-      const float w = ex2(ml.x - sub);
-      weight[i * kRows + row] = w;
-      sum = fmaf(ml.y, w, sum);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) {
-      st.fin[row] = make_float2(0.f, sum == 0.f ? 0.f : 1.f / sum);
-      if (a.lse) a.lse[out_row(row)] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-    }
+// Whether a page holds each head's slots, and their scales, next to each other, in pieces
+// that bulk copies take.
+bool in_runs(const AttendArgs& a) {
+  if (a.c.page.d % 16 != 0 || a.D % 64 != 0) return false;
+  for (int v = 0; v < 2; ++v) {
+    const Rows &x = a.c.x[v], &s = a.c.scale[v];
+    if (x.slot != (uint32_t)a.D / 2 || s.slot != (uint32_t)a.D / 16) return false;
+    if ((reinterpret_cast<uintptr_t>(s.p) | (uint64_t)s.head | s.page) % 16 != 0) return false;
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < rows * (DP / 4); i += L::kThreads) {
-    const int row = i / (DP / 4), c = i % (DP / 4);
-    if (4 * c >= a.D) continue;
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = 0; k < parts; ++k) {
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o + part_at(k) * (kRows * DP)) + i);
-      const float w = weight[k * kRows + row];
-      y.x = fmaf(x.x, w, y.x);
-      y.y = fmaf(x.y, w, y.y);
-      y.z = fmaf(x.z, w, y.z);
-      y.w = fmaf(x.w, w, y.w);
-    }
-    // l = 0: every weight was 0, and so is O
-    const float inv = st.fin[row].y;
-    *reinterpret_cast<uint2*>(a.out + out_row(row) * a.D + 4 * c) =
-        make_uint2(pack2<F16>(y.x * inv, y.y * inv), pack2<F16>(y.z * inv, y.w * inv));
-  }
-}
-
-template <bool F16, int DP, int NT, bool CAP>
-__global__ void __launch_bounds__(Few4<DP, NT>::kThreads, 1)
-    few4_kernel(const __grid_constant__ AttendArgs a) {
-  using L = Few4<DP, NT>;
-  using Item = typename L::Item;
-  using Segment = typename Item::Segment;
-  constexpr int kGroups = L::kGroups, kBlock = L::kBlock, kTiles = L::kTiles;
-  constexpr float kShift = 7.f;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ Few4State st;
-  __shared__ typename Item::Walker walker;
-  __shared__ Segment segments[2];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane >> 2, q = lane & 3;
-  uint8_t* ring = smem + warp * L::kRing;
-  uint4* q_mem = reinterpret_cast<uint4*>(smem + L::kQ);
-  const uint32_t scale_mem = ptx::smem_u32(ring + L::kScale);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (threadIdx.x < DSPARK_TREE_MAX_NODES / 32) st.bad[threadIdx.x] = 0;
-  Item::template plan<L::kThreads>(a, &st.share, st.sums);
-
-  // ---- the copies' side: the warp's blocks in order, one ahead of the products
-  BlockCursor<Item, L::kExtra> c;
-  c.init(a, st.share, warp);
-  const uint32_t top_page = (uint32_t)(a.c.n_pages - 1);
-  const bool even = a.c.page.d % 16 == 0;        // half a block lies in one page
-  // of the next block: the pages of its halves, or that of key `lane`
-  uint32_t page[2] = {0, 0}, worst = 0;
-  auto look = [&]() {
-    if (!c.more) return;
-    const int32_t* table = a.b.pages + (int64_t)c.b * a.b.pages_stride;
-    const int pos = c.t * kBlock + (even ? 0 : lane), last = c.start + c.rows - 1;
-    page[0] = (uint32_t)__ldg(table + a.c.page.div(min(pos, last)));
-    if (even) page[1] = (uint32_t)__ldg(table + a.c.page.div(min(pos + 16, last)));
-  };
-  look();
-  // this lane's place in a copy: its row of the rows at once, and its chunk.  V's lie so
-  // that the lanes of a load take all banks: pairs of rows (halves of 128 bytes for 128
-  // elements) change places by the key, and chunks of 128 elements by half of it.
-  const int copy_row = lane / L::kChunks, copy_chunk = lane % L::kChunks;
-  auto v_place = [](int key, int chunk) {        // of a chunk, in bytes
-    if (DP == 128)
-      return (key >> 1) * 128 + ((key ^ key >> 1) & 1) * 64 + (chunk ^ (key >> 2 & 1) * 2) * 16;
-    return (key >> 1) * 64 + ((key ^ key >> 2) & 1) * 32 + chunk * 16;
-  };
-  const bool chunk_in = copy_chunk * 32 < a.D;
-  int stage_in = 0;
-  uint2 k_scale = make_uint2(0u, 0u), v_scale = make_uint2(0u, 0u);   // of key `lane` in the block in flight
-  auto issue = [&]() {
-    if (c.more) {
-      const int pos0 = c.t * kBlock, last = c.start + c.rows - 1, head = c.head;
-      worst = max(worst, max(page[0], page[1])); // a bad page is reported at the end
-      const uint32_t pg0 = min(page[0], top_page), pg1 = min(page[1], top_page);
-      // slots of the halves' first keys, or of key `lane`
-      const int pos = even ? pos0 : min(pos0 + lane, last);
-      const int slot0 = pos - a.c.page.div(pos) * a.c.page.d;
-      const int slot1 = pos + 16 - a.c.page.div(pos + 16) * a.c.page.d;
-      const bool upper = lane >= 16 && even;
-      const uint32_t my_page = upper ? pg1 : pg0;
-      const int my_slot = !even ? slot0 : upper ? slot1 + lane - 16 : slot0 + lane;
-      k_scale = load_scales(a.c.scale[0].at(my_page, my_slot, head), a.D);
-      v_scale = load_scales(a.c.scale[1].at(my_page, my_slot, head), a.D);
-      c.next(a, warp, L::kWarps);
-      look();
-      uint8_t* dst = ring + stage_in * L::kStage;
-      const Rows &kr = a.c.x[0], &vr = a.c.x[1];
-      const uint8_t* k = kr.of_head(head) + copy_chunk * 16;
-      const uint8_t* v = vr.of_head(head) + copy_chunk * 16;
-#pragma unroll
-      for (int i = 0; i < L::kCopies; ++i) {
-        const int key = i * L::kRowsAtOnce + copy_row;
-        uint32_t p;
-        int s;
-        if (even) {
-          const bool second = i * L::kRowsAtOnce >= 16;
-          p = second ? pg1 : pg0;
-          s = (second ? slot1 : slot0) + key % 16;
-        } else {
-          p = __shfl_sync(0xffffffffu, my_page, key);
-          s = __shfl_sync(0xffffffffu, my_slot, key);
-        }
-        ptx::cp_async16_or_zero(dst + i * 512 + lane * 16, k + kr.offset(p, s), chunk_in);
-        ptx::cp_async16_or_zero(dst + L::kVPart + v_place(key, copy_chunk), v + vr.offset(p, s), chunk_in);
-      }
-    }
-    ptx::cp_async_commit();
-    stage_in ^= 1;
-  };
-
-  // ---- Q of a segment, warp nt the rows 8 nt ..: lane (g, q) the q-th quarter of row g
-  const Score sc = Score::of(a);
-  constexpr int kQChunks = DP / 32;              // 16-byte chunks of a row of Q a lane
-  uint4 qx[kQChunks];
-  auto load_q = [&](const Segment& s) {
-    const int rows = Item::group_rows(a, s), row = 8 * warp + g;
-    const int grow = s.group * L::kRows + (row < rows ? row : 0), nd = a.group.div(grow);
-    const uint4* src = reinterpret_cast<const uint4*>(
-        a.q + (int64_t)(s.row0 + nd) * a.q_row + (int64_t)(s.head * a.G + grow - nd * a.G) * a.q_head);
-#pragma unroll
-    for (int j = 0; j < kQChunks; ++j) {
-      qx[j] = make_uint4(0, 0, 0, 0);
-      if (row < rows && (q * kQChunks + j) * 8 < a.D) qx[j] = __ldg(src + q * kQChunks + j);
-    }
-  };
-  auto store_q = [&]() {
-    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
-    float row_mul = CAP ? 1.f : sc.sl2, r = 1.f;
-    if (!F16) {
-      // the row's largest magnitude to [2^14, 2^15): r a power of two, exact
-      uint32_t big = 0;
-#pragma unroll
-      for (int j = 0; j < kQChunks; ++j) {
-        const uint32_t w[4] = {qx[j].x, qx[j].y, qx[j].z, qx[j].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) big = max(big, max((w[k] & 0x7fffu) << 16, w[k] & 0x7fff0000u));
-      }
-      big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
-      big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-      const int e = (int)(big >> 23);
-      const int up = big == 0 || e == 255 ? 0 : min(127 + 14 - e, 126);
-      r = __uint_as_float((uint32_t)(127 + up) << 23);
-      row_mul *= __uint_as_float((uint32_t)(127 - up) << 23);
-    }
-    if (q == 0) st.row_mul[8 * warp + g] = row_mul;
-#pragma unroll
-    for (int j = 0; j < kQChunks; ++j) {
-      uint32_t w[4] = {qx[j].x ^ flip, qx[j].y ^ flip, qx[j].z ^ flip, qx[j].w ^ flip};
-      if (!F16) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          w[k] = pack2<true>(to_float<false>((uint16_t)w[k]) * r,
-                             to_float<false>((uint16_t)(w[k] >> 16)) * r);
-      }
-      q_mem[(warp * kQChunks + j) * 32 + lane] = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-  };
-  if (threadIdx.x == 0) {
-    walker.init(a, st.share);
-    st.live[0] = walker.next(a, &segments[0]);
-  }
-  issue();
-  __syncthreads();
-  if (st.live[0] && warp < NT) {
-    load_q(segments[0]);
-    store_q();
-  }
-  __syncthreads();
-
-  // ---- the products' side
-  int stage = 0, cur = 0;
-  while (st.live[cur]) {
-    const Segment& s = segments[cur];
-    const int rows = Item::group_rows(a, s), t1 = s.t1, start = s.start;
-    // O^T: tile t of row tile nt has columns (DP / 8) g + 2 t, + 1 of rows 8 nt + 2q, + 1
-    float o[NT][kTiles][4], mref[NT][2], l[NT][2], row_mul[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        mref[nt][e] = -INFINITY;
-        l[nt][e] = 0.f;
-        row_mul[nt][e] = st.row_mul[8 * nt + 2 * q + e];
-      }
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[nt][t][k] = 0.f;
-    }
-    // the segment after this one, meanwhile
-    if (threadIdx.x == L::kThreads - 1) st.live[cur ^ 1] = walker.next(a, &segments[cur ^ 1]);
-#pragma unroll 1
-    for (int t = s.t0 + warp; t < t1; t += L::kWarps) {
-      const int pos0 = t * kBlock;
-      const bool masked = pos0 + kBlock > start;
-      // this block's scales have landed with lane = key
-      {
-        uint2 vs = v_scale;
-        if (masked) {
-          const int j = pos0 + lane - start;     // place in the draft
-          if (j >= s.rows) {                     // past the end: anything may stand there
-            vs = make_uint2(0u, 0u);
-          } else if (j >= 0) {
-            const bool x = zero_nonnumbers(&vs.x), y = zero_nonnumbers(&vs.y);
-            if (x || y) atomicOr(&st.bad[j >> 5], 1u << (j & 31));
-          }
-        }
-        __syncwarp();                            // the block before has been read
-        uint4* to = reinterpret_cast<uint4*>(ring + L::kScale);
-        to[lane] = spread_scales<DP>(k_scale);
-        to[32 + lane] = spread_scales<DP>(vs);
-      }
-      issue();
-      ptx::cp_async_wait_group<1>();
-      __syncwarp();
-      const uint8_t* src = ring + stage * L::kStage;
-      stage ^= 1;
-      // S^T: keys g, g + 8, .. of rows 8 nt + 2q, + 1
-      uint32_t ks[4];
-      ptx::ldmatrix_x4(scale_mem + lane * 16, ks[0], ks[1], ks[2], ks[3]);
-      float x[NT][kGroups][2];
-#pragma unroll
-      for (int mt = 0; mt < kGroups / 2; ++mt) {
-        uint32_t kw[2][L::kWords];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint8_t* row = src + (2 * mt + h) * (8 * L::kBytes) + lane * (L::kBytes / 4);
-          if (DP == 128) {
-            const uint4 y = *reinterpret_cast<const uint4*>(row);
-            kw[h][0] = y.x, kw[h][1] = y.y, kw[h][2 % L::kWords] = y.z, kw[h][3 % L::kWords] = y.w;
-          } else {
-            const uint2 y = *reinterpret_cast<const uint2*>(row);
-            kw[h][0] = y.x, kw[h][1] = y.y;
-          }
-        }
-        float acc[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) acc[nt][k] = 0.f;
-#pragma unroll
-        for (int i = 0; i < L::kWords; ++i) {    // a word: two steps
-          // 128 elements: the lane's first two words are under one scale, the others under the next
-          const uint32_t sel = i < 2 ? 0x1010 : 0x3232;
-          const uint32_t s0 = __byte_perm(ks[2 * mt], 0, sel), s1 = __byte_perm(ks[2 * mt + 1], 0, sel);
-          uint4 ka = e2m1x8_to_f16(kw[0][i]), kb = e2m1x8_to_f16(kw[1][i]);
-          ka = make_uint4(mul_f16x2(ka.x, s0), mul_f16x2(ka.y, s0), mul_f16x2(ka.z, s0), mul_f16x2(ka.w, s0));
-          kb = make_uint4(mul_f16x2(kb.x, s1), mul_f16x2(kb.y, s1), mul_f16x2(kb.z, s1), mul_f16x2(kb.w, s1));
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const uint4 b = q_mem[(nt * kQChunks + i) * 32 + lane];
-            ptx::mma_16816_f16(acc[nt], ka.x, kb.x, ka.y, kb.y, b.x, b.y);
-            ptx::mma_16816_f16(acc[nt], ka.z, kb.z, ka.w, kb.w, b.z, b.w);
-          }
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) x[nt][2 * mt + k / 2][k % 2] = acc[nt][k];
-      }
-      // invisible scores -infinity; see: bit 8 i, the row sees key 8 i + g
-      uint32_t see[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          see[nt][e] = 0x01010101u;
-          if (masked) {
-            const int row = 8 * nt + 2 * q + e;
-            const int nd = a.group.div(s.group * L::kRows + (row < rows ? row : 0));
-            see[nt][e] = sees_32(a.mask ? a.mask + (int64_t)(s.row0 + nd) * a.mask_stride : nullptr,
-                                 s.rows, nd, pos0 - start) >> g & 0x01010101u;
-#pragma unroll
-            for (int i = 0; i < kGroups; ++i)
-              if (!(see[nt][e] >> (8 * i) & 1)) x[nt][i][e] = -INFINITY;
-          }
-        }
-      float mx[NT][2];
-      bool over = false;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float y = fmaxf(fmaxf(x[nt][0][e], x[nt][1][e]), fmaxf(x[nt][2][e], x[nt][3][e]));
-          y = y == -INFINITY ? -INFINITY : y * row_mul[nt][e];
-          // a visible score of -infinity is the cap's negative, an invisible one nothing
-          if (CAP && see[nt][e] != 0) y = capped(sc, y, 0.f);
-          mx[nt][e] = y;
-          over |= y > mref[nt][e] + (mref[nt][e] == -INFINITY ? 0.f : kShift + 8.f);
-        }
-      // the first visible key sets a row's m, later ones when the maximum has grown enough
-      if (__any_sync(0xffffffffu, over)) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float y = mx[nt][e];
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, off));
-            const float old = mref[nt][e];
-            if (y > old + (old == -INFINITY ? 0.f : kShift + 8.f)) {
-              mref[nt][e] = y - kShift;
-              const float back = old == -INFINITY ? 0.f : ex2(old - mref[nt][e]);
-              l[nt][e] *= back;
-#pragma unroll
-              for (int t8 = 0; t8 < kTiles; ++t8) {
-                o[nt][t8][e] *= back;
-                o[nt][t8][2 + e] *= back;
-              }
-            }
-          }
-      }
-      // weights, as the B operand of the second product
-      uint32_t p[NT][kGroups];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float w[kGroups][2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float sub = mref[nt][e] == -INFINITY ? 0.f : mref[nt][e];
-          if (!CAP) {
-#pragma unroll
-            for (int i = 0; i < kGroups; ++i) w[i][e] = fmaf(x[nt][i][e], row_mul[nt][e], -sub);
-          } else {
-            float raw[kGroups], big = 0.f;
-#pragma unroll
-            for (int i = 0; i < kGroups; ++i) {
-              raw[i] = x[nt][i][e] * row_mul[nt][e];
-              big = fmaxf(big, fabsf(raw[i]));
-              w[i][e] = capped_near(sc, raw[i], sub);
-            }
-            if (__any_sync(0xffffffffu, past_near(sc, big))) {
-#pragma unroll
-              for (int i = 0; i < kGroups; ++i) {
-                const float past = capped_past(sc, raw[i], sub);
-                if (past_near(sc, raw[i])) w[i][e] = past;
-              }
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < kGroups; ++i) w[i][e] = ex2(w[i][e]);
-          // by the bits: an invisible key's exponent can be anything (-infinity times a
-          // scale of zero)
-          if (masked) {
-#pragma unroll
-            for (int i = 0; i < kGroups; ++i)
-              if (!(see[nt][e] >> (8 * i) & 1)) w[i][e] = 0.f;
-          }
-          l[nt][e] += (w[0][e] + w[1][e]) + (w[2][e] + w[3][e]);
-        }
-#pragma unroll
-        for (int i = 0; i < kGroups; ++i) p[nt][i] = transpose8x8(pack2<true>(w[i][0], w[i][1]));
-      }
-      // O^T += V^T P^T, 16 keys at a time
-      uint32_t vs[4];
-      ldmatrix_x4_trans(scale_mem + kBlock * 16 + lane * 16, vs);
-#pragma unroll
-      for (int mt = 0; mt < kGroups / 2; ++mt) {
-        // the lane's codes of keys 16 mt + 2q, + 1, + 8, + 9
-        constexpr int kV = DP / 64;              // words a key
-        uint32_t vw[4][kV];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int key = 16 * mt + 2 * q + (k & 1) + 8 * (k >> 1);
-          const uint8_t* row = src + L::kVPart + v_place(key, g * kV / 4) + g * kV % 4 * 4;
-          if (DP == 128) {
-            const uint2 y = *reinterpret_cast<const uint2*>(row);
-            vw[k][0] = y.x, vw[k][kV - 1] = y.y;
-          } else {
-            vw[k][0] = *reinterpret_cast<const uint32_t*>(row);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kV; ++i) {
-          // even elements of the pairs of keys, and odd ones: a byte a column
-          uint4 even2[2], odd2[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t wa = vw[2 * h][i], wb = vw[2 * h + 1][i], sv = vs[2 * mt + h];
-            uint4 y = e2m1x8_to_f16((wa & 0x0f0f0f0fu) | (wb << 4 & 0xf0f0f0f0u));
-            even2[h] = make_uint4(mul_f16x2(y.x, sv), mul_f16x2(y.y, sv), mul_f16x2(y.z, sv), mul_f16x2(y.w, sv));
-            y = e2m1x8_to_f16((wa >> 4 & 0x0f0f0f0fu) | (wb & 0xf0f0f0f0u));
-            odd2[h] = make_uint4(mul_f16x2(y.x, sv), mul_f16x2(y.y, sv), mul_f16x2(y.z, sv), mul_f16x2(y.w, sv));
-          }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const uint32_t b0 = p[nt][2 * mt], b1 = p[nt][2 * mt + 1];
-            ptx::mma_16816_f16(o[nt][4 * i], even2[0].x, odd2[0].x, even2[1].x, odd2[1].x, b0, b1);
-            ptx::mma_16816_f16(o[nt][4 * i + 1], even2[0].y, odd2[0].y, even2[1].y, odd2[1].y, b0, b1);
-            ptx::mma_16816_f16(o[nt][4 * i + 2], even2[0].z, odd2[0].z, even2[1].z, odd2[1].z, b0, b1);
-            ptx::mma_16816_f16(o[nt][4 * i + 3], even2[0].w, odd2[0].w, even2[1].w, odd2[1].w, b0, b1);
-          }
-        }
-      }
-    }
-
-    // the warps meet: O, m and l of the segment
-    const bool whole = s.whole();
-    const int64_t part = 2 * blockIdx.x + (s.t0 == 0 ? 1 : 0);
-    const int live = min(L::kWarps, s.t1 - s.t0);          // warps that had a block
-    float* merge = reinterpret_cast<float*>(smem + L::kMerge);
-    auto out_row = [&](int row) {
-      const int grow = s.group * L::kRows + row, nd = a.group.div(grow);
-      return (int64_t)(s.row0 + nd) * a.Hq + s.head * a.G + grow - nd * a.G;
-    };
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float sum = l[nt][e];
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        if (g == 0) st.ml[warp][8 * nt + 2 * q + e] = make_float2(mref[nt][e], sum);
-      }
-    __syncthreads();
-    const bool next_live = st.live[cur ^ 1];
-    if (warp == 0 && lane < L::kRows) {          // a row a lane: m and l of all warps
-      float top = -INFINITY, sum = 0.f;
-      for (int i = 0; i < live; ++i) top = fmaxf(top, st.ml[i][lane].x);
-      const float sub = top == -INFINITY ? 0.f : top;
-      for (int i = 0; i < live; ++i) sum = fmaf(st.ml[i][lane].y, ex2(st.ml[i][lane].x - sub), sum);
-      st.fin[lane] = make_float2(sub, sum == 0.f ? 0.f : 1.f / sum);
-      if (lane < rows) {
-        if (!whole) a.part_ml[part * L::kRows + lane] = make_float2(top, sum);
-        else if (a.lse) a.lse[out_row(lane)] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-      }
-    }
-    if (next_live && warp < NT) load_q(segments[cur ^ 1]);
-    __syncthreads();
-    // every warp's O by its weight, half the columns at a time
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      if (warp < live) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int row = 8 * nt + 2 * q + e;
-            const float w = ex2(mref[nt][e] - st.fin[row].x);
-            float* dst = merge + (warp * L::kRows + row) * L::kMergeRow + g * (DP / 16);
-#pragma unroll
-            for (int k = 0; k < kTiles / 2; k += 2) {
-              const float* y = o[nt][half * (kTiles / 2) + k];
-              const float* z = o[nt][half * (kTiles / 2) + k + 1];
-              *reinterpret_cast<float4*>(dst + 2 * k) = make_float4(y[e] * w, y[2 + e] * w, z[e] * w, z[2 + e] * w);
-            }
-          }
-      }
-      __syncthreads();
-      for (int i = threadIdx.x; i < rows * (L::kHalf / 2); i += L::kThreads) {
-        const int row = i / (L::kHalf / 2), n = i % (L::kHalf / 2) * 2;
-        float2 y = make_float2(0.f, 0.f);
-#pragma unroll 4
-        for (int k = 0; k < live; ++k) {
-          const float2 v = *reinterpret_cast<const float2*>(merge + (k * L::kRows + row) * L::kMergeRow + n);
-          y.x += v.x;
-          y.y += v.y;
-        }
-        const int d = n / (DP / 16) * (DP / 8) + half * (DP / 16) + n % (DP / 16);
-        if (!whole) {
-          *reinterpret_cast<float2*>(a.part_o + (part * L::kRows + row) * DP + d) = y;
-        } else if (d < a.D) {
-          // l = 0: every weight was 0, and so is O
-          const float inv = st.fin[row].y;
-          *reinterpret_cast<uint32_t*>(a.out + out_row(row) * a.D + d) = pack2<F16>(y.x * inv, y.y * inv);
-        }
-      }
-      __syncthreads();
-    }
-    uint32_t any_bad = 0;
-#pragma unroll
-    for (int k = 0; k < DSPARK_TREE_MAX_NODES / 32; ++k) any_bad |= st.bad[k];
-    __syncthreads();
-    if (next_live && warp < NT) store_q();
-    if (any_bad != 0) {
-      if ((int)threadIdx.x < rows) {
-        const int nd = a.group.div(s.group * L::kRows + threadIdx.x);
-        add_nan(a, st.bad, a.mask ? a.mask + (int64_t)(s.row0 + nd) * a.mask_stride : nullptr, s.b, s.rows,
-                s.start, s.head, nd, whole ? a.out + out_row(threadIdx.x) * a.D : nullptr,
-                a.part_o + (part * L::kRows + threadIdx.x) * DP);
-      }
-      __syncthreads();
-      if (threadIdx.x < DSPARK_TREE_MAX_NODES / 32) st.bad[threadIdx.x] = 0;
-    }
-    if (!whole) {
-      // the last CTA to leave its part of the item joins them all
-      __threadfence();
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        const int w = Item::part_of(s, st.share.cut).w;
-        int* count = a.arrived + (w & 0xffff);
-        const bool last = atomicAdd(count, 1) == (w >> 16) - 1;
-        if (last) *count = 0;
-        __threadfence();
-        st.join = last ? w : 0;
-      }
-      __syncthreads();
-      if (st.join)
-        join_parts<F16, DP, NT>(a, st, merge, st.join & 0xffff, st.join >> 16, s.row0, s.head, s.group, rows);
-    }
-    __syncthreads();
-    cur ^= 1;
-  }
-  ptx::cp_async_wait_group<0>();
-  if (worst > top_page) set_status(a.status, DSPARK_EPAGES);
-}
-
-template <bool F16, int DP, int NT, bool CAP>
-cudaError_t launch(const AttendArgs& a, cudaStream_t stream) {
-  using L = Few4<DP, NT>;
-  // launched while the kernel before it in the stream ends, which it waits for before
-  // anything else
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(a.n_cta);
-  cfg.blockDim = dim3(L::kThreads);
-  cfg.dynamicSmemBytes = L::kSmem;
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, few4_kernel<F16, DP, NT, CAP>, a);
-}
-
-template <bool F16, int DP, int NT>
-cudaError_t setup() {
-  using L = Few4<DP, NT>;
-  static_assert(L::kSmem + sizeof(Few4State) + 512 <= 232448, "shared memory of an SM");
-  static_assert(L::kWarps * L::kMergeRow >= kMaxWorkers, "a part's weights fit the merge's place");
-  const cudaError_t e = cudaFuncSetAttribute(
-      few4_kernel<F16, DP, NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(few4_kernel<F16, DP, NT, true>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
-}
-
-template <bool F16, int DP>
-cudaError_t setup_both() {
-  const cudaError_t e = setup<F16, DP, 1>();
-  return e != cudaSuccess ? e : setup<F16, DP, 2>();
-}
-
-template <bool F16, int DP, int NT>
-cudaError_t launch_cap(const AttendArgs& a, cudaStream_t stream) {
-  return a.softcap > 0.f ? launch<F16, DP, NT, true>(a, stream)
-                         : launch<F16, DP, NT, false>(a, stream);
-}
-
-// One tile of eight rows an item where the requests have no more on average.
-template <bool F16, int DP>
-cudaError_t launch_rows(const AttendArgs& a, cudaStream_t stream) {
-  return (int64_t)a.b.N * a.G <= (int64_t)8 * a.b.B ? launch_cap<F16, DP, 1>(a, stream)
-                                                    : launch_cap<F16, DP, 2>(a, stream);
+  return true;
 }
 
 }  // namespace
 
-cudaError_t few4_setup(bool f16, int D) {
-  if (padded_dim(D) == 64) return f16 ? setup_both<true, 64>() : setup_both<false, 64>();
-  return f16 ? setup_both<true, 128>() : setup_both<false, 128>();
-}
+cudaError_t few4_setup(int D) { return padded_dim(D) == 64 ? setup64() : few4_setup128(); }
 
-cudaError_t few4_launch(const AttendArgs& a, bool f16, cudaStream_t stream) {
-  if (a.n_cta > kMaxWorkers) return cudaErrorNotSupported;
-  if (padded_dim(a.D) == 64) return f16 ? launch_rows<true, 64>(a, stream) : launch_rows<false, 64>(a, stream);
-  return f16 ? launch_rows<true, 128>(a, stream) : launch_rows<false, 128>(a, stream);
+cudaError_t few4_launch(const AttendArgs& a, cudaStream_t stream) {
+  // one tile of eight rows an item where the requests have no more on average
+  const bool two = (int64_t)a.b.N * a.G > (int64_t)8 * a.b.B;
+  // workers of four warps where there are two items a SM (64 heads on 8, 500 to 9,000
+  // tokens, us with four / with a CTA's: 48 requests 76 / 93, 128 167 / 207; 16 requests 38 /
+  // 39, 1 of 5,000 27 / 16, 19 of 32,767 156 / 144)
+  const int64_t items = ((int64_t)a.b.N * a.G + 7) / 8 * a.Hkv;
+  const bool alone = items < (int64_t)2 * a.n_cta;
+  const bool bulk = in_runs(a);
+  return padded_dim(a.D) == 64 ? launch64(a, two, alone, bulk, stream)
+                               : few4_launch128(a, two, alone, bulk, stream);
 }
 
 }  // namespace tree

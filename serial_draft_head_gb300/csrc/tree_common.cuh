@@ -282,7 +282,7 @@ struct AttendArgs {
   int Hq, Hkv, G, D;
   int max_nodes;
   FastDiv group;             // by G
-  int n_cta;
+  int n_cta;                 // workers
   // partial results of items that several CTAs share: per CTA two parts of
   // part_rows rows: O (fp32, [D / 4][part_rows][4]) and {m, l} a row
   float* part_o;
@@ -290,6 +290,7 @@ struct AttendArgs {
   int4* part_of;             // per part: {request, head, row group, first worker | parts << 16}
   int part_rows;
   int* arrived;              // few rows: parts written of the item whose first is a worker's, 0 between calls
+  bool f16;                  // few rows over e2m1: the handle's type
   int* status;
 };
 
@@ -306,9 +307,11 @@ struct TileMaps {
   int rows;
 };
 
-// e2m1 cache, few rows a cached head (tree_attend_few4.cu).
-cudaError_t few4_setup(bool f16, int D);
-cudaError_t few4_launch(const AttendArgs& a, bool f16, cudaStream_t stream);
+// e2m1 cache, few rows a cached head (tree_attend_few4.cuh).  kFew4Workers: most workers
+// an SM, kFew4PartRows: rows of their parts.
+constexpr int kFew4Workers = 4, kFew4PartRows = 96;
+cudaError_t few4_setup(int D);
+cudaError_t few4_launch(const AttendArgs& a, cudaStream_t stream);
 
 // e2m1 cache, more rows (tree_attend4.cu).
 cudaError_t attend4_setup(bool f16, int D);

@@ -162,13 +162,14 @@ struct Work {
     return r;
   }
 
-  // The CTA's share, by all its THREADS threads: sums the requests' units in order.
-  template <int THREADS>
+  // The shares of the CTA's WORKERS workers, by all its THREADS threads: sums the requests'
+  // units in order.
+  template <int THREADS, int WORKERS = 1>
   __device__ static __forceinline__ void plan(const AttendArgs& a, Share* share,
                                               int64_t* warp_sum) {
     constexpr int kPer = (DSPARK_TREE_MAX_REQUESTS + THREADS - 1) / THREADS;
     int64_t mine[kPer], sum = 0;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, worker = blockIdx.x;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int per = (a.b.B + THREADS - 1) / THREADS;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
@@ -178,7 +179,7 @@ struct Work {
         bool ok;
         const Request r = load_request(a, b, &ok);
         if (ok && r.rows > 0) mine[k] = (int64_t)(r.tiles + EXTRA) * r.groups * a.Hkv;
-        if (!ok && worker == 0) set_status(a.status, DSPARK_EPAGES);
+        if (!ok && blockIdx.x == 0) set_status(a.status, DSPARK_EPAGES);
       }
       sum += mine[k];
     }
@@ -189,7 +190,7 @@ struct Work {
       if (lane >= o) incl += y;
     }
     if (lane == 31) warp_sum[warp] = incl;
-    if (threadIdx.x == 0) share->units = 0;
+    if (threadIdx.x < WORKERS) share[threadIdx.x].units = 0;
     __syncthreads();
     int64_t before = incl - sum, total = 0;
 #pragma unroll
@@ -199,28 +200,32 @@ struct Work {
       total += y;
     }
     const Cut cut = Cut::of(total, a.n_cta);
-    const int64_t u0 = cut.start(worker);
-    // the thread whose requests hold the share's first unit writes it
-    if (worker < cut.workers && u0 >= before && u0 < before + sum) {
-      int64_t at = before;
 #pragma unroll 1
-      for (int b = threadIdx.x * per; b < a.b.B; ++b) {
-        bool ok;
-        const Request r = load_request(a, b, &ok);
-        const int64_t units = (int64_t)(r.tiles + EXTRA) * r.groups * a.Hkv;
-        if (u0 < at + units) {
-          share->unit0 = u0;
-          share->units = cut.start(worker + 1) - u0;
-          share->cut = cut;
-          const int64_t item = quotient(u0 - at, r.tiles + EXTRA);
-          const int head = (int)quotient(item, r.groups);
-          share->b0 = b;
-          share->t0 = (int)(u0 - at - item * (r.tiles + EXTRA)) - EXTRA;
-          share->head0 = head;
-          share->group0 = (int)(item - (int64_t)head * r.groups);
-          break;
+    for (int k = 0; k < WORKERS; ++k, ++share) {
+      const int worker = blockIdx.x * WORKERS + k;
+      const int64_t u0 = cut.start(worker);
+      // the thread whose requests hold the share's first unit writes it
+      if (worker < cut.workers && u0 >= before && u0 < before + sum) {
+        int64_t at = before;
+#pragma unroll 1
+        for (int b = threadIdx.x * per; b < a.b.B; ++b) {
+          bool ok;
+          const Request r = load_request(a, b, &ok);
+          const int64_t units = (int64_t)(r.tiles + EXTRA) * r.groups * a.Hkv;
+          if (u0 < at + units) {
+            share->unit0 = u0;
+            share->units = cut.start(worker + 1) - u0;
+            share->cut = cut;
+            const int64_t item = quotient(u0 - at, r.tiles + EXTRA);
+            const int head = (int)quotient(item, r.groups);
+            share->b0 = b;
+            share->t0 = (int)(u0 - at - item * (r.tiles + EXTRA)) - EXTRA;
+            share->head0 = head;
+            share->group0 = (int)(item - (int64_t)head * r.groups);
+            break;
+          }
+          at += units;
         }
-        at += units;
       }
     }
     __syncthreads();
