@@ -6,7 +6,7 @@ namespace dspark {
 namespace tree {
 
 cudaError_t few4_setup128();
-cudaError_t few4_launch128(const AttendArgs& a, bool two, bool alone, bool bulk, cudaStream_t stream);
+cudaError_t few4_launch128(const AttendArgs& a, bool two, bool alone, bool runs, cudaStream_t stream);
 
 namespace {
 
@@ -24,9 +24,9 @@ cudaError_t setup64() {
   return e;
 }
 
-cudaError_t launch64(const AttendArgs& a, bool two, bool alone, bool bulk, cudaStream_t stream) {
+cudaError_t launch64(const AttendArgs& a, bool two, bool alone, bool runs, cudaStream_t stream) {
   const bool cap = a.softcap > 0.f;
-  if (!bulk) {
+  if (!runs) {
     if (two) return cap ? launch<64, 2, 12, false, true>(a, stream) : launch<64, 2, 12, false, false>(a, stream);
     return cap ? launch<64, 1, 16, false, true>(a, stream) : launch<64, 1, 16, false, false>(a, stream);
   }
@@ -39,7 +39,7 @@ cudaError_t launch64(const AttendArgs& a, bool two, bool alone, bool bulk, cudaS
 }
 
 // Whether a page holds each head's slots, and their scales, next to each other, in pieces
-// that bulk copies take.
+// that 16-byte copies take.
 bool in_runs(const AttendArgs& a) {
   if (a.c.page.d % 16 != 0 || a.D % 64 != 0) return false;
   for (int v = 0; v < 2; ++v) {
@@ -62,9 +62,9 @@ cudaError_t few4_launch(const AttendArgs& a, cudaStream_t stream) {
   // 39, 1 of 5,000 27 / 16, 19 of 32,767 156 / 144)
   const int64_t items = ((int64_t)a.b.N * a.G + 7) / 8 * a.Hkv;
   const bool alone = items < (int64_t)2 * a.n_cta;
-  const bool bulk = in_runs(a);
-  return padded_dim(a.D) == 64 ? launch64(a, two, alone, bulk, stream)
-                               : few4_launch128(a, two, alone, bulk, stream);
+  const bool runs = in_runs(a);
+  return padded_dim(a.D) == 64 ? launch64(a, two, alone, runs, stream)
+                               : few4_launch128(a, two, alone, runs, stream);
 }
 
 }  // namespace tree

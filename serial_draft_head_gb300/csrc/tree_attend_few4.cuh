@@ -6,11 +6,12 @@
 // group take a segment's blocks in turn, each with its own O, m and l, and meet at its
 // end; with four to a group the others of the SM go on meanwhile.
 //
-// Each warp has a ring of two blocks, which it fills itself, so that nothing is handed
-// between warps.  Where a page holds a head's slots and their scales next to each other
-// (KVCache.zeros lays them so), blocks are copied in bulk, a lane for the codes and the
-// scales of K and V each (a warp that copied for all others took 340 cycles a block, more
-// than the others need for it); else by 16 bytes a lane.
+// Each warp has a ring of two blocks, which it fills itself by copies of 16 bytes a lane,
+// so that nothing is handed between warps.  Where a page holds a head's slots and their
+// scales next to each other (KVCache.zeros lays them so: RUNS), a block is a run of memory
+// and a copy an address and an immediate offset.  (Bulk copies: by a warp for all others
+// 340 cycles a block, more than the others need for it; by each warp for itself about 60
+// instructions a block more than these.)
 //
 // A cached row of 128 elements is 72 bytes, so what bounds the kernel is less the memory
 // than what is done to every element on the way to the products (f16 mma.sync
@@ -42,8 +43,8 @@ namespace tree {
 namespace {
 
 // DP: head dimension as laid out, 64 or 128; NT: tiles of eight rows; GROUP: warps of a
-// worker; BULK: blocks come by bulk copies.
-template <int DP, int NT, int GROUP, bool BULK>
+// worker; RUNS: slots and scales lie next to each other.
+template <int DP, int NT, int GROUP, bool RUNS>
 struct Few4 {
   static constexpr int kRows = 8 * NT;
   static constexpr int kBlock = 32;
@@ -55,14 +56,14 @@ struct Few4 {
   static constexpr int kWorkers = kWarps / GROUP;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kBytes = DP / 2;                  // of a row of codes
-  static constexpr int kScaleBytes = DP / 16;            // of its scales (BULK)
+  static constexpr int kScaleBytes = DP / 16;            // of its scales (RUNS)
   static constexpr int kChunks = kBytes / 16;            // 16-byte copies of a row
   static constexpr int kRowsAtOnce = 32 / kChunks;       // rows of one copy instruction
   static constexpr int kCopies = kBlock / kRowsAtOnce;
   static constexpr int kWords = kBytes / 16;             // 32-bit words a lane, of a row of K
   static constexpr int kVPart = kBlock * kBytes;         // V's place in a stage
   static constexpr int kScales = 2 * kVPart;             // and the scales' bytes
-  static constexpr int kStage = kScales + (BULK ? 2 * kBlock * kScaleBytes : 0);
+  static constexpr int kStage = kScales + (RUNS ? 2 * kBlock * kScaleBytes : 0);
   static constexpr int kStages = 2;
   static constexpr int kTiles = DP / 16;                 // of O^T
   static constexpr int kScale = kStages * kStage;        // a block's scales as f16: [K, V][key][8]
@@ -77,8 +78,6 @@ struct Few4 {
   using Item = Work<kBlock, kRows, kExtra>;
 };
 
-constexpr uint64_t kWaitLimitNs = 1000000000ull;
-
 template <int GROUP>
 struct WorkerState {
   float2 ml[GROUP][16];                 // [warp][row]
@@ -88,34 +87,6 @@ struct WorkerState {
   int live[2];                          // there is a segment; the next one
   int join;                             // an item to join: first worker | parts << 16
 };
-
-struct Pipe {
-  uint64_t full[16][2];                 // [warp][stage]
-  int abort;
-};
-
-__device__ __forceinline__ uint64_t globaltimer_ns() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-  return t;
-}
-
-// Every wait ends: past the limit the abort flag makes all waits of the CTA return at once,
-// the loops run on without starting copies, and the status says so.
-__device__ __forceinline__ void wait(Pipe* s, uint64_t* bar, uint32_t parity, int* status) {
-  if (ptx::mbar_try_wait(bar, parity)) return;
-  const uint64_t t0 = globaltimer_ns();
-  uint32_t spins = 0;
-  while (!ptx::mbar_try_wait(bar, parity)) {
-    if ((++spins & 63u) != 0u) continue;
-    if (*(const volatile int*)&s->abort) return;
-    if (globaltimer_ns() - t0 > kWaitLimitNs) {
-      *(volatile int*)&s->abort = 1;
-      set_status(status, DSPARK_ETIMEOUT);
-      return;
-    }
-  }
-}
 
 // The warps of worker w meet.
 template <int GROUP>
@@ -274,10 +245,10 @@ __device__ __noinline__ void join_parts(const AttendArgs& a, WorkerState<GROUP>&
   }
 }
 
-template <int DP, int NT, int GROUP, bool BULK, bool CAP>
-__global__ void __launch_bounds__(Few4<DP, NT, GROUP, BULK>::kThreads, 1)
+template <int DP, int NT, int GROUP, bool RUNS, bool CAP>
+__global__ void __launch_bounds__(Few4<DP, NT, GROUP, RUNS>::kThreads, 1)
     few4_kernel(const __grid_constant__ AttendArgs a) {
-  using L = Few4<DP, NT, GROUP, BULK>;
+  using L = Few4<DP, NT, GROUP, RUNS>;
   using Item = typename L::Item;
   using Segment = typename Item::Segment;
   constexpr int kParts = L::kParts, kBlock = L::kBlock, kTiles = L::kTiles;
@@ -289,7 +260,6 @@ __global__ void __launch_bounds__(Few4<DP, NT, GROUP, BULK>::kThreads, 1)
   __shared__ int64_t sums[L::kThreads / 32];
   __shared__ typename Item::Walker walkers[L::kWorkers];
   __shared__ Segment all_segments[L::kWorkers][2];
-  __shared__ Pipe pipe;
   const int cta_warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane >> 2, q = lane & 3;
   const int worker = cta_warp / GROUP, warp = cta_warp % GROUP;
   const int tid = threadIdx.x % kWorkerThreads;  // in the worker
@@ -301,12 +271,6 @@ __global__ void __launch_bounds__(Few4<DP, NT, GROUP, BULK>::kThreads, 1)
                              (lane / 8 * 8 + row_key(lane % 8)) * 16;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (tid < DSPARK_TREE_MAX_NODES / 32) st.bad[tid] = 0;
-  if (BULK && threadIdx.x == 0) {
-    for (int i = 0; i < L::kWarps; ++i)
-      for (int k = 0; k < L::kStages; ++k) ptx::mbar_init(&pipe.full[i][k], 1);
-    ptx::fence_mbar_init();
-    pipe.abort = 0;
-  }
   Item::template plan<L::kThreads, L::kWorkers>(a, shares, sums);
   const Share& share = shares[worker];
   Segment* segments = all_segments[worker];
@@ -315,25 +279,40 @@ __global__ void __launch_bounds__(Few4<DP, NT, GROUP, BULK>::kThreads, 1)
   BlockCursor<Item, L::kExtra> c;
   c.init(a, share, warp);
   const uint32_t top_page = (uint32_t)(a.c.n_pages - 1);
-  const bool even = BULK || a.c.page.d % 16 == 0;          // half a block lies in one page
-  // of the next block: the pages of its halves (bulk: of the lane's), or that of key `lane`
+  const bool even = RUNS || a.c.page.d % 16 == 0;          // half a block lies in one page
+  const bool in_two = RUNS && a.c.page.d % kBlock != 0;    // a block can lie in two
+  // of the next block: the pages of its halves and (RUNS) their first slots, or that of key `lane`
   uint32_t page[2] = {0, 0}, worst = 0;
-  // bulk: lanes 0 to 3 the codes and scales of K and V; where pages are of 16 slots, or a
-  // block can lie in two for another reason, four more for its second half
-  const bool in_two = BULK && a.c.page.d % kBlock != 0;
-  const int bulk_half = in_two ? lane >> 2 & 1 : 0;
-  const bool bulk_lane = lane < (in_two ? 8 : 4);
-  const Rows bulk_rows = lane & 2 ? a.c.scale[lane & 1] : a.c.x[lane & 1];
-  const uint32_t bulk_bytes = (lane & 2 ? kBlock * L::kScaleBytes : kBlock * L::kBytes) >> (in_two ? 1 : 0);
-  const uint32_t bulk_place = (lane & 2 ? L::kScales : 0) +
-                              (lane & 1) * (lane & 2 ? kBlock * L::kScaleBytes : kBlock * L::kBytes) +
-                              bulk_half * bulk_bytes;
+  int slots[2] = {0, 0};
+  // RUNS: what changes with the request and with the head alone is kept from block to block:
+  // the request's row of the table; this lane's places in the head's codes of K and V, and
+  // in the scales, lanes 0 .. K's, as many after them V's
+  constexpr int kScaleLanes = kBlock * L::kScaleBytes / 16;
+  const int32_t* table = nullptr;
+  const uint8_t *k_head = nullptr, *v_head = nullptr, *s_head = nullptr;
+  int at_b = -1, at_head = -1;
+  const Rows scale_rows = a.c.scale[lane / kScaleLanes % 2];
   auto look = [&]() {
     if (!c.more) return;
-    const int32_t* table = a.b.pages + (int64_t)c.b * a.b.pages_stride;
-    const int pos = c.t * kBlock + (BULK ? 16 * bulk_half : even ? 0 : lane), last = c.start + c.rows - 1;
-    page[0] = (uint32_t)__ldg(table + a.c.page.div(min(pos, last)));
-    if (!BULK && even) page[1] = (uint32_t)__ldg(table + a.c.page.div(min(pos + 16, last)));
+    if (RUNS) {
+      if (c.b != at_b) {
+        at_b = c.b;
+        table = a.b.pages + (int64_t)c.b * a.b.pages_stride;
+      }
+      const int pos = c.t * kBlock, i = a.c.page.div(pos);
+      slots[0] = pos - i * a.c.page.d;
+      page[0] = (uint32_t)__ldg(table + i);
+      if (in_two) {                              // its second half may lie past the end
+        const int pos1 = pos + 16, j = a.c.page.div(pos1);
+        slots[1] = pos1 - j * a.c.page.d;
+        page[1] = (uint32_t)__ldg(table + (pos1 < c.start + c.rows ? j : i));
+      }
+      return;
+    }
+    const int32_t* row = a.b.pages + (int64_t)c.b * a.b.pages_stride;
+    const int pos = c.t * kBlock + (even ? 0 : lane), last = c.start + c.rows - 1;
+    page[0] = (uint32_t)__ldg(row + a.c.page.div(min(pos, last)));
+    if (even) page[1] = (uint32_t)__ldg(row + a.c.page.div(min(pos + 16, last)));
   };
   look();
   // this lane's place in a copy: its row of the rows at once, and its chunk
@@ -342,19 +321,47 @@ __global__ void __launch_bounds__(Few4<DP, NT, GROUP, BULK>::kThreads, 1)
   int stage_in = 0;
   uint2 k_scale = make_uint2(0u, 0u), v_scale = make_uint2(0u, 0u);   // of key `lane` in the block in flight
   auto issue = [&]() {
-    if (BULK) {
+    if (RUNS) {
       if (c.more) {
+        constexpr int kCodes = kBlock * L::kBytes, kHalfRun = kCodes / 2;
+        if (c.head != at_head) {
+          at_head = c.head;
+          k_head = a.c.x[0].of_head(at_head) + lane * 16;
+          v_head = a.c.x[1].of_head(at_head) + lane * 16;
+          s_head = scale_rows.of_head(at_head) + lane % kScaleLanes * 16;
+        }
         worst = max(worst, page[0]);             // a bad page is reported at the end
-        if (lane == 0) ptx::mbar_expect_tx(&pipe.full[cta_warp][stage_in], L::kStage);
-        __syncwarp();
-        const int pos = c.t * kBlock + 16 * bulk_half, slot = pos - a.c.page.div(pos) * a.c.page.d;
-        if (bulk_lane && !*(const volatile int*)&pipe.abort)
-          ptx::bulk_g2s(ring + stage_in * L::kStage + bulk_place,
-                        bulk_rows.at(min(page[0], top_page), slot, c.head), bulk_bytes,
-                        &pipe.full[cta_warp][stage_in]);
+        const uint32_t pg = min(page[0], top_page);
+        uint8_t* dst = ring + stage_in * L::kStage + lane * 16;
+        const uint8_t* k = k_head + a.c.x[0].offset(pg, 0) + slots[0] * L::kBytes;
+        const uint8_t* v = v_head + a.c.x[1].offset(pg, 0) + slots[0] * L::kBytes;
+        if (!in_two) {
+#pragma unroll
+          for (int i = 0; i < kCodes; i += 512) ptx::cp_async16(dst + i, k + i);
+#pragma unroll
+          for (int i = 0; i < kCodes; i += 512) ptx::cp_async16(dst + kCodes + i, v + i);
+          if (lane < 2 * kScaleLanes)
+            ptx::cp_async16(dst + L::kScales, s_head + scale_rows.offset(pg, 0) + slots[0] * L::kScaleBytes);
+        } else {
+          worst = max(worst, page[1]);
+          const uint32_t pg1 = min(page[1], top_page);
+          const uint8_t* k1 = k_head + a.c.x[0].offset(pg1, 0) + slots[1] * L::kBytes - kHalfRun;
+          const uint8_t* v1 = v_head + a.c.x[1].offset(pg1, 0) + slots[1] * L::kBytes - kHalfRun;
+#pragma unroll
+          for (int i = 0; i < kCodes; i += 512) {
+            ptx::cp_async16(dst + i, (i < kHalfRun ? k : k1) + i);
+            ptx::cp_async16(dst + kCodes + i, (i < kHalfRun ? v : v1) + i);
+          }
+          const bool first = lane % kScaleLanes < kScaleLanes / 2;
+          if (lane < 2 * kScaleLanes)
+            ptx::cp_async16(dst + L::kScales,
+                            s_head + scale_rows.offset(first ? pg : pg1, 0) +
+                                (first ? slots[0] : slots[1] - 16) * L::kScaleBytes);
+        }
         c.next(a, warp, GROUP);
         look();
       }
+      ptx::cp_async_commit();
       stage_in ^= 1;
       return;
     }
@@ -460,17 +467,18 @@ __global__ void __launch_bounds__(Few4<DP, NT, GROUP, BULK>::kThreads, 1)
 
   // ---- the products' side
   int stage = 0, cur = 0;
-  uint32_t phase = 0;
   while (st.live[cur]) {
     const Segment& s = segments[cur];
     const int rows = Item::group_rows(a, s), t1 = s.t1, start = s.start;
     // O^T: tile t of row tile nt has columns (DP / 8) g + 2 t, + 1 of rows 8 nt + 2q, + 1
-    float o[NT][kTiles][4], mref[NT][2], l[NT][2], row_mul[NT][2];
+    // limit: what an exponent has to pass to move m; sub: m, or 0 before the first visible key
+    float o[NT][kTiles][4], mref[NT][2], l[NT][2], row_mul[NT][2], limit[NT][2], sub[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        mref[nt][e] = -INFINITY;
+        mref[nt][e] = limit[nt][e] = -INFINITY;
+        sub[nt][e] = 0.f;
         l[nt][e] = 0.f;
         row_mul[nt][e] = st.row_mul[8 * nt + 2 * q + e];
       }
@@ -487,9 +495,10 @@ __global__ void __launch_bounds__(Few4<DP, NT, GROUP, BULK>::kThreads, 1)
       const bool masked = pos0 + kBlock > start;
       const uint8_t* src = ring + stage * L::kStage;
       __syncwarp();                              // the block before has been read
-      if (BULK) {
+      if (RUNS) {
         issue();
-        wait(&pipe, &pipe.full[cta_warp][stage], phase, a.status);
+        ptx::cp_async_wait_group<1>();
+        __syncwarp();
         const uint8_t* raw = src + L::kScales + lane * L::kScaleBytes;
         if (DP == 128) {
           k_scale = *reinterpret_cast<const uint2*>(raw);
@@ -515,7 +524,7 @@ __global__ void __launch_bounds__(Few4<DP, NT, GROUP, BULK>::kThreads, 1)
         to[lane] = spread_scales<DP>(k_scale);
         to[32 + lane] = spread_scales<DP>(vs);
       }
-      if (!BULK) {
+      if (!RUNS) {
         issue();
         ptx::cp_async_wait_group<1>();
       }
@@ -600,7 +609,7 @@ __global__ void __launch_bounds__(Few4<DP, NT, GROUP, BULK>::kThreads, 1)
           // a visible score of -infinity is the cap's negative, an invisible one nothing
           if (CAP && see[nt][e] != 0) y = capped(sc, y, 0.f);
           mx[nt][e] = y;
-          over |= y > mref[nt][e] + (mref[nt][e] == -INFINITY ? 0.f : kShift + 8.f);
+          over |= y > limit[nt][e];
         }
       // the first visible key sets a row's m, later ones when the maximum has grown enough
       if (__any_sync(0xffffffffu, over)) {
@@ -612,8 +621,9 @@ __global__ void __launch_bounds__(Few4<DP, NT, GROUP, BULK>::kThreads, 1)
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, off));
             const float old = mref[nt][e];
-            if (y > old + (old == -INFINITY ? 0.f : kShift + 8.f)) {
-              mref[nt][e] = y - kShift;
+            if (y > limit[nt][e]) {
+              mref[nt][e] = sub[nt][e] = y - kShift;
+              limit[nt][e] = y + 8.f;
               const float back = old == -INFINITY ? 0.f : ex2(old - mref[nt][e]);
               l[nt][e] *= back;
 #pragma unroll
@@ -631,22 +641,21 @@ __global__ void __launch_bounds__(Few4<DP, NT, GROUP, BULK>::kThreads, 1)
         float w[kParts][2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float sub = mref[nt][e] == -INFINITY ? 0.f : mref[nt][e];
           if (!CAP) {
 #pragma unroll
-            for (int i = 0; i < kParts; ++i) w[i][e] = fmaf(x[nt][i][e], row_mul[nt][e], -sub);
+            for (int i = 0; i < kParts; ++i) w[i][e] = fmaf(x[nt][i][e], row_mul[nt][e], -sub[nt][e]);
           } else {
             float raw[kParts], big = 0.f;
 #pragma unroll
             for (int i = 0; i < kParts; ++i) {
               raw[i] = x[nt][i][e] * row_mul[nt][e];
               big = fmaxf(big, fabsf(raw[i]));
-              w[i][e] = capped_near(sc, raw[i], sub);
+              w[i][e] = capped_near(sc, raw[i], sub[nt][e]);
             }
             if (__any_sync(0xffffffffu, past_near(sc, big))) {
 #pragma unroll
               for (int i = 0; i < kParts; ++i) {
-                const float past = capped_past(sc, raw[i], sub);
+                const float past = capped_past(sc, raw[i], sub[nt][e]);
                 if (past_near(sc, raw[i])) w[i][e] = past;
               }
             }
@@ -707,7 +716,6 @@ __global__ void __launch_bounds__(Few4<DP, NT, GROUP, BULK>::kThreads, 1)
         }
       }
       stage ^= 1;
-      if (stage == 0) phase ^= 1;
     }
 
     // the warps meet: O, m and l of the segment
@@ -818,21 +826,13 @@ __global__ void __launch_bounds__(Few4<DP, NT, GROUP, BULK>::kThreads, 1)
     meet<GROUP>(worker);
     cur ^= 1;
   }
+  ptx::cp_async_wait_group<0>();
   if (worst > top_page) set_status(a.status, DSPARK_EPAGES);
-  if (BULK) {
-    __syncthreads();
-    if (*(const volatile int*)&pipe.abort) {     // let what was started land
-      const uint64_t t0 = globaltimer_ns();
-      while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
-    }
-  } else {
-    ptx::cp_async_wait_group<0>();
-  }
 }
 
-template <int DP, int NT, int GROUP, bool BULK, bool CAP>
+template <int DP, int NT, int GROUP, bool RUNS, bool CAP>
 cudaError_t launch(AttendArgs a, cudaStream_t stream) {
-  using L = Few4<DP, NT, GROUP, BULK>;
+  using L = Few4<DP, NT, GROUP, RUNS>;
   // launched while the kernel before it in the stream ends, which it waits for before
   // anything else
   cudaLaunchAttribute attr{};
@@ -846,16 +846,16 @@ cudaError_t launch(AttendArgs a, cudaStream_t stream) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   a.n_cta *= L::kWorkers;
-  return cudaLaunchKernelEx(&cfg, few4_kernel<DP, NT, GROUP, BULK, CAP>, a);
+  return cudaLaunchKernelEx(&cfg, few4_kernel<DP, NT, GROUP, RUNS, CAP>, a);
 }
 
-template <int DP, int NT, int GROUP, bool BULK, bool CAP>
+template <int DP, int NT, int GROUP, bool RUNS, bool CAP>
 cudaError_t setup() {
-  using L = Few4<DP, NT, GROUP, BULK>;
+  using L = Few4<DP, NT, GROUP, RUNS>;
   static_assert(L::kSmem + L::kWorkers * (sizeof(WorkerState<GROUP>) + 300) + 1024 <= 232448,
                 "shared memory of an SM");
   static_assert(L::kWorkers <= kFew4Workers && 2 * L::kWorkers * L::kRows <= kFew4PartRows, "the parts' place");
-  return cudaFuncSetAttribute(few4_kernel<DP, NT, GROUP, BULK, CAP>,
+  return cudaFuncSetAttribute(few4_kernel<DP, NT, GROUP, RUNS, CAP>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
 }
 

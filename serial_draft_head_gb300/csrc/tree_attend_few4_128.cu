@@ -18,9 +18,9 @@ cudaError_t few4_setup128() {
   return e;
 }
 
-cudaError_t few4_launch128(const AttendArgs& a, bool two, bool alone, bool bulk, cudaStream_t stream) {
+cudaError_t few4_launch128(const AttendArgs& a, bool two, bool alone, bool runs, cudaStream_t stream) {
   const bool cap = a.softcap > 0.f;
-  if (!bulk) {
+  if (!runs) {
     if (two) return cap ? launch<128, 2, 12, false, true>(a, stream) : launch<128, 2, 12, false, false>(a, stream);
     return cap ? launch<128, 1, 16, false, true>(a, stream) : launch<128, 1, 16, false, false>(a, stream);
   }
