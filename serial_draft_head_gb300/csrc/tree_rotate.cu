@@ -4,8 +4,10 @@
 // A row (one token, one head) is handled by D / 16 lanes, rounded up to 4 or 8, 16
 // elements each: for rotation by halves an 8-element chunk of the first half and the one
 // that it turns with, so that a pair is in one thread and only the norm's sum crosses
-// lanes.  A block has 1, 2 or 4 tokens; sines and cosines of a token are worked out once,
-// one a thread, and kept in registers over its heads.
+// lanes.  A warp has a token (or, so that few tokens fill the device, a share of its
+// heads): it works out the token's sines and cosines, one a lane, keeps them, times the
+// norm's weights, in registers, and goes through the heads with two rows' loads in flight.
+// Nothing is handed between warps.
 //
 // Angles: a frequency is held in turns a position, as a 64-bit fraction, so that position
 // times frequency modulo one turn is one integer product, exact at any position; its
@@ -21,114 +23,148 @@ namespace tree {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTok = 4;         // tokens of a block
+constexpr int kWarps = kThreads / 32;
+constexpr int kDepth = 5;          // rounds of a warp's loads in flight, a KB each
 
-// PLACE: k and v go to the cache, as HELD says; else k to out_k and there is no v.
+// PLACE: k and v go to the cache, as HELD says; else k to out_k and there is no v.  `split`
+// warps a token.
 template <bool F16, bool PLACE, Held HELD, int LANES>
-__global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant__ RotateArgs a, int tok) {
-  __shared__ float2 turn[kMaxTok][LANES][9];       // [token][lane][of its pairs], a column spare
-  constexpr int kGroups = kThreads / LANES;        // rows at a time
-  const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
-  const int per = kGroups / tok;                   // groups of a token
-  const int t = group / per, n = blockIdx.x * tok + t;
+__global__ void __launch_bounds__(kThreads, 3) rotate_kernel(const __grid_constant__ RotateArgs a, int split) {
+  __shared__ float2 turns[kWarps][8 * LANES];      // {cosine, sine} of the token's pairs
+  __shared__ uint4 rows_in[kWarps][kDepth][2][32]; // each lane the chunks that it copied itself
+  constexpr int kGroups = 32 / LANES;              // rows at a time
+  const int warp = threadIdx.x / 32, wl = threadIdx.x % 32, lane = wl % LANES, group = wl / LANES;
+  const int64_t job = (int64_t)blockIdx.x * kWarps + warp;
+  const int n = (int)(job / split), share = (int)(job - (int64_t)n * split);
+  if (n >= a.N) return;
+  int64_t page = 0;
+  int place = 0;
+  if (PLACE) {
+    const int slot = __ldg(a.slot + n);
+    if (slot < 0 || slot >= a.slots) {             // left out
+      if (slot >= 0 && wl == 0) set_status(a.status, DSPARK_EPAGES);
+      return;
+    }
+    page = a.c.page.div(slot);
+    place = slot - (int)page * a.c.page.d;
+  }
   const int half = a.R / 16;                       // chunks of half a turned part
   const bool in_row = lane * 16 < a.D, turned = lane < half;
   // the lane's two chunks
   const int c0 = turned ? (a.pairs ? 2 * lane : lane) : 2 * lane;
   const int c1 = turned && !a.pairs ? lane + half : c0 + 1;
-  int slot = 0;
-  bool on = n < a.N;
-  if (PLACE && on) {
-    slot = a.slot[n];
-    on = slot >= 0 && slot < a.slots;
-    if (slot >= a.slots && lane == 0) set_status(a.status, DSPARK_EPAGES);
-  }
-  const int heads = a.Hq + a.Hkv * (PLACE ? 2 : 1);
-  uint4 x[2], next[2];
+  const int heads = a.Hq + a.Hkv * (PLACE ? 2 : 1), step = split * kGroups;
+  uint4 x[2];
+  int in = 0;
   auto load = [&](int h) {
-    next[0] = next[1] = make_uint4(0, 0, 0, 0);
-    if (!on || !in_row || h >= heads) return;
-    const int i = h < a.Hq ? 0 : h < a.Hq + a.Hkv ? 1 : 2;
-    const int head = h - (i == 0 ? 0 : i == 1 ? a.Hq : a.Hq + a.Hkv);
-    const uint4* src = reinterpret_cast<const uint4*>(a.src[i] + (int64_t)n * a.src_row[i] +
-                                                      head * a.src_head[i]);
-    next[0] = __ldg(src + (i == 2 ? 2 * lane : c0));
-    next[1] = __ldg(src + (i == 2 ? 2 * lane + 1 : c1));
+    if (in_row && h < heads) {
+      const int i = h < a.Hq ? 0 : h < a.Hq + a.Hkv ? 1 : 2;
+      const int head = h - (i == 0 ? 0 : i == 1 ? a.Hq : a.Hq + a.Hkv);
+      const uint4* src = reinterpret_cast<const uint4*>(a.src[i] + (int64_t)n * a.src_row[i] +
+                                                        head * a.src_head[i]);
+      ptx::cp_async16(&rows_in[warp][in][0][wl], src + (i == 2 ? 2 * lane : c0));
+      ptx::cp_async16(&rows_in[warp][in][1][wl], src + (i == 2 ? 2 * lane + 1 : c1));
+    }
+    ptx::cp_async_commit();
+    if (++in == kDepth) in = 0;
   };
-  load(group % per);
-  // sines and cosines of the block's tokens, pair i of a token for lane i / 8
-  for (int i = threadIdx.x; i < tok * (a.R / 2); i += kThreads) {
-    const int tt = i / (a.R / 2), f = i - tt * (a.R / 2), row = blockIdx.x * tok + tt;
-    const int64_t pos = row < a.N ? a.position[row] : 0;
+#pragma unroll
+  for (int i = 0; i < kDepth - 1; ++i) load(share * kGroups + group + i * step);
+  const int64_t pos = __ldg(a.position + n);
+  for (int f = wl; f < a.R / 2; f += 32) {
     const int32_t part = (int32_t)((uint64_t)pos * __ldg(a.turns + f) >> 32);
     float s, c;
     sincospif((float)part * 0x1p-31f, &s, &c);
-    turn[tt][f / 8][f % 8] = make_float2(c, s);
+    // pair f is pair f % 8 of lane f / 8
+    turns[warp][f % 8 * LANES + f / 8] = make_float2(c, s);
   }
-  __syncthreads();
-  float2 cs[8];
+  __syncwarp();
+  // a pair (u, z) becomes r (u k0 - z k1), r (z k2 + u k3), r the norm's factor; a pair that
+  // is not turned r u k0, r z k2
+  float k0[8], k1[8], k2[8], k3[8];
+  bool of_k = true;                                // whose weights these are: none yet
+  auto weigh = [&](bool key) {
+    of_k = key;
+    const float* norm = key ? a.k_norm : a.q_norm;
+    float w0[8], w1[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) cs[k] = turned ? turn[t][lane][k] : make_float2(0.f, 0.f);
-  int64_t page = 0;
-  int place = 0;
-  if (PLACE && on) {
-    page = a.c.page.div(slot);
-    place = slot - (int)page * a.c.page.d;
-  }
+    for (int k = 0; k < 8; ++k) w0[k] = w1[k] = 1.f;
+    if (norm && in_row) {
+      const float4* g = reinterpret_cast<const float4*>(norm);
+      const float4 y[4] = {__ldg(g + 2 * c0), __ldg(g + 2 * c0 + 1), __ldg(g + 2 * c1), __ldg(g + 2 * c1 + 1)};
+      const float e[16] = {y[0].x, y[0].y, y[0].z, y[0].w, y[1].x, y[1].y, y[1].z, y[1].w,
+                           y[2].x, y[2].y, y[2].z, y[2].w, y[3].x, y[3].y, y[3].z, y[3].w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        w0[k] = a.pairs ? e[2 * k] : e[k];
+        w1[k] = a.pairs ? e[2 * k + 1] : e[8 + k];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float2 t = turned ? turns[warp][k * LANES + lane] : make_float2(1.f, 0.f);
+      k0[k] = w0[k] * t.x;
+      k1[k] = w1[k] * t.y;
+      k2[k] = w1[k] * t.x;
+      k3[k] = w0[k] * t.y;
+    }
+  };
+  weigh(false);
 #pragma unroll 1
-  for (int h0 = 0; h0 < heads; h0 += per) {        // whole warps stay in the loop: the shuffles
-    const int h = h0 + group % per;
-    x[0] = next[0];
-    x[1] = next[1];
-    load(h + per);
-    const bool q = h < a.Hq, v = PLACE && h >= a.Hq + a.Hkv, live = on && h < heads;
+  for (int h0 = share * kGroups; h0 < heads; h0 += step) {   // whole warps stay in: the shuffles
+    const int h = h0 + group;
+    load(h + (kDepth - 1) * step);
+    ptx::cp_async_wait_group<kDepth - 1>();
+    const int out = in;                            // the oldest
+    x[0] = x[1] = make_uint4(0, 0, 0, 0);
+    if (in_row && h < heads) {
+      x[0] = rows_in[warp][out][0][wl];
+      x[1] = rows_in[warp][out][1][wl];
+    }
+    const bool q = h < a.Hq, v = PLACE && h >= a.Hq + a.Hkv, live = h < heads;
     const int head = q ? h : v ? h - a.Hq - a.Hkv : h - a.Hq;
     uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
     if (!__all_sync(0xffffffffu, v)) {
-      float y[16];
+      // the warp's rows are of q, of k, or of both: then each half in turn
+      const bool some_q = __any_sync(0xffffffffu, q), some_k = __any_sync(0xffffffffu, !q && !v);
+      float u[8], z[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        y[2 * k] = to_float<F16>((uint16_t)w[k]);
-        y[2 * k + 1] = to_float<F16>((uint16_t)(w[k] >> 16));
-      }
-      const float* norm = q ? a.q_norm : a.k_norm;
-      float sum = 0.f;
-#pragma unroll
-      for (int k = 0; k < 16; ++k) sum = fmaf(y[k], y[k], sum);
-#pragma unroll
-      for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (norm && in_row) {
-        const float r = rsqrtf(sum * a.inv_dim + a.eps);
-        const float4* g0 = reinterpret_cast<const float4*>(norm) + 2 * c0;
-        const float4* g1 = reinterpret_cast<const float4*>(norm) + 2 * c1;
-        const float4 g[4] = {__ldg(g0), __ldg(g0 + 1), __ldg(g1), __ldg(g1 + 1)};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          y[4 * k] *= r * g[k].x;
-          y[4 * k + 1] *= r * g[k].y;
-          y[4 * k + 2] *= r * g[k].z;
-          y[4 * k + 3] *= r * g[k].w;
+        const float lo = to_float<F16>((uint16_t)w[k]), hi = to_float<F16>((uint16_t)(w[k] >> 16));
+        if (a.pairs) {
+          u[k] = lo;
+          z[k] = hi;
+        } else {
+          (k < 4 ? u : z)[2 * (k % 4)] = lo;
+          (k < 4 ? u : z)[2 * (k % 4) + 1] = hi;
         }
       }
-      if (!turned) {
-      } else if (a.pairs) {
+      float r = 1.f;
+      if (a.q_norm || a.k_norm) {
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum = fmaf(u[k], u[k], fmaf(z[k], z[k], sum));
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (q ? a.q_norm != nullptr : a.k_norm != nullptr) r = rsqrtf(sum * a.inv_dim + a.eps);
+      }
+#pragma unroll 1
+      for (int side = 0; side < 2; ++side) {
+        if (!(side ? some_k : some_q)) continue;
+        if (of_k != (side == 1)) weigh(side == 1);
+        if (v || q == (side == 1)) continue;
+        float y0[8], y1[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const float u = y[2 * k], z = y[2 * k + 1];
-          y[2 * k] = fmaf(u, cs[k].x, -z * cs[k].y);
-          y[2 * k + 1] = fmaf(z, cs[k].x, u * cs[k].y);
+          y0[k] = turned ? r * fmaf(u[k], k0[k], -z[k] * k1[k]) : r * (u[k] * k0[k]);
+          y1[k] = turned ? r * fmaf(z[k], k2[k], u[k] * k3[k]) : r * (z[k] * k2[k]);
         }
-      } else {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const float u = y[k], z = y[8 + k];
-          y[k] = fmaf(u, cs[k].x, -z * cs[k].y);
-          y[8 + k] = fmaf(z, cs[k].x, u * cs[k].y);
+          const int j = 2 * (k % 4);
+          w[k] = a.pairs ? pack2<F16>(y0[k], y1[k])
+                         : k < 4 ? pack2<F16>(y0[j], y0[j + 1]) : pack2<F16>(y1[j], y1[j + 1]);
         }
-      }
-      if (!v) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] = pack2<F16>(y[2 * k], y[2 * k + 1]);
       }
     }
     const bool cached = PLACE && !q;
@@ -170,10 +206,13 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant_
 
 template <bool F16, bool PLACE, Held HELD, int LANES>
 void launch(const RotateArgs& a, int sm_count, cudaStream_t stream) {
-  // four tokens a block share what a block costs, unless that leaves SMs without one
-  int tok = kMaxTok;
-  while (tok > 1 && (a.N - 1) / tok + 1 < 2 * sm_count) tok >>= 1;
-  rotate_kernel<F16, PLACE, HELD, LANES><<<(a.N - 1) / tok + 1, kThreads, 0, stream>>>(a, tok);
+  // a token's heads over as many warps as give every SM 16, at least two rounds each
+  const int heads = a.Hq + a.Hkv * (PLACE ? 2 : 1), rounds = (heads + 32 / LANES - 1) / (32 / LANES);
+  int split = 1;
+  while (2 * split <= rounds && (int64_t)a.N * split < (int64_t)16 * sm_count) split *= 2;
+  const int64_t jobs = (int64_t)a.N * split;
+  rotate_kernel<F16, PLACE, HELD, LANES>
+      <<<(unsigned)((jobs + kWarps - 1) / kWarps), kThreads, 0, stream>>>(a, split);
 }
 
 template <bool F16, bool PLACE, Held HELD>
