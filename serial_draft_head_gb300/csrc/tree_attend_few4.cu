@@ -1,42 +1,35 @@
-// tree_attend_few4.cu -- tree_attend_few4.cuh for heads of up to 64 elements, and the choice among
-// its forms.
+// tree_attend_few4.cu -- the choice among the forms of tree_attend_few4.cuh.
 #include "tree_attend_few4.cuh"
 
 namespace dspark {
 namespace tree {
 
-cudaError_t few4_setup128();
-cudaError_t few4_launch128(const AttendArgs& a, bool two, bool alone, bool runs, cudaStream_t stream);
+template <>
+cudaError_t few4_setup_of<64, 1>();
+template <>
+cudaError_t few4_setup_of<64, 2>();
+template <>
+cudaError_t few4_setup_of<64, 4>();
+template <>
+cudaError_t few4_setup_of<128, 1>();
+template <>
+cudaError_t few4_setup_of<128, 2>();
+template <>
+cudaError_t few4_setup_of<128, 4>();
+template <>
+cudaError_t few4_launch_of<64, 1>(const AttendArgs& a, bool alone, bool runs, cudaStream_t stream);
+template <>
+cudaError_t few4_launch_of<64, 2>(const AttendArgs& a, bool alone, bool runs, cudaStream_t stream);
+template <>
+cudaError_t few4_launch_of<64, 4>(const AttendArgs& a, bool alone, bool runs, cudaStream_t stream);
+template <>
+cudaError_t few4_launch_of<128, 1>(const AttendArgs& a, bool alone, bool runs, cudaStream_t stream);
+template <>
+cudaError_t few4_launch_of<128, 2>(const AttendArgs& a, bool alone, bool runs, cudaStream_t stream);
+template <>
+cudaError_t few4_launch_of<128, 4>(const AttendArgs& a, bool alone, bool runs, cudaStream_t stream);
 
 namespace {
-
-cudaError_t setup64() {
-  cudaError_t e = setup<64, 1, 16, false, false>();
-  if (e == cudaSuccess) e = setup<64, 1, 16, false, true>();
-  if (e == cudaSuccess) e = setup<64, 1, 16, true, false>();
-  if (e == cudaSuccess) e = setup<64, 1, 16, true, true>();
-  if (e == cudaSuccess) e = setup<64, 1, 4, true, false>();
-  if (e == cudaSuccess) e = setup<64, 2, 12, false, false>();
-  if (e == cudaSuccess) e = setup<64, 2, 12, false, true>();
-  if (e == cudaSuccess) e = setup<64, 2, 12, true, false>();
-  if (e == cudaSuccess) e = setup<64, 2, 12, true, true>();
-  if (e == cudaSuccess) e = setup<64, 2, 4, true, false>();
-  return e;
-}
-
-cudaError_t launch64(const AttendArgs& a, bool two, bool alone, bool runs, cudaStream_t stream) {
-  const bool cap = a.softcap > 0.f;
-  if (!runs) {
-    if (two) return cap ? launch<64, 2, 12, false, true>(a, stream) : launch<64, 2, 12, false, false>(a, stream);
-    return cap ? launch<64, 1, 16, false, true>(a, stream) : launch<64, 1, 16, false, false>(a, stream);
-  }
-  if (two) {
-    if (cap) return launch<64, 2, 12, true, true>(a, stream);
-    return alone ? launch<64, 2, 12, true, false>(a, stream) : launch<64, 2, 4, true, false>(a, stream);
-  }
-  if (cap) return launch<64, 1, 16, true, true>(a, stream);
-  return alone ? launch<64, 1, 16, true, false>(a, stream) : launch<64, 1, 4, true, false>(a, stream);
-}
 
 // Whether a page holds each head's slots, and their scales, next to each other, in pieces
 // that 16-byte copies take.
@@ -50,21 +43,37 @@ bool in_runs(const AttendArgs& a) {
   return true;
 }
 
+template <int DP>
+cudaError_t setup_for() {
+  cudaError_t e = few4_setup_of<DP, 1>();
+  if (e == cudaSuccess) e = few4_setup_of<DP, 2>();
+  if (e == cudaSuccess) e = few4_setup_of<DP, 4>();
+  return e;
+}
+
+template <int DP>
+cudaError_t launch_for(const AttendArgs& a, int tiles, bool alone, bool runs, cudaStream_t stream) {
+  if (tiles == 1) return few4_launch_of<DP, 1>(a, alone, runs, stream);
+  return tiles == 2 ? few4_launch_of<DP, 2>(a, alone, runs, stream)
+                    : few4_launch_of<DP, 4>(a, alone, runs, stream);
+}
+
 }  // namespace
 
-cudaError_t few4_setup(int D) { return padded_dim(D) == 64 ? setup64() : few4_setup128(); }
+cudaError_t few4_setup(int D) { return padded_dim(D) == 64 ? setup_for<64>() : setup_for<128>(); }
 
 cudaError_t few4_launch(const AttendArgs& a, cudaStream_t stream) {
-  // one tile of eight rows an item where the requests have no more on average
-  const bool two = (int64_t)a.b.N * a.G > (int64_t)8 * a.b.B;
+  // rows of an item: what the requests have on average, in whole tiles of eight
+  const int64_t rows = (int64_t)a.b.N * a.G;
+  const int tiles = rows <= (int64_t)8 * a.b.B ? 1 : rows <= (int64_t)16 * a.b.B ? 2 : 4;
   // workers of four warps where there are two items a SM (64 heads on 8, 500 to 9,000
   // tokens, us with four / with a CTA's: 48 requests 76 / 93, 128 167 / 207; 16 requests 38 /
   // 39, 1 of 5,000 27 / 16, 19 of 32,767 156 / 144)
-  const int64_t items = ((int64_t)a.b.N * a.G + 7) / 8 * a.Hkv;
+  const int64_t items = (rows + 8 * tiles - 1) / (8 * tiles) * a.Hkv;
   const bool alone = items < (int64_t)2 * a.n_cta;
   const bool runs = in_runs(a);
-  return padded_dim(a.D) == 64 ? launch64(a, two, alone, runs, stream)
-                               : few4_launch128(a, two, alone, runs, stream);
+  return padded_dim(a.D) == 64 ? launch_for<64>(a, tiles, alone, runs, stream)
+                               : launch_for<128>(a, tiles, alone, runs, stream);
 }
 
 }  // namespace tree

@@ -1,7 +1,7 @@
 // tree_attend_few4.cuh -- attention of few drafted rows (single tokens, short chains:
 // dspark_tree_attend has the rule) over a paged cache in 4 bits.
 //
-// Items are 8 or 16 rows by blocks of 32 keys, a worker is a group of warps, four or a
+// Items are 8, 16 or 32 rows by blocks of 32 keys, a worker is a group of warps, four or a
 // CTA's (tree_items.cuh says how the work is cut, and the mathematics).  The warps of a
 // group take a segment's blocks in turn, each with its own O, m and l, and meet at its
 // end; with four to a group the others of the SM go on meanwhile.
@@ -52,7 +52,7 @@ struct Few4 {
   // units an item counts beside its blocks, for Q, the first copies and the warps'
   // meeting
   static constexpr int kExtra = GROUP == 4 ? 10 : 20;
-  static constexpr int kWarps = NT == 1 ? 16 : 12;       // that compute
+  static constexpr int kWarps = NT == 1 ? 16 : NT == 2 ? 12 : 8;   // as many as registers allow
   static constexpr int kWorkers = kWarps / GROUP;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kBytes = DP / 2;                  // of a row of codes
@@ -78,11 +78,11 @@ struct Few4 {
   using Item = Work<kBlock, kRows, kExtra>;
 };
 
-template <int GROUP>
+template <int GROUP, int ROWS>
 struct WorkerState {
-  float2 ml[GROUP][16];                 // [warp][row]
-  float2 fin[16];                       // a row's m of all warps, and 1 / l (l = 0: 0)
-  float row_mul[16];                    // a row's factor on the raw scores
+  float2 ml[GROUP][ROWS];               // [warp][row]
+  float2 fin[ROWS];                     // a row's m of all warps, and 1 / l (l = 0: 0)
+  float2 row_mul[ROWS / 2];             // two rows' factors on the raw scores
   uint32_t bad[DSPARK_TREE_MAX_NODES / 32];
   int live[2];                          // there is a segment; the next one
   int join;                             // an item to join: first worker | parts << 16
@@ -177,7 +177,7 @@ __device__ __noinline__ void add_nan(const AttendArgs& a, const uint32_t* bad,
 // result does not depend on which came last.  As many parts at a time as the merge's place
 // has weights for.
 template <class L, int GROUP>
-__device__ __noinline__ void join_parts(const AttendArgs& a, WorkerState<GROUP>& st, float* weight,
+__device__ __noinline__ void join_parts(const AttendArgs& a, WorkerState<GROUP, L::kRows>& st, float* weight,
                                         int worker, int first, int parts, int row0, int head, int group,
                                         int rows) {
   constexpr int kRows = L::kRows, DP = L::kHalf * 2, kThreads = GROUP * 32;
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(Few4<DP, NT, GROUP, RUNS>::kThreads, 1)
   constexpr int kWorkerThreads = GROUP * 32;
   constexpr float kShift = 7.f;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ WorkerState<GROUP> states[L::kWorkers];
+  __shared__ WorkerState<GROUP, L::kRows> states[L::kWorkers];
   __shared__ Share shares[L::kWorkers];
   __shared__ int64_t sums[L::kThreads / 32];
   __shared__ typename Item::Walker walkers[L::kWorkers];
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(Few4<DP, NT, GROUP, RUNS>::kThreads, 1)
   const int worker = cta_warp / GROUP, warp = cta_warp % GROUP;
   const int tid = threadIdx.x % kWorkerThreads;  // in the worker
   const int gk = row_key(g);
-  WorkerState<GROUP>& st = states[worker];
+  WorkerState<GROUP, L::kRows>& st = states[worker];
   uint8_t* ring = smem + cta_warp * L::kRing;
   uint4* q_mem = reinterpret_cast<uint4*>(smem + L::kQ + worker * L::kQBytes);
   const uint32_t scale_mem = ptx::smem_u32(ring + L::kScale) +
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(Few4<DP, NT, GROUP, RUNS>::kThreads, 1)
       r = __uint_as_float((uint32_t)(127 + up) << 23);
       row_mul *= __uint_as_float((uint32_t)(127 - up) << 23);
     }
-    if (q == 0) st.row_mul[8 * warp + g] = row_mul;
+    if (q == 0) reinterpret_cast<float*>(st.row_mul)[8 * warp + g] = row_mul;
 #pragma unroll
     for (int j = 0; j < kQChunks; ++j) {
       uint32_t w[4] = {qx[j].x ^ flip, qx[j].y ^ flip, qx[j].z ^ flip, qx[j].w ^ flip};
@@ -471,16 +471,34 @@ __global__ void __launch_bounds__(Few4<DP, NT, GROUP, RUNS>::kThreads, 1)
     const Segment& s = segments[cur];
     const int rows = Item::group_rows(a, s), t1 = s.t1, start = s.start;
     // O^T: tile t of row tile nt has columns (DP / 8) g + 2 t, + 1 of rows 8 nt + 2q, + 1
-    // limit: what an exponent has to pass to move m; sub: m, or 0 before the first visible key
-    float o[NT][kTiles][4], mref[NT][2], l[NT][2], row_mul[NT][2], limit[NT][2], sub[NT][2];
+    float o[NT][kTiles][4], mref[NT][2], l[NT][2];
+    // kept in registers where there are some left, else worked out each time: a row's
+    // factor, what an exponent has to pass to move m, and m, or 0 before the first visible key
+    constexpr int kKept = NT <= 2 ? NT : 1;
+    float kept_mul[kKept][2], kept_limit[kKept][2], kept_sub[kKept][2];
+    auto row_mul = [&](int nt, int e) {
+      if (NT <= 2) return kept_mul[nt % kKept][e];
+      const float2 y = st.row_mul[4 * nt + q];
+      return e ? y.y : y.x;
+    };
+    auto limit = [&](int nt, int e) {
+      return NT <= 2 ? kept_limit[nt % kKept][e]
+                     : mref[nt][e] == -INFINITY ? -INFINITY : mref[nt][e] + (kShift + 8.f);
+    };
+    auto sub = [&](int nt, int e) {
+      return NT <= 2 ? kept_sub[nt % kKept][e] : mref[nt][e] == -INFINITY ? 0.f : mref[nt][e];
+    };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        mref[nt][e] = limit[nt][e] = -INFINITY;
-        sub[nt][e] = 0.f;
+        mref[nt][e] = -INFINITY;
         l[nt][e] = 0.f;
-        row_mul[nt][e] = st.row_mul[8 * nt + 2 * q + e];
+        if (NT <= 2) {
+          kept_limit[nt % kKept][e] = -INFINITY;
+          kept_sub[nt % kKept][e] = 0.f;
+          kept_mul[nt % kKept][e] = e ? st.row_mul[4 * nt + q].y : st.row_mul[4 * nt + q].x;
+        }
       }
 #pragma unroll
       for (int t = 0; t < kTiles; ++t)
@@ -533,12 +551,15 @@ __global__ void __launch_bounds__(Few4<DP, NT, GROUP, RUNS>::kThreads, 1)
       uint32_t ks[4];
       ptx::ldmatrix_x4(scale_mem, ks[0], ks[1], ks[2], ks[3]);
       float x[NT][kParts][2];
-      {
-        // both tiles of 16 keys side by side, for the products of one follow each other
-        uint32_t kw[kParts][L::kWords];
+      // with eight rows both tiles of 16 keys side by side, for the products of one follow
+      // each other; with more there are others to go between
+      constexpr int kSide = NT == 1 ? 2 : 1;
 #pragma unroll
-        for (int h = 0; h < kParts; ++h) {
-          const uint8_t* row = src + (h * 8 + gk) * L::kBytes + q * (L::kBytes / 4);
+      for (int m0 = 0; m0 < kParts / 2; m0 += kSide) {
+        uint32_t kw[2 * kSide][L::kWords];
+#pragma unroll
+        for (int h = 0; h < 2 * kSide; ++h) {
+          const uint8_t* row = src + ((2 * m0 + h) * 8 + gk) * L::kBytes + q * (L::kBytes / 4);
           if (DP == 128) {
             const uint4 y = *reinterpret_cast<const uint4*>(row);
             kw[h][0] = y.x, kw[h][1] = y.y, kw[h][2 % L::kWords] = y.z, kw[h][3 % L::kWords] = y.w;
@@ -547,9 +568,9 @@ __global__ void __launch_bounds__(Few4<DP, NT, GROUP, RUNS>::kThreads, 1)
             kw[h][0] = y.x, kw[h][1] = y.y;
           }
         }
-        float acc[kParts / 2][NT][4];
+        float acc[kSide][NT][4];
 #pragma unroll
-        for (int mt = 0; mt < kParts / 2; ++mt)
+        for (int mt = 0; mt < kSide; ++mt)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -560,26 +581,26 @@ __global__ void __launch_bounds__(Few4<DP, NT, GROUP, RUNS>::kThreads, 1)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) b[nt] = q_mem[(nt * kQChunks + i) * 32 + lane];
 #pragma unroll
-          for (int mt = 0; mt < kParts / 2; ++mt) {
+          for (int mt = 0; mt < kSide; ++mt) {
             // 128 elements: the lane's first two words are under one scale, the others under the next
             const uint32_t sel = i < 2 ? 0x1010 : 0x3232;
-            const uint32_t s0 = __byte_perm(ks[2 * mt], 0, sel), s1 = __byte_perm(ks[2 * mt + 1], 0, sel);
+            const uint32_t s0 = __byte_perm(ks[2 * (m0 + mt)], 0, sel);
+            const uint32_t s1 = __byte_perm(ks[2 * (m0 + mt) + 1], 0, sel);
             uint4 ka = e2m1x8_to_f16(kw[2 * mt][i]), kb = e2m1x8_to_f16(kw[2 * mt + 1][i]);
             ka = make_uint4(mul_f16x2(ka.x, s0), mul_f16x2(ka.y, s0), mul_f16x2(ka.z, s0), mul_f16x2(ka.w, s0));
             kb = make_uint4(mul_f16x2(kb.x, s1), mul_f16x2(kb.y, s1), mul_f16x2(kb.z, s1), mul_f16x2(kb.w, s1));
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              ptx::mma_16816_f16(acc[mt][nt], ka.x, kb.x, ka.y, kb.y, b[nt].x, b[nt].y);
-              ptx::mma_16816_f16(acc[mt][nt], ka.z, kb.z, ka.w, kb.w, b[nt].z, b[nt].w);
-            }
+            for (int nt = 0; nt < NT; ++nt) ptx::mma_16816_f16(acc[mt][nt], ka.x, kb.x, ka.y, kb.y, b[nt].x, b[nt].y);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) ptx::mma_16816_f16(acc[mt][nt], ka.z, kb.z, ka.w, kb.w, b[nt].z, b[nt].w);
           }
         }
 #pragma unroll
-        for (int mt = 0; mt < kParts / 2; ++mt)
+        for (int mt = 0; mt < kSide; ++mt)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) x[nt][2 * mt + k / 2][k % 2] = acc[mt][nt][k];
+            for (int k = 0; k < 4; ++k) x[nt][2 * (m0 + mt) + k / 2][k % 2] = acc[mt][nt][k];
       }
       // invisible scores -infinity; see: bit 8 i, the row sees key 8 i + row_key(g)
       uint32_t see[NT][2];
@@ -605,11 +626,11 @@ __global__ void __launch_bounds__(Few4<DP, NT, GROUP, RUNS>::kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float y = fmaxf(fmaxf(x[nt][0][e], x[nt][1][e]), fmaxf(x[nt][2][e], x[nt][3][e]));
-          y = y == -INFINITY ? -INFINITY : y * row_mul[nt][e];
+          y = y == -INFINITY ? -INFINITY : y * row_mul(nt, e);
           // a visible score of -infinity is the cap's negative, an invisible one nothing
           if (CAP && see[nt][e] != 0) y = capped(sc, y, 0.f);
           mx[nt][e] = y;
-          over |= y > limit[nt][e];
+          over |= y > limit(nt, e);
         }
       // the first visible key sets a row's m, later ones when the maximum has grown enough
       if (__any_sync(0xffffffffu, over)) {
@@ -621,9 +642,12 @@ __global__ void __launch_bounds__(Few4<DP, NT, GROUP, RUNS>::kThreads, 1)
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, off));
             const float old = mref[nt][e];
-            if (y > limit[nt][e]) {
-              mref[nt][e] = sub[nt][e] = y - kShift;
-              limit[nt][e] = y + 8.f;
+            if (y > limit(nt, e)) {
+              mref[nt][e] = y - kShift;
+              if (NT <= 2) {
+                kept_sub[nt % kKept][e] = mref[nt][e];
+                kept_limit[nt % kKept][e] = y + 8.f;
+              }
               const float back = old == -INFINITY ? 0.f : ex2(old - mref[nt][e]);
               l[nt][e] *= back;
 #pragma unroll
@@ -643,19 +667,19 @@ __global__ void __launch_bounds__(Few4<DP, NT, GROUP, RUNS>::kThreads, 1)
         for (int e = 0; e < 2; ++e) {
           if (!CAP) {
 #pragma unroll
-            for (int i = 0; i < kParts; ++i) w[i][e] = fmaf(x[nt][i][e], row_mul[nt][e], -sub[nt][e]);
+            for (int i = 0; i < kParts; ++i) w[i][e] = fmaf(x[nt][i][e], row_mul(nt, e), -sub(nt, e));
           } else {
             float raw[kParts], big = 0.f;
 #pragma unroll
             for (int i = 0; i < kParts; ++i) {
-              raw[i] = x[nt][i][e] * row_mul[nt][e];
+              raw[i] = x[nt][i][e] * row_mul(nt, e);
               big = fmaxf(big, fabsf(raw[i]));
-              w[i][e] = capped_near(sc, raw[i], sub[nt][e]);
+              w[i][e] = capped_near(sc, raw[i], sub(nt, e));
             }
             if (__any_sync(0xffffffffu, past_near(sc, big))) {
 #pragma unroll
               for (int i = 0; i < kParts; ++i) {
-                const float past = capped_past(sc, raw[i], sub[nt][e]);
+                const float past = capped_past(sc, raw[i], sub(nt, e));
                 if (past_near(sc, raw[i])) w[i][e] = past;
               }
             }
@@ -852,13 +876,41 @@ cudaError_t launch(AttendArgs a, cudaStream_t stream) {
 template <int DP, int NT, int GROUP, bool RUNS, bool CAP>
 cudaError_t setup() {
   using L = Few4<DP, NT, GROUP, RUNS>;
-  static_assert(L::kSmem + L::kWorkers * (sizeof(WorkerState<GROUP>) + 300) + 1024 <= 232448,
+  static_assert(L::kSmem + L::kWorkers * (sizeof(WorkerState<GROUP, L::kRows>) + 300) + 1024 <= 232448,
                 "shared memory of an SM");
   static_assert(L::kWorkers <= kFew4Workers && 2 * L::kWorkers * L::kRows <= kFew4PartRows, "the parts' place");
   return cudaFuncSetAttribute(few4_kernel<DP, NT, GROUP, RUNS, CAP>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
 }
 
+template <int DP, int NT, int WARPS>
+cudaError_t setup_all() {
+  cudaError_t e = setup<DP, NT, WARPS, false, false>();
+  if (e == cudaSuccess) e = setup<DP, NT, WARPS, false, true>();
+  if (e == cudaSuccess) e = setup<DP, NT, WARPS, true, false>();
+  if (e == cudaSuccess) e = setup<DP, NT, WARPS, true, true>();
+  if (e == cudaSuccess) e = setup<DP, NT, 4, true, false>();
+  return e;
+}
+
+// alone: a worker a CTA; else of four warps, where slots lie in runs and scores are not
+// capped.
+template <int DP, int NT, int WARPS>
+cudaError_t launch_all(const AttendArgs& a, bool alone, bool runs, cudaStream_t stream) {
+  const bool cap = a.softcap > 0.f;
+  if (!runs)
+    return cap ? launch<DP, NT, WARPS, false, true>(a, stream) : launch<DP, NT, WARPS, false, false>(a, stream);
+  if (cap) return launch<DP, NT, WARPS, true, true>(a, stream);
+  return alone ? launch<DP, NT, WARPS, true, false>(a, stream) : launch<DP, NT, 4, true, false>(a, stream);
+}
+
 }  // namespace
+
+// A source file each.
+template <int DP, int NT>
+cudaError_t few4_setup_of();
+template <int DP, int NT>
+cudaError_t few4_launch_of(const AttendArgs& a, bool alone, bool runs, cudaStream_t stream);
+
 }  // namespace tree
 }  // namespace dspark

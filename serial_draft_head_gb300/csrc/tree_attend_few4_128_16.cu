@@ -1,0 +1,19 @@
+// tree_attend_few4_128_16.cu -- tree_attend_few4.cuh for heads of up to 128 elements and items of
+// 16 rows.
+#include "tree_attend_few4.cuh"
+
+namespace dspark {
+namespace tree {
+
+template <>
+cudaError_t few4_setup_of<128, 2>() {
+  return setup_all<128, 2, 12>();
+}
+
+template <>
+cudaError_t few4_launch_of<128, 2>(const AttendArgs& a, bool alone, bool runs, cudaStream_t stream) {
+  return launch_all<128, 2, 12>(a, alone, runs, stream);
+}
+
+}  // namespace tree
+}  // namespace dspark

@@ -1,0 +1,19 @@
+// tree_attend_few4_64_16.cu -- tree_attend_few4.cuh for heads of up to 64 elements and items of
+// 16 rows.
+#include "tree_attend_few4.cuh"
+
+namespace dspark {
+namespace tree {
+
+template <>
+cudaError_t few4_setup_of<64, 2>() {
+  return setup_all<64, 2, 12>();
+}
+
+template <>
+cudaError_t few4_launch_of<64, 2>(const AttendArgs& a, bool alone, bool runs, cudaStream_t stream) {
+  return launch_all<64, 2, 12>(a, alone, runs, stream);
+}
+
+}  // namespace tree
+}  // namespace dspark

@@ -1,0 +1,19 @@
+// tree_attend_few4_64_8.cu -- tree_attend_few4.cuh for heads of up to 64 elements and items of
+// 8 rows.
+#include "tree_attend_few4.cuh"
+
+namespace dspark {
+namespace tree {
+
+template <>
+cudaError_t few4_setup_of<64, 1>() {
+  return setup_all<64, 1, 16>();
+}
+
+template <>
+cudaError_t few4_launch_of<64, 1>(const AttendArgs& a, bool alone, bool runs, cudaStream_t stream) {
+  return launch_all<64, 1, 16>(a, alone, runs, stream);
+}
+
+}  // namespace tree
+}  // namespace dspark

@@ -309,9 +309,9 @@ struct TileMaps {
 
 // e2m1 cache, few rows a cached head (tree_attend_few4.cuh).  kFew4Workers: most workers
 // an SM, kFew4PartRows: rows of their parts.
-constexpr int kFew4Workers = 4, kFew4PartRows = 96;
+constexpr int kFew4Workers = 4, kFew4PartRows = 128;
 cudaError_t few4_setup(int D);
-cudaError_t few4_launch(const AttendArgs& a, cudaStream_t stream);
+cudaError_t few4_launch(const AttendArgs& a, cudaStream_t stream);    // up to 32 rows a cached head on average
 
 // e2m1 cache, more rows (tree_attend4.cu).
 cudaError_t attend4_setup(bool f16, int D);

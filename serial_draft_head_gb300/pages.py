@@ -77,6 +77,7 @@ class Pages:
                               requests, max_pages)
         self._at = ctypes.addressof(self.c)
         self.reset()
+        torch.cuda.current_stream(self.device).synchronize()     # ready for calls on any stream
 
     def _call(self, what, *args):
         if torch.cuda.current_device() == self._index:
@@ -89,6 +90,9 @@ class Pages:
 
     def _stream(self, stream):
         return _raw_stream(self._index) if stream is None else walk._stream(stream)
+
+    def _empty(self, n):
+        return torch.empty(n, dtype=_int32, device=self.device)
 
     def _numbers(self, x):
         if not (x.dtype is _int32 and x.get_device() == self._index and x.shape == (self.requests,)
@@ -116,16 +120,16 @@ class Pages:
             m, ms, mw = mask.data_ptr(), mask.stride(0), mask.shape[1]
         if out is None:
             if stream is None:
-                out = [torch.empty(n, dtype=_int32, device=self.device) for n in (self.requests + 1, n_rows, n_rows)]
+                first, slot, position = self._empty(self.requests + 1), self._empty(n_rows), self._empty(n_rows)
             else:
                 s = torch.cuda.ExternalStream(stream, device=self.device) if isinstance(stream, int) else stream
                 with torch.cuda.stream(s):           # the blocks belong to the stream that fills them
-                    out = [torch.empty(n, dtype=_int32, device=self.device)
-                           for n in (self.requests + 1, n_rows, n_rows)]
-        first, slot, position = out
-        for x, n in ((first, self.requests + 1), (slot, n_rows), (position, n_rows)):
-            if not (x.dtype is _int32 and x.get_device() == self._index and x.shape == (n,) and x.is_contiguous()):
-                raise ValueError("out is int32 [requests + 1], [n_rows] and [n_rows] on the pool's device")
+                    first, slot, position = self._empty(self.requests + 1), self._empty(n_rows), self._empty(n_rows)
+        else:
+            first, slot, position = out
+            for x, n in ((first, self.requests + 1), (slot, n_rows), (position, n_rows)):
+                if not (x.dtype is _int32 and x.get_device() == self._index and x.shape == (n,) and x.is_contiguous()):
+                    raise ValueError("out is int32 [requests + 1], [n_rows] and [n_rows] on the pool's device")
         self._call("dspark_pages_grow", at_length, at_count, n_rows, m, ms, mw, first.data_ptr(), slot.data_ptr(),
                    position.data_ptr(), self._stream(stream))
         return first, slot, position

@@ -64,7 +64,7 @@ class Case:
         tol, tol_lse = e2m1.bounds(want, weight, sums, self.D, self.dtype, softcap, max(self.T) + max(self.L),
                                    self.q.abs().max().item() * abs(scale), torch.nan_to_num(k).abs().max().item(),
                                    torch.nan_to_num(v).abs().max().item(),
-                                   self.N * self.Hq // self.Hkv > 16 * self.B)
+                                   self.N * self.Hq // self.Hkv > 32 * self.B)
         out, lse, want, want_lse, tol, tol_lse = (x[rows] for x in (out, lse, want, want_lse, tol, tol_lse))
         assert not torch.isnan(out).any() and not torch.isnan(lse).any()
         off = (out.double() - want).abs() - tol
