@@ -70,9 +70,11 @@ struct Few4 {
   static constexpr int kRing = kScale + 2 * kBlock * 16; // of a warp
   static constexpr int kQ = kWarps * kRing;              // [worker][NT][DP / 32][lane] 16 bytes
   static constexpr int kQBytes = kRows * DP * 2;
-  static constexpr int kMerge = kQ + kWorkers * kQBytes; // [warp][row][kHalf + 4] floats
-  static constexpr int kHalf = DP / 2;                   // columns merged at a time
-  static constexpr int kMergeRow = kHalf + 4;
+  static constexpr int kMerge = kQ + kWorkers * kQBytes; // [warp][row][kCols + 4] floats
+  // columns merged at a time: all where there is room
+  static constexpr int kPasses = kMerge + kWarps * kRows * (DP + 4) * 4 <= 232448 - 6144 ? 1 : 2;
+  static constexpr int kCols = DP / kPasses;
+  static constexpr int kMergeRow = kCols + 4;
   static constexpr int kMergeWarp = kRows * kMergeRow * 4;
   static constexpr int kSmem = kMerge + kWarps * kMergeWarp;
   using Item = Work<kBlock, kRows, kExtra>;
@@ -180,7 +182,7 @@ template <class L, int GROUP>
 __device__ __noinline__ void join_parts(const AttendArgs& a, WorkerState<GROUP, L::kRows>& st, float* weight,
                                         int worker, int first, int parts, int row0, int head, int group,
                                         int rows) {
-  constexpr int kRows = L::kRows, DP = L::kHalf * 2, kThreads = GROUP * 32;
+  constexpr int kRows = L::kRows, DP = L::kBytes * 2, kThreads = GROUP * 32;
   constexpr int kMost = GROUP * L::kMergeWarp / (4 * kRows);    // parts with a weight
   const int tid = threadIdx.x % kThreads, warp = tid / 32, lane = tid % 32;
   auto part_at = [&](int i) { return (int64_t)2 * (first + i) + (i == 0 ? 1 : 0); };
@@ -760,67 +762,71 @@ __global__ void __launch_bounds__(Few4<DP, NT, GROUP, RUNS>::kThreads, 1)
         for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
         if (g == 0) st.ml[warp][8 * nt + 2 * q + e] = make_float2(mref[nt][e], sum);
       }
-    meet<GROUP>(worker);
-    const bool next_live = st.live[cur ^ 1];
-    if (warp == 0 && lane < L::kRows) {          // a row a lane: m and l of all warps
-      float top = -INFINITY, sum = 0.f;
-      for (int i = 0; i < live; ++i) top = fmaxf(top, st.ml[i][lane].x);
-      const float sub = top == -INFINITY ? 0.f : top;
-      for (int i = 0; i < live; ++i) sum = fmaf(st.ml[i][lane].y, ex2(st.ml[i][lane].x - sub), sum);
-      st.fin[lane] = make_float2(sub, sum == 0.f ? 0.f : 1.f / sum);
-      if (lane < rows) {
-        if (!whole) a.part_ml[part * L::kRows + lane] = make_float2(top, sum);
-        else if (a.lse) a.lse[out_row(lane)] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-      }
-    }
-    if (next_live && warp < NT) load_q(segments[cur ^ 1]);
-    meet<GROUP>(worker);
-    // every warp's O by its weight, half the columns at a time
+    // every warp's O, some columns at a time, and by which weight is for those to see who add
+    // them up
+    constexpr int kT = kTiles / L::kPasses, kCols = L::kCols;
+    bool next_live = false;
+    uint32_t any_bad = 0;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
+    for (int pass = 0; pass < L::kPasses; ++pass) {
       if (warp < live) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int row = 8 * nt + 2 * q + e;
-            const float w = ex2(mref[nt][e] - st.fin[row].x);
-            float* dst = merge + (warp * L::kRows + row) * L::kMergeRow + g * (DP / 16);
+            float* dst = merge + (warp * L::kRows + 8 * nt + 2 * q + e) * L::kMergeRow + g * (2 * kT);
 #pragma unroll
-            for (int k = 0; k < kTiles / 2; k += 2) {
-              const float* y = o[nt][half * (kTiles / 2) + k];
-              const float* z = o[nt][half * (kTiles / 2) + k + 1];
-              *reinterpret_cast<float4*>(dst + 2 * k) = make_float4(y[e] * w, y[2 + e] * w, z[e] * w, z[2 + e] * w);
+            for (int k = 0; k < kT; k += 2) {
+              const float* y = o[nt][pass * kT + k];
+              const float* z = o[nt][pass * kT + k + 1];
+              *reinterpret_cast<float4*>(dst + 2 * k) = make_float4(y[e], y[2 + e], z[e], z[2 + e]);
             }
           }
       }
       meet<GROUP>(worker);
-      for (int i = tid; i < rows * (L::kHalf / 2); i += kWorkerThreads) {
-        const int row = i / (L::kHalf / 2), n = i % (L::kHalf / 2) * 2;
-        float2 y = make_float2(0.f, 0.f);
+      if (pass == 0) {
+        next_live = st.live[cur ^ 1];
+        if (next_live && warp < NT) load_q(segments[cur ^ 1]);
+#pragma unroll
+        for (int k = 0; k < DSPARK_TREE_MAX_NODES / 32; ++k) any_bad |= st.bad[k];
+      }
+      for (int i = tid; i < rows * (kCols / 4); i += kWorkerThreads) {
+        const int row = i / (kCols / 4), n = i % (kCols / 4) * 4;
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < live; ++k) top = fmaxf(top, st.ml[k][row].x);
+        const float base = top == -INFINITY ? 0.f : top;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
         for (int k = 0; k < live; ++k) {
-          const float2 v = *reinterpret_cast<const float2*>(merge + (k * L::kRows + row) * L::kMergeRow + n);
-          y.x += v.x;
-          y.y += v.y;
+          const float2 ml = st.ml[k][row];
+          const float4 v = *reinterpret_cast<const float4*>(merge + (k * L::kRows + row) * L::kMergeRow + n);
+          const float w = ex2(ml.x - base);
+          sum = fmaf(ml.y, w, sum);
+          y.x = fmaf(v.x, w, y.x);
+          y.y = fmaf(v.y, w, y.y);
+          y.z = fmaf(v.z, w, y.z);
+          y.w = fmaf(v.w, w, y.w);
         }
-        const int d = n / (DP / 16) * (DP / 8) + half * (DP / 16) + n % (DP / 16);
+        const int d = n / (2 * kT) * (DP / 8) + pass * (2 * kT) + n % (2 * kT);
         if (!whole) {
-          *reinterpret_cast<float2*>(a.part_o + (part * L::kRows + row) * DP + d) = y;
-        } else if (d < a.D) {
+          *reinterpret_cast<float4*>(a.part_o + (part * L::kRows + row) * DP + d) = y;
+          if (pass == 0 && n == 0) a.part_ml[part * L::kRows + row] = make_float2(top, sum);
+        } else {
           // l = 0: every weight was 0, and so is O
-          const float inv = st.fin[row].y;
-          *reinterpret_cast<uint32_t*>(a.out + out_row(row) * a.D + d) = pack_out(a.f16, y.x * inv, y.y * inv);
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          const int64_t to = out_row(row);
+          if (d < a.D)
+            *reinterpret_cast<uint2*>(a.out + to * a.D + d) =
+                make_uint2(pack_out(a.f16, y.x * inv, y.y * inv), pack_out(a.f16, y.z * inv, y.w * inv));
+          if (pass == 0 && n == 0 && a.lse) a.lse[to] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
         }
       }
-      meet<GROUP>(worker);
+      if (pass + 1 < L::kPasses) meet<GROUP>(worker);
     }
-    uint32_t any_bad = 0;
-#pragma unroll
-    for (int k = 0; k < DSPARK_TREE_MAX_NODES / 32; ++k) any_bad |= st.bad[k];
-    meet<GROUP>(worker);
-    if (next_live && warp < NT) store_q();
+    if (next_live && warp < NT) store_q();       // all are past the segment's products
     if (any_bad != 0) {
+      meet<GROUP>(worker);
       if ((int)tid < rows) {
         const int nd = a.group.div(s.group * L::kRows + tid);
         add_nan(a, st.bad, a.mask ? a.mask + (int64_t)(s.row0 + nd) * a.mask_stride : nullptr, s.b, s.rows,
