@@ -80,6 +80,12 @@ struct Few4 {
   using Item = Work<kBlock, kRows, kExtra>;
 };
 
+// A part of an item that others share, and what its join needs.
+struct Left {
+  int item;                             // first worker | parts << 16; 0: none
+  int row0, head, group, rows;
+};
+
 template <int GROUP, int ROWS>
 struct WorkerState {
   float2 ml[GROUP][ROWS];               // [warp][row]
@@ -87,7 +93,8 @@ struct WorkerState {
   float2 row_mul[ROWS / 2];             // two rows' factors on the raw scores
   uint32_t bad[DSPARK_TREE_MAX_NODES / 32];
   int live[2];                          // there is a segment; the next one
-  int join;                             // an item to join: first worker | parts << 16
+  Left left[2];                         // the parts that the worker leaves: of its first item and its last
+  int join[2];                          // whether all parts of theirs are there
 };
 
 // The warps of worker w meet.
@@ -174,76 +181,60 @@ __device__ __noinline__ void add_nan(const AttendArgs& a, const uint32_t* bad,
   }
 }
 
-// Joins the `parts` parts of an item that several workers share, the first of them worker
-// `first`: a part's weight a row, then the sum over the parts in order, so that the
-// result does not depend on which came last.  As many parts at a time as the merge's place
-// has weights for.
+// Joins the parts of an item that several workers share, in their order, so that the result
+// does not depend on which came last.  A thread has four columns of a row and eight parts'
+// loads in flight.
 template <class L, int GROUP>
-__device__ __noinline__ void join_parts(const AttendArgs& a, WorkerState<GROUP, L::kRows>& st, float* weight,
-                                        int worker, int first, int parts, int row0, int head, int group,
-                                        int rows) {
-  constexpr int kRows = L::kRows, DP = L::kBytes * 2, kThreads = GROUP * 32;
-  constexpr int kMost = GROUP * L::kMergeWarp / (4 * kRows);    // parts with a weight
-  const int tid = threadIdx.x % kThreads, warp = tid / 32, lane = tid % 32;
+__device__ __noinline__ void join_parts(const AttendArgs& a, const Left& of, int tid) {
+  constexpr int kRows = L::kRows, DP = L::kBytes * 2, kAtOnce = 8;
+  const int first = of.item & 0xffff, parts = of.item >> 16;
   auto part_at = [&](int i) { return (int64_t)2 * (first + i) + (i == 0 ? 1 : 0); };
-  auto out_row = [&](int row) {
-    const int grow = group * kRows + row, node = a.group.div(grow);
-    return (int64_t)(row0 + node) * a.Hq + head * a.G + grow - node * a.G;
-  };
-  for (int row = warp; row < rows; row += GROUP) {
-    float top = -INFINITY, sum = 0.f;
-    for (int i = lane; i < parts; i += 32) top = fmaxf(top, __ldcg(a.part_ml + part_at(i) * kRows + row).x);
+#pragma unroll 1
+  for (int i = tid; i < of.rows * (DP / 4); i += GROUP * 32) {
+    const int row = i / (DP / 4), c = i % (DP / 4);
+    if (4 * c >= a.D) continue;
+    float m = -INFINITY, l = 0.f;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int k0 = 0; k0 < parts; k0 += kAtOnce) {
+      float4 x[kAtOnce];
+      float2 ml[kAtOnce];
+      float top = m;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float sub = top == -INFINITY ? 0.f : top;
-    for (int i = lane; i < parts; i += 32) {
-      const float2 ml = __ldcg(a.part_ml + part_at(i) * kRows + row);
-      sum = fmaf(ml.y, ex2(ml.x - sub), sum);
-    }
+      for (int k = 0; k < kAtOnce; ++k) {
+        ml[k] = make_float2(-INFINITY, 0.f);
+        x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k0 + k < parts) {
+          ml[k] = __ldcg(a.part_ml + part_at(k0 + k) * kRows + row);
+          x[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + part_at(k0 + k) * (kRows * DP)) + i);
+        }
+      }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) {
-      st.fin[row] = make_float2(sub, sum == 0.f ? 0.f : 1.f / sum);
-      if (a.lse) a.lse[out_row(row)] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-    }
-  }
-  // float4 columns of rows, some to a thread
-  constexpr int kEach = (kRows * (DP / 4) + kThreads - 1) / kThreads;
-  float4 y[kEach];
+      for (int k = 0; k < kAtOnce; ++k) top = fmaxf(top, ml[k].x);
+      const float base = top == -INFINITY ? 0.f : top, old = ex2(m - base);
+      m = top;
+      l *= old;
+      y.x *= old;
+      y.y *= old;
+      y.z *= old;
+      y.w *= old;
 #pragma unroll
-  for (int e = 0; e < kEach; ++e) y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = 0; k0 < parts; k0 += kMost) {
-    const int n = min(kMost, parts - k0);
-    meet<GROUP>(worker);
-    for (int i = tid; i < n * rows; i += kThreads) {
-      const int k = i / rows, row = i - k * rows;
-      weight[k * kRows + row] = ex2(__ldcg(a.part_ml + part_at(k0 + k) * kRows + row).x - st.fin[row].x);
-    }
-    meet<GROUP>(worker);
-#pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-      const int i = tid + e * kThreads, row = i / (DP / 4);
-      if (row >= rows || 4 * (i % (DP / 4)) >= a.D) continue;
-#pragma unroll 8
-      for (int k = 0; k < n; ++k) {
-        const float4 x =
-            __ldcg(reinterpret_cast<const float4*>(a.part_o + part_at(k0 + k) * (kRows * DP)) + i);
-        const float w = weight[k * kRows + row];
-        y[e].x = fmaf(x.x, w, y[e].x);
-        y[e].y = fmaf(x.y, w, y[e].y);
-        y[e].z = fmaf(x.z, w, y[e].z);
-        y[e].w = fmaf(x.w, w, y[e].w);
+      for (int k = 0; k < kAtOnce; ++k) {
+        const float w = ex2(ml[k].x - base);
+        l = fmaf(ml[k].y, w, l);
+        y.x = fmaf(x[k].x, w, y.x);
+        y.y = fmaf(x[k].y, w, y.y);
+        y.z = fmaf(x[k].z, w, y.z);
+        y.w = fmaf(x[k].w, w, y.w);
       }
     }
-  }
-#pragma unroll
-  for (int e = 0; e < kEach; ++e) {
-    const int i = tid + e * kThreads, row = i / (DP / 4), c = i % (DP / 4);
-    if (row >= rows || 4 * c >= a.D) continue;
     // l = 0: every weight was 0, and so is O
-    const float inv = st.fin[row].y;
-    *reinterpret_cast<uint2*>(a.out + out_row(row) * a.D + 4 * c) =
-        make_uint2(pack_out(a.f16, y[e].x * inv, y[e].y * inv), pack_out(a.f16, y[e].z * inv, y[e].w * inv));
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int grow = of.group * kRows + row, node = a.group.div(grow);
+    const int64_t to = (int64_t)(of.row0 + node) * a.Hq + of.head * a.G + grow - node * a.G;
+    *reinterpret_cast<uint2*>(a.out + to * a.D + 4 * c) =
+        make_uint2(pack_out(a.f16, y.x * inv, y.y * inv), pack_out(a.f16, y.z * inv, y.w * inv));
+    if (c == 0 && a.lse) a.lse[to] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   }
 }
 
@@ -273,6 +264,7 @@ __global__ void __launch_bounds__(Few4<DP, NT, GROUP, RUNS>::kThreads, 1)
                              (lane / 8 * 8 + row_key(lane % 8)) * 16;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (tid < DSPARK_TREE_MAX_NODES / 32) st.bad[tid] = 0;
+  if (tid < 2) st.left[tid].item = 0;
   Item::template plan<L::kThreads, L::kWorkers>(a, shares, sums);
   const Share& share = shares[worker];
   Segment* segments = all_segments[worker];
@@ -836,25 +828,32 @@ __global__ void __launch_bounds__(Few4<DP, NT, GROUP, RUNS>::kThreads, 1)
       meet<GROUP>(worker);
       if (tid < DSPARK_TREE_MAX_NODES / 32) st.bad[tid] = 0;
     }
-    if (!whole) {
-      // the last CTA to leave its part of the item joins them all
-      __threadfence();
-      meet<GROUP>(worker);
-      if (tid == 0) {
-        const int w = Item::part_of(s, share.cut).w;
-        int* count = a.arrived + (w & 0xffff);
-        const bool last = atomicAdd(count, 1) == (w >> 16) - 1;
-        if (last) *count = 0;
-        __threadfence();
-        st.join = last ? w : 0;
-      }
-      meet<GROUP>(worker);
-      if (st.join)
-        join_parts<L, GROUP>(a, st, merge, worker, st.join & 0xffff, st.join >> 16, s.row0, s.head, s.group,
-                             rows);
-    }
+    if (!whole && tid == 0)
+      st.left[s.t0 == 0 ? 1 : 0] = {Item::part_of(s, share.cut).w, s.row0, s.head, s.group, rows};
     meet<GROUP>(worker);
     cur ^= 1;
+  }
+  // items whose parts are all there now are joined by this worker, at its end: in between,
+  // what makes a part seen by others would have held up all of its warps (20 requests of
+  // 1,000 tokens: 22.9 us, with no item shared 12.2)
+  if (st.left[0].item | st.left[1].item) {
+    __threadfence();
+    meet<GROUP>(worker);
+    if (tid < 2) {
+      const int item = st.left[tid].item;
+      bool last = false;
+      if (item != 0) {
+        int* count = a.arrived + (item & 0xffff);
+        last = atomicAdd(count, 1) == (item >> 16) - 1;
+        if (last) *count = 0;
+        __threadfence();
+      }
+      st.join[tid] = last;
+    }
+    meet<GROUP>(worker);
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k)
+      if (st.join[k]) join_parts<L, GROUP>(a, st.left[k], tid);
   }
   ptx::cp_async_wait_group<0>();
   if (worst > top_page) set_status(a.status, DSPARK_EPAGES);
