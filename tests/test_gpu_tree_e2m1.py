@@ -53,7 +53,7 @@ class Case:
 
     def attend(self, **kw):
         r = self.tree.attend(self.q, self.cache, self.pages, self.length, self.first, mask=self.mask, **kw)
-        assert self.tree.status() == 0
+        assert self.tree.status(stream=kw.get("stream")) == 0      # a call of the handle as any other: in order
         return r
 
     def check(self, out, lse, scale=None, softcap=0.0, rows=slice(None)):
