@@ -54,15 +54,17 @@ constexpr int kSoftWarps = 8;
 // Warps and registers.  The softmax groups take registers from the others: for
 // a 16-bit cache enough to hold a row of scores; for codes the producers need
 // theirs to convert in, and the softmax reads its scores in two halves.
-template <bool CODES>
+template <int HELD>
 struct Roles {
-  static constexpr int kProdWarps = CODES ? 8 : 4;
+  static constexpr bool kCodes = HELD != k16;
+  static constexpr int kProdWarps = kCodes ? 8 : 4;
   static constexpr int kMmaWarp = kSoftWarps + kProdWarps;
   static constexpr int kThreads = (kMmaWarp + 4) * 32;
   static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
-  static constexpr int kSoftRegs = CODES ? 120 : 184;
-  static constexpr int kProdRegs = CODES ? 96 : 88;
-  static constexpr int kMmaRegs = CODES ? 48 : 56;
+  static constexpr int kSoftRegs = kCodes ? 120 : 184;
+  // e2m1, 64 x 64: producers 88 and products 64 477 us, 96 and 48 519
+  static constexpr int kProdRegs = HELD == kE4M3 ? 96 : 88;
+  static constexpr int kMmaRegs = HELD == kE4M3 ? 48 : HELD == kE2M1 ? 64 : 56;
   static constexpr int kSplit =
       kSoftWarps * kSoftRegs + kProdWarps * kProdRegs + 4 * kMmaRegs;   // times 32
   static_assert(kSplit * 32 <= kThreads * kLaunchRegs, "the split asks for more than there is");
@@ -173,7 +175,7 @@ template <bool F16, int DP>
 __device__ __forceinline__ void produce16(const AttendArgs& a, const TileMaps& maps, uint8_t* smem,
                                           Tail* sh) {
   using L = Layout<DP>;
-  constexpr int kWarps = Roles<false>::kProdWarps;
+  constexpr int kWarps = Roles<k16>::kProdWarps;
   constexpr int kChunks = DP / 8;                // 16-byte chunks of a row
   constexpr int kSub = 32 / kChunks;             // rows of one copy instruction
   static_assert(kWarps * 32 == kKeys, "32 rows a warp");
@@ -311,7 +313,7 @@ __device__ __noinline__ void store_any(uint4 x, uint32_t byte, uint8_t* p0, uint
 template <bool F16, int DP>
 __device__ __forceinline__ void produce8(const AttendArgs& a, uint8_t* smem, Tail* sh) {
   using L = Layout<DP>;
-  constexpr int kWarps = Roles<true>::kProdWarps;
+  constexpr int kWarps = Roles<kE4M3>::kProdWarps;
   constexpr int kChunks = DP / 16;               // 16-code chunks of a row
   constexpr int kWarpRows = 32 / kChunks;
   constexpr int kRows = kWarps * kWarpRows;      // rows a pass
@@ -451,7 +453,7 @@ __device__ __forceinline__ void produce8(const AttendArgs& a, uint8_t* smem, Tai
 template <bool F16, int DP>
 __device__ __forceinline__ void produce4(const AttendArgs& a, uint8_t* smem, Tail* sh) {
   using L = Layout<DP>;
-  constexpr int kWarps = Roles<true>::kProdWarps;
+  constexpr int kWarps = Roles<kE2M1>::kProdWarps;
   constexpr int kChunks = DP / 16;               // blocks of a row
   constexpr int kWarpRows = 32 / kChunks;
   constexpr int kRows = kWarps * kWarpRows;      // rows a pass
@@ -772,6 +774,24 @@ __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t sub_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// Two values of at most 2^100 rounded to eight significant bits (Veltkamp's splitting):
+// upper halves that are theirs as bf16, without the conversion pipe and with their floats
+// at hand.
+__device__ __forceinline__ uint64_t round8_f32x2(uint64_t x) {
+  // the product rounded by itself: as a fused one with the zero, which is fused no further
+  const uint64_t t = fma_f32x2(x, pack_f32x2(65537.f, 65537.f), pack_f32x2(0.f, 0.f));
+  return sub_f32x2(t, sub_f32x2(t, x));
+}
 // O of this row times `back`.
 template <int DP>
 __device__ __forceinline__ void scale_row(uint32_t tm_o, float back) {
@@ -791,8 +811,31 @@ __device__ __forceinline__ void scale_row(uint32_t tm_o, float back) {
 // has bf16's relative precision whatever its size, and what moves m costs (64 x 64 with
 // a key in 50 eight times the others: 8 607 us, 64 495).  In f16 no further than f16 goes.
 template <bool F16, int HELD>
+constexpr bool far_growth() {
+  return HELD == kE2M1 && !F16;
+}
+template <bool F16, int HELD>
 constexpr float grow_limit() {
-  return HELD == kE2M1 && !F16 ? 64.f : 8.f;
+  return far_growth<F16, HELD>() ? 64.f : 8.f;
+}
+
+// A row's sum of weights, and, where m need not be near the maximum, of the weights as
+// they are rounded.  There a row's largest weights are no powers of two (next to a m that
+// is the maximum the largest is 1), and divided by the sum that is not rounded their
+// error would be that of a row with few large ones (2.2e-3 of the result in all, bf16's own
+// rounding 1.6e-3); divided by the rounded sum it is not.
+struct Sum {
+  float l = 0.f, rounded = 0.f;
+  __device__ __forceinline__ void times(float x) {
+    l *= x;
+    rounded *= x;
+  }
+};
+
+// What two packed bf16 weights come to.
+__device__ __forceinline__ void add_rounded(uint32_t pk, float* even, float* odd) {
+  *even += __uint_as_float(pk << 16);
+  *odd += __uint_as_float(pk & 0xffff0000u);
 }
 
 // The row's m after keys whose largest exponent is x_max; l and O follow if it
@@ -801,7 +844,7 @@ constexpr float grow_limit() {
 template <bool F16, int HELD, int DP>
 __device__ __forceinline__ float move_reference(float x_max, Tail* sh, uint64_t* o_done,
                                                 uint32_t parity, int* status, uint32_t tm_o,
-                                                float mref, float* l) {
+                                                float mref, Sum* l) {
   constexpr float kShift = F16 ? 7.f : 0.f;
   const bool move = x_max > mref + (mref == -INFINITY ? 0.f : kShift + grow_limit<F16, HELD>());
   const float m_new = move ? x_max - kShift : mref;
@@ -809,7 +852,7 @@ __device__ __forceinline__ float move_reference(float x_max, Tail* sh, uint64_t*
     wait(sh, o_done, parity, status);
     ptx::tc_fence_after();
     const float back = mref == -INFINITY ? 0.f : ex2(mref - m_new);
-    *l *= back;
+    l->times(back);
     scale_row<DP>(tm_o, back);
   }
   return m_new;
@@ -821,13 +864,14 @@ __device__ __forceinline__ float move_reference(float x_max, Tail* sh, uint64_t*
 // the warp, S is still there and they are done again (false; x_max is the row's largest
 // exponent).  A 16-bit cache: the next 32 scores are loaded while these are worked on.
 template <bool F16, int HELD, int KEYS>
-__device__ __forceinline__ bool softmax_plain(float sl2, uint32_t tm_s, float mref, float* l,
+__device__ __forceinline__ bool softmax_plain(float sl2, uint32_t tm_s, float mref, Sum* l,
                                               float* x_max) {
   constexpr float kShift = F16 ? 7.f : 0.f;
   constexpr bool WIDE = HELD == k16;
   constexpr int kBuf = WIDE ? 2 : 1, kChunks = KEYS / 32;
   uint32_t v[kBuf][32], pk[kChunks][16];
   float mx[2] = {-INFINITY, -INFINITY}, sum[4] = {0.f, 0.f, 0.f, 0.f};
+  uint64_t sum2[2] = {0, 0}, rounded2[2] = {0, 0};         // pairs of zeros
   const uint64_t mul = pack_f32x2(sl2, sl2), neg = pack_f32x2(-mref, -mref);
   ptx::tmem_ld32(tm_s, v[0]);
 #pragma unroll
@@ -843,9 +887,17 @@ __device__ __forceinline__ bool softmax_plain(float sl2, uint32_t tm_s, float mr
       unpack_f32x2(fma_f32x2(pack_f32x2(r0, r1), mul, neg), &p0, &p1);
       p0 = ex2(p0);
       p1 = ex2(p1);
-      sum[2 * k & 3] += p0;
-      sum[(2 * k + 1) & 3] += p1;
-      pk[c][k] = pack2<F16>(p0, p1);
+      if (far_growth<F16, HELD>()) {
+        const uint64_t p = pack_f32x2(p0, p1), near = round8_f32x2(p);
+        sum2[k & 1] = add_f32x2(sum2[k & 1], p);
+        rounded2[k & 1] = add_f32x2(rounded2[k & 1], near);
+        unpack_f32x2(near, &p0, &p1);
+        pk[c][k] = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
+      } else {
+        sum[2 * k & 3] += p0;
+        sum[(2 * k + 1) & 3] += p1;
+        pk[c][k] = pack2<F16>(p0, p1);
+      }
     }
     if (!WIDE && c < kChunks - 1) ptx::tmem_ld32(tm_s + 32 * (c + 1), v[0]);
   }
@@ -853,17 +905,27 @@ __device__ __forceinline__ bool softmax_plain(float sl2, uint32_t tm_s, float mr
   if (__any_sync(0xffffffffu, *x_max > mref + (kShift + grow_limit<F16, HELD>()))) return false;
 #pragma unroll
   for (int c = 0; c < kChunks; ++c) ptx::tmem_st16(tm_s + 16 * c, pk[c]);
-  *l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  if (far_growth<F16, HELD>()) {
+    unpack_f32x2(add_f32x2(sum2[0], sum2[1]), &sum[0], &sum[1]);
+    float r0, r1;
+    unpack_f32x2(add_f32x2(rounded2[0], rounded2[1]), &r0, &r1);
+    l->rounded += r0 + r1;
+  }
+  l->l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
   ptx::tmem_wait_st();
   return true;
 }
 
 // 64 or 128 keys of one row, also with invisible keys (see: a bit a key), capped
-// scores, or a maximum that moves m; 32 keys at a time.  Returns {m, l}.
+// scores, or a maximum that moves m; 32 keys at a time.  Returns m and the sums.
+struct Softened {
+  float m;
+  Sum l;
+};
 template <bool F16, int HELD, int DP>
-__device__ __noinline__ float2 softmax_any(Score sc, Tail* sh, uint64_t* o_done, uint32_t parity,
+__device__ __noinline__ Softened softmax_any(Score sc, Tail* sh, uint64_t* o_done, uint32_t parity,
                                            int* status, uint32_t tm_s, uint32_t tm_o, int keys,
-                                           uint4 see, float mref, float l) {
+                                           uint4 see, float mref, Sum l) {
   const bool cap = sc.cap2 > 0.f;
   uint32_t any = 0;                              // whether the row sees one of the keys
   float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -921,7 +983,7 @@ __device__ __noinline__ float2 softmax_any(Score sc, Tail* sh, uint64_t* o_done,
       v[k + 1] = __float_as_uint(x[1]);
     }
   };
-  float sum[2] = {0.f, 0.f};
+  float sum[2] = {0.f, 0.f}, rounded[2] = {0.f, 0.f};
 #pragma unroll 1
   for (int c = 0; c < keys / 32; ++c) {
     const uint32_t m = c == 0 ? see.x : c == 1 ? see.y : c == 2 ? see.z : see.w;
@@ -953,11 +1015,14 @@ __device__ __noinline__ float2 softmax_any(Score sc, Tail* sh, uint64_t* o_done,
       sum[0] += p0;
       sum[1] += p1;
       pk[k] = pack2<F16>(p0, p1);
+      if (far_growth<F16, HELD>()) add_rounded(pk[k], &rounded[0], &rounded[1]);
     }
     ptx::tmem_st16(tm_s + 16 * c, pk);
   }
   ptx::tmem_wait_st();
-  return make_float2(mref, l + (sum[0] + sum[1]));
+  l.l += sum[0] + sum[1];
+  if (far_growth<F16, HELD>()) l.rounded += rounded[0] + rounded[1];
+  return {mref, l};
 }
 
 template <bool F16, int HELD, int DP>
@@ -1025,6 +1090,7 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
     const uint32_t* mask_row =
         a.mask ? a.mask + (int64_t)(s.row0 + node) * a.mask_stride : nullptr;
     float mref = -INFINITY, l = 0.f;
+    Sum sums;
     const int step = pair ? 1 : 2;
     const int keys = pair ? kHalf : kKeys;       // of one step
     for (int i = pair ? 0 : wg; i < n; i += step) {
@@ -1043,24 +1109,24 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
           if (done) {
             float x_max;
             auto plain = [&]() {
-              return pair ? softmax_plain<F16, HELD, kHalf>(sc.sl2, tm_s + h * kHalf, mref, &l, &x_max)
-                          : softmax_plain<F16, HELD, kKeys>(sc.sl2, tm_s, mref, &l, &x_max);
+              return pair ? softmax_plain<F16, HELD, kHalf>(sc.sl2, tm_s + h * kHalf, mref, &sums, &x_max)
+                          : softmax_plain<F16, HELD, kKeys>(sc.sl2, tm_s, mref, &sums, &x_max);
             };
             done = plain();
             if (HELD == kE2M1 && !done) {        // as long as m follows, the second time it fits
               mref = move_reference<F16, HELD, DP>(x_max, sh, o_done, phase & 1, a.status, tm_o + wg * 128,
-                                                   mref, &l);
+                                                   mref, &sums);
               done = plain();
             }
           }
           if (!done) {
-            const float2 r = softmax_any<F16, HELD, DP>(
+            const Softened r = softmax_any<F16, HELD, DP>(
                 sc, sh, o_done, phase & 1, a.status, tm_s + h * kHalf, tm_o + wg * 128, keys,
                 masked ? sees_128(mask_row, s.rows, node, pos0 - s.start)
                        : make_uint4(~0u, ~0u, ~0u, ~0u),
-                mref, l);
-            mref = r.x;
-            l = r.y;
+                mref, sums);
+            mref = r.m;
+            sums = r.l;
           }
           ptx::tc_fence_before();
         }
@@ -1071,6 +1137,13 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
       }
     }
 
+    // as O's weights add up to the rounded sum, m stands so much higher that the sum is the
+    // same: from here on m and l are any row's
+    l = sums.l;
+    if (far_growth<F16, HELD>() && sums.rounded > 0.f) {
+      mref += log2f(sums.l / sums.rounded);
+      l = sums.rounded;
+    }
     // the segment's result
     const int n1 = n / 2;                        // the second stream's tiles, not in pairs
     if (pair || wg < n) wait(sh, &sh->o_done[wg][0], (count0 - 1) & 1, a.status);
@@ -1179,9 +1252,9 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
 // REGS: the registers a thread that the roles' split counts on at launch.  In the
 // kernel's name, where the build checks it against what the compiler gave.
 template <bool F16, int HELD, int DP, int REGS>
-__global__ void __launch_bounds__(Roles<HELD != k16>::kThreads, 1)
+__global__ void __launch_bounds__(Roles<HELD>::kThreads, 1)
     attend_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ TileMaps maps) {
-  using R = Roles<HELD != k16>;
+  using R = Roles<HELD>;
   extern __shared__ __align__(1024) uint8_t smem[];
   Tail* sh = reinterpret_cast<Tail*>(smem + Layout<DP>::kTail);
   const int warp = threadIdx.x / 32;
@@ -1365,7 +1438,7 @@ constexpr size_t smem_bytes() {
 
 template <bool F16, int HELD, int DP>
 cudaError_t launch(const AttendArgs& a, const TileMaps& maps, cudaStream_t stream) {
-  using R = Roles<HELD != k16>;
+  using R = Roles<HELD>;
   // either kernel is launched while the one before it ends (the join: runs), and waits
   // for it itself before anything else
   cudaLaunchAttribute attr{};
@@ -1389,7 +1462,7 @@ cudaError_t launch(const AttendArgs& a, const TileMaps& maps, cudaStream_t strea
 template <bool F16, int HELD, int DP>
 cudaError_t setup() {
   static_assert(smem_bytes<DP>() <= 232448, "shared memory of an SM");
-  return cudaFuncSetAttribute(attend_kernel<F16, HELD, DP, Roles<HELD != k16>::kLaunchRegs>,
+  return cudaFuncSetAttribute(attend_kernel<F16, HELD, DP, Roles<HELD>::kLaunchRegs>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<DP>());
 }
 
