@@ -157,6 +157,13 @@ __device__ __noinline__ uint4 sees_128(const uint32_t* mask_row, int rows, int n
                     __funnelshift_r(x[2], x[3], j0 & 31), __funnelshift_r(x[3], x[4], j0 & 31));
 }
 
+using ptx::add_f32x2;
+using ptx::fma_f32x2;
+using ptx::mul_f32x2;
+using ptx::pack_f32x2;
+using ptx::sub_f32x2;
+using ptx::unpack_f32x2;
+
 // ------------------------------------------------------------- producers --
 
 // Byte offset of (row, 16-byte chunk) in a tile: 64-element blocks of 128 rows.
@@ -755,35 +762,6 @@ __device__ __noinline__ void add_nonfinite(const AttendArgs& a, const uint32_t* 
   }
 }
 
-// Two fp32 values at once.
-__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void unpack_f32x2(uint64_t x, float* lo, float* hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(x));
-}
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t sub_f32x2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 // Two values of at most 2^100 rounded to eight significant bits (Veltkamp's splitting):
 // upper halves that are theirs as bf16, without the conversion pipe and with their floats
 // at hand.

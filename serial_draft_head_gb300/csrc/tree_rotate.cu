@@ -22,14 +22,14 @@ namespace dspark {
 namespace tree {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kDepth = 5;          // rounds of a warp's loads in flight, a KB each
 
 // PLACE: k and v go to the cache, as HELD says; else k to out_k and there is no v.  `split`
 // warps a token.
 template <bool F16, bool PLACE, Held HELD, int LANES>
-__global__ void __launch_bounds__(kThreads, 3) rotate_kernel(const __grid_constant__ RotateArgs a, int split) {
+__global__ void __launch_bounds__(kThreads, 6) rotate_kernel(const __grid_constant__ RotateArgs a, int split) {
   __shared__ float2 turns[kWarps][8 * LANES];      // {cosine, sine} of the token's pairs
   __shared__ uint4 rows_in[kWarps][kDepth][2][32]; // each lane the chunks that it copied itself
   constexpr int kGroups = 32 / LANES;              // rows at a time
@@ -79,9 +79,9 @@ __global__ void __launch_bounds__(kThreads, 3) rotate_kernel(const __grid_consta
     turns[warp][f % 8 * LANES + f / 8] = make_float2(c, s);
   }
   __syncwarp();
-  // a pair (u, z) becomes r (u k0 - z k1), r (z k2 + u k3), r the norm's factor; a pair that
-  // is not turned r u k0, r z k2
-  float k0[8], k1[8], k2[8], k3[8];
+  // a pair (u, z), each times the norm's factor, becomes u k0 - z k1, z k2 + u k3; one that
+  // is not turned u k0, z k2.  Two pairs at once.
+  uint64_t k0[4], k1[4], k2[4], k3[4];
   bool of_k = true;                                // whose weights these are: none yet
   auto weigh = [&](bool key) {
     of_k = key;
@@ -101,12 +101,13 @@ __global__ void __launch_bounds__(kThreads, 3) rotate_kernel(const __grid_consta
       }
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float2 t = turned ? turns[warp][k * LANES + lane] : make_float2(1.f, 0.f);
-      k0[k] = w0[k] * t.x;
-      k1[k] = w1[k] * t.y;
-      k2[k] = w1[k] * t.x;
-      k3[k] = w0[k] * t.y;
+    for (int k = 0; k < 8; k += 2) {
+      const float2 s = turned ? turns[warp][k * LANES + lane] : make_float2(1.f, 0.f);
+      const float2 t = turned ? turns[warp][(k + 1) * LANES + lane] : make_float2(1.f, 0.f);
+      k0[k / 2] = ptx::pack_f32x2(w0[k] * s.x, w0[k + 1] * t.x);
+      k1[k / 2] = ptx::pack_f32x2(-w1[k] * s.y, -w1[k + 1] * t.y);
+      k2[k / 2] = ptx::pack_f32x2(w1[k] * s.x, w1[k + 1] * t.x);
+      k3[k / 2] = ptx::pack_f32x2(w0[k] * s.y, w0[k + 1] * t.y);
     }
   };
   weigh(false);
@@ -127,43 +128,57 @@ __global__ void __launch_bounds__(kThreads, 3) rotate_kernel(const __grid_consta
     if (!__all_sync(0xffffffffu, v)) {
       // the warp's rows are of q, of k, or of both: then each half in turn
       const bool some_q = __any_sync(0xffffffffu, q), some_k = __any_sync(0xffffffffu, !q && !v);
-      float u[8], z[8];
+      uint64_t u[4], z[4];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float lo = to_float<F16>((uint16_t)w[k]), hi = to_float<F16>((uint16_t)(w[k] >> 16));
-        if (a.pairs) {
-          u[k] = lo;
-          z[k] = hi;
-        } else {
-          (k < 4 ? u : z)[2 * (k % 4)] = lo;
-          (k < 4 ? u : z)[2 * (k % 4) + 1] = hi;
-        }
+      for (int k = 0; k < 4; ++k) {
+        // two words: the pairs 2 k and 2 k + 1
+        const uint32_t v0 = a.pairs ? w[2 * k] : w[k], v1 = a.pairs ? w[2 * k + 1] : w[4 + k];
+        const float a0 = to_float<F16>((uint16_t)v0), a1 = to_float<F16>((uint16_t)(v0 >> 16));
+        const float b0 = to_float<F16>((uint16_t)v1), b1 = to_float<F16>((uint16_t)(v1 >> 16));
+        u[k] = a.pairs ? ptx::pack_f32x2(a0, b0) : ptx::pack_f32x2(a0, a1);
+        z[k] = a.pairs ? ptx::pack_f32x2(a1, b1) : ptx::pack_f32x2(b0, b1);
       }
-      float r = 1.f;
       if (a.q_norm || a.k_norm) {
-        float sum = 0.f;
+        uint64_t squares = 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) sum = fmaf(u[k], u[k], fmaf(z[k], z[k], sum));
+        for (int k = 0; k < 4; ++k) squares = ptx::fma_f32x2(u[k], u[k], ptx::fma_f32x2(z[k], z[k], squares));
+        float sum, odd;
+        ptx::unpack_f32x2(squares, &sum, &odd);
+        sum += odd;
 #pragma unroll
         for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (q ? a.q_norm != nullptr : a.k_norm != nullptr) r = rsqrtf(sum * a.inv_dim + a.eps);
+        if (q ? a.q_norm != nullptr : a.k_norm != nullptr) {
+          const float r = rsqrtf(sum * a.inv_dim + a.eps);
+          const uint64_t r2 = ptx::pack_f32x2(r, r);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            u[k] = ptx::mul_f32x2(u[k], r2);
+            z[k] = ptx::mul_f32x2(z[k], r2);
+          }
+        }
       }
 #pragma unroll 1
       for (int side = 0; side < 2; ++side) {
         if (!(side ? some_k : some_q)) continue;
         if (of_k != (side == 1)) weigh(side == 1);
         if (v || q == (side == 1)) continue;
-        float y0[8], y1[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          y0[k] = turned ? r * fmaf(u[k], k0[k], -z[k] * k1[k]) : r * (u[k] * k0[k]);
-          y1[k] = turned ? r * fmaf(z[k], k2[k], u[k] * k3[k]) : r * (z[k] * k2[k]);
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int j = 2 * (k % 4);
-          w[k] = a.pairs ? pack2<F16>(y0[k], y1[k])
-                         : k < 4 ? pack2<F16>(y0[j], y0[j + 1]) : pack2<F16>(y1[j], y1[j + 1]);
+        for (int k = 0; k < 4; ++k) {
+          uint64_t y0 = ptx::mul_f32x2(u[k], k0[k]), y1 = ptx::mul_f32x2(z[k], k2[k]);
+          if (turned) {
+            y0 = ptx::fma_f32x2(z[k], k1[k], y0);
+            y1 = ptx::fma_f32x2(u[k], k3[k], y1);
+          }
+          float a0, a1, b0, b1;
+          ptx::unpack_f32x2(y0, &a0, &a1);
+          ptx::unpack_f32x2(y1, &b0, &b1);
+          if (a.pairs) {
+            w[2 * k] = pack2<F16>(a0, b0);
+            w[2 * k + 1] = pack2<F16>(a1, b1);
+          } else {
+            w[k] = pack2<F16>(a0, a1);
+            w[4 + k] = pack2<F16>(b0, b1);
+          }
         }
       }
     }
