@@ -26,17 +26,17 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kDepth = 5;          // rounds of a warp's loads in flight, a KB each
 
-// PLACE: k and v go to the cache, as HELD says; else k to out_k and there is no v.  `split`
+// PLACE: k and v go to the cache, as HELD says; else k to out_k and there is no v.  2^`shift`
 // warps a token.
 template <bool F16, bool PLACE, Held HELD, int LANES>
-__global__ void __launch_bounds__(kThreads, 6) rotate_kernel(const __grid_constant__ RotateArgs a, int split) {
+__global__ void __launch_bounds__(kThreads, 6) rotate_kernel(const __grid_constant__ RotateArgs a, int shift) {
   __shared__ float2 turns[kWarps][8 * LANES];      // {cosine, sine} of the token's pairs
   __shared__ uint4 rows_in[kWarps][kDepth][2][32]; // each lane the chunks that it copied itself
   constexpr int kGroups = 32 / LANES;              // rows at a time
   const int warp = threadIdx.x / 32, wl = threadIdx.x % 32, lane = wl % LANES, group = wl / LANES;
   const int64_t job = (int64_t)blockIdx.x * kWarps + warp;
-  const int n = (int)(job / split), share = (int)(job - (int64_t)n * split);
-  if (n >= a.N) return;
+  if (job >> shift >= a.N) return;
+  const int n = (int)(job >> shift), share = (int)(job & ((1 << shift) - 1));
   int64_t page = 0;
   int place = 0;
   if (PLACE) {
@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kThreads, 6) rotate_kernel(const __grid_consta
   // the lane's two chunks
   const int c0 = turned ? (a.pairs ? 2 * lane : lane) : 2 * lane;
   const int c1 = turned && !a.pairs ? lane + half : c0 + 1;
-  const int heads = a.Hq + a.Hkv * (PLACE ? 2 : 1), step = split * kGroups;
+  const int heads = a.Hq + a.Hkv * (PLACE ? 2 : 1), step = kGroups << shift;
   uint4 x[2];
   int in = 0;
   auto load = [&](int h) {
@@ -223,11 +223,11 @@ template <bool F16, bool PLACE, Held HELD, int LANES>
 void launch(const RotateArgs& a, int sm_count, cudaStream_t stream) {
   // a token's heads over as many warps as give every SM 16, at least two rounds each
   const int heads = a.Hq + a.Hkv * (PLACE ? 2 : 1), rounds = (heads + 32 / LANES - 1) / (32 / LANES);
-  int split = 1;
-  while (2 * split <= rounds && (int64_t)a.N * split < (int64_t)16 * sm_count) split *= 2;
-  const int64_t jobs = (int64_t)a.N * split;
+  int shift = 0;
+  while (2 << shift <= rounds && (int64_t)a.N << shift < (int64_t)16 * sm_count) ++shift;
+  const int64_t jobs = (int64_t)a.N << shift;
   rotate_kernel<F16, PLACE, HELD, LANES>
-      <<<(unsigned)((jobs + kWarps - 1) / kWarps), kThreads, 0, stream>>>(a, split);
+      <<<(unsigned)((jobs + kWarps - 1) / kWarps), kThreads, 0, stream>>>(a, shift);
 }
 
 template <bool F16, bool PLACE, Held HELD>

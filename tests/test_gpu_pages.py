@@ -285,3 +285,36 @@ def test_rounds_together(Pages, tree, held, dtype):
             assert (off <= top * 1.13 / 6 + 2.0 ** -17).all()
             value, byte = e2m1.quantise(raw_v)
             assert torch.equal(got_v.double(), value * e2m1.scale_of(byte).repeat_interleave(16, -1))
+
+
+@pytest.mark.parametrize("cache,rotary", [("e2m1", False), ("e2m1", True), ("e4m3", True), ("16", True)])
+def test_example_runs(tree, cache, rotary):
+    """The example's loop over a 4-bit cache, and with pages from the pool and turned heads: it ends with the
+    requests' rows in the cache, and with no more pages held than they need."""
+    import os
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    sys.path.insert(0, os.path.join(root, "examples"))
+    try:
+        import draft_and_check as ex
+    finally:
+        sys.path.pop(0)
+    target = ex.Target(vocab=2048)
+    texts, cached, pages, length = ex.decode(target, [5, 9, 77], rounds=4, gamma=5, cache=cache, rotary=rotary)
+    assert [len(t) - 1 for t in texts] == length.tolist()
+    if rotary:
+        assert (pages >= 0).sum(1).tolist() == [-(-n // 16) for n in length.tolist()]
+    t = tree.Tree(8, 2, 64, max_requests=3)
+    n = int(length.sum())
+    first = torch.tensor([0] + length.cumsum(0).tolist(), dtype=torch.int32, device="cuda")
+    k, v = t.read(cached, pages, torch.zeros_like(length), first, n)
+    assert t.status() == 0
+    tokens = torch.tensor([x for text in texts for x in text[:-1]], device="cuda")
+    if cache == "e2m1":
+        value, byte = e2m1.quantise(target.v[tokens])
+        assert torch.equal(v.double(), value * e2m1.scale_of(byte).repeat_interleave(16, -1))
+    elif cache == "16":
+        assert torch.equal(v, target.v[tokens])
+    if not rotary:
+        value, byte = e2m1.quantise(target.k[tokens])
+        assert torch.equal(k.double(), value * e2m1.scale_of(byte).repeat_interleave(16, -1))
