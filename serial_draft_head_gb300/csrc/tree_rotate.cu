@@ -53,15 +53,15 @@ __global__ void __launch_bounds__(kThreads, 6) rotate_kernel(const __grid_consta
   // the lane's two chunks
   const int c0 = turned ? (a.pairs ? 2 * lane : lane) : 2 * lane;
   const int c1 = turned && !a.pairs ? lane + half : c0 + 1;
-  const int heads = a.Hq + a.Hkv * (PLACE ? 2 : 1), step = kGroups << shift;
-  uint4 x[2];
+  // rounds: kGroups heads each, those of q, then k, then v
+  const int of_q = (a.Hq + kGroups - 1) / kGroups, of_kv = (a.Hkv + kGroups - 1) / kGroups;
+  const int rounds = of_q + of_kv * (PLACE ? 2 : 1), step = 1 << shift;
   int in = 0;
-  auto load = [&](int h) {
-    if (in_row && h < heads) {
-      const int i = h < a.Hq ? 0 : h < a.Hq + a.Hkv ? 1 : 2;
-      const int head = h - (i == 0 ? 0 : i == 1 ? a.Hq : a.Hq + a.Hkv);
-      const uint4* src = reinterpret_cast<const uint4*>(a.src[i] + (int64_t)n * a.src_row[i] +
-                                                        head * a.src_head[i]);
+  auto load = [&](int round) {
+    const int i = round < of_q ? 0 : round < of_q + of_kv ? 1 : 2;
+    const int head = (round - (i == 0 ? 0 : i == 1 ? of_q : of_q + of_kv)) * kGroups + group;
+    if (in_row && round < rounds && head < (i == 0 ? a.Hq : a.Hkv)) {
+      const uint4* src = reinterpret_cast<const uint4*>(a.src[i] + n * a.src_row[i] + head * a.src_head[i]);
       ptx::cp_async16(&rows_in[warp][in][0][wl], src + (i == 2 ? 2 * lane : c0));
       ptx::cp_async16(&rows_in[warp][in][1][wl], src + (i == 2 ? 2 * lane + 1 : c1));
     }
@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kThreads, 6) rotate_kernel(const __grid_consta
     if (++in == kDepth) in = 0;
   };
 #pragma unroll
-  for (int i = 0; i < kDepth - 1; ++i) load(share * kGroups + group + i * step);
+  for (int i = 0; i < kDepth - 1; ++i) load(share + i * step);
   const int64_t pos = __ldg(a.position + n);
   for (int f = wl; f < a.R / 2; f += 32) {
     const int32_t part = (int32_t)((uint64_t)pos * __ldg(a.turns + f) >> 32);
@@ -82,9 +82,7 @@ __global__ void __launch_bounds__(kThreads, 6) rotate_kernel(const __grid_consta
   // a pair (u, z), each times the norm's factor, becomes u k0 - z k1, z k2 + u k3; one that
   // is not turned u k0, z k2.  Two pairs at once.
   uint64_t k0[4], k1[4], k2[4], k3[4];
-  bool of_k = true;                                // whose weights these are: none yet
   auto weigh = [&](bool key) {
-    of_k = key;
     const float* norm = key ? a.k_norm : a.q_norm;
     float w0[8], w1[8];
 #pragma unroll
@@ -110,24 +108,25 @@ __global__ void __launch_bounds__(kThreads, 6) rotate_kernel(const __grid_consta
       k3[k / 2] = ptx::pack_f32x2(w0[k] * s.y, w0[k + 1] * t.y);
     }
   };
-  weigh(false);
+  int weights = -1;                                // whose they are: of q 0, of k 1
 #pragma unroll 1
-  for (int h0 = share * kGroups; h0 < heads; h0 += step) {   // whole warps stay in: the shuffles
-    const int h = h0 + group;
-    load(h + (kDepth - 1) * step);
+  for (int round = share; round < rounds; round += step) {
+    load(round + (kDepth - 1) * step);
     ptx::cp_async_wait_group<kDepth - 1>();
-    const int out = in;                            // the oldest
-    x[0] = x[1] = make_uint4(0, 0, 0, 0);
-    if (in_row && h < heads) {
-      x[0] = rows_in[warp][out][0][wl];
-      x[1] = rows_in[warp][out][1][wl];
+    const int i = round < of_q ? 0 : round < of_q + of_kv ? 1 : 2;       // the warp's rows are of one kind
+    const int head = (round - (i == 0 ? 0 : i == 1 ? of_q : of_q + of_kv)) * kGroups + group;
+    const bool live = head < (i == 0 ? a.Hq : a.Hkv);
+    uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (in_row && live) {
+      x[0] = rows_in[warp][in][0][wl];             // the oldest
+      x[1] = rows_in[warp][in][1][wl];
     }
-    const bool q = h < a.Hq, v = PLACE && h >= a.Hq + a.Hkv, live = h < heads;
-    const int head = q ? h : v ? h - a.Hq - a.Hkv : h - a.Hq;
     uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
-    if (!__all_sync(0xffffffffu, v)) {
-      // the warp's rows are of q, of k, or of both: then each half in turn
-      const bool some_q = __any_sync(0xffffffffu, q), some_k = __any_sync(0xffffffffu, !q && !v);
+    if (i < 2) {
+      if (weights != i) {
+        weights = i;
+        weigh(i == 1);
+      }
       uint64_t u[4], z[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -138,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 6) rotate_kernel(const __grid_consta
         u[k] = a.pairs ? ptx::pack_f32x2(a0, b0) : ptx::pack_f32x2(a0, a1);
         z[k] = a.pairs ? ptx::pack_f32x2(a1, b1) : ptx::pack_f32x2(b0, b1);
       }
-      if (a.q_norm || a.k_norm) {
+      if (i == 0 ? a.q_norm != nullptr : a.k_norm != nullptr) {
         uint64_t squares = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) squares = ptx::fma_f32x2(u[k], u[k], ptx::fma_f32x2(z[k], z[k], squares));
@@ -147,55 +146,46 @@ __global__ void __launch_bounds__(kThreads, 6) rotate_kernel(const __grid_consta
         sum += odd;
 #pragma unroll
         for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (q ? a.q_norm != nullptr : a.k_norm != nullptr) {
-          const float r = rsqrtf(sum * a.inv_dim + a.eps);
-          const uint64_t r2 = ptx::pack_f32x2(r, r);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            u[k] = ptx::mul_f32x2(u[k], r2);
-            z[k] = ptx::mul_f32x2(z[k], r2);
-          }
-        }
-      }
-#pragma unroll 1
-      for (int side = 0; side < 2; ++side) {
-        if (!(side ? some_k : some_q)) continue;
-        if (of_k != (side == 1)) weigh(side == 1);
-        if (v || q == (side == 1)) continue;
+        const float r = rsqrtf(sum * a.inv_dim + a.eps);
+        const uint64_t r2 = ptx::pack_f32x2(r, r);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          uint64_t y0 = ptx::mul_f32x2(u[k], k0[k]), y1 = ptx::mul_f32x2(z[k], k2[k]);
-          if (turned) {
-            y0 = ptx::fma_f32x2(z[k], k1[k], y0);
-            y1 = ptx::fma_f32x2(u[k], k3[k], y1);
-          }
-          float a0, a1, b0, b1;
-          ptx::unpack_f32x2(y0, &a0, &a1);
-          ptx::unpack_f32x2(y1, &b0, &b1);
-          if (a.pairs) {
-            w[2 * k] = pack2<F16>(a0, b0);
-            w[2 * k + 1] = pack2<F16>(a1, b1);
-          } else {
-            w[k] = pack2<F16>(a0, a1);
-            w[4 + k] = pack2<F16>(b0, b1);
-          }
+          u[k] = ptx::mul_f32x2(u[k], r2);
+          z[k] = ptx::mul_f32x2(z[k], r2);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint64_t y0 = ptx::mul_f32x2(u[k], k0[k]), y1 = ptx::mul_f32x2(z[k], k2[k]);
+        if (turned) {
+          y0 = ptx::fma_f32x2(z[k], k1[k], y0);
+          y1 = ptx::fma_f32x2(u[k], k3[k], y1);
+        }
+        float a0, a1, b0, b1;
+        ptx::unpack_f32x2(y0, &a0, &a1);
+        ptx::unpack_f32x2(y1, &b0, &b1);
+        if (a.pairs) {
+          w[2 * k] = pack2<F16>(a0, b0);
+          w[2 * k + 1] = pack2<F16>(a1, b1);
+        } else {
+          w[k] = pack2<F16>(a0, a1);
+          w[4 + k] = pack2<F16>(b0, b1);
         }
       }
     }
-    const bool cached = PLACE && !q;
-    if (!cached || HELD == k16) {
+    if (!PLACE || i == 0 || HELD == k16) {
       if (live && in_row) {
-        uint4* dst = !cached ? reinterpret_cast<uint4*>((q ? a.out_q : a.out_k) +
-                                                        ((int64_t)n * (q ? a.Hq : a.Hkv) + head) * a.D)
-                             : reinterpret_cast<uint4*>(a.c.x[v].at((uint32_t)page, place, head));
-        dst[v ? 2 * lane : c0] = make_uint4(w[0], w[1], w[2], w[3]);
-        dst[v ? 2 * lane + 1 : c1] = make_uint4(w[4], w[5], w[6], w[7]);
+        uint4* dst;
+        if (PLACE && i > 0) dst = reinterpret_cast<uint4*>(a.c.x[i - 1].at((uint32_t)page, place, head));
+        else dst = reinterpret_cast<uint4*>((i ? a.out_k : a.out_q) + ((int64_t)n * (i ? a.Hkv : a.Hq) + head) * a.D);
+        dst[i == 2 ? 2 * lane : c0] = make_uint4(w[0], w[1], w[2], w[3]);
+        dst[i == 2 ? 2 * lane + 1 : c1] = make_uint4(w[4], w[5], w[6], w[7]);
       }
+      continue;
     }
     if constexpr (PLACE && HELD != k16) {
-      if (!__any_sync(0xffffffffu, cached)) continue;
-      // a row of k as it lies: lane i chunks 2 i and 2 i + 1
-      if (!a.pairs) {
+      if (i == 1 && !a.pairs) {
+        // a row of k as it lies: lane i chunks 2 i and 2 i + 1
         uint32_t natural[8];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -210,11 +200,11 @@ __global__ void __launch_bounds__(kThreads, 6) rotate_kernel(const __grid_consta
           }
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] = v ? w[k] : natural[k];
+        for (int k = 0; k < 8; ++k) w[k] = natural[k];
       }
-      store_codes<F16, HELD, LANES>(w, a.c.x[v].at((uint32_t)page, place, cached ? head : 0),
-                                    a.c.scale[v].at((uint32_t)page, place, cached ? head : 0), lane,
-                                    live && cached && in_row, live && cached);
+      const int to = live ? head : 0;
+      store_codes<F16, HELD, LANES>(w, a.c.x[i - 1].at((uint32_t)page, place, to),
+                                    a.c.scale[i - 1].at((uint32_t)page, place, to), lane, live && in_row, live);
     }
   }
 }
@@ -222,7 +212,9 @@ __global__ void __launch_bounds__(kThreads, 6) rotate_kernel(const __grid_consta
 template <bool F16, bool PLACE, Held HELD, int LANES>
 void launch(const RotateArgs& a, int sm_count, cudaStream_t stream) {
   // a token's heads over as many warps as give every SM 16, at least two rounds each
-  const int heads = a.Hq + a.Hkv * (PLACE ? 2 : 1), rounds = (heads + 32 / LANES - 1) / (32 / LANES);
+  constexpr int kGroups = 32 / LANES;
+  const int of_kv = (a.Hkv + kGroups - 1) / kGroups;
+  const int rounds = (a.Hq + kGroups - 1) / kGroups + of_kv * (PLACE ? 2 : 1);
   int shift = 0;
   while (2 << shift <= rounds && (int64_t)a.N << shift < (int64_t)16 * sm_count) ++shift;
   const int64_t jobs = (int64_t)a.N << shift;
