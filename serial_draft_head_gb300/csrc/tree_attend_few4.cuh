@@ -34,6 +34,12 @@
 // Keys stand in the products' rows in the order `row_key`, so that the rows that lanes
 // read together lie in different banks.  Rows of Q are brought to f16 by a power of two
 // a row.
+//
+// What bounds it.  128 single tokens of 500 to 9,000 (64 heads on 8): 150 us, 4.8 TB/s;
+// 700 warp instructions a block, issued at 64% of the slots, held by fixed latencies and
+// the pipes of the conversions and 16-bit products (without the products: 125).  19
+// requests of 32,767: 128 us, 5.6 TB/s.  Items of 32 rows (16 chains of 8 over 300 to 6,000
+// with 4 heads on one: 74 us): two warps a scheduler, issued at 28%.
 #pragma once
 
 #include "tree_items.cuh"

@@ -15,6 +15,12 @@
 //
 // Everything between the loads and the stores is fp32; k is rounded to the handle's type
 // before it is quantised, as if it had been stored and written.
+//
+// What bounds it: memory.  32,284 tokens of 32 + 8 + 8 heads of 128: into a 16-bit cache 132
+// us, 6.0 TB/s of bytes read and written; q and k alone 105 us, 6.3; into e2m1 148 (the
+// quantising).  With the next rows in registers instead of five rounds of copies into
+// shared memory 172.  128 tokens: 4.6 us, a chain of the slot, the position, the angles and
+// the rows.
 #include "tc_ptx.cuh"
 #include "tree_codes.cuh"
 
