@@ -603,17 +603,19 @@ __global__ void __launch_bounds__(Few4<DP, NT, GROUP, RUNS>::kThreads, 1)
             for (int k = 0; k < 4; ++k) x[nt][2 * (m0 + mt) + k / 2][k % 2] = acc[mt][nt][k];
       }
       // invisible scores -infinity; see: bit 8 i, the row sees key 8 i + row_key(g)
-      uint32_t see[NT][2];
+      uint32_t see[NT][2], of_row = ~0u;         // of row `lane`, all 32 keys
+      if (masked) {
+        const int row = lane % L::kRows, nd = a.group.div(s.group * L::kRows + (row < rows ? row : 0));
+        of_row = sees_32(a.mask ? a.mask + (int64_t)(s.row0 + nd) * a.mask_stride : nullptr, s.rows, nd,
+                         pos0 - start);
+      }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           see[nt][e] = 0x01010101u;
           if (masked) {
-            const int row = 8 * nt + 2 * q + e;
-            const int nd = a.group.div(s.group * L::kRows + (row < rows ? row : 0));
-            see[nt][e] = sees_32(a.mask ? a.mask + (int64_t)(s.row0 + nd) * a.mask_stride : nullptr,
-                                 s.rows, nd, pos0 - start) >> gk & 0x01010101u;
+            see[nt][e] = __shfl_sync(0xffffffffu, of_row, 8 * nt + 2 * q + e) >> gk & 0x01010101u;
 #pragma unroll
             for (int i = 0; i < kParts; ++i)
               if (!(see[nt][e] >> (8 * i) & 1)) x[nt][i][e] = -INFINITY;
@@ -648,12 +650,14 @@ __global__ void __launch_bounds__(Few4<DP, NT, GROUP, RUNS>::kThreads, 1)
                 kept_sub[nt % kKept][e] = mref[nt][e];
                 kept_limit[nt % kKept][e] = y + 8.f;
               }
-              const float back = old == -INFINITY ? 0.f : ex2(old - mref[nt][e]);
-              l[nt][e] *= back;
+              if (t >= s.t0 + GROUP) {           // not the warp's first block: O and l are zeros there
+                const float back = old == -INFINITY ? 0.f : ex2(old - mref[nt][e]);
+                l[nt][e] *= back;
 #pragma unroll
-              for (int t8 = 0; t8 < kTiles; ++t8) {
-                o[nt][t8][e] *= back;
-                o[nt][t8][2 + e] *= back;
+                for (int t8 = 0; t8 < kTiles; ++t8) {
+                  o[nt][t8][e] *= back;
+                  o[nt][t8][2 + e] *= back;
+                }
               }
             }
           }
