@@ -102,10 +102,12 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(const __grid_constant__ 
   __shared__ Sums s;
   const dspark_pages& p = a.p;
   const int R = p.requests, page = p.page_size;
-  const int n_free = *p.n_free;
+  const int counted = *p.n_free;
+  const bool miscounted = counted < 0 || counted > p.n_pages;   // then none is handed out
+  const int n_free = miscounted ? 0 : counted;
   if (threadIdx.x == 0) s.total = 0;
   int length[kPer], rows[kPer], need[kPer], held[kPer];
-  bool bad[kPer], wrong = false;
+  bool bad[kPer], wrong = miscounted;
   long long sum[2] = {0, 0};
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
@@ -193,7 +195,7 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(const __grid_constant__ 
       const int r = threadIdx.x * kPer + k;
       if (r < R && need[k] > 0 && s.held[r] >= 0) p.held[r] = held[k] + need[k];
     }
-    if (threadIdx.x == 0) *p.n_free = n_free - total;
+    if (threadIdx.x == 0 && total > 0) *p.n_free = n_free - total;
   }
 }
 

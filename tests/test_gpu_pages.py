@@ -201,6 +201,32 @@ def test_refusals(Pages):
     assert first.tolist() == [0, 0, 0, 0] and len(slot) == len(position) == 0 and pool.status() == 0
 
 
+@pytest.mark.parametrize("n", [-1, 9, 2 ** 31 - 1])
+def test_a_wrong_count_of_free_pages_hands_none_out(Pages, n):
+    """A count that the pool cannot have, and a table that holds what is no page: reported, nothing given."""
+    from serial_draft_head_gb300 import walk
+    pool = Pages(8, 16, 3, 4)
+    before = [x.clone() for x in (pool.table, pool.held, pool.free)]
+    pool.n_free.fill_(n)
+    z, c = ints([0, 0, 0]), ints([20, 1, 0])
+    first, slot, position = pool.grow(z, c, 21)
+    assert pool.status() == walk.EPAGES
+    assert first.tolist() == [0, 20, 21, 21] and (slot == -1).all() and position.tolist() == list(range(20)) + [0]
+    pool.trim(z)
+    assert all(torch.equal(x, y) for x, y in zip(before, (pool.table, pool.held, pool.free))) and pool.n_free.item() == n
+    pool.status()
+    pool.reset()
+    pool.held.fill_(5)                                 # more than a request's row has
+    first, slot, position = pool.grow(z, c, 21)
+    assert pool.status() == walk.EPAGES and (slot == -1).all()
+    pool.trim(z)
+    assert pool.status() == walk.EPAGES and pool.n_free.item() == 8
+    pool.reset()
+    pool.held.fill_(1)                                 # held, but -1 in the table
+    first, slot, position = pool.grow(z, c, 21)
+    assert pool.status() == walk.EPAGES and (slot[:16] == -1).all() and (slot[16:20] >= 0).all()
+
+
 @pytest.mark.parametrize("held", ["e2m1", "e4m3", "16"])
 @pytest.mark.parametrize("dtype", [BF16, F16])
 def test_rounds_together(Pages, tree, held, dtype):
