@@ -453,29 +453,32 @@ __device__ __forceinline__ void produce8(const AttendArgs& a, uint8_t* smem, Tai
   if (worst > top_page) set_status(a.status, DSPARK_EPAGES);
 }
 
-// e2m1 cache, through registers, as e4m3: a lane has the 16 codes of a block, 8 bytes,
-// of several rows, and multiplies them by their scale, exactly.  A warp has 16 rows of the
-// tile; two lanes look a row's page up, ask for half of its scales each, and hand both
-// round.  K and V have registers of their own, so that what is asked for is used a whole
-// tile later.
+// e2m1 cache, through registers, as e4m3: a lane has 32 codes, two blocks, of one or two
+// rows and multiplies them by their scales, exactly.  A warp has 16 rows of the tile; two
+// lanes look a row's page up, ask for half of its scales each, and hand both round.  K and
+// V have registers of their own, so that what is asked for is used a whole tile later.
 template <bool F16, int DP>
 __device__ __forceinline__ void produce4(const AttendArgs& a, uint8_t* smem, Tail* sh) {
   using L = Layout<DP>;
   constexpr int kWarps = Roles<kE2M1>::kProdWarps;
-  constexpr int kChunks = DP / 16;               // blocks of a row
-  constexpr int kWarpRows = 32 / kChunks;
+  constexpr int kLanes = DP / 32;                // of a row
+  constexpr int kWarpRows = 32 / kLanes;
   constexpr int kRows = kWarps * kWarpRows;      // rows a pass
   constexpr int kPasses = kKeys / kRows;
   constexpr int kAhead = 4;
   static_assert(kWarps * 32 == 2 * kKeys, "one row of K or V a thread");
   static_assert(kPasses * kWarpRows == 16, "16 rows a warp");
   const int tid = threadIdx.x - kSoftWarps * 32, lane = tid % 32, warp = tid / 32;
-  // as in produce8: eight lanes store to all banks once
-  const int chunk = (lane & 3) | (DP == 128 ? (lane >> 1) & 4 : 0);
-  const int w0 = DP == 128 ? ((lane >> 2) & 1) | ((lane >> 3) & 2) : lane >> 2;
-  const int r0 = warp * kWarpRows + w0;
-  const bool in_dim = chunk * 16 < a.D;
-  const uint32_t to0 = tile_offset(r0, 2 * chunk), to1 = tile_offset(r0, 2 * chunk + 1);
+  // Eight lanes store to all banks once: of 128 elements two rows whose numbers differ by two,
+  // and in their second 64 elements, which lie behind the same banks, each pair of 16-byte
+  // chunks the other way round.
+  const int part = lane % kLanes, i0 = lane / kLanes;
+  const int w0 = DP == 128 ? (i0 & 4) | (i0 & 1) << 1 | (i0 >> 1 & 1) : i0;
+  const int r0 = warp * kWarpRows + w0, turn = DP == 128 ? part >> 1 : 0;
+  const bool in_dim = part * 32 < a.D;
+  uint32_t to[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) to[k] = tile_offset(r0, 4 * part + (k ^ turn));
   // row lane / 2 of the warp's, and which half of its scales
   const int own = lane / 2, half = lane & 1;
   const int own_row = own / kWarpRows * kRows + warp * kWarpRows + own % kWarpRows;
@@ -520,31 +523,31 @@ __device__ __forceinline__ void produce4(const AttendArgs& a, uint8_t* smem, Tai
     ask_slot = pos - at * a.c.page.d;
   };
   struct Part {
-    uint2 x[kPasses];
+    uint4 x[kPasses];
     uint32_t scales;                             // four bytes of row `own`
   };
-  auto load = [&](Part& part, int v, int head) {
+  auto load = [&](Part& half_tile, int v, int head) {
     const Rows rows = a.c.x[v];
-    const uint8_t* src = rows.of_head(head) + (in_dim ? chunk * 8 : 0);
+    const uint8_t* src = rows.of_head(head) + (in_dim ? part * 16 : 0);
     const uint8_t* sc = a.c.scale[v].at(page, slot, head) + (own_in ? half * 4 : 0);
     if (a.D % 64 == 0) {
-      part.scales = __ldg(reinterpret_cast<const uint32_t*>(sc));
+      half_tile.scales = __ldg(reinterpret_cast<const uint32_t*>(sc));
     } else {                                     // heads of 32 and 96: two bytes at their end
-      part.scales = __ldg(reinterpret_cast<const uint16_t*>(sc));
+      half_tile.scales = __ldg(reinterpret_cast<const uint16_t*>(sc));
       if (half * 64 + 32 < a.D)
-        part.scales |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(sc) + 1) << 16;
+        half_tile.scales |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(sc) + 1) << 16;
     }
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
       const int from = 2 * (i * kWarpRows + w0);
       const uint32_t p = __shfl_sync(0xffffffffu, page, from);
       const int s = __shfl_sync(0xffffffffu, slot, from);
-      part.x[i] = __ldg(reinterpret_cast<const uint2*>(src + rows.offset(p, s)));
+      half_tile.x[i] = ptx::ldg_nc_na(src + rows.offset(p, s));
     }
   };
   RingPos<L::kSlots> at;
-  auto convert = [&](const Part& part, bool v, const Tile& tile) {
-    uint32_t scales = part.scales;
+  auto convert = [&](const Part& half_tile, bool v, const Tile& tile) {
+    uint32_t scales = half_tile.scales;
     if (own_row >= tile.rows) scales = 0;        // rows past the end are zeros
     if (v && tile.draft < kKeys) {               // draft rows: zeros for blocks that are no numbers
       const uint32_t over = __vcmpgtu4(scales, kTopScale * 0x01010101u);
@@ -558,10 +561,17 @@ __device__ __forceinline__ void produce4(const AttendArgs& a, uint8_t* smem, Tai
     uint8_t* dst = ring + at.slot * L::kTile;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-      const uint32_t four = __shfl_sync(0xffffffffu, scales, 2 * (i * kWarpRows + w0) + chunk / 4);
-      const uint32_t s = e2m1_mul2<F16>(in_dim ? four >> (chunk % 4 * 8) & 0xffu : 0u);
-      *reinterpret_cast<uint4*>(dst + to0 + i * kRows * 128) = e2m1x8_times<F16>(part.x[i].x, s);
-      *reinterpret_cast<uint4*>(dst + to1 + i * kRows * 128) = e2m1x8_times<F16>(part.x[i].y, s);
+      const uint32_t four = __shfl_sync(0xffffffffu, scales, 2 * (i * kWarpRows + w0) + part / 2);
+      const uint32_t two = in_dim ? four >> (part % 2 * 16) : 0u;
+      const uint4 x = half_tile.x[i];
+      const uint32_t w[4] = {turn ? x.y : x.x, turn ? x.x : x.y, turn ? x.w : x.z, turn ? x.z : x.w};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t s = e2m1_mul2<F16>(two >> (8 * h) & 0xffu);
+#pragma unroll
+        for (int k = 2 * h; k < 2 * h + 2; ++k)
+          *reinterpret_cast<uint4*>(dst + to[k] + i * kRows * 128) = e2m1x8_times<F16>(w[k], s);
+      }
     }
     ptx::fence_proxy_async_smem();
     __syncwarp();
