@@ -38,8 +38,8 @@
 // chain softmax - product - next S of two streams, and 15 us an item for Q, the
 // masked tiles and the result.  17 nodes over 131,000 tokens: 99 us, 5.4 TB/s.
 // 16 requests of 8 nodes: 60 us, 2.9 TB/s, the ring's five slots against the
-// copies' latency (long scoreboard 7.2 of 15 warp cycles an issue).  64 x 64 over e2m1: 475
-// us (without the producers' loads 427, without their conversions too 390).
+// copies' latency (long scoreboard 7.2 of 15 warp cycles an issue).  64 x 64 over e2m1: 462
+// us (at 495: without the producers' loads 427, without their conversions too 390).
 #pragma once
 
 #include "tree_items.cuh"
@@ -63,7 +63,8 @@ struct Roles {
   static constexpr int kThreads = (kMmaWarp + 4) * 32;
   static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
   static constexpr int kSoftRegs = kCodes ? 120 : 184;
-  // e2m1, 64 x 64: producers 88 and products 64 477 us, 96 and 48 519
+  // e2m1, 64 x 64: producers 88 and products 64 477 us, 96 and 48 519, while the latter
+  // had registers to spill
   static constexpr int kProdRegs = HELD == kE4M3 ? 96 : 88;
   static constexpr int kMmaRegs = HELD == kE4M3 ? 48 : HELD == kE2M1 ? 64 : 56;
   static constexpr int kSplit =
