@@ -158,8 +158,16 @@ class KVCache:
         return cls(*x)
 
 
-# 1 / (2 pi), to 2^-150
+# 1 / (2 pi), to 2^-150, and as a fraction of 2^256
 _TURN = Fraction(15915494309189533576888376337251436203445964574, 10 ** 47)
+_TURN_256 = round(_TURN * 2 ** 256)
+
+
+def _turns(f):
+    """The turns of f radians, a float, as a fraction of 2^64; whole ones do not count."""
+    n, d = f.as_integer_ratio()                      # d is a power of two
+    shift = 256 - 64 + d.bit_length() - 1
+    return ((n * _TURN_256 + (1 << (shift - 1))) >> shift) % 2 ** 64
 
 
 class Rotation:
@@ -182,7 +190,7 @@ class Rotation:
         _need(head_dim % 16 == 0 and len(f) % 8 == 0 and 2 * len(f) <= head_dim,
               "head_dim and R are multiples of 16, R at most head_dim")
         _need(eps >= 0.0 and math.isfinite(eps), "eps is a number from 0 on")
-        turns = [round((Fraction(x) * _TURN % 1) * 2 ** 64) % 2 ** 64 for x in f]
+        turns = [_turns(x) for x in f]
         self.turns = torch.tensor([x - 2 ** 64 if x >= 2 ** 63 else x for x in turns],
                                   dtype=torch.int64).to(device)
         norms = []

@@ -113,6 +113,7 @@ def test_frequencies_become_turns():
     assert abs(tree._TURN * 2 * pi - 1) < Fraction(1, 2 ** 150)
     for f in (1.0, 1e-4, 0.7943, -0.25, 123.5):
         turns = round((Fraction(f) * tree._TURN % 1) * 2 ** 64) % 2 ** 64
+        assert tree._turns(f) == turns
         for pos in (1, 131071, 2 ** 31 - 1, -5):
             x = (pos * turns) % 2 ** 64 / 2 ** 64
             want = Fraction(f) * pos / (2 * pi) % 1
