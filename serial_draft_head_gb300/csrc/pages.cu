@@ -185,8 +185,8 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(const __grid_constant__ 
   }
   const int total = s.total;
 #pragma unroll 1
-  for (int j = i0; j < total; j += step) {
-    const int r = find(s.pages, R, j);
+  for (int64_t i = i0; i < total; i += step) {   // i + step can pass 31 bits
+    const int j = (int)i, r = find(s.pages, R, j);
     p.table[r * p.table_stride + s.held[r] + (j - s.pages[r])] = p.free[n_free - 1 - j];
   }
   if (arrive_last(s, p.state + 1)) {
@@ -237,8 +237,8 @@ __global__ void __launch_bounds__(kThreads) trim_kernel(const dspark_pages p, co
   }
   if (wrong && blockIdx.x == 0) atomicExch(p.state, DSPARK_EPAGES);
 #pragma unroll 1
-  for (int j = blockIdx.x * kThreads + threadIdx.x; j < total; j += gridDim.x * kThreads) {
-    const int r = find(s.pages, R, j);
+  for (int64_t i = blockIdx.x * kThreads + threadIdx.x; i < total; i += gridDim.x * kThreads) {
+    const int j = (int)i, r = find(s.pages, R, j);
     int32_t* entry = p.table + r * p.table_stride + s.held[r] + (j - s.pages[r]);
     // the last to go is the first to be handed out again: the order that they came in
     p.free[n_free + total - 1 - j] = *entry;

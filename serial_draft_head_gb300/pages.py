@@ -111,6 +111,8 @@ class Pages:
         in the tree.  Rows past the last request's have slot -1.  Requests that do not fit, or that no
         page is left for, get slot -1 too, and `status` says so."""
         at_length, at_count = self._numbers(length), self._numbers(count)
+        if not 0 <= n_rows < 2 ** 31:
+            raise ValueError("n_rows is from 0 on and below 2^31")
         m, ms, mw = None, 0, 0
         if mask is not None:
             if not (mask.dtype is _int32 and mask.get_device() == self._index and mask.dim() == 2

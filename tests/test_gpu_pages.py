@@ -227,6 +227,32 @@ def test_a_wrong_count_of_free_pages_hands_none_out(Pages, n):
     assert pool.status() == walk.EPAGES and (slot[:16] == -1).all() and (slot[16:20] >= 0).all()
 
 
+def test_all_pages_there_can_be_at_once(Pages):
+    """2^31 - 1 pages of one slot (8.6 GB of them free, 8.6 GB of table) go to one request and back."""
+    n, some = 2 ** 31 - 1, 100000
+    pool = Pages(n, 1, 1, n)
+    first, slot, position = pool.grow(ints([0]), ints([n]), n)
+    assert pool.status() == 0 and int(pool.held) == n and int(pool.n_free) == 0
+    assert first.tolist() == [0, n]
+    for at in (0, n // 2, n - some):
+        want = torch.arange(at, at + some, dtype=torch.int32, device="cuda")
+        assert torch.equal(slot[at:at + some], want)
+        assert torch.equal(position[at:at + some], want)
+        assert torch.equal(pool.table[0, at:at + some], want)
+    del slot, position
+    pool.free[:some] = -7                            # what comes back is written again
+    pool.free[n - some:] = -7
+    pool.trim(ints([0]))
+    assert pool.status() == 0 and int(pool.held) == 0 and int(pool.n_free) == n
+    for at in (0, n // 2, n - some):
+        want = n - 1 - torch.arange(at, at + some, dtype=torch.int32, device="cuda")
+        assert torch.equal(pool.free[at:at + some], want)
+        assert bool((pool.table[0, at:at + some] == -1).all())
+    for many in (-1, 2 ** 31):
+        with pytest.raises(ValueError):
+            pool.grow(ints([0]), ints([0]), many)
+
+
 @pytest.mark.parametrize("held", ["e2m1", "e4m3", "16"])
 @pytest.mark.parametrize("dtype", [BF16, F16])
 def test_rounds_together(Pages, tree, held, dtype):
