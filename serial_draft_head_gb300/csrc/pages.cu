@@ -10,6 +10,8 @@
 #include <limits.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/dspark_pages.h"
 
 namespace dspark {
@@ -298,7 +300,12 @@ int dspark_pages_grow(const dspark_pages* p, const int32_t* length, const int32_
 
 int dspark_pages_trim(const dspark_pages* p, const int32_t* length, void* stream) {
   if (!fine(p) || !length) return DSPARK_EINVAL;
-  trim_kernel<<<blocks(4 * p->requests), kThreads, 0, static_cast<cudaStream_t>(stream)>>>(*p, length);
+  // What goes back is not known here: at most all that can be held, at 16 pages a thread then.
+  // 131,072 pages of 16 requests 12.7 us; with blocks for the requests alone, 1 here, 213.
+  // Where little goes back (16 pages of 6,400) 2.9 us either way.
+  const int64_t most = std::min((int64_t)p->n_pages, (int64_t)p->requests * p->max_pages);
+  trim_kernel<<<blocks(std::max((int64_t)4 * p->requests, most / 8)), kThreads, 0,
+                static_cast<cudaStream_t>(stream)>>>(*p, length);
   return code(cudaGetLastError());
 }
 
