@@ -3,9 +3,9 @@
 // Every block sums the requests' numbers up by itself, four a thread, and then does its
 // share of the rows and pages: a row finds its request in the sums by bisection.  What a
 // call changes that other blocks read (held, n_free) is written by the block that arrives
-// last, after all have read.  One launch, bound by its chain of dependent loads: 16
-// requests of 8 rows 4.2 us, taken back 2.7; 1,024 requests of 131,000 rows 6.8 (by depth
-// of a tree 7.6), taken back 3.4.
+// last, after all have read.  One launch, bound by its chain of dependent loads; in a
+// replayed graph 16 requests of 8 rows take 5.1 us, taken back 2.9; 1,024 requests of 128
+// rows 7.1, taken back 5.5.
 #include <cuda_runtime.h>
 #include <limits.h>
 #include <stdint.h>
