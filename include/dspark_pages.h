@@ -51,10 +51,12 @@ int dspark_pages_reset(const struct dspark_pages *p, void *stream);
  *
  * mask uint32, mask_words words a row, rows mask_stride words apart, or null.  Rows from
  * first[requests] on get slot and position -1.  A request whose numbers do not fit (below 0,
- * past max_pages) gets no pages, its rows slot and position -1; one that the free pages left by
- * those before it do not serve gets none either, its rows slot -1; of one whose rows go past N
- * those below N get slot and position -1.  dspark_pages_status then returns DSPARK_EPAGES.  A
- * count below 0 counts as 0 in first.
+ * past max_pages) gets no pages, its rows slot and position -1.  Free pages go to the requests
+ * in order and to none past its turn: the first request that they do not serve gets none, its
+ * rows slot -1, nor does any later one that lacks a page, also where one is left for it; those
+ * that lack none get their slots all the same.  Of a request whose rows go past N those below N
+ * get slot and position -1.  dspark_pages_status then returns DSPARK_EPAGES.  A count below 0
+ * counts as 0 in first.
  */
 int dspark_pages_grow(const struct dspark_pages *p, const int32_t *length, const int32_t *count,
                       int N, const uint32_t *mask, int64_t mask_stride, int mask_words,

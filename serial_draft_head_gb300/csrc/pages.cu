@@ -141,7 +141,8 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(const __grid_constant__ 
       const bool fits = sum[0] <= a.N;
       const bool out = bad[k] || !served || !fits;
       wrong |= out;
-      // sums of pages stay at what is handed out: none from the first that is not served on
+      // what one that is not served lacks stays in the sums, so nobody overtakes it, and who is
+      // served is known from one scan
       s.rows[r] = (int)min(before, (long long)INT_MAX);
       s.pages[r] = (int)min(sum[1], (long long)INT_MAX);
       s.length[r] = bad[k] || !fits ? -1 : length[k];

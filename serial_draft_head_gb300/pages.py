@@ -108,8 +108,9 @@ class Pages:
         """Pages for count[r] more rows of each request behind its length[r], and (first int32
         [requests + 1], slot int32 [n_rows], position int32 [n_rows]) of the rows: where each goes in
         the cache and its position, with mask int32 [n_rows, words] (see `ancestor_bits`) by its depth
-        in the tree.  Rows past the last request's have slot -1.  Requests that do not fit, or that no
-        page is left for, get slot -1 too, and `status` says so."""
+        in the tree.  Rows past the last request's have slot -1.  Free pages go to the requests in
+        order: from the first that they do not serve on, those that lack a page get none, also where
+        one is left, and slot -1; so do requests that do not fit, and `status` says so."""
         at_length, at_count = self._numbers(length), self._numbers(count)
         if not 0 <= n_rows < 2 ** 31:
             raise ValueError("n_rows is from 0 on and below 2^31")
