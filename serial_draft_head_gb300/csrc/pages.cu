@@ -29,6 +29,7 @@ struct Sums {
   long long warp[2][kThreads / 32];
   int total;                                     // pages
   int last;
+  int flagged;
 };
 
 // Exclusive sums over the block of two numbers a thread.
@@ -67,12 +68,16 @@ __device__ __forceinline__ int find(const int* sum, int n, int i) {
   return lo;
 }
 
-// Whether this block is the last of the grid to get here.
-__device__ __forceinline__ bool arrive_last(Sums& s, int* count) {
-  __syncthreads();
+// Whether this block is the last of the grid to get here, and then s.flagged, whether a thread of
+// any of them had its flag set: a block that has one counts kFlagged more.
+constexpr int kFlagged = 1 << 16;
+__device__ __forceinline__ bool arrive_last(Sums& s, int* count, bool flag = false) {
+  const bool any = __syncthreads_or(flag);
   if (threadIdx.x == 0) {
     __threadfence();
-    s.last = atomicAdd(count, 1) == (int)gridDim.x - 1;
+    const int before = atomicAdd(count, any ? 1 + kFlagged : 1);
+    s.last = before % kFlagged == (int)gridDim.x - 1;
+    s.flagged = any || before >= kFlagged;
     if (s.last) *count = 0;
   }
   __syncthreads();
@@ -202,6 +207,25 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(const __grid_constant__ 
   }
 }
 
+// Takes the entries below 0 out of x[0 .. n-1], which other blocks wrote; returns how many are
+// left.  By one block, chunk by chunk: what a chunk writes lies in it or before it.
+__device__ __noinline__ int close_up(Sums& s, int32_t* x, int n) {
+  int kept = 0;
+  __threadfence();
+#pragma unroll 1
+  for (int64_t at = 0; at < n; at += kThreads) {
+    const int64_t i = at + threadIdx.x;
+    const int pg = i < n ? __ldcg(x + i) : -1;
+    long long rank[2] = {pg >= 0 ? 1 : 0, 0};
+    scan(s, rank);                               // all have read
+    if (pg >= 0) x[kept + (int)rank[0]] = pg;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) kept += (int)s.warp[0][w];
+    __syncthreads();
+  }
+  return kept;
+}
+
 __global__ void __launch_bounds__(kThreads) trim_kernel(const dspark_pages p, const int32_t* length) {
   __shared__ Sums s;
   const int R = p.requests, page = p.page_size;
@@ -239,21 +263,30 @@ __global__ void __launch_bounds__(kThreads) trim_kernel(const dspark_pages p, co
     total = 0;
   }
   if (wrong && blockIdx.x == 0) atomicExch(p.state, DSPARK_EPAGES);
+  bool lost = false;
 #pragma unroll 1
   for (int64_t i = blockIdx.x * kThreads + threadIdx.x; i < total; i += gridDim.x * kThreads) {
     const int j = (int)i, r = find(s.pages, R, j);
     int32_t* entry = p.table + r * p.table_stride + s.held[r] + (j - s.pages[r]);
+    const int pg = *entry;
+    const bool is = pg >= 0 && pg < p.n_pages;
+    lost |= !is;
     // the last to go is the first to be handed out again: the order that they came in
-    p.free[n_free + total - 1 - j] = *entry;
+    p.free[n_free + total - 1 - j] = is ? pg : -1;
     *entry = -1;
   }
-  if (arrive_last(s, p.state + 1) && total > 0) {
+  if (arrive_last(s, p.state + 1, lost) && total > 0) {
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       const int r = threadIdx.x * kPer + k;
       if (r < R && gone[k] > 0) p.held[r] = keep[k];
     }
-    if (threadIdx.x == 0) *p.n_free = n_free + total;
+    int back = total;
+    if (s.flagged) back = close_up(s, p.free + n_free, total);
+    if (threadIdx.x == 0) {
+      *p.n_free = n_free + back;
+      if (s.flagged) atomicExch(p.state, DSPARK_EPAGES);
+    }
   }
 }
 
