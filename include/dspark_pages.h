@@ -64,7 +64,8 @@ int dspark_pages_grow(const struct dspark_pages *p, const int32_t *length, const
 
 /*
  * Request r keeps the pages of its first length[r] rows and gives the others back, so that
- * trim after grow with the same lengths leaves everything as it was.  length[r] = 0: all of
+ * trim after grow with the same lengths leaves everything as it was, where no request held
+ * more pages before than its length needs (trim takes those, too).  length[r] = 0: all of
  * them.  A length below 0 or past max_pages changes nothing of its request and is reported
  * as above.  So is an entry of the table on its way back that is no page of the pool: it
  * leaves the table and becomes no free page, so n_free grows by the others alone.

@@ -71,3 +71,16 @@ def test_trim_of_many_entries_that_are_no_pages(Pages, requests, each, share):  
         count = torch.minimum(count, torch.full_like(count, len(want) // requests))
         pool.grow(z, count, 0)
         pool.status()
+
+
+def test_trim_takes_pages_held_before_the_rows_came(Pages):  # noqa: F811
+    """A request that held more than its length needs gives that back as well; the others end as they began."""
+    pool = Pages(20, 16, 2, 10)
+    pool.grow(ints([0, 0]), ints([100, 20]), 120)                  # 7 and 2 pages
+    length = ints([40, 20])
+    pool.grow(length, ints([5, 30]), 35)                           # none and 2 more
+    assert pool.held.tolist() == [7, 4] and pool.n_free.item() == 9
+    pool.trim(length)
+    assert pool.held.tolist() == [3, 2] and pool.n_free.item() == 15 and pool.status() == 0
+    assert pool.table[0].tolist() == [0, 1, 2] + [-1] * 7 and pool.table[1].tolist() == [7, 8] + [-1] * 8
+    assert pool.free[:15].tolist() == list(range(19, 10, -1)) + [10, 9, 6, 5, 4, 3]
