@@ -814,6 +814,7 @@ constexpr float grow_limit() {
 // is the maximum the largest is 1), and divided by the sum that is not rounded their
 // error would be that of a row with few large ones (2.2e-3 of the result in all, bf16's own
 // rounding 1.6e-3); divided by the rounded sum it is not.
+template <bool FAR>
 struct Sum {
   float l = 0.f, rounded = 0.f;
   __device__ __forceinline__ void times(float x) {
@@ -821,6 +822,13 @@ struct Sum {
     rounded *= x;
   }
 };
+template <>
+struct Sum<false> {                              // any other row's
+  float l = 0.f;
+  __device__ __forceinline__ void times(float x) { l *= x; }
+};
+template <bool F16, int HELD>
+using SumOf = Sum<far_growth<F16, HELD>()>;
 
 // What two packed bf16 weights come to.
 __device__ __forceinline__ void add_rounded(uint32_t pk, float* even, float* odd) {
@@ -834,7 +842,7 @@ __device__ __forceinline__ void add_rounded(uint32_t pk, float* even, float* odd
 template <bool F16, int HELD, int DP>
 __device__ __forceinline__ float move_reference(float x_max, Tail* sh, uint64_t* o_done,
                                                 uint32_t parity, int* status, uint32_t tm_o,
-                                                float mref, Sum* l) {
+                                                float mref, SumOf<F16, HELD>* l) {
   constexpr float kShift = F16 ? 7.f : 0.f;
   const bool move = x_max > mref + (mref == -INFINITY ? 0.f : kShift + grow_limit<F16, HELD>());
   const float m_new = move ? x_max - kShift : mref;
@@ -854,8 +862,8 @@ __device__ __forceinline__ float move_reference(float x_max, Tail* sh, uint64_t*
 // the warp, S is still there and they are done again (false; x_max is the row's largest
 // exponent).  A 16-bit cache: the next 32 scores are loaded while these are worked on.
 template <bool F16, int HELD, int KEYS>
-__device__ __forceinline__ bool softmax_plain(float sl2, uint32_t tm_s, float mref, Sum* l,
-                                              float* x_max) {
+__device__ __forceinline__ bool softmax_plain(float sl2, uint32_t tm_s, float mref,
+                                              SumOf<F16, HELD>* l, float* x_max) {
   constexpr float kShift = F16 ? 7.f : 0.f;
   constexpr bool WIDE = HELD == k16;
   constexpr int kBuf = WIDE ? 2 : 1, kChunks = KEYS / 32;
@@ -877,7 +885,7 @@ __device__ __forceinline__ bool softmax_plain(float sl2, uint32_t tm_s, float mr
       unpack_f32x2(fma_f32x2(pack_f32x2(r0, r1), mul, neg), &p0, &p1);
       p0 = ex2(p0);
       p1 = ex2(p1);
-      if (far_growth<F16, HELD>()) {
+      if constexpr (far_growth<F16, HELD>()) {
         const uint64_t p = pack_f32x2(p0, p1), near = round8_f32x2(p);
         sum2[k & 1] = add_f32x2(sum2[k & 1], p);
         rounded2[k & 1] = add_f32x2(rounded2[k & 1], near);
@@ -895,7 +903,7 @@ __device__ __forceinline__ bool softmax_plain(float sl2, uint32_t tm_s, float mr
   if (__any_sync(0xffffffffu, *x_max > mref + (kShift + grow_limit<F16, HELD>()))) return false;
 #pragma unroll
   for (int c = 0; c < kChunks; ++c) ptx::tmem_st16(tm_s + 16 * c, pk[c]);
-  if (far_growth<F16, HELD>()) {
+  if constexpr (far_growth<F16, HELD>()) {
     unpack_f32x2(add_f32x2(sum2[0], sum2[1]), &sum[0], &sum[1]);
     float r0, r1;
     unpack_f32x2(add_f32x2(rounded2[0], rounded2[1]), &r0, &r1);
@@ -908,14 +916,15 @@ __device__ __forceinline__ bool softmax_plain(float sl2, uint32_t tm_s, float mr
 
 // 64 or 128 keys of one row, also with invisible keys (see: a bit a key), capped
 // scores, or a maximum that moves m; 32 keys at a time.  Returns m and the sums.
+template <bool FAR>
 struct Softened {
   float m;
-  Sum l;
+  Sum<FAR> l;
 };
 template <bool F16, int HELD, int DP>
-__device__ __noinline__ Softened softmax_any(Score sc, Tail* sh, uint64_t* o_done, uint32_t parity,
-                                           int* status, uint32_t tm_s, uint32_t tm_o, int keys,
-                                           uint4 see, float mref, Sum l) {
+__device__ __noinline__ Softened<far_growth<F16, HELD>()> softmax_any(
+    Score sc, Tail* sh, uint64_t* o_done, uint32_t parity, int* status, uint32_t tm_s, uint32_t tm_o,
+    int keys, uint4 see, float mref, SumOf<F16, HELD> l) {
   const bool cap = sc.cap2 > 0.f;
   uint32_t any = 0;                              // whether the row sees one of the keys
   float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -1011,7 +1020,7 @@ __device__ __noinline__ Softened softmax_any(Score sc, Tail* sh, uint64_t* o_don
   }
   ptx::tmem_wait_st();
   l.l += sum[0] + sum[1];
-  if (far_growth<F16, HELD>()) l.rounded += rounded[0] + rounded[1];
+  if constexpr (far_growth<F16, HELD>()) l.rounded += rounded[0] + rounded[1];
   return {mref, l};
 }
 
@@ -1080,7 +1089,7 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
     const uint32_t* mask_row =
         a.mask ? a.mask + (int64_t)(s.row0 + node) * a.mask_stride : nullptr;
     float mref = -INFINITY, l = 0.f;
-    Sum sums;
+    SumOf<F16, HELD> sums;
     const int step = pair ? 1 : 2;
     const int keys = pair ? kHalf : kKeys;       // of one step
     for (int i = pair ? 0 : wg; i < n; i += step) {
@@ -1094,8 +1103,8 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
           bool done = !masked && sc.cap2 == 0.f && !__any_sync(0xffffffffu, mref == -INFINITY);
           // the product before this one
           const int before = pair ? h ^ 1 : 0;
-          const uint32_t phase = (before ? count1 : count0) - 1;
-          uint64_t* o_done = h == 1 || i >= step ? &sh->o_done[wg][before] : nullptr;
+          auto phase = [&]() { return ((before ? count1 : count0) - 1) & 1; };
+          auto o_done = [&]() { return h == 1 || i >= step ? &sh->o_done[wg][before] : nullptr; };
           if (done) {
             float x_max;
             auto plain = [&]() {
@@ -1104,14 +1113,14 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
             };
             done = plain();
             if (HELD == kE2M1 && !done) {        // as long as m follows, the second time it fits
-              mref = move_reference<F16, HELD, DP>(x_max, sh, o_done, phase & 1, a.status, tm_o + wg * 128,
+              mref = move_reference<F16, HELD, DP>(x_max, sh, o_done(), phase(), a.status, tm_o + wg * 128,
                                                    mref, &sums);
               done = plain();
             }
           }
           if (!done) {
-            const Softened r = softmax_any<F16, HELD, DP>(
-                sc, sh, o_done, phase & 1, a.status, tm_s + h * kHalf, tm_o + wg * 128, keys,
+            const auto r = softmax_any<F16, HELD, DP>(
+                sc, sh, o_done(), phase(), a.status, tm_s + h * kHalf, tm_o + wg * 128, keys,
                 masked ? sees_128(mask_row, s.rows, node, pos0 - s.start)
                        : make_uint4(~0u, ~0u, ~0u, ~0u),
                 mref, sums);
@@ -1130,9 +1139,11 @@ __device__ __forceinline__ void softmax(const AttendArgs& a, uint8_t* smem, Tail
     // as O's weights add up to the rounded sum, m stands so much higher that the sum is the
     // same: from here on m and l are any row's
     l = sums.l;
-    if (far_growth<F16, HELD>() && sums.rounded > 0.f) {
-      mref += log2f(sums.l / sums.rounded);
-      l = sums.rounded;
+    if constexpr (far_growth<F16, HELD>()) {
+      if (sums.rounded > 0.f) {
+        mref += log2f(sums.l / sums.rounded);
+        l = sums.rounded;
+      }
     }
     // the segment's result
     const int n1 = n / 2;                        // the second stream's tiles, not in pairs
