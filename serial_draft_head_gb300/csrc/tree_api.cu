@@ -22,6 +22,7 @@ struct dspark_tree {
   float2* part_ml = nullptr;
   int4* part_of = nullptr;
   int part_rows = 0;
+  uint32_t ready = 0;             // e2m1 kernels that have been launched (few4_launch)
   PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
 };
 
@@ -224,7 +225,8 @@ int dspark_tree_create(const dspark_tree_config* cfg, dspark_tree_t* out) {
   const int64_t rows = (int64_t)cfg->max_nodes * G;
   h->part_rows = rows >= kGroupRows ? kGroupRows : (int)((rows + 31) / 32 * 32);
   const size_t n_parts = (size_t)2 * sms;
-  const size_t n_rows = std::max(n_parts * h->part_rows, (size_t)kFew4PartRows * sms);
+  size_t n_rows = n_parts * h->part_rows;
+  if (cfg->head_dim % 32 == 0) n_rows = std::max(n_rows, (size_t)kFew4PartRows * sms);   // e2m1 may come
   const size_t o_bytes = n_rows * padded_dim(cfg->head_dim) * sizeof(float);
   const size_t ml_bytes = n_rows * sizeof(float2);
   e = cudaMalloc(&h->parts, o_bytes + ml_bytes + n_parts * sizeof(int4));
@@ -246,8 +248,6 @@ int dspark_tree_create(const dspark_tree_config* cfg, dspark_tree_t* out) {
   }
   if (e == cudaSuccess) e = attend_setup(cfg->type == DSPARK_TYPE_F16, cfg->head_dim);
   if (e == cudaSuccess) e = few_setup(cfg->type == DSPARK_TYPE_F16, cfg->head_dim);
-  if (e == cudaSuccess) e = few4_setup(cfg->head_dim);
-  if (e == cudaSuccess) e = attend4_setup(cfg->type == DSPARK_TYPE_F16, cfg->head_dim);
   if (e != cudaSuccess) {
     dspark_tree_destroy(h);
     return cuda_code(e);
@@ -384,8 +384,8 @@ int dspark_tree_attend(dspark_tree_t h, const dspark_tree_cache* cache,
     // items of 32 rows where the others have 16 (16 requests as above, here / there: 24 rows
     // 62 / 70 us, 32 rows 65 / 70, 40 rows 102 / 71)
     const bool few4 = (int64_t)a.b.N * a.G <= (int64_t)32 * a.b.B;
-    return cuda_code(few4 ? few4_launch(a, static_cast<cudaStream_t>(stream))
-                         : attend4_launch(a, a.f16, static_cast<cudaStream_t>(stream)));
+    return cuda_code(few4 ? few4_launch(a, &h->ready, static_cast<cudaStream_t>(stream))
+                         : attend4_launch(a, a.f16, &h->ready, static_cast<cudaStream_t>(stream)));
   }
   if (few)
     return cuda_code(few_launch(a, h->cfg.type == DSPARK_TYPE_F16,

@@ -6,23 +6,22 @@ namespace tree {
 namespace {
 
 template <bool F16, int DP>
-cudaError_t setup_both() {
-  const cudaError_t e = setup<F16, kE2M1, DP>();
-  return e == cudaSuccess ? setup_join<F16, DP>() : e;
+cudaError_t launch_ready(const AttendArgs& a, uint32_t* ready, cudaStream_t stream) {
+  if (!(*ready & kReadyMany)) {
+    cudaError_t e = setup<F16, kE2M1, DP>();
+    if (e == cudaSuccess) e = setup_join<F16, DP>();
+    if (e != cudaSuccess) return e;
+    *ready |= kReadyMany;
+  }
+  return launch<F16, kE2M1, DP>(a, TileMaps{}, stream);
 }
 
 }  // namespace
 
-cudaError_t attend4_setup(bool f16, int D) {
-  if (padded_dim(D) == 64) return f16 ? setup_both<true, 64>() : setup_both<false, 64>();
-  return f16 ? setup_both<true, 128>() : setup_both<false, 128>();
-}
-
-cudaError_t attend4_launch(const AttendArgs& a, bool f16, cudaStream_t stream) {
-  TileMaps maps{};
+cudaError_t attend4_launch(const AttendArgs& a, bool f16, uint32_t* ready, cudaStream_t stream) {
   if (padded_dim(a.D) == 64)
-    return f16 ? launch<true, kE2M1, 64>(a, maps, stream) : launch<false, kE2M1, 64>(a, maps, stream);
-  return f16 ? launch<true, kE2M1, 128>(a, maps, stream) : launch<false, kE2M1, 128>(a, maps, stream);
+    return f16 ? launch_ready<true, 64>(a, ready, stream) : launch_ready<false, 64>(a, ready, stream);
+  return f16 ? launch_ready<true, 128>(a, ready, stream) : launch_ready<false, 128>(a, ready, stream);
 }
 
 }  // namespace tree

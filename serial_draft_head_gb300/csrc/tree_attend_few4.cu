@@ -5,29 +5,23 @@ namespace dspark {
 namespace tree {
 
 template <>
-cudaError_t few4_setup_of<64, 1>();
+cudaError_t few4_launch_of<64, 1>(const AttendArgs& a, bool alone, bool runs, uint32_t* ready,
+                                   cudaStream_t stream);
 template <>
-cudaError_t few4_setup_of<64, 2>();
+cudaError_t few4_launch_of<64, 2>(const AttendArgs& a, bool alone, bool runs, uint32_t* ready,
+                                   cudaStream_t stream);
 template <>
-cudaError_t few4_setup_of<64, 4>();
+cudaError_t few4_launch_of<64, 4>(const AttendArgs& a, bool alone, bool runs, uint32_t* ready,
+                                   cudaStream_t stream);
 template <>
-cudaError_t few4_setup_of<128, 1>();
+cudaError_t few4_launch_of<128, 1>(const AttendArgs& a, bool alone, bool runs, uint32_t* ready,
+                                   cudaStream_t stream);
 template <>
-cudaError_t few4_setup_of<128, 2>();
+cudaError_t few4_launch_of<128, 2>(const AttendArgs& a, bool alone, bool runs, uint32_t* ready,
+                                   cudaStream_t stream);
 template <>
-cudaError_t few4_setup_of<128, 4>();
-template <>
-cudaError_t few4_launch_of<64, 1>(const AttendArgs& a, bool alone, bool runs, cudaStream_t stream);
-template <>
-cudaError_t few4_launch_of<64, 2>(const AttendArgs& a, bool alone, bool runs, cudaStream_t stream);
-template <>
-cudaError_t few4_launch_of<64, 4>(const AttendArgs& a, bool alone, bool runs, cudaStream_t stream);
-template <>
-cudaError_t few4_launch_of<128, 1>(const AttendArgs& a, bool alone, bool runs, cudaStream_t stream);
-template <>
-cudaError_t few4_launch_of<128, 2>(const AttendArgs& a, bool alone, bool runs, cudaStream_t stream);
-template <>
-cudaError_t few4_launch_of<128, 4>(const AttendArgs& a, bool alone, bool runs, cudaStream_t stream);
+cudaError_t few4_launch_of<128, 4>(const AttendArgs& a, bool alone, bool runs, uint32_t* ready,
+                                   cudaStream_t stream);
 
 namespace {
 
@@ -44,25 +38,16 @@ bool in_runs(const AttendArgs& a) {
 }
 
 template <int DP>
-cudaError_t setup_for() {
-  cudaError_t e = few4_setup_of<DP, 1>();
-  if (e == cudaSuccess) e = few4_setup_of<DP, 2>();
-  if (e == cudaSuccess) e = few4_setup_of<DP, 4>();
-  return e;
-}
-
-template <int DP>
-cudaError_t launch_for(const AttendArgs& a, int tiles, bool alone, bool runs, cudaStream_t stream) {
-  if (tiles == 1) return few4_launch_of<DP, 1>(a, alone, runs, stream);
-  return tiles == 2 ? few4_launch_of<DP, 2>(a, alone, runs, stream)
-                    : few4_launch_of<DP, 4>(a, alone, runs, stream);
+cudaError_t launch_for(const AttendArgs& a, int tiles, bool alone, bool runs, uint32_t* ready,
+                       cudaStream_t stream) {
+  if (tiles == 1) return few4_launch_of<DP, 1>(a, alone, runs, ready, stream);
+  return tiles == 2 ? few4_launch_of<DP, 2>(a, alone, runs, ready, stream)
+                    : few4_launch_of<DP, 4>(a, alone, runs, ready, stream);
 }
 
 }  // namespace
 
-cudaError_t few4_setup(int D) { return padded_dim(D) == 64 ? setup_for<64>() : setup_for<128>(); }
-
-cudaError_t few4_launch(const AttendArgs& a, cudaStream_t stream) {
+cudaError_t few4_launch(const AttendArgs& a, uint32_t* ready, cudaStream_t stream) {
   // rows of an item: what the requests have on average, in whole tiles of eight
   const int64_t rows = (int64_t)a.b.N * a.G;
   const int tiles = rows <= (int64_t)8 * a.b.B ? 1 : rows <= (int64_t)16 * a.b.B ? 2 : 4;
@@ -72,8 +57,8 @@ cudaError_t few4_launch(const AttendArgs& a, cudaStream_t stream) {
   const int64_t items = (rows + 8 * tiles - 1) / (8 * tiles) * a.Hkv;
   const bool alone = items < (int64_t)2 * a.n_cta;
   const bool runs = in_runs(a);
-  return padded_dim(a.D) == 64 ? launch_for<64>(a, tiles, alone, runs, stream)
-                               : launch_for<128>(a, tiles, alone, runs, stream);
+  return padded_dim(a.D) == 64 ? launch_for<64>(a, tiles, alone, runs, ready, stream)
+                               : launch_for<128>(a, tiles, alone, runs, ready, stream);
 }
 
 }  // namespace tree

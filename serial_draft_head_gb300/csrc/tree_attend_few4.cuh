@@ -870,8 +870,19 @@ __global__ void __launch_bounds__(Few4<DP, NT, GROUP, RUNS>::kThreads, 1)
 }
 
 template <int DP, int NT, int GROUP, bool RUNS, bool CAP>
-cudaError_t launch(AttendArgs a, cudaStream_t stream) {
+cudaError_t launch(AttendArgs a, uint32_t* ready, cudaStream_t stream) {
   using L = Few4<DP, NT, GROUP, RUNS>;
+  static_assert(L::kSmem + L::kWorkers * (sizeof(WorkerState<GROUP, L::kRows>) + 300) + 1024 <= 232448,
+                "shared memory of an SM");
+  static_assert(L::kWorkers <= kFew4Workers && 2 * L::kWorkers * L::kRows <= kFew4PartRows, "the parts' place");
+  constexpr uint32_t kBit = 1u << (NT / 2 * 5 + (GROUP == 4 ? 4 : 2 * RUNS + CAP));
+  static_assert(kBit < kReadyMany, "a bit of its own");
+  if (!(*ready & kBit)) {
+    const cudaError_t e = cudaFuncSetAttribute(few4_kernel<DP, NT, GROUP, RUNS, CAP>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+    if (e != cudaSuccess) return e;
+    *ready |= kBit;
+  }
   // launched while the kernel before it in the stream ends, which it waits for before
   // anything else
   cudaLaunchAttribute attr{};
@@ -888,44 +899,24 @@ cudaError_t launch(AttendArgs a, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, few4_kernel<DP, NT, GROUP, RUNS, CAP>, a);
 }
 
-template <int DP, int NT, int GROUP, bool RUNS, bool CAP>
-cudaError_t setup() {
-  using L = Few4<DP, NT, GROUP, RUNS>;
-  static_assert(L::kSmem + L::kWorkers * (sizeof(WorkerState<GROUP, L::kRows>) + 300) + 1024 <= 232448,
-                "shared memory of an SM");
-  static_assert(L::kWorkers <= kFew4Workers && 2 * L::kWorkers * L::kRows <= kFew4PartRows, "the parts' place");
-  return cudaFuncSetAttribute(few4_kernel<DP, NT, GROUP, RUNS, CAP>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
-}
-
-template <int DP, int NT, int WARPS>
-cudaError_t setup_all() {
-  cudaError_t e = setup<DP, NT, WARPS, false, false>();
-  if (e == cudaSuccess) e = setup<DP, NT, WARPS, false, true>();
-  if (e == cudaSuccess) e = setup<DP, NT, WARPS, true, false>();
-  if (e == cudaSuccess) e = setup<DP, NT, WARPS, true, true>();
-  if (e == cudaSuccess) e = setup<DP, NT, 4, true, false>();
-  return e;
-}
-
 // alone: a worker a CTA; else of four warps, where slots lie in runs and scores are not
 // capped.
 template <int DP, int NT, int WARPS>
-cudaError_t launch_all(const AttendArgs& a, bool alone, bool runs, cudaStream_t stream) {
+cudaError_t launch_all(const AttendArgs& a, bool alone, bool runs, uint32_t* ready, cudaStream_t stream) {
   const bool cap = a.softcap > 0.f;
   if (!runs)
-    return cap ? launch<DP, NT, WARPS, false, true>(a, stream) : launch<DP, NT, WARPS, false, false>(a, stream);
-  if (cap) return launch<DP, NT, WARPS, true, true>(a, stream);
-  return alone ? launch<DP, NT, WARPS, true, false>(a, stream) : launch<DP, NT, 4, true, false>(a, stream);
+    return cap ? launch<DP, NT, WARPS, false, true>(a, ready, stream)
+               : launch<DP, NT, WARPS, false, false>(a, ready, stream);
+  if (cap) return launch<DP, NT, WARPS, true, true>(a, ready, stream);
+  return alone ? launch<DP, NT, WARPS, true, false>(a, ready, stream)
+               : launch<DP, NT, 4, true, false>(a, ready, stream);
 }
 
 }  // namespace
 
 // A source file each.
 template <int DP, int NT>
-cudaError_t few4_setup_of();
-template <int DP, int NT>
-cudaError_t few4_launch_of(const AttendArgs& a, bool alone, bool runs, cudaStream_t stream);
+cudaError_t few4_launch_of(const AttendArgs& a, bool alone, bool runs, uint32_t* ready, cudaStream_t stream);
 
 }  // namespace tree
 }  // namespace dspark

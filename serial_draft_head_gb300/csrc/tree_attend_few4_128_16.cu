@@ -6,13 +6,8 @@ namespace dspark {
 namespace tree {
 
 template <>
-cudaError_t few4_setup_of<128, 2>() {
-  return setup_all<128, 2, 12>();
-}
-
-template <>
-cudaError_t few4_launch_of<128, 2>(const AttendArgs& a, bool alone, bool runs, cudaStream_t stream) {
-  return launch_all<128, 2, 12>(a, alone, runs, stream);
+cudaError_t few4_launch_of<128, 2>(const AttendArgs& a, bool alone, bool runs, uint32_t* ready, cudaStream_t stream) {
+  return launch_all<128, 2, 12>(a, alone, runs, ready, stream);
 }
 
 }  // namespace tree

@@ -6,13 +6,8 @@ namespace dspark {
 namespace tree {
 
 template <>
-cudaError_t few4_setup_of<64, 1>() {
-  return setup_all<64, 1, 16>();
-}
-
-template <>
-cudaError_t few4_launch_of<64, 1>(const AttendArgs& a, bool alone, bool runs, cudaStream_t stream) {
-  return launch_all<64, 1, 16>(a, alone, runs, stream);
+cudaError_t few4_launch_of<64, 1>(const AttendArgs& a, bool alone, bool runs, uint32_t* ready, cudaStream_t stream) {
+  return launch_all<64, 1, 16>(a, alone, runs, ready, stream);
 }
 
 }  // namespace tree

@@ -310,12 +310,15 @@ struct TileMaps {
 // e2m1 cache, few rows a cached head (tree_attend_few4.cuh).  kFew4Workers: most workers
 // an SM, kFew4PartRows: rows of their parts.
 constexpr int kFew4Workers = 4, kFew4PartRows = 128;
-cudaError_t few4_setup(int D);
-cudaError_t few4_launch(const AttendArgs& a, cudaStream_t stream);    // up to 32 rows a cached head on average
+// The kernels over e2m1 get their attributes, which loads them, before a handle's first launch of
+// each, so that handles without such a cache do not pay for 17 of them (all in the handle: the
+// first of 128 elements in a process 4.4 ms instead of 2.6, of 64 1.7 instead of 0.4); `ready`
+// has a bit a kernel that the handle has launched.
+constexpr uint32_t kReadyMany = 1u << 15;        // below it the few-row forms' bits
+cudaError_t few4_launch(const AttendArgs& a, uint32_t* ready, cudaStream_t stream);    // up to 32 rows a cached head on average
 
 // e2m1 cache, more rows (tree_attend4.cu).
-cudaError_t attend4_setup(bool f16, int D);
-cudaError_t attend4_launch(const AttendArgs& a, bool f16, cudaStream_t stream);
+cudaError_t attend4_launch(const AttendArgs& a, bool f16, uint32_t* ready, cudaStream_t stream);
 
 // Few rows a cached head, on mma.sync (tree_attend_few.cu).
 cudaError_t few_setup(bool f16, int D);
