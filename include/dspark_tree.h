@@ -201,7 +201,8 @@ int dspark_tree_attend(dspark_tree_t h, const struct dspark_tree_cache *cache,
  *
  * for the pairs i < rotary_dim / 2 (rotary_dim a multiple of 16, from 0 to head_dim):
  * elements i and i + rotary_dim / 2, or, interleaved, 2 i and 2 i + 1.  The elements
- * past rotary_dim are not turned.  Arrays on the device: turns [rotary_dim / 2], the
+ * past rotary_dim are not turned.  Rows of any size are normed: one whose squares leave
+ * fp32 is multiplied by a power of two first.  Arrays on the device: turns [rotary_dim / 2], the
  * turns of a position as fractions of 2^64 (whole turns do not count), norms fp32
  * [head_dim], 16-byte aligned.
  */

@@ -172,6 +172,8 @@ int make_rotation(const dspark_tree* h, const dspark_tree_rotation* r, int N, Ro
   a->q_norm = r->q_norm;
   a->k_norm = r->k_norm;
   a->eps = r->eps;
+  // fp32 loses squares below 2^-149: nothing beside a sum of 2^-80, or beside an eps of 2^-60
+  a->least = r->eps < 0x1p-60f ? 0x1p-80f : 0.f;
   a->inv_dim = 1.f / (float)D;
   a->pairs = r->interleaved != 0;
   a->N = N;

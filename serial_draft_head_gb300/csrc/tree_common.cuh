@@ -371,6 +371,7 @@ struct RotateArgs {
   const uint64_t* turns;
   const float *q_norm, *k_norm;    // null: no norm
   float eps, inv_dim;
+  float least;               // sums of squares below it have lost some of theirs
   int N, Hq, Hkv, D, R;
   bool pairs;                // neighbours turn with each other, else halves
   int* status;

@@ -17,7 +17,7 @@
 // before it is quantised, as if it had been stored and written.
 //
 // What bounds it: memory.  32,284 tokens of 32 + 8 + 8 heads of 128: into a 16-bit cache 132
-// us, 6.0 TB/s of bytes read and written; q and k alone 105 us, 6.3; into e2m1 148 (the
+// us, 6.0 TB/s of bytes read and written; q and k alone 107 us, 6.2; into e2m1 148 (the
 // quantising).  With the next rows in registers instead of five rounds of copies into
 // shared memory 172.  128 tokens: 4.6 us, a chain of the slot, the position, the angles and
 // the rows.
@@ -31,6 +31,38 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kDepth = 5;          // rounds of a warp's loads in flight, a KB each
+
+// The sum of a row's squares, in all its lanes.
+template <int LANES>
+__device__ __forceinline__ float row_squares(const uint64_t (&u)[4], const uint64_t (&z)[4]) {
+  uint64_t squares = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) squares = ptx::fma_f32x2(u[k], u[k], ptx::fma_f32x2(z[k], z[k], squares));
+  float sum, odd;
+  ptx::unpack_f32x2(squares, &sum, &odd);
+  sum += odd;
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum;
+}
+
+// The power of two, 2^-120 to 2^top, that brings a row's largest element near 1.
+template <int LANES>
+__device__ __forceinline__ float row_unit(const uint64_t (&u)[4], const uint64_t (&z)[4], int top) {
+  float big = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float lo, hi;
+    ptx::unpack_f32x2(u[k], &lo, &hi);
+    big = fmaxf(big, fmaxf(fabsf(lo), fabsf(hi)));
+    ptx::unpack_f32x2(z[k], &lo, &hi);
+    big = fmaxf(big, fmaxf(fabsf(lo), fabsf(hi)));
+  }
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+  const int e = 127 - (int)(__float_as_uint(big) >> 23);
+  return __uint_as_float((uint32_t)(127 + min(max(e, -120), top)) << 23);
+}
 
 // PLACE: k and v go to the cache, as HELD says; else k to out_k and there is no v.  2^`shift`
 // warps a token.
@@ -144,15 +176,24 @@ __global__ void __launch_bounds__(kThreads, 6) rotate_kernel(const __grid_consta
         z[k] = a.pairs ? ptx::pack_f32x2(a1, b1) : ptx::pack_f32x2(b0, b1);
       }
       if (i == 0 ? a.q_norm != nullptr : a.k_norm != nullptr) {
-        uint64_t squares = 0;
+        float sum = row_squares<LANES>(u, z), eps = a.eps;
+        if (!F16) {
+          // squares can leave fp32 (bf16 past 2^63; below 2^-40 without an eps): such a row is
+          // brought near 1 by a power of two, which the norm takes out again
+          const bool far = !(sum <= 3.40282347e38f && sum >= a.least);
+          if (__any_sync(0xffffffffu, far && live)) {
+            const float unit = row_unit<LANES>(u, z, a.eps > 0.f ? 60 : 120), by = far ? unit : 1.f;
+            const uint64_t by2 = ptx::pack_f32x2(by, by);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) squares = ptx::fma_f32x2(u[k], u[k], ptx::fma_f32x2(z[k], z[k], squares));
-        float sum, odd;
-        ptx::unpack_f32x2(squares, &sum, &odd);
-        sum += odd;
-#pragma unroll
-        for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float r = rsqrtf(sum * a.inv_dim + a.eps);
+            for (int k = 0; k < 4; ++k) {
+              u[k] = ptx::mul_f32x2(u[k], by2);
+              z[k] = ptx::mul_f32x2(z[k], by2);
+            }
+            eps = eps * by * by;                   // 0 stays 0
+            sum = row_squares<LANES>(u, z);
+          }
+        }
+        const float r = rsqrtf(sum * a.inv_dim + eps);
         const uint64_t r2 = ptx::pack_f32x2(r, r);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
