@@ -158,21 +158,38 @@ class KVCache:
         return cls(*x)
 
 
-# 1 / (2 pi), to 2^-150, and as a fraction of 2^256
-_TURN = Fraction(15915494309189533576888376337251436203445964574, 10 ** 47)
-_TURN_256 = round(_TURN * 2 ** 256)
+def _turn(bits):
+    """1 / (2 pi) as a fraction of 2^bits, to half of one: pi by Machin's formula."""
+    one = 1 << (bits + 32)
+
+    def arctan_inverse(n):
+        total, term, k = 0, one // n, 1
+        while term:
+            total += term // k if k % 4 == 1 else -(term // k)
+            term //= n * n
+            k += 2
+        return total
+
+    pi = 4 * (4 * arctan_inverse(5) - arctan_inverse(239))
+    return ((one << bits) // pi + 1) >> 1
+
+
+# enough for the turns of any float, up to 2^1024, to 2^-64
+_TURN_BITS = 1152
+_TURN_WHOLE = _turn(_TURN_BITS)
+_TURN = Fraction(_TURN_WHOLE, 1 << _TURN_BITS)
 
 
 def _turns(f):
     """The turns of f radians, a float, as a fraction of 2^64; whole ones do not count."""
     n, d = f.as_integer_ratio()                      # d is a power of two
-    shift = 256 - 64 + d.bit_length() - 1
-    return ((n * _TURN_256 + (1 << (shift - 1))) >> shift) % 2 ** 64
+    shift = _TURN_BITS - 64 + d.bit_length() - 1
+    return ((n * _TURN_WHOLE + (1 << (shift - 1))) >> shift) % 2 ** 64
 
 
 class Rotation:
     """How query and key heads are normed and turned (see `Tree.rotate`): `freq` [R / 2], radians a
-    position of every pair (any real numbers, taken as float64), or None: no rotation; q_norm and
+    position of every pair (any finite numbers, taken as float64), or None: no rotation; q_norm and
     k_norm [head_dim] or None: no norm; pairs are elements i and i + R / 2, or, `interleaved`, 2 i
     and 2 i + 1.  Copies what it is given, on the host where needed: made once, not in a graph."""
 
