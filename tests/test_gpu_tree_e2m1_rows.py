@@ -1,0 +1,32 @@
+"""Attention over a 4-bit cache where the rows of q are of extreme size, and its tcgen05 kernel on other
+streams and in graphs."""
+import math
+
+import pytest
+import torch
+
+import e2m1_reference as e2m1
+from test_gpu_tree import BF16, F16, tree  # noqa: F401
+from test_gpu_tree_e2m1 import Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("T", [1, 2, 4, 40])       # items of 8, 16 and 32 rows, and tcgen05
+@pytest.mark.parametrize("size,scale", [(2.0 ** 120, 2.0 ** 30), (-2.0 ** 110, 2.0 ** 127), (2.0 ** 127, 1.0), (2.0 ** -126, 1.0)])
+def test_scores_of_zero_under_any_scale(tree, T, size, scale):  # noqa: F811
+    """Keys of zeros: every score is zero, whatever the rows and the scale, and every visible key weighs the
+    same."""
+    c = Case(tree, 8, 1, 64, 16, BF16, [T], [50], seed=400 + T, mask=None)
+    c.k.zero_()
+    c.ks[c.ks != 255] = 0
+    c.q.fill_(size)
+    out, lse = c.attend(scale=scale)
+    v = e2m1.values(c.v, c.vs)
+    for i in range(T):
+        at = torch.arange(51 + i, device="cuda")
+        rows = v[c.pages[0][at // 16].long(), at % 16, 0]
+        # a weight of 1 is exact in both types, fp32 sums of up to 90 numbers, one rounding
+        want, size_of = rows.mean(0), rows.abs().mean(0)
+        assert ((out[i].double() - want).abs() <= 2.0 ** -8 * want.abs() + 90 * 2.0 ** -23 * size_of).all()
+        assert (lse[i].double() - math.log(51 + i)).abs().max() < 1e-5
