@@ -408,7 +408,8 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
       const int e = (int)(big >> 23);
       const int up = big == 0 || e == 255 ? 0 : min(127 + 14 - e, 126);
       r = __uint_as_float((uint32_t)(127 + up) << 23);
-      row_mul *= __uint_as_float((uint32_t)(127 - up) << 23);
+      // finite, so that a score of zero stays one
+      row_mul = fminf(row_mul * __uint_as_float((uint32_t)(127 - up) << 23), 3.40282347e38f);
     }
     if (q == 0) st.row_mul[q_row] = row_mul;
 #pragma unroll

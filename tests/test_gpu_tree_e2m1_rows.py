@@ -30,3 +30,24 @@ def test_scores_of_zero_under_any_scale(tree, T, size, scale):  # noqa: F811
         want, size_of = rows.mean(0), rows.abs().mean(0)
         assert ((out[i].double() - want).abs() <= 2.0 ** -8 * want.abs() + 90 * 2.0 ** -23 * size_of).all()
         assert (lse[i].double() - math.log(51 + i)).abs().max() < 1e-5
+
+
+@pytest.mark.parametrize("T", [1, 2, 40])          # few rows, and tcgen05
+@pytest.mark.parametrize("size,scale", [(2.0 ** 120, 2.0 ** 30), (-2.0 ** 110, 2.0 ** 127)])
+def test_scores_of_zero_over_e4m3(tree, T, size, scale):  # noqa: F811
+    """The same over a cache of e4m3, whose few-row kernel brings rows of q to f16 as well."""
+    from test_gpu_tree import Case as Wide
+    c = Wide(tree, 8, 1, 64, 16, BF16, "e4m3", [T], [50], seed=410 + T, mask=None, garbage=None)
+    c.k.view(torch.uint8).zero_()
+    c.ks.fill_(127)
+    c.q.fill_(size)
+    t = tree.Tree(8, 1, 64, BF16, max_nodes=T)
+    out, lse = t.attend(c.q, tree.KVCache(c.k, c.v, c.ks, c.vs), c.pages, c.length, c.first, scale=scale)
+    assert t.status() == 0
+    v = c.v.double() * torch.exp2(c.vs.double() - 127)[..., None]
+    for i in range(T):
+        at = torch.arange(51 + i, device="cuda")
+        rows = v[c.pages[0][at // 16].long(), at % 16, 0]
+        want, size_of = rows.mean(0), rows.abs().mean(0)
+        assert ((out[i].double() - want).abs() <= 2.0 ** -8 * want.abs() + 90 * 2.0 ** -23 * size_of).all()
+        assert (lse[i].double() - math.log(51 + i)).abs().max() < 1e-5
