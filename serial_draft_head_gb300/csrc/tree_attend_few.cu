@@ -395,18 +395,18 @@ __global__ void __launch_bounds__(Few<E4M3, DP>::kThreads, 1)
     const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
     float row_mul = CAP ? 1.f : sc.sl2, r = 1.f;
     if (E4M3 && !F16) {
-      // the row's largest magnitude to [2^14, 2^15): r a power of two, exact
+      // the row's largest finite magnitude to [2^14, 2^15): r a power of two, exact
       uint32_t big = 0;
 #pragma unroll
       for (int j = 0; j < kQChunks; ++j) {
         const uint32_t w[4] = {qx[j].x, qx[j].y, qx[j].z, qx[j].w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) big = max(big, max((w[k] & 0x7fffu) << 16, w[k] & 0x7fff0000u));
+        for (int k = 0; k < 4; ++k) big = max(big, max(finite_bits(w[k] << 16), finite_bits(w[k])));
       }
       big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
       big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
       const int e = (int)(big >> 23);
-      const int up = big == 0 || e == 255 ? 0 : min(127 + 14 - e, 126);
+      const int up = big == 0 ? 0 : min(127 + 14 - e, 126);
       r = __uint_as_float((uint32_t)(127 + up) << 23);
       // finite, so that a score of zero stays one
       row_mul = fminf(row_mul * __uint_as_float((uint32_t)(127 - up) << 23), 3.40282347e38f);

@@ -437,6 +437,12 @@ static __device__ __noinline__ uint32_t sees_32(const uint32_t* mask_row, int ro
   return __funnelshift_r(lo, hi, j0 & 31);
 }
 
+// The magnitude's bits of the upper half of a word, a bf16; 0 where it is not finite.
+__device__ __forceinline__ uint32_t finite_bits(uint32_t w) {
+  const uint32_t x = w & 0x7fff0000u;
+  return x >= 0x7f800000u ? 0u : x;
+}
+
 template <bool F16>
 __device__ __forceinline__ bool nonfinite16(uint32_t x) {
   constexpr uint32_t e = F16 ? 0x7c00u : 0x7f80u;

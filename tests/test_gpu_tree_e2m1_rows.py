@@ -51,3 +51,43 @@ def test_scores_of_zero_over_e4m3(tree, T, size, scale):  # noqa: F811
         want, size_of = rows.mean(0), rows.abs().mean(0)
         assert ((out[i].double() - want).abs() <= 2.0 ** -8 * want.abs() + 90 * 2.0 ** -23 * size_of).all()
         assert (lse[i].double() - math.log(51 + i)).abs().max() < 1e-5
+
+
+@pytest.mark.parametrize("held", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("T", [1, 2, 4, 40])
+def test_an_infinity_beside_large_elements_of_a_row(tree, held, T):  # noqa: F811
+    """A row with an infinity and elements past f16's range, capped scores: those are infinite, the cap or
+    its negative by the sign that the infinity meets, however large the others' part is."""
+    from test_gpu_tree import Case as Wide
+    cap = 2.0
+    if held == "e2m1":
+        c = Case(tree, 8, 1, 64, 16, BF16, [T], [50], seed=420 + T, mask=None)
+        k = torch.ones(c.n_pages, 16, 1, 64, dtype=torch.float64, device="cuda")
+    else:
+        c = Wide(tree, 8, 1, 64, 16, BF16, "e4m3", [T], [50], seed=420 + T, mask=None, garbage=None)
+        k = torch.ones(c.n_pages, 16, 1, 64, dtype=torch.float64, device="cuda")
+    sign = torch.where(torch.rand(c.n_pages, 16, 1, generator=c.g, device="cuda") < 0.5, -1.0, 1.0).double()
+    k[..., 7] = sign
+    if held == "e2m1":
+        value, byte = e2m1.quantise(k)
+        cache = tree.KVCache(e2m1.pack(value), c.v, byte, c.vs)
+        v = e2m1.values(c.v, c.vs)
+    else:
+        import tree_reference as ref
+        value, byte = ref.quantise(k)
+        cache = tree.KVCache(value.float().to(torch.float8_e4m3fn), c.v, byte, c.vs)
+        v = c.v.double() * torch.exp2(c.vs.double() - 127)[..., None]
+    c.q[..., :] = -2.0 ** 20                           # against the infinity where it meets 1
+    c.q[..., 7] = math.inf
+    t = tree.Tree(8, 1, 64, BF16, max_nodes=T)
+    out, lse = t.attend(c.q, cache, c.pages, c.length, c.first, softcap=cap)
+    assert t.status() == 0
+    for i in range(T):
+        at = torch.arange(51 + i, device="cuda")
+        where = c.pages[0][at // 16].long(), at % 16, 0
+        w = torch.exp(cap * sign[where])
+        want = (w[:, None] * v[where]).sum(0) / w.sum()
+        size_of = (w[:, None] * v[where].abs()).sum(0) / w.sum()
+        # a weight: one rounding to either type, 2^-8 at most, and 2^-19 of the exponential; the result's own
+        assert ((out[i].double() - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -15) * size_of).all()
+        assert (lse[i].double() - w.sum().log()).abs().max() < 2.0 ** -15
