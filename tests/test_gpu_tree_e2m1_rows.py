@@ -91,3 +91,63 @@ def test_an_infinity_beside_large_elements_of_a_row(tree, held, T):  # noqa: F81
         # a weight: one rounding to either type, 2^-8 at most, and 2^-19 of the exponential; the result's own
         assert ((out[i].double() - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -15) * size_of).all()
         assert (lse[i].double() - w.sum().log()).abs().max() < 2.0 ** -15
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("step", [-1, 1, -2, 2])
+def test_codes_beside_every_border(tree, dtype, step):  # noqa: F811
+    """The values one and two of the type's steps below and above every border of codes, times every scale
+    that the type holds it with, beside six times that scale."""
+    scales = e2m1.scale_of(torch.arange(227, device="cuda"))[1:]
+    border = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0], dtype=torch.float64, device="cuda")
+    ties = scales[:, None] * border
+    ties = torch.cat([ties, -ties], 1)[(ties.to(dtype).double() == ties).all(1)].to(dtype)
+    near = ties.view(torch.int16).clone()
+    near[:, [i for i in range(16) if i % 8 != 7]] += step          # magnitudes: the sign is a bit apart
+    x = near.view(dtype)
+    # the smallest steps below a border under the smallest scales must not pass zero
+    assert len(x) > 100 and (x.sign() * ties.sign() >= 0).all()
+    rows = torch.zeros(len(x), 1, 32, dtype=dtype, device="cuda")
+    rows[:, 0, :16] = x
+    rows[:, 0, 16:] = x.flip(0)
+    n = -(-len(x) // 16)
+    t = tree.Tree(1, 1, 32, dtype)
+    cache = tree.KVCache.zeros(n, 16, 1, 32, torch.uint8)
+    pages = torch.arange(n, dtype=torch.int32, device="cuda")[None]
+    z = torch.zeros(1, dtype=torch.int32, device="cuda")
+    t.write(cache, pages, z, torch.tensor([0, len(x)], dtype=torch.int32, device="cuda"), rows, rows)
+    assert t.status() == 0
+    value, byte = e2m1.quantise(rows[:, 0])
+    for codes, scale in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+        assert torch.equal(scale.transpose(1, 2).reshape(n * 16, 2)[:len(x)], byte)
+        assert torch.equal(e2m1.unpack(codes.transpose(1, 2).reshape(n * 16, 16)[:len(x)]), value)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("T", [[20] * 5, [40, 9, 1, 33, 64]])
+def test_many_rows_on_streams_and_in_graphs(tree, T, dtype):  # noqa: F811
+    """The tcgen05 kernel and its join: the same bits on another stream and from a graph, also after the
+    lengths have changed, with calls of the handle in between."""
+    L = [3000, 10, 0, 900, 4000]
+    c = Case(tree, 32, 8, 128, 16, dtype, T, L, seed=430)
+    out, lse = c.attend()
+    c.check(out, lse)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    o2, l2 = c.attend(stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+    o3, l3 = torch.empty_like(out), torch.empty_like(lse)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.tree.attend(c.q, c.cache, c.pages, c.length, c.first, mask=c.mask, out=o3, lse=l3)
+    for n in (L, [17, 10, 0, 900, 2], L):
+        c.L = n
+        c.length.copy_(torch.tensor(n, dtype=torch.int32))
+        o3.fill_(7.0)
+        graph.replay()
+        c.attend()
+        graph.replay()
+        torch.cuda.synchronize()
+        c.check(o3, l3)
+    assert torch.equal(out, o3) and torch.equal(lse, l3)
