@@ -383,8 +383,12 @@ int dspark_tree_attend(dspark_tree_t h, const dspark_tree_cache* cache,
   const bool few = (int64_t)a.b.N * a.G <= (int64_t)16 * a.b.B;
   if (held_as(cache) == kE2M1) {
     a.f16 = h->cfg.type == DSPARK_TYPE_F16;
-    // items of 32 rows where the others have 16 (16 requests as above, here / there: 24 rows
-    // 62 / 70 us, 32 rows 65 / 70, 40 rows 102 / 71)
+    // Items of 32 rows where the others have 16.  8 heads of 128, 300 to 6,000 tokens, bf16, keys
+    // alike, here / there: 16 requests (56,874 keys) over 16-slot pages 17 rows 59 / 66 us, 24 rows
+    // 59 / 66, 32 rows 62 / 66, over 64-slot ones 58 / 66, 58 / 66, 61 / 66; 128 requests 359 / 390,
+    // 365 / 390, 378 / 391 and 347, 349, 365.  With one key in 50 eight times the others, which moves
+    // maxima here, 24 rows 63 / 66 and 384 / 390, 32 rows 66 / 66 and 397 / 391 (32 requests 124 /
+    // 119), in f16 66 / 71 and 398 / 415.  Weights are f16 here, eight times as fine as bf16 there.
     const bool few4 = (int64_t)a.b.N * a.G <= (int64_t)32 * a.b.B;
     return cuda_code(few4 ? few4_launch(a, &h->ready, static_cast<cudaStream_t>(stream))
                          : attend4_launch(a, a.f16, &h->ready, static_cast<cudaStream_t>(stream)));

@@ -51,9 +51,11 @@ cudaError_t few4_launch(const AttendArgs& a, uint32_t* ready, cudaStream_t strea
   // rows of an item: what the requests have on average, in whole tiles of eight
   const int64_t rows = (int64_t)a.b.N * a.G;
   const int tiles = rows <= (int64_t)8 * a.b.B ? 1 : rows <= (int64_t)16 * a.b.B ? 2 : 4;
-  // workers of four warps where there are two items a SM (64 heads on 8, 500 to 9,000
-  // tokens, us with four / with a CTA's: 48 requests 76 / 93, 128 167 / 207; 16 requests 38 /
-  // 39, 1 of 5,000 27 / 16, 19 of 32,767 156 / 144)
+  // Workers of four warps where there are two items a SM (64 heads on 8, 500 to 9,000
+  // tokens, us with four / with a CTA's: 48 requests 69 / 87, 128 146 / 195; 16 requests 36 /
+  // 35, 1 of 5,000 28 / 14, 19 of 32,767 135 / 128).  Items of 16 and 32 rows (32 heads on 8):
+  // 128 requests of 100 to 300 tokens 46 / 55 and 81 / 90, of 300 to 6,000 272 / 269 and 400 / 381,
+  // with heads of 64 elements 107 / 124 and 200 / 205; the lengths are not known here.
   const int64_t items = (rows + 8 * tiles - 1) / (8 * tiles) * a.Hkv;
   const bool alone = items < (int64_t)2 * a.n_cta;
   const bool runs = in_runs(a);

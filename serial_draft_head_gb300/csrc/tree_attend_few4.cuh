@@ -35,11 +35,11 @@
 // read together lie in different banks.  Rows of Q are brought to f16 by a power of two
 // a row.
 //
-// What bounds it.  128 single tokens of 500 to 9,000 (64 heads on 8): 150 us, 4.8 TB/s;
+// What bounds it.  128 single tokens of 500 to 9,000 (64 heads on 8): 147 us, 4.9 TB/s;
 // 700 warp instructions a block, issued at 64% of the slots, held by fixed latencies and
 // the pipes of the conversions and 16-bit products (without the products: 125).  19
 // requests of 32,767: 128 us, 5.6 TB/s.  Items of 32 rows (16 chains of 8 over 300 to 6,000
-// with 4 heads on one: 74 us): two warps a scheduler, issued at 28%.
+// with 4 heads on one: 66 us of 56,874 keys, 72 of 64,643): two warps a scheduler, issued at 28%.
 #pragma once
 
 #include "tree_items.cuh"
@@ -58,7 +58,9 @@ struct Few4 {
   // units an item counts beside its blocks, for Q, the first copies and the warps'
   // meeting
   static constexpr int kExtra = GROUP == 4 ? 10 : 20;
-  static constexpr int kWarps = NT == 1 ? 16 : NT == 2 ? 12 : 8;   // as many as registers allow
+  // as many as leave O, m and l in registers; with heads of 128 what a segment needs now and
+  // then is spilled: 136 bytes at most (NT 1), 356 (2), 388 (4)
+  static constexpr int kWarps = NT == 1 ? 16 : NT == 2 ? 12 : 8;
   static constexpr int kWorkers = kWarps / GROUP;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kBytes = DP / 2;                  // of a row of codes
@@ -901,7 +903,8 @@ cudaError_t launch(AttendArgs a, uint32_t* ready, cudaStream_t stream) {
 }
 
 // alone: a worker a CTA; else of four warps, where slots lie in runs and scores are not
-// capped.
+// capped (those, and slots that are no runs, go with a worker a CTA: 128 tokens as above 147 us,
+// capped 223, a slot's heads next to each other 280).
 template <int DP, int NT, int WARPS>
 cudaError_t launch_all(const AttendArgs& a, bool alone, bool runs, uint32_t* ready, cudaStream_t stream) {
   const bool cap = a.softcap > 0.f;

@@ -1,5 +1,5 @@
-// tree_items.cuh -- how both attention kernels cut their work, and the parts of
-// the softmax they share.
+// tree_items.cuh -- how the attention kernels (tree_attend.cuh, tree_attend_few.cu,
+// tree_attend_few4.cuh) cut their work, and the parts of the softmax they share.
 //
 // Per cached head the rows that read it are (node, query head of the group):
 // T * G of them.  A work item is (request, cached head, up to ROWS of its rows)
@@ -7,12 +7,12 @@
 // and so that short items do not pile up on one worker, EXTRA more units stand
 // before an item's first for what it costs beside its tiles (Q, the result, the
 // way into the loop).  The units of all items, in order, are split evenly over
-// the workers (one CTA a SM): the lengths are known on the device only, so every
-// CTA sums them up itself.  An item that lies inside one worker's share is
+// the workers (one CTA a SM, or, over e2m1, up to four in it): the lengths are known on the
+// device only, so every CTA sums them up itself.  An item that lies inside one worker's share is
 // finished there; one that several workers share leaves parts (unnormalised O,
 // maximum, sum), at most one a worker, joined in an order that does not depend on
-// timing: by the CTA that is last to leave its part (few rows: 16 rows a part), or by
-// a second kernel over all SMs (tcgen05: up to 256 rows a part).
+// timing: by the worker that is last to leave its part (few rows: 16 rows a part, over e2m1
+// 8, 16 or 32), or by a second kernel over all SMs (tcgen05: up to 256 rows a part).
 //
 // Mathematics, per row, one pass over the tiles in the base-2 exponent:
 //   x_j = log2(e) * scale * q.k_j              (capped: log2(e) c tanh(s / c))
@@ -23,7 +23,9 @@
 // to 2^-21 of the largest stay normal numbers: p <= 2^15 then, and f16 ends at 65,504.
 // O and l in fp32 keep their relative precision.  p is rounded once to the 16-bit type
 // for the second product (half a unit, as the result itself is rounded); l sums the
-// unrounded p.
+// unrounded p.  Over e2m1 in bf16 on tcgen05 it is otherwise: m moves when the maximum has
+// grown by more than 64, so p <= 2^64, and rows are divided by the sum of the rounded p
+// (grow_limit and Sum in tree_attend.cuh have the reasons).
 #pragma once
 
 #include <math.h>

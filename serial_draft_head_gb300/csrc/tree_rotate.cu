@@ -6,7 +6,7 @@
 // that it turns with, so that a pair is in one thread and only the norm's sum crosses
 // lanes.  A warp has a token (or, so that few tokens fill the device, a share of its
 // heads): it works out the token's sines and cosines, one a lane, keeps them, times the
-// norm's weights, in registers, and goes through the heads with two rows' loads in flight.
+// norm's weights, in registers, and goes through the heads with five rounds' loads in flight.
 // Nothing is handed between warps.
 //
 // Angles: a frequency is held in turns a position, as a 64-bit fraction, so that position
